@@ -27,7 +27,7 @@ __device__ unsigned int g_error_word[2];
 
 static thread_local int t_last_cuda_error = 0;
 
-static int cuda_fail(cudaError_t e) {
+int cuda_fail(cudaError_t e) {
   t_last_cuda_error = static_cast<int>(e);
   return GF_ERR_CUDA;
 }
@@ -46,7 +46,7 @@ unsigned* device_error_word() {
   return addr[dev];
 }
 
-static DeviceLimits device_limits() {
+DeviceLimits device_limits() {
   static std::mutex mu;
   static DeviceLimits lim[64];
   static bool have[64] = {false};
@@ -73,7 +73,7 @@ static DeviceLimits device_limits() {
 
 // ------------------------------------------------------------------ helpers
 
-static int64_t row_bytes_of(int wtype, int64_t K) {
+int64_t row_bytes_of(int wtype, int64_t K) {
   switch (wtype) {
     case GF_F32: return 4 * K;
     case GF_F16: return 2 * K;
@@ -83,7 +83,7 @@ static int64_t row_bytes_of(int wtype, int64_t K) {
   }
 }
 
-static bool ranges_overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
+bool ranges_overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
   if (!a || !b || abytes <= 0 || bbytes <= 0) return false;
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
   return a0 < b0 + static_cast<uintptr_t>(bbytes) && b0 < a0 + static_cast<uintptr_t>(abytes);
@@ -368,29 +368,6 @@ static int plan_call(const Call& c, Plan& p, int* generic_smem, int* generic_gri
   return PATH_GENERIC;
 }
 
-// One kernel launch with every argument resolved: what a call plans, and what a
-// prepared call keeps (gf_prepare) so that launching it does no planning at all.
-enum { REC_FWHT = 0, REC_TC = 1, REC_STREAM = 2, REC_GENERIC = 3, REC_COPY = 4 };
-struct LaunchRec {
-  int kind;
-  bool pdl;
-  const void* csrc;  // host staging copy (device-addressable pointers)
-  void* cdst;
-  int64_t cbytes;
-  int wtype, ncols;
-  const void* W;  // tensor-core path: the matrix of the tensor map
-  const float* fx;  // stand-alone FWHT
-  const float* fsigns;
-  float* fdst;
-  int64_t fn;
-  int fB, fnsigns;
-  TcPlan tp;
-  Plan p;
-  GenericArgs g;
-  int ggrid, gsmem;
-};
-constexpr int kMaxRecs = 1 + kMaxSeg * (kMaxBatch / kMaxCols);  // transform + column blocks (per matrix)
-
 // The operand pointers of a streamed launch of call c (the plan holds the shapes).
 static void fill_stream_ptrs(const Call& c, float* dst, unsigned* err, StreamArgs& s) {
   s.W = static_cast<const uint8_t*>(c.W);
@@ -458,9 +435,17 @@ static int plan_one(const Call& c, float* dst, LaunchRec& r) {
   return GF_OK;
 }
 
-static int issue(const LaunchRec& r, cudaStream_t st) {
+int issue(const LaunchRec& r, cudaStream_t st) {
   int e;
-  if (r.kind == REC_COPY) {
+  if (r.kind == REC_ROUTE) {
+    e = launch_route(r.route, st, r.pdl);
+  } else if (r.kind == REC_EXPERTS) {
+    e = launch_experts(r.experts, st, r.pdl);
+  } else if (r.kind == REC_LORA) {
+    e = launch_lora(r.lora, st, r.pdl);
+  } else if (r.kind == REC_EW) {
+    e = launch_elementwise(r.ewop, r.fx, r.fsigns, r.fn, r.fdst, r.fn, st);
+  } else if (r.kind == REC_COPY) {
     e = launch_copy(r.cdst, r.csrc, r.cbytes, st, r.pdl);
   } else if (r.kind == REC_FWHT) {
     e = launch_fwht(r.fx, r.fsigns, r.fdst, r.fn, r.fB, r.fnsigns, st);
@@ -918,6 +903,156 @@ int gf_prepare_multi(const gf_multi_item* items, int n, int wtype, const float* 
   return prepare(c, opts, out);
 }
 
+// ------------------------------------------------------------------ low-rank adapters
+int64_t gf_lora_workspace(int64_t ncols, int64_t M, int64_t K, int64_t rank, int64_t n) {
+  if (ncols < 0 || M < 0 || K < 0 || n < 0 || rank < 1) return GF_ERR_INVALID;
+  if (ncols > kMaxBatch || rank > kLoraMaxRank || M > INT32_MAX) return GF_ERR_UNSUPPORTED;
+  // the columns' rank-sized products, then room for one output (silu(y)*m in place)
+  return (ncols * rank * 4 + 255) / 256 * 256 + (ncols * M * 4 + 255) / 256 * 256;
+}
+
+// The launches of a gemv_lora call: [transform,] shrink, expand, the shared product with
+// the expansion as its addend [, the product with aux].
+static int plan_lora(const void* W, int wtype, const float* x, int64_t M, int64_t K, int epilogue, const float* aux,
+                     float* dst, const gf_lora* lo, const gf_opts* opts, LaunchRec* recs, int cap, int* n) {
+  *n = 0;
+  Call c = make_call(W, wtype, x, M, K, epilogue, aux, dst, opts);
+  int v = validate(c);
+  if (v != GF_OK) return v;
+  v = check_view(opts, M);
+  if (v != GF_OK) return v;
+  if (!lo) return GF_ERR_INVALID;
+  if (lo->atype != GF_F16 && lo->atype != GF_F32) return GF_ERR_INVALID;
+  if (lo->n < 0 || lo->rank < 1) return GF_ERR_INVALID;
+  if (lo->rank > kLoraMaxRank || lo->n > INT32_MAX) return GF_ERR_UNSUPPORTED;
+  if (c.signs && !c.workspace) return GF_ERR_UNSUPPORTED;
+  if (M == 0) return GF_OK;
+  if (!lo->ids || !lo->workspace || (lo->n > 0 && ((K > 0 && !lo->A) || !lo->B))) return GF_ERR_INVALID;
+  const uintptr_t al = lo->atype == GF_F32 ? 4 : 2;
+  if (!aligned(lo->ids, 4) || !aligned(lo->workspace, 256) || !aligned(lo->A, al) || !aligned(lo->B, al) ||
+      !aligned(lo->scales, 4))
+    return GF_ERR_ALIGN;
+  const int64_t need = gf_lora_workspace(c.ncols, M, K, lo->rank, lo->n);
+  if (need < 0) return static_cast<int>(need);
+  if (lo->workspace_bytes < need) return GF_ERR_INVALID;
+  const int64_t el = lo->atype == GF_F32 ? 4 : 2;
+  const bool need_aux = c.aux != nullptr;
+  const int64_t dbytes = c.ncols * M * 4, xbytes = c.ncols * K * 4, wbytes = M * row_bytes_of(wtype, K);
+  const struct { const void* p; int64_t bytes; } side[4] = {{lo->A, lo->n * lo->rank * K * el},
+                                                            {lo->B, lo->n * M * lo->rank * el},
+                                                            {lo->ids, c.ncols * 4},
+                                                            {lo->scales, lo->n * 4}};
+  for (const auto& s : side)
+    if (ranges_overlap(dst, dbytes, s.p, s.bytes) || ranges_overlap(lo->workspace, need, s.p, s.bytes) ||
+        (c.workspace && ranges_overlap(c.workspace, xbytes, s.p, s.bytes)))
+      return GF_ERR_ALIAS;
+  if (ranges_overlap(lo->workspace, need, dst, dbytes) || ranges_overlap(lo->workspace, need, x, xbytes) ||
+      ranges_overlap(lo->workspace, need, W, wbytes) || (need_aux && ranges_overlap(lo->workspace, need, aux, dbytes)) ||
+      (c.gamma && ranges_overlap(lo->workspace, need, c.gamma, K * 4)) ||
+      (c.signs && ranges_overlap(lo->workspace, need, c.signs, c.nsigns * 4)) ||
+      (c.workspace && ranges_overlap(lo->workspace, need, c.workspace, xbytes)))
+    return GF_ERR_ALIAS;
+  if (K == 0 || lo->n == 0) return plan_launches(c, dst, recs, cap, n);  // nothing to add
+
+  bool pdl = (c.flags & GF_FLAG_PDL) != 0;
+  if (c.workspace) {  // the transform once; shrink and product both read it
+    LaunchRec& f = recs[(*n)++];
+    f.kind = REC_FWHT;
+    f.pdl = false;
+    f.fx = x;
+    f.fsigns = c.signs;
+    f.fdst = c.workspace;
+    f.fn = c.ncols * K;
+    f.fB = static_cast<int>(c.fwht_block);
+    f.fnsigns = static_cast<int>(c.nsigns);
+    c.x = c.workspace;
+    c.signs = nullptr;
+    c.fwht_block = c.nsigns = 0;
+    c.workspace = nullptr;
+    pdl = true;
+  }
+  float* ws = static_cast<float*>(lo->workspace);
+  float* spare = ws + (c.ncols * lo->rank * 4 + 255) / 256 * 64;
+  LoraArgs l = {};
+  l.atype = lo->atype;
+  l.A = static_cast<const uint8_t*>(lo->A);
+  l.B = static_cast<const uint8_t*>(lo->B);
+  l.ids = lo->ids;
+  l.scales = lo->scales;
+  l.x = c.x;
+  l.gamma = c.gamma;
+  l.eps = c.eps;
+  l.v = ws;
+  l.n = static_cast<int>(lo->n);
+  l.r = static_cast<int>(lo->rank);
+  l.M = static_cast<int>(M);
+  l.K = static_cast<int>(K);
+  l.ncols = static_cast<int>(c.ncols);
+  // silu(y)*m in place needs its own room for y: m is still to be read
+  float* out = (epilogue == GF_EPI_SILU_MUL && aux == dst) ? spare : dst;
+  l.out = out;
+  l.aux = epilogue == GF_EPI_ADD ? aux : nullptr;
+  l.phase = LORA_SHRINK;
+  LaunchRec& r0 = recs[(*n)++];
+  r0.kind = REC_LORA;
+  r0.pdl = pdl;
+  r0.lora = l;
+  l.phase = LORA_EXPAND;
+  LaunchRec& r1 = recs[(*n)++];
+  r1.kind = REC_LORA;
+  r1.pdl = true;
+  r1.lora = l;
+  c.aux = out;
+  c.dst = out;
+  c.flags |= GF_FLAG_PDL;
+  switch (epilogue) {
+    case GF_EPI_SIGMOID: c.epi = EPI_ADD_SIGMOID; break;
+    case GF_EPI_SILU:
+    case GF_EPI_SILU_MUL: c.epi = EPI_ADD_SILU; break;
+    default: c.epi = GF_EPI_ADD; break;
+  }
+  int m = 0;
+  v = plan_launches(c, out, recs + *n, cap - *n, &m);
+  if (v != GF_OK) return v;
+  *n += m;
+  if (epilogue == GF_EPI_SILU_MUL) {
+    if (*n >= cap) return GF_ERR_UNSUPPORTED;
+    LaunchRec& e = recs[(*n)++];
+    e.kind = REC_EW;
+    e.pdl = false;
+    e.ewop = GF_EW_MUL;
+    e.fx = out;
+    e.fsigns = aux;
+    e.fdst = dst;
+    e.fn = c.ncols * M;
+  }
+  return GF_OK;
+}
+
+int gemv_lora(const void* W, int wtype, const float* x, int64_t M, int64_t K, int epilogue, const float* aux, float* dst,
+              const gf_lora* lora, const gf_opts* opts, void* stream) {
+  LaunchRec recs[kMaxRecs];
+  int n = 0;
+  const int v = plan_lora(W, wtype, x, M, K, epilogue, aux, dst, lora, opts, recs, kMaxRecs, &n);
+  if (v != GF_OK) return v;
+  for (int i = 0; i < n; ++i) {
+    const int e = issue(recs[i], static_cast<cudaStream_t>(stream));
+    if (e != GF_OK) return e;
+  }
+  return GF_OK;
+}
+
+int gf_prepare_lora(const void* W, int wtype, const float* x, int64_t M, int64_t K, int epilogue, const float* aux,
+                    float* dst, const gf_lora* lora, const gf_opts* opts, gf_prepared** out) {
+  if (!out) return GF_ERR_INVALID;
+  *out = nullptr;
+  LaunchRec recs[kMaxRecs];
+  int n = 0;
+  const int v = plan_lora(W, wtype, x, M, K, epilogue, aux, dst, lora, opts, recs, kMaxRecs, &n);
+  if (v != GF_OK) return v;
+  return make_prepared(recs, n, out);
+}
+
 int gf_launch_prepared(const gf_prepared* const* calls, int n, void* stream) {
   if (n < 0 || (n > 0 && !calls)) return GF_ERR_INVALID;
   for (int i = 0; i < n; ++i)
@@ -1080,3 +1215,20 @@ void gf_graph_free(gf_graph* g) {
 }
 
 }  // extern "C"
+
+namespace gf {
+
+int make_prepared(const LaunchRec* recs, int n, gf_prepared** out) {
+  gf_prepared* p = new (std::nothrow) gf_prepared;
+  if (!p) return GF_ERR_INVALID;
+  if (cudaGetDevice(&p->device) != cudaSuccess) {
+    delete p;
+    return cuda_fail(cudaGetLastError());
+  }
+  p->n = n;
+  for (int i = 0; i < n; ++i) p->recs[i] = recs[i];
+  *out = p;
+  return GF_OK;
+}
+
+}  // namespace gf

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kGenericThreads) gemv_generic_kernel(const Gen
         if (dual) {
           a.dst[o] = tail_silu(s) * su;
         } else {
-          const float av = (a.epi == EPI_SILU_MUL || a.epi == EPI_ADD) ? a.aux[o] : 0.0f;
+          const float av = epi_takes_aux(a.epi) ? a.aux[o] : 0.0f;
           a.dst[o] = apply_tail(a.epi, s, av);
         }
       }

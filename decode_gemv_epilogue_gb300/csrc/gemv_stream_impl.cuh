@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(stream_threads(WT, NC), 1)
     // wait gave up; after an abort the remaining work is skipped, not the barriers.
     const int cw = warp - 1, ctid = threadIdx.x - 32, nt = a.ncw * 32;
     const uint32_t qr = lane_quad_rot<WT>(lane);
-    auto epi_aux = [](int e) { return e == EPI_SILU_MUL || e == EPI_ADD; };
+    auto epi_aux = [](int e) { return epi_takes_aux(e); };
     const bool finalizer = (crank == 0);
     pdl_wait();  // x, aux and dst may belong to the preceding grid
     int slot = 0;            // ring slot of the next tile

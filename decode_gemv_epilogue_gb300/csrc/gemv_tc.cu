@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemv_tc_kernel(const __grid_con
     const int q = warp & 3;           // TMEM lane quarter this warp can read
     const int r = 32 * q + lane;      // row within the tile
     const int64_t row = static_cast<int64_t>(row0) + r;
-    const bool need_aux = (a.epi == EPI_SILU_MUL || a.epi == EPI_ADD);
+    const bool need_aux = epi_takes_aux(a.epi);
     uint64_t own_tbl = 0;
     uint32_t mine = 0;
     {

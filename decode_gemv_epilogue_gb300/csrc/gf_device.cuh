@@ -12,6 +12,11 @@ enum { WT_F32 = 0, WT_F16 = 1, WT_Q8_0 = 2, WT_Q4_0 = 3, WT_Q4_K = 4 };
 enum { EPI_NONE = 0, EPI_SIGMOID = 1, EPI_SILU = 2, EPI_SILU_MUL = 3, EPI_ADD = 4 };
 // Internal tail of the gated dual GEMV: silu(gate row) * (up row).
 enum { EPI_GLU = 5 };
+// Internal tails of a product whose addend (aux) comes before the activation.
+enum { EPI_ADD_SIGMOID = 6, EPI_ADD_SILU = 7 };
+__host__ __device__ constexpr bool epi_takes_aux(int e) {
+  return e == EPI_SILU_MUL || e == EPI_ADD || e == EPI_ADD_SIGMOID || e == EPI_ADD_SILU;
+}
 enum { ERRBIT_TIMEOUT = 1u };
 
 // A bounded wait gives up after this many nanoseconds of %globaltimer.
@@ -736,6 +741,8 @@ __device__ __forceinline__ float apply_tail(int epi, float y, float a) {
     case EPI_SILU: return tail_silu(y);
     case EPI_SILU_MUL: return tail_silu(y) * a;
     case EPI_ADD: return y + a;
+    case EPI_ADD_SIGMOID: return tail_sigmoid(y + a);
+    case EPI_ADD_SILU: return tail_silu(y + a);
     default: return y;
   }
 }

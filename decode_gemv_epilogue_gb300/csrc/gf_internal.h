@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 struct CUtensorMap_st;  // the driver's tensor-map descriptor (cuda.h)
+struct gf_prepared;
 
 namespace gf {
 
@@ -218,6 +219,114 @@ int launch_elementwise(int op, const float* a, const float* b, int64_t nb, float
                        cudaStream_t st);
 int launch_dequantize(int wtype, const uint8_t* W, int64_t M, int64_t K, int64_t row_bytes,
                       float* out, cudaStream_t st);
+
+// ------------------------------------------------------------------ weights chosen per column
+// Routing to experts (route.cu).
+constexpr int kRouteMaxExperts = 1024;
+constexpr int kRouteMaxTopK = 32;
+constexpr int kRouteMaxGroups = 32;
+struct RouteArgs {
+  const float* logits;
+  const float* bias;
+  int32_t* ids;
+  float* weights;
+  int64_t T, ld;
+  int E, k, sigmoid, n_group, topk_group, group_top, norm;
+  float scale;
+};
+int launch_route(const RouteArgs& a, cudaStream_t st, bool pdl);
+
+// The chosen experts' gated product (experts.cu): one launch of one phase.
+constexpr int kExpMaxTokens = 256;
+enum { EXP_PREP = 0, EXP_GLU = 1, EXP_DOWN = 2, EXP_COMBINE = 3, EXP_GLU_GENERIC = 4, EXP_DOWN_GENERIC = 5 };
+// float2 per 32 elements of a packed row, padded to whole 16-byte words.
+__host__ __device__ constexpr int expert_meta_stride(int n) { return ((n + 31) / 32 + 1) / 2 * 2; }
+struct ExpertsArgs {
+  int phase;
+  int wtype;            // of this phase's matrices
+  int order;            // element order of the packed x this phase writes (see experts.cu)
+  const uint8_t* W;     // gate (EXP_GLU*) or down (EXP_DOWN*)
+  const uint8_t* W2;    // up
+  const float* x;
+  const int32_t* ids;
+  const float* weights;
+  const float* aux;
+  float* dst;
+  unsigned* err;
+  int E, T, k;
+  int M, K;             // ffn width, model width
+  int cols;             // columns per group (8, 16 or 32)
+  // workspace
+  int32_t* slots;       // [T k] slots by expert, in slot order
+  int4* groups;         // {expert, first, count, 0} of each column group
+  int32_t* n_groups;
+  uint8_t* xpack;       // [T][K * 4]
+  float2* xmeta;        // [T][meta_stride(K)]
+  uint8_t* hpack;       // [T k][M * 4], or h itself in float32 (generic)
+  float2* hmeta;        // [T k][meta_stride(M)]
+  float* y;             // [T k][K]
+  int sm_count, smem_optin;
+};
+int launch_experts(const ExpertsArgs& a, cudaStream_t st, bool pdl);
+
+// Low-rank adapters (lora.cu): one launch of one phase.
+constexpr int kLoraMaxRank = 256;
+enum { LORA_SHRINK = 0, LORA_EXPAND = 1 };
+struct LoraArgs {
+  int phase;
+  int atype;            // GF_F16 or GF_F32
+  const uint8_t* A;     // [n][r][K]
+  const uint8_t* B;     // [n][M][r]
+  const int32_t* ids;
+  const float* scales;
+  const float* x;       // [ncols][K]
+  const float* gamma;
+  float eps;
+  const float* aux;     // added by the expansion (nullptr: none)
+  float* v;             // [ncols][r]
+  float* out;           // [ncols][M]
+  int n, r, M, K, ncols;
+};
+int launch_lora(const LoraArgs& a, cudaStream_t st, bool pdl);
+
+// One kernel launch with every argument resolved: what a call plans, and what a
+// prepared call keeps (gf_prepare) so that launching it does no planning at all.
+enum {
+  REC_FWHT = 0, REC_TC = 1, REC_STREAM = 2, REC_GENERIC = 3, REC_COPY = 4, REC_ROUTE = 5, REC_EXPERTS = 6,
+  REC_LORA = 7, REC_EW = 8
+};
+struct LaunchRec {
+  int kind;
+  bool pdl;
+  const void* csrc;  // host staging copy (device-addressable pointers)
+  void* cdst;
+  int64_t cbytes;
+  int wtype, ncols;
+  const void* W;  // tensor-core path: the matrix of the tensor map
+  const float* fx;  // stand-alone FWHT
+  const float* fsigns;
+  float* fdst;
+  int64_t fn;
+  int fB, fnsigns;
+  TcPlan tp;
+  Plan p;
+  GenericArgs g;
+  int ggrid, gsmem;
+  int ewop;           // element-wise op over fx and fsigns (fn elements)
+  RouteArgs route;
+  ExpertsArgs experts;
+  LoraArgs lora;
+};
+constexpr int kMaxRecs = 1 + kMaxSeg * (kMaxBatch / kMaxCols);  // transform + column blocks (per matrix)
+
+// Shared by the entry points (api.cu, api_select.cu).
+int64_t row_bytes_of(int wtype, int64_t K);
+bool ranges_overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes);
+int cuda_fail(cudaError_t e);
+DeviceLimits device_limits();
+int issue(const LaunchRec& r, cudaStream_t st);
+// A handle over n (<= kMaxRecs) planned launches; a gf_status.
+int make_prepared(const LaunchRec* recs, int n, gf_prepared** out);
 
 unsigned* device_error_word();  // this device's error word (nullptr on failure)
 int launch_selftest_wait(unsigned* err, uint64_t limit_ns, int* out, cudaStream_t st);

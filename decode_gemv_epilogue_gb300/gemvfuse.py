@@ -81,6 +81,36 @@ _graph_create = _sig("gf_graph_create", [ctypes.POINTER(_vp), _i32, ctypes.POINT
 _graph_launch = _sig("gf_graph_launch", [_vp, _vp])
 _graph_free = _sig("gf_graph_free", [_vp], None)
 
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+
+
+class RouteOpts(ctypes.Structure):
+    _fields_ = [("top_k", _i64), ("score", _i32), ("norm", _i32), ("scale", ctypes.c_float), ("bias", _vp),
+                ("n_group", _i64), ("topk_group", _i64), ("group_top", _i32), ("ld", _i64), ("flags", _u32)]
+
+
+class Experts(ctypes.Structure):
+    _fields_ = [("W_gate", _vp), ("W_up", _vp), ("W_down", _vp), ("wtype", _i32), ("wtype_down", _i32), ("E", _i64),
+                ("M", _i64), ("K", _i64), ("ids", _vp), ("weights", _vp), ("top_k", _i64), ("workspace", _vp),
+                ("workspace_bytes", _i64), ("flags", _u32)]
+
+
+class Lora(ctypes.Structure):
+    _fields_ = [("A", _vp), ("B", _vp), ("atype", _i32), ("n", _i64), ("rank", _i64), ("ids", _vp), ("scales", _vp),
+                ("workspace", _vp), ("workspace_bytes", _i64)]
+
+
+_route = _sig("gf_route", [_vp, _i64, _i64, ctypes.POINTER(RouteOpts), _vp, _vp, _vp])
+_prepare_route = _sig("gf_prepare_route", [_vp, _i64, _i64, ctypes.POINTER(RouteOpts), _vp, _vp, ctypes.POINTER(_vp)])
+_gemv_experts = _sig("gemv_experts", [ctypes.POINTER(Experts), _vp, _i64, _vp, _vp, _vp])
+_prepare_experts = _sig("gf_prepare_experts", [ctypes.POINTER(Experts), _vp, _i64, _vp, _vp, ctypes.POINTER(_vp)])
+_experts_workspace = _sig("gf_experts_workspace", [_i64] * 5, _i64)
+_gemv_lora = _sig("gemv_lora", [_vp, _i32, _vp, _i64, _i64, _i32, _vp, _vp, ctypes.POINTER(Lora),
+                                ctypes.POINTER(GfOpts), _vp])
+_prepare_lora = _sig("gf_prepare_lora", [_vp, _i32, _vp, _i64, _i64, _i32, _vp, _vp, ctypes.POINTER(Lora),
+                                         ctypes.POINTER(GfOpts), ctypes.POINTER(_vp)])
+_lora_workspace = _sig("gf_lora_workspace", [_i64] * 5, _i64)
+
 #: the raw C functions, for callers that want the status codes themselves
 raw = _lib
 
@@ -400,3 +430,111 @@ def prepare_copy(dst, src, nbytes, pdl=False, check=True):
     if check:
         _check(st, "gf_prepare_copy")
     return Prepared(h.value, (dst, src)) if st == OK else st
+
+
+# ---- products whose weights are chosen per column
+
+def _nbytes(a, given):
+    if given is not None:
+        return given
+    return 0 if a is None or isinstance(a, int) else a.numel() * a.element_size()
+
+
+def _route_opts(top_k, score, bias, n_group, topk_group, group_top, norm, scale, ld, pdl):
+    return RouteOpts(top_k, score, 1 if norm else 0, scale, _ptr(bias), n_group, topk_group, group_top, ld,
+                     FLAG_PDL if pdl else 0)
+
+
+def route(logits, T, E, top_k, ids, weights, score=SCORE_SOFTMAX, bias=None, n_group=1, topk_group=1, group_top=2,
+          norm=True, scale=1.0, ld=0, pdl=False, stream=None, check=True):
+    """gf_route: the top_k experts of each of T tokens and their weights (see include/gemvfuse.h)."""
+    o = _route_opts(top_k, score, bias, n_group, topk_group, group_top, norm, scale, ld, pdl)
+    st = _route(_ptr(logits), T, E, ctypes.byref(o), _ptr(ids), _ptr(weights), _stream(stream))
+    if check:
+        _check(st, "gf_route")
+    return st
+
+
+def prepare_route(logits, T, E, top_k, ids, weights, score=SCORE_SOFTMAX, bias=None, n_group=1, topk_group=1,
+                  group_top=2, norm=True, scale=1.0, ld=0, pdl=False, check=True):
+    """gf_prepare_route: the call route(...) would make, planned once (see Prepared)."""
+    o = _route_opts(top_k, score, bias, n_group, topk_group, group_top, norm, scale, ld, pdl)
+    h = _vp()
+    st = _prepare_route(_ptr(logits), T, E, ctypes.byref(o), _ptr(ids), _ptr(weights), ctypes.byref(h))
+    if check:
+        _check(st, "gf_prepare_route")
+    return Prepared(h.value, (logits, ids, weights, bias)) if st == OK else st
+
+
+def experts_workspace(E, T, top_k, M, K):
+    """Bytes of workspace gemv_experts needs for these sizes."""
+    n = _experts_workspace(E, T, top_k, M, K)
+    if n < 0:
+        raise GemvFuseError(n, "gf_experts_workspace")
+    return n
+
+
+def _experts_struct(W_gate, W_up, wtype, W_down, wtype_down, E, M, K, ids, weights, top_k, workspace,
+                    workspace_bytes, pdl):
+    return Experts(_ptr(W_gate), _ptr(W_up), _ptr(W_down), wtype, wtype_down, E, M, K, _ptr(ids), _ptr(weights),
+                   top_k, _ptr(workspace), _nbytes(workspace, workspace_bytes), FLAG_PDL if pdl else 0)
+
+
+def gemv_experts(W_gate, W_up, wtype, W_down, wtype_down, E, x, M, K, ids, weights, T, top_k, aux, dst, workspace,
+                 workspace_bytes=None, pdl=False, stream=None, check=True):
+    """dst_t = aux_t + sum_j weights_tj Wd_e (silu(Wg_e x_t) * (Wu_e x_t)), e = ids_tj (see
+    include/gemvfuse.h)."""
+    ex = _experts_struct(W_gate, W_up, wtype, W_down, wtype_down, E, M, K, ids, weights, top_k, workspace,
+                         workspace_bytes, pdl)
+    st = _gemv_experts(ctypes.byref(ex), _ptr(x), T, _ptr(aux), _ptr(dst), _stream(stream))
+    if check:
+        _check(st, "gemv_experts")
+    return st
+
+
+def prepare_experts(W_gate, W_up, wtype, W_down, wtype_down, E, x, M, K, ids, weights, T, top_k, aux, dst, workspace,
+                    workspace_bytes=None, pdl=False, check=True):
+    """gf_prepare_experts: the call gemv_experts(...) would make, planned once (see Prepared)."""
+    ex = _experts_struct(W_gate, W_up, wtype, W_down, wtype_down, E, M, K, ids, weights, top_k, workspace,
+                         workspace_bytes, pdl)
+    h = _vp()
+    st = _prepare_experts(ctypes.byref(ex), _ptr(x), T, _ptr(aux), _ptr(dst), ctypes.byref(h))
+    if check:
+        _check(st, "gf_prepare_experts")
+    return Prepared(h.value, (W_gate, W_up, W_down, x, ids, weights, aux, dst, workspace)) if st == OK else st
+
+
+def lora_workspace(ncols, M, K, rank, n):
+    """Bytes of workspace gemv_lora needs for these sizes."""
+    b = _lora_workspace(ncols, M, K, rank, n)
+    if b < 0:
+        raise GemvFuseError(b, "gf_lora_workspace")
+    return b
+
+
+def gemv_lora(W, wtype, x, M, K, epilogue, aux, dst, A, B, atype, n, rank, ids, scales, workspace,
+              workspace_bytes=None, stream=None, check=True, **opts):
+    """dst_c = tail(W x'_c + scales_a B_a (A_a x'_c), aux_c), a = ids_c; opts as make_opts (see
+    include/gemvfuse.h)."""
+    o = make_opts(**opts)
+    lo = Lora(_ptr(A), _ptr(B), atype, n, rank, _ptr(ids), _ptr(scales), _ptr(workspace),
+              _nbytes(workspace, workspace_bytes))
+    st = _gemv_lora(_ptr(W), wtype, _ptr(x), M, K, epilogue, _ptr(aux), _ptr(dst), ctypes.byref(lo), ctypes.byref(o),
+                    _stream(stream))
+    if check:
+        _check(st, "gemv_lora")
+    return st
+
+
+def prepare_lora(W, wtype, x, M, K, epilogue, aux, dst, A, B, atype, n, rank, ids, scales, workspace,
+                 workspace_bytes=None, check=True, **opts):
+    """gf_prepare_lora: the call gemv_lora(...) would make, planned once (see Prepared)."""
+    o = make_opts(**opts)
+    lo = Lora(_ptr(A), _ptr(B), atype, n, rank, _ptr(ids), _ptr(scales), _ptr(workspace),
+              _nbytes(workspace, workspace_bytes))
+    h = _vp()
+    st = _prepare_lora(_ptr(W), wtype, _ptr(x), M, K, epilogue, _ptr(aux), _ptr(dst), ctypes.byref(lo),
+                       ctypes.byref(o), ctypes.byref(h))
+    if check:
+        _check(st, "gf_prepare_lora")
+    return Prepared(h.value, (W, x, aux, dst, A, B, ids, scales, workspace, opts)) if st == OK else st

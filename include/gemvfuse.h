@@ -281,6 +281,112 @@ GF_API int gemv_fused_fwht_noalloc(const void* W, int wtype, const float* x, int
                                    const float* fwht_signs, int64_t fwht_block, int64_t nsigns,
                                    uint32_t flags, void* stream);
 
+/* ---- Products whose weights are chosen per column (no counterpart on the pages; the
+ * operators a decode step with a mixture of experts or with per-request adapters needs
+ * next to the products above).  The conventions of this header hold: device pointers,
+ * checks before any launch, nothing allocated; each call has a prepared form. */
+
+/* Routing: for each token t (a row of E logits, `ld` elements apart)
+ *     s = softmax(l_t)  or  1 / (1 + exp(-l_t));      key_e = s_e + bias_e
+ *     with n_group > 1: the experts form n_group groups of E / n_group neighbours; a group's
+ *         score is its largest key (group_top 1) or the sum of its two largest (group_top 2;
+ *         one where only one is choosable); the topk_group best groups stay
+ *     ids_t     = the top_k experts of the largest keys, descending
+ *     weights_t = scale * s of those, first divided by their sum if `norm`
+ * Ties (of keys and of group scores) go to the lowest index; which of two near keys is the
+ * larger is decided in 64 bits.  Without a bias the order is that of the logits.  Logits of
+ * -inf or NaN (and keys made so by the bias) are never chosen and count for nothing; +inf
+ * counts as the largest float.  Places that find no expert get id -1 and weight 0, so a
+ * wholly masked row gives only those.
+ *  ids : int32 [T][top_k], weights : float32 [T][top_k]; neither may overlap an input or the
+ *  other.  T == 0 launches nothing.
+ *  Limits (GF_ERR_UNSUPPORTED beyond): E <= 1024, top_k <= 32, n_group <= 32, T <= 2^24.
+ *  GF_ERR_INVALID: E < 1, top_k < 1 or > E, n_group not dividing E, topk_group outside
+ *  1..n_group, group_top not 1 or 2, 0 < ld < E, a scale that is not finite.  */
+typedef enum { GF_SCORE_SOFTMAX = 0, GF_SCORE_SIGMOID = 1 } gf_score;
+typedef struct {
+  int64_t top_k;
+  int score;           /* gf_score                                                  */
+  int norm;            /* non-zero: divide the chosen weights by their sum          */
+  float scale;         /* factor of every weight (0 is read as 1)                   */
+  const float* bias;   /* [E], added for the choice only; NULL: none                */
+  int64_t n_group;     /* 0 or 1: no groups                                         */
+  int64_t topk_group;  /* groups that stay (read only with n_group > 1)             */
+  int group_top;       /* keys a group's score is made of: 1 or 2 (n_group > 1)     */
+  int64_t ld;          /* elements between rows of logits; 0: E                     */
+  uint32_t flags;      /* GF_FLAG_PDL                                               */
+} gf_route_opts;
+GF_API int gf_route(const float* logits, int64_t T, int64_t E, const gf_route_opts* opts, int32_t* ids,
+                    float* weights, void* stream);
+GF_API int gf_prepare_route(const float* logits, int64_t T, int64_t E, const gf_route_opts* opts, int32_t* ids,
+                            float* weights, gf_prepared** out);
+
+/* The gated feed-forward product of the chosen experts:
+ *     dst_t = aux_t + sum_j weights_tj * Wd_e (silu(Wg_e x_t) * (Wu_e x_t)),   e = ids_tj
+ * for T tokens, each chosen expert's matrices read once for all the tokens that take it
+ * (up to 32 at a time).  The sums of a token run over j in order: deterministic.
+ *  W_gate, W_up : E matrices of M rows and K columns one after another, format `wtype`;
+ *  W_down       : E matrices of K rows and M columns, format `wtype_down`.
+ *  ids          : int32 [T][top_k]; a value outside 0..E-1 takes no expert and adds nothing.
+ *  weights      : float32 [T][top_k].          x : [T][K].
+ *  aux          : [T][K] or NULL (0); dst == aux is allowed (in place).
+ *  workspace    : device memory of at least gf_experts_workspace() bytes, 256-byte aligned,
+ *                 contents undefined before and after; not shared by calls that may overlap.
+ *  Shapes: K and M multiples of 32 (256 for a Q4_K matrix's columns) with 16-byte aligned
+ *  matrices take the tiled kernels, F32 and anything else the generic ones.
+ *  dst may not overlap W_*, x, ids, weights or the workspace; the workspace no argument.
+ *  Limits (GF_ERR_UNSUPPORTED beyond): T <= 256, top_k <= 32, E <= 1024, M and K <= 2^20,
+ *  columns no whole number of the format's blocks.  T == 0 or K == 0 launches nothing. */
+typedef struct {
+  const void* W_gate;
+  const void* W_up;
+  const void* W_down;
+  int wtype, wtype_down;
+  int64_t E, M, K;
+  const int32_t* ids;
+  const float* weights;
+  int64_t top_k;
+  void* workspace;
+  int64_t workspace_bytes;
+  uint32_t flags;      /* GF_FLAG_PDL                                               */
+} gf_experts;
+GF_API int gemv_experts(const gf_experts* ex, const float* x, int64_t T, const float* aux, float* dst,
+                        void* stream);
+GF_API int gf_prepare_experts(const gf_experts* ex, const float* x, int64_t T, const float* aux, float* dst,
+                              gf_prepared** out);
+/* Bytes of workspace for these sizes (any format); negative: a gf_status. */
+GF_API int64_t gf_experts_workspace(int64_t E, int64_t T, int64_t top_k, int64_t M, int64_t K);
+
+/* A shared projection with a low-rank adapter per column:
+ *     dst_c = tail(W x'_c + scales_a * B_a (A_a x'_c), aux_c),   a = ids_c
+ * i.e. gemv_fused_ex (W .. dst, opts as there) with the adapters' products added before the
+ * tail.  x' is x after the prologue in `opts`; the FWHT prologue needs opts->fwht_workspace
+ * (GF_ERR_UNSUPPORTED without).
+ *  A      : n matrices of rank rows and K columns, B : n matrices of M rows and rank columns,
+ *           one after another, format atype (GF_F16 or GF_F32).
+ *  ids    : int32 [ncols]; a value outside 0..n-1 takes no adapter (dst_c = tail(W x'_c)).
+ *  scales : float32 [n] or NULL (1).
+ *  workspace : device memory of at least gf_lora_workspace() bytes, 256-byte aligned,
+ *           contents undefined before and after.
+ *  Limits: rank 1..256 (GF_ERR_INVALID below, GF_ERR_UNSUPPORTED above).  dst may not
+ *  overlap A, B, ids, scales or the workspace; the workspace no argument. */
+typedef struct {
+  const void* A;
+  const void* B;
+  int atype;
+  int64_t n, rank;
+  const int32_t* ids;
+  const float* scales;
+  void* workspace;
+  int64_t workspace_bytes;
+} gf_lora;
+GF_API int gemv_lora(const void* W, int wtype, const float* x, int64_t M, int64_t K, int epilogue, const float* aux,
+                     float* dst, const gf_lora* lora, const gf_opts* opts, void* stream);
+GF_API int gf_prepare_lora(const void* W, int wtype, const float* x, int64_t M, int64_t K, int epilogue,
+                           const float* aux, float* dst, const gf_lora* lora, const gf_opts* opts, gf_prepared** out);
+/* Bytes of workspace for these sizes (any format); negative: a gf_status. */
+GF_API int64_t gf_lora_workspace(int64_t ncols, int64_t M, int64_t K, int64_t rank, int64_t n);
+
 /* Signed FWHT, stand-alone ([FWHT] Overview): for every block of `block` consecutive
  * elements of x[0..n), dst_b = H_block (x_b * s) / sqrt(block), with element i using
  * signs[i % nsigns]; signs == NULL means all +1 (the plain normalised transform).
