@@ -6,8 +6,7 @@
 #include <cstring>
 
 #include "gemvfuse.h"
-#include "gf_device.cuh"
-#include "gf_internal.h"
+#include "tile_mma.cuh"
 
 namespace gf {
 
@@ -100,8 +99,16 @@ static bool columns_ok(int wtype, int64_t n) {
 
 // Whether the tiled kernels take this call (both products or neither).
 static bool experts_tiled(const gf_experts* x) {
-  (void)x;
-  return false;
+  return x->wtype != GF_F32 && x->wtype_down != GF_F32 && x->K % 32 == 0 && x->M % 32 == 0 && x->M > 0 &&
+         aligned_to(x->W_gate, 16) && aligned_to(x->W_up, 16) && aligned_to(x->W_down, 16);
+}
+
+// Columns of a group: matrix tiles are eight columns wide, and a group of more than an
+// expert's tokens costs registers and shared memory for nothing.
+static int experts_cols(int64_t E, int64_t T, int64_t k) {
+  const double mean = static_cast<double>(T) * k / std::min<double>(E, static_cast<double>(T) * k);
+  const int cap = mean <= 5.0 ? 8 : mean <= 12.0 ? 16 : 32;
+  return static_cast<int>(std::min<int64_t>(T, cap));
 }
 
 constexpr int kExpMaxRecs = 4;
@@ -159,6 +166,8 @@ static int plan_experts(const gf_experts* ex, const float* x, int64_t T, const f
   a.hpack = ws + l.hpack;
   a.hmeta = reinterpret_cast<float2*>(ws + l.hmeta);
   a.y = reinterpret_cast<float*>(ws + l.y);
+  a.cols = experts_cols(ex->E, T, ex->top_k);
+  a.order = pack_swapped(wd) ? 1 : 0;
   a.sm_count = lim.sm_count;
   a.smem_optin = lim.smem_optin;
   bool pdl = (ex->flags & GF_FLAG_PDL) != 0;
