@@ -67,7 +67,7 @@ static int plan_route(const float* logits, int64_t T, int64_t E, const gf_route_
 
 // ------------------------------------------------------------------ experts
 struct ExpertsLayout {
-  int64_t slots, groups, n_groups, xpack, xmeta, hpack, hmeta, y, bytes;
+  int64_t slots, groups, n_groups, xrec, hrec, y, max_tiles, bytes;
 };
 
 static int experts_layout(int64_t E, int64_t T, int64_t k, int64_t M, int64_t K, ExpertsLayout& l) {
@@ -80,14 +80,15 @@ static int experts_layout(int64_t E, int64_t T, int64_t k, int64_t M, int64_t K,
     at += (bytes + 255) / 256 * 256;
     return p;
   };
-  const int64_t S = T * k, K32 = (K + 31) / 32 * 32, M32 = (M + 31) / 32 * 32;
+  const int64_t S = T * k, K32 = (K + 31) / 32, M32 = (M + 31) / 32;
+  // every expert's slots in tiles of eight: at most one part-filled tile an expert
+  const int64_t cp = std::min<int64_t>(8, std::max<int64_t>(T, 1));
+  l.max_tiles = std::min(S, std::min(E, S) + S / 8);
   l.n_groups = take(16);
   l.slots = take(S * 4);
   l.groups = take(S * 16);
-  l.xpack = take(T * K32 * 4);
-  l.xmeta = take(T * expert_meta_stride(static_cast<int>(K)) * 8);
-  l.hpack = take(S * M32 * 4);
-  l.hmeta = take(S * expert_meta_stride(static_cast<int>(M)) * 8);
+  l.xrec = take(l.max_tiles * K32 * record_bytes(static_cast<int>(cp)));
+  l.hrec = take(std::max(l.max_tiles * M32 * record_bytes(static_cast<int>(cp)), S * M * 4));
   l.y = take(S * K * 4);
   l.bytes = at;
   return GF_OK;
@@ -107,8 +108,7 @@ static bool experts_tiled(const gf_experts* x) {
 // expert's tokens costs registers and shared memory for nothing.
 static int experts_cols(int64_t E, int64_t T, int64_t k) {
   const double mean = static_cast<double>(T) * k / std::min<double>(E, static_cast<double>(T) * k);
-  const int cap = mean <= 5.0 ? 8 : mean <= 12.0 ? 16 : 32;
-  return static_cast<int>(std::min<int64_t>(T, cap));
+  return static_cast<int>(std::min<int64_t>(T, 8)) < 8 ? static_cast<int>(T) : mean <= 5.0 ? 8 : mean <= 12.0 ? 16 : 32;
 }
 
 constexpr int kExpMaxRecs = 4;
@@ -161,13 +161,13 @@ static int plan_experts(const gf_experts* ex, const float* x, int64_t T, const f
   a.n_groups = reinterpret_cast<int32_t*>(ws + l.n_groups);
   a.slots = reinterpret_cast<int32_t*>(ws + l.slots);
   a.groups = reinterpret_cast<int4*>(ws + l.groups);
-  a.xpack = ws + l.xpack;
-  a.xmeta = reinterpret_cast<float2*>(ws + l.xmeta);
-  a.hpack = ws + l.hpack;
-  a.hmeta = reinterpret_cast<float2*>(ws + l.hmeta);
+  a.xrec = ws + l.xrec;
+  a.hrec = ws + l.hrec;
+  a.cp = static_cast<int>(std::min<int64_t>(8, T));
+  a.max_tiles = static_cast<int>(l.max_tiles);
   a.y = reinterpret_cast<float*>(ws + l.y);
   a.cols = experts_cols(ex->E, T, ex->top_k);
-  a.order = pack_swapped(wd) ? 1 : 0;
+  a.order = pack_order(wd);
   a.sm_count = lim.sm_count;
   a.smem_optin = lim.smem_optin;
   bool pdl = (ex->flags & GF_FLAG_PDL) != 0;

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(32 * kExpGenericWarps) experts_generic_kernel(
   if (row >= rows) return;
   const int64_t rb = expert_row_bytes<WT>(K), off = (static_cast<int64_t>(e) * rows + row) * rb;
   const float* x = GLU ? a.x + static_cast<int64_t>(s / a.k) * K
-                       : reinterpret_cast<const float*>(a.hpack) + static_cast<int64_t>(s) * K;
+                       : reinterpret_cast<const float*>(a.hrec) + static_cast<int64_t>(s) * K;
   float g = 0.0f, u = 0.0f;
   for (int k = lane; k < K; k += 32) {
     const float xv = x[k];
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(32 * kExpGenericWarps) experts_generic_kernel(
   }
   if (lane == 0) {
     if constexpr (GLU)
-      reinterpret_cast<float*>(a.hpack)[static_cast<int64_t>(s) * a.M + row] = tail_silu(g) * u;
+      reinterpret_cast<float*>(a.hrec)[static_cast<int64_t>(s) * a.M + row] = tail_silu(g) * u;
     else
       a.y[static_cast<int64_t>(s) * a.K + row] = a.weights[s] * g;
   }
@@ -93,14 +93,26 @@ static cudaLaunchConfig_t config(dim3 grid, int threads, cudaStream_t st, bool p
 constexpr int kPrepThreads = 1024;
 constexpr int kPrepMaxIter = kExpMaxTokens * kRouteMaxTopK / kPrepThreads;  // 32-slot steps of a warp
 
-static int prep_smem(int E) { return 32 * E * 2 + E * 4 + 32 * 4; }
+static int prep_smem(int E) { return 32 * E * 2 + E * 4 + (32 + 16) * 4; }
+
+// The column tile of a prep CTA: up to eight slots of one expert.
+struct PrepTile {
+  int count;
+  int slot[8];
+};
 
 // The slots of each expert in slot order: a counting sort whose counts are kept per warp
 // (each warp owns a run of consecutive slots) and ranked within a 32-slot step by matching.
-__device__ void list_slots(const ExpertsArgs& a, uint16_t* cnt, uint32_t* offs, uint32_t* wsum) {
+// Every CTA of the launch makes the whole list (a few microseconds, less than another launch)
+// and keeps its own column tile; the first one also writes the list and the column groups.
+__device__ void list_slots(const ExpertsArgs& a, bool write, int my_tile, PrepTile* out, uint16_t* cnt, uint32_t* offs,
+                           uint32_t* wsum, int* range) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int S = a.T * a.k, run = ((S + 31) / 32 + 31) / 32 * 32;  // slots of a warp
-  for (int i = threadIdx.x; i < 32 * a.E; i += kPrepThreads) cnt[i] = 0;
+  const int S = a.T * a.k;
+  const int run = ((S + 31) / 32 + 31) / 32 * 32;  // slots of a warp
+  const int nw = (S + run - 1) / run;              // warps that have some
+  for (int i = threadIdx.x; i < nw * a.E; i += kPrepThreads) cnt[i] = 0;
+  if (threadIdx.x < 2) range[threadIdx.x] = 0;
   __syncthreads();
   int ex[kPrepMaxIter], rank[kPrepMaxIter];
   uint16_t* mine = cnt + w * a.E;
@@ -108,7 +120,7 @@ __device__ void list_slots(const ExpertsArgs& a, uint16_t* cnt, uint32_t* offs, 
   for (int j = 0; j < kPrepMaxIter; ++j) {
     ex[j] = -1;
     rank[j] = 0;
-    if (32 * j < run) {
+    if (32 * j < run && w < nw) {
       const int s = w * run + 32 * j + lane;
       const int e = s < S ? a.ids[s] : -1;
       const bool valid = e >= 0 && e < a.E;
@@ -125,166 +137,203 @@ __device__ void list_slots(const ExpertsArgs& a, uint16_t* cnt, uint32_t* offs, 
     }
   }
   __syncthreads();
-  // per expert: offsets of the warps' runs, then of the experts and of their column groups
-  // (slots in the low half of a word, groups in the high one: both at most 8192 in all)
+  // per expert: offsets of the warps' runs, then of the experts and of their column tiles
+  // (slots in the low half of a word, tiles in the high one: both at most 8192 in all)
   const int e = threadIdx.x;
   uint32_t total = 0;
   if (e < a.E)
-    for (int q = 0; q < 32; ++q) {
+    for (int q = 0; q < nw; ++q) {
       const uint32_t c = cnt[q * a.E + e];
       cnt[q * a.E + e] = static_cast<uint16_t>(total);
       total += c;
     }
-  const uint32_t ng = (total + a.cols - 1) / a.cols;
-  const uint32_t v = total | (ng << 16);
-  uint32_t incl = v;
+  const uint32_t nt = (total + 7) / 8, gt = (a.cols + 7) / 8;  // column tiles of the expert, of a full group
+  const uint32_t ng = (nt + gt - 1) / gt;
+  auto scan = [&](uint32_t v, uint32_t& all) -> uint32_t {  // exclusive over the CTA
+    uint32_t incl = v;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) wsum[w] = incl;
+    __syncthreads();
+    const uint32_t ws = wsum[lane];
+    uint32_t before = ws;  // every warp scans the warps' sums
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += up;
+    }
+    all = __shfl_sync(0xffffffffu, before, 31);
+    const uint32_t mine_before = __shfl_sync(0xffffffffu, before - ws, w);
+    __syncthreads();
+    return mine_before + incl - v;
+  };
+  uint32_t all;
+  const uint32_t ex0 = scan(total | (nt << 16), all);
+  const uint32_t off = ex0 & 0xffffu, t0 = ex0 >> 16;
+  if (e < a.E) offs[e] = off;
+  if (static_cast<uint32_t>(my_tile) >= t0 && static_cast<uint32_t>(my_tile) < t0 + nt) {
+    const uint32_t f = 8u * (static_cast<uint32_t>(my_tile) - t0);
+    range[0] = static_cast<int>(off + f);
+    range[1] = static_cast<int>(min(8u, total - f));
   }
-  if (lane == 31) wsum[w] = incl;
-  __syncthreads();
-  uint32_t before = 0;
-  for (int q = 0; q < w; ++q) before += wsum[q];
-  const uint32_t excl = before + incl - v;
-  const uint32_t off = excl & 0xffffu, gbase = excl >> 16;
-  if (e < a.E) {
-    offs[e] = off;
-    for (uint32_t i = 0; i < ng; ++i)
-      a.groups[gbase + i] = make_int4(e, static_cast<int>(off + i * a.cols),
-                                      static_cast<int>(min(static_cast<uint32_t>(a.cols), total - i * a.cols)), 0);
+  if (write) {
+    uint32_t groups;
+    const uint32_t g0 = scan(ng, groups);
+    for (uint32_t i = 0; i < ng; ++i) {
+      const uint32_t f = i * gt * 8u;
+      a.groups[g0 + i] = make_int4(e, static_cast<int>(off + f), static_cast<int>(min(gt * 8u, total - f)),
+                                   static_cast<int>(t0 + i * gt));
+    }
+    if (threadIdx.x == 0) *a.n_groups = static_cast<int>(groups);
   }
-  if (e == kPrepThreads - 1) *a.n_groups = static_cast<int>((before + incl) >> 16);
   __syncthreads();
+  const int first = range[0], count = range[1];
+  if (threadIdx.x == 0) out->count = count;
 #pragma unroll
   for (int j = 0; j < kPrepMaxIter; ++j)
-    if (ex[j] >= 0) a.slots[offs[ex[j]] + mine[ex[j]] + rank[j]] = w * run + 32 * j + lane;
+    if (ex[j] >= 0) {
+      const int pos = static_cast<int>(offs[ex[j]]) + mine[ex[j]] + rank[j], s = w * run + 32 * j + lane;
+      if (write) a.slots[pos] = s;
+      if (pos >= first && pos < first + count) out->slot[pos - first] = s;
+    }
+  __syncthreads();
 }
 
-// Column c of x packed with one scale for the whole column.
-__device__ void pack_column(const float* x, int K, uint8_t* xp, float2* meta, bool swapped, float* wmax) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, n4 = K / 4;
+// The column tile's records: 128 threads a column, one scale for the whole column.
+__device__ void pack_tile(const ExpertsArgs& a, int tile, const PrepTile& pt, float* wmax) {
+  const int c = threadIdx.x >> 7, i0 = threadIdx.x & 127, lane = threadIdx.x & 31;
+  const bool live = c < pt.count;
+  const int n4 = a.K / 4, cp = a.cp, order = pack_order(a.wtype);
+  const float* x = a.x + static_cast<int64_t>(live ? pt.slot[c] / a.k : 0) * a.K;
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
   auto load = [&](int i) -> float4 {
+    if (!live || i >= n4) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (vec) return reinterpret_cast<const float4*>(x)[i];
     return make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
   };
-  constexpr int kKeep = 2;  // groups of four a thread keeps between the two passes
+  constexpr int kKeep = 4;  // groups of four a thread keeps between the two passes
   float4 keep[kKeep];
   float m = 0.0f;
 #pragma unroll
-  for (int j = 0; j < kKeep; ++j) {
-    const int i = threadIdx.x + j * kPrepThreads;
-    keep[j] = i < n4 ? load(i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    m = fmaxf(fmaxf(m, fmaxf(finite_abs(keep[j].x), finite_abs(keep[j].y))),
-              fmaxf(finite_abs(keep[j].z), finite_abs(keep[j].w)));
-  }
-  for (int i = threadIdx.x + kKeep * kPrepThreads; i < n4; i += kPrepThreads) {
-    const float4 v = load(i);
-    m = fmaxf(fmaxf(m, fmaxf(finite_abs(v.x), finite_abs(v.y))), fmaxf(finite_abs(v.z), finite_abs(v.w)));
-  }
+  for (int j = 0; j < kKeep; ++j) keep[j] = load(i0 + 128 * j);
+  auto top = [](float4 v) {
+    return fmaxf(fmaxf(finite_abs(v.x), finite_abs(v.y)), fmaxf(finite_abs(v.z), finite_abs(v.w)));
+  };
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j) m = fmaxf(m, top(keep[j]));
+  for (int i = i0 + 128 * kKeep; i < n4; i += 128) m = fmaxf(m, top(load(i)));
   m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-  if (lane == 0) wmax[w] = m;
+  if (lane == 0) wmax[threadIdx.x >> 5] = m;
   __syncthreads();
-  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(wmax[lane])));
+#pragma unroll
+  for (int q = 0; q < 4; ++q) m = fmaxf(m, wmax[4 * c + q]);
   const float sc = pack_scale(m), inv = pow2_inverse(sc);
+  const int rec = record_bytes(cp);
+  uint8_t* base = a.xrec + static_cast<int64_t>(tile) * (a.K / 32) * rec;
   auto put = [&](int i, float4 v) {
     v.x *= sc; v.y *= sc; v.z *= sc; v.w *= sc;
     float sum = (v.x + v.y) + (v.z + v.w);
 #pragma unroll
     for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (i < n4) {
-      reinterpret_cast<uint4*>(xp)[i] = pack_group(v, swapped);
-      if ((i & 7) == 0) meta[i >> 3] = make_float2(inv, sum);
+    if (live && i < n4) {
+      uint8_t* r = base + static_cast<int64_t>(i >> 3) * rec;
+      *reinterpret_cast<uint4*>(r + record_offset(i & 7, c, cp, order)) = pack_group(v, order == ORDER_NIBBLE);
+      if ((i & 7) == 0) *reinterpret_cast<float2*>(r + cp * 128 + c * 8) = make_float2(inv, sum);
     }
   };
 #pragma unroll
-  for (int j = 0; j < kKeep; ++j) put(threadIdx.x + j * kPrepThreads, keep[j]);
-  for (int i0 = kKeep * kPrepThreads; i0 < n4; i0 += kPrepThreads) {
-    const int i = i0 + threadIdx.x;
-    put(i, i < n4 ? load(i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f));
-  }
+  for (int j = 0; j < kKeep; ++j) put(i0 + 128 * j, keep[j]);
+  for (int b = 128 * kKeep; b < n4; b += 128) put(b + i0, load(b + i0));
 }
 
 __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(const __grid_constant__ ExpertsArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ PrepTile pt;
+  __shared__ float wmax[kPrepThreads / 32];
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x == 0) {
-    uint32_t* offs = reinterpret_cast<uint32_t*>(smem);
-    uint32_t* wsum = offs + a.E;
-    list_slots(a, reinterpret_cast<uint16_t*>(wsum + 32), offs, wsum);
-  } else {
-    const int64_t c = blockIdx.x - 1;
-    pack_column(a.x + c * a.K, a.K, a.xpack + c * a.K * 4, a.xmeta + c * expert_meta_stride(a.K), pack_swapped(a.wtype),
-                reinterpret_cast<float*>(smem));
-  }
+  uint32_t* offs = reinterpret_cast<uint32_t*>(smem);
+  uint32_t* wsum = offs + a.E;
+  int* range = reinterpret_cast<int*>(wsum + 32);
+  const int tile = static_cast<int>(blockIdx.x);
+  list_slots(a, tile == 0, tile, &pt, reinterpret_cast<uint16_t*>(range + 16), offs, wsum, range);
+  if (pt.count > 0) pack_tile(a, tile, pt, wmax);
 }
 
 // ------------------------------------------------------------------ tiled products
-template <int WT, int MODE, int NT, int WR>
-static cudaError_t launch_tile_t(const TileArgs& t, int grid, int smem, cudaStream_t st, bool pdl) {
-  auto kern = tile_kernel<WT, MODE, NT, WR>;
-  static int configured[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && configured[dev] < smem) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    configured[dev] = smem;
-  }
-  cudaLaunchAttribute attr;
-  cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(grid)), 32 * (1 + kTileWarpsK * WR), st, pdl, &attr);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  return cudaLaunchKernelEx(&cfg, kern, t);
+// Tensor map over the rows of all matrices of one kind.
+template <int WT>
+static int tile_map(const void* W, int64_t all_rows, int row_bytes, CUtensorMap* out) {
+  if (WT == WT_F16)
+    return cached_map_2d(W, kMapF16, static_cast<uint64_t>(row_bytes / 2), static_cast<uint64_t>(all_rows), 64, 32, true, out);
+  const int p = tile_period(row_bytes);
+  return cached_map_2d(W, kMapF16, static_cast<uint64_t>(row_bytes) * p / 2, static_cast<uint64_t>(all_rows / p),
+                       static_cast<uint32_t>(tile_pitch<WT>(p) / 2), static_cast<uint32_t>(32 / p), false, out);
 }
 
-template <int WT, int MODE, int NT, int WR>
-static cudaError_t launch_tile_shape(TileArgs t, const ExpertsArgs& a, cudaStream_t st, bool pdl) {
-  constexpr int kCtas = (WR == 1 && NT <= 2) ? 2 : 1;  // CTAs per SM the registers allow
-  const int stage = tile_stage_bytes<WT, NT>(WR, a.cols), fixed = kTileBarBytes + tile_red_bytes(WR);
-  // as many CTAs per SM as leave each three stages
+template <int WT, int MODE, int NT>
+static int launch_tile_t(TileArgs t, const ExpertsArgs& a, cudaStream_t st, bool pdl) {
+  auto kern = tile_kernel<WT, MODE, NT>;
+  CUtensorMap m0, m1;
+  const int64_t all_rows = static_cast<int64_t>(a.E) * t.rows;
+  int e = tile_map<WT>(a.W, all_rows, t.row_bytes, &m0);
+  if (e != cudaSuccess) return e;
+  m1 = m0;
+  if (MODE == TILE_GLU) e = tile_map<WT>(a.W2, all_rows, t.row_bytes, &m1);
+  if (e != cudaSuccess) return e;
+  constexpr int kCtas = NT <= 2 ? 2 : 1;  // CTAs per SM the registers allow
+  const int stage = tile_stage_bytes<WT>(t.period, NT, t.cp), fixed = kTileBarBytes + kTileRedBytes + 1024;
+  // as many CTAs per SM as leave each three stages; 1 KB a CTA is the system's
   int ctas = kCtas, ns = 0;
   for (; ctas >= 1; --ctas) {
-    const int budget = ctas == 1 ? a.smem_optin : (a.smem_optin + 1024) / ctas - 1024;  // 1 KB a CTA is the system's
+    const int budget = ctas == 1 ? a.smem_optin : (a.smem_optin + 1024) / ctas - 1024;
     ns = std::min(kTileMaxStages, (budget - fixed) / stage);
     if (ns >= 3 || ctas == 1) break;
   }
   if (ns < 2) return cudaErrorInvalidConfiguration;
   t.NS = ns;
-  return launch_tile_t<WT, MODE, NT, WR>(t, ctas * a.sm_count, fixed + ns * stage, st, pdl);
+  const int smem = fixed + ns * stage;
+  static int configured[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && configured[dev] < smem) {
+    const cudaError_t c = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (c != cudaSuccess) return c;
+    configured[dev] = smem;
+  }
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(ctas * a.sm_count)), kTileThreads, st, pdl, &attr);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  return cudaLaunchKernelEx(&cfg, kern, m0, m1, t);
 }
 
 template <int WT, int MODE>
-static cudaError_t launch_tile_cols(const TileArgs& t, const ExpertsArgs& a, cudaStream_t st, bool pdl) {
-  if (a.cols <= 8) return launch_tile_shape<WT, MODE, 1, 1>(t, a, st, pdl);
-  if (a.cols <= 16) return launch_tile_shape<WT, MODE, 2, 1>(t, a, st, pdl);
-  return launch_tile_shape<WT, MODE, 4, 1>(t, a, st, pdl);
+static int launch_tile_cols(const TileArgs& t, const ExpertsArgs& a, cudaStream_t st, bool pdl) {
+  if (a.cols <= 8) return launch_tile_t<WT, MODE, 1>(t, a, st, pdl);
+  if (a.cols <= 16) return launch_tile_t<WT, MODE, 2>(t, a, st, pdl);
+  return launch_tile_t<WT, MODE, 4>(t, a, st, pdl);
 }
 
 template <int MODE>
-static cudaError_t launch_tiles(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
+static int launch_tiles(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
   TileArgs t = {};
-  t.W = a.W;
-  t.W2 = a.W2;
   t.rows = MODE == TILE_GLU ? a.M : a.K;
   t.K = MODE == TILE_GLU ? a.K : a.M;
+  t.row_bytes = static_cast<int>(row_bytes_of(a.wtype, t.K));
+  t.period = tile_period(t.row_bytes);
   t.groups = a.groups;
   t.n_groups = a.n_groups;
   t.slots = a.slots;
-  t.slot_div = MODE == TILE_GLU ? a.k : 1;
-  t.xpack = MODE == TILE_GLU ? a.xpack : a.hpack;
-  t.xmeta = MODE == TILE_GLU ? a.xmeta : a.hmeta;
-  t.cols = a.cols;
+  t.records = MODE == TILE_GLU ? a.xrec : a.hrec;
+  t.cp = a.cp;
   t.err = a.err;
-  t.hpack = a.hpack;
-  t.hmeta = a.hmeta;
-  t.h_swapped = a.order;
+  t.out_records = a.hrec;
+  t.out_order = a.order;
   t.weights = a.weights;
   t.y = a.y;
-  t.row_bytes = static_cast<int>(row_bytes_of(a.wtype, t.K));
-  t.total_bytes = static_cast<int64_t>(a.E) * t.rows * t.row_bytes;
   switch (a.wtype) {
     case WT_F16: return launch_tile_cols<WT_F16, MODE>(t, a, st, pdl);
     case WT_Q8_0: return launch_tile_cols<WT_Q8_0, MODE>(t, a, st, pdl);
@@ -324,7 +373,7 @@ int launch_experts(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
         if (e != cudaSuccess) return e;
         configured[dev] = smem;
       }
-      cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(1 + a.T)), kPrepThreads, st, pdl, &attr);
+      cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(a.max_tiles)), kPrepThreads, st, pdl, &attr);
       cfg.dynamicSmemBytes = static_cast<size_t>(smem);
       return cudaLaunchKernelEx(&cfg, experts_prep_kernel, a);
     }

@@ -619,8 +619,8 @@ int g_map_used = 0, g_map_next = 0;
 }  // namespace
 
 // A dense row-major [rows][inner] operand (rows `inner` elements apart).
-static int cached_map(const void* base, int dtype, uint64_t inner, uint64_t rows, uint32_t box_inner,
-                      uint32_t box_rows, bool swizzle128, CUtensorMap* out) {
+int cached_map_2d(const void* base, int dtype, uint64_t inner, uint64_t rows, uint32_t box_inner, uint32_t box_rows,
+                  bool swizzle128, CUtensorMap* out) {
   std::lock_guard<std::mutex> lock(g_map_mu);
   for (int i = 0; i < g_map_used; ++i) {
     const MapEntry& e = g_maps[i];
@@ -652,12 +652,12 @@ int launch_tc(const TcPlan& p, const void* W, cudaStream_t st, bool pdl) {
   CUtensorMap wmap, xmap;  // the type carries the 64-byte alignment the driver requires
   // W: 128 x 64 f16 boxes, 128-byte swizzle; x (beyond 8 columns): [ncols][K] fp32, one
   // stage of every column
-  int e = cached_map(W, kMapF16, static_cast<uint64_t>(p.a.K), static_cast<uint64_t>(p.a.M), kTcK, kTcRows, true,
+  int e = cached_map_2d(W, kMapF16, static_cast<uint64_t>(p.a.K), static_cast<uint64_t>(p.a.M), kTcK, kTcRows, true,
                      &wmap);
   if (e != cudaSuccess) return e;
   std::memset(&xmap, 0, sizeof(xmap));  // unused up to 8 columns
   if (p.a.ncols > 8) {
-    e = cached_map(p.a.x, kMapF32, static_cast<uint64_t>(p.a.K), static_cast<uint64_t>(p.a.ncols),
+    e = cached_map_2d(p.a.x, kMapF32, static_cast<uint64_t>(p.a.K), static_cast<uint64_t>(p.a.ncols),
                    static_cast<uint32_t>(p.a.subs * kTcK), static_cast<uint32_t>(p.a.ncols), false, &xmap);
     if (e != cudaSuccess) return e;
   }

@@ -166,6 +166,9 @@ int launch_tc(const TcPlan& p, const void* W, cudaStream_t st, bool pdl);
 // elements, `stride_bytes` apart, with boxes of box_inner x box_rows (128-byte swizzle or
 // none).  `map` points to a 64-byte aligned CUtensorMap.  Returns a cudaError_t.
 enum { kMapU8 = 0, kMapF16 = 1, kMapF32 = 2 };
+// The same over a dense [rows][inner] operand, from the cache of recent maps.
+int cached_map_2d(const void* base, int dtype, uint64_t inner, uint64_t rows, uint32_t box_inner, uint32_t box_rows,
+                  bool swizzle128, ::CUtensorMap_st* out);
 int encode_map_2d(::CUtensorMap_st* map, int dtype, const void* base, uint64_t inner, uint64_t rows,
                   uint64_t stride_bytes, uint32_t box_inner, uint32_t box_rows, bool swizzle128);
 
@@ -239,12 +242,10 @@ int launch_route(const RouteArgs& a, cudaStream_t st, bool pdl);
 // The chosen experts' gated product (experts.cu): one launch of one phase.
 constexpr int kExpMaxTokens = 256;
 enum { EXP_PREP = 0, EXP_GLU = 1, EXP_DOWN = 2, EXP_COMBINE = 3, EXP_GLU_GENERIC = 4, EXP_DOWN_GENERIC = 5 };
-// float2 per 32 elements of a packed row, padded to whole 16-byte words.
-__host__ __device__ constexpr int expert_meta_stride(int n) { return ((n + 31) / 32 + 1) / 2 * 2; }
 struct ExpertsArgs {
   int phase;
   int wtype;            // of this phase's matrices
-  int order;            // element order of the packed x this phase writes (see experts.cu)
+  int order;            // element order of the records that the gated product writes
   const uint8_t* W;     // gate (EXP_GLU*) or down (EXP_DOWN*)
   const uint8_t* W2;    // up
   const float* x;
@@ -255,15 +256,15 @@ struct ExpertsArgs {
   unsigned* err;
   int E, T, k;
   int M, K;             // ffn width, model width
-  int cols;             // columns per group (8, 16 or 32)
+  int cols;             // columns per group (8, 16 or 32, or the tokens if fewer than 8)
+  int cp;               // columns stored per column tile: min(8, T)
+  int max_tiles;        // upper bound on the column tiles of all experts
   // workspace
   int32_t* slots;       // [T k] slots by expert, in slot order
-  int4* groups;         // {expert, first, count, 0} of each column group
+  int4* groups;         // {expert, first entry, columns, first column tile} of each column group
   int32_t* n_groups;
-  uint8_t* xpack;       // [T][K * 4]
-  float2* xmeta;        // [T][meta_stride(K)]
-  uint8_t* hpack;       // [T k][M * 4], or h itself in float32 (generic)
-  float2* hmeta;        // [T k][meta_stride(M)]
+  uint8_t* xrec;        // [column tile][K / 32] records of packed x (see tile_mma.cuh)
+  uint8_t* hrec;        // the same of the gated values, or [T k][M] float32 (generic)
   float* y;             // [T k][K]
   int sm_count, smem_optin;
 };

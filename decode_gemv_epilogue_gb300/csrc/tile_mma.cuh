@@ -16,8 +16,8 @@
 // accumulators in tensor memory that is one read-back per two instructions.
 #pragma once
 
-#include "gf_device.cuh"
 #include "gf_internal.h"
+#include "tc_device.cuh"
 
 namespace gf {
 
@@ -74,11 +74,26 @@ __device__ __forceinline__ uint32_t lds32_half_aligned(uint32_t a) {
 }
 
 // ------------------------------------------------------------------ packing x
-// A packed column: per 32 elements 128 bytes, per four elements 4q .. 4q+3 the 16 bytes
-// {hi, hi, hi, hi, lo, lo, lo, lo}.  For the nibble formats the four are in the order
-// 0, 2, 1, 3, the order in which two masks take the nibbles of a code word apart.
-// Beside it per 32 elements {2^-s, the sum of x 2^s}.
-__host__ __device__ constexpr bool pack_swapped(int wt) { return wt == WT_Q4_0 || wt == WT_Q4_K; }
+// Packed columns lie in the order in which the matrix instruction takes them.  Eight columns
+// form a column tile, and for every 32 elements a column tile has one record:
+//   [step s of 2][column of cp][thread t of 4] 16 bytes {hi, hi, hi, hi, lo, lo, lo, lo},
+//   then per column {2^-s, the sum of x 2^s over the 32 elements};
+// cp = min(8, columns of the call) columns are stored, so that a single column does not move
+// eight.  A warp's 16-byte reads of a step are then consecutive, and the records of a K chunk
+// are one piece of memory for one bulk copy.  Which four elements (s, t) holds is the
+// weights' choice: 16 s + 4 t + .. in the order 0, 2, 1, 3 for the nibble formats (two masks
+// take a code word apart in that order), 16 s + 4 t + 0..3 for Q8_0, and 8 t + 4 s + 0..3
+// for F16 (a thread then reads 16 bytes of a row at once).
+enum { ORDER_NIBBLE = 0, ORDER_BYTE = 1, ORDER_F16 = 2 };
+__host__ __device__ constexpr int pack_order(int wt) {
+  return wt == WT_F16 ? ORDER_F16 : wt == WT_Q8_0 ? ORDER_BYTE : ORDER_NIBBLE;
+}
+__host__ __device__ constexpr int record_bytes(int cp) { return cp * 128 + (cp * 8 + 15) / 16 * 16; }
+// Byte offset in a record of the four elements 4q .. 4q + 3 of column c.
+__device__ __forceinline__ uint32_t record_offset(uint32_t q, uint32_t c, uint32_t cp, int order) {
+  const uint32_t s = order == ORDER_F16 ? (q & 1u) : (q >> 2), t = order == ORDER_F16 ? (q >> 1) : (q & 3u);
+  return (s * cp + c) * 64u + t * 16u;
+}
 
 // 2^s for the largest magnitude m (finite), s in [-112, 126]; 1 for m = 0.
 __device__ __forceinline__ float pack_scale(float m) {
@@ -113,12 +128,6 @@ __device__ __forceinline__ uint4 pack_group(float4 v, bool swapped) {
   return swapped ? make_uint4(half_pair(a.hi, c.hi), half_pair(b.hi, d.hi), half_pair(a.lo, c.lo), half_pair(b.lo, d.lo))
                  : make_uint4(half_pair(a.hi, b.hi), half_pair(c.hi, d.hi), half_pair(a.lo, b.lo), half_pair(c.lo, d.lo));
 }
-// Byte offset in a packed 32-element block of the hi half of element i (lo: 8 further).
-__device__ __forceinline__ uint32_t packed_offset(uint32_t i, bool swapped) {
-  const uint32_t p = i & 3u, slot = swapped ? ((p & 1u) << 1) | (p >> 1) : p;
-  return (i >> 2) * 16u + slot * 2u;
-}
-
 __device__ __forceinline__ float finite_abs(float v) {
   const float a = fabsf(v);
   return a <= 3.402823466e38f ? a : 0.0f;  // Inf and NaN do not set the scale
@@ -128,8 +137,8 @@ __device__ __forceinline__ float finite_abs(float v) {
 // One 32-element block of rows g and g + 8 of a 16-row tile as the A operands of two
 // m16n8k16 steps: a[s] = {row g k-slots 2t, 2t+1; row g+8 the same; row g slots 2t+8, 2t+9;
 // row g+8 the same}, thread (g, t) = (lane / 4, lane % 4).  Which element sits in which
-// k-slot is free as long as the packed x has the same one; step s, thread t holds elements
-// 16 s + 4 t .. + 3 of the block.  d: the rows' block scales (unused for F16).
+// k-slot is free as long as the packed x has the same one (see pack_order).  d: the rows'
+// block scales (unused for F16).
 // d * sc[j] and dmin * m[j] of a Q4_K super-block from its first 16 bytes (both exact).  The
 // 6-bit integers become floats in the low bits of 2^23: a conversion instruction has a
 // quarter of an addition's rate.
@@ -145,10 +154,10 @@ __device__ __forceinline__ void q4k_scale_of(const uint4 hd, uint32_t j, float& 
 template <int WT>
 __device__ __forceinline__ void load_block_row(uint32_t row, uint32_t blk, uint32_t t, uint32_t (&a0)[2],
                                                uint32_t (&a1)[2], float& d) {
-  if constexpr (WT == WT_F16) {
-    const uint2 u = lds64(row + blk * 64u + t * 8u), v = lds64(row + blk * 64u + 32u + t * 8u);
+  if constexpr (WT == WT_F16) {  // the thread's 16 bytes, swizzled: see tile_kernel
+    const uint4 u = lds128(row);
     a0[0] = u.x; a0[1] = u.y;
-    a1[0] = v.x; a1[1] = v.y;
+    a1[0] = u.z; a1[1] = u.w;
     d = 1.0f;
   } else if constexpr (WT == WT_Q8_0) {
     const uint32_t p = row + blk * 34u;
@@ -184,114 +193,103 @@ __device__ __forceinline__ void load_block_row(uint32_t row, uint32_t blk, uint3
 
 // ------------------------------------------------------------------ the tiled kernel
 // A work item is (column group, row tile): up to 8 NT columns that share one matrix, and
-// 64 WR rows of it (gated: 32 WR gate rows and the same up rows).  Warp 0 streams the
-// item's K chunks -- the rows' weights, one bulk copy per row, and the columns' packed x --
-// through a ring of shared-memory stages.  8 WR consumer warps: row group wr takes 64 rows
-// (four 16-row matrix tiles), and the 8 warps of a row group share the K axis block by
-// block, so that each packed x fragment that a warp loads serves four matrix tiles.  At the
-// end of an item the warps' accumulators are added through shared memory in warp order
-// (deterministic) and the tail is applied.
+// 64 rows of it (gated: 32 gate rows and the same up rows).  Warp 0 streams the item's K
+// chunks of 256 -- the rows' weights by tensor-map copies of 32 rows, the columns' records
+// by one bulk copy per column tile -- through a ring of shared-memory stages.  The eight
+// consumer warps share the K axis: a warp takes one 32-element block of the chunk for all 64
+// rows (four 16-row matrix tiles), so that a packed x fragment, once loaded, serves four
+// matrix tiles.  At the end of an item the warps' accumulators are added through shared
+// memory in warp order (deterministic) and the tail is applied.
 //
-// Rows lie in a stage `pitch` bytes apart, an odd multiple of 16 (of 32 for F16): the eight
-// rows that a warp reads together then fall on distinct banks.  Bulk copies want 16-byte
-// boundaries: a row that starts or ends off one is copied with the bytes around it, cut at
-// the end of the matrices (the last bytes are then copied by hand), and read from the
-// offset.
+// (A first version copied every row of a chunk by its own bulk copy: each took about 90
+// cycles of an SM's copy engine whatever its size, three to ten times the time of the bytes.)
+//
+// Rows in a stage.  Q4_0, Q4_K: 144 bytes a row and chunk, Q8_0: 272, odd multiples of 16, so
+// that the eight rows a warp reads together fall on distinct banks.  Where K is no multiple
+// of 256, rows of these formats are no whole number of 16-byte words, which a tensor map
+// cannot express; but `period` = 2, 4 or 8 rows together are, and the map is laid over
+// those: the rows of each residue are copied apart, from the 16-byte boundary before them
+// and 32 bytes wider.  F16: four boxes of 64 elements, 128-byte swizzled; lanes 2q and
+// 2q + 1 take rows q and q + 4 of eight, so that a quarter warp's reads cover all banks.
 //
 // Every wait is bounded; a timeout sets the device error word, and the kernel returns after
 // draining its own copies.
-constexpr int kTileRows = 64;           // rows of a row group
-constexpr int kTileWarpsK = 8;          // warps sharing K in a row group
+constexpr int kTileRows = 64;
+constexpr int kTileK = 256;
+constexpr int kTileWarps = 8;           // consumer warps, sharing K
+constexpr int kTileThreads = 32 * (1 + kTileWarps);
 constexpr int kTileMaxStages = 8;
+constexpr int kTileBarBytes = 256;
 constexpr int kRedPitch = kTileRows + 4;
-enum { TILE_GLU = 0, TILE_DOWN = 1, TILE_LIN = 2 };
+constexpr int kTileRedBytes = kTileWarps * 8 * kRedPitch * 4;  // the warps' sums of eight columns
+enum { TILE_GLU = 0, TILE_DOWN = 1 };
 
-// K elements of a stage: two 32-element blocks per warp for the 4-bit formats, one for the
-// others and for wide groups, whose packed x fills the stage.
-template <int WT, int NT>
-__host__ __device__ constexpr int tile_kc() {
-  return ((WT == WT_Q4_0 || WT == WT_Q4_K) && NT <= 2) ? 512 : 256;
+template <int WT>
+__host__ __device__ constexpr int tile_seg() {  // bytes of a row and chunk
+  return WT == WT_F16 ? 2 * kTileK : WT == WT_Q8_0 ? kTileK / 32 * 34 : 144;
+}
+// Rows that make a whole number of 16-byte words.
+__host__ __device__ constexpr int tile_period(int row_bytes) {
+  return row_bytes % 16 == 0 ? 1 : row_bytes % 8 == 0 ? 2 : row_bytes % 4 == 0 ? 4 : 8;
 }
 template <int WT>
-__host__ __device__ constexpr int tile_seg(int k) {
-  return WT == WT_F16 ? 2 * k : WT == WT_Q8_0 ? (k / 32) * 34 : WT == WT_Q4_0 ? (k / 32) * 18 : (k / 256) * 144;
+__host__ __device__ constexpr int tile_pitch(int period) { return tile_seg<WT>() + (period > 1 ? 32 : 0); }
+// Bytes of the rows of one residue in a 32-row half (boxes start on 128-byte boundaries).
+template <int WT>
+__host__ __device__ constexpr int tile_part(int period) {
+  return (32 / period * tile_pitch<WT>(period) + 127) / 128 * 128;
 }
-// Bytes between the rows of a stage: room for the chunk and up to 30 bytes around it, and
-// an odd multiple of 16 (32 for F16, whose rows are always whole 16-byte words).
-template <int WT, int NT>
-__host__ __device__ constexpr int tile_pitch() {
-  constexpr int seg = tile_seg<WT>(tile_kc<WT, NT>());
-  if constexpr (WT == WT_F16) return seg + 32;
-  constexpr int need = (seg + (WT == WT_Q4_K ? 0 : 30) + 15) / 16;
-  return 16 * (need % 2 ? need : need + 1);
+template <int WT>
+__host__ __device__ constexpr int tile_weight_bytes(int period) {
+  return WT == WT_F16 ? kTileRows * kTileK * 2 : 2 * period * tile_part<WT>(period);
 }
-constexpr int kXPitchPad = 64;     // packed columns half a bank row apart
-constexpr int kMetaPitchPad = 16;
-template <int WT, int NT>
-__host__ __device__ constexpr int tile_xpitch() { return tile_kc<WT, NT>() * 4 + kXPitchPad; }
-template <int WT, int NT>
-__host__ __device__ constexpr int tile_mpitch() { return tile_kc<WT, NT>() / 4 + kMetaPitchPad; }
-template <int WT, int NT>
-__host__ __device__ constexpr int tile_stage_bytes(int wr, int cols) {
-  return (kTileRows * wr * tile_pitch<WT, NT>() + cols * (tile_xpitch<WT, NT>() + tile_mpitch<WT, NT>()) + 16 + 127) / 128 * 128;
+template <int WT>
+__host__ __device__ constexpr int tile_stage_bytes(int period, int nt, int cp) {
+  return (tile_weight_bytes<WT>(period) + 16 + nt * (kTileK / 32) * record_bytes(cp) + 1023) / 1024 * 1024;
 }
-constexpr int kTileBarBytes = 256;
-// The warps' sums of eight columns at a time.
-__host__ __device__ constexpr int tile_red_bytes(int wr) { return wr * kTileWarpsK * 8 * kRedPitch * 4; }
 
 struct TileArgs {
-  const uint8_t* W;       // matrices one after another
-  const uint8_t* W2;      // gated: the up matrices
-  int64_t total_bytes;    // of all matrices of W (of W2 the same)
-  int rows, K, row_bytes; // rows of one matrix (outputs), columns
-  const int4* groups;     // {matrix, first slot entry, columns, 0}
+  int rows, K, row_bytes;   // rows of one matrix (outputs), columns
+  int period;
+  const int4* groups;       // {matrix, first entry, columns, first column tile}
   const int32_t* n_groups;
-  const int32_t* slots;   // slot of each entry
-  int slot_div;           // packed column of a slot: slot / slot_div
-  const uint8_t* xpack;
-  const float2* xmeta;
-  int cols;               // columns a stage has room for (<= 8 NT)
+  const int32_t* slots;     // slot of each entry
+  const uint8_t* records;   // [column tile][K / 32] records of x
+  int cp;
   int NS;
   unsigned* err;
   // tails
-  uint8_t* hpack;         // gated: packed output columns, by slot
-  float2* hmeta;
-  int h_swapped;
-  const float* weights;   // down: factor of a slot
-  float* y;               // down: [slot][rows]
+  uint8_t* out_records;     // gated: records of the next product's x
+  int out_order;
+  const float* weights;     // down: factor of a slot
+  float* y;                 // down: [slot][rows]
 };
 
-struct TileRing {
-  uint32_t base, full0, empty0;
-};
-
-// The rows and columns of an item.
-struct TileItem {
-  int4 g;
-  int row0;      // first output row
-};
-
-template <int WT, int MODE, int NT, int WR>
-__global__ void __launch_bounds__(32 * (1 + kTileWarpsK * WR), (WR == 1 && NT <= 2) ? 2 : 1)
-    tile_kernel(const __grid_constant__ TileArgs a) {
-  constexpr int KC = tile_kc<WT, NT>(), P = tile_pitch<WT, NT>(), XP = tile_xpitch<WT, NT>(), MP = tile_mpitch<WT, NT>();
+template <int WT, int MODE, int NT>
+__global__ void __launch_bounds__(kTileThreads, NT <= 2 ? 2 : 1)
+    tile_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
+                const __grid_constant__ TileArgs a) {
   constexpr bool kMeta = MODE == TILE_DOWN || WT == WT_Q4_K;  // per-block scales or sums are read in the loop
-  constexpr int kOutRows = MODE == TILE_GLU ? 32 * WR : kTileRows * WR;
+  constexpr int kOutRows = MODE == TILE_GLU ? 32 : kTileRows;
+  constexpr int kBlocks = kTileK / 32;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(smem), full0 = sbase, empty0 = sbase + 8u * kTileMaxStages;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kTileBarBytes - 8);
   float* red = reinterpret_cast<float*>(smem + kTileBarBytes);
-  const uint32_t ring = sbase + kTileBarBytes + tile_red_bytes(WR);
-  const uint32_t stage_bytes = tile_stage_bytes<WT, NT>(WR, a.cols);
-  const uint32_t xoff = kTileRows * WR * P + 16, moff = xoff + a.cols * XP;
+  const uint32_t ring = (sbase + kTileBarBytes + kTileRedBytes + 1023u) & ~1023u;
+  const uint32_t rec = static_cast<uint32_t>(record_bytes(a.cp));
+  const uint32_t stage_bytes = tile_stage_bytes<WT>(a.period, NT, a.cp);
+  const uint32_t xoff = tile_weight_bytes<WT>(a.period) + 16;  // slack: words are read up to 3 bytes past a row
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < a.NS; ++i) {
       mbar_init(full0 + 8u * i, 1);
-      mbar_init(empty0 + 8u * i, kTileWarpsK * WR);
+      mbar_init(empty0 + 8u * i, kTileWarps);
     }
     fence_mbar_init();
+    prefetch_tmap(&map0);
+    if (MODE == TILE_GLU) prefetch_tmap(&map1);
   }
   __syncthreads();
   pdl_trigger();
@@ -299,91 +297,88 @@ __global__ void __launch_bounds__(32 * (1 + kTileWarpsK * WR), (WR == 1 && NT <=
   const int tiles = (a.rows + kOutRows - 1) / kOutRows;
   const int64_t items = static_cast<int64_t>(*a.n_groups) * tiles;
   const int64_t lo = items * blockIdx.x / gridDim.x, hi = items * (blockIdx.x + 1) / gridDim.x;
-  const int n_kc = (a.K + KC - 1) / KC;
+  const int n_kc = (a.K + kTileK - 1) / kTileK, nblk = a.K / 32;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    const uint64_t pol = l2_policy_evict_first();
-    int slot = 0, issued = 0;
-    uint32_t phase = 1u;
-    bool ok = true;
-    for (int64_t it = lo; it < hi && ok; ++it) {
-      const int gi = static_cast<int>(it / tiles);
-      const int row0 = static_cast<int>(it - static_cast<int64_t>(gi) * tiles) * kOutRows;
-      const int4 g = a.groups[gi];
-      // lane c holds the packed column of the group's column c
-      const int64_t col = lane < g.z ? a.slots[g.y + lane] / a.slot_div : 0;
-      for (int kc = 0; kc < n_kc; ++kc) {
-        if (issued >= a.NS) ok = mbar_wait_or_abort(empty0 + 8u * slot, phase, abort_flag, a.err);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const int klen = min(KC, a.K - kc * KC);
-        const int seg = tile_seg<WT>(klen), segoff = tile_seg<WT>(kc * KC);
-        const uint32_t st = ring + static_cast<uint32_t>(slot) * stage_bytes, full = full0 + 8u * slot;
-        // rows lane, lane + 32, ... of the stage
-        uint32_t bytes = 0;
-        uint32_t len[2 * WR];
-        int64_t src[2 * WR];
-#pragma unroll
-        for (int q = 0; q < 2 * WR; ++q) {
-          // gated: 32-row halves alternate between gate and up
-          const int out = MODE == TILE_GLU ? row0 + 32 * (q >> 1) + lane : row0 + 32 * q + lane;
-          len[q] = 0;
-          if (out < a.rows) {
-            const int64_t off = (static_cast<int64_t>(g.x) * a.rows + out) * a.row_bytes + segoff;
-            src[q] = off & ~15ll;
-            len[q] = static_cast<uint32_t>(((off + seg + 15) & ~15ll) - src[q]);
-            if (src[q] + len[q] > a.total_bytes) {  // the end of the last matrix, copied by hand
-              len[q] -= 16;
-              const uint8_t* W = (MODE == TILE_GLU && (q & 1)) ? a.W2 : a.W;
-              for (int64_t b = src[q] + len[q]; b < a.total_bytes; b += 2) {
-                const uint16_t v = *reinterpret_cast<const uint16_t*>(W + b);
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(st + (32 * q + lane) * P + static_cast<uint32_t>(b - src[q])),
-                             "h"(v)
-                             : "memory");
-              }
-              fence_proxy_async_smem();
+    if (lane == 0) {
+      int slot = 0, issued = 0;
+      uint32_t phase = 1u;
+      bool ok = true;
+      const uint32_t box = 32u / a.period * static_cast<uint32_t>(tile_pitch<WT>(a.period));
+      for (int64_t it = lo; it < hi && ok; ++it) {
+        const int gi = static_cast<int>(it / tiles);
+        const int row0 = static_cast<int>(it - static_cast<int64_t>(gi) * tiles) * kOutRows;
+        const int4 g = a.groups[gi];
+        const int halves = MODE == TILE_GLU || row0 + 32 < a.rows ? 2 : 1;
+        const int nt = (g.z + 7) / 8;
+        const int64_t first = static_cast<int64_t>(g.x) * a.rows + row0;
+        for (int kc = 0; kc < n_kc; ++kc) {
+          if (issued >= a.NS && !mbar_wait_or_abort(empty0 + 8u * slot, phase, abort_flag, a.err)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = ring + static_cast<uint32_t>(slot) * stage_bytes, full = full0 + 8u * slot;
+          const uint32_t xlen = static_cast<uint32_t>(min(kBlocks, nblk - kc * kBlocks)) * rec;
+          const uint32_t wlen = WT == WT_F16 ? 32u * kTileK * 2u : box * a.period;
+          mbar_arrive_expect_tx(full, halves * wlen + nt * xlen);
+          for (int h = 0; h < halves; ++h) {
+            const CUtensorMap* map = MODE == TILE_GLU && h ? &map1 : &map0;
+            const int64_t row = first + (MODE == TILE_GLU ? 0 : 32 * h);
+            if constexpr (WT == WT_F16) {
+              for (int q = 0; q < 4; ++q)
+                tma_load_2d(st + static_cast<uint32_t>((2 * q + h) * 4096), map, kc * kTileK + 64 * q,
+                            static_cast<int>(row), full);
+            } else {
+              for (int i = 0; i < a.period; ++i)
+                tma_load_2d(st + static_cast<uint32_t>((h * a.period + i) * tile_part<WT>(a.period)), map,
+                            ((i * a.row_bytes + kc * tile_seg<WT>()) & ~15) / 2, static_cast<int>(row / a.period), full);
             }
-            bytes += len[q];
+          }
+          for (int n = 0; n < nt; ++n)
+            bulk_g2s(st + xoff + static_cast<uint32_t>(n) * kBlocks * rec,
+                     a.records + (static_cast<int64_t>(g.w + n) * nblk + kc * kBlocks) * rec, xlen, full);
+          ++issued;
+          if (++slot == a.NS) {
+            slot = 0;
+            phase ^= 1u;
           }
         }
-        const uint32_t xlen = static_cast<uint32_t>(klen) * 4u;
-        const uint32_t mlen = (static_cast<uint32_t>(klen) / 4u + 15u) & ~15u;
-        if (lane < g.z) bytes += xlen + (kMeta ? mlen : 0u);
-        bytes = __reduce_add_sync(0xffffffffu, bytes);
-        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < 2 * WR; ++q) {
-          const uint8_t* W = (MODE == TILE_GLU && (q & 1)) ? a.W2 : a.W;
-          if (len[q]) bulk_g2s(st + (32 * q + lane) * P, W + src[q], len[q], full, pol);
-        }
-        if (lane < g.z) {
-          bulk_g2s(st + xoff + lane * XP, a.xpack + (col * a.K + static_cast<int64_t>(kc) * KC) * 4, xlen, full);
-          if constexpr (kMeta)
-            bulk_g2s(st + moff + lane * MP, a.xmeta + col * expert_meta_stride(a.K) + kc * (KC / 32), mlen, full);
-        }
-        ++issued;
-        if (++slot == a.NS) {
-          slot = 0;
-          phase ^= 1u;
-        }
       }
-    }
-    // Drain after an abort: every copy this warp issued lands before the CTA leaves.
-    if (!ok) {
-      for (int i = max(0, issued - a.NS); i < issued; ++i)
-        (void)mbar_wait(full0 + 8u * (i % a.NS), static_cast<uint32_t>((i / a.NS) & 1));
+      // Drain after an abort: every copy this thread issued lands before the CTA leaves.
+      if (!ok)
+        for (int i = max(0, issued - a.NS); i < issued; ++i)
+          (void)mbar_wait(full0 + 8u * (i % a.NS), static_cast<uint32_t>((i / a.NS) & 1));
     }
   } else {
     // ------------------------------------------------------------ consumers
-    const int cw = warp - 1, wr = cw / kTileWarpsK, wk = cw % kTileWarpsK;
+    const int wk = warp - 1;
     const uint32_t g4 = static_cast<uint32_t>(lane) >> 2, t4 = static_cast<uint32_t>(lane) & 3u;
+    // the row of eight that this lane takes
+    const uint32_t row8 = WT == WT_F16 ? ((g4 >> 1) | ((g4 & 1u) << 2)) : g4;
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
-    float* myred = red + wr * (kTileWarpsK * 8 * kRedPitch);
-    auto group_bar = [&]() { named_bar_sync(1u + static_cast<uint32_t>(wr), 32u * kTileWarpsK); };
+    // stage address of rows row8 (+ 8) of a 16-row tile, and the distances of rows 8 and 16
+    // apart and of the halves
+    const uint32_t P = tile_pitch<WT>(a.period), per = static_cast<uint32_t>(a.period);
+    uint32_t rowbase, step8, step16, half;
+    if constexpr (WT == WT_F16) {
+      rowbase = row8 * 128u;
+      step8 = 1024u;
+      step16 = 2048u;
+      half = 4096u;
+    } else {
+      const uint32_t res = row8 % per;
+      rowbase = res * tile_part<WT>(a.period) + row8 / per * P + ((res * static_cast<uint32_t>(a.row_bytes)) & 15u);
+      step8 = 8u / per * P;
+      step16 = 16u / per * P;
+      half = per * tile_part<WT>(a.period);
+    }
+    const uint32_t cp = static_cast<uint32_t>(a.cp);
+    const uint32_t xlane = min(g4, cp - 1u) * 64u + t4 * 16u;  // lanes past the columns read the last one
+    const uint32_t m0 = cp * 128u + min(2u * t4, cp - 1u) * 8u, m1 = cp * 128u + min(2u * t4 + 1u, cp - 1u) * 8u;
+    auto group_bar = [&]() { named_bar_sync(1u, 32u * kTileWarps); };
     for (int64_t it = lo; it < hi; ++it) {
       const int gi = static_cast<int>(it / tiles);
       const int row0 = static_cast<int>(it - static_cast<int64_t>(gi) * tiles) * kOutRows;
@@ -396,96 +391,76 @@ __global__ void __launch_bounds__(32 * (1 + kTileWarpsK * WR), (WR == 1 && NT <=
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-      // Stage rows g and g + 8 of the row group's first matrix tile (the others lie 16 rows
-      // apart).  A row's first byte sits at (its offset in the matrices) mod 16, the same for
-      // rows 16 apart, and so for the gate row and the up row 32 stage rows apart.
-      uint32_t rowaddr[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 8 * h + static_cast<int>(g4);
-        uint32_t shift = 0;
-        if constexpr (WT != WT_F16 && WT != WT_Q4_K)
-          shift = (static_cast<uint32_t>(g.x * a.rows + row0 + kOutRows / WR * wr + r) *
-                   static_cast<uint32_t>(a.row_bytes)) & 15u;
-        rowaddr[h] = static_cast<uint32_t>((kTileRows * wr + r) * P) + shift;
-      }
       for (int kc = 0; kc < n_kc; ++kc) {
         ok = ok && mbar_wait_or_abort(full0 + 8u * slot, phase, abort_flag, a.err);
         const uint32_t st = ring + static_cast<uint32_t>(slot) * stage_bytes;
-        const int units = min(KC, a.K - kc * KC) / 32;
-        if (ok) {
-#pragma unroll 1
-          for (int u = wk; u < units; u += kTileWarpsK) {
-            const uint32_t blk = static_cast<uint32_t>(u);
-            uint4 b[NT][2];
-            float2 meta[NT][2];  // of columns 2t and 2t + 1 of each column tile
+        const uint32_t blk = static_cast<uint32_t>(wk);  // this warp's block of the chunk
+        if (ok && kc * kBlocks + wk < nblk) {
+          uint4 b[NT][2];
+          float2 meta[NT][2];  // of columns 2t and 2t + 1 of each column tile
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (8 * n < ncol) {
+              const uint32_t xa = st + xoff + (static_cast<uint32_t>(n) * kBlocks + blk) * rec;
+              b[n][0] = lds128(xa + xlane);
+              b[n][1] = lds128(xa + xlane + cp * 64u);
+              if constexpr (kMeta) {
+                const uint2 u = lds64(xa + m0), v = lds64(xa + m1);
+                meta[n][0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+                meta[n][1] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+              }
+            }
+          }
+          // Q4_K: taking a row's 6-bit scale and min apart costs as much as its codes; the four
+          // lanes of a row would all do it, so lane t does it for matrix tile t only
+          float qd[2], qm[2];
+          if constexpr (WT == WT_Q4_K) {
+            const uint32_t mine = st + rowbase + (t4 & 1u) * step16 + (t4 >> 1) * half;
+            q4k_scale_of(lds128(mine), blk, qd[0], qm[0]);
+            q4k_scale_of(lds128(mine + step8), blk, qd[1], qm[1]);
+          }
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            uint32_t a0[2][2], a1[2][2];
+            float d[2], dm[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t row = st + rowbase + (m & 1) * step16 + (m >> 1) * half + h * step8;
+              if constexpr (WT == WT_F16)  // box blk / 2, 16-byte word 4 (blk % 2) + t of the 128, swizzled by the row
+                row += (blk >> 1) * 8192u + ((((blk & 1u) * 4u + t4) ^ row8) << 4);
+              load_block_row<WT>(row, blk, t4, a0[h], a1[h], d[h]);
+              dm[h] = 0.0f;
+              if constexpr (WT == WT_Q4_K) {
+                d[h] = __shfl_sync(0xffffffffu, qd[h], m, 4);
+                dm[h] = __shfl_sync(0xffffffffu, qm[h], m, 4);
+              }
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               if (8 * n < ncol) {
-                // lanes past the group's columns read its last column; their sums are dropped
-                const uint32_t c = static_cast<uint32_t>(min(8 * n + static_cast<int>(g4), ncol - 1));
-                const uint32_t xa = st + xoff + c * XP + blk * 128u + t4 * 16u;
-                b[n][0] = lds128(xa);
-                b[n][1] = lds128(xa + 64u);
-                if constexpr (kMeta) {
+                if constexpr (WT == WT_F16 && MODE != TILE_DOWN) {  // one scale per column: no block scale at all
+                  float (&s)[4] = acc[m][n];
+                  mma_f16(s, a0[0][0], a0[1][0], a0[0][1], a0[1][1], b[n][0].x, b[n][0].y);
+                  mma_f16(s, a1[0][0], a1[1][0], a1[0][1], a1[1][1], b[n][1].x, b[n][1].y);
+                  mma_f16(s, a0[0][0], a0[1][0], a0[0][1], a0[1][1], b[n][0].z, b[n][0].w);
+                  mma_f16(s, a1[0][0], a1[1][0], a1[0][1], a1[1][1], b[n][1].z, b[n][1].w);
+                } else {
+                  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                  mma_f16(s, a0[0][0], a0[1][0], a0[0][1], a0[1][1], b[n][0].x, b[n][0].y);
+                  mma_f16(s, a1[0][0], a1[1][0], a1[0][1], a1[1][1], b[n][1].x, b[n][1].y);
+                  mma_f16(s, a0[0][0], a0[1][0], a0[0][1], a0[1][1], b[n][0].z, b[n][0].w);
+                  mma_f16(s, a1[0][0], a1[1][0], a1[0][1], a1[1][1], b[n][1].z, b[n][1].w);
+                  // i: row row8 (0, 1) or row8 + 8 (2, 3), column 2t + (i & 1)
 #pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    const uint32_t mc = static_cast<uint32_t>(min(8 * n + 2 * static_cast<int>(t4) + h, ncol - 1));
-                    const uint2 v = lds64(st + moff + mc * MP + blk * 8u);
-                    meta[n][h] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
-                  }
-                }
-              }
-            }
-            // Q4_K: taking a row's 6-bit scale and min apart costs as much as its codes; the four
-            // lanes of a row would all do it, so lane t does it for matrix tile t only
-            float qd[2], qm[2];
-            if constexpr (WT == WT_Q4_K) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                q4k_scale_of(lds128(st + rowaddr[h] + t4 * (16u * P) + (blk >> 3) * kQ4kBytes), blk & 7u, qd[h], qm[h]);
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              uint32_t a0[2][2], a1[2][2];
-              float d[2], dm[2];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t row = st + rowaddr[h] + m * (16u * P);
-                load_block_row<WT>(row, blk, t4, a0[h], a1[h], d[h]);
-                dm[h] = 0.0f;
-                if constexpr (WT == WT_Q4_K) {
-                  d[h] = __shfl_sync(0xffffffffu, qd[h], m, 4);
-                  dm[h] = __shfl_sync(0xffffffffu, qm[h], m, 4);
-                }
-              }
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                if (8 * n < ncol) {
-                  if constexpr (WT == WT_F16 && MODE != TILE_DOWN) {  // one scale per column: no block scale at all
-                    float (&s)[4] = acc[m][n];
-                    mma_f16(s, a0[0][0], a0[1][0], a0[0][1], a0[1][1], b[n][0].x, b[n][0].y);
-                    mma_f16(s, a1[0][0], a1[1][0], a1[0][1], a1[1][1], b[n][1].x, b[n][1].y);
-                    mma_f16(s, a0[0][0], a0[1][0], a0[0][1], a0[1][1], b[n][0].z, b[n][0].w);
-                    mma_f16(s, a1[0][0], a1[1][0], a1[0][1], a1[1][1], b[n][1].z, b[n][1].w);
-                  } else {
-                    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma_f16(s, a0[0][0], a0[1][0], a0[0][1], a0[1][1], b[n][0].x, b[n][0].y);
-                    mma_f16(s, a1[0][0], a1[1][0], a1[0][1], a1[1][1], b[n][1].x, b[n][1].y);
-                    mma_f16(s, a0[0][0], a0[1][0], a0[0][1], a0[1][1], b[n][0].z, b[n][0].w);
-                    mma_f16(s, a1[0][0], a1[1][0], a1[0][1], a1[1][1], b[n][1].z, b[n][1].w);
-                    // i: row g (0, 1) or g + 8 (2, 3), column 2t + (i & 1)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                      const int h = i >> 1, c = i & 1;
-                      if constexpr (MODE == TILE_DOWN) {
-                        float v = WT == WT_F16 ? s[i] : d[h] * s[i];
-                        if constexpr (WT == WT_Q4_K) v = fmaf(-dm[h], meta[n][c].y, v);
-                        acc[m][n][i] = fmaf(meta[n][c].x, v, acc[m][n][i]);
-                      } else {
-                        acc[m][n][i] = fmaf(d[h], s[i], acc[m][n][i]);
-                        if constexpr (WT == WT_Q4_K) acc[m][n][i] = fmaf(-dm[h], meta[n][c].y, acc[m][n][i]);
-                      }
+                  for (int i = 0; i < 4; ++i) {
+                    const int h = i >> 1, c = i & 1;
+                    if constexpr (MODE == TILE_DOWN) {
+                      float v = WT == WT_F16 ? s[i] : d[h] * s[i];
+                      if constexpr (WT == WT_Q4_K) v = fmaf(-dm[h], meta[n][c].y, v);
+                      acc[m][n][i] = fmaf(meta[n][c].x, v, acc[m][n][i]);
+                    } else {
+                      acc[m][n][i] = fmaf(d[h], s[i], acc[m][n][i]);
+                      if constexpr (WT == WT_Q4_K) acc[m][n][i] = fmaf(-dm[h], meta[n][c].y, acc[m][n][i]);
                     }
                   }
                 }
@@ -500,8 +475,8 @@ __global__ void __launch_bounds__(32 * (1 + kTileWarpsK * WR), (WR == 1 && NT <=
           phase ^= 1u;
         }
       }
-      // the warps' sums of the row group through shared memory, eight columns at a time:
-      // red[warp][column][row]; then warp wk takes column 8n + wk
+      // the warps' sums through shared memory, eight columns at a time: red[warp][column][row];
+      // then warp wk takes column 8n + wk
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         if (8 * n >= ncol) break;
@@ -510,44 +485,44 @@ __global__ void __launch_bounds__(32 * (1 + kTileWarpsK * WR), (WR == 1 && NT <=
         for (int m = 0; m < 4; ++m)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            myred[(wk * 8 + 2 * t4 + (i & 1)) * kRedPitch + 16 * m + g4 + 8 * (i >> 1)] = acc[m][n][i];
+            red[(wk * 8 + 2 * t4 + (i & 1)) * kRedPitch + 16 * m + row8 + 8 * (i >> 1)] = acc[m][n][i];
         group_bar();
         const int c = 8 * n + wk;
         if (c < ncol && ok && !*abort_flag) {
-          const int sl = a.slots[g.y + c];
           float v[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float s = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kTileWarpsK; ++w) s += myred[(w * 8 + wk) * kRedPitch + 32 * h + lane];
+            for (int w = 0; w < kTileWarps; ++w) s += red[(w * 8 + wk) * kRedPitch + 32 * h + lane];
             v[h] = s;
           }
           if constexpr (MODE == TILE_GLU) {
-            // 32 output rows of the gated product: one packed block of the slot's column
-            const float sx = a.xmeta[static_cast<int64_t>(sl / a.slot_div) * expert_meta_stride(a.K)].x;
-            const int r0 = row0 + 32 * wr;
-            if (r0 < a.rows) {  // rows are a multiple of 32
-              const float h = tail_silu(v[0] * sx) * (v[1] * sx);
-              const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(finite_abs(h))));
-              const float sc = pack_scale(m), hs = h * sc;
-              float sum = hs;
+            // 32 output rows of the gated product (rows are a multiple of 32): one record's column
+            const int64_t tile = g.w + n;
+            const float sx =
+                *reinterpret_cast<const float*>(a.records + tile * nblk * rec + cp * 128u + static_cast<uint32_t>(wk) * 8u);
+            const float h = tail_silu(v[0] * sx) * (v[1] * sx);
+            const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(finite_abs(h))));
+            const float sc = pack_scale(m), hs = h * sc;
+            float sum = hs;
 #pragma unroll
-              for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-              const HiLo p = split_hi_lo(hs);
-              uint8_t* q = a.hpack + (static_cast<int64_t>(sl) * a.rows + r0) * 4 +
-                           packed_offset(static_cast<uint32_t>(lane), a.h_swapped != 0);
-              *reinterpret_cast<__half*>(q) = p.hi;
-              *reinterpret_cast<__half*>(q + 8) = p.lo;
-              if (lane == 0)
-                a.hmeta[static_cast<int64_t>(sl) * expert_meta_stride(a.rows) + r0 / 32] =
-                    make_float2(pow2_inverse(sc), sum);
-            }
+            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const HiLo p = split_hi_lo(hs);
+            uint8_t* q = a.out_records + (tile * (a.rows / 32) + row0 / 32) * rec;
+            const uint32_t i = static_cast<uint32_t>(lane) & 3u;
+            const uint32_t at = record_offset(static_cast<uint32_t>(lane) >> 2, static_cast<uint32_t>(wk), cp, a.out_order) +
+                                2u * (a.out_order == ORDER_NIBBLE ? ((i & 1u) << 1) | (i >> 1) : i);
+            *reinterpret_cast<__half*>(q + at) = p.hi;
+            *reinterpret_cast<__half*>(q + at + 8) = p.lo;
+            if (lane == 0)
+              *reinterpret_cast<float2*>(q + cp * 128u + static_cast<uint32_t>(wk) * 8u) = make_float2(pow2_inverse(sc), sum);
           } else {
+            const int sl = a.slots[g.y + c];
             const float w = a.weights[sl];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const int r = row0 + kTileRows * wr + 32 * h + lane;
+              const int r = row0 + 32 * h + lane;
               if (r < a.rows) a.y[static_cast<int64_t>(sl) * a.rows + r] = w * v[h];
             }
           }
