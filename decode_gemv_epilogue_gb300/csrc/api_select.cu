@@ -108,7 +108,7 @@ static bool experts_tiled(const gf_experts* x) {
 // expert's tokens costs registers and shared memory for nothing.
 static int experts_cols(int64_t E, int64_t T, int64_t k) {
   const double mean = static_cast<double>(T) * k / std::min<double>(E, static_cast<double>(T) * k);
-  return static_cast<int>(std::min<int64_t>(T, 8)) < 8 ? static_cast<int>(T) : mean <= 5.0 ? 8 : mean <= 12.0 ? 16 : 32;
+  return static_cast<int>(std::min<int64_t>(T, 8)) < 8 ? static_cast<int>(T) : mean <= 5.0 ? 8 : mean <= 10.0 ? 16 : 24;
 }
 
 constexpr int kExpMaxRecs = 4;
@@ -167,7 +167,7 @@ static int plan_experts(const gf_experts* ex, const float* x, int64_t T, const f
   a.max_tiles = static_cast<int>(l.max_tiles);
   a.y = reinterpret_cast<float*>(ws + l.y);
   a.cols = experts_cols(ex->E, T, ex->top_k);
-  a.order = pack_order(wd);
+  a.out_format = wd;
   a.sm_count = lim.sm_count;
   a.smem_optin = lim.smem_optin;
   bool pdl = (ex->flags & GF_FLAG_PDL) != 0;

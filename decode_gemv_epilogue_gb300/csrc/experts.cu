@@ -207,6 +207,7 @@ __device__ void pack_tile(const ExpertsArgs& a, int tile, const PrepTile& pt, fl
   const int c = threadIdx.x >> 7, i0 = threadIdx.x & 127, lane = threadIdx.x & 31;
   const bool live = c < pt.count;
   const int n4 = a.K / 4, cp = a.cp, order = pack_order(a.wtype);
+  const float high = pack_high(a.wtype), sumf = pack_sum(a.wtype);
   const float* x = a.x + static_cast<int64_t>(live ? pt.slot[c] / a.k : 0) * a.K;
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
   auto load = [&](int i) -> float4 {
@@ -238,10 +239,13 @@ __device__ void pack_tile(const ExpertsArgs& a, int tile, const PrepTile& pt, fl
     float sum = (v.x + v.y) + (v.z + v.w);
 #pragma unroll
     for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((i & 4) != 0) {
+      v.x *= high; v.y *= high; v.z *= high; v.w *= high;
+    }
     if (live && i < n4) {
       uint8_t* r = base + static_cast<int64_t>(i >> 3) * rec;
       *reinterpret_cast<uint4*>(r + record_offset(i & 7, c, cp, order)) = pack_group(v, order == ORDER_NIBBLE);
-      if ((i & 7) == 0) *reinterpret_cast<float2*>(r + cp * 128 + c * 8) = make_float2(inv, sum);
+      if ((i & 7) == 0) *reinterpret_cast<float2*>(r + cp * 128 + c * 8) = make_float2(inv, sum * sumf);
     }
   };
 #pragma unroll
@@ -274,9 +278,9 @@ static int tile_map(const void* W, int64_t all_rows, int row_bytes, CUtensorMap*
                        static_cast<uint32_t>(tile_pitch<WT>(p) / 2), static_cast<uint32_t>(32 / p), false, out);
 }
 
-template <int WT, int MODE, int NT>
+template <int WT, int MODE, int NT, bool PER1>
 static int launch_tile_t(TileArgs t, const ExpertsArgs& a, cudaStream_t st, bool pdl) {
-  auto kern = tile_kernel<WT, MODE, NT>;
+  auto kern = tile_kernel<WT, MODE, NT, PER1>;
   CUtensorMap m0, m1;
   const int64_t all_rows = static_cast<int64_t>(a.E) * t.rows;
   int e = tile_map<WT>(a.W, all_rows, t.row_bytes, &m0);
@@ -284,16 +288,15 @@ static int launch_tile_t(TileArgs t, const ExpertsArgs& a, cudaStream_t st, bool
   m1 = m0;
   if (MODE == TILE_GLU) e = tile_map<WT>(a.W2, all_rows, t.row_bytes, &m1);
   if (e != cudaSuccess) return e;
-  constexpr int kCtas = NT <= 2 ? 2 : 1;  // CTAs per SM the registers allow
-  const int stage = tile_stage_bytes<WT>(t.period, NT, t.cp), fixed = kTileBarBytes + kTileRedBytes + 1024;
+  const int stage = tile_stage_bytes<WT>(t.period, NT, t.cp), fixed = kTileHeadBytes + kTileRedBytes + 1024;
   // as many CTAs per SM as leave each three stages; 1 KB a CTA is the system's
-  int ctas = kCtas, ns = 0;
+  int ctas = tile_ctas(NT), ns = 0;
   for (; ctas >= 1; --ctas) {
     const int budget = ctas == 1 ? a.smem_optin : (a.smem_optin + 1024) / ctas - 1024;
     ns = std::min(kTileMaxStages, (budget - fixed) / stage);
     if (ns >= 3 || ctas == 1) break;
   }
-  if (ns < 2) return cudaErrorInvalidConfiguration;
+  if (ns < 2 || a.max_tiles / (ctas * a.sm_count) + 2 > kTileMaxGroups) return cudaErrorInvalidConfiguration;
   t.NS = ns;
   const int smem = fixed + ns * stage;
   static int configured[64] = {0};
@@ -310,11 +313,11 @@ static int launch_tile_t(TileArgs t, const ExpertsArgs& a, cudaStream_t st, bool
   return cudaLaunchKernelEx(&cfg, kern, m0, m1, t);
 }
 
-template <int WT, int MODE>
+template <int WT, int MODE, bool PER1>
 static int launch_tile_cols(const TileArgs& t, const ExpertsArgs& a, cudaStream_t st, bool pdl) {
-  if (a.cols <= 8) return launch_tile_t<WT, MODE, 1>(t, a, st, pdl);
-  if (a.cols <= 16) return launch_tile_t<WT, MODE, 2>(t, a, st, pdl);
-  return launch_tile_t<WT, MODE, 4>(t, a, st, pdl);
+  if (a.cols <= 8) return launch_tile_t<WT, MODE, 1, PER1>(t, a, st, pdl);
+  if (a.cols <= 16) return launch_tile_t<WT, MODE, 2, PER1>(t, a, st, pdl);
+  return launch_tile_t<WT, MODE, 3, PER1>(t, a, st, pdl);
 }
 
 template <int MODE>
@@ -331,14 +334,18 @@ static int launch_tiles(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
   t.cp = a.cp;
   t.err = a.err;
   t.out_records = a.hrec;
-  t.out_order = a.order;
+  t.out_format = a.out_format;
   t.weights = a.weights;
   t.y = a.y;
   switch (a.wtype) {
-    case WT_F16: return launch_tile_cols<WT_F16, MODE>(t, a, st, pdl);
-    case WT_Q8_0: return launch_tile_cols<WT_Q8_0, MODE>(t, a, st, pdl);
-    case WT_Q4_0: return launch_tile_cols<WT_Q4_0, MODE>(t, a, st, pdl);
-    case WT_Q4_K: return launch_tile_cols<WT_Q4_K, MODE>(t, a, st, pdl);
+    case WT_F16: return launch_tile_cols<WT_F16, MODE, true>(t, a, st, pdl);
+    case WT_Q8_0:
+      return t.period == 1 ? launch_tile_cols<WT_Q8_0, MODE, true>(t, a, st, pdl)
+                           : launch_tile_cols<WT_Q8_0, MODE, false>(t, a, st, pdl);
+    case WT_Q4_0:
+      return t.period == 1 ? launch_tile_cols<WT_Q4_0, MODE, true>(t, a, st, pdl)
+                           : launch_tile_cols<WT_Q4_0, MODE, false>(t, a, st, pdl);
+    case WT_Q4_K: return launch_tile_cols<WT_Q4_K, MODE, true>(t, a, st, pdl);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -245,7 +245,7 @@ enum { EXP_PREP = 0, EXP_GLU = 1, EXP_DOWN = 2, EXP_COMBINE = 3, EXP_GLU_GENERIC
 struct ExpertsArgs {
   int phase;
   int wtype;            // of this phase's matrices
-  int order;            // element order of the records that the gated product writes
+  int out_format;       // of the weights that take the gated product's records
   const uint8_t* W;     // gate (EXP_GLU*) or down (EXP_DOWN*)
   const uint8_t* W2;    // up
   const float* x;
@@ -256,7 +256,7 @@ struct ExpertsArgs {
   unsigned* err;
   int E, T, k;
   int M, K;             // ffn width, model width
-  int cols;             // columns per group (8, 16 or 32, or the tokens if fewer than 8)
+  int cols;             // columns per group (8, 16 or 24, or the tokens if fewer than 8)
   int cp;               // columns stored per column tile: min(8, T)
   int max_tiles;        // upper bound on the column tiles of all experts
   // workspace

@@ -1,14 +1,20 @@
 // Tiled products of block-format weights with several columns on the tensor cores: the
-// device code shared by the chosen experts' kernels and the shared projection of a wide
-// batch with adapters.
+// device code of the chosen experts' kernels.
 //
 // x is "packed" first: every 32 elements of a column become 32 pairs of f16,
 //     x * 2^s = hi + lo,   hi = f16(x 2^s),   lo = f16(x 2^s - hi)
 // with a power of two 2^s that puts the largest magnitude into [2^14, 2^15): hi + lo carries
-// x to 2^-22 of itself (2^-39 of the largest where lo is subnormal), less than the rounding
-// of a 32-bit sum.  The codes of the weights are exact in f16, the products of f16 are exact
-// in the 32-bit accumulators, and the blocks' scales multiply the accumulated sum of a block
-// in 32 bits: the only roundings are those of 32-bit sums.
+// x to 2^-22 of itself (2^-35 of the largest where lo is subnormal), less than the rounding
+// of a 32-bit sum.  The weights' codes are exact in f16, the products of f16 are exact in
+// the 32-bit accumulators, and the blocks' scales multiply the accumulated sum of a block in
+// 32 bits: the only roundings are those of 32-bit sums.
+//
+// Codes become f16 by masking alone: the f16 with the bits of a code c below 1024 is the
+// subnormal c 2^-24, which the matrix unit takes exactly (a 4-bit code four bits higher is
+// 16 c 2^-24; its x is packed 1/16 as large).  The sums are then in units of 2^-24, taken
+// back in the tail, and the formats' offsets (8 and 128) enter as the matrix instruction's
+// addend, -offset times the sum of x over the block: no instruction per weight is left but
+// the masks.
 //
 // Why mma.sync and not the asynchronous matrix unit: a block format's scale belongs to 32
 // weights of one row, so the accumulator of every 32 columns of K has to pass through
@@ -28,23 +34,18 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-__device__ __forceinline__ uint32_t hadd2u(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
+// d = A B + {c0, c1, c0, c1}: an addend per column.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1, float c0, float c1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %10, %11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
-__device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-// (w & mask) | 0x64006400: two f16 of 1024 plus a code each.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t mask) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(0x64006400u));
-  return d;
-}
+template <int N>
+struct TileConst {
+  static constexpr int value = N;
+};
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
@@ -66,18 +67,12 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-// The 32-bit word at a 2-byte aligned address, from the two aligned words around it (may
-// read up to 3 bytes past it; stages keep slack).
-__device__ __forceinline__ uint32_t lds32_half_aligned(uint32_t a) {
-  const uint32_t b = a & ~3u;
-  return __funnelshift_r(lds32(b), lds32(b + 4u), (a & 3u) * 8u);
-}
 
 // ------------------------------------------------------------------ packing x
 // Packed columns lie in the order in which the matrix instruction takes them.  Eight columns
 // form a column tile, and for every 32 elements a column tile has one record:
 //   [step s of 2][column of cp][thread t of 4] 16 bytes {hi, hi, hi, hi, lo, lo, lo, lo},
-//   then per column {2^-s, the sum of x 2^s over the 32 elements};
+//   then per column {2^-s, the block's sum of x 2^s times pack_sum(format)};
 // cp = min(8, columns of the call) columns are stored, so that a single column does not move
 // eight.  A warp's 16-byte reads of a step are then consecutive, and the records of a K chunk
 // are one piece of memory for one bulk copy.  Which four elements (s, t) holds is the
@@ -88,6 +83,15 @@ enum { ORDER_NIBBLE = 0, ORDER_BYTE = 1, ORDER_F16 = 2 };
 __host__ __device__ constexpr int pack_order(int wt) {
   return wt == WT_F16 ? ORDER_F16 : wt == WT_Q8_0 ? ORDER_BYTE : ORDER_NIBBLE;
 }
+// What the sum of a block is stored for: the offset of the codes, or Q4_K's mins, both in
+// the units of the accumulators.
+__host__ __device__ constexpr float pack_sum(int wt) {
+  return wt == WT_Q4_0 ? -8.0f * 0x1p-24f : wt == WT_Q8_0 ? -128.0f * 0x1p-24f : 0x1p-24f;
+}
+// Factor of elements 16 .. 31 of a block: their Q4_0 codes are masked in place, 16 times as large.
+__host__ __device__ constexpr float pack_high(int wt) { return wt == WT_Q4_0 ? 0.0625f : 1.0f; }
+// Unit of the accumulators.
+__host__ __device__ constexpr float tile_unit(int wt) { return wt == WT_F16 ? 1.0f : 0x1p24f; }
 __host__ __device__ constexpr int record_bytes(int cp) { return cp * 128 + (cp * 8 + 15) / 16 * 16; }
 // Byte offset in a record of the four elements 4q .. 4q + 3 of column c.
 __device__ __forceinline__ uint32_t record_offset(uint32_t q, uint32_t c, uint32_t cp, int order) {
@@ -134,11 +138,6 @@ __device__ __forceinline__ float finite_abs(float v) {
 }
 
 // ------------------------------------------------------------------ A fragments
-// One 32-element block of rows g and g + 8 of a 16-row tile as the A operands of two
-// m16n8k16 steps: a[s] = {row g k-slots 2t, 2t+1; row g+8 the same; row g slots 2t+8, 2t+9;
-// row g+8 the same}, thread (g, t) = (lane / 4, lane % 4).  Which element sits in which
-// k-slot is free as long as the packed x has the same one (see pack_order).  d: the rows'
-// block scales (unused for F16).
 // d * sc[j] and dmin * m[j] of a Q4_K super-block from its first 16 bytes (both exact).  The
 // 6-bit integers become floats in the low bits of 2^23: a conversion instruction has a
 // quarter of an addition's rate.
@@ -151,43 +150,71 @@ __device__ __forceinline__ void q4k_scale_of(const uint4 hd, uint32_t j, float& 
   dmn = h2f(hd.x >> 16) * (__uint_as_float(0x4B000000u | mn) - kMagic);
 }
 
+// One lane's place in a row of a stage: what it reads of its warp's block.
+struct RowPlace {
+  uint32_t code;   // first aligned word of its codes
+  uint32_t scale;  // the block's scale (Q4_0, Q8_0)
+  uint32_t shift;  // bits the codes start above that word's first (0 or 16)
+  uint32_t mask;   // Q4_K: which nibbles
+};
 template <int WT>
-__device__ __forceinline__ void load_block_row(uint32_t row, uint32_t blk, uint32_t t, uint32_t (&a0)[2],
-                                               uint32_t (&a1)[2], float& d) {
-  if constexpr (WT == WT_F16) {  // the thread's 16 bytes, swizzled: see tile_kernel
-    const uint4 u = lds128(row);
+__device__ __forceinline__ RowPlace row_place(uint32_t row, uint32_t blk, uint32_t t) {
+  RowPlace p = {};
+  if constexpr (WT == WT_Q8_0 || WT == WT_Q4_0) {
+    p.scale = row + blk * (WT == WT_Q8_0 ? 34u : 18u);
+    const uint32_t c = p.scale + 2u + 4u * t;
+    p.code = c & ~3u;
+    p.shift = (c & 3u) * 8u;
+  } else if constexpr (WT == WT_Q4_K) {
+    p.code = row + 16u + ((blk >> 1) & 3u) * 32u + 4u * t;
+    p.mask = 0x000F000Fu << (4u * (blk & 1u));
+  } else {
+    p.code = row;  // F16: swizzled by the caller
+  }
+  return p;
+}
+
+// One 32-element block of a row, at `off` bytes from the place, as A operands of two
+// m16n8k16 steps: a[step] = {k-slots 2t, 2t+1; 2t+8, 2t+9}.  Which element sits in which
+// k-slot is free as long as the packed x has the same one (see pack_order).
+// WHOLE: the codes start on a word (shift 0).  d: the block's scale.
+template <int WT, bool WHOLE>
+__device__ __forceinline__ void load_block_row(const RowPlace& p, uint32_t off, uint32_t (&a0)[2], uint32_t (&a1)[2],
+                                               float& d) {
+  if constexpr (WT == WT_F16) {
+    const uint4 u = lds128(p.code + off);
     a0[0] = u.x; a0[1] = u.y;
     a1[0] = u.z; a1[1] = u.w;
     d = 1.0f;
   } else if constexpr (WT == WT_Q8_0) {
-    const uint32_t p = row + blk * 34u;
-    d = h2f(lds16(p));
-    const uint32_t u = lds32_half_aligned(p + 2u + 4u * t) ^ 0x80808080u;
-    const uint32_t v = lds32_half_aligned(p + 18u + 4u * t) ^ 0x80808080u;
-    constexpr uint32_t kBias = 0xE480E480u;  // -(1024 + 128) twice
-    a0[0] = hadd2u(__byte_perm(u, 0x64646464u, 0x4140), kBias);
-    a0[1] = hadd2u(__byte_perm(u, 0x64646464u, 0x4342), kBias);
-    a1[0] = hadd2u(__byte_perm(v, 0x64646464u, 0x4140), kBias);
-    a1[1] = hadd2u(__byte_perm(v, 0x64646464u, 0x4342), kBias);
-  } else if constexpr (WT == WT_Q4_K) {  // the scale and min come apart elsewhere
-    const uint32_t p = row + (blk >> 3) * kQ4kBytes + 16u + ((blk >> 1) & 3u) * 32u + 4u * t;
-    const uint32_t sh = 4u * (blk & 1u), w = lds32(p) >> sh, v = lds32(p + 16u) >> sh;
-    constexpr uint32_t kLow = 0xE400E400u;              // -1024
-    a0[0] = hadd2u(code_pair(w, 0x000F000Fu), kLow);
-    a0[1] = hadd2u(code_pair(w >> 8, 0x000F000Fu), kLow);
-    a1[0] = hadd2u(code_pair(v, 0x000F000Fu), kLow);
-    a1[1] = hadd2u(code_pair(v >> 8, 0x000F000Fu), kLow);
+    d = h2f(lds16(p.scale + off));
+    uint32_t u = lds32(p.code + off), v = lds32(p.code + off + 16u);
+    if constexpr (!WHOLE) {
+      u = __funnelshift_r(u, lds32(p.code + off + 4u), p.shift);
+      v = __funnelshift_r(v, lds32(p.code + off + 20u), p.shift);
+    }
+    u ^= 0x80808080u;  // q + 128
+    v ^= 0x80808080u;
+    a0[0] = __byte_perm(u, 0u, 0x4140);
+    a0[1] = __byte_perm(u, 0u, 0x4342);
+    a1[0] = __byte_perm(v, 0u, 0x4140);
+    a1[1] = __byte_perm(v, 0u, 0x4342);
+  } else if constexpr (WT == WT_Q4_K) {  // scale and min come apart elsewhere
+    const uint32_t w = lds32(p.code + off), v = lds32(p.code + off + 16u);
+    a0[0] = w & p.mask;
+    a0[1] = (w >> 8) & p.mask;
+    a1[0] = v & p.mask;
+    a1[1] = (v >> 8) & p.mask;
+    d = 1.0f;
   } else {  // Q4_0
-    const uint32_t p = row + blk * 18u;
-    d = h2f(lds16(p));
-    const uint32_t w = lds32_half_aligned(p + 2u + 4u * t), w8 = w >> 8;
-    constexpr uint32_t kLow = 0xE408E408u;              // -(1024 + 8)
-    constexpr uint32_t kSixteenth = 0x2C002C00u;        // 1/16
-    constexpr uint32_t kHigh = 0xD480D480u;             // -(64 + 8)
-    a0[0] = hadd2u(code_pair(w, 0x000F000Fu), kLow);    // elements 4t, 4t+2
-    a0[1] = hadd2u(code_pair(w8, 0x000F000Fu), kLow);   // 4t+1, 4t+3
-    a1[0] = hfma2u(code_pair(w, 0x00F000F0u), kSixteenth, kHigh);
-    a1[1] = hfma2u(code_pair(w8, 0x00F000F0u), kSixteenth, kHigh);
+    d = h2f(lds16(p.scale + off));
+    uint32_t w = lds32(p.code + off);
+    if constexpr (!WHOLE) w = __funnelshift_r(w, lds32(p.code + off + 4u), p.shift);
+    const uint32_t w8 = w >> 8;
+    a0[0] = w & 0x000F000Fu;   // elements 4t, 4t + 2
+    a0[1] = w8 & 0x000F000Fu;  // 4t + 1, 4t + 3
+    a1[0] = w & 0x00F000F0u;
+    a1[1] = w8 & 0x00F000F0u;
   }
 }
 
@@ -199,10 +226,14 @@ __device__ __forceinline__ void load_block_row(uint32_t row, uint32_t blk, uint3
 // consumer warps share the K axis: a warp takes one 32-element block of the chunk for all 64
 // rows (four 16-row matrix tiles), so that a packed x fragment, once loaded, serves four
 // matrix tiles.  At the end of an item the warps' accumulators are added through shared
-// memory in warp order (deterministic) and the tail is applied.
+// memory in warp order (deterministic) and the tail is applied.  Up to two column tiles two
+// CTAs share an SM, so that one's reduction overlaps the other's stream; three take the
+// registers of one.
 //
 // (A first version copied every row of a chunk by its own bulk copy: each took about 90
-// cycles of an SM's copy engine whatever its size, three to ten times the time of the bytes.)
+// cycles of an SM's copy engine whatever its size, three to ten times the time of the bytes.
+// One without a copying warp, whose warps took turns refilling a stage, fell into step with
+// itself and was 10 to 30% slower.)
 //
 // Rows in a stage.  Q4_0, Q4_K: 144 bytes a row and chunk, Q8_0: 272, odd multiples of 16, so
 // that the eight rows a warp reads together fall on distinct banks.  Where K is no multiple
@@ -216,17 +247,20 @@ __device__ __forceinline__ void load_block_row(uint32_t row, uint32_t blk, uint3
 // draining its own copies.
 constexpr int kTileRows = 64;
 constexpr int kTileK = 256;
+constexpr int kTileBlocks = kTileK / 32;
 constexpr int kTileWarps = 8;           // consumer warps, sharing K
 constexpr int kTileThreads = 32 * (1 + kTileWarps);
 constexpr int kTileMaxStages = 8;
-constexpr int kTileBarBytes = 256;
+constexpr int kTileMaxGroups = 64;      // column groups a CTA's items may touch
+constexpr int kTileHeadBytes = 256 + 16 * kTileMaxGroups;  // barriers, abort flag, groups
 constexpr int kRedPitch = kTileRows + 4;
 constexpr int kTileRedBytes = kTileWarps * 8 * kRedPitch * 4;  // the warps' sums of eight columns
 enum { TILE_GLU = 0, TILE_DOWN = 1 };
+__host__ __device__ constexpr int tile_ctas(int nt) { return nt <= 2 ? 2 : 1; }
 
 template <int WT>
 __host__ __device__ constexpr int tile_seg() {  // bytes of a row and chunk
-  return WT == WT_F16 ? 2 * kTileK : WT == WT_Q8_0 ? kTileK / 32 * 34 : 144;
+  return WT == WT_F16 ? 2 * kTileK : WT == WT_Q8_0 ? kTileBlocks * 34 : 144;
 }
 // Rows that make a whole number of 16-byte words.
 __host__ __device__ constexpr int tile_period(int row_bytes) {
@@ -245,7 +279,7 @@ __host__ __device__ constexpr int tile_weight_bytes(int period) {
 }
 template <int WT>
 __host__ __device__ constexpr int tile_stage_bytes(int period, int nt, int cp) {
-  return (tile_weight_bytes<WT>(period) + 16 + nt * (kTileK / 32) * record_bytes(cp) + 1023) / 1024 * 1024;
+  return (tile_weight_bytes<WT>(period) + 16 + nt * kTileBlocks * record_bytes(cp) + 1023) / 1024 * 1024;
 }
 
 struct TileArgs {
@@ -260,24 +294,133 @@ struct TileArgs {
   unsigned* err;
   // tails
   uint8_t* out_records;     // gated: records of the next product's x
-  int out_order;
+  int out_format;           // of the next product's weights
   const float* weights;     // down: factor of a slot
   float* y;                 // down: [slot][rows]
 };
 
-template <int WT, int MODE, int NT>
-__global__ void __launch_bounds__(kTileThreads, NT <= 2 ? 2 : 1)
+// One lane's constants of the walk over a stage.
+struct TileLane {
+  uint32_t rowbase, step8, step16, half;  // rows row8, + 8, + 16, + 32
+  uint32_t row8, t4;
+  uint32_t xlane, m0, m1, cp, rec;
+};
+
+// This warp's block `blk` of a stage (weights at st, its records at xs): acc += W x for 64
+// rows and NTA column tiles.  PER1: rows lie at the constant pitch of period 1.
+template <int WT, int MODE, int NTA, int NT, bool PER1, bool WHOLE>
+__device__ __forceinline__ void tile_block(const TileLane& l, uint32_t st, uint32_t xs, uint32_t blk,
+                                           float (&acc)[4][NT][4]) {
+  constexpr bool kMeta = MODE == TILE_DOWN || WT != WT_F16;  // per-block scales or sums are read here
+  constexpr bool kOffset = WT == WT_Q4_0 || WT == WT_Q8_0;   // the sums are the codes' offset
+  constexpr bool kDirect = WT == WT_F16 && MODE != TILE_DOWN;  // one scale per column: no block scale at all
+  constexpr uint32_t kP = tile_pitch<WT>(1);
+  const uint32_t step8 = WT == WT_F16 ? 1024u : PER1 ? 8u * kP : l.step8;
+  const uint32_t step16 = WT == WT_F16 ? 2048u : PER1 ? 16u * kP : l.step16;
+  const uint32_t half = WT == WT_F16 ? 4096u : PER1 ? static_cast<uint32_t>(tile_part<WT>(1)) : l.half;
+  uint4 b[NTA][2];
+  float2 meta[NTA][2];  // of columns 2t and 2t + 1 of each column tile
+#pragma unroll
+  for (int n = 0; n < NTA; ++n) {
+    const uint32_t xa = xs + static_cast<uint32_t>(n) * kTileBlocks * l.rec;
+    b[n][0] = lds128(xa + l.xlane);
+    b[n][1] = lds128(xa + l.xlane + l.cp * 64u);
+    if constexpr (kMeta) {
+      const uint2 u = lds64(xa + l.m0), v = lds64(xa + l.m1);
+      meta[n][0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+      meta[n][1] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+    }
+  }
+  const uint32_t row = st + l.rowbase;
+  RowPlace place = row_place<WT>(row, blk, l.t4);
+  if constexpr (WT == WT_F16)  // box blk / 2, 16-byte word 4 (blk % 2) + t of the 128, swizzled by the row
+    place.code += (blk >> 1) * 8192u + ((((blk & 1u) * 4u + l.t4) ^ l.row8) << 4);
+  // Q4_K: taking a row's 6-bit scale and min apart costs as much as its codes; the four
+  // lanes of a row would all do it, so lane t does it for matrix tile t only
+  float qd[2], qm[2];
+  if constexpr (WT == WT_Q4_K) {
+    const uint32_t mine = row + (l.t4 & 1u) * step16 + (l.t4 >> 1) * half;
+    const float nib = (blk & 1u) ? 0.0625f : 1.0f;  // high nibbles are masked in place
+    q4k_scale_of(lds128(mine), blk, qd[0], qm[0]);
+    q4k_scale_of(lds128(mine + step8), blk, qd[1], qm[1]);
+    qd[0] *= nib;
+    qd[1] *= nib;
+  }
+  // A matrix instruction takes long to give its sum back and the four of a block follow one
+  // another in it: MG matrix tiles are taken side by side
+  constexpr int MG = 2;
+#pragma unroll
+  for (int mg = 0; mg < 4; mg += MG) {
+    uint32_t a0[MG][2][2], a1[MG][2][2];
+    float d[MG][2], dm[MG][2];
+#pragma unroll
+    for (int j = 0; j < MG; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int m = mg + j;
+        load_block_row<WT, WHOLE>(place, (m & 1) * step16 + (m >> 1) * half + h * step8, a0[j][h], a1[j][h], d[j][h]);
+        dm[j][h] = 0.0f;
+        if constexpr (WT == WT_Q4_K) {
+          d[j][h] = __shfl_sync(0xffffffffu, qd[h], m, 4);
+          dm[j][h] = __shfl_sync(0xffffffffu, qm[h], m, 4);
+        }
+      }
+    float s[MG][NTA][4];
+    auto step = [&](int i) {  // hi of both k-steps, then lo of both
+#pragma unroll
+      for (int j = 0; j < MG; ++j)
+#pragma unroll
+        for (int n = 0; n < NTA; ++n) {
+          const uint32_t (&x)[2][2] = (i & 1) ? a1[j] : a0[j];
+          const uint4 v = b[n][i & 1];
+          const uint32_t p = i < 2 ? v.x : v.z, q = i < 2 ? v.y : v.w;
+          if constexpr (kDirect)
+            mma_f16(acc[mg + j][n], x[0][0], x[1][0], x[0][1], x[1][1], p, q);
+          else if (i == 0)
+            mma_f16_first(s[j][n], x[0][0], x[1][0], x[0][1], x[1][1], p, q, kOffset ? meta[n][0].y : 0.0f,
+                          kOffset ? meta[n][1].y : 0.0f);
+          else
+            mma_f16(s[j][n], x[0][0], x[1][0], x[0][1], x[1][1], p, q);
+        }
+    };
+    step(0);
+    step(1);
+    step(2);
+    step(3);
+    if constexpr (!kDirect) {
+#pragma unroll
+      for (int j = 0; j < MG; ++j)
+#pragma unroll
+        for (int n = 0; n < NTA; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // row row8 (0, 1) or row8 + 8 (2, 3), column 2t + (i & 1)
+            const int h = i >> 1, c = i & 1;
+            float& o = acc[mg + j][n][i];
+            if constexpr (MODE == TILE_DOWN) {
+              float v = WT == WT_F16 ? s[j][n][i] : d[j][h] * s[j][n][i];
+              if constexpr (WT == WT_Q4_K) v = fmaf(-dm[j][h], meta[n][c].y, v);
+              o = fmaf(meta[n][c].x, v, o);
+            } else {
+              o = fmaf(d[j][h], s[j][n][i], o);
+              if constexpr (WT == WT_Q4_K) o = fmaf(-dm[j][h], meta[n][c].y, o);
+            }
+          }
+    }
+  }
+}
+
+template <int WT, int MODE, int NT, bool PER1>
+__global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
     tile_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
                 const __grid_constant__ TileArgs a) {
-  constexpr bool kMeta = MODE == TILE_DOWN || WT == WT_Q4_K;  // per-block scales or sums are read in the loop
   constexpr int kOutRows = MODE == TILE_GLU ? 32 : kTileRows;
-  constexpr int kBlocks = kTileK / 32;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(smem), full0 = sbase, empty0 = sbase + 8u * kTileMaxStages;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kTileBarBytes - 8);
-  float* red = reinterpret_cast<float*>(smem + kTileBarBytes);
-  const uint32_t ring = (sbase + kTileBarBytes + kTileRedBytes + 1023u) & ~1023u;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 248);
+  int4* groups = reinterpret_cast<int4*>(smem + 256);
+  float* red = reinterpret_cast<float*>(smem + kTileHeadBytes);
+  const uint32_t ring = (sbase + kTileHeadBytes + kTileRedBytes + 1023u) & ~1023u;
   const uint32_t rec = static_cast<uint32_t>(record_bytes(a.cp));
   const uint32_t stage_bytes = tile_stage_bytes<WT>(a.period, NT, a.cp);
   const uint32_t xoff = tile_weight_bytes<WT>(a.period) + 16;  // slack: words are read up to 3 bytes past a row
@@ -291,58 +434,69 @@ __global__ void __launch_bounds__(kTileThreads, NT <= 2 ? 2 : 1)
     prefetch_tmap(&map0);
     if (MODE == TILE_GLU) prefetch_tmap(&map1);
   }
-  __syncthreads();
   pdl_trigger();
   pdl_wait();
   const int tiles = (a.rows + kOutRows - 1) / kOutRows;
   const int64_t items = static_cast<int64_t>(*a.n_groups) * tiles;
   const int64_t lo = items * blockIdx.x / gridDim.x, hi = items * (blockIdx.x + 1) / gridDim.x;
+  const int g_lo = static_cast<int>(lo / tiles);
+  if (lo < hi)
+    for (int i = threadIdx.x; i <= static_cast<int>((hi - 1) / tiles) - g_lo; i += kTileThreads)
+      groups[i] = a.groups[g_lo + i];
+  __syncthreads();
   const int n_kc = (a.K + kTileK - 1) / kTileK, nblk = a.K / 32;
+  const int n_items = static_cast<int>(hi - lo);
+  const int tile_lo = static_cast<int>(lo - static_cast<int64_t>(g_lo) * tiles);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int slot = 0, issued = 0;
+      int slot = 0, issued = 0, gi = 0, tile = tile_lo;
       uint32_t phase = 1u;
       bool ok = true;
-      const uint32_t box = 32u / a.period * static_cast<uint32_t>(tile_pitch<WT>(a.period));
-      for (int64_t it = lo; it < hi && ok; ++it) {
-        const int gi = static_cast<int>(it / tiles);
-        const int row0 = static_cast<int>(it - static_cast<int64_t>(gi) * tiles) * kOutRows;
-        const int4 g = a.groups[gi];
+      const uint32_t wlen = WT == WT_F16 ? 32u * kTileK * 2u : 32u * static_cast<uint32_t>(tile_pitch<WT>(a.period));
+      for (int it = 0; it < n_items && ok; ++it) {
+        const int4 g = groups[gi];
+        const int row0 = tile * kOutRows;
         const int halves = MODE == TILE_GLU || row0 + 32 < a.rows ? 2 : 1;
         const int nt = (g.z + 7) / 8;
-        const int64_t first = static_cast<int64_t>(g.x) * a.rows + row0;
+        const int first = g.x * a.rows + row0;
+        const uint8_t* xsrc = a.records + static_cast<int64_t>(g.w) * nblk * rec;
         for (int kc = 0; kc < n_kc; ++kc) {
           if (issued >= a.NS && !mbar_wait_or_abort(empty0 + 8u * slot, phase, abort_flag, a.err)) {
             ok = false;
             break;
           }
           const uint32_t st = ring + static_cast<uint32_t>(slot) * stage_bytes, full = full0 + 8u * slot;
-          const uint32_t xlen = static_cast<uint32_t>(min(kBlocks, nblk - kc * kBlocks)) * rec;
-          const uint32_t wlen = WT == WT_F16 ? 32u * kTileK * 2u : box * a.period;
+          const uint32_t xlen = static_cast<uint32_t>(min(kTileBlocks, nblk - kc * kTileBlocks)) * rec;
           mbar_arrive_expect_tx(full, halves * wlen + nt * xlen);
           for (int h = 0; h < halves; ++h) {
             const CUtensorMap* map = MODE == TILE_GLU && h ? &map1 : &map0;
-            const int64_t row = first + (MODE == TILE_GLU ? 0 : 32 * h);
+            const int row = first + (MODE == TILE_GLU ? 0 : 32 * h);
             if constexpr (WT == WT_F16) {
+#pragma unroll
               for (int q = 0; q < 4; ++q)
-                tma_load_2d(st + static_cast<uint32_t>((2 * q + h) * 4096), map, kc * kTileK + 64 * q,
-                            static_cast<int>(row), full);
+                tma_load_2d(st + static_cast<uint32_t>((2 * q + h) * 4096), map, kc * kTileK + 64 * q, row, full);
+            } else if constexpr (PER1) {
+              tma_load_2d(st + static_cast<uint32_t>(h * tile_part<WT>(1)), map, kc * (tile_seg<WT>() / 2), row, full);
             } else {
               for (int i = 0; i < a.period; ++i)
                 tma_load_2d(st + static_cast<uint32_t>((h * a.period + i) * tile_part<WT>(a.period)), map,
-                            ((i * a.row_bytes + kc * tile_seg<WT>()) & ~15) / 2, static_cast<int>(row / a.period), full);
+                            ((i * a.row_bytes + kc * tile_seg<WT>()) & ~15) / 2, row / a.period, full);
             }
           }
           for (int n = 0; n < nt; ++n)
-            bulk_g2s(st + xoff + static_cast<uint32_t>(n) * kBlocks * rec,
-                     a.records + (static_cast<int64_t>(g.w + n) * nblk + kc * kBlocks) * rec, xlen, full);
+            bulk_g2s(st + xoff + static_cast<uint32_t>(n) * kTileBlocks * rec,
+                     xsrc + (static_cast<int64_t>(n) * nblk + kc * kTileBlocks) * rec, xlen, full);
           ++issued;
           if (++slot == a.NS) {
             slot = 0;
             phase ^= 1u;
           }
+        }
+        if (++tile == tiles) {
+          tile = 0;
+          ++gi;
         }
       }
       // Drain after an abort: every copy this thread issued lands before the CTA leaves.
@@ -353,37 +507,54 @@ __global__ void __launch_bounds__(kTileThreads, NT <= 2 ? 2 : 1)
   } else {
     // ------------------------------------------------------------ consumers
     const int wk = warp - 1;
-    const uint32_t g4 = static_cast<uint32_t>(lane) >> 2, t4 = static_cast<uint32_t>(lane) & 3u;
-    // the row of eight that this lane takes
-    const uint32_t row8 = WT == WT_F16 ? ((g4 >> 1) | ((g4 & 1u) << 2)) : g4;
-    int slot = 0;
+    TileLane l;
+    {
+      const uint32_t g4 = static_cast<uint32_t>(lane) >> 2, per = static_cast<uint32_t>(a.period);
+      l.t4 = static_cast<uint32_t>(lane) & 3u;
+      l.row8 = WT == WT_F16 ? ((g4 >> 1) | ((g4 & 1u) << 2)) : g4;  // the row of eight that this lane takes
+      l.cp = static_cast<uint32_t>(a.cp);
+      l.rec = rec;
+      l.step8 = l.step16 = l.half = 0;
+      if constexpr (WT == WT_F16) {
+        l.rowbase = l.row8 * 128u;
+      } else if constexpr (PER1) {
+        l.rowbase = l.row8 * tile_pitch<WT>(1);
+      } else {
+        const uint32_t P = tile_pitch<WT>(a.period), res = l.row8 % per;
+        l.rowbase = res * tile_part<WT>(a.period) + l.row8 / per * P + ((res * static_cast<uint32_t>(a.row_bytes)) & 15u);
+        l.step8 = 8u / per * P;
+        l.step16 = 16u / per * P;
+        l.half = per * tile_part<WT>(a.period);
+      }
+      l.xlane = min(g4, l.cp - 1u) * 64u + l.t4 * 16u;  // lanes past the columns read the last one
+      l.m0 = l.cp * 128u + min(2u * l.t4, l.cp - 1u) * 8u;
+      l.m1 = l.cp * 128u + min(2u * l.t4 + 1u, l.cp - 1u) * 8u;
+    }
+    auto group_bar = [&]() { named_bar_sync(1u, 32u * kTileWarps); };
+    int slot = 0, gi = 0, tile = tile_lo;
     uint32_t phase = 0;
     bool ok = true;
-    // stage address of rows row8 (+ 8) of a 16-row tile, and the distances of rows 8 and 16
-    // apart and of the halves
-    const uint32_t P = tile_pitch<WT>(a.period), per = static_cast<uint32_t>(a.period);
-    uint32_t rowbase, step8, step16, half;
-    if constexpr (WT == WT_F16) {
-      rowbase = row8 * 128u;
-      step8 = 1024u;
-      step16 = 2048u;
-      half = 4096u;
-    } else {
-      const uint32_t res = row8 % per;
-      rowbase = res * tile_part<WT>(a.period) + row8 / per * P + ((res * static_cast<uint32_t>(a.row_bytes)) & 15u);
-      step8 = 8u / per * P;
-      step16 = 16u / per * P;
-      half = per * tile_part<WT>(a.period);
-    }
-    const uint32_t cp = static_cast<uint32_t>(a.cp);
-    const uint32_t xlane = min(g4, cp - 1u) * 64u + t4 * 16u;  // lanes past the columns read the last one
-    const uint32_t m0 = cp * 128u + min(2u * t4, cp - 1u) * 8u, m1 = cp * 128u + min(2u * t4 + 1u, cp - 1u) * 8u;
-    auto group_bar = [&]() { named_bar_sync(1u, 32u * kTileWarps); };
-    for (int64_t it = lo; it < hi; ++it) {
-      const int gi = static_cast<int>(it / tiles);
-      const int row0 = static_cast<int>(it - static_cast<int64_t>(gi) * tiles) * kOutRows;
-      const int4 g = a.groups[gi];
+    for (int it = 0; it < n_items; ++it) {
+      const int4 g = groups[gi];
+      const int row0 = tile * kOutRows;
       const int ncol = g.z;
+      // what the tail needs of this warp's columns 8n + wk, on its way during the K loop
+      float factor[NT];
+      int sl[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        factor[n] = 0.0f;
+        sl[n] = 0;
+        if (8 * n + wk < ncol) {
+          if constexpr (MODE == TILE_GLU) {
+            factor[n] = *reinterpret_cast<const float*>(a.records + static_cast<int64_t>(g.w + n) * nblk * rec +
+                                                        l.cp * 128u + static_cast<uint32_t>(wk) * 8u);
+          } else {
+            sl[n] = a.slots[g.y + 8 * n + wk];
+            factor[n] = a.weights[sl[n]];
+          }
+        }
+      }
       float acc[4][NT][4];
 #pragma unroll
       for (int m = 0; m < 4; ++m)
@@ -391,90 +562,33 @@ __global__ void __launch_bounds__(kTileThreads, NT <= 2 ? 2 : 1)
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-      for (int kc = 0; kc < n_kc; ++kc) {
-        ok = ok && mbar_wait_or_abort(full0 + 8u * slot, phase, abort_flag, a.err);
-        const uint32_t st = ring + static_cast<uint32_t>(slot) * stage_bytes;
-        const uint32_t blk = static_cast<uint32_t>(wk);  // this warp's block of the chunk
-        if (ok && kc * kBlocks + wk < nblk) {
-          uint4 b[NT][2];
-          float2 meta[NT][2];  // of columns 2t and 2t + 1 of each column tile
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (8 * n < ncol) {
-              const uint32_t xa = st + xoff + (static_cast<uint32_t>(n) * kBlocks + blk) * rec;
-              b[n][0] = lds128(xa + xlane);
-              b[n][1] = lds128(xa + xlane + cp * 64u);
-              if constexpr (kMeta) {
-                const uint2 u = lds64(xa + m0), v = lds64(xa + m1);
-                meta[n][0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
-                meta[n][1] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
-              }
-            }
+      // the K chunks, for NTA column tiles
+      auto walk = [&](auto nta) {
+        constexpr int NTA = decltype(nta)::value;
+#pragma unroll 1
+        for (int kc = 0; kc < n_kc; ++kc) {
+          ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(full0 + 8u * slot, phase, abort_flag, a.err));
+          const uint32_t st = ring + static_cast<uint32_t>(slot) * stage_bytes;
+          if (ok && kc * kTileBlocks + wk < nblk) {
+            const uint32_t xs = st + xoff + static_cast<uint32_t>(wk) * rec, blk = static_cast<uint32_t>(wk);
+            // codes behind a two-byte scale start on a word in every other block (in rows that
+            // themselves do)
+            if (PER1 && (WT == WT_Q4_0 || WT == WT_Q8_0) && (wk & 1))
+              tile_block<WT, MODE, NTA, NT, PER1, true>(l, st, xs, blk, acc);
+            else
+              tile_block<WT, MODE, NTA, NT, PER1, false>(l, st, xs, blk, acc);
           }
-          // Q4_K: taking a row's 6-bit scale and min apart costs as much as its codes; the four
-          // lanes of a row would all do it, so lane t does it for matrix tile t only
-          float qd[2], qm[2];
-          if constexpr (WT == WT_Q4_K) {
-            const uint32_t mine = st + rowbase + (t4 & 1u) * step16 + (t4 >> 1) * half;
-            q4k_scale_of(lds128(mine), blk, qd[0], qm[0]);
-            q4k_scale_of(lds128(mine + step8), blk, qd[1], qm[1]);
-          }
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            uint32_t a0[2][2], a1[2][2];
-            float d[2], dm[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t row = st + rowbase + (m & 1) * step16 + (m >> 1) * half + h * step8;
-              if constexpr (WT == WT_F16)  // box blk / 2, 16-byte word 4 (blk % 2) + t of the 128, swizzled by the row
-                row += (blk >> 1) * 8192u + ((((blk & 1u) * 4u + t4) ^ row8) << 4);
-              load_block_row<WT>(row, blk, t4, a0[h], a1[h], d[h]);
-              dm[h] = 0.0f;
-              if constexpr (WT == WT_Q4_K) {
-                d[h] = __shfl_sync(0xffffffffu, qd[h], m, 4);
-                dm[h] = __shfl_sync(0xffffffffu, qm[h], m, 4);
-              }
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if (8 * n < ncol) {
-                if constexpr (WT == WT_F16 && MODE != TILE_DOWN) {  // one scale per column: no block scale at all
-                  float (&s)[4] = acc[m][n];
-                  mma_f16(s, a0[0][0], a0[1][0], a0[0][1], a0[1][1], b[n][0].x, b[n][0].y);
-                  mma_f16(s, a1[0][0], a1[1][0], a1[0][1], a1[1][1], b[n][1].x, b[n][1].y);
-                  mma_f16(s, a0[0][0], a0[1][0], a0[0][1], a0[1][1], b[n][0].z, b[n][0].w);
-                  mma_f16(s, a1[0][0], a1[1][0], a1[0][1], a1[1][1], b[n][1].z, b[n][1].w);
-                } else {
-                  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                  mma_f16(s, a0[0][0], a0[1][0], a0[0][1], a0[1][1], b[n][0].x, b[n][0].y);
-                  mma_f16(s, a1[0][0], a1[1][0], a1[0][1], a1[1][1], b[n][1].x, b[n][1].y);
-                  mma_f16(s, a0[0][0], a0[1][0], a0[0][1], a0[1][1], b[n][0].z, b[n][0].w);
-                  mma_f16(s, a1[0][0], a1[1][0], a1[0][1], a1[1][1], b[n][1].z, b[n][1].w);
-                  // i: row row8 (0, 1) or row8 + 8 (2, 3), column 2t + (i & 1)
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const int h = i >> 1, c = i & 1;
-                    if constexpr (MODE == TILE_DOWN) {
-                      float v = WT == WT_F16 ? s[i] : d[h] * s[i];
-                      if constexpr (WT == WT_Q4_K) v = fmaf(-dm[h], meta[n][c].y, v);
-                      acc[m][n][i] = fmaf(meta[n][c].x, v, acc[m][n][i]);
-                    } else {
-                      acc[m][n][i] = fmaf(d[h], s[i], acc[m][n][i]);
-                      if constexpr (WT == WT_Q4_K) acc[m][n][i] = fmaf(-dm[h], meta[n][c].y, acc[m][n][i]);
-                    }
-                  }
-                }
-              }
-            }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty0 + 8u * slot);
+          if (++slot == a.NS) {
+            slot = 0;
+            phase ^= 1u;
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty0 + 8u * slot);
-        if (++slot == a.NS) {
-          slot = 0;
-          phase ^= 1u;
-        }
-      }
+      };
+      if (NT >= 3 && ncol > 16) walk(TileConst<NT >= 3 ? 3 : 1>());
+      else if (NT >= 2 && ncol > 8) walk(TileConst<NT >= 2 ? 2 : 1>());
+      else walk(TileConst<1>());
       // the warps' sums through shared memory, eight columns at a time: red[warp][column][row];
       // then warp wk takes column 8n + wk
 #pragma unroll
@@ -485,7 +599,7 @@ __global__ void __launch_bounds__(kTileThreads, NT <= 2 ? 2 : 1)
         for (int m = 0; m < 4; ++m)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            red[(wk * 8 + 2 * t4 + (i & 1)) * kRedPitch + 16 * m + row8 + 8 * (i >> 1)] = acc[m][n][i];
+            red[(wk * 8 + 2 * l.t4 + (i & 1)) * kRedPitch + 16 * m + l.row8 + 8 * (i >> 1)] = acc[m][n][i];
         group_bar();
         const int c = 8 * n + wk;
         if (c < ncol && ok && !*abort_flag) {
@@ -499,34 +613,36 @@ __global__ void __launch_bounds__(kTileThreads, NT <= 2 ? 2 : 1)
           }
           if constexpr (MODE == TILE_GLU) {
             // 32 output rows of the gated product (rows are a multiple of 32): one record's column
-            const int64_t tile = g.w + n;
-            const float sx =
-                *reinterpret_cast<const float*>(a.records + tile * nblk * rec + cp * 128u + static_cast<uint32_t>(wk) * 8u);
-            const float h = tail_silu(v[0] * sx) * (v[1] * sx);
+            const float gv = v[0] * tile_unit(WT) * factor[n], uv = v[1] * tile_unit(WT) * factor[n];
+            const float h = tail_silu(gv) * uv;
             const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(finite_abs(h))));
             const float sc = pack_scale(m), hs = h * sc;
             float sum = hs;
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const HiLo p = split_hi_lo(hs);
-            uint8_t* q = a.out_records + (tile * (a.rows / 32) + row0 / 32) * rec;
+            const HiLo p = split_hi_lo(lane < 16 ? hs : hs * pack_high(a.out_format));
+            uint8_t* r = a.out_records + (static_cast<int64_t>(g.w + n) * (a.rows / 32) + row0 / 32) * rec;
+            const int order = pack_order(a.out_format);
             const uint32_t i = static_cast<uint32_t>(lane) & 3u;
-            const uint32_t at = record_offset(static_cast<uint32_t>(lane) >> 2, static_cast<uint32_t>(wk), cp, a.out_order) +
-                                2u * (a.out_order == ORDER_NIBBLE ? ((i & 1u) << 1) | (i >> 1) : i);
-            *reinterpret_cast<__half*>(q + at) = p.hi;
-            *reinterpret_cast<__half*>(q + at + 8) = p.lo;
+            const uint32_t at = record_offset(static_cast<uint32_t>(lane) >> 2, static_cast<uint32_t>(wk), l.cp, order) +
+                                2u * (order == ORDER_NIBBLE ? ((i & 1u) << 1) | (i >> 1) : i);
+            *reinterpret_cast<__half*>(r + at) = p.hi;
+            *reinterpret_cast<__half*>(r + at + 8) = p.lo;
             if (lane == 0)
-              *reinterpret_cast<float2*>(q + cp * 128u + static_cast<uint32_t>(wk) * 8u) = make_float2(pow2_inverse(sc), sum);
+              *reinterpret_cast<float2*>(r + l.cp * 128u + static_cast<uint32_t>(wk) * 8u) =
+                  make_float2(pow2_inverse(sc), sum * pack_sum(a.out_format));
           } else {
-            const int sl = a.slots[g.y + c];
-            const float w = a.weights[sl];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int r = row0 + 32 * h + lane;
-              if (r < a.rows) a.y[static_cast<int64_t>(sl) * a.rows + r] = w * v[h];
+              if (r < a.rows) a.y[static_cast<int64_t>(sl[n]) * a.rows + r] = factor[n] * (v[h] * tile_unit(WT));
             }
           }
         }
+      }
+      if (++tile == tiles) {
+        tile = 0;
+        ++gi;
       }
     }
   }
