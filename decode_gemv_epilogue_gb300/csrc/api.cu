@@ -443,6 +443,8 @@ int issue(const LaunchRec& r, cudaStream_t st) {
     e = launch_experts(r.experts, st, r.pdl);
   } else if (r.kind == REC_LORA) {
     e = launch_lora(r.lora, st, r.pdl);
+  } else if (r.kind == REC_LIN) {
+    e = launch_lin(r.lin, st, r.pdl);
   } else if (r.kind == REC_EW) {
     e = launch_elementwise(r.ewop, r.fx, r.fsigns, r.fn, r.fdst, r.fn, st);
   } else if (r.kind == REC_COPY) {
@@ -904,11 +906,27 @@ int gf_prepare_multi(const gf_multi_item* items, int n, int wtype, const float* 
 }
 
 // ------------------------------------------------------------------ low-rank adapters
+static int64_t round_up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// Packed x of the tensor-core projection: per 8 columns and 32 elements a record (tile_mma.cuh).
+static int64_t lin_record_bytes(int64_t ncols, int64_t K) {
+  const int64_t cp = std::min<int64_t>(8, ncols);
+  return round_up256((ncols + 7) / 8 * ((K + 31) / 32) * (cp * 128 + (cp * 8 + 15) / 16 * 16));
+}
+
+// The tensor-core projection takes batches of a block format with rows of whole 16-byte
+// words.
+static bool lin_takes(const Call& c) {
+  const bool fmt = c.wtype == GF_Q8_0 || c.wtype == GF_Q4_0 || c.wtype == GF_Q4_K;
+  return fmt && c.ncols >= 2 && c.K >= 32 && row_bytes_of(c.wtype, c.K) % 16 == 0 && c.K <= (1 << 20) &&
+         aligned(c.W, 16) && !(c.flags & GF_FLAG_NO_TENSOR_CORES);
+}
+
 int64_t gf_lora_workspace(int64_t ncols, int64_t M, int64_t K, int64_t rank, int64_t n) {
   if (ncols < 0 || M < 0 || K < 0 || n < 0 || rank < 1) return GF_ERR_INVALID;
   if (ncols > kMaxBatch || rank > kLoraMaxRank || M > INT32_MAX) return GF_ERR_UNSUPPORTED;
-  // the columns' rank-sized products, then room for one output (silu(y)*m in place)
-  return (ncols * rank * 4 + 255) / 256 * 256 + (ncols * M * 4 + 255) / 256 * 256;
+  // the columns' rank-sized products, room for one output (silu(y)*m in place), packed x
+  return round_up256(ncols * rank * 4) + round_up256(ncols * M * 4) + lin_record_bytes(ncols, K);
 }
 
 // The launches of a gemv_lora call: [transform,] shrink, expand, the shared product with
@@ -972,7 +990,7 @@ static int plan_lora(const void* W, int wtype, const float* x, int64_t M, int64_
     pdl = true;
   }
   float* ws = static_cast<float*>(lo->workspace);
-  float* spare = ws + (c.ncols * lo->rank * 4 + 255) / 256 * 64;
+  float* spare = ws + round_up256(c.ncols * lo->rank * 4) / 4;
   LoraArgs l = {};
   l.atype = lo->atype;
   l.A = static_cast<const uint8_t*>(lo->A);
@@ -992,6 +1010,34 @@ static int plan_lora(const void* W, int wtype, const float* x, int64_t M, int64_
   float* out = (epilogue == GF_EPI_SILU_MUL && aux == dst) ? spare : dst;
   l.out = out;
   l.aux = epilogue == GF_EPI_ADD ? aux : nullptr;
+  const bool lin = lin_takes(c);
+  LinArgs q = {};
+  if (lin) {
+    unsigned* err = device_error_word();
+    if (!err) return cuda_fail(cudaGetLastError());
+    const DeviceLimits lim = device_limits();
+    q.wtype = wtype;
+    q.W = static_cast<const uint8_t*>(W);
+    q.x = c.x;
+    q.gamma = c.gamma;
+    q.eps = c.eps;
+    q.aux = q.dst = out;
+    q.records = reinterpret_cast<uint8_t*>(spare) + round_up256(c.ncols * M * 4);
+    q.err = err;
+    q.M = static_cast<int>(M);
+    q.K = static_cast<int>(K);
+    q.ncols = static_cast<int>(c.ncols);
+    q.cols = c.ncols <= 8 ? static_cast<int>(c.ncols) : c.ncols <= 16 ? 16 : 24;
+    q.cp = static_cast<int>(std::min<int64_t>(8, c.ncols));
+    q.sm_count = lim.sm_count;
+    q.smem_optin = lim.smem_optin;
+    q.phase = LIN_PACK;
+    LaunchRec& r = recs[(*n)++];
+    r.kind = REC_LIN;
+    r.pdl = pdl;
+    r.lin = q;
+    pdl = true;
+  }
   l.phase = LORA_SHRINK;
   LaunchRec& r0 = recs[(*n)++];
   r0.kind = REC_LORA;
@@ -1011,10 +1057,19 @@ static int plan_lora(const void* W, int wtype, const float* x, int64_t M, int64_
     case GF_EPI_SILU_MUL: c.epi = EPI_ADD_SILU; break;
     default: c.epi = GF_EPI_ADD; break;
   }
-  int m = 0;
-  v = plan_launches(c, out, recs + *n, cap - *n, &m);
-  if (v != GF_OK) return v;
-  *n += m;
+  if (lin) {
+    q.phase = LIN_PRODUCT;
+    q.epi = c.epi;
+    LaunchRec& r = recs[(*n)++];
+    r.kind = REC_LIN;
+    r.pdl = true;
+    r.lin = q;
+  } else {
+    int m = 0;
+    v = plan_launches(c, out, recs + *n, cap - *n, &m);
+    if (v != GF_OK) return v;
+    *n += m;
+  }
   if (epilogue == GF_EPI_SILU_MUL) {
     if (*n >= cap) return GF_ERR_UNSUPPORTED;
     LaunchRec& e = recs[(*n)++];

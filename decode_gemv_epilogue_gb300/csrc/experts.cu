@@ -13,7 +13,7 @@
 // row of a slot's expert, weights decoded element by element, then the same combination.
 #include <algorithm>
 
-#include "tile_mma.cuh"
+#include "tile_host.cuh"
 
 namespace gf {
 
@@ -77,20 +77,8 @@ __global__ void __launch_bounds__(256) experts_combine_kernel(const __grid_const
   a.dst[o] = s;
 }
 
-static cudaLaunchConfig_t config(dim3 grid, int threads, cudaStream_t st, bool pdl, cudaLaunchAttribute* attr) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.stream = st;
-  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr->val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cfg;
-}
-
 // ------------------------------------------------------------------ lists and packed x
-constexpr int kPrepThreads = 1024;
+constexpr int kPrepThreads = kPackThreads;
 constexpr int kPrepMaxIter = kExpMaxTokens * kRouteMaxTopK / kPrepThreads;  // 32-slot steps of a warp
 
 static int prep_smem(int E) { return 32 * E * 2 + E * 4 + (32 + 16) * 4; }
@@ -202,61 +190,10 @@ __device__ void list_slots(const ExpertsArgs& a, bool write, int my_tile, PrepTi
   __syncthreads();
 }
 
-// The column tile's records: 128 threads a column, one scale for the whole column.
-__device__ void pack_tile(const ExpertsArgs& a, int tile, const PrepTile& pt, float* wmax) {
-  const int c = threadIdx.x >> 7, i0 = threadIdx.x & 127, lane = threadIdx.x & 31;
-  const bool live = c < pt.count;
-  const int n4 = a.K / 4, cp = a.cp, order = pack_order(a.wtype);
-  const float high = pack_high(a.wtype), sumf = pack_sum(a.wtype);
-  const float* x = a.x + static_cast<int64_t>(live ? pt.slot[c] / a.k : 0) * a.K;
-  const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
-  auto load = [&](int i) -> float4 {
-    if (!live || i >= n4) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (vec) return reinterpret_cast<const float4*>(x)[i];
-    return make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-  };
-  constexpr int kKeep = 4;  // groups of four a thread keeps between the two passes
-  float4 keep[kKeep];
-  float m = 0.0f;
-#pragma unroll
-  for (int j = 0; j < kKeep; ++j) keep[j] = load(i0 + 128 * j);
-  auto top = [](float4 v) {
-    return fmaxf(fmaxf(finite_abs(v.x), finite_abs(v.y)), fmaxf(finite_abs(v.z), finite_abs(v.w)));
-  };
-#pragma unroll
-  for (int j = 0; j < kKeep; ++j) m = fmaxf(m, top(keep[j]));
-  for (int i = i0 + 128 * kKeep; i < n4; i += 128) m = fmaxf(m, top(load(i)));
-  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-  if (lane == 0) wmax[threadIdx.x >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int q = 0; q < 4; ++q) m = fmaxf(m, wmax[4 * c + q]);
-  const float sc = pack_scale(m), inv = pow2_inverse(sc);
-  const int rec = record_bytes(cp);
-  uint8_t* base = a.xrec + static_cast<int64_t>(tile) * (a.K / 32) * rec;
-  auto put = [&](int i, float4 v) {
-    v.x *= sc; v.y *= sc; v.z *= sc; v.w *= sc;
-    float sum = (v.x + v.y) + (v.z + v.w);
-#pragma unroll
-    for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((i & 4) != 0) {
-      v.x *= high; v.y *= high; v.z *= high; v.w *= high;
-    }
-    if (live && i < n4) {
-      uint8_t* r = base + static_cast<int64_t>(i >> 3) * rec;
-      *reinterpret_cast<uint4*>(r + record_offset(i & 7, c, cp, order)) = pack_group(v, order == ORDER_NIBBLE);
-      if ((i & 7) == 0) *reinterpret_cast<float2*>(r + cp * 128 + c * 8) = make_float2(inv, sum * sumf);
-    }
-  };
-#pragma unroll
-  for (int j = 0; j < kKeep; ++j) put(i0 + 128 * j, keep[j]);
-  for (int b = 128 * kKeep; b < n4; b += 128) put(b + i0, load(b + i0));
-}
-
 __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(const __grid_constant__ ExpertsArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ PrepTile pt;
-  __shared__ float wmax[kPrepThreads / 32];
+  __shared__ float wmax[2 * kPrepThreads / 32];
   pdl_wait();
   pdl_trigger();
   uint32_t* offs = reinterpret_cast<uint32_t*>(smem);
@@ -264,60 +201,21 @@ __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(const __grid
   int* range = reinterpret_cast<int*>(wsum + 32);
   const int tile = static_cast<int>(blockIdx.x);
   list_slots(a, tile == 0, tile, &pt, reinterpret_cast<uint16_t*>(range + 16), offs, wsum, range);
-  if (pt.count > 0) pack_tile(a, tile, pt, wmax);
+  if (pt.count > 0) {
+    const int c = threadIdx.x / kPackColumn;
+    const float* x = c < pt.count ? a.x + static_cast<int64_t>(pt.slot[c] / a.k) * a.K : nullptr;
+    pack_tile(x, nullptr, 0.0f, a.K, a.wtype, a.cp, a.xrec + static_cast<int64_t>(tile) * (a.K / 32) * record_bytes(a.cp),
+              wmax);
+  }
 }
 
 // ------------------------------------------------------------------ tiled products
-// Tensor map over the rows of all matrices of one kind.
-template <int WT>
-static int tile_map(const void* W, int64_t all_rows, int row_bytes, CUtensorMap* out) {
-  if (WT == WT_F16)
-    return cached_map_2d(W, kMapF16, static_cast<uint64_t>(row_bytes / 2), static_cast<uint64_t>(all_rows), 64, 32, true, out);
-  const int p = tile_period(row_bytes);
-  return cached_map_2d(W, kMapF16, static_cast<uint64_t>(row_bytes) * p / 2, static_cast<uint64_t>(all_rows / p),
-                       static_cast<uint32_t>(tile_pitch<WT>(p) / 2), static_cast<uint32_t>(32 / p), false, out);
-}
-
-template <int WT, int MODE, int NT, bool PER1>
-static int launch_tile_t(TileArgs t, const ExpertsArgs& a, cudaStream_t st, bool pdl) {
-  auto kern = tile_kernel<WT, MODE, NT, PER1>;
-  CUtensorMap m0, m1;
-  const int64_t all_rows = static_cast<int64_t>(a.E) * t.rows;
-  int e = tile_map<WT>(a.W, all_rows, t.row_bytes, &m0);
-  if (e != cudaSuccess) return e;
-  m1 = m0;
-  if (MODE == TILE_GLU) e = tile_map<WT>(a.W2, all_rows, t.row_bytes, &m1);
-  if (e != cudaSuccess) return e;
-  const int stage = tile_stage_bytes<WT>(t.period, NT, t.cp), fixed = kTileHeadBytes + kTileRedBytes + 1024;
-  // as many CTAs per SM as leave each three stages; 1 KB a CTA is the system's
-  int ctas = tile_ctas(NT), ns = 0;
-  for (; ctas >= 1; --ctas) {
-    const int budget = ctas == 1 ? a.smem_optin : (a.smem_optin + 1024) / ctas - 1024;
-    ns = std::min(kTileMaxStages, (budget - fixed) / stage);
-    if (ns >= 3 || ctas == 1) break;
-  }
-  if (ns < 2 || a.max_tiles / (ctas * a.sm_count) + 2 > kTileMaxGroups) return cudaErrorInvalidConfiguration;
-  t.NS = ns;
-  const int smem = fixed + ns * stage;
-  static int configured[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && configured[dev] < smem) {
-    const cudaError_t c = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (c != cudaSuccess) return c;
-    configured[dev] = smem;
-  }
-  cudaLaunchAttribute attr;
-  cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(ctas * a.sm_count)), kTileThreads, st, pdl, &attr);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  return cudaLaunchKernelEx(&cfg, kern, m0, m1, t);
-}
-
 template <int WT, int MODE, bool PER1>
 static int launch_tile_cols(const TileArgs& t, const ExpertsArgs& a, cudaStream_t st, bool pdl) {
-  if (a.cols <= 8) return launch_tile_t<WT, MODE, 1, PER1>(t, a, st, pdl);
-  if (a.cols <= 16) return launch_tile_t<WT, MODE, 2, PER1>(t, a, st, pdl);
-  return launch_tile_t<WT, MODE, 3, PER1>(t, a, st, pdl);
+  const TileOperands o = {a.W, a.W2, static_cast<int64_t>(a.E) * t.rows, a.max_tiles, a.sm_count, a.smem_optin};
+  if (a.cols <= 8) return launch_tile<WT, MODE, 1, PER1>(t, o, st, pdl);
+  if (a.cols <= 16) return launch_tile<WT, MODE, 2, PER1>(t, o, st, pdl);
+  return launch_tile<WT, MODE, 3, PER1>(t, o, st, pdl);
 }
 
 template <int MODE>
@@ -335,8 +233,8 @@ static int launch_tiles(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
   t.err = a.err;
   t.out_records = a.hrec;
   t.out_format = a.out_format;
-  t.weights = a.weights;
-  t.y = a.y;
+  t.factors = a.weights;
+  t.out = a.y;
   switch (a.wtype) {
     case WT_F16: return launch_tile_cols<WT_F16, MODE, true>(t, a, st, pdl);
     case WT_Q8_0:

@@ -290,11 +290,30 @@ struct LoraArgs {
 };
 int launch_lora(const LoraArgs& a, cudaStream_t st, bool pdl);
 
+// The shared projection of a batch in a block format on the tensor cores (tile_lin.cu).
+enum { LIN_PACK = 0, LIN_PRODUCT = 1 };
+struct LinArgs {
+  int phase;
+  int wtype;            // GF_Q8_0, GF_Q4_0, GF_Q4_K, rows of whole 16-byte words
+  const uint8_t* W;
+  const float* x;       // [ncols][K]
+  const float* gamma;
+  float eps;
+  const float* aux;
+  float* dst;           // [ncols][M]
+  uint8_t* records;     // packed x
+  unsigned* err;
+  int M, K, epi, ncols;
+  int cols, cp;         // columns per group, stored per column tile
+  int sm_count, smem_optin;
+};
+int launch_lin(const LinArgs& a, cudaStream_t st, bool pdl);
+
 // One kernel launch with every argument resolved: what a call plans, and what a
 // prepared call keeps (gf_prepare) so that launching it does no planning at all.
 enum {
   REC_FWHT = 0, REC_TC = 1, REC_STREAM = 2, REC_GENERIC = 3, REC_COPY = 4, REC_ROUTE = 5, REC_EXPERTS = 6,
-  REC_LORA = 7, REC_EW = 8
+  REC_LORA = 7, REC_EW = 8, REC_LIN = 9
 };
 struct LaunchRec {
   int kind;
@@ -317,6 +336,7 @@ struct LaunchRec {
   RouteArgs route;
   ExpertsArgs experts;
   LoraArgs lora;
+  LinArgs lin;
 };
 constexpr int kMaxRecs = 1 + kMaxSeg * (kMaxBatch / kMaxCols);  // transform + column blocks (per matrix)
 

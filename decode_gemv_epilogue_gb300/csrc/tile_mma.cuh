@@ -137,6 +137,83 @@ __device__ __forceinline__ float finite_abs(float v) {
   return a <= 3.402823466e38f ? a : 0.0f;  // Inf and NaN do not set the scale
 }
 
+// A column tile's records, by a CTA of kPackThreads: 128 threads a column, one scale for the
+// whole column.  x: this thread's column (nullptr: none).  With gamma the column is first
+// normalised, x / sqrt(mean(x^2) + eps) gamma: gamma multiplies before packing, the root
+// enters through the stored scale.  wmax: 2 kPackThreads / 32 floats of shared memory.
+constexpr int kPackThreads = 1024;
+constexpr int kPackColumn = 128;
+__device__ inline void pack_tile(const float* x, const float* gamma, float eps, int K, int fmt, int cp, uint8_t* base,
+                                 float* wmax) {
+  const int c = threadIdx.x / kPackColumn, i0 = threadIdx.x % kPackColumn, lane = threadIdx.x & 31;
+  const int n4 = K / 4, order = pack_order(fmt);
+  const float high = pack_high(fmt), sumf = pack_sum(fmt);
+  const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(gamma)) & 15u) == 0;
+  auto four = [&](const float* p, int i) -> float4 {
+    if (vec) return reinterpret_cast<const float4*>(p)[i];
+    return make_float4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+  };
+  float ss = 0.0f;
+  auto load = [&](int i, bool sq) -> float4 {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (x != nullptr && i < n4) {
+      v = four(x, i);
+      if (gamma != nullptr) {
+        if (sq) ss = fmaf(v.x, v.x, fmaf(v.y, v.y, fmaf(v.z, v.z, fmaf(v.w, v.w, ss))));
+        const float4 g = four(gamma, i);
+        v.x *= g.x; v.y *= g.y; v.z *= g.z; v.w *= g.w;
+      }
+    }
+    return v;
+  };
+  auto top = [](float4 v) {
+    return fmaxf(fmaxf(finite_abs(v.x), finite_abs(v.y)), fmaxf(finite_abs(v.z), finite_abs(v.w)));
+  };
+  constexpr int kKeep = 4;  // groups of four a thread keeps between the two passes
+  float4 keep[kKeep];
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j) keep[j] = load(i0 + kPackColumn * j, true);
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j) m = fmaxf(m, top(keep[j]));
+  for (int i = i0 + kPackColumn * kKeep; i < n4; i += kPackColumn) m = fmaxf(m, top(load(i, true)));
+  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (lane == 0) {
+    wmax[threadIdx.x >> 5] = m;
+    wmax[kPackThreads / 32 + (threadIdx.x >> 5)] = ss;
+  }
+  __syncthreads();
+  ss = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    m = fmaxf(m, wmax[4 * c + q]);
+    ss += wmax[kPackThreads / 32 + 4 * c + q];
+  }
+  const float sc = pack_scale(m);
+  float inv = pow2_inverse(sc);
+  if (gamma != nullptr) inv *= 1.0f / sqrtf(ss / static_cast<float>(K) + eps);
+  const int rec = record_bytes(cp);
+  auto put = [&](int i, float4 v) {
+    v.x *= sc; v.y *= sc; v.z *= sc; v.w *= sc;
+    float sum = (v.x + v.y) + (v.z + v.w);
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((i & 4) != 0) {
+      v.x *= high; v.y *= high; v.z *= high; v.w *= high;
+    }
+    if (x != nullptr && i < n4) {
+      uint8_t* r = base + static_cast<int64_t>(i >> 3) * rec;
+      *reinterpret_cast<uint4*>(r + record_offset(i & 7, c, cp, order)) = pack_group(v, order == ORDER_NIBBLE);
+      if ((i & 7) == 0) *reinterpret_cast<float2*>(r + cp * 128 + c * 8) = make_float2(inv, sum * sumf);
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < kKeep; ++j) put(i0 + kPackColumn * j, keep[j]);
+  for (int b = kPackColumn * kKeep; b < n4; b += kPackColumn) put(b + i0, load(b + i0, false));
+}
+
 // ------------------------------------------------------------------ A fragments
 // d * sc[j] and dmin * m[j] of a Q4_K super-block from its first 16 bytes (both exact).  The
 // 6-bit integers become floats in the low bits of 2^23: a conversion instruction has a
@@ -255,7 +332,9 @@ constexpr int kTileMaxGroups = 64;      // column groups a CTA's items may touch
 constexpr int kTileHeadBytes = 256 + 16 * kTileMaxGroups;  // barriers, abort flag, groups
 constexpr int kRedPitch = kTileRows + 4;
 constexpr int kTileRedBytes = kTileWarps * 8 * kRedPitch * 4;  // the warps' sums of eight columns
-enum { TILE_GLU = 0, TILE_DOWN = 1 };
+// The gated product; one that scales each column by a factor of its own; the plain product
+// of all columns of a batch with a fused tail.
+enum { TILE_GLU = 0, TILE_DOWN = 1, TILE_LIN = 2 };
 __host__ __device__ constexpr int tile_ctas(int nt) { return nt <= 2 ? 2 : 1; }
 
 template <int WT>
@@ -293,10 +372,13 @@ struct TileArgs {
   int NS;
   unsigned* err;
   // tails
-  uint8_t* out_records;     // gated: records of the next product's x
+  uint8_t* out_records;     // TILE_GLU: records of the next product's x
   int out_format;           // of the next product's weights
-  const float* weights;     // down: factor of a slot
-  float* y;                 // down: [slot][rows]
+  const float* factors;     // TILE_DOWN: factor of a slot
+  float* out;               // TILE_DOWN: [slot][rows]; TILE_LIN: [column][rows]
+  const float* aux;         // TILE_LIN: may be `out`
+  int epi;
+  int ncols, group_cols;    // TILE_LIN: columns of the batch, of a group (no list of groups)
 };
 
 // One lane's constants of the walk over a stage.
@@ -437,12 +519,15 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
   pdl_trigger();
   pdl_wait();
   const int tiles = (a.rows + kOutRows - 1) / kOutRows;
-  const int64_t items = static_cast<int64_t>(*a.n_groups) * tiles;
+  const int n_groups = MODE == TILE_LIN ? (a.ncols + a.group_cols - 1) / a.group_cols : *a.n_groups;
+  const int64_t items = static_cast<int64_t>(n_groups) * tiles;
   const int64_t lo = items * blockIdx.x / gridDim.x, hi = items * (blockIdx.x + 1) / gridDim.x;
   const int g_lo = static_cast<int>(lo / tiles);
   if (lo < hi)
     for (int i = threadIdx.x; i <= static_cast<int>((hi - 1) / tiles) - g_lo; i += kTileThreads)
-      groups[i] = a.groups[g_lo + i];
+      groups[i] = MODE == TILE_LIN ? make_int4(0, 0, min(a.group_cols, a.ncols - (g_lo + i) * a.group_cols),
+                                               (g_lo + i) * ((a.group_cols + 7) / 8))
+                                   : a.groups[g_lo + i];
   __syncthreads();
   const int n_kc = (a.K + kTileK - 1) / kTileK, nblk = a.K / 32;
   const int n_items = static_cast<int>(hi - lo);
@@ -546,12 +631,12 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
         factor[n] = 0.0f;
         sl[n] = 0;
         if (8 * n + wk < ncol) {
-          if constexpr (MODE == TILE_GLU) {
+          if constexpr (MODE != TILE_DOWN) {
             factor[n] = *reinterpret_cast<const float*>(a.records + static_cast<int64_t>(g.w + n) * nblk * rec +
                                                         l.cp * 128u + static_cast<uint32_t>(wk) * 8u);
           } else {
             sl[n] = a.slots[g.y + 8 * n + wk];
-            factor[n] = a.weights[sl[n]];
+            factor[n] = a.factors[sl[n]];
           }
         }
       }
@@ -635,7 +720,15 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int r = row0 + 32 * h + lane;
-              if (r < a.rows) a.y[static_cast<int64_t>(sl[n]) * a.rows + r] = factor[n] * (v[h] * tile_unit(WT));
+              if (r < a.rows) {
+                const int64_t col = MODE == TILE_LIN ? (g.w + n) * 8 + wk : sl[n];
+                const int64_t o = col * a.rows + r;
+                const float y = factor[n] * (v[h] * tile_unit(WT));
+                if constexpr (MODE == TILE_LIN)
+                  a.out[o] = apply_tail(a.epi, y, epi_takes_aux(a.epi) ? a.aux[o] : 0.0f);  // aux may be out
+                else
+                  a.out[o] = y;
+              }
             }
           }
         }
