@@ -85,7 +85,7 @@ static int prep_smem(int E) { return 32 * E * 2 + E * 4 + (32 + 16) * 4; }
 
 // The column tile of a prep CTA: up to eight slots of one expert.
 struct PrepTile {
-  int count;
+  int count, cp;  // columns of the tile; stored per column tile of its group
   int slot[8];
 };
 
@@ -166,6 +166,8 @@ __device__ void list_slots(const ExpertsArgs& a, bool write, int my_tile, PrepTi
     const uint32_t f = 8u * (static_cast<uint32_t>(my_tile) - t0);
     range[0] = static_cast<int>(off + f);
     range[1] = static_cast<int>(min(8u, total - f));
+    const uint32_t group = f / (gt * 8u) * (gt * 8u);  // the group's first column
+    out->cp = static_cast<int>(min(8u, total - group));
   }
   if (write) {
     uint32_t groups;
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(const __grid
   if (pt.count > 0) {
     const int c = threadIdx.x / kPackColumn;
     const float* x = c < pt.count ? a.x + static_cast<int64_t>(pt.slot[c] / a.k) * a.K : nullptr;
-    pack_tile(x, nullptr, 0.0f, a.K, a.wtype, a.cp, a.xrec + static_cast<int64_t>(tile) * (a.K / 32) * record_bytes(a.cp),
+    pack_tile(x, nullptr, 0.0f, a.K, a.wtype, pt.cp, a.xrec + static_cast<int64_t>(tile) * (a.K / 32) * record_bytes(a.cp),
               wmax);
   }
 }

@@ -46,17 +46,28 @@ int launch_tile(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
   m1 = m0;
   if (MODE == TILE_GLU) e = tile_map<WT>(o.W2, o.all_rows, t.row_bytes, &m1);
   if (e != cudaSuccess) return e;
-  const int stage = tile_stage_bytes<WT>(t.period, NT, t.cp), fixed = kTileHeadBytes + kTileRedBytes + 1024;
-  // as many CTAs per SM as leave each three stages; 1 KB a CTA is the system's
-  int ctas = tile_ctas(NT), ns = 0;
-  for (; ctas >= 1; --ctas) {
-    const int budget = ctas == 1 ? o.smem_optin : (o.smem_optin + 1024) / ctas - 1024;
-    ns = std::min(kTileMaxStages, (budget - fixed) / stage);
-    if (ns >= 3 || ctas == 1) break;
-  }
+  // The columns' records of whole groups where they leave three stages of weights, in two
+  // buffers where those leave four, with as many CTAs per SM as the registers allow or one;
+  // else the records go with the weights.  1 KB a CTA is the system's.
+  const int fixed = kTileHeadBytes + kTileRedBytes + 1024;
+  const int64_t xb = tile_x_bytes(t.K, NT, t.cp);
+  int ctas = tile_ctas(NT), ns = 0, stage = 0;
+  int64_t x_all = 0;
+  auto plan = [&](int n, int buffers, int want) {
+    const int budget = n == 1 ? o.smem_optin : (o.smem_optin + 1024) / n - 1024;
+    if (fixed + buffers * xb >= budget) return false;
+    stage = tile_stage_bytes<WT>(t.period, NT, t.cp, buffers > 0);
+    ns = static_cast<int>(std::min<int64_t>(kTileMaxStages, (budget - fixed - buffers * xb) / stage));
+    ctas = n;
+    t.xbuffers = buffers;
+    x_all = buffers * xb;
+    return ns >= want;
+  };
+  const int most = tile_ctas(NT);
+  if (!plan(most, 2, 4) && !plan(most, 1, 3) && !plan(1, 2, 4) && !plan(1, 1, 3) && !plan(most, 0, 3)) plan(1, 0, 2);
   if (ns < 2 || o.max_groups / (ctas * o.sm_count) + 2 > kTileMaxGroups) return cudaErrorInvalidConfiguration;
   t.NS = ns;
-  const int smem = fixed + ns * stage;
+  const int smem = fixed + static_cast<int>(x_all) + ns * stage;
   static int configured[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);

@@ -9,8 +9,10 @@ __global__ void __launch_bounds__(kPackThreads) tile_pack_kernel(const __grid_co
   __shared__ float wmax[2 * kPackThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int col = static_cast<int>(blockIdx.x) * 8 + threadIdx.x / kPackColumn;
-  pack_tile(col < a.ncols ? a.x + static_cast<int64_t>(col) * a.K : nullptr, a.gamma, a.eps, a.K, a.wtype, a.cp,
+  const int tile = static_cast<int>(blockIdx.x), col = tile * 8 + threadIdx.x / kPackColumn;
+  const int first = tile * 8 / a.cols * a.cols;  // of the column group
+  const int cp = min(8, min(a.cols, a.ncols - first));
+  pack_tile(col < a.ncols ? a.x + static_cast<int64_t>(col) * a.K : nullptr, a.gamma, a.eps, a.K, a.wtype, cp,
             a.records + static_cast<int64_t>(blockIdx.x) * (a.K / 32) * record_bytes(a.cp), wmax);
 }
 

@@ -73,8 +73,8 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 // form a column tile, and for every 32 elements a column tile has one record:
 //   [step s of 2][column of cp][thread t of 4] 16 bytes {hi, hi, hi, hi, lo, lo, lo, lo},
 //   then per column {2^-s, the block's sum of x 2^s times pack_sum(format)};
-// cp = min(8, columns of the call) columns are stored, so that a single column does not move
-// eight.  A warp's 16-byte reads of a step are then consecutive, and the records of a K chunk
+// cp = min(8, columns of the group) columns are stored, so that a single column does not move
+// eight (column tiles are allocated for the most any group of the call can have).  A warp's 16-byte reads of a step are then consecutive, and the records of a K chunk
 // are one piece of memory for one bulk copy.  Which four elements (s, t) holds is the
 // weights' choice: 16 s + 4 t + .. in the order 0, 2, 1, 3 for the nibble formats (two masks
 // take a code word apart in that order), 16 s + 4 t + 0..3 for Q8_0, and 8 t + 4 s + 0..3
@@ -297,9 +297,11 @@ __device__ __forceinline__ void load_block_row(const RowPlace& p, uint32_t off, 
 
 // ------------------------------------------------------------------ the tiled kernel
 // A work item is (column group, row tile): up to 8 NT columns that share one matrix, and
-// 64 rows of it (gated: 32 gate rows and the same up rows).  Warp 0 streams the item's K
-// chunks of 256 -- the rows' weights by tensor-map copies of 32 rows, the columns' records
-// by one bulk copy per column tile -- through a ring of shared-memory stages.  The eight
+// 64 rows of it (gated: 32 gate rows and the same up rows).  Warp 0 streams the rows' weights
+// in K chunks of 256, by tensor-map copies of 32 rows, through a ring of shared-memory
+// stages.  The columns' records are brought in once for all the row tiles of a group that a
+// CTA has (items are handed out in that order) where the whole K of them fits beside three
+// stages, else chunk by chunk with the weights.  The eight
 // consumer warps share the K axis: a warp takes one 32-element block of the chunk for all 64
 // rows (four 16-row matrix tiles), so that a packed x fragment, once loaded, serves four
 // matrix tiles.  At the end of an item the warps' accumulators are added through shared
@@ -330,6 +332,7 @@ constexpr int kTileThreads = 32 * (1 + kTileWarps);
 constexpr int kTileMaxStages = 8;
 constexpr int kTileMaxGroups = 64;      // column groups a CTA's items may touch
 constexpr int kTileHeadBytes = 256 + 16 * kTileMaxGroups;  // barriers, abort flag, groups
+constexpr int kTileMaxXBuffers = 2;
 constexpr int kRedPitch = kTileRows + 4;
 constexpr int kTileRedBytes = kTileWarps * 8 * kRedPitch * 4;  // the warps' sums of eight columns
 // The gated product; one that scales each column by a factor of its own; the plain product
@@ -356,9 +359,14 @@ template <int WT>
 __host__ __device__ constexpr int tile_weight_bytes(int period) {
   return WT == WT_F16 ? kTileRows * kTileK * 2 : 2 * period * tile_part<WT>(period);
 }
+// A stage: weights, and in the chunk by chunk case the records of the chunk.
 template <int WT>
-__host__ __device__ constexpr int tile_stage_bytes(int period, int nt, int cp) {
-  return (tile_weight_bytes<WT>(period) + 16 + nt * kTileBlocks * record_bytes(cp) + 1023) / 1024 * 1024;
+__host__ __device__ constexpr int tile_stage_bytes(int period, int nt, int cp, bool resident) {
+  return (tile_weight_bytes<WT>(period) + 16 + (resident ? 0 : nt * kTileBlocks * record_bytes(cp)) + 1023) / 1024 * 1024;
+}
+// Records of a group's whole K.
+__host__ __device__ constexpr int64_t tile_x_bytes(int K, int nt, int cp) {
+  return (static_cast<int64_t>(nt) * (K / 32) * record_bytes(cp) + 127) / 128 * 128;
 }
 
 struct TileArgs {
@@ -368,8 +376,9 @@ struct TileArgs {
   const int32_t* n_groups;
   const int32_t* slots;     // slot of each entry
   const uint8_t* records;   // [column tile][K / 32] records of x
-  int cp;
+  int cp;                   // most columns stored per column tile
   int NS;
+  int xbuffers;             // 1 or 2 buffers of a group's records; 0: they come chunk by chunk
   unsigned* err;
   // tails
   uint8_t* out_records;     // TILE_GLU: records of the next product's x
@@ -385,7 +394,8 @@ struct TileArgs {
 struct TileLane {
   uint32_t rowbase, step8, step16, half;  // rows row8, + 8, + 16, + 32
   uint32_t row8, t4;
-  uint32_t xlane, m0, m1, cp, rec;
+  uint32_t xlane, m0, m1, cp, rec;        // of the group's records
+  uint32_t xtile;                         // distance of column tiles in shared memory
 };
 
 // This warp's block `blk` of a stage (weights at st, its records at xs): acc += W x for 64
@@ -404,7 +414,7 @@ __device__ __forceinline__ void tile_block(const TileLane& l, uint32_t st, uint3
   float2 meta[NTA][2];  // of columns 2t and 2t + 1 of each column tile
 #pragma unroll
   for (int n = 0; n < NTA; ++n) {
-    const uint32_t xa = xs + static_cast<uint32_t>(n) * kTileBlocks * l.rec;
+    const uint32_t xa = xs + static_cast<uint32_t>(n) * l.xtile;
     b[n][0] = lds128(xa + l.xlane);
     b[n][1] = lds128(xa + l.xlane + l.cp * 64u);
     if constexpr (kMeta) {
@@ -502,15 +512,22 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 248);
   int4* groups = reinterpret_cast<int4*>(smem + 256);
   float* red = reinterpret_cast<float*>(smem + kTileHeadBytes);
-  const uint32_t ring = (sbase + kTileHeadBytes + kTileRedBytes + 1023u) & ~1023u;
-  const uint32_t rec = static_cast<uint32_t>(record_bytes(a.cp));
-  const uint32_t stage_bytes = tile_stage_bytes<WT>(a.period, NT, a.cp);
+  const uint32_t xfull0 = sbase + 128u, xempty0 = xfull0 + 8u * kTileMaxXBuffers;
+  const bool resident = a.xbuffers > 0;
+  const uint32_t xbytes = resident ? static_cast<uint32_t>(tile_x_bytes(a.K, NT, a.cp)) : 0u;
+  const uint32_t xres = sbase + kTileHeadBytes + kTileRedBytes;
+  const uint32_t ring = (xres + a.xbuffers * xbytes + 1023u) & ~1023u;
+  const uint32_t stage_bytes = tile_stage_bytes<WT>(a.period, NT, a.cp, resident);
   const uint32_t xoff = tile_weight_bytes<WT>(a.period) + 16;  // slack: words are read up to 3 bytes past a row
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < a.NS; ++i) {
       mbar_init(full0 + 8u * i, 1);
       mbar_init(empty0 + 8u * i, kTileWarps);
+    }
+    for (int i = 0; i < kTileMaxXBuffers; ++i) {
+      mbar_init(xfull0 + 8u * i, 1);
+      mbar_init(xempty0 + 8u * i, kTileWarps);
     }
     fence_mbar_init();
     prefetch_tmap(&map0);
@@ -532,11 +549,12 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
   const int n_kc = (a.K + kTileK - 1) / kTileK, nblk = a.K / 32;
   const int n_items = static_cast<int>(hi - lo);
   const int tile_lo = static_cast<int>(lo - static_cast<int64_t>(g_lo) * tiles);
+  const int64_t tile_stride = static_cast<int64_t>(nblk) * record_bytes(a.cp);  // of column tiles in memory
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int slot = 0, issued = 0, gi = 0, tile = tile_lo;
+      int slot = 0, issued = 0, gi = 0, tile = tile_lo, xgroups = 0;
       uint32_t phase = 1u;
       bool ok = true;
       const uint32_t wlen = WT == WT_F16 ? 32u * kTileK * 2u : 32u * static_cast<uint32_t>(tile_pitch<WT>(a.period));
@@ -546,14 +564,28 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
         const int halves = MODE == TILE_GLU || row0 + 32 < a.rows ? 2 : 1;
         const int nt = (g.z + 7) / 8;
         const int first = g.x * a.rows + row0;
-        const uint8_t* xsrc = a.records + static_cast<int64_t>(g.w) * nblk * rec;
+        const uint8_t* xsrc = a.records + g.w * tile_stride;
+        const uint32_t rec = static_cast<uint32_t>(record_bytes(min(8, g.z)));
+        if (resident && (it == 0 || tile == 0)) {  // a new group: its records, once the buffer is free
+          const int b = gi % a.xbuffers;
+          if (gi >= a.xbuffers &&
+              !mbar_wait_or_abort(xempty0 + 8u * b, static_cast<uint32_t>((gi / a.xbuffers - 1) & 1), abort_flag, a.err)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(xfull0 + 8u * b, static_cast<uint32_t>(nt * nblk) * rec);
+          for (int n = 0; n < nt; ++n)
+            bulk_g2s(xres + b * xbytes + static_cast<uint32_t>(n * nblk) * rec, xsrc + n * tile_stride,
+                     static_cast<uint32_t>(nblk) * rec, xfull0 + 8u * b);
+          xgroups = gi + 1;
+        }
         for (int kc = 0; kc < n_kc; ++kc) {
           if (issued >= a.NS && !mbar_wait_or_abort(empty0 + 8u * slot, phase, abort_flag, a.err)) {
             ok = false;
             break;
           }
           const uint32_t st = ring + static_cast<uint32_t>(slot) * stage_bytes, full = full0 + 8u * slot;
-          const uint32_t xlen = static_cast<uint32_t>(min(kTileBlocks, nblk - kc * kTileBlocks)) * rec;
+          const uint32_t xlen = resident ? 0u : static_cast<uint32_t>(min(kTileBlocks, nblk - kc * kTileBlocks)) * rec;
           mbar_arrive_expect_tx(full, halves * wlen + nt * xlen);
           for (int h = 0; h < halves; ++h) {
             const CUtensorMap* map = MODE == TILE_GLU && h ? &map1 : &map0;
@@ -570,9 +602,9 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
                             ((i * a.row_bytes + kc * tile_seg<WT>()) & ~15) / 2, row / a.period, full);
             }
           }
-          for (int n = 0; n < nt; ++n)
+          for (int n = 0; n < nt && !resident; ++n)
             bulk_g2s(st + xoff + static_cast<uint32_t>(n) * kTileBlocks * rec,
-                     xsrc + (static_cast<int64_t>(n) * nblk + kc * kTileBlocks) * rec, xlen, full);
+                     xsrc + n * tile_stride + static_cast<uint32_t>(kc * kTileBlocks) * rec, xlen, full);
           ++issued;
           if (++slot == a.NS) {
             slot = 0;
@@ -585,9 +617,12 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
         }
       }
       // Drain after an abort: every copy this thread issued lands before the CTA leaves.
-      if (!ok)
+      if (!ok) {
         for (int i = max(0, issued - a.NS); i < issued; ++i)
           (void)mbar_wait(full0 + 8u * (i % a.NS), static_cast<uint32_t>((i / a.NS) & 1));
+        for (int i = max(0, xgroups - a.xbuffers); i < xgroups; ++i)
+          (void)mbar_wait(xfull0 + 8u * (i % a.xbuffers), static_cast<uint32_t>((i / a.xbuffers) & 1));
+      }
     }
   } else {
     // ------------------------------------------------------------ consumers
@@ -597,8 +632,6 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
       const uint32_t g4 = static_cast<uint32_t>(lane) >> 2, per = static_cast<uint32_t>(a.period);
       l.t4 = static_cast<uint32_t>(lane) & 3u;
       l.row8 = WT == WT_F16 ? ((g4 >> 1) | ((g4 & 1u) << 2)) : g4;  // the row of eight that this lane takes
-      l.cp = static_cast<uint32_t>(a.cp);
-      l.rec = rec;
       l.step8 = l.step16 = l.half = 0;
       if constexpr (WT == WT_F16) {
         l.rowbase = l.row8 * 128u;
@@ -611,9 +644,6 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
         l.step16 = 16u / per * P;
         l.half = per * tile_part<WT>(a.period);
       }
-      l.xlane = min(g4, l.cp - 1u) * 64u + l.t4 * 16u;  // lanes past the columns read the last one
-      l.m0 = l.cp * 128u + min(2u * l.t4, l.cp - 1u) * 8u;
-      l.m1 = l.cp * 128u + min(2u * l.t4 + 1u, l.cp - 1u) * 8u;
     }
     auto group_bar = [&]() { named_bar_sync(1u, 32u * kTileWarps); };
     int slot = 0, gi = 0, tile = tile_lo;
@@ -623,6 +653,18 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
       const int4 g = groups[gi];
       const int row0 = tile * kOutRows;
       const int ncol = g.z;
+      {
+        const uint32_t g4 = static_cast<uint32_t>(lane) >> 2;
+        l.cp = static_cast<uint32_t>(min(8, ncol));
+        l.rec = static_cast<uint32_t>(record_bytes(static_cast<int>(l.cp)));
+        l.xtile = (resident ? static_cast<uint32_t>(nblk) : static_cast<uint32_t>(kTileBlocks)) * l.rec;
+        l.xlane = min(g4, l.cp - 1u) * 64u + l.t4 * 16u;  // lanes past the columns read the last one
+        l.m0 = l.cp * 128u + min(2u * l.t4, l.cp - 1u) * 8u;
+        l.m1 = l.cp * 128u + min(2u * l.t4 + 1u, l.cp - 1u) * 8u;
+      }
+      const uint32_t xbuf = resident ? static_cast<uint32_t>(gi % a.xbuffers) : 0u;
+      if (resident && (it == 0 || tile == 0))
+        ok = ok && mbar_wait_or_abort(xfull0 + 8u * xbuf, static_cast<uint32_t>((gi / a.xbuffers) & 1), abort_flag, a.err);
       // what the tail needs of this warp's columns 8n + wk, on its way during the K loop
       float factor[NT];
       int sl[NT];
@@ -632,8 +674,8 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
         sl[n] = 0;
         if (8 * n + wk < ncol) {
           if constexpr (MODE != TILE_DOWN) {
-            factor[n] = *reinterpret_cast<const float*>(a.records + static_cast<int64_t>(g.w + n) * nblk * rec +
-                                                        l.cp * 128u + static_cast<uint32_t>(wk) * 8u);
+            factor[n] = *reinterpret_cast<const float*>(a.records + (g.w + n) * tile_stride + l.cp * 128u +
+                                                        static_cast<uint32_t>(wk) * 8u);
           } else {
             sl[n] = a.slots[g.y + 8 * n + wk];
             factor[n] = a.factors[sl[n]];
@@ -655,7 +697,9 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
           ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(full0 + 8u * slot, phase, abort_flag, a.err));
           const uint32_t st = ring + static_cast<uint32_t>(slot) * stage_bytes;
           if (ok && kc * kTileBlocks + wk < nblk) {
-            const uint32_t xs = st + xoff + static_cast<uint32_t>(wk) * rec, blk = static_cast<uint32_t>(wk);
+            const uint32_t blk = static_cast<uint32_t>(wk);
+            const uint32_t xs = resident ? xres + xbuf * xbytes + (static_cast<uint32_t>(kc * kTileBlocks) + blk) * l.rec
+                                         : st + xoff + blk * l.rec;
             // codes behind a two-byte scale start on a word in every other block (in rows that
             // themselves do)
             if (PER1 && (WT == WT_Q4_0 || WT == WT_Q8_0) && (wk & 1))
@@ -674,6 +718,10 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
       if (NT >= 3 && ncol > 16) walk(TileConst<NT >= 3 ? 3 : 1>());
       else if (NT >= 2 && ncol > 8) walk(TileConst<NT >= 2 ? 2 : 1>());
       else walk(TileConst<1>());
+      if (resident && (tile + 1 == tiles || it + 1 == n_items)) {  // done with the group's records
+        __syncwarp();
+        if (lane == 0) mbar_arrive(xempty0 + 8u * xbuf);
+      }
       // the warps' sums through shared memory, eight columns at a time: red[warp][column][row];
       // then warp wk takes column 8n + wk
 #pragma unroll
@@ -706,7 +754,8 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             const HiLo p = split_hi_lo(lane < 16 ? hs : hs * pack_high(a.out_format));
-            uint8_t* r = a.out_records + (static_cast<int64_t>(g.w + n) * (a.rows / 32) + row0 / 32) * rec;
+            uint8_t* r = a.out_records + static_cast<int64_t>(g.w + n) * (a.rows / 32) * record_bytes(a.cp) +
+                         static_cast<int64_t>(row0 / 32) * l.rec;
             const int order = pack_order(a.out_format);
             const uint32_t i = static_cast<uint32_t>(lane) & 3u;
             const uint32_t at = record_offset(static_cast<uint32_t>(lane) >> 2, static_cast<uint32_t>(wk), l.cp, order) +
