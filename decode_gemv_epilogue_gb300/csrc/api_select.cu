@@ -6,7 +6,7 @@
 #include <cstring>
 
 #include "gemvfuse.h"
-#include "tile_mma.cuh"
+#include "tile_host.cuh"
 
 namespace gf {
 
@@ -106,9 +106,15 @@ static bool experts_tiled(const gf_experts* x) {
 
 // Columns of a group: matrix tiles are eight columns wide, and a group of more than an
 // expert's tokens costs registers and shared memory for nothing.
-static int experts_cols(int64_t E, int64_t T, int64_t k) {
-  const double mean = static_cast<double>(T) * k / std::min<double>(E, static_cast<double>(T) * k);
-  return static_cast<int>(std::min<int64_t>(T, 8)) < 8 ? static_cast<int>(T) : mean <= 5.0 ? 8 : mean <= 10.0 ? 16 : 24;
+static int experts_cols(const gf_experts* x, int64_t T) {
+  if (T < 8) return static_cast<int>(T);
+  const double slots = static_cast<double>(T) * x->top_k;
+  const double mean = slots / std::min<double>(static_cast<double>(x->E), slots);
+  if (mean <= 5.0) return 8;
+  if (mean <= 10.0) return 16;
+  const bool wide = wide_takes(x->wtype, static_cast<int>(row_bytes_of(x->wtype, x->K))) &&
+                    wide_takes(x->wtype_down, static_cast<int>(row_bytes_of(x->wtype_down, x->M)));
+  return mean <= 18.0 || !wide ? 24 : 32;
 }
 
 constexpr int kExpMaxRecs = 4;
@@ -166,7 +172,7 @@ static int plan_experts(const gf_experts* ex, const float* x, int64_t T, const f
   a.cp = static_cast<int>(std::min<int64_t>(8, T));
   a.max_tiles = static_cast<int>(l.max_tiles);
   a.y = reinterpret_cast<float*>(ws + l.y);
-  a.cols = experts_cols(ex->E, T, ex->top_k);
+  a.cols = experts_cols(ex, T);
   a.out_format = wd;
   a.sm_count = lim.sm_count;
   a.smem_optin = lim.smem_optin;

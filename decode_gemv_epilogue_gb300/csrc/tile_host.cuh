@@ -3,7 +3,7 @@
 
 #include <algorithm>
 
-#include "tile_mma.cuh"
+#include "tile_wide.cuh"
 
 namespace gf {
 
@@ -47,7 +47,7 @@ int launch_tile(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
   if (MODE == TILE_GLU) e = tile_map<WT>(o.W2, o.all_rows, t.row_bytes, &m1);
   if (e != cudaSuccess) return e;
   // The columns' records of whole groups where they leave three stages of weights, in two
-  // buffers where those leave four, with as many CTAs per SM as the registers allow or one;
+  // buffers where those leave four, with as many CTAs per SM as the registers allow;
   // else the records go with the weights.  1 KB a CTA is the system's.
   const int fixed = kTileHeadBytes + kTileRedBytes + 1024;
   const int64_t xb = tile_x_bytes(t.K, NT, t.cp);
@@ -64,7 +64,7 @@ int launch_tile(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
     return ns >= want;
   };
   const int most = tile_ctas(NT);
-  if (!plan(most, 2, 4) && !plan(most, 1, 3) && !plan(1, 2, 4) && !plan(1, 1, 3) && !plan(most, 0, 3)) plan(1, 0, 2);
+  if (!plan(most, 2, 4) && !plan(most, 1, 3) && !plan(most, 0, 3) && !plan(1, 1, 3)) plan(1, 0, 2);
   if (ns < 2 || o.max_groups / (ctas * o.sm_count) + 2 > kTileMaxGroups) return cudaErrorInvalidConfiguration;
   t.NS = ns;
   const int smem = fixed + static_cast<int>(x_all) + ns * stage;
@@ -78,6 +78,36 @@ int launch_tile(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
   }
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(ctas * o.sm_count)), kTileThreads, st, pdl, &attr);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  return cudaLaunchKernelEx(&cfg, kern, m0, m1, t);
+}
+
+// Block formats whose rows are whole 16-byte words: groups of more than 16 columns.
+inline bool wide_takes(int wt, int row_bytes) { return wt != WT_F32 && wt != WT_F16 && row_bytes % 16 == 0; }
+
+template <int WT, int MODE, int NT>
+int launch_wide(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
+  auto kern = wide_kernel<WT, MODE, NT>;
+  CUtensorMap m0, m1;
+  int e = tile_map<WT>(o.W, o.all_rows, t.row_bytes, &m0);
+  if (e != cudaSuccess) return e;
+  m1 = m0;
+  if (MODE == TILE_GLU) e = tile_map<WT>(o.W2, o.all_rows, t.row_bytes, &m1);
+  if (e != cudaSuccess) return e;
+  const int stage = wide_stage_bytes<WT>(NT), fixed = kTileHeadBytes + kWideXchg + 1024;
+  t.NS = std::min(kTileMaxStages, (o.smem_optin - fixed) / stage);
+  if (t.NS < 2 || o.max_groups / o.sm_count + 2 > kTileMaxGroups) return cudaErrorInvalidConfiguration;
+  const int smem = fixed + t.NS * stage;
+  static int configured[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && configured[dev] < smem) {
+    const cudaError_t c = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (c != cudaSuccess) return c;
+    configured[dev] = smem;
+  }
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(o.sm_count)), kTileThreads, st, pdl, &attr);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   return cudaLaunchKernelEx(&cfg, kern, m0, m1, t);
 }

@@ -16,12 +16,12 @@ __global__ void __launch_bounds__(kPackThreads) tile_pack_kernel(const __grid_co
             a.records + static_cast<int64_t>(blockIdx.x) * (a.K / 32) * record_bytes(a.cp), wmax);
 }
 
-template <int WT, bool PER1>
+template <int WT>
 static int launch_lin_cols(const TileArgs& t, const LinArgs& a, cudaStream_t st, bool pdl) {
   const TileOperands o = {a.W, nullptr, a.M, (a.ncols + a.cols - 1) / a.cols, a.sm_count, a.smem_optin};
-  if (a.cols <= 8) return launch_tile<WT, TILE_LIN, 1, PER1>(t, o, st, pdl);
-  if (a.cols <= 16) return launch_tile<WT, TILE_LIN, 2, PER1>(t, o, st, pdl);
-  return launch_tile<WT, TILE_LIN, 3, PER1>(t, o, st, pdl);
+  if (a.cols <= 8) return launch_tile<WT, TILE_LIN, 1, true>(t, o, st, pdl);
+  if (a.cols <= 16) return launch_tile<WT, TILE_LIN, 2, true>(t, o, st, pdl);
+  return a.cols <= 24 ? launch_wide<WT, TILE_LIN, 3>(t, o, st, pdl) : launch_wide<WT, TILE_LIN, 4>(t, o, st, pdl);
 }
 
 int launch_lin(const LinArgs& a, cudaStream_t st, bool pdl) {
@@ -44,9 +44,9 @@ int launch_lin(const LinArgs& a, cudaStream_t st, bool pdl) {
   t.ncols = a.ncols;
   t.group_cols = a.cols;
   switch (a.wtype) {
-    case WT_Q8_0: return launch_lin_cols<WT_Q8_0, true>(t, a, st, pdl);
-    case WT_Q4_0: return launch_lin_cols<WT_Q4_0, true>(t, a, st, pdl);
-    case WT_Q4_K: return launch_lin_cols<WT_Q4_K, true>(t, a, st, pdl);
+    case WT_Q8_0: return launch_lin_cols<WT_Q8_0>(t, a, st, pdl);
+    case WT_Q4_0: return launch_lin_cols<WT_Q4_0>(t, a, st, pdl);
+    case WT_Q4_K: return launch_lin_cols<WT_Q4_K>(t, a, st, pdl);
     default: return cudaErrorInvalidValue;
   }
 }

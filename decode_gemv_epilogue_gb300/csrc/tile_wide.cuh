@@ -1,0 +1,399 @@
+// The tiled product for wide column groups (more than 16 columns, block formats): the same
+// operands, stages and records as tile_mma.cuh, cut the other way.
+//
+// With two or more column tiles a matrix tile's instructions outweigh its decode, and what
+// the K-sharing kernel pays per chunk and item (records as large as the weights beside them,
+// a wait per block, the sums of eight warps through shared memory) is no longer hidden: it
+// reached a quarter of the matrix unit's rate.  Here a CTA takes 256 rows (gated: 128 gate
+// rows and the same up rows), and each of its eight consumer warps 32 of them for all of K: a
+// chunk's records serve four times the rows, a warp runs eight blocks between two waits, and
+// nothing is added across warps.  Gated, a warp has 16 gate rows and their up rows, so that
+// the gated value forms in the thread that holds both sums; two warps make one packed block
+// of 32 and exchange its largest value and its sum.
+#pragma once
+
+#include "tile_mma.cuh"
+
+namespace gf {
+
+constexpr int kWideRows = 256;
+constexpr int kWideMaxNT = 4;
+constexpr int kWideXchg = 2 * kTileWarps * 8 * kWideMaxNT * 8;  // [item parity][warp][column] {largest, sum}
+
+template <int WT>
+__host__ __device__ constexpr int wide_weight_bytes() { return 8 * tile_part<WT>(1); }
+template <int WT>
+__host__ __device__ constexpr int wide_stage_bytes(int nt) {
+  return (wide_weight_bytes<WT>() + 16 + nt * kTileBlocks * record_bytes(8) + 1023) / 1024 * 1024;
+}
+
+// A warp's walk over one pair of blocks (2 b, 2 b + 1) of a chunk: its 32 rows, NTA column tiles.
+// rows: stage addresses of (m, h): rows g + 8 h of matrix tile m.
+template <int WT, int MODE, int NTA, int NT>
+__device__ __forceinline__ void wide_pair(const TileLane& l, const uint32_t (&rows)[2][2], uint32_t xs, uint32_t pair,
+                                          bool second, float (&acc)[2][NT][4]) {
+  const uint32_t t4 = l.t4;
+  constexpr uint32_t kBlock = WT == WT_Q8_0 ? 34u : WT == WT_Q4_0 ? 18u : 0u;
+  // the code words: of one block at a time, except Q4_K, whose two blocks are the low and the
+  // high nibbles of the same words
+  uint32_t kw[2][2], kv[2][2];
+  float qd[2], qm[2];  // Q4_K: scale and min of the two blocks, of the row (t4 / 2, t4 % 2)
+  if constexpr (WT == WT_Q4_K) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        kw[m][h] = lds32(rows[m][h] + 16u + pair * 32u + 4u * t4);
+        kv[m][h] = lds32(rows[m][h] + 32u + pair * 32u + 4u * t4);
+      }
+    const uint32_t mine = (t4 & 2u) ? ((t4 & 1u) ? rows[1][1] : rows[1][0]) : ((t4 & 1u) ? rows[0][1] : rows[0][0]);
+    const uint4 hd = lds128(mine);
+    q4k_scale_of(hd, 2u * pair, qd[0], qm[0]);
+    q4k_scale_of(hd, 2u * pair + 1u, qd[1], qm[1]);
+    qd[1] *= 0.0625f;  // high nibbles are masked in place
+  }
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    if (o == 1 && !second) break;
+    uint4 b[NTA][2];
+    float4 meta[NTA];  // {2^-s, sum} of columns 2t and 2t + 1
+    const uint32_t xo = xs + (2u * pair + o) * l.rec;
+#pragma unroll
+    for (int n = 0; n < NTA; ++n) {
+      const uint32_t xa = xo + static_cast<uint32_t>(n) * l.xtile;
+      b[n][0] = lds128(xa + l.xlane);
+      b[n][1] = lds128(xa + l.xlane + l.cp * 64u);
+      const uint2 u = lds64(xa + l.m0), v = lds64(xa + l.m1);
+      meta[n] = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(v.x), __uint_as_float(v.y));
+    }
+    uint32_t a0[2][2][2], a1[2][2][2];
+    float d[2][2], dm[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        dm[m][h] = 0.0f;
+        if constexpr (WT == WT_Q4_K) {
+          const uint32_t mask = o ? 0x00F000F0u : 0x000F000Fu;
+          a0[m][h][0] = kw[m][h] & mask;
+          a0[m][h][1] = (kw[m][h] >> 8) & mask;
+          a1[m][h][0] = kv[m][h] & mask;
+          a1[m][h][1] = (kv[m][h] >> 8) & mask;
+          d[m][h] = __shfl_sync(0xffffffffu, qd[o], 2 * m + h, 4);
+          dm[m][h] = __shfl_sync(0xffffffffu, qm[o], 2 * m + h, 4);
+        } else {
+          // even blocks start on a word, their codes two bytes later; odd ones the other way
+          RowPlace p;
+          p.scale = rows[m][h] + 2u * kBlock * pair + o * kBlock;
+          p.code = p.scale + (o ? 2u : 0u) + 4u * t4;
+          p.shift = 16u;
+          p.mask = 0u;
+          if (o)
+            load_block_row<WT, true>(p, 0u, a0[m][h], a1[m][h], d[m][h]);
+          else
+            load_block_row<WT, false>(p, 0u, a0[m][h], a1[m][h], d[m][h]);
+        }
+      }
+    constexpr bool kOffset = WT == WT_Q4_0 || WT == WT_Q8_0;
+    float s[2][NTA][4];
+    auto step = [&](int i) {  // hi of both k-steps, then lo of both
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < NTA; ++n) {
+          const uint32_t (&x)[2][2] = (i & 1) ? a1[m] : a0[m];
+          const uint4 v = b[n][i & 1];
+          const uint32_t p = i < 2 ? v.x : v.z, q = i < 2 ? v.y : v.w;
+          if (i == 0)
+            mma_f16_first(s[m][n], x[0][0], x[1][0], x[0][1], x[1][1], p, q, kOffset ? meta[n].y : 0.0f,
+                          kOffset ? meta[n].w : 0.0f);
+          else
+            mma_f16(s[m][n], x[0][0], x[1][0], x[0][1], x[1][1], p, q);
+        }
+    };
+    step(0);
+    step(1);
+    step(2);
+    step(3);
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < NTA; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // row g + 8 (i / 2), column 2t + i % 2
+          const int h = i >> 1;
+          const float sx = (i & 1) ? meta[n].z : meta[n].x, xsum = (i & 1) ? meta[n].w : meta[n].y;
+          float& r = acc[m][n][i];
+          if constexpr (MODE == TILE_DOWN) {
+            float v = d[m][h] * s[m][n][i];
+            if constexpr (WT == WT_Q4_K) v = fmaf(-dm[m][h], xsum, v);
+            r = fmaf(sx, v, r);
+          } else {
+            r = fmaf(d[m][h], s[m][n][i], r);
+            if constexpr (WT == WT_Q4_K) r = fmaf(-dm[m][h], xsum, r);
+          }
+        }
+  }
+}
+
+template <int WT, int MODE, int NT>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    wide_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
+                const __grid_constant__ TileArgs a) {
+  constexpr int kOutRows = MODE == TILE_GLU ? kWideRows / 2 : kWideRows;
+  constexpr uint32_t P = tile_pitch<WT>(1), kPart = tile_part<WT>(1), kRec = record_bytes(8);
+  constexpr uint32_t kStage = wide_stage_bytes<WT>(NT), kXoff = wide_weight_bytes<WT>() + 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sbase = smem_u32(smem), full0 = sbase, empty0 = sbase + 8u * kTileMaxStages;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 248);
+  int4* groups = reinterpret_cast<int4*>(smem + 256);
+  float2* xchg = reinterpret_cast<float2*>(smem + kTileHeadBytes);
+  const uint32_t ring = (sbase + kTileHeadBytes + kWideXchg + 1023u) & ~1023u;
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < a.NS; ++i) {
+      mbar_init(full0 + 8u * i, 1);
+      mbar_init(empty0 + 8u * i, kTileWarps);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&map0);
+    if (MODE == TILE_GLU) prefetch_tmap(&map1);
+  }
+  pdl_trigger();
+  pdl_wait();
+  const int tiles = (a.rows + kOutRows - 1) / kOutRows;
+  const int n_groups = MODE == TILE_LIN ? (a.ncols + a.group_cols - 1) / a.group_cols : *a.n_groups;
+  const int64_t items = static_cast<int64_t>(n_groups) * tiles;
+  const int64_t lo = items * blockIdx.x / gridDim.x, hi = items * (blockIdx.x + 1) / gridDim.x;
+  const int g_lo = static_cast<int>(lo / tiles);
+  if (lo < hi)
+    for (int i = threadIdx.x; i <= static_cast<int>((hi - 1) / tiles) - g_lo; i += kTileThreads)
+      groups[i] = MODE == TILE_LIN ? make_int4(0, 0, min(a.group_cols, a.ncols - (g_lo + i) * a.group_cols),
+                                               (g_lo + i) * ((a.group_cols + 7) / 8))
+                                   : a.groups[g_lo + i];
+  __syncthreads();
+  const int n_kc = (a.K + kTileK - 1) / kTileK, nblk = a.K / 32;
+  const int n_items = static_cast<int>(hi - lo);
+  const int tile_lo = static_cast<int>(lo - static_cast<int64_t>(g_lo) * tiles);
+  const int64_t tile_stride = static_cast<int64_t>(nblk) * kRec;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int slot = 0, issued = 0, gi = 0, tile = tile_lo;
+      uint32_t phase = 1u;
+      bool ok = true;
+      for (int it = 0; it < n_items && ok; ++it) {
+        const int4 g = groups[gi];
+        const int row0 = tile * kOutRows;
+        const int boxes = min(kOutRows / 32, (a.rows - row0 + 31) / 32);  // of each matrix
+        const int nt = (g.z + 7) / 8;
+        const uint32_t rec = static_cast<uint32_t>(record_bytes(min(8, g.z)));
+        const uint8_t* xsrc = a.records + g.w * tile_stride;
+        for (int kc = 0; kc < n_kc; ++kc) {
+          if (issued >= a.NS && !mbar_wait_or_abort(empty0 + 8u * slot, phase, abort_flag, a.err)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = ring + static_cast<uint32_t>(slot) * kStage, full = full0 + 8u * slot;
+          const uint32_t xlen = static_cast<uint32_t>(min(kTileBlocks, nblk - kc * kTileBlocks)) * rec;
+          mbar_arrive_expect_tx(full, (MODE == TILE_GLU ? 2u : 1u) * boxes * 32u * P + nt * xlen);
+          for (int i = 0; i < boxes; ++i) {
+            tma_load_2d(st + i * kPart, &map0, kc * (tile_seg<WT>() / 2), g.x * a.rows + row0 + 32 * i, full);
+            if constexpr (MODE == TILE_GLU)
+              tma_load_2d(st + (4u + i) * kPart, &map1, kc * (tile_seg<WT>() / 2), g.x * a.rows + row0 + 32 * i, full);
+          }
+          for (int n = 0; n < nt; ++n)
+            bulk_g2s(st + kXoff + static_cast<uint32_t>(n) * kTileBlocks * rec,
+                     xsrc + n * tile_stride + static_cast<uint32_t>(kc * kTileBlocks) * rec, xlen, full);
+          ++issued;
+          if (++slot == a.NS) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+        if (++tile == tiles) {
+          tile = 0;
+          ++gi;
+        }
+      }
+      // Drain after an abort: every copy this thread issued lands before the CTA leaves.
+      if (!ok)
+        for (int i = max(0, issued - a.NS); i < issued; ++i)
+          (void)mbar_wait(full0 + 8u * (i % a.NS), static_cast<uint32_t>((i / a.NS) & 1));
+    }
+  } else {
+    // ------------------------------------------------------------ consumers
+    const int w = warp - 1;
+    const uint32_t g4 = static_cast<uint32_t>(lane) >> 2, t4 = static_cast<uint32_t>(lane) & 3u;
+    uint32_t place[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        place[m][h] = MODE == TILE_GLU ? (4u * m + static_cast<uint32_t>(w >> 1)) * kPart + (16u * (w & 1) + 8u * h + g4) * P
+                                       : static_cast<uint32_t>(w) * kPart + (16u * m + 8u * h + g4) * P;
+    TileLane l = {};
+    l.t4 = t4;
+    int slot = 0, gi = 0, tile = tile_lo;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int it = 0; it < n_items; ++it) {
+      const int4 g = groups[gi];
+      const int row0 = tile * kOutRows;
+      const int ncol = g.z;
+      l.cp = static_cast<uint32_t>(min(8, ncol));
+      l.rec = static_cast<uint32_t>(record_bytes(static_cast<int>(l.cp)));
+      l.xtile = kTileBlocks * l.rec;
+      l.xlane = min(g4, l.cp - 1u) * 64u + t4 * 16u;  // lanes past the columns read the last one
+      l.m0 = l.cp * 128u + min(2u * t4, l.cp - 1u) * 8u;
+      l.m1 = l.cp * 128u + min(2u * t4 + 1u, l.cp - 1u) * 8u;
+      const uint32_t cp = l.cp, rec = l.rec;
+      const bool mine = MODE != TILE_GLU || row0 + 16 * w < a.rows;
+      // the tail's factors of columns 8n + 2t + c, on their way during the K loop
+      float factor[NT][2];
+      int sl[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col = 8 * n + 2 * static_cast<int>(t4) + c;
+          factor[n][c] = 0.0f;
+          sl[n][c] = 0;
+          if (col < ncol) {
+            if constexpr (MODE != TILE_DOWN) {
+              factor[n][c] = *reinterpret_cast<const float*>(a.records + (g.w + n) * tile_stride + cp * 128u +
+                                                             (2u * t4 + c) * 8u);
+            } else {
+              sl[n][c] = a.slots[g.y + col];
+              factor[n][c] = a.factors[sl[n][c]];
+            }
+          }
+        }
+      float acc[2][NT][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+      auto walk = [&](auto nta) {
+        constexpr int NTA = decltype(nta)::value;
+#pragma unroll 1
+        for (int kc = 0; kc < n_kc; ++kc) {
+          ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(full0 + 8u * slot, phase, abort_flag, a.err));
+          const uint32_t st = ring + static_cast<uint32_t>(slot) * kStage;
+          const uint32_t nb = static_cast<uint32_t>(min(kTileBlocks, nblk - kc * kTileBlocks));
+          if (ok && mine) {
+            uint32_t rows[2][2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) rows[m][h] = st + place[m][h];
+#pragma unroll 1
+            for (uint32_t p = 0; 2u * p < nb; ++p)
+              wide_pair<WT, MODE, NTA, NT>(l, rows, st + kXoff, p, 2u * p + 1u < nb, acc);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty0 + 8u * slot);
+          if (++slot == a.NS) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      };
+      if (NT >= 4 && ncol > 24) walk(TileConst<NT >= 4 ? 4 : 1>());
+      else if (NT >= 3 && ncol > 16) walk(TileConst<NT >= 3 ? 3 : 1>());
+      else if (NT >= 2 && ncol > 8) walk(TileConst<NT >= 2 ? 2 : 1>());
+      else walk(TileConst<1>());
+      if constexpr (MODE == TILE_GLU) {
+        // the gated values of rows 8h + g (of the warp's 16) and columns 2t + c, in place of the
+        // gate sums
+        float2* mx = xchg + (it & 1) * (kTileWarps * 8 * kWideMaxNT);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float top = 0.0f, sum = 0.0f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int i = 2 * h + c;
+              const float f = tile_unit(WT) * factor[n][c];
+              const float v = tail_silu(acc[0][n][i] * f) * (acc[1][n][i] * f);
+              acc[0][n][i] = v;
+              top = fmaxf(top, finite_abs(v));
+              sum += v;
+            }
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) {
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            }
+            if (g4 == 0) mx[w * 8 * kWideMaxNT + 8 * n + 2 * t4 + c] = make_float2(top, sum);
+          }
+        named_bar_sync(1u + static_cast<uint32_t>(w >> 1), 64u);
+        const int r0 = row0 + 32 * (w >> 1);
+        if (r0 < a.rows && ok && !*abort_flag) {
+          const int order = pack_order(a.out_format);
+          const float high = pack_high(a.out_format);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            uint8_t* r = a.out_records + static_cast<int64_t>(g.w + n) * (a.rows / 32) * kRec +
+                         static_cast<int64_t>(r0 / 32) * rec;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t col = 2u * t4 + c;
+              if (8 * n + static_cast<int>(col) >= ncol) continue;
+              // in the order of the rows, whichever warp looks
+              const float2 u = mx[(w & ~1) * 8 * kWideMaxNT + 8 * n + col], v = mx[(w | 1) * 8 * kWideMaxNT + 8 * n + col];
+              const float sc = pack_scale(fmaxf(u.x, v.x));
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t rr = 16u * (w & 1) + 8u * h + g4, i = rr & 3u;
+                const float hs = acc[0][n][2 * h + c] * sc;
+                const HiLo p = split_hi_lo((w & 1) ? hs * high : hs);
+                uint8_t* q = r + record_offset(rr >> 2, col, cp, order) +
+                             2u * (order == ORDER_NIBBLE ? ((i & 1u) << 1) | (i >> 1) : i);
+                *reinterpret_cast<__half*>(q) = p.hi;
+                *reinterpret_cast<__half*>(q + 8) = p.lo;
+              }
+              if (g4 == 0 && !(w & 1))
+                *reinterpret_cast<float2*>(r + cp * 128u + col * 8u) =
+                    make_float2(pow2_inverse(sc), (u.y + v.y) * sc * pack_sum(a.out_format));
+            }
+          }
+        }
+      } else if (ok && !*abort_flag) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int col = 8 * n + 2 * static_cast<int>(t4) + c;
+            if (col >= ncol) continue;
+            const int64_t base = (MODE == TILE_LIN ? static_cast<int64_t>(g.w) * 8 + col : sl[n][c]) * a.rows;
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int r = row0 + 32 * w + 16 * m + 8 * h + static_cast<int>(g4);
+                if (r < a.rows) {
+                  const float y = factor[n][c] * (acc[m][n][2 * h + c] * tile_unit(WT));
+                  if constexpr (MODE == TILE_LIN)
+                    a.out[base + r] = apply_tail(a.epi, y, epi_takes_aux(a.epi) ? a.aux[base + r] : 0.0f);
+                  else
+                    a.out[base + r] = y;
+                }
+              }
+          }
+      }
+      if (++tile == tiles) {
+        tile = 0;
+        ++gi;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+}  // namespace gf
