@@ -1027,7 +1027,7 @@ static int plan_lora(const void* W, int wtype, const float* x, int64_t M, int64_
     q.M = static_cast<int>(M);
     q.K = static_cast<int>(K);
     q.ncols = static_cast<int>(c.ncols);
-    q.cols = c.ncols <= 8 ? static_cast<int>(c.ncols) : c.ncols <= 16 ? 16 : c.ncols <= 24 ? 24 : 32;
+    q.cols = c.ncols <= 8 ? static_cast<int>(c.ncols) : 16;
     q.cp = static_cast<int>(std::min<int64_t>(8, c.ncols));
     q.sm_count = lim.sm_count;
     q.smem_optin = lim.smem_optin;

@@ -111,10 +111,10 @@ static int experts_cols(const gf_experts* x, int64_t T) {
   const double slots = static_cast<double>(T) * x->top_k;
   const double mean = slots / std::min<double>(static_cast<double>(x->E), slots);
   if (mean <= 5.0) return 8;
-  if (mean <= 10.0) return 16;
-  const bool wide = wide_takes(x->wtype, static_cast<int>(row_bytes_of(x->wtype, x->K))) &&
+  // more than 16 only in the K-sharing kernel
+  const bool wide = wide_takes(x->wtype, static_cast<int>(row_bytes_of(x->wtype, x->K))) ||
                     wide_takes(x->wtype_down, static_cast<int>(row_bytes_of(x->wtype_down, x->M)));
-  return mean <= 18.0 || !wide ? 24 : 32;
+  return mean <= 10.0 || wide ? 16 : 24;
 }
 
 constexpr int kExpMaxRecs = 4;

@@ -82,19 +82,19 @@ int launch_tile(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
   return cudaLaunchKernelEx(&cfg, kern, m0, m1, t);
 }
 
-// Block formats whose rows are whole 16-byte words: groups of more than 16 columns.
+// Block formats whose rows are whole 16-byte words: groups of 9 to 16 columns.
 inline bool wide_takes(int wt, int row_bytes) { return wt != WT_F32 && wt != WT_F16 && row_bytes % 16 == 0; }
 
-template <int WT, int MODE, int NT>
+template <int WT, int MODE>
 int launch_wide(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
-  auto kern = wide_kernel<WT, MODE, NT>;
+  auto kern = wide_kernel<WT, MODE>;
   CUtensorMap m0, m1;
   int e = tile_map<WT>(o.W, o.all_rows, t.row_bytes, &m0);
   if (e != cudaSuccess) return e;
   m1 = m0;
   if (MODE == TILE_GLU) e = tile_map<WT>(o.W2, o.all_rows, t.row_bytes, &m1);
   if (e != cudaSuccess) return e;
-  const int stage = wide_stage_bytes<WT>(NT), fixed = kTileHeadBytes + kWideXchg + 1024;
+  const int stage = wide_stage_bytes<WT>(), fixed = kTileHeadBytes + wide_xchg<WT>() + 1024;
   t.NS = std::min(kTileMaxStages, (o.smem_optin - fixed) / stage);
   if (t.NS < 2 || o.max_groups / o.sm_count + 2 > kTileMaxGroups) return cudaErrorInvalidConfiguration;
   const int smem = fixed + t.NS * stage;
@@ -107,7 +107,7 @@ int launch_wide(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
     configured[dev] = smem;
   }
   cudaLaunchAttribute attr;
-  cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(o.sm_count)), kTileThreads, st, pdl, &attr);
+  cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(o.sm_count)), 32 * (1 + wide_warps<WT>()), st, pdl, &attr);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   return cudaLaunchKernelEx(&cfg, kern, m0, m1, t);
 }

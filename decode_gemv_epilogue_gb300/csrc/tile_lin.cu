@@ -20,8 +20,8 @@ template <int WT>
 static int launch_lin_cols(const TileArgs& t, const LinArgs& a, cudaStream_t st, bool pdl) {
   const TileOperands o = {a.W, nullptr, a.M, (a.ncols + a.cols - 1) / a.cols, a.sm_count, a.smem_optin};
   if (a.cols <= 8) return launch_tile<WT, TILE_LIN, 1, true>(t, o, st, pdl);
-  if (a.cols <= 16) return launch_tile<WT, TILE_LIN, 2, true>(t, o, st, pdl);
-  return a.cols <= 24 ? launch_wide<WT, TILE_LIN, 3>(t, o, st, pdl) : launch_wide<WT, TILE_LIN, 4>(t, o, st, pdl);
+
+  return launch_wide<WT, TILE_LIN>(t, o, st, pdl);
 }
 
 int launch_lin(const LinArgs& a, cudaStream_t st, bool pdl) {

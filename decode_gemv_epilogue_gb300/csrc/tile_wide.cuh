@@ -1,37 +1,48 @@
-// The tiled product for wide column groups (more than 16 columns, block formats): the same
-// operands, stages and records as tile_mma.cuh, cut the other way.
+// The tiled product for wide column groups (up to 16 columns, block formats in rows of whole
+// 16-byte words): the same operands, stages and records as tile_mma.cuh, cut the other way.
 //
-// With two or more column tiles a matrix tile's instructions outweigh its decode, and what
-// the K-sharing kernel pays per chunk and item (records as large as the weights beside them,
-// a wait per block, the sums of eight warps through shared memory) is no longer hidden: it
-// reached a quarter of the matrix unit's rate.  Here a CTA takes 256 rows (gated: 128 gate
-// rows and the same up rows), and each of its eight consumer warps 32 of them for all of K: a
-// chunk's records serve four times the rows, a warp runs eight blocks between two waits, and
-// nothing is added across warps.  Gated, a warp has 16 gate rows and their up rows, so that
-// the gated value forms in the thread that holds both sums; two warps make one packed block
-// of 32 and exchange its largest value and its sum.
+// With two column tiles the matrix instructions outweigh the decode, and what the K-sharing
+// kernel pays per chunk and item (records as large as the weights beside them, a wait per
+// block, the sums of eight warps through shared memory) is no longer hidden: it reached a
+// quarter of the matrix unit's rate.  Here each of a CTA's consumer warps takes 32 rows for
+// all of K (gated: 16 gate rows and their up rows): a chunk's records serve all the warps'
+// rows, a warp runs eight blocks between two waits, and nothing is added across warps.
+// Gated, the gated value forms in the thread that holds both sums; two warps make one packed
+// block of 32 and exchange its largest value and its sum.
+//
+// Sixteen warps, four a scheduler (eight for Q8_0, whose rows leave no room for two stages of
+// sixteen warps' rows).  Measured on 256 tokens, 128 experts, 8 choices, 768 x 2048 Q4_K,
+// gate and up: eight warps with three column tiles 166 us, twelve (spilling) 178, sixteen
+// with two 153; 64 columns of 14336 x 4096 Q4_0: 77, 101, 67.
 #pragma once
 
 #include "tile_mma.cuh"
 
 namespace gf {
 
-constexpr int kWideRows = 256;
-constexpr int kWideMaxNT = 4;
-constexpr int kWideXchg = 2 * kTileWarps * 8 * kWideMaxNT * 8;  // [item parity][warp][column] {largest, sum}
-
+constexpr int kWideNT = 2;  // column tiles
+// Consumer warps, 32 rows each.
 template <int WT>
-__host__ __device__ constexpr int wide_weight_bytes() { return 8 * tile_part<WT>(1); }
+__host__ __device__ constexpr int wide_warps() { return WT == WT_Q8_0 ? 8 : 16; }
 template <int WT>
-__host__ __device__ constexpr int wide_stage_bytes(int nt) {
-  return (wide_weight_bytes<WT>() + 16 + nt * kTileBlocks * record_bytes(8) + 1023) / 1024 * 1024;
+__host__ __device__ constexpr int wide_xchg() {  // [item parity][warp][column] {largest, sum}
+  return 2 * wide_warps<WT>() * 8 * kWideNT * 8;
+}
+template <int WT>
+__host__ __device__ constexpr int wide_weight_bytes() { return wide_warps<WT>() * tile_part<WT>(1); }
+template <int WT>
+__host__ __device__ constexpr int wide_stage_bytes() {
+  return (wide_weight_bytes<WT>() + 16 + kWideNT * kTileBlocks * record_bytes(8) + 1023) / 1024 * 1024;
 }
 
 // A warp's walk over one pair of blocks (2 b, 2 b + 1) of a chunk: its 32 rows, NTA column tiles.
-// rows: stage addresses of (m, h): rows g + 8 h of matrix tile m.
-template <int WT, int MODE, int NTA, int NT>
-__device__ __forceinline__ void wide_pair(const TileLane& l, const uint32_t (&rows)[2][2], uint32_t xs, uint32_t pair,
-                                          bool second, float (&acc)[2][NT][4]) {
+// row: stage address of row g of matrix tile 0; rows 8 further and matrix tile 1 lie constant
+// distances on.
+template <int WT, int MODE, int NTA>
+__device__ __forceinline__ void wide_pair(const TileLane& l, uint32_t row, uint32_t xs, uint32_t pair,
+                                          float (&acc)[2][kWideNT][4]) {
+  constexpr uint32_t kP = tile_pitch<WT>(1);
+  constexpr uint32_t kM = MODE == TILE_GLU ? wide_warps<WT>() / 2 * tile_part<WT>(1) : 16u * kP;  // matrix tiles apart
   const uint32_t t4 = l.t4;
   constexpr uint32_t kBlock = WT == WT_Q8_0 ? 34u : WT == WT_Q4_0 ? 18u : 0u;
   // the code words: of one block at a time, except Q4_K, whose two blocks are the low and the
@@ -43,29 +54,17 @@ __device__ __forceinline__ void wide_pair(const TileLane& l, const uint32_t (&ro
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        kw[m][h] = lds32(rows[m][h] + 16u + pair * 32u + 4u * t4);
-        kv[m][h] = lds32(rows[m][h] + 32u + pair * 32u + 4u * t4);
+        kw[m][h] = lds32(row + m * kM + h * 8u * kP + 16u + pair * 32u + 4u * t4);
+        kv[m][h] = lds32(row + m * kM + h * 8u * kP + 32u + pair * 32u + 4u * t4);
       }
-    const uint32_t mine = (t4 & 2u) ? ((t4 & 1u) ? rows[1][1] : rows[1][0]) : ((t4 & 1u) ? rows[0][1] : rows[0][0]);
-    const uint4 hd = lds128(mine);
+    const uint4 hd = lds128(row + (t4 >> 1) * kM + (t4 & 1u) * (8u * kP));
     q4k_scale_of(hd, 2u * pair, qd[0], qm[0]);
     q4k_scale_of(hd, 2u * pair + 1u, qd[1], qm[1]);
     qd[1] *= 0.0625f;  // high nibbles are masked in place
   }
 #pragma unroll
   for (int o = 0; o < 2; ++o) {
-    if (o == 1 && !second) break;
-    uint4 b[NTA][2];
-    float4 meta[NTA];  // {2^-s, sum} of columns 2t and 2t + 1
     const uint32_t xo = xs + (2u * pair + o) * l.rec;
-#pragma unroll
-    for (int n = 0; n < NTA; ++n) {
-      const uint32_t xa = xo + static_cast<uint32_t>(n) * l.xtile;
-      b[n][0] = lds128(xa + l.xlane);
-      b[n][1] = lds128(xa + l.xlane + l.cp * 64u);
-      const uint2 u = lds64(xa + l.m0), v = lds64(xa + l.m1);
-      meta[n] = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(v.x), __uint_as_float(v.y));
-    }
     uint32_t a0[2][2][2], a1[2][2][2];
     float d[2][2], dm[2][2];
 #pragma unroll
@@ -84,7 +83,7 @@ __device__ __forceinline__ void wide_pair(const TileLane& l, const uint32_t (&ro
         } else {
           // even blocks start on a word, their codes two bytes later; odd ones the other way
           RowPlace p;
-          p.scale = rows[m][h] + 2u * kBlock * pair + o * kBlock;
+          p.scale = row + m * kM + h * 8u * kP + 2u * kBlock * pair + o * kBlock;
           p.code = p.scale + (o ? 2u : 0u) + 4u * t4;
           p.shift = 16u;
           p.mask = 0u;
@@ -95,66 +94,70 @@ __device__ __forceinline__ void wide_pair(const TileLane& l, const uint32_t (&ro
         }
       }
     constexpr bool kOffset = WT == WT_Q4_0 || WT == WT_Q8_0;
-    float s[2][NTA][4];
-    auto step = [&](int i) {  // hi of both k-steps, then lo of both
+    // column tile by column tile: few registers, so that four warps a scheduler hide the latency
+#pragma unroll
+    for (int n = 0; n < NTA; ++n) {
+      const uint32_t xa = xo + static_cast<uint32_t>(n) * l.xtile;
+      const uint4 b0 = lds128(xa + l.xlane), b1 = lds128(xa + l.xlane + l.cp * 64u);
+      const uint2 u = lds64(xa + l.m0), v = lds64(xa + l.m1);  // {2^-s, sum} of columns 2t and 2t + 1
+      const float sx[2] = {__uint_as_float(u.x), __uint_as_float(v.x)}, xsum[2] = {__uint_as_float(u.y), __uint_as_float(v.y)};
+      float s[2][4];
+      auto step = [&](int i) {  // hi of both k-steps, then lo of both
+        const uint32_t p = i == 0 ? b0.x : i == 1 ? b1.x : i == 2 ? b0.z : b1.z;
+        const uint32_t q = i == 0 ? b0.y : i == 1 ? b1.y : i == 2 ? b0.w : b1.w;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const uint32_t (&x)[2][2] = (i & 1) ? a1[m] : a0[m];
+          if (i == 0)
+            mma_f16_first(s[m], x[0][0], x[1][0], x[0][1], x[1][1], p, q, kOffset ? xsum[0] : 0.0f, kOffset ? xsum[1] : 0.0f);
+          else
+            mma_f16(s[m], x[0][0], x[1][0], x[0][1], x[1][1], p, q);
+        }
+      };
+      step(0);
+      step(1);
+      step(2);
+      step(3);
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int n = 0; n < NTA; ++n) {
-          const uint32_t (&x)[2][2] = (i & 1) ? a1[m] : a0[m];
-          const uint4 v = b[n][i & 1];
-          const uint32_t p = i < 2 ? v.x : v.z, q = i < 2 ? v.y : v.w;
-          if (i == 0)
-            mma_f16_first(s[m][n], x[0][0], x[1][0], x[0][1], x[1][1], p, q, kOffset ? meta[n].y : 0.0f,
-                          kOffset ? meta[n].w : 0.0f);
-          else
-            mma_f16(s[m][n], x[0][0], x[1][0], x[0][1], x[1][1], p, q);
-        }
-    };
-    step(0);
-    step(1);
-    step(2);
-    step(3);
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int n = 0; n < NTA; ++n)
-#pragma unroll
         for (int i = 0; i < 4; ++i) {  // row g + 8 (i / 2), column 2t + i % 2
-          const int h = i >> 1;
-          const float sx = (i & 1) ? meta[n].z : meta[n].x, xsum = (i & 1) ? meta[n].w : meta[n].y;
+          const int h = i >> 1, c = i & 1;
           float& r = acc[m][n][i];
           if constexpr (MODE == TILE_DOWN) {
-            float v = d[m][h] * s[m][n][i];
-            if constexpr (WT == WT_Q4_K) v = fmaf(-dm[m][h], xsum, v);
-            r = fmaf(sx, v, r);
+            float y = d[m][h] * s[m][i];
+            if constexpr (WT == WT_Q4_K) y = fmaf(-dm[m][h], xsum[c], y);
+            r = fmaf(sx[c], y, r);
           } else {
-            r = fmaf(d[m][h], s[m][n][i], r);
-            if constexpr (WT == WT_Q4_K) r = fmaf(-dm[m][h], xsum, r);
+            r = fmaf(d[m][h], s[m][i], r);
+            if constexpr (WT == WT_Q4_K) r = fmaf(-dm[m][h], xsum[c], r);
           }
         }
+    }
   }
 }
 
-template <int WT, int MODE, int NT>
-__global__ void __launch_bounds__(kTileThreads, 1)
+template <int WT, int MODE>
+__global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
     wide_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
                 const __grid_constant__ TileArgs a) {
-  constexpr int kOutRows = MODE == TILE_GLU ? kWideRows / 2 : kWideRows;
+  constexpr int NT = kWideNT;
+  constexpr int kWarps = wide_warps<WT>(), kThreads = 32 * (1 + kWarps);
+  constexpr int kOutRows = MODE == TILE_GLU ? 16 * kWarps : 32 * kWarps;
   constexpr uint32_t P = tile_pitch<WT>(1), kPart = tile_part<WT>(1), kRec = record_bytes(8);
-  constexpr uint32_t kStage = wide_stage_bytes<WT>(NT), kXoff = wide_weight_bytes<WT>() + 16;
+  constexpr uint32_t kStage = wide_stage_bytes<WT>(), kXoff = wide_weight_bytes<WT>() + 16;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(smem), full0 = sbase, empty0 = sbase + 8u * kTileMaxStages;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 248);
   int4* groups = reinterpret_cast<int4*>(smem + 256);
   float2* xchg = reinterpret_cast<float2*>(smem + kTileHeadBytes);
-  const uint32_t ring = (sbase + kTileHeadBytes + kWideXchg + 1023u) & ~1023u;
+  const uint32_t ring = (sbase + kTileHeadBytes + wide_xchg<WT>() + 1023u) & ~1023u;
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < a.NS; ++i) {
       mbar_init(full0 + 8u * i, 1);
-      mbar_init(empty0 + 8u * i, kTileWarps);
+      mbar_init(empty0 + 8u * i, kWarps);
     }
     fence_mbar_init();
     prefetch_tmap(&map0);
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int64_t lo = items * blockIdx.x / gridDim.x, hi = items * (blockIdx.x + 1) / gridDim.x;
   const int g_lo = static_cast<int>(lo / tiles);
   if (lo < hi)
-    for (int i = threadIdx.x; i <= static_cast<int>((hi - 1) / tiles) - g_lo; i += kTileThreads)
+    for (int i = threadIdx.x; i <= static_cast<int>((hi - 1) / tiles) - g_lo; i += kThreads)
       groups[i] = MODE == TILE_LIN ? make_int4(0, 0, min(a.group_cols, a.ncols - (g_lo + i) * a.group_cols),
                                                (g_lo + i) * ((a.group_cols + 7) / 8))
                                    : a.groups[g_lo + i];
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int i = 0; i < boxes; ++i) {
             tma_load_2d(st + i * kPart, &map0, kc * (tile_seg<WT>() / 2), g.x * a.rows + row0 + 32 * i, full);
             if constexpr (MODE == TILE_GLU)
-              tma_load_2d(st + (4u + i) * kPart, &map1, kc * (tile_seg<WT>() / 2), g.x * a.rows + row0 + 32 * i, full);
+              tma_load_2d(st + (kWarps / 2 + i) * kPart, &map1, kc * (tile_seg<WT>() / 2), g.x * a.rows + row0 + 32 * i, full);
           }
           for (int n = 0; n < nt; ++n)
             bulk_g2s(st + kXoff + static_cast<uint32_t>(n) * kTileBlocks * rec,
@@ -227,13 +230,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ------------------------------------------------------------ consumers
     const int w = warp - 1;
     const uint32_t g4 = static_cast<uint32_t>(lane) >> 2, t4 = static_cast<uint32_t>(lane) & 3u;
-    uint32_t place[2][2];
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        place[m][h] = MODE == TILE_GLU ? (4u * m + static_cast<uint32_t>(w >> 1)) * kPart + (16u * (w & 1) + 8u * h + g4) * P
-                                       : static_cast<uint32_t>(w) * kPart + (16u * m + 8u * h + g4) * P;
+    const uint32_t place = MODE == TILE_GLU ? static_cast<uint32_t>(w >> 1) * kPart + (16u * (w & 1) + g4) * P
+                                            : static_cast<uint32_t>(w) * kPart + g4 * P;
     TileLane l = {};
     l.t4 = t4;
     int slot = 0, gi = 0, tile = tile_lo;
@@ -251,7 +249,35 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       l.m1 = l.cp * 128u + min(2u * t4 + 1u, l.cp - 1u) * 8u;
       const uint32_t cp = l.cp, rec = l.rec;
       const bool mine = MODE != TILE_GLU || row0 + 16 * w < a.rows;
-      // the tail's factors of columns 8n + 2t + c, on their way during the K loop
+      float acc[2][NT][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+      auto walk = [&](auto nta) {
+        constexpr int NTA = decltype(nta)::value;
+#pragma unroll 1
+        for (int kc = 0; kc < n_kc; ++kc) {
+          ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(full0 + 8u * slot, phase, abort_flag, a.err));
+          const uint32_t st = ring + static_cast<uint32_t>(slot) * kStage;
+          if (ok && mine) {
+            // rows of whole 16-byte words have whole chunks
+#pragma unroll 1
+            for (uint32_t p = 0; p < kTileBlocks / 2; ++p) wide_pair<WT, MODE, NTA>(l, st + place, st + kXoff, p, acc);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty0 + 8u * slot);
+          if (++slot == a.NS) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      };
+      if (ncol > 8) walk(TileConst<2>());
+      else walk(TileConst<1>());
+      // the tail's factors of columns 8n + 2t + c
       float factor[NT][2];
       int sl[NT][2];
 #pragma unroll
@@ -271,46 +297,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
           }
         }
-      float acc[2][NT][4];
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-      auto walk = [&](auto nta) {
-        constexpr int NTA = decltype(nta)::value;
-#pragma unroll 1
-        for (int kc = 0; kc < n_kc; ++kc) {
-          ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(full0 + 8u * slot, phase, abort_flag, a.err));
-          const uint32_t st = ring + static_cast<uint32_t>(slot) * kStage;
-          const uint32_t nb = static_cast<uint32_t>(min(kTileBlocks, nblk - kc * kTileBlocks));
-          if (ok && mine) {
-            uint32_t rows[2][2];
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) rows[m][h] = st + place[m][h];
-#pragma unroll 1
-            for (uint32_t p = 0; 2u * p < nb; ++p)
-              wide_pair<WT, MODE, NTA, NT>(l, rows, st + kXoff, p, 2u * p + 1u < nb, acc);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(empty0 + 8u * slot);
-          if (++slot == a.NS) {
-            slot = 0;
-            phase ^= 1u;
-          }
-        }
-      };
-      if (NT >= 4 && ncol > 24) walk(TileConst<NT >= 4 ? 4 : 1>());
-      else if (NT >= 3 && ncol > 16) walk(TileConst<NT >= 3 ? 3 : 1>());
-      else if (NT >= 2 && ncol > 8) walk(TileConst<NT >= 2 ? 2 : 1>());
-      else walk(TileConst<1>());
       if constexpr (MODE == TILE_GLU) {
         // the gated values of rows 8h + g (of the warp's 16) and columns 2t + c, in place of the
         // gate sums
-        float2* mx = xchg + (it & 1) * (kTileWarps * 8 * kWideMaxNT);
+        float2* mx = xchg + (it & 1) * (kWarps * 8 * NT);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -330,7 +320,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
               sum += __shfl_xor_sync(0xffffffffu, sum, o);
             }
-            if (g4 == 0) mx[w * 8 * kWideMaxNT + 8 * n + 2 * t4 + c] = make_float2(top, sum);
+            if (g4 == 0) mx[w * 8 * NT + 8 * n + 2 * t4 + c] = make_float2(top, sum);
           }
         named_bar_sync(1u + static_cast<uint32_t>(w >> 1), 64u);
         const int r0 = row0 + 32 * (w >> 1);
@@ -346,7 +336,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               const uint32_t col = 2u * t4 + c;
               if (8 * n + static_cast<int>(col) >= ncol) continue;
               // in the order of the rows, whichever warp looks
-              const float2 u = mx[(w & ~1) * 8 * kWideMaxNT + 8 * n + col], v = mx[(w | 1) * 8 * kWideMaxNT + 8 * n + col];
+              const float2 u = mx[(w & ~1) * 8 * NT + 8 * n + col], v = mx[(w | 1) * 8 * NT + 8 * n + col];
               const float sc = pack_scale(fmaxf(u.x, v.x));
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
