@@ -914,11 +914,10 @@ static int64_t lin_record_bytes(int64_t ncols, int64_t K) {
   return round_up256((ncols + 7) / 8 * ((K + 31) / 32) * (cp * 128 + (cp * 8 + 15) / 16 * 16));
 }
 
-// The tensor-core projection takes batches of a block format with rows of whole 16-byte
-// words.
+// The tensor-core projection takes batches of any format but F16 (whose batches have a
+// tensor-core kernel already), K in whole blocks.  Measured: see tile_lin.cu.
 static bool lin_takes(const Call& c) {
-  const bool fmt = c.wtype == GF_Q8_0 || c.wtype == GF_Q4_0 || c.wtype == GF_Q4_K;
-  return fmt && c.ncols >= 2 && c.K >= 32 && row_bytes_of(c.wtype, c.K) % 16 == 0 && c.K <= (1 << 20) &&
+  return c.wtype != GF_F16 && c.ncols >= 2 && c.K >= 32 && c.K % 32 == 0 && c.K <= (1 << 20) && c.M >= 8 &&
          aligned(c.W, 16) && !(c.flags & GF_FLAG_NO_TENSOR_CORES);
 }
 
@@ -1026,6 +1025,7 @@ static int plan_lora(const void* W, int wtype, const float* x, int64_t M, int64_
     q.err = err;
     q.M = static_cast<int>(M);
     q.K = static_cast<int>(K);
+    q.row_bytes = static_cast<int>(row_bytes_of(wtype, K));
     q.ncols = static_cast<int>(c.ncols);
     q.cols = c.ncols <= 8 ? static_cast<int>(c.ncols) : 16;
     q.cp = static_cast<int>(std::min<int64_t>(8, c.ncols));
@@ -1064,6 +1064,14 @@ static int plan_lora(const void* W, int wtype, const float* x, int64_t M, int64_
     r.kind = REC_LIN;
     r.pdl = true;
     r.lin = q;
+    const int period = q.row_bytes % 16 == 0 ? 1 : q.row_bytes % 8 == 0 ? 2 : q.row_bytes % 4 == 0 ? 4 : 8;
+    if (M % period != 0) {
+      q.phase = LIN_TAIL;
+      LaunchRec& e = recs[(*n)++];
+      e.kind = REC_LIN;
+      e.pdl = true;
+      e.lin = q;
+    }
   } else {
     int m = 0;
     v = plan_launches(c, out, recs + *n, cap - *n, &m);

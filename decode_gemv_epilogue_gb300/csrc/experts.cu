@@ -9,7 +9,7 @@
 //            gated values go out packed for the next product;
 //   down     the same for the down matrices, each slot's column times its weight;
 //   combine  adds a token's slots in the order of its choices.
-// Generic path, for shapes and alignments (and F32) that the tiles do not take: a warp per
+// Generic path, for shapes and alignments that the tiles do not take: a warp per
 // row of a slot's expert, weights decoded element by element, then the same combination.
 #include <algorithm>
 
@@ -216,7 +216,7 @@ template <int WT, int MODE, bool PER1>
 static int launch_tile_cols(const TileArgs& t, const ExpertsArgs& a, cudaStream_t st, bool pdl) {
   const TileOperands o = {a.W, a.W2, static_cast<int64_t>(a.E) * t.rows, a.max_tiles, a.sm_count, a.smem_optin};
   if (a.cols <= 8) return launch_tile<WT, MODE, 1, PER1>(t, o, st, pdl);
-  if constexpr (PER1 && WT != WT_F16) {
+  if constexpr (PER1 && !tile_plain(WT)) {
     return launch_wide<WT, MODE>(t, o, st, pdl);
   } else {
     if (a.cols <= 16) return launch_tile<WT, MODE, 2, PER1>(t, o, st, pdl);
@@ -241,7 +241,9 @@ static int launch_tiles(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
   t.out_format = a.out_format;
   t.factors = a.weights;
   t.out = a.y;
+  t.out_ld = t.rows;
   switch (a.wtype) {
+    case WT_F32: return launch_tile_cols<WT_F32, MODE, true>(t, a, st, pdl);
     case WT_F16: return launch_tile_cols<WT_F16, MODE, true>(t, a, st, pdl);
     case WT_Q8_0:
       return t.period == 1 ? launch_tile_cols<WT_Q8_0, MODE, true>(t, a, st, pdl)

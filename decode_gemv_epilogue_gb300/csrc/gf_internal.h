@@ -290,11 +290,11 @@ struct LoraArgs {
 };
 int launch_lora(const LoraArgs& a, cudaStream_t st, bool pdl);
 
-// The shared projection of a batch in a block format on the tensor cores (tile_lin.cu).
-enum { LIN_PACK = 0, LIN_PRODUCT = 1 };
+// The shared projection of a batch on the tensor cores (tile_lin.cu).
+enum { LIN_PACK = 0, LIN_PRODUCT = 1, LIN_TAIL = 2 };
 struct LinArgs {
   int phase;
-  int wtype;            // GF_Q8_0, GF_Q4_0, GF_Q4_K, rows of whole 16-byte words
+  int wtype;            // GF_F32, GF_Q8_0, GF_Q4_0, GF_Q4_K
   const uint8_t* W;
   const float* x;       // [ncols][K]
   const float* gamma;
@@ -303,7 +303,7 @@ struct LinArgs {
   float* dst;           // [ncols][M]
   uint8_t* records;     // packed x
   unsigned* err;
-  int M, K, epi, ncols;
+  int M, K, row_bytes, epi, ncols;
   int cols, cp;         // columns per group, stored per column tile
   int sm_count, smem_optin;
 };

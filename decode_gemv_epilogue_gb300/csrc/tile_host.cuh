@@ -24,6 +24,8 @@ template <int WT>
 int tile_map(const void* W, int64_t all_rows, int row_bytes, CUtensorMap* out) {
   if (WT == WT_F16)
     return cached_map_2d(W, kMapF16, static_cast<uint64_t>(row_bytes / 2), static_cast<uint64_t>(all_rows), 64, 32, true, out);
+  if (WT == WT_F32)
+    return cached_map_2d(W, kMapF32, static_cast<uint64_t>(row_bytes / 4), static_cast<uint64_t>(all_rows), 32, 32, true, out);
   const int p = tile_period(row_bytes);
   return cached_map_2d(W, kMapF16, static_cast<uint64_t>(row_bytes) * p / 2, static_cast<uint64_t>(all_rows / p),
                        static_cast<uint32_t>(tile_pitch<WT>(p) / 2), static_cast<uint32_t>(32 / p), false, out);
@@ -51,7 +53,7 @@ int launch_tile(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
   // else the records go with the weights.  1 KB a CTA is the system's.
   const int fixed = kTileHeadBytes + kTileRedBytes + 1024;
   const int64_t xb = tile_x_bytes(t.K, NT, t.cp);
-  int ctas = tile_ctas(NT), ns = 0, stage = 0;
+  int ctas = tile_ctas(WT, NT), ns = 0, stage = 0;
   int64_t x_all = 0;
   auto plan = [&](int n, int buffers, int want) {
     const int budget = n == 1 ? o.smem_optin : (o.smem_optin + 1024) / n - 1024;
@@ -63,7 +65,7 @@ int launch_tile(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
     x_all = buffers * xb;
     return ns >= want;
   };
-  const int most = tile_ctas(NT);
+  const int most = tile_ctas(WT, NT);
   if (!plan(most, 2, 4) && !plan(most, 1, 3) && !plan(most, 0, 3) && !plan(1, 1, 3)) plan(1, 0, 2);
   if (ns < 2 || o.max_groups / (ctas * o.sm_count) + 2 > kTileMaxGroups) return cudaErrorInvalidConfiguration;
   t.NS = ns;

@@ -20,6 +20,9 @@
 // weights of one row, so the accumulator of every 32 columns of K has to pass through
 // registers to be scaled (folding the scale into f16 weights would round them); with
 // accumulators in tensor memory that is one read-back per two instructions.
+//
+// F32 weights take tf32 instructions: w = hi + lo in two tf32 (to 2^-22 of it), and the sums
+// hi(w) hi(x) + lo(w) hi(x) + hi(w) lo(x); hi(x) and lo(x), f16, are exact in tf32.
 #pragma once
 
 #include "gf_internal.h"
@@ -41,6 +44,19 @@ __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32
       "{%10, %11, %10, %11};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+// tf32 operands (f32 registers whose low 13 bits do not count), k = 8.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t to_tf32(float v) {  // to nearest
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
+  return r;
 }
 template <int N>
 struct TileConst {
@@ -77,11 +93,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 // eight (column tiles are allocated for the most any group of the call can have).  A warp's 16-byte reads of a step are then consecutive, and the records of a K chunk
 // are one piece of memory for one bulk copy.  Which four elements (s, t) holds is the
 // weights' choice: 16 s + 4 t + .. in the order 0, 2, 1, 3 for the nibble formats (two masks
-// take a code word apart in that order), 16 s + 4 t + 0..3 for Q8_0, and 8 t + 4 s + 0..3
+// take a code word apart in that order), 16 s + 4 t + 0..3 for Q8_0 and F32, and 8 t + 4 s + 0..3
 // for F16 (a thread then reads 16 bytes of a row at once).
 enum { ORDER_NIBBLE = 0, ORDER_BYTE = 1, ORDER_F16 = 2 };
 __host__ __device__ constexpr int pack_order(int wt) {
-  return wt == WT_F16 ? ORDER_F16 : wt == WT_Q8_0 ? ORDER_BYTE : ORDER_NIBBLE;
+  return wt == WT_F16 ? ORDER_F16 : wt == WT_Q8_0 || wt == WT_F32 ? ORDER_BYTE : ORDER_NIBBLE;
 }
 // What the sum of a block is stored for: the offset of the codes, or Q4_K's mins, both in
 // the units of the accumulators.
@@ -91,7 +107,7 @@ __host__ __device__ constexpr float pack_sum(int wt) {
 // Factor of elements 16 .. 31 of a block: their Q4_0 codes are masked in place, 16 times as large.
 __host__ __device__ constexpr float pack_high(int wt) { return wt == WT_Q4_0 ? 0.0625f : 1.0f; }
 // Unit of the accumulators.
-__host__ __device__ constexpr float tile_unit(int wt) { return wt == WT_F16 ? 1.0f : 0x1p24f; }
+__host__ __device__ constexpr float tile_unit(int wt) { return wt == WT_F16 || wt == WT_F32 ? 1.0f : 0x1p24f; }
 __host__ __device__ constexpr int record_bytes(int cp) { return cp * 128 + (cp * 8 + 15) / 16 * 16; }
 // Byte offset in a record of the four elements 4q .. 4q + 3 of column c.
 __device__ __forceinline__ uint32_t record_offset(uint32_t q, uint32_t c, uint32_t cp, int order) {
@@ -338,11 +354,14 @@ constexpr int kTileRedBytes = kTileWarps * 8 * kRedPitch * 4;  // the warps' sum
 // The gated product; one that scales each column by a factor of its own; the plain product
 // of all columns of a batch with a fused tail.
 enum { TILE_GLU = 0, TILE_DOWN = 1, TILE_LIN = 2 };
-__host__ __device__ constexpr int tile_ctas(int nt) { return nt <= 2 ? 2 : 1; }
+// Rows without codes: swizzled 128-byte boxes.
+__host__ __device__ constexpr bool tile_plain(int wt) { return wt == WT_F16 || wt == WT_F32; }
+// (F32's stages are too large for two CTAs.)
+__host__ __device__ constexpr int tile_ctas(int wt, int nt) { return nt <= 2 && wt != WT_F32 ? 2 : 1; }
 
 template <int WT>
 __host__ __device__ constexpr int tile_seg() {  // bytes of a row and chunk
-  return WT == WT_F16 ? 2 * kTileK : WT == WT_Q8_0 ? kTileBlocks * 34 : 144;
+  return WT == WT_F32 ? 4 * kTileK : WT == WT_F16 ? 2 * kTileK : WT == WT_Q8_0 ? kTileBlocks * 34 : 144;
 }
 // Rows that make a whole number of 16-byte words.
 __host__ __device__ constexpr int tile_period(int row_bytes) {
@@ -357,7 +376,7 @@ __host__ __device__ constexpr int tile_part(int period) {
 }
 template <int WT>
 __host__ __device__ constexpr int tile_weight_bytes(int period) {
-  return WT == WT_F16 ? kTileRows * kTileK * 2 : 2 * period * tile_part<WT>(period);
+  return tile_plain(WT) ? kTileRows * tile_seg<WT>() : 2 * period * tile_part<WT>(period);
 }
 // A stage: weights, and in the chunk by chunk case the records of the chunk.
 template <int WT>
@@ -384,7 +403,8 @@ struct TileArgs {
   uint8_t* out_records;     // TILE_GLU: records of the next product's x
   int out_format;           // of the next product's weights
   const float* factors;     // TILE_DOWN: factor of a slot
-  float* out;               // TILE_DOWN: [slot][rows]; TILE_LIN: [column][rows]
+  float* out;               // TILE_DOWN: [slot][out_ld]; TILE_LIN: [column][out_ld]
+  int64_t out_ld;
   const float* aux;         // TILE_LIN: may be `out`
   int epi;
   int ncols, group_cols;    // TILE_LIN: columns of the batch, of a group (no list of groups)
@@ -501,8 +521,69 @@ __device__ __forceinline__ void tile_block(const TileLane& l, uint32_t st, uint3
   }
 }
 
+// The same for F32 rows: boxes of one block each, 16-byte words 4 s + t of the 128 swizzled by
+// the row.
+template <int MODE, int NTA, int NT>
+__device__ __forceinline__ void tile_block_f32(const TileLane& l, uint32_t st, uint32_t xs, uint32_t blk,
+                                               float (&acc)[4][NT][4]) {
+  const uint32_t row = st + l.rowbase + blk * 8192u;
+  float sum[4][NTA][4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int n = 0; n < NTA; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[m][n][i] = 0.0f;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    float xh[NTA][4], xl[NTA][4];  // elements 16 s + 4 t + 0..3 of column g
+#pragma unroll
+    for (int n = 0; n < NTA; ++n) {
+      const uint4 b = lds128(xs + static_cast<uint32_t>(n) * l.xtile + l.xlane + s * l.cp * 64u);
+      const float2 h0 = h2pair(b.x), h1 = h2pair(b.y), l0 = h2pair(b.z), l1 = h2pair(b.w);
+      xh[n][0] = h0.x; xh[n][1] = h0.y; xh[n][2] = h1.x; xh[n][3] = h1.y;
+      xl[n][0] = l0.x; xl[n][1] = l0.y; xl[n][2] = l1.x; xl[n][3] = l1.y;
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      uint32_t wh[2][4], wl[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 u = lds128(row + (m & 1) * 2048u + (m >> 1) * 4096u + h * 1024u + (((4u * s + l.t4) ^ l.row8) << 4));
+        const float w[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          wh[h][k] = to_tf32(w[k]);
+          const float rest = w[k] - __uint_as_float(wh[h][k]);
+          wl[h][k] = to_tf32(fabsf(w[k]) <= 3.402823466e38f ? rest : 0.0f);  // no NaN beside an infinite weight
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)  // k-slots t and t + 4 hold elements 2j and 2j + 1
+#pragma unroll
+        for (int n = 0; n < NTA; ++n) {
+          const uint32_t h0 = __float_as_uint(xh[n][2 * j]), h1 = __float_as_uint(xh[n][2 * j + 1]);
+          const uint32_t l0 = __float_as_uint(xl[n][2 * j]), l1 = __float_as_uint(xl[n][2 * j + 1]);
+          mma_tf32(sum[m][n], wh[0][2 * j], wh[1][2 * j], wh[0][2 * j + 1], wh[1][2 * j + 1], h0, h1);
+          mma_tf32(sum[m][n], wl[0][2 * j], wl[1][2 * j], wl[0][2 * j + 1], wl[1][2 * j + 1], h0, h1);
+          mma_tf32(sum[m][n], wh[0][2 * j], wh[1][2 * j], wh[0][2 * j + 1], wh[1][2 * j + 1], l0, l1);
+        }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NTA; ++n) {
+    const float sx[2] = {__uint_as_float(lds32(xs + static_cast<uint32_t>(n) * l.xtile + l.m0)),
+                         __uint_as_float(lds32(xs + static_cast<uint32_t>(n) * l.xtile + l.m1))};
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[m][n][i] = MODE == TILE_DOWN ? fmaf(sx[i & 1], sum[m][n][i], acc[m][n][i]) : acc[m][n][i] + sum[m][n][i];
+  }
+}
+
 template <int WT, int MODE, int NT, bool PER1>
-__global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
+__global__ void __launch_bounds__(kTileThreads, tile_ctas(WT, NT))
     tile_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
                 const __grid_constant__ TileArgs a) {
   constexpr int kOutRows = MODE == TILE_GLU ? 32 : kTileRows;
@@ -557,7 +638,7 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
       int slot = 0, issued = 0, gi = 0, tile = tile_lo, xgroups = 0;
       uint32_t phase = 1u;
       bool ok = true;
-      const uint32_t wlen = WT == WT_F16 ? 32u * kTileK * 2u : 32u * static_cast<uint32_t>(tile_pitch<WT>(a.period));
+      const uint32_t wlen = 32u * static_cast<uint32_t>(tile_plain(WT) ? tile_seg<WT>() : tile_pitch<WT>(a.period));
       for (int it = 0; it < n_items && ok; ++it) {
         const int4 g = groups[gi];
         const int row0 = tile * kOutRows;
@@ -590,10 +671,11 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
           for (int h = 0; h < halves; ++h) {
             const CUtensorMap* map = MODE == TILE_GLU && h ? &map1 : &map0;
             const int row = first + (MODE == TILE_GLU ? 0 : 32 * h);
-            if constexpr (WT == WT_F16) {
+            if constexpr (tile_plain(WT)) {
+              constexpr int kBox = WT == WT_F16 ? 64 : 32;  // elements of 128 bytes
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                tma_load_2d(st + static_cast<uint32_t>((2 * q + h) * 4096), map, kc * kTileK + 64 * q, row, full);
+              for (int q = 0; q < kTileK / kBox; ++q)
+                tma_load_2d(st + static_cast<uint32_t>((2 * q + h) * 4096), map, kc * kTileK + kBox * q, row, full);
             } else if constexpr (PER1) {
               tma_load_2d(st + static_cast<uint32_t>(h * tile_part<WT>(1)), map, kc * (tile_seg<WT>() / 2), row, full);
             } else {
@@ -631,9 +713,9 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
     {
       const uint32_t g4 = static_cast<uint32_t>(lane) >> 2, per = static_cast<uint32_t>(a.period);
       l.t4 = static_cast<uint32_t>(lane) & 3u;
-      l.row8 = WT == WT_F16 ? ((g4 >> 1) | ((g4 & 1u) << 2)) : g4;  // the row of eight that this lane takes
+      l.row8 = tile_plain(WT) ? ((g4 >> 1) | ((g4 & 1u) << 2)) : g4;  // the row of eight that this lane takes
       l.step8 = l.step16 = l.half = 0;
-      if constexpr (WT == WT_F16) {
+      if constexpr (tile_plain(WT)) {
         l.rowbase = l.row8 * 128u;
       } else if constexpr (PER1) {
         l.rowbase = l.row8 * tile_pitch<WT>(1);
@@ -702,7 +784,9 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
                                          : st + xoff + blk * l.rec;
             // codes behind a two-byte scale start on a word in every other block (in rows that
             // themselves do)
-            if (PER1 && (WT == WT_Q4_0 || WT == WT_Q8_0) && (wk & 1))
+            if constexpr (WT == WT_F32)
+              tile_block_f32<MODE, NTA, NT>(l, st, xs, blk, acc);
+            else if (PER1 && (WT == WT_Q4_0 || WT == WT_Q8_0) && (wk & 1))
               tile_block<WT, MODE, NTA, NT, PER1, true>(l, st, xs, blk, acc);
             else
               tile_block<WT, MODE, NTA, NT, PER1, false>(l, st, xs, blk, acc);
@@ -771,7 +855,7 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(NT))
               const int r = row0 + 32 * h + lane;
               if (r < a.rows) {
                 const int64_t col = MODE == TILE_LIN ? (g.w + n) * 8 + wk : sl[n];
-                const int64_t o = col * a.rows + r;
+                const int64_t o = col * a.out_ld + r;
                 const float y = factor[n] * (v[h] * tile_unit(WT));
                 if constexpr (MODE == TILE_LIN)
                   a.out[o] = apply_tail(a.epi, y, epi_takes_aux(a.epi) ? a.aux[o] : 0.0f);  // aux may be out

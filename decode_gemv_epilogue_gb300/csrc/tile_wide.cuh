@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
           for (int c = 0; c < 2; ++c) {
             const int col = 8 * n + 2 * static_cast<int>(t4) + c;
             if (col >= ncol) continue;
-            const int64_t base = (MODE == TILE_LIN ? static_cast<int64_t>(g.w) * 8 + col : sl[n][c]) * a.rows;
+            const int64_t base = (MODE == TILE_LIN ? static_cast<int64_t>(g.w) * 8 + col : sl[n][c]) * a.out_ld;
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll

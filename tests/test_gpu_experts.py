@@ -105,9 +105,19 @@ def test_formats(G, T, E, k, M, K, wt):
     Case(G, T, E, k, M, K, wt, wt).check()
 
 
+@pytest.mark.parametrize("wt", [F32, F16, Q8, Q4, Q4K])
+@pytest.mark.parametrize("T, E, k, M, K", [(40, 3, 1, 288, 256), (100, 4, 2, 512, 512), (256, 3, 2, 256, 768),
+                                           (61, 5, 2, 96, 1056)])
+def test_many_columns_per_expert(G, T, E, k, M, K, wt):
+    if wt == Q4K:
+        M, K = (M + 255) // 256 * 256, (K + 255) // 256 * 256
+    Case(G, T, E, k, M, K, wt, wt, seed=15).check()
+
+
 @pytest.mark.parametrize("wt, wd", [(Q4K, Q8), (Q4, F16), (F16, Q4), (Q8, Q4K), (F32, Q4), (Q4, F32)])
 def test_mixed_formats(G, wt, wd):
     Case(G, 6, 5, 3, 256, 512, wt, wd, seed=20).check()
+    Case(G, 60, 4, 2, 256, 512, wt, wd, seed=21).check()
 
 
 @pytest.mark.parametrize("wt", [F32, F16])

@@ -105,6 +105,24 @@ def test_ragged_shapes(G, M, K, at):
     Case(G, 4, M, K, F32, 3, 12, at, seed=M).check(2)
 
 
+@pytest.mark.parametrize("wt", [Q8, Q4])
+@pytest.mark.parametrize("N, M, K", [(2, 8, 32), (3, 71, 96), (9, 302, 3648), (20, 131, 1056), (33, 100, 1984)])
+def test_rows_of_no_whole_16_byte_words(G, N, M, K, wt):
+    """Block-format batches whose rows a tensor map reaches only several at a time, and rows
+    left over at the end."""
+    c = Case(G, N, M, K, wt, 3, 8, F16, seed=M + K)
+    c.check(1)
+    c.check(4)
+
+
+@pytest.mark.parametrize("wt", [F32, Q8, Q4, Q4K])
+@pytest.mark.parametrize("N, M, K", [(2, 8, 256), (9, 33, 512), (16, 1000, 768), (17, 513, 256), (64, 600, 1024)])
+def test_batches(G, N, M, K, wt):
+    c = Case(G, N, M, K, wt, 5, 16, F16, seed=N)
+    c.check(2)
+    c.check(3)
+
+
 @pytest.mark.parametrize("at", [F16, F32])
 @pytest.mark.parametrize("shift", [1, 4])
 def test_adapters_off_a_16_byte_boundary(G, at, shift):
@@ -138,9 +156,12 @@ def test_split_rows(G):
     c.check(1)
 
 
-def test_rms_prologue(G):
-    c = Case(G, 3, 128, 1024, Q4, 3, 16, F16, seed=8)
-    gam, eps = (1.0 + 0.1 * synth.normal(1024, seed=9)).astype(np.float32), 1e-6
+@pytest.mark.parametrize("N, M, wt", [(1, 128, Q4), (3, 128, Q4), (3, 130, Q8), (18, 64, Q4K), (4, 96, F16)])
+def test_rms_prologue(G, N, M, wt):
+    c = Case(G, N, M, 1024, wt, 3, 16, F16, seed=8)
+    if wt == Q8:  # rows a tensor map reaches two at a time, two rows left over
+        c = Case(G, N, M, 1120, wt, 3, 16, F16, seed=8)
+    gam, eps = (1.0 + 0.1 * synth.normal(c.K, seed=9)).astype(np.float32), 1e-6
     xn = onorm.rms_norm(c.x, gam, eps, c.K)
     y, b = c.want(4, x=xn)
     extra = TOL_NORM_REL * (ogemv.abs_dot(c.raw, c.wt, xn, c.M, c.K))
