@@ -81,47 +81,53 @@ __global__ void __launch_bounds__(256) experts_combine_kernel(const __grid_const
 constexpr int kPrepThreads = kPackThreads;
 constexpr int kPrepMaxIter = kExpMaxTokens * kRouteMaxTopK / kPrepThreads;  // 32-slot steps of a warp
 
-static int prep_smem(int E) { return 32 * E * 2 + E * 4 + (32 + 16) * 4; }
+static int prep_smem(int E) { return 32 * E * 2 + E * 4; }
 
 // The column tile of a prep CTA: up to eight slots of one expert.
 struct PrepTile {
-  int count, cp;  // columns of the tile; stored per column tile of its group
+  int first, count, cp;  // entry and columns of the tile; columns stored per column tile of its group
   int slot[8];
 };
 
 // The slots of each expert in slot order: a counting sort whose counts are kept per warp
 // (each warp owns a run of consecutive slots) and ranked within a 32-slot step by matching.
 // Every CTA of the launch makes the whole list (a few microseconds, less than another launch)
-// and keeps its own column tile; the first one also writes the list and the column groups.
-__device__ void list_slots(const ExpertsArgs& a, bool write, int my_tile, PrepTile* out, uint16_t* cnt, uint32_t* offs,
-                           uint32_t* wsum, int* range) {
+// and packs its own column tiles; the first one also writes the list and the column groups.
+__global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(const __grid_constant__ ExpertsArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ PrepTile pt;
+  __shared__ uint32_t wsum[32];
+  __shared__ float wmax[2 * kPrepThreads / 32];
+  uint32_t* offs = reinterpret_cast<uint32_t*>(smem);
+  uint16_t* cnt = reinterpret_cast<uint16_t*>(offs + a.E);
+  pdl_wait();
+  pdl_trigger();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int S = a.T * a.k;
   const int run = ((S + 31) / 32 + 31) / 32 * 32;  // slots of a warp
   const int nw = (S + run - 1) / run;              // warps that have some
-  for (int i = threadIdx.x; i < nw * a.E; i += kPrepThreads) cnt[i] = 0;
-  if (threadIdx.x < 2) range[threadIdx.x] = 0;
-  __syncthreads();
   int ex[kPrepMaxIter], rank[kPrepMaxIter];
+#pragma unroll
+  for (int j = 0; j < kPrepMaxIter; ++j) {
+    const int s = w * run + 32 * j + lane;
+    ex[j] = 32 * j < run && s < S ? a.ids[s] : -1;
+    if (ex[j] >= a.E) ex[j] = -1;
+  }
+  for (int i = threadIdx.x; i < nw * a.E; i += kPrepThreads) cnt[i] = 0;
+  __syncthreads();
   uint16_t* mine = cnt + w * a.E;
 #pragma unroll
   for (int j = 0; j < kPrepMaxIter; ++j) {
-    ex[j] = -1;
     rank[j] = 0;
     if (32 * j < run && w < nw) {
-      const int s = w * run + 32 * j + lane;
-      const int e = s < S ? a.ids[s] : -1;
-      const bool valid = e >= 0 && e < a.E;
-      const uint32_t same = __match_any_sync(0xffffffffu, valid ? e : -1);
+      const bool valid = ex[j] >= 0;
+      const uint32_t same = __match_any_sync(0xffffffffu, valid ? ex[j] : -1);
       const int before = __popc(same & ((1u << lane) - 1u));
-      const int base = valid ? mine[e] : 0;
+      const int base = valid ? mine[ex[j]] : 0;
       __syncwarp();
-      if (valid && before == 0) mine[e] = static_cast<uint16_t>(base + __popc(same));
+      if (valid && before == 0) mine[ex[j]] = static_cast<uint16_t>(base + __popc(same));
       __syncwarp();
-      if (valid) {
-        ex[j] = e;
-        rank[j] = base + before;
-      }
+      rank[j] = base + before;
     }
   }
   __syncthreads();
@@ -130,10 +136,15 @@ __device__ void list_slots(const ExpertsArgs& a, bool write, int my_tile, PrepTi
   const int e = threadIdx.x;
   uint32_t total = 0;
   if (e < a.E)
-    for (int q = 0; q < nw; ++q) {
-      const uint32_t c = cnt[q * a.E + e];
-      cnt[q * a.E + e] = static_cast<uint16_t>(total);
-      total += c;
+    for (int q0 = 0; q0 < nw; q0 += 8) {
+      uint32_t c[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) c[q] = q0 + q < nw ? cnt[(q0 + q) * a.E + e] : 0u;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        if (q0 + q < nw) cnt[(q0 + q) * a.E + e] = static_cast<uint16_t>(total);
+        total += c[q];
+      }
     }
   const uint32_t nt = (total + 7) / 8, gt = (a.cols + 7) / 8;  // column tiles of the expert, of a full group
   const uint32_t ng = (nt + gt - 1) / gt;
@@ -161,15 +172,9 @@ __device__ void list_slots(const ExpertsArgs& a, bool write, int my_tile, PrepTi
   uint32_t all;
   const uint32_t ex0 = scan(total | (nt << 16), all);
   const uint32_t off = ex0 & 0xffffu, t0 = ex0 >> 16;
+  const int tiles = static_cast<int>(all >> 16);
   if (e < a.E) offs[e] = off;
-  if (static_cast<uint32_t>(my_tile) >= t0 && static_cast<uint32_t>(my_tile) < t0 + nt) {
-    const uint32_t f = 8u * (static_cast<uint32_t>(my_tile) - t0);
-    range[0] = static_cast<int>(off + f);
-    range[1] = static_cast<int>(min(8u, total - f));
-    const uint32_t group = f / (gt * 8u) * (gt * 8u);  // the group's first column
-    out->cp = static_cast<int>(min(8u, total - group));
-  }
-  if (write) {
+  if (blockIdx.x == 0) {
     uint32_t groups;
     const uint32_t g0 = scan(ng, groups);
     for (uint32_t i = 0; i < ng; ++i) {
@@ -180,34 +185,31 @@ __device__ void list_slots(const ExpertsArgs& a, bool write, int my_tile, PrepTi
     if (threadIdx.x == 0) *a.n_groups = static_cast<int>(groups);
   }
   __syncthreads();
-  const int first = range[0], count = range[1];
-  if (threadIdx.x == 0) out->count = count;
+  int pos[kPrepMaxIter];  // places of this thread's slots in the list
 #pragma unroll
-  for (int j = 0; j < kPrepMaxIter; ++j)
+  for (int j = 0; j < kPrepMaxIter; ++j) {
+    pos[j] = -1;
     if (ex[j] >= 0) {
-      const int pos = static_cast<int>(offs[ex[j]]) + mine[ex[j]] + rank[j], s = w * run + 32 * j + lane;
-      if (write) a.slots[pos] = s;
-      if (pos >= first && pos < first + count) out->slot[pos - first] = s;
+      pos[j] = static_cast<int>(offs[ex[j]]) + mine[ex[j]] + rank[j];
+      if (blockIdx.x == 0) a.slots[pos[j]] = w * run + 32 * j + lane;
     }
-  __syncthreads();
-}
-
-__global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(const __grid_constant__ ExpertsArgs a) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ PrepTile pt;
-  __shared__ float wmax[2 * kPrepThreads / 32];
-  pdl_wait();
-  pdl_trigger();
-  uint32_t* offs = reinterpret_cast<uint32_t*>(smem);
-  uint32_t* wsum = offs + a.E;
-  int* range = reinterpret_cast<int*>(wsum + 32);
-  const int tile = static_cast<int>(blockIdx.x);
-  list_slots(a, tile == 0, tile, &pt, reinterpret_cast<uint16_t*>(range + 16), offs, wsum, range);
-  if (pt.count > 0) {
-    const int c = threadIdx.x / kPackColumn;
+  }
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    if (static_cast<uint32_t>(tile) >= t0 && static_cast<uint32_t>(tile) < t0 + nt) {  // one thread's expert
+      const uint32_t f = 8u * (static_cast<uint32_t>(tile) - t0), group = f / (gt * 8u) * (gt * 8u);
+      pt.first = static_cast<int>(off + f);
+      pt.count = static_cast<int>(min(8u, total - f));
+      pt.cp = static_cast<int>(min(8u, total - group));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPrepMaxIter; ++j)
+      if (pos[j] >= pt.first && pos[j] < pt.first + pt.count) pt.slot[pos[j] - pt.first] = w * run + 32 * j + lane;
+    __syncthreads();
+    const int share = pack_share(pt.count), c = threadIdx.x / share;
     const float* x = c < pt.count ? a.x + static_cast<int64_t>(pt.slot[c] / a.k) * a.K : nullptr;
-    pack_tile(x, nullptr, 0.0f, a.K, a.wtype, pt.cp, a.xrec + static_cast<int64_t>(tile) * (a.K / 32) * record_bytes(a.cp),
-              wmax);
+    pack_column(x, c, threadIdx.x % share, share, nullptr, 0.0f, a.K, a.wtype, pt.cp,
+                a.xrec + static_cast<int64_t>(tile) * (a.K / 32) * record_bytes(a.cp), wmax);
   }
 }
 
@@ -233,6 +235,7 @@ static int launch_tiles(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
   t.period = tile_period(t.row_bytes);
   t.groups = a.groups;
   t.n_groups = a.n_groups;
+  t.max_groups = a.T * a.k;
   t.slots = a.slots;
   t.records = MODE == TILE_GLU ? a.xrec : a.hrec;
   t.cp = a.cp;
@@ -286,7 +289,7 @@ int launch_experts(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
         if (e != cudaSuccess) return e;
         configured[dev] = smem;
       }
-      cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(a.max_tiles)), kPrepThreads, st, pdl, &attr);
+      cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(std::min(a.max_tiles, 2 * a.sm_count))), kPrepThreads, st, pdl, &attr);
       cfg.dynamicSmemBytes = static_cast<size_t>(smem);
       return cudaLaunchKernelEx(&cfg, experts_prep_kernel, a);
     }

@@ -8,18 +8,52 @@
 // order the shared product, launched with programmatic dependent launch, already streams its
 // weights while the two small kernels run, and the output is read and written once more only.
 //
-// Shrink: a CTA takes eight rows of one column's A; its 256 threads share the K axis, every
-// thread holding eight row sums, so that one round of independent 16-byte loads covers
-// 2048 elements of the eight rows and a decode-sized K is a latency of one or two rounds.
-// Sums: 32 bits, per thread in K order, then a shuffle tree, then the warps in order.
-// Expand: a thread per output row walks its r contiguous values of B.
+// Columns that share an adapter are served together: the CTA of the first such column takes
+// all of them, the others' CTAs leave at once, so that an adapter's rows are fetched once per
+// four columns (shrink) or once (expand).
+//
+// Shrink: a CTA takes a few rows of an adapter's A; its 256 threads share the K axis, every
+// thread holding the sums of its rows and up to four columns, so that one round of
+// independent 16-byte loads covers 2048 elements and a decode-sized K is a latency of one or
+// two rounds.  Two rows a CTA while that leaves SMs idle (16 rows of 4096 for one column: 6.1
+// -> 3.4 us against eight), eight once the columns fill them.  Sums: 32 bits, per thread in K
+// order, then a shuffle tree, then the warps in order.
+// Expand: a CTA takes 128 rows of B, 64 (f32: 32) values of each at a time through shared
+// memory, a thread per row walks them for four columns at a time.
 #include "gf_device.cuh"
 #include "gf_internal.h"
 
 namespace gf {
 
 constexpr int kLoraThreads = 256;
-constexpr int kShrinkRows = 8;
+constexpr int kLoraCols = 4;      // columns of an adapter served at once
+constexpr int kExpandRows = 128;  // rows, and threads, of an expansion CTA
+
+// The columns from c on that take the adapter of column c, in order, into cols; their number.
+// 0 where an earlier column takes it: that column's CTA serves them all.  Called by every
+// thread of a CTA of `threads` >= 128.
+__device__ __forceinline__ int adapter_columns(const LoraArgs& a, int c, int threads, int* cols, int* seen) {
+  const int ad = a.ids[c];
+  if (threadIdx.x == 0) seen[0] = 0;
+  __syncthreads();
+  for (int q = threadIdx.x; q < c; q += threads)
+    if (a.ids[q] == ad) seen[0] = 1;
+  __syncthreads();
+  if (seen[0]) return 0;
+  if (threadIdx.x < 32) {  // one warp lists them, in order
+    int n = 0;
+    for (int q0 = c; q0 < a.ncols; q0 += 32) {
+      const int q = q0 + static_cast<int>(threadIdx.x);
+      const bool is = q < a.ncols && a.ids[q] == ad;
+      const uint32_t m = __ballot_sync(0xffffffffu, is);
+      if (is) cols[n + __popc(m & ((1u << threadIdx.x) - 1u))] = q;
+      n += __popc(m);
+    }
+    if (threadIdx.x == 0) seen[1] = n;
+  }
+  __syncthreads();
+  return seen[1];
+}
 
 // Eight consecutive adapter weights.
 template <int AT>
@@ -45,109 +79,204 @@ __device__ __forceinline__ float load1(const uint8_t* base, int64_t i) {
 }
 
 // VEC: rows of A, x and gamma are read 16 bytes at a time (K a multiple of 8, all 16-byte
-// aligned); otherwise element by element.
-template <int AT, bool VEC>
+// aligned); otherwise element by element.  RB rows, up to CT columns at once.
+template <int AT, bool VEC, int RB, int CT>
 __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const __grid_constant__ LoraArgs a) {
-  constexpr int kEl = AT == WT_F16 ? 2 : 4;
-  __shared__ float part[kLoraThreads / 32][kShrinkRows + 1];
+  constexpr int kEl = AT == WT_F16 ? 2 : 4, V = RB * CT;
+  __shared__ float part[kLoraThreads / 32][V + CT];
+  __shared__ int cols[256], seen[2];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.y, j0 = blockIdx.x * kShrinkRows;
-  const int rows = min(kShrinkRows, a.r - j0);
+  const int c = blockIdx.y, j0 = blockIdx.x * RB;
+  const int rows = min(RB, a.r - j0);
   const int ad = a.ids[c];
   if (ad < 0 || ad >= a.n) return;  // the expansion does not read v for this column
-  const float* x = a.x + static_cast<int64_t>(c) * a.K;
-  const uint8_t* A = a.A + (static_cast<int64_t>(ad) * a.r + j0) * a.K * kEl;
-  float acc[kShrinkRows], ss = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kShrinkRows; ++i) acc[i] = 0.0f;
-  if constexpr (VEC) {
-    for (int k = threadIdx.x * 8; k < a.K; k += kLoraThreads * 8) {
-      float xv[8];
-      load8<WT_F32>(reinterpret_cast<const uint8_t*>(x + k), xv);
-      if (a.gamma) {
-        float g[8];
-        load8<WT_F32>(reinterpret_cast<const uint8_t*>(a.gamma + k), g);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          ss = fmaf(xv[q], xv[q], ss);
-          xv[q] *= g[q];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kShrinkRows; ++i)
-        if (i < rows) {
-          float w[8];
-          load8<AT>(A + (static_cast<int64_t>(i) * a.K + k) * kEl, w);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) acc[i] = fmaf(w[q], xv[q], acc[i]);
-        }
-    }
-  } else {
-    for (int k = threadIdx.x; k < a.K; k += kLoraThreads) {
-      float xv = x[k];
-      if (a.gamma) {
-        ss = fmaf(xv, xv, ss);
-        xv *= a.gamma[k];
-      }
-#pragma unroll
-      for (int i = 0; i < kShrinkRows; ++i)
-        if (i < rows) acc[i] = fmaf(load1<AT>(A, static_cast<int64_t>(i) * a.K + k), xv, acc[i]);
-    }
-  }
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const float t = WarpVecReduce<kShrinkRows>::run(acc, lane);
-  if (lane % (32 / kShrinkRows) == 0) part[w][lane / (32 / kShrinkRows)] = t;
-  if (a.gamma) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (lane == 0) part[w][kShrinkRows] = ss;
+  int n = 1;
+  if (a.ncols > 1) {
+    n = adapter_columns(a, c, kLoraThreads, cols, seen);
+    if (n == 0) return;
+  } else if (threadIdx.x == 0) {
+    cols[0] = c;
   }
   __syncthreads();
-  if (static_cast<int>(threadIdx.x) < rows) {
-    float s = 0.0f;
-    for (int q = 0; q < kLoraThreads / 32; ++q) s += part[q][threadIdx.x];
-    if (a.gamma) {
-      float q2 = 0.0f;
-      for (int q = 0; q < kLoraThreads / 32; ++q) q2 += part[q][kShrinkRows];
-      s *= 1.0f / sqrtf(q2 / static_cast<float>(a.K) + a.eps);
+  const uint8_t* A = a.A + (static_cast<int64_t>(ad) * a.r + j0) * a.K * kEl;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  for (int q0 = 0; q0 < n; q0 += CT) {
+    const int nc = min(CT, n - q0);
+    const float* x[CT];
+#pragma unroll
+    for (int t = 0; t < CT; ++t) x[t] = a.x + static_cast<int64_t>(cols[q0 + min(t, nc - 1)]) * a.K;
+    float acc[V], ss[CT];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < CT; ++t) ss[t] = 0.0f;
+    if constexpr (VEC) {
+#pragma unroll 2
+      for (int k = threadIdx.x * 8; k < a.K; k += kLoraThreads * 8) {
+        float xv[CT][8], g[8];
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+          if (t < nc) load8<WT_F32>(reinterpret_cast<const uint8_t*>(x[t] + k), xv[t]);
+        if (a.gamma) {
+          load8<WT_F32>(reinterpret_cast<const uint8_t*>(a.gamma + k), g);
+#pragma unroll
+          for (int t = 0; t < CT; ++t)
+            if (t < nc)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                ss[t] = fmaf(xv[t][e], xv[t][e], ss[t]);
+                xv[t][e] *= g[e];
+              }
+        }
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+          if (i < rows) {
+            float wv[8];
+            load8<AT>(A + (static_cast<int64_t>(i) * a.K + k) * kEl, wv);
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+              if (t < nc)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[i * CT + t] = fmaf(wv[e], xv[t][e], acc[i * CT + t]);
+          }
+      }
+    } else {
+      for (int k = threadIdx.x; k < a.K; k += kLoraThreads) {
+        float xv[CT];
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+          xv[t] = x[t][k];
+          if (a.gamma) {
+            ss[t] = fmaf(xv[t], xv[t], ss[t]);
+            xv[t] *= a.gamma[k];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+          if (i < rows) {
+            const float wv = load1<AT>(A, static_cast<int64_t>(i) * a.K + k);
+#pragma unroll
+            for (int t = 0; t < CT; ++t) acc[i * CT + t] = fmaf(wv, xv[t], acc[i * CT + t]);
+          }
+      }
     }
-    a.v[static_cast<int64_t>(c) * a.r + j0 + threadIdx.x] = a.scales ? s * a.scales[ad] : s;
+    const float t = WarpVecReduce<V>::run(acc, lane);
+    if (lane % (32 / V) == 0) part[w][lane / (32 / V)] = t;
+    if (a.gamma) {
+#pragma unroll
+      for (int q = 0; q < CT; ++q) {
+        float v = ss[q];
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) part[w][V + q] = v;
+      }
+    }
+    __syncthreads();
+    const int i = threadIdx.x / CT, q = threadIdx.x % CT;
+    if (i < rows && q < nc) {
+      float s = 0.0f;
+      for (int p = 0; p < kLoraThreads / 32; ++p) s += part[p][i * CT + q];
+      if (a.gamma) {
+        float z = 0.0f;
+        for (int p = 0; p < kLoraThreads / 32; ++p) z += part[p][V + q];
+        s *= 1.0f / sqrtf(z / static_cast<float>(a.K) + a.eps);
+      }
+      a.v[static_cast<int64_t>(cols[q0 + q]) * a.r + j0 + i] = a.scales ? s * a.scales[ad] : s;
+    }
+    __syncthreads();  // part is written again
   }
 }
 
-// VEC: rows of B read 16 bytes at a time (r a multiple of 8, B 16-byte aligned).
+// VEC: rows of B are whole 16-byte words.
 template <int AT, bool VEC>
-__global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const __grid_constant__ LoraArgs a) {
+__global__ void __launch_bounds__(kExpandRows) lora_expand_kernel(const __grid_constant__ LoraArgs a) {
   constexpr int kEl = AT == WT_F16 ? 2 : 4;
-  __shared__ __align__(16) float vs[kLoraMaxRank];
+  constexpr int kChunk = 128 / kEl;    // values of a row at a time
+  constexpr int kPitch = 128 + 16;     // bytes: rows a bank row and a word apart
+  __shared__ __align__(16) uint8_t bs[kExpandRows * kPitch];
+  __shared__ __align__(16) float vs[kLoraCols][kChunk];
+  __shared__ int cols[256], seen[2];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.y;
+  const int c = blockIdx.y, m0 = blockIdx.x * kExpandRows, m = m0 + threadIdx.x;
   const int ad = a.ids[c];
-  const bool live = ad >= 0 && ad < a.n;
-  if (live) {
-    for (int j = threadIdx.x; j < a.r; j += kLoraThreads) vs[j] = a.v[static_cast<int64_t>(c) * a.r + j];
+  if (ad < 0 || ad >= a.n) {  // no adapter: the addend alone
+    if (m < a.M) {
+      const int64_t o = static_cast<int64_t>(c) * a.M + m;
+      a.out[o] = a.aux ? a.aux[o] : 0.0f;
+    }
+    return;
   }
-  __syncthreads();
-  const int m = blockIdx.x * kLoraThreads + threadIdx.x;
-  if (m >= a.M) return;
-  const int64_t o = static_cast<int64_t>(c) * a.M + m;
-  float s = 0.0f;
-  if (live) {
-    const uint8_t* B = a.B + (static_cast<int64_t>(ad) * a.M + m) * a.r * kEl;
+  int n = 1;
+  if (a.ncols > 1) {
+    n = adapter_columns(a, c, kExpandRows, cols, seen);
+    if (n == 0) return;
+  } else if (threadIdx.x == 0) {
+    cols[0] = c;
+  }
+  const int rows = min(kExpandRows, a.M - m0);
+  const uint8_t* B = a.B + (static_cast<int64_t>(ad) * a.M + m0) * a.r * kEl;
+  for (int k0 = 0; k0 < a.r; k0 += kChunk) {
+    const int len = min(kChunk, a.r - k0);
+    __syncthreads();  // cols is listed; the previous chunk has been read
     if constexpr (VEC) {
-      for (int j = 0; j < a.r; j += 8) {
-        float w[8];
-        load8<AT>(B + j * kEl, w);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) s = fmaf(w[q], vs[j + q], s);
+      const int words = len * kEl / 16;
+      for (int i = threadIdx.x; i < rows * words; i += kExpandRows) {
+        const int r = i / words, q = i - r * words;
+        *reinterpret_cast<uint4*>(bs + r * kPitch + q * 16) =
+            *reinterpret_cast<const uint4*>(B + (static_cast<int64_t>(r) * a.r + k0) * kEl + q * 16);
       }
     } else {
-      for (int j = 0; j < a.r; ++j) s = fmaf(load1<AT>(B, j), vs[j], s);
+      for (int i = threadIdx.x; i < rows * len; i += kExpandRows) {
+        const int r = i / len, q = i - r * len;
+        const int64_t at = static_cast<int64_t>(r) * a.r + k0 + q;
+        if constexpr (AT == WT_F16)
+          reinterpret_cast<uint16_t*>(bs + r * kPitch)[q] = reinterpret_cast<const uint16_t*>(B)[at];
+        else
+          reinterpret_cast<uint32_t*>(bs + r * kPitch)[q] = reinterpret_cast<const uint32_t*>(B)[at];
+      }
+    }
+    for (int q0 = 0; q0 < n; q0 += kLoraCols) {
+      const int nc = min(kLoraCols, n - q0);
+      __syncthreads();  // the rows are staged; the previous columns' v has been read
+      for (int i = threadIdx.x; i < kLoraCols * kChunk; i += kExpandRows) {
+        const int t = i / kChunk, j = i - t * kChunk;
+        vs[t][j] = t < nc && j < len ? a.v[static_cast<int64_t>(cols[q0 + t]) * a.r + k0 + j] : 0.0f;
+      }
+      __syncthreads();
+      if (m < a.M) {
+        float s[kLoraCols] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint8_t* b = bs + threadIdx.x * kPitch;
+        int j = 0;
+        for (; j + 8 <= len; j += 8) {
+          float wv[8];
+          load8<AT>(b + j * kEl, wv);
+#pragma unroll
+          for (int t = 0; t < kLoraCols; ++t)
+            if (t < nc) {
+              const float4 v0 = *reinterpret_cast<const float4*>(&vs[t][j]), v1 = *reinterpret_cast<const float4*>(&vs[t][j + 4]);
+              s[t] = fmaf(wv[0], v0.x, s[t]); s[t] = fmaf(wv[1], v0.y, s[t]);
+              s[t] = fmaf(wv[2], v0.z, s[t]); s[t] = fmaf(wv[3], v0.w, s[t]);
+              s[t] = fmaf(wv[4], v1.x, s[t]); s[t] = fmaf(wv[5], v1.y, s[t]);
+              s[t] = fmaf(wv[6], v1.z, s[t]); s[t] = fmaf(wv[7], v1.w, s[t]);
+            }
+        }
+        for (; j < len; ++j) {
+          const float wv = load1<AT>(b, j);
+#pragma unroll
+          for (int t = 0; t < kLoraCols; ++t) s[t] = fmaf(wv, vs[t][j], s[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < kLoraCols; ++t)
+          if (t < nc) {
+            const int64_t o = static_cast<int64_t>(cols[q0 + t]) * a.M + m;
+            const float base = k0 > 0 ? a.out[o] : a.aux ? a.aux[o] : 0.0f;  // later chunks add to the first one's
+            a.out[o] = base + s[t];
+          }
+      }
     }
   }
-  a.out[o] = a.aux ? a.aux[o] + s : s;
 }
 
 static bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -163,13 +292,19 @@ static cudaError_t launch_lora_t(const LoraArgs& a, cudaStream_t st, bool pdl) {
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   if (a.phase == LORA_SHRINK) {
-    cfg.gridDim = dim3(static_cast<unsigned>((a.r + kShrinkRows - 1) / kShrinkRows), static_cast<unsigned>(a.ncols));
     const bool vec = a.K % 8 == 0 && al16(a.A) && al16(a.x) && al16(a.gamma);
-    return vec ? cudaLaunchKernelEx(&cfg, lora_shrink_kernel<AT, true>, a)
-               : cudaLaunchKernelEx(&cfg, lora_shrink_kernel<AT, false>, a);
+    const bool few = a.ncols * ((a.r + 7) / 8) <= 32;  // two rows a CTA, a column at a time
+    const int rb = few ? 2 : 8;
+    cfg.gridDim = dim3(static_cast<unsigned>((a.r + rb - 1) / rb), static_cast<unsigned>(a.ncols));
+    if (few)
+      return vec ? cudaLaunchKernelEx(&cfg, lora_shrink_kernel<AT, true, 2, 1>, a)
+                 : cudaLaunchKernelEx(&cfg, lora_shrink_kernel<AT, false, 2, 1>, a);
+    return vec ? cudaLaunchKernelEx(&cfg, lora_shrink_kernel<AT, true, 8, kLoraCols>, a)
+               : cudaLaunchKernelEx(&cfg, lora_shrink_kernel<AT, false, 8, kLoraCols>, a);
   }
-  cfg.gridDim = dim3(static_cast<unsigned>((a.M + kLoraThreads - 1) / kLoraThreads), static_cast<unsigned>(a.ncols));
-  const bool vec = a.r % 8 == 0 && al16(a.B);
+  cfg.blockDim = dim3(kExpandRows);
+  cfg.gridDim = dim3(static_cast<unsigned>((a.M + kExpandRows - 1) / kExpandRows), static_cast<unsigned>(a.ncols));
+  const bool vec = a.r * (AT == WT_F16 ? 2 : 4) % 16 == 0 && al16(a.B);
   return vec ? cudaLaunchKernelEx(&cfg, lora_expand_kernel<AT, true>, a)
              : cudaLaunchKernelEx(&cfg, lora_expand_kernel<AT, false>, a);
 }

@@ -10,11 +10,12 @@ __global__ void __launch_bounds__(kPackThreads) tile_pack_kernel(const __grid_co
   __shared__ float wmax[2 * kPackThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int tile = static_cast<int>(blockIdx.x), col = tile * 8 + threadIdx.x / kPackColumn;
+  // a CTA a column
+  const int col = static_cast<int>(blockIdx.x), tile = col / 8;
   const int first = tile * 8 / a.cols * a.cols;  // of the column group
   const int cp = min(8, min(a.cols, a.ncols - first));
-  pack_tile(col < a.ncols ? a.x + static_cast<int64_t>(col) * a.K : nullptr, a.gamma, a.eps, a.K, a.wtype, cp,
-            a.records + static_cast<int64_t>(blockIdx.x) * (a.K / 32) * record_bytes(a.cp), wmax);
+  pack_column(a.x + static_cast<int64_t>(col) * a.K, col % 8, threadIdx.x, kPackThreads, a.gamma, a.eps, a.K, a.wtype, cp,
+              a.records + static_cast<int64_t>(tile) * (a.K / 32) * record_bytes(a.cp), wmax);
 }
 
 // The last rows of a matrix whose rows are no whole 16-byte words and whose number is no
@@ -58,7 +59,7 @@ static int launch_lin_cols(const TileArgs& t, const LinArgs& a, cudaStream_t st,
 int launch_lin(const LinArgs& a, cudaStream_t st, bool pdl) {
   cudaLaunchAttribute attr;
   if (a.phase == LIN_PACK) {
-    const cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>((a.ncols + 7) / 8)), kPackThreads, st, pdl, &attr);
+    const cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(a.ncols)), kPackThreads, st, pdl, &attr);
     return cudaLaunchKernelEx(&cfg, tile_pack_kernel, a);
   }
   const int period = tile_period(a.row_bytes), main_rows = a.M / period * period;

@@ -153,15 +153,19 @@ __device__ __forceinline__ float finite_abs(float v) {
   return a <= 3.402823466e38f ? a : 0.0f;  // Inf and NaN do not set the scale
 }
 
-// A column tile's records, by a CTA of kPackThreads: 128 threads a column, one scale for the
-// whole column.  x: this thread's column (nullptr: none).  With gamma the column is first
-// normalised, x / sqrt(mean(x^2) + eps) gamma: gamma multiplies before packing, the root
-// enters through the stored scale.  wmax: 2 kPackThreads / 32 floats of shared memory.
+// Column c of a column tile's records, by `share` consecutive threads (a multiple of 32) of a
+// CTA of kPackThreads, thread i0 of them; one scale for the whole column.  x: the column
+// (nullptr: none).  With gamma the column is first normalised, x / sqrt(mean(x^2) + eps)
+// gamma: gamma multiplies before packing, the root enters through the stored scale.  Every
+// thread of the CTA takes part.  wmax: 2 kPackThreads / 32 floats of shared memory.
 constexpr int kPackThreads = 1024;
-constexpr int kPackColumn = 128;
-__device__ inline void pack_tile(const float* x, const float* gamma, float eps, int K, int fmt, int cp, uint8_t* base,
-                                 float* wmax) {
-  const int c = threadIdx.x / kPackColumn, i0 = threadIdx.x % kPackColumn, lane = threadIdx.x & 31;
+// Threads of a column when `columns` (1..8) share a CTA.
+__device__ __forceinline__ int pack_share(int columns) {
+  return columns <= 1 ? 1024 : columns <= 2 ? 512 : columns <= 4 ? 256 : 128;
+}
+__device__ inline void pack_column(const float* x, int c, int i0, int share, const float* gamma, float eps, int K, int fmt,
+                                   int cp, uint8_t* base, float* wmax) {
+  const int lane = threadIdx.x & 31;
   const int n4 = K / 4, order = pack_order(fmt);
   const float high = pack_high(fmt), sumf = pack_sum(fmt);
   const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(gamma)) & 15u) == 0;
@@ -189,10 +193,10 @@ __device__ inline void pack_tile(const float* x, const float* gamma, float eps, 
   float4 keep[kKeep];
   float m = 0.0f;
 #pragma unroll
-  for (int j = 0; j < kKeep; ++j) keep[j] = load(i0 + kPackColumn * j, true);
+  for (int j = 0; j < kKeep; ++j) keep[j] = load(i0 + share * j, true);
 #pragma unroll
   for (int j = 0; j < kKeep; ++j) m = fmaxf(m, top(keep[j]));
-  for (int i = i0 + kPackColumn * kKeep; i < n4; i += kPackColumn) m = fmaxf(m, top(load(i, true)));
+  for (int i = i0 + share * kKeep; i < n4; i += share) m = fmaxf(m, top(load(i, true)));
   m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -202,10 +206,10 @@ __device__ inline void pack_tile(const float* x, const float* gamma, float eps, 
   }
   __syncthreads();
   ss = 0.0f;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    m = fmaxf(m, wmax[4 * c + q]);
-    ss += wmax[kPackThreads / 32 + 4 * c + q];
+  const int w0 = (threadIdx.x - i0) >> 5;  // the column's first warp
+  for (int q = 0; q < share / 32; ++q) {
+    m = fmaxf(m, wmax[w0 + q]);
+    ss += wmax[kPackThreads / 32 + w0 + q];
   }
   const float sc = pack_scale(m);
   float inv = pow2_inverse(sc);
@@ -226,8 +230,9 @@ __device__ inline void pack_tile(const float* x, const float* gamma, float eps, 
     }
   };
 #pragma unroll
-  for (int j = 0; j < kKeep; ++j) put(i0 + kPackColumn * j, keep[j]);
-  for (int b = kPackColumn * kKeep; b < n4; b += kPackColumn) put(b + i0, load(b + i0, false));
+  for (int j = 0; j < kKeep; ++j) put(i0 + share * j, keep[j]);
+  for (int b = share * kKeep; b < n4; b += share) put(b + i0, load(b + i0, false));
+  __syncthreads();  // wmax may be used again
 }
 
 // ------------------------------------------------------------------ A fragments
@@ -393,6 +398,7 @@ struct TileArgs {
   int period;
   const int4* groups;       // {matrix, first entry, columns, first column tile}
   const int32_t* n_groups;
+  int max_groups;           // entries `groups` has room for
   const int32_t* slots;     // slot of each entry
   const uint8_t* records;   // [column tile][K / 32] records of x
   int cp;                   // most columns stored per column tile
@@ -617,11 +623,15 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(WT, NT))
   pdl_trigger();
   pdl_wait();
   const int tiles = (a.rows + kOutRows - 1) / kOutRows;
+  // (a call of few groups: the list is fetched beside its length, not after it)
+  if (MODE != TILE_LIN)
+    for (int i = threadIdx.x; i < min(kTileMaxGroups, a.max_groups); i += kTileThreads) groups[i] = a.groups[i];
   const int n_groups = MODE == TILE_LIN ? (a.ncols + a.group_cols - 1) / a.group_cols : *a.n_groups;
   const int64_t items = static_cast<int64_t>(n_groups) * tiles;
   const int64_t lo = items * blockIdx.x / gridDim.x, hi = items * (blockIdx.x + 1) / gridDim.x;
-  const int g_lo = static_cast<int>(lo / tiles);
-  if (lo < hi)
+  const bool all = MODE != TILE_LIN && n_groups <= kTileMaxGroups;
+  const int g_lo = static_cast<int>(lo / tiles), g_at = all ? g_lo : 0;  // the first group's place in `groups`
+  if (lo < hi && !all)
     for (int i = threadIdx.x; i <= static_cast<int>((hi - 1) / tiles) - g_lo; i += kTileThreads)
       groups[i] = MODE == TILE_LIN ? make_int4(0, 0, min(a.group_cols, a.ncols - (g_lo + i) * a.group_cols),
                                                (g_lo + i) * ((a.group_cols + 7) / 8))
@@ -635,12 +645,12 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(WT, NT))
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int slot = 0, issued = 0, gi = 0, tile = tile_lo, xgroups = 0;
+      int slot = 0, issued = 0, gi = 0, tile = tile_lo, xgroups = 0;  // gi: groups since the first
       uint32_t phase = 1u;
       bool ok = true;
       const uint32_t wlen = 32u * static_cast<uint32_t>(tile_plain(WT) ? tile_seg<WT>() : tile_pitch<WT>(a.period));
       for (int it = 0; it < n_items && ok; ++it) {
-        const int4 g = groups[gi];
+        const int4 g = groups[g_at + gi];
         const int row0 = tile * kOutRows;
         const int halves = MODE == TILE_GLU || row0 + 32 < a.rows ? 2 : 1;
         const int nt = (g.z + 7) / 8;
@@ -732,7 +742,7 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(WT, NT))
     uint32_t phase = 0;
     bool ok = true;
     for (int it = 0; it < n_items; ++it) {
-      const int4 g = groups[gi];
+      const int4 g = groups[g_at + gi];
       const int row0 = tile * kOutRows;
       const int ncol = g.z;
       {
