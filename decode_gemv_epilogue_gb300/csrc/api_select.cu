@@ -67,7 +67,7 @@ static int plan_route(const float* logits, int64_t T, int64_t E, const gf_route_
 
 // ------------------------------------------------------------------ experts
 struct ExpertsLayout {
-  int64_t slots, groups, n_groups, xrec, hrec, y, max_tiles, bytes;
+  int64_t slots, groups, n_groups, places, xrec, hrec, y, max_tiles, bytes;
 };
 
 static int experts_layout(int64_t E, int64_t T, int64_t k, int64_t M, int64_t K, ExpertsLayout& l) {
@@ -87,6 +87,7 @@ static int experts_layout(int64_t E, int64_t T, int64_t k, int64_t M, int64_t K,
   l.n_groups = take(16);
   l.slots = take(S * 4);
   l.groups = take(S * 16);
+  l.places = take(S * 8);
   l.xrec = take(l.max_tiles * K32 * record_bytes(static_cast<int>(cp)));
   l.hrec = take(std::max(l.max_tiles * M32 * record_bytes(static_cast<int>(cp)), S * M * 4));
   l.y = take(S * K * 4);
@@ -167,6 +168,7 @@ static int plan_experts(const gf_experts* ex, const float* x, int64_t T, const f
   a.n_groups = reinterpret_cast<int32_t*>(ws + l.n_groups);
   a.slots = reinterpret_cast<int32_t*>(ws + l.slots);
   a.groups = reinterpret_cast<int4*>(ws + l.groups);
+  a.places = reinterpret_cast<int2*>(ws + l.places);
   a.xrec = ws + l.xrec;
   a.hrec = ws + l.hrec;
   a.cp = static_cast<int>(std::min<int64_t>(8, T));

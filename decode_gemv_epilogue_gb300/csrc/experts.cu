@@ -81,7 +81,10 @@ __global__ void __launch_bounds__(256) experts_combine_kernel(const __grid_const
 constexpr int kPrepThreads = kPackThreads;
 constexpr int kPrepMaxIter = kExpMaxTokens * kRouteMaxTopK / kPrepThreads;  // 32-slot steps of a warp
 
-static int prep_smem(int E) { return 32 * E * 2 + E * 4; }
+constexpr int kPrepFused = 256;        // slots
+constexpr int kPackSlotThreads = 256;
+
+static int prep_smem(int E) { return 32 * E * 2 + 3 * E * 4; }
 
 // The column tile of a prep CTA: up to eight slots of one expert.
 struct PrepTile {
@@ -91,15 +94,19 @@ struct PrepTile {
 
 // The slots of each expert in slot order: a counting sort whose counts are kept per warp
 // (each warp owns a run of consecutive slots) and ranked within a 32-slot step by matching.
-// Every CTA of the launch makes the whole list (a few microseconds, less than another launch)
-// and packs its own column tiles; the first one also writes the list and the column groups.
+// PACK: every CTA of the launch makes the whole list (a few microseconds, less than another
+// launch) and packs its own column tiles; the first one also writes the list and the column
+// groups.  Otherwise one CTA makes the list, and a launch of a CTA per slot packs: a list of
+// more than kPrepFused slots takes longer than that launch (2048 slots: 23 us against 11).
+template <bool PACK>
 __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(const __grid_constant__ ExpertsArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ PrepTile pt;
   __shared__ uint32_t wsum[32];
   __shared__ float wmax[2 * kPrepThreads / 32];
   uint32_t* offs = reinterpret_cast<uint32_t*>(smem);
-  uint16_t* cnt = reinterpret_cast<uint16_t*>(offs + a.E);
+  uint32_t *first_tile = offs + a.E, *totals = first_tile + a.E;
+  uint16_t* cnt = reinterpret_cast<uint16_t*>(totals + a.E);
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -173,7 +180,11 @@ __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(const __grid
   const uint32_t ex0 = scan(total | (nt << 16), all);
   const uint32_t off = ex0 & 0xffffu, t0 = ex0 >> 16;
   const int tiles = static_cast<int>(all >> 16);
-  if (e < a.E) offs[e] = off;
+  if (e < a.E) {
+    offs[e] = off;
+    first_tile[e] = t0;
+    totals[e] = total;
+  }
   if (blockIdx.x == 0) {
     uint32_t groups;
     const uint32_t g0 = scan(ng, groups);
@@ -191,8 +202,19 @@ __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(const __grid
     pos[j] = -1;
     if (ex[j] >= 0) {
       pos[j] = static_cast<int>(offs[ex[j]]) + mine[ex[j]] + rank[j];
-      if (blockIdx.x == 0) a.slots[pos[j]] = w * run + 32 * j + lane;
+      const int s = w * run + 32 * j + lane;
+      if (blockIdx.x == 0) a.slots[pos[j]] = s;
+      if constexpr (!PACK) {
+        const uint32_t f = static_cast<uint32_t>(pos[j]) - offs[ex[j]], group = f / (gt * 8u) * (gt * 8u);
+        a.places[s] = make_int2(static_cast<int>(first_tile[ex[j]] + f / 8u),
+                                static_cast<int>((f % 8u) | (min(8u, totals[ex[j]] - group) << 8)));
+      }
     }
+  }
+  if constexpr (!PACK) {
+    for (int s = threadIdx.x; s < S; s += kPrepThreads)  // slots without an expert
+      if (static_cast<uint32_t>(a.ids[s]) >= static_cast<uint32_t>(a.E)) a.places[s] = make_int2(-1, 0);
+    return;
   }
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     if (static_cast<uint32_t>(tile) >= t0 && static_cast<uint32_t>(tile) < t0 + nt) {  // one thread's expert
@@ -211,6 +233,17 @@ __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(const __grid
     pack_column(x, c, threadIdx.x % share, share, nullptr, 0.0f, a.K, a.wtype, pt.cp,
                 a.xrec + static_cast<int64_t>(tile) * (a.K / 32) * record_bytes(a.cp), wmax);
   }
+}
+
+__global__ void __launch_bounds__(kPackSlotThreads) experts_pack_kernel(const __grid_constant__ ExpertsArgs a) {
+  __shared__ float wmax[2 * kPackThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int s = blockIdx.x;
+  const int2 p = a.places[s];  // {column tile, column | columns stored << 8}
+  if (p.x < 0) return;
+  pack_column(a.x + static_cast<int64_t>(s / a.k) * a.K, p.y & 255, threadIdx.x, kPackSlotThreads, nullptr, 0.0f, a.K,
+              a.wtype, p.y >> 8, a.xrec + static_cast<int64_t>(p.x) * (a.K / 32) * record_bytes(a.cp), wmax);
 }
 
 // ------------------------------------------------------------------ tiled products
@@ -280,18 +313,26 @@ int launch_experts(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
   cudaLaunchAttribute attr;
   switch (a.phase) {
     case EXP_PREP: {
-      static int configured[64] = {0};
+      const bool fused = a.T * a.k <= kPrepFused;
+      auto kern = fused ? experts_prep_kernel<true> : experts_prep_kernel<false>;
+      static int configured[64][2] = {};
       int dev = 0;
       cudaGetDevice(&dev);
       const int smem = prep_smem(a.E);
-      if (smem > 48 * 1024 && dev < 64 && configured[dev] < smem) {
-        const cudaError_t e = cudaFuncSetAttribute(experts_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (smem > 48 * 1024 && dev < 64 && configured[dev][fused] < smem) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        configured[dev] = smem;
+        configured[dev][fused] = smem;
       }
-      cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(std::min(a.max_tiles, 2 * a.sm_count))), kPrepThreads, st, pdl, &attr);
+      cudaLaunchConfig_t cfg =
+          config(dim3(static_cast<unsigned>(fused ? std::min(a.max_tiles, a.sm_count) : 1)), kPrepThreads, st, pdl, &attr);
       cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-      return cudaLaunchKernelEx(&cfg, experts_prep_kernel, a);
+      const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+      if (e != cudaSuccess || fused) return e;
+      cudaLaunchAttribute attr2;
+      const cudaLaunchConfig_t cfg2 =
+          config(dim3(static_cast<unsigned>(a.T * a.k)), kPackSlotThreads, st, true, &attr2);
+      return cudaLaunchKernelEx(&cfg2, experts_pack_kernel, a);
     }
     case EXP_GLU: return launch_tiles<TILE_GLU>(a, st, pdl);
     case EXP_DOWN: return launch_tiles<TILE_DOWN>(a, st, pdl);

@@ -263,6 +263,7 @@ struct ExpertsArgs {
   int32_t* slots;       // [T k] slots by expert, in slot order
   int4* groups;         // {expert, first entry, columns, first column tile} of each column group
   int32_t* n_groups;
+  int2* places;         // [T k] {column tile, column | columns stored << 8} of each slot, or {-1, 0}
   uint8_t* xrec;        // [column tile][K / 32] records of packed x (see tile_mma.cuh)
   uint8_t* hrec;        // the same of the gated values, or [T k][M] float32 (generic)
   float* y;             // [T k][K]

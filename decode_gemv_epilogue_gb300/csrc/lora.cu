@@ -16,7 +16,7 @@
 // thread holding the sums of its rows and up to four columns, so that one round of
 // independent 16-byte loads covers 2048 elements and a decode-sized K is a latency of one or
 // two rounds.  Two rows a CTA while that leaves SMs idle (16 rows of 4096 for one column: 6.1
-// -> 3.4 us against eight), eight once the columns fill them.  Sums: 32 bits, per thread in K
+// -> 3.4 us against eight), four once the columns fill them.  Sums: 32 bits, per thread in K
 // order, then a shuffle tree, then the warps in order.
 // Expand: a CTA takes 128 rows of B, 64 (f32: 32) values of each at a time through shared
 // memory, a thread per row walks them for four columns at a time.
@@ -294,13 +294,13 @@ static cudaError_t launch_lora_t(const LoraArgs& a, cudaStream_t st, bool pdl) {
   if (a.phase == LORA_SHRINK) {
     const bool vec = a.K % 8 == 0 && al16(a.A) && al16(a.x) && al16(a.gamma);
     const bool few = a.ncols * ((a.r + 7) / 8) <= 32;  // two rows a CTA, a column at a time
-    const int rb = few ? 2 : 8;
+    const int rb = few ? 2 : 4;
     cfg.gridDim = dim3(static_cast<unsigned>((a.r + rb - 1) / rb), static_cast<unsigned>(a.ncols));
     if (few)
       return vec ? cudaLaunchKernelEx(&cfg, lora_shrink_kernel<AT, true, 2, 1>, a)
                  : cudaLaunchKernelEx(&cfg, lora_shrink_kernel<AT, false, 2, 1>, a);
-    return vec ? cudaLaunchKernelEx(&cfg, lora_shrink_kernel<AT, true, 8, kLoraCols>, a)
-               : cudaLaunchKernelEx(&cfg, lora_shrink_kernel<AT, false, 8, kLoraCols>, a);
+    return vec ? cudaLaunchKernelEx(&cfg, lora_shrink_kernel<AT, true, 4, kLoraCols>, a)
+               : cudaLaunchKernelEx(&cfg, lora_shrink_kernel<AT, false, 4, kLoraCols>, a);
   }
   cfg.blockDim = dim3(kExpandRows);
   cfg.gridDim = dim3(static_cast<unsigned>((a.M + kExpandRows - 1) / kExpandRows), static_cast<unsigned>(a.ncols));
