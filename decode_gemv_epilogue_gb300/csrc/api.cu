@@ -915,10 +915,19 @@ static int64_t lin_record_bytes(int64_t ncols, int64_t K) {
 }
 
 // The tensor-core projection takes batches of any format but F16 (whose batches have a
-// tensor-core kernel already), K in whole blocks.  Measured: see tile_lin.cu.
+// tensor-core kernel already), K in whole blocks, where it beats blocks of eight columns on
+// the streamed kernel: from 17 columns, and in the block formats from three where the product
+// is large enough to hide one more launch.  Measured with 16-row adapters, us, tiles and
+// streamed: Q4_0 512 x 1024, 8 columns 18 / 12, 17 21 / 23, 64 28 / 48; 4096 x 4096, 6 columns
+// 29 / 27, 8 29 / 29, 64 57 / 160; 14336 x 4096, 2 columns 27 / 27, 4 29 / 37, 8 29 / 62; Q4_K
+// 35 / 106; F32 512 x 1024, 32 columns 29 / 27, 64 33 / 43; 14336 x 4096, 8 76 / 60, 32 122 / 209.
 static bool lin_takes(const Call& c) {
-  return c.wtype != GF_F16 && c.ncols >= 2 && c.K >= 32 && c.K % 32 == 0 && c.K <= (1 << 20) && c.M >= 8 &&
-         aligned(c.W, 16) && !(c.flags & GF_FLAG_NO_TENSOR_CORES);
+  if (c.wtype == GF_F16 || c.K < 32 || c.K % 32 != 0 || c.K > (1 << 20) || c.M < 8 || !aligned(c.W, 16) ||
+      (c.flags & GF_FLAG_NO_TENSOR_CORES))
+    return false;
+  const int64_t work = c.M * c.K * c.ncols;
+  if (c.wtype == GF_F32) return c.ncols > 16 && work >= (1LL << 25);
+  return c.ncols > 16 || (c.ncols >= 3 && work >= (1LL << 27));
 }
 
 int64_t gf_lora_workspace(int64_t ncols, int64_t M, int64_t K, int64_t rank, int64_t n) {
@@ -1027,10 +1036,10 @@ static int plan_lora(const void* W, int wtype, const float* x, int64_t M, int64_
     q.K = static_cast<int>(K);
     q.row_bytes = static_cast<int>(row_bytes_of(wtype, K));
     q.ncols = static_cast<int>(c.ncols);
-    q.cols = c.ncols <= 8 ? static_cast<int>(c.ncols) : 16;
     q.cp = static_cast<int>(std::min<int64_t>(8, c.ncols));
     q.sm_count = lim.sm_count;
     q.smem_optin = lim.smem_optin;
+    q.cols = lin_cols(wtype, M, K, q.row_bytes, q.ncols, q.sm_count);
     q.phase = LIN_PACK;
     LaunchRec& r = recs[(*n)++];
     r.kind = REC_LIN;

@@ -105,17 +105,23 @@ static bool experts_tiled(const gf_experts* x) {
          aligned_to(x->W_gate, 16) && aligned_to(x->W_up, 16) && aligned_to(x->W_down, 16);
 }
 
-// Columns of a group: matrix tiles are eight columns wide, and a group of more than an
-// expert's tokens costs registers and shared memory for nothing.
-static int experts_cols(const gf_experts* x, int64_t T) {
+// Columns of a group.  Rows without codes are read once per group and decode for nothing:
+// as many column tiles as the experts' mean fills (256 tokens on 8 F16 experts, 8 columns
+// each: 374 us in groups of 8, 332 in groups of 16).  Block formats: groups of 16 on the wide
+// kernel where that is estimated to be faster, else of 8.  One format of each kind: 8.
+static int experts_cols(const gf_experts* x, int64_t T, int sms) {
   if (T < 8) return static_cast<int>(T);
   const double slots = static_cast<double>(T) * x->top_k;
-  const double mean = slots / std::min<double>(static_cast<double>(x->E), slots);
-  if (mean <= 5.0) return 8;
-  // more than 16 only in the K-sharing kernel
-  const bool wide = wide_takes(x->wtype, static_cast<int>(row_bytes_of(x->wtype, x->K))) ||
-                    wide_takes(x->wtype_down, static_cast<int>(row_bytes_of(x->wtype_down, x->M)));
-  return mean <= 10.0 || wide ? 16 : 24;
+  const double used = std::min<double>(static_cast<double>(x->E), slots), mean = slots / used;
+  const int wg = x->wtype, wd = x->wtype_down;
+  if (tile_plain(wg) && tile_plain(wd)) return mean <= 5.0 ? 8 : mean <= 10.0 ? 16 : 24;
+  if (!wide_takes(wg, static_cast<int>(row_bytes_of(wg, x->K))) || !wide_takes(wd, static_cast<int>(row_bytes_of(wd, x->M))))
+    return 8;
+  // groups an expert's slots make, their number spread like a Poisson one: half a group is lost
+  const double g8 = used * std::max(1.0, mean / 8.0 + 0.5), g16 = used * std::max(1.0, mean / 16.0 + 0.5);
+  const double narrow = tile_cost(x->M, x->K, 32, g8, sms) + tile_cost(x->K, x->M, kTileRows, g8, sms);
+  const double wide = wide_cost(wg, x->M, x->K, wide_rows(wg) / 2, g16, sms) + wide_cost(wd, x->K, x->M, wide_rows(wd), g16, sms);
+  return mean > 5.0 && wide < narrow ? 16 : 8;
 }
 
 constexpr int kExpMaxRecs = 4;
@@ -174,7 +180,7 @@ static int plan_experts(const gf_experts* ex, const float* x, int64_t T, const f
   a.cp = static_cast<int>(std::min<int64_t>(8, T));
   a.max_tiles = static_cast<int>(l.max_tiles);
   a.y = reinterpret_cast<float*>(ws + l.y);
-  a.cols = experts_cols(ex, T);
+  a.cols = experts_cols(ex, T, lim.sm_count);
   a.out_format = wd;
   a.sm_count = lim.sm_count;
   a.smem_optin = lim.smem_optin;

@@ -250,13 +250,13 @@ __global__ void __launch_bounds__(kPackSlotThreads) experts_pack_kernel(const __
 template <int WT, int MODE, bool PER1>
 static int launch_tile_cols(const TileArgs& t, const ExpertsArgs& a, cudaStream_t st, bool pdl) {
   const TileOperands o = {a.W, a.W2, static_cast<int64_t>(a.E) * t.rows, a.max_tiles, a.sm_count, a.smem_optin};
-  if (a.cols <= 8) return launch_tile<WT, MODE, 1, PER1>(t, o, st, pdl);
-  if constexpr (PER1 && !tile_plain(WT)) {
-    return launch_wide<WT, MODE>(t, o, st, pdl);
-  } else {
-    if (a.cols <= 16) return launch_tile<WT, MODE, 2, PER1>(t, o, st, pdl);
-    return launch_tile<WT, MODE, 3, PER1>(t, o, st, pdl);
+  if constexpr (tile_plain(WT)) {
+    if (a.cols > 16) return launch_tile<WT, MODE, 3, PER1>(t, o, st, pdl);
+    if (a.cols > 8) return launch_tile<WT, MODE, 2, PER1>(t, o, st, pdl);
+  } else if constexpr (PER1) {
+    if (a.cols > 8) return launch_wide<WT, MODE>(t, o, st, pdl);
   }
+  return launch_tile<WT, MODE, 1, PER1>(t, o, st, pdl);
 }
 
 template <int MODE>

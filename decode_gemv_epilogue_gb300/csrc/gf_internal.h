@@ -309,6 +309,8 @@ struct LinArgs {
   int sm_count, smem_optin;
 };
 int launch_lin(const LinArgs& a, cudaStream_t st, bool pdl);
+// Columns of a group.
+int lin_cols(int wtype, int64_t M, int64_t K, int row_bytes, int ncols, int sms);
 
 // One kernel launch with every argument resolved: what a call plans, and what a
 // prepared call keeps (gf_prepare) so that launching it does no planning at all.

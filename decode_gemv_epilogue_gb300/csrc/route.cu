@@ -15,9 +15,11 @@
 // Without a bias and without groups the key is the logit itself (both scores grow with it),
 // exact.  Otherwise the keys are computed in 32 bits, and a warp that finds two neighbours
 // of its choice within the error bound of that arithmetic (and not made of the same logit
-// and bias) computes its row again in 64 bits.  Roughly one row in a hundred to a thousand
-// does; computing every row in 64 bits would cost an exp of ~30 double operations per
-// expert at a rate of two per clock and SM.
+// and bias) computes the keys that can matter again in 64 bits.  Roughly one row in a hundred
+// to a thousand does; an exponential and a division in 64 bits take a warp some 1000 cycles
+// at this machine's two double operations per clock and SM, so a row is not computed so
+// throughout (a batch with one such row, 256 experts in groups: 28 us for all its keys, 13 for
+// those that matter).
 #include <cfloat>
 #include <cmath>
 
@@ -50,11 +52,29 @@ __device__ __forceinline__ T warp_sum(T v) {
   return v;
 }
 
+// 64-bit keys as integers in the same order: comparing doubles costs a trip through the few
+// double units each.
+__device__ __forceinline__ long long ordered64(double v) {
+  const long long u = __double_as_longlong(v + 0.0);
+  return u ^ ((u >> 63) & 0x7fffffffffffffffLL);
+}
+__device__ __forceinline__ double from_ordered64(long long k) {
+  return __longlong_as_double(k ^ ((k >> 63) & 0x7fffffffffffffffLL));
+}
+constexpr long long kLowest64 = -0x7ff0000000000001LL;  // of -inf
+
+__device__ __forceinline__ float lowest(float) { return -INFINITY; }
+__device__ __forceinline__ long long lowest(long long) { return kLowest64; }
+__device__ __forceinline__ float add_keys(float a, float b) { return a + b; }
+__device__ __forceinline__ long long add_keys(long long a, long long b) {
+  return ordered64(from_ordered64(a) + from_ordered64(b));
+}
+
 // The best key of a warp in 64 bits: largest, ties to the lowest index.
-__device__ __forceinline__ void warp_best(double& key, int& e) {
+__device__ __forceinline__ void warp_best(long long& key, int& e) {
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) {
-    const double k2 = __shfl_xor_sync(0xffffffffu, key, o);
+    const long long k2 = __shfl_xor_sync(0xffffffffu, key, o);
     const int e2 = __shfl_xor_sync(0xffffffffu, e, o);
     if (k2 > key || (k2 == key && e2 < e)) {
       key = k2;
@@ -75,16 +95,16 @@ __device__ __forceinline__ void warp_top2(T& a, T& b) {
   }
 }
 
-// Groups that stay, as a bit mask, from the keys kv (value type T, -inf: not choosable).
-// ambiguous: the last kept and the first dropped score are within tol.
+// Groups that stay, as a bit mask, from the keys kv (float or ordered64; the lowest: not
+// choosable).  unsure (may be NULL; floats): the last kept and the first dropped score are
+// within tol.
 template <int VPL, class T>
-__device__ __forceinline__ uint32_t choose_groups(const RouteArgs& a, const T (&kv)[VPL], int lane, T tol,
-                                                  bool& ambiguous) {
-  const T ninf = -static_cast<T>(INFINITY);
+__device__ __forceinline__ uint32_t choose_groups(const RouteArgs& a, const T (&kv)[VPL], int lane, float tol, bool* unsure) {
+  const T low = lowest(T());
   const int gs = a.E / a.n_group;
-  T mine = ninf;
+  T mine = low;
   for (int g = 0; g < a.n_group; ++g) {
-    T t1 = ninf, t2 = ninf;
+    T t1 = low, t2 = low;
     const int lo = g * gs, hi = lo + gs;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
@@ -96,7 +116,7 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteArgs& a, const T (&
       }
     }
     warp_top2(t1, t2);
-    const T s = (a.group_top == 2 && t2 > ninf) ? t1 + t2 : t1;
+    const T s = (a.group_top == 2 && t2 > low) ? add_keys(t1, t2) : t1;
     if (lane == g) mine = s;
   }
   int rank = 0;
@@ -106,59 +126,87 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteArgs& a, const T (&
   }
   const bool in = lane < a.n_group;
   const uint32_t kept = __ballot_sync(0xffffffffu, in && rank < a.topk_group);
-  const uint32_t last = __ballot_sync(0xffffffffu, in && rank == a.topk_group - 1);
-  const uint32_t next = __ballot_sync(0xffffffffu, in && rank == a.topk_group);
-  if (next) {
-    const T v = __shfl_sync(0xffffffffu, mine, __ffs(last) - 1), w = __shfl_sync(0xffffffffu, mine, __ffs(next) - 1);
-    ambiguous = w > ninf && v - w <= tol;  // nothing in doubt where the next group is empty
+  if (unsure) {
+    const uint32_t last = __ballot_sync(0xffffffffu, in && rank == a.topk_group - 1);
+    const uint32_t next = __ballot_sync(0xffffffffu, in && rank == a.topk_group);
+    if (next) {
+      const T v = __shfl_sync(0xffffffffu, mine, __ffs(last) - 1), w = __shfl_sync(0xffffffffu, mine, __ffs(next) - 1);
+      // nothing in doubt where the next group is empty
+      *unsure = w > low && static_cast<float>(v - w) <= tol;
+    }
   }
   return kept;
 }
 
-// The row once more in 64 bits.  Returns the expert that lane j takes in round j.
+// Keys in 64 bits, as ordered64, of the experts in `need` (bit i: expert lane + 32 i); the
+// others get the lowest.  Each lane takes its next needed expert in each round: a few rounds,
+// where computing all of them would take VPL.
 template <int VPL>
-__device__ __noinline__ int route_row_f64(const RouteArgs& a, const float (&l)[VPL], int lane) {
-  const double ninf = -static_cast<double>(INFINITY);
-  double key[VPL];
-  if (a.sigmoid) {
+__device__ __forceinline__ void exact_keys(const RouteArgs& a, const float (&l)[VPL], int lane, uint32_t need, float m,
+                                           double z, long long (&key)[VPL]) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = 1.0 / (1.0 + exp(-static_cast<double>(l[i])));
-  } else {
-    float m = -INFINITY;
+  for (int i = 0; i < VPL; ++i) key[i] = kLowest64;
+  while (__any_sync(0xffffffffu, need != 0u)) {
+    const int at = __ffs(need) - 1;
+    need &= need - 1u;
+    float v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) m = fmaxf(m, l[i]);
-    m = warp_max(m);
-    double z = 0.0;
+    for (int i = 0; i < VPL; ++i)
+      if (i == at) v = l[i];
+    double k = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(v)))
+                         : exp(static_cast<double>(v) - static_cast<double>(m)) / z;
+    if (a.bias && at >= 0) k += static_cast<double>(a.bias[lane + 32 * at]);
+    const long long o = ordered64(k);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      key[i] = l[i] > -INFINITY ? exp(static_cast<double>(l[i]) - static_cast<double>(m)) : 0.0;
-      z += key[i];
-    }
-    z = warp_sum(z);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] /= z;
+    for (int i = 0; i < VPL; ++i)
+      if (i == at) key[i] = o;
   }
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 32 * i;
-    if (!(l[i] > -INFINITY)) key[i] = ninf;
-    else if (a.bias) key[i] += static_cast<double>(a.bias[e]);
-    if (!(key[i] == key[i])) key[i] = ninf;
-  }
-  if (a.n_group > 1) {
-    bool unused = false;
-    const uint32_t kept = choose_groups<VPL, double>(a, key, lane, 0.0, unused);
-    const int gs = a.E / a.n_group;
+}
+
+// The row's groups once more in 64 bits.  s: the 32-bit keys, the lowest where not choosable.
+template <int VPL>
+__device__ __noinline__ uint32_t exact_groups(const RouteArgs& a, const float (&l)[VPL], const float (&s)[VPL], int lane,
+                                              float tol, float m, double z) {
+  // all that can be among a group's two best
+  const int gs = a.E / a.n_group;
+  uint32_t need = 0;
+  for (int g = 0; g < a.n_group; ++g) {
+    float t1 = -INFINITY, t2 = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = lane + 32 * i;
-      if (!a.bias && key[i] > ninf) key[i] = static_cast<double>(l[i]);  // the order of the logits
-      if (e < a.E && !((kept >> (e / gs)) & 1u)) key[i] = ninf;
+      if (e >= g * gs && e < (g + 1) * gs) {
+        t2 = s[i] > t1 ? t1 : fmaxf(s[i], t2);
+        t1 = fmaxf(s[i], t1);
+      }
+    }
+    warp_top2(t1, t2);
+    const float edge = (a.group_top == 2 ? t2 : t1) - tol;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane + 32 * i;
+      if (e >= g * gs && e < (g + 1) * gs && s[i] > -INFINITY && !(s[i] < edge)) need |= 1u << i;
     }
   }
+  long long key[VPL];
+  exact_keys<VPL>(a, l, lane, need, m, z, key);
+  return choose_groups<VPL, long long>(a, key, lane, 0.0f, nullptr);
+}
+
+// The row's choice once more in 64 bits, among the experts whose 32-bit keys s reach `edge`.
+// Returns the expert that lane j takes in round j.
+template <int VPL>
+__device__ __noinline__ int exact_choice(const RouteArgs& a, const float (&l)[VPL], const float (&s)[VPL], int lane,
+                                         float edge, float m, double z) {
+  uint32_t need = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (s[i] > -INFINITY && !(s[i] < edge)) need |= 1u << i;
+  long long key[VPL];
+  exact_keys<VPL>(a, l, lane, need, m, z, key);
   int mine = -1;
   for (int j = 0; j < a.k; ++j) {
-    double bk = ninf;
+    long long bk = kLowest64;
     int be = 0x7fffffff;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
@@ -167,13 +215,23 @@ __device__ __noinline__ int route_row_f64(const RouteArgs& a, const float (&l)[V
         be = lane + 32 * i;
       }
     warp_best(bk, be);
-    if (!(bk > ninf)) break;
+    if (bk <= kLowest64) break;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (lane + 32 * i == be) key[i] = ninf;
+      if (lane + 32 * i == be) key[i] = kLowest64;
     if (lane == j) mine = be;
   }
   return mine;
+}
+
+// Sum of the row's exponentials in 64 bits (softmax).
+template <int VPL>
+__device__ __noinline__ double exact_sum(const float (&l)[VPL], float m) {
+  double z = 0.0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (l[i] > -INFINITY) z += exp(static_cast<double>(l[i]) - static_cast<double>(m));
+  return warp_sum(z);
 }
 
 template <int VPL>
@@ -195,13 +253,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
   }
   float key[VPL], b[VPL];
   const bool plain_key = !a.bias && a.n_group <= 1;
-  bool redo = false;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = lane + 32 * i;
     b[i] = (a.bias && e < a.E) ? a.bias[e] : 0.0f;
     key[i] = l[i] + 0.0f;  // -0 and +0 tie
   }
+  float top = 0.0f, tol = 0.0f;  // largest logit; bound on the error of a 32-bit key
   if (!plain_key) {
     float s[VPL];
     if (a.sigmoid) {
@@ -211,11 +269,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
       float m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) m = fmaxf(m, l[i]);
-      m = warp_max(m);
+      top = warp_max(m);
       float z = 0.0f;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        s[i] = l[i] > -INFINITY ? expf(l[i] - m) : 0.0f;
+        s[i] = l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
         z += s[i];
       }
       const float inv = 1.0f / warp_sum(z);
@@ -223,19 +281,20 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
       for (int i = 0; i < VPL; ++i) s[i] *= inv;
     }
     // s + bias; without a bias the groups are chosen by s and the experts by the logit
+    float big = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       s[i] = l[i] > -INFINITY ? s[i] + b[i] : -INFINITY;
       if (!(s[i] == s[i])) s[i] = -INFINITY;  // a NaN bias: not choosable
       s[i] += 0.0f;
+      if (s[i] > -INFINITY && s[i] < INFINITY) big = fmaxf(big, fabsf(s[i]));
     }
+    tol = kKeyTolAbs + kKeyTolRel * warp_max(big);
     uint32_t kept = 0xffffffffu;
     if (a.n_group > 1) {
-      float big = 0.0f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (s[i] > -INFINITY) big = fmaxf(big, fabsf(s[i]));
-      kept = choose_groups<VPL, float>(a, s, lane, 4.0f * (kKeyTolAbs + kKeyTolRel * warp_max(big)), redo);
+      bool unsure = false;
+      kept = choose_groups<VPL, float>(a, s, lane, 4.0f * tol, &unsure);
+      if (unsure) kept = exact_groups<VPL>(a, l, s, lane, 2.0f * tol, top, a.sigmoid ? 1.0 : exact_sum<VPL>(l, top));
     }
     const int gs = a.E / a.n_group;
 #pragma unroll
@@ -248,13 +307,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
   // top_k rounds (one more where the keys are rounded, to see the first one left out)
   int mine = -1;
   float pk = 0.0f, pl = 0.0f, pb = 0.0f;  // the previous round's key, logit and bias
+  float last = -INFINITY;                 // the k-th key
+  uint32_t taken = 0;                     // of this lane's experts
+  bool unsure = false;
   const int rounds = a.bias ? a.k + 1 : a.k;
-  for (int j = 0; j < rounds && !redo; ++j) {
-    float bk = key[0], bl = l[0], bb = b[0];
+  for (int j = 0; j < rounds; ++j) {
+    float bk = -INFINITY, bl = 0.0f, bb = 0.0f;
     int bi = 0;
 #pragma unroll
-    for (int i = 1; i < VPL; ++i)
-      if (key[i] > bk) {
+    for (int i = 0; i < VPL; ++i)
+      if (!((taken >> i) & 1u) && key[i] > bk) {
         bk = key[i];
         bl = l[i];
         bb = b[i];
@@ -268,19 +330,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
     if (a.bias) {
       const float kk = __shfl_sync(0xffffffffu, bk, owner), kl = __shfl_sync(0xffffffffu, bl, owner),
                   kb = __shfl_sync(0xffffffffu, bb, owner);
-      if (j > 0 && !(kl == pl && kb == pb) &&
-          pk - kk <= 2.0f * (kKeyTolAbs + kKeyTolRel * fmaxf(fabsf(pk), fabsf(kk))))
-        redo = true;
+      if (j > 0 && !(kl == pl && kb == pb) && pk - kk <= 2.0f * tol) unsure = true;
       pk = kk;
       pl = kl;
       pb = kb;
+      if (j == a.k - 1) last = kk;
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (lane + 32 * i == static_cast<int>(e)) key[i] = -INFINITY;
+    if (lane == owner) taken |= 1u << (e >> 5);
     if (lane == j && j < a.k) mine = static_cast<int>(e);
   }
-  if (redo) mine = route_row_f64<VPL>(a, l, lane);
+  if (unsure) mine = exact_choice<VPL>(a, l, key, lane, last - 2.0f * tol, top, a.sigmoid ? 1.0 : exact_sum<VPL>(l, top));
 
   // weights of the chosen, one lane each.  Normalised ones are taken relative to the largest
   // of them, so that scores that would vanish in 32 bits still share the whole.

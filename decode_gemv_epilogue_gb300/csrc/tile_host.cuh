@@ -2,6 +2,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 
 #include "tile_wide.cuh"
 
@@ -84,8 +85,23 @@ int launch_tile(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
   return cudaLaunchKernelEx(&cfg, kern, m0, m1, t);
 }
 
-// Block formats whose rows are whole 16-byte words: groups of 9 to 16 columns.
-inline bool wide_takes(int wt, int row_bytes) { return wt != WT_F32 && wt != WT_F16 && row_bytes % 16 == 0; }
+// The wide kernel takes block formats whose rows are whole 16-byte words.
+inline bool wide_takes(int wt, int row_bytes) { return !tile_plain(wt) && row_bytes % 16 == 0; }
+
+// Time of a product of `rows` outputs and K columns over `groups` column groups, in units of
+// one K-sharing item: items run in waves of as many as fit the device (the K-sharing kernel's
+// many small ones level out, the wide kernel's few large ones do not).  A wide item takes as
+// long as 3.7 K-sharing ones of 64 rows and 8 columns, 2.6 for Q8_0 with half the rows
+// (measured at 14336 x 4096: 67, 46 and 18 us).
+inline double tile_cost(int64_t rows, int64_t K, int tile_rows, double groups, int sms) {
+  const double items = groups * static_cast<double>((rows + tile_rows - 1) / tile_rows);
+  return static_cast<double>(K) * std::max(1.0, items / (2.0 * sms));
+}
+inline double wide_cost(int wt, int64_t rows, int64_t K, int tile_rows, double groups, int sms) {
+  const double items = groups * static_cast<double>((rows + tile_rows - 1) / tile_rows);
+  return static_cast<double>(K) * (wt == WT_Q8_0 ? 2.6 : 3.7) * std::ceil(items / sms);
+}
+inline int wide_rows(int wt) { return wt == WT_Q8_0 ? 32 * wide_warps<WT_Q8_0>() : 32 * wide_warps<WT_Q4_0>(); }
 
 template <int WT, int MODE>
 int launch_wide(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
