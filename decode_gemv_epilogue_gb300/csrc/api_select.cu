@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <limits>
 
 #include "gemvfuse.h"
 #include "tile_host.cuh"
@@ -144,12 +145,15 @@ static int plan_experts(const gf_experts* ex, const float* x, int64_t T, const f
   const uintptr_t ag = wg == GF_F32 ? 4 : 2, adn = wd == GF_F32 ? 4 : 2;
   if (!aligned_to(ex->W_gate, ag) || !aligned_to(ex->W_up, ag) || !aligned_to(ex->W_down, adn) || !aligned_to(x, 4) ||
       !aligned_to(dst, 4) || !aligned_to(aux, 4) || !aligned_to(ex->ids, 4) || !aligned_to(ex->weights, 4) ||
-      !aligned_to(ex->workspace, 256))
+      !aligned_to(ex->workspace, 256) || !aligned_to(ex->rms_norm_weight, 4))
     return GF_ERR_ALIGN;
+  if (ex->rms_norm_weight && !(ex->rms_norm_eps >= 0.0f && ex->rms_norm_eps <= std::numeric_limits<float>::max()))
+    return GF_ERR_INVALID;
   const int64_t xb = T * ex->K * 4, sb = T * ex->top_k * 4;
   const int64_t gb = ex->E * ex->M * row_bytes_of(wg, ex->K), db = ex->E * ex->K * row_bytes_of(wd, ex->M);
-  const struct { const void* p; int64_t bytes; } in[6] = {{ex->W_gate, gb}, {ex->W_up, gb},       {ex->W_down, db},
-                                                          {x, xb},          {ex->ids, sb},        {ex->weights, sb}};
+  const struct { const void* p; int64_t bytes; } in[7] = {{ex->W_gate, gb}, {ex->W_up, gb},  {ex->W_down, db},
+                                                          {x, xb},          {ex->ids, sb},   {ex->weights, sb},
+                                                          {ex->rms_norm_weight, ex->K * 4}};
   for (const auto& i : in)
     if (ranges_overlap(dst, xb, i.p, i.bytes) || ranges_overlap(ex->workspace, l.bytes, i.p, i.bytes)) return GF_ERR_ALIAS;
   if (ranges_overlap(ex->workspace, l.bytes, dst, xb) || ranges_overlap(ex->workspace, l.bytes, aux, xb) ||
@@ -163,6 +167,8 @@ static int plan_experts(const gf_experts* ex, const float* x, int64_t T, const f
   a.x = x;
   a.ids = ex->ids;
   a.weights = ex->weights;
+  a.gamma = ex->rms_norm_weight;
+  a.eps = ex->rms_norm_eps;
   a.aux = aux;
   a.dst = dst;
   a.err = err;

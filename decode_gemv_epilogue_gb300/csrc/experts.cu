@@ -43,17 +43,31 @@ __global__ void __launch_bounds__(32 * kExpGenericWarps) experts_generic_kernel(
   const int64_t rb = expert_row_bytes<WT>(K), off = (static_cast<int64_t>(e) * rows + row) * rb;
   const float* x = GLU ? a.x + static_cast<int64_t>(s / a.k) * K
                        : reinterpret_cast<const float*>(a.hrec) + static_cast<int64_t>(s) * K;
-  float g = 0.0f, u = 0.0f;
+  float g = 0.0f, u = 0.0f, ss = 0.0f;
   for (int k = lane; k < K; k += 32) {
-    const float xv = x[k];
+    float xv = x[k];
+    if constexpr (GLU)
+      if (a.gamma) {
+        ss = fmaf(xv, xv, ss);
+        xv *= a.gamma[k];
+      }
     g = fmaf(decode_elem<WT>(a.W + off, k), xv, g);
     if constexpr (GLU) u = fmaf(decode_elem<WT>(a.W2 + off, k), xv, u);
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) {
     g += __shfl_xor_sync(0xffffffffu, g, o);
-    if constexpr (GLU) u += __shfl_xor_sync(0xffffffffu, u, o);
+    if constexpr (GLU) {
+      u += __shfl_xor_sync(0xffffffffu, u, o);
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    }
   }
+  if constexpr (GLU)
+    if (a.gamma) {
+      const float inv = 1.0f / sqrtf(ss / static_cast<float>(K) + a.eps);
+      g *= inv;
+      u *= inv;
+    }
   if (lane == 0) {
     if constexpr (GLU)
       reinterpret_cast<float*>(a.hrec)[static_cast<int64_t>(s) * a.M + row] = tail_silu(g) * u;
@@ -230,7 +244,7 @@ __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(const __grid
     __syncthreads();
     const int share = pack_share(pt.count), c = threadIdx.x / share;
     const float* x = c < pt.count ? a.x + static_cast<int64_t>(pt.slot[c] / a.k) * a.K : nullptr;
-    pack_column(x, c, threadIdx.x % share, share, nullptr, 0.0f, a.K, a.wtype, pt.cp,
+    pack_column(x, c, threadIdx.x % share, share, a.gamma, a.eps, a.K, a.wtype, pt.cp,
                 a.xrec + static_cast<int64_t>(tile) * (a.K / 32) * record_bytes(a.cp), wmax);
   }
 }
@@ -242,7 +256,7 @@ __global__ void __launch_bounds__(kPackSlotThreads) experts_pack_kernel(const __
   const int s = blockIdx.x;
   const int2 p = a.places[s];  // {column tile, column | columns stored << 8}
   if (p.x < 0) return;
-  pack_column(a.x + static_cast<int64_t>(s / a.k) * a.K, p.y & 255, threadIdx.x, kPackSlotThreads, nullptr, 0.0f, a.K,
+  pack_column(a.x + static_cast<int64_t>(s / a.k) * a.K, p.y & 255, threadIdx.x, kPackSlotThreads, a.gamma, a.eps, a.K,
               a.wtype, p.y >> 8, a.xrec + static_cast<int64_t>(p.x) * (a.K / 32) * record_bytes(a.cp), wmax);
 }
 

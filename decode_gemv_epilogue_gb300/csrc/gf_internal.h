@@ -251,6 +251,8 @@ struct ExpertsArgs {
   const float* x;
   const int32_t* ids;
   const float* weights;
+  const float* gamma;   // RMS normalisation of x (nullptr: none)
+  float eps;
   const float* aux;
   float* dst;
   unsigned* err;

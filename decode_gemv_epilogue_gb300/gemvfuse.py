@@ -92,7 +92,8 @@ class RouteOpts(ctypes.Structure):
 class Experts(ctypes.Structure):
     _fields_ = [("W_gate", _vp), ("W_up", _vp), ("W_down", _vp), ("wtype", _i32), ("wtype_down", _i32), ("E", _i64),
                 ("M", _i64), ("K", _i64), ("ids", _vp), ("weights", _vp), ("top_k", _i64), ("workspace", _vp),
-                ("workspace_bytes", _i64), ("flags", _u32)]
+                ("workspace_bytes", _i64), ("rms_norm_weight", _vp), ("rms_norm_eps", ctypes.c_float),
+                ("flags", _u32)]
 
 
 class Lora(ctypes.Structure):
@@ -475,17 +476,18 @@ def experts_workspace(E, T, top_k, M, K):
 
 
 def _experts_struct(W_gate, W_up, wtype, W_down, wtype_down, E, M, K, ids, weights, top_k, workspace,
-                    workspace_bytes, pdl):
+                    workspace_bytes, rms_norm_weight, rms_norm_eps, pdl):
     return Experts(_ptr(W_gate), _ptr(W_up), _ptr(W_down), wtype, wtype_down, E, M, K, _ptr(ids), _ptr(weights),
-                   top_k, _ptr(workspace), _nbytes(workspace, workspace_bytes), FLAG_PDL if pdl else 0)
+                   top_k, _ptr(workspace), _nbytes(workspace, workspace_bytes), _ptr(rms_norm_weight), rms_norm_eps,
+                   FLAG_PDL if pdl else 0)
 
 
 def gemv_experts(W_gate, W_up, wtype, W_down, wtype_down, E, x, M, K, ids, weights, T, top_k, aux, dst, workspace,
-                 workspace_bytes=None, pdl=False, stream=None, check=True):
-    """dst_t = aux_t + sum_j weights_tj Wd_e (silu(Wg_e x_t) * (Wu_e x_t)), e = ids_tj (see
+                 workspace_bytes=None, rms_norm_weight=None, rms_norm_eps=0.0, pdl=False, stream=None, check=True):
+    """dst_t = aux_t + sum_j weights_tj Wd_e (silu(Wg_e x'_t) * (Wu_e x'_t)), e = ids_tj (see
     include/gemvfuse.h)."""
     ex = _experts_struct(W_gate, W_up, wtype, W_down, wtype_down, E, M, K, ids, weights, top_k, workspace,
-                         workspace_bytes, pdl)
+                         workspace_bytes, rms_norm_weight, rms_norm_eps, pdl)
     st = _gemv_experts(ctypes.byref(ex), _ptr(x), T, _ptr(aux), _ptr(dst), _stream(stream))
     if check:
         _check(st, "gemv_experts")
@@ -493,15 +495,16 @@ def gemv_experts(W_gate, W_up, wtype, W_down, wtype_down, E, x, M, K, ids, weigh
 
 
 def prepare_experts(W_gate, W_up, wtype, W_down, wtype_down, E, x, M, K, ids, weights, T, top_k, aux, dst, workspace,
-                    workspace_bytes=None, pdl=False, check=True):
+                    workspace_bytes=None, rms_norm_weight=None, rms_norm_eps=0.0, pdl=False, check=True):
     """gf_prepare_experts: the call gemv_experts(...) would make, planned once (see Prepared)."""
     ex = _experts_struct(W_gate, W_up, wtype, W_down, wtype_down, E, M, K, ids, weights, top_k, workspace,
-                         workspace_bytes, pdl)
+                         workspace_bytes, rms_norm_weight, rms_norm_eps, pdl)
     h = _vp()
     st = _prepare_experts(ctypes.byref(ex), _ptr(x), T, _ptr(aux), _ptr(dst), ctypes.byref(h))
     if check:
         _check(st, "gf_prepare_experts")
-    return Prepared(h.value, (W_gate, W_up, W_down, x, ids, weights, aux, dst, workspace)) if st == OK else st
+    return Prepared(h.value, (W_gate, W_up, W_down, x, ids, weights, aux, dst, workspace,
+                              rms_norm_weight)) if st == OK else st
 
 
 def lora_workspace(ncols, M, K, rank, n):

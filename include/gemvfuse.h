@@ -322,19 +322,21 @@ GF_API int gf_prepare_route(const float* logits, int64_t T, int64_t E, const gf_
                             float* weights, gf_prepared** out);
 
 /* The gated feed-forward product of the chosen experts:
- *     dst_t = aux_t + sum_j weights_tj * Wd_e (silu(Wg_e x_t) * (Wu_e x_t)),   e = ids_tj
+ *     dst_t = aux_t + sum_j weights_tj * Wd_e (silu(Wg_e x'_t) * (Wu_e x'_t)),   e = ids_tj
  * for T tokens, each chosen expert's matrices read once for all the tokens that take it
- * (up to 32 at a time).  The sums of a token run over j in order: deterministic.
+ * (up to 24 at a time).  The sums of a token run over j in order: deterministic.
  *  W_gate, W_up : E matrices of M rows and K columns one after another, format `wtype`;
  *  W_down       : E matrices of K rows and M columns, format `wtype_down`.
  *  ids          : int32 [T][top_k]; a value outside 0..E-1 takes no expert and adds nothing.
  *  weights      : float32 [T][top_k].          x : [T][K].
+ *  x'           : x, or with rms_norm_weight its RMS normalisation (as in gf_opts).
  *  aux          : [T][K] or NULL (0); dst == aux is allowed (in place).
  *  workspace    : device memory of at least gf_experts_workspace() bytes, 256-byte aligned,
  *                 contents undefined before and after; not shared by calls that may overlap.
  *  Shapes: K and M multiples of 32 (256 for a Q4_K matrix's columns) with 16-byte aligned
- *  matrices take the tiled kernels, F32 and anything else the generic ones.
- *  dst may not overlap W_*, x, ids, weights or the workspace; the workspace no argument.
+ *  matrices take the tiled kernels, anything else the generic ones.
+ *  dst may not overlap W_*, x, ids, weights, rms_norm_weight or the workspace; the workspace
+ *  no argument.
  *  Limits (GF_ERR_UNSUPPORTED beyond): T <= 256, top_k <= 32, E <= 1024, M and K <= 2^20,
  *  columns no whole number of the format's blocks.  T == 0 or K == 0 launches nothing. */
 typedef struct {
@@ -348,6 +350,8 @@ typedef struct {
   int64_t top_k;
   void* workspace;
   int64_t workspace_bytes;
+  const float* rms_norm_weight;  /* [K] or NULL: no normalisation of x              */
+  float rms_norm_eps;
   uint32_t flags;      /* GF_FLAG_PDL                                               */
 } gf_experts;
 GF_API int gemv_experts(const gf_experts* ex, const float* x, int64_t T, const float* aux, float* dst,

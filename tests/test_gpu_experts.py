@@ -6,6 +6,7 @@ import pytest
 
 from decode_gemv_epilogue_gb300 import synth
 from gpu_util import assert_within, dev_tensor
+from oracle import norm as onorm
 from oracle import select as osel
 
 pytestmark = pytest.mark.gpu
@@ -42,7 +43,7 @@ class Case:
             b[shift:shift + r.size] = dev_tensor(r)
             self.dev.append(b[shift:])
 
-    def run(self, aux="given", prepared=False, pdl=False, ids=None, x=None, w=None):
+    def run(self, aux="given", prepared=False, pdl=False, ids=None, x=None, w=None, norm=None):
         G, T, K = self.G, self.T, self.K
         ids = self.ids if ids is None else ids
         x = self.x if x is None else x
@@ -63,7 +64,8 @@ class Case:
             if aux != "inplace":
                 graph.launch()
         else:
-            G.gemv_experts(*args, workspace_bytes=n, pdl=pdl)
+            G.gemv_experts(*args, workspace_bytes=n, pdl=pdl, rms_norm_weight=None if norm is None else dev_tensor(norm),
+                           rms_norm_eps=1e-6)
         torch.cuda.synchronize()
         assert torch.all(dst[T * K:] == -55.0) and torch.all(ws[n:] == 0xA5)
         return dst[:T * K].view(T, K).cpu().numpy()
@@ -188,6 +190,18 @@ def test_non_finite_values_stay_in_their_token(G, wt):
     got = c.run(w=w)
     assert np.all(np.isnan(got[2]))
     assert np.array_equal(np.delete(got, 2, 0).view(np.uint32), np.delete(ref, 2, 0).view(np.uint32))
+
+
+@pytest.mark.parametrize("wt, shift", [(F32, 0), (F16, 0), (Q8, 0), (Q4, 0), (Q4K, 0), (Q4, 2)])
+@pytest.mark.parametrize("T", [1, 5, 70])
+def test_rms_prologue(G, T, wt, shift):
+    """x normalised as it is packed (or, off a 16-byte boundary, as it is read)."""
+    c = Case(G, T, 6, 4, 256, 512, wt, wt, seed=100 + T, shift=shift)
+    gam = (1.0 + 0.1 * synth.normal(c.K, seed=9)).astype(np.float32)
+    xn = onorm.rms_norm(c.x, gam, 1e-6, c.K)
+    y, b = c.want(x=xn)
+    # the normalisation's own rounding: a tenth of the tolerance of each product (TOL_NORM_REL)
+    assert_within(c.run(norm=gam), y, 1.1 * b)
 
 
 def test_zero_ffn_width(G):

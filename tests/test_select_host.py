@@ -44,9 +44,9 @@ def test_route_null_options(lib):
 
 
 def e(lib, T=2, E=4, k=2, M=64, K=128, wt=3, wd=3, gate=G, up=U, down=D, x=X, ids=I, w=WT, aux=None, dst=DST, ws=WS,
-      nbytes=BIG):
+      nbytes=BIG, norm=None, eps=1e-6):
     return lib.gemv_experts(gate, up, wt, down, wd, E, x, M, K, ids, w, T, k, aux, dst, ws, workspace_bytes=nbytes,
-                            check=False, stream=0)
+                            rms_norm_weight=norm, rms_norm_eps=eps, check=False, stream=0)
 
 
 @pytest.mark.parametrize("kw, want", [
@@ -62,6 +62,8 @@ def e(lib, T=2, E=4, k=2, M=64, K=128, wt=3, wd=3, gate=G, up=U, down=D, x=X, id
     (dict(ids=I + 2), "ALIGN"), (dict(w=WT + 1), "ALIGN"), (dict(aux=B + 2), "ALIGN"), (dict(down=D + 1), "ALIGN"),
     (dict(dst=X), "ALIAS"), (dict(dst=G + 16), "ALIAS"), (dict(dst=U), "ALIAS"), (dict(dst=D), "ALIAS"),
     (dict(dst=I), "ALIAS"), (dict(dst=WT), "ALIAS"), (dict(aux=DST + 4), "ALIAS"), (dict(ws=X), "ALIAS"),
+    (dict(norm=B + 2), "ALIGN"), (dict(norm=B, eps=-1.0), "INVALID"), (dict(norm=B, eps=float("nan")), "INVALID"),
+    (dict(norm=DST), "ALIAS"), (dict(norm=WS + 64), "ALIAS"),
     (dict(dst=WS + 256), "ALIAS"), (dict(aux=WS), "ALIAS"), (dict(ids=WS + 4), "ALIAS"), (dict(gate=WS + 1024), "ALIAS"),
 ])
 def test_experts_refusals(lib, kw, want):
