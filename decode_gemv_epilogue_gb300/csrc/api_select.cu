@@ -82,11 +82,11 @@ static int experts_layout(int64_t E, int64_t T, int64_t k, int64_t M, int64_t K,
     return p;
   };
   const int64_t S = T * k, K32 = (K + 31) / 32, M32 = (M + 31) / 32;
-  // every expert's slots in tiles of eight: at most one part-filled tile an expert
+  // every expert's slots in column tiles of cp: at most one part-filled tile an expert
   const int64_t cp = std::min<int64_t>(8, std::max<int64_t>(T, 1));
-  l.max_tiles = std::min(S, std::min(E, S) + S / 8);
+  l.max_tiles = std::min(S, std::min(E, S) + S / cp);
   l.n_groups = take(16);
-  l.slots = take(S * 4);
+  l.slots = take(std::max(S, l.max_tiles * 8) * 4);
   l.groups = take(S * 16);
   l.places = take(S * 8);
   l.xrec = take(l.max_tiles * K32 * record_bytes(static_cast<int>(cp)));

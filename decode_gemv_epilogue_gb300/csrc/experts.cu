@@ -4,7 +4,8 @@
 //
 // Tiled path, four launches chained with programmatic dependent launch:
 //   prep     lists the slots of every expert (stable, so that nothing depends on the order
-//            in which threads run), cuts them into column groups, and packs x;
+//            in which threads run), cuts them into column groups, and packs x (two launches
+//            where the list is long);
 //   gate/up  every chosen expert's gate and up rows are read once per column group; the
 //            gated values go out packed for the next product;
 //   down     the same for the down matrices, each slot's column times its weight;
@@ -95,29 +96,77 @@ __global__ void __launch_bounds__(256) experts_combine_kernel(const __grid_const
 constexpr int kPrepThreads = kPackThreads;
 constexpr int kPrepMaxIter = kExpMaxTokens * kRouteMaxTopK / kPrepThreads;  // 32-slot steps of a warp
 
-constexpr int kPrepFused = 256;        // slots
 constexpr int kPackSlotThreads = 256;
 
 static int prep_smem(int E) { return 32 * E * 2 + 3 * E * 4; }
 
-// The column tile of a prep CTA: up to eight slots of one expert.
-struct PrepTile {
-  int first, count, cp;  // entry and columns of the tile; columns stored per column tile of its group
-  int slot[8];
-};
+// A short list (at most a slot a thread, groups of one column tile): every CTA packs one
+// slot's column, and finds its place by counting over all slots; the first one writes the
+// groups too.  Groups are numbered in the order of their first slots.
+__global__ void __launch_bounds__(kPackSlotThreads) experts_prep_short_kernel(const __grid_constant__ ExpertsArgs a) {
+  __shared__ int ids[kPackSlotThreads];
+  __shared__ uint32_t leaders[kPackSlotThreads / 32];
+  __shared__ int place[3];  // of this CTA's slot: group (-1: none), column, columns of the group
+  __shared__ float wmax[2 * kPackThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int S = a.T * a.k, s = threadIdx.x, mine = blockIdx.x, lane = s & 31;
+  int e = s < S ? a.ids[s] : -1;
+  if (e >= a.E) e = -1;
+  if (e < 0) e = -1;
+  ids[s] = e;
+  __syncthreads();
+  // (a group has no more columns than its records have room for: a token may name an expert twice)
+  const int width = a.cp;
+  // slots of the same expert before this one, in all; the group's first; the next slot's column
+  int before = 0, all = 0, first = 0, next = 0;
+  if (e >= 0) {
+    for (int q = 0; q < S; ++q) {
+      const bool same = ids[q] == e;
+      if (same && q <= s && next == 0) first = q;
+      if (same && q < s) ++before;
+      if (same) {
+        ++all;
+        next = next + 1 == width ? 0 : next + 1;
+      }
+    }
+  }
+  const uint32_t lead = __ballot_sync(0xffffffffu, e >= 0 && first == s);
+  if (lane == 0) leaders[s >> 5] = lead;
+  __syncthreads();
+  if (e >= 0) {
+    int g = __popc(leaders[first >> 5] & ((1u << (first & 31)) - 1u));
+    for (int q = 0; q < (first >> 5); ++q) g += __popc(leaders[q]);
+    const int col = before % width, count = min(width, all - (before - col));
+    if (mine == 0) {
+      a.slots[8 * g + col] = s;
+      if (first == s) a.groups[g] = make_int4(e, 8 * g, count, g);
+    }
+    if (s == mine) {
+      place[0] = g;
+      place[1] = col;
+      place[2] = count;
+    }
+  } else if (s == mine) {
+    place[0] = -1;
+  }
+  if (mine == 0 && s == 0) {
+    int n = 0;
+    for (int q = 0; q < kPackSlotThreads / 32; ++q) n += __popc(leaders[q]);
+    *a.n_groups = n;
+  }
+  __syncthreads();
+  if (place[0] < 0) return;
+  pack_column(a.x + static_cast<int64_t>(mine / a.k) * a.K, place[1], s, kPackSlotThreads, a.gamma, a.eps, a.K, a.wtype,
+              place[2], a.xrec + static_cast<int64_t>(place[0]) * (a.K / 32) * record_bytes(a.cp), wmax);
+}
 
 // The slots of each expert in slot order: a counting sort whose counts are kept per warp
 // (each warp owns a run of consecutive slots) and ranked within a 32-slot step by matching.
-// PACK: every CTA of the launch makes the whole list (a few microseconds, less than another
-// launch) and packs its own column tiles; the first one also writes the list and the column
-// groups.  Otherwise one CTA makes the list, and a launch of a CTA per slot packs: a list of
-// more than kPrepFused slots takes longer than that launch (2048 slots: 23 us against 11).
-template <bool PACK>
-__global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(const __grid_constant__ ExpertsArgs a) {
+// One CTA; a launch of a CTA per slot then packs.
+__global__ void __launch_bounds__(kPrepThreads) experts_list_kernel(const __grid_constant__ ExpertsArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ PrepTile pt;
   __shared__ uint32_t wsum[32];
-  __shared__ float wmax[2 * kPrepThreads / 32];
   uint32_t* offs = reinterpret_cast<uint32_t*>(smem);
   uint32_t *first_tile = offs + a.E, *totals = first_tile + a.E;
   uint16_t* cnt = reinterpret_cast<uint16_t*>(totals + a.E);
@@ -193,59 +242,31 @@ __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(const __grid
   uint32_t all;
   const uint32_t ex0 = scan(total | (nt << 16), all);
   const uint32_t off = ex0 & 0xffffu, t0 = ex0 >> 16;
-  const int tiles = static_cast<int>(all >> 16);
   if (e < a.E) {
     offs[e] = off;
     first_tile[e] = t0;
     totals[e] = total;
   }
-  if (blockIdx.x == 0) {
-    uint32_t groups;
-    const uint32_t g0 = scan(ng, groups);
-    for (uint32_t i = 0; i < ng; ++i) {
-      const uint32_t f = i * gt * 8u;
-      a.groups[g0 + i] = make_int4(e, static_cast<int>(off + f), static_cast<int>(min(gt * 8u, total - f)),
-                                   static_cast<int>(t0 + i * gt));
-    }
-    if (threadIdx.x == 0) *a.n_groups = static_cast<int>(groups);
+  uint32_t groups;
+  const uint32_t g0 = scan(ng, groups);
+  for (uint32_t i = 0; i < ng; ++i) {
+    const uint32_t f = i * gt * 8u;
+    a.groups[g0 + i] = make_int4(e, static_cast<int>(off + f), static_cast<int>(min(gt * 8u, total - f)),
+                                 static_cast<int>(t0 + i * gt));
   }
+  if (threadIdx.x == 0) *a.n_groups = static_cast<int>(groups);
   __syncthreads();
-  int pos[kPrepMaxIter];  // places of this thread's slots in the list
 #pragma unroll
   for (int j = 0; j < kPrepMaxIter; ++j) {
-    pos[j] = -1;
+    const int s = w * run + 32 * j + lane;
     if (ex[j] >= 0) {
-      pos[j] = static_cast<int>(offs[ex[j]]) + mine[ex[j]] + rank[j];
-      const int s = w * run + 32 * j + lane;
-      if (blockIdx.x == 0) a.slots[pos[j]] = s;
-      if constexpr (!PACK) {
-        const uint32_t f = static_cast<uint32_t>(pos[j]) - offs[ex[j]], group = f / (gt * 8u) * (gt * 8u);
-        a.places[s] = make_int2(static_cast<int>(first_tile[ex[j]] + f / 8u),
-                                static_cast<int>((f % 8u) | (min(8u, totals[ex[j]] - group) << 8)));
-      }
+      const uint32_t f = mine[ex[j]] + rank[j], group = f / (gt * 8u) * (gt * 8u);  // among the expert's slots
+      a.slots[offs[ex[j]] + f] = s;
+      a.places[s] = make_int2(static_cast<int>(first_tile[ex[j]] + f / 8u),
+                              static_cast<int>((f % 8u) | (min(8u, totals[ex[j]] - group) << 8)));
+    } else if (32 * j < run && s < S) {
+      a.places[s] = make_int2(-1, 0);
     }
-  }
-  if constexpr (!PACK) {
-    for (int s = threadIdx.x; s < S; s += kPrepThreads)  // slots without an expert
-      if (static_cast<uint32_t>(a.ids[s]) >= static_cast<uint32_t>(a.E)) a.places[s] = make_int2(-1, 0);
-    return;
-  }
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    if (static_cast<uint32_t>(tile) >= t0 && static_cast<uint32_t>(tile) < t0 + nt) {  // one thread's expert
-      const uint32_t f = 8u * (static_cast<uint32_t>(tile) - t0), group = f / (gt * 8u) * (gt * 8u);
-      pt.first = static_cast<int>(off + f);
-      pt.count = static_cast<int>(min(8u, total - f));
-      pt.cp = static_cast<int>(min(8u, total - group));
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kPrepMaxIter; ++j)
-      if (pos[j] >= pt.first && pos[j] < pt.first + pt.count) pt.slot[pos[j] - pt.first] = w * run + 32 * j + lane;
-    __syncthreads();
-    const int share = pack_share(pt.count), c = threadIdx.x / share;
-    const float* x = c < pt.count ? a.x + static_cast<int64_t>(pt.slot[c] / a.k) * a.K : nullptr;
-    pack_column(x, c, threadIdx.x % share, share, a.gamma, a.eps, a.K, a.wtype, pt.cp,
-                a.xrec + static_cast<int64_t>(tile) * (a.K / 32) * record_bytes(a.cp), wmax);
   }
 }
 
@@ -327,26 +348,27 @@ int launch_experts(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
   cudaLaunchAttribute attr;
   switch (a.phase) {
     case EXP_PREP: {
-      const bool fused = a.T * a.k <= kPrepFused;
-      auto kern = fused ? experts_prep_kernel<true> : experts_prep_kernel<false>;
-      static int configured[64][2] = {};
+      const cudaLaunchConfig_t pack =
+          config(dim3(static_cast<unsigned>(a.T * a.k)), kPackSlotThreads, st, pdl, &attr);
+      // (fewer than eight tokens always come this way: their groups are narrower than a column
+      // tile; measured, 8 and 42 slots: 6.5 us through the list, 3.7 and 4.6 so)
+      if (a.T * a.k <= kPackSlotThreads && a.cols <= 8) return cudaLaunchKernelEx(&pack, experts_prep_short_kernel, a);
+      static int configured[64] = {0};
       int dev = 0;
       cudaGetDevice(&dev);
       const int smem = prep_smem(a.E);
-      if (smem > 48 * 1024 && dev < 64 && configured[dev][fused] < smem) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (smem > 48 * 1024 && dev < 64 && configured[dev] < smem) {
+        const cudaError_t e = cudaFuncSetAttribute(experts_list_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        configured[dev][fused] = smem;
+        configured[dev] = smem;
       }
-      cudaLaunchConfig_t cfg =
-          config(dim3(static_cast<unsigned>(fused ? std::min(a.max_tiles, a.sm_count) : 1)), kPrepThreads, st, pdl, &attr);
-      cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-      const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
-      if (e != cudaSuccess || fused) return e;
-      cudaLaunchAttribute attr2;
-      const cudaLaunchConfig_t cfg2 =
-          config(dim3(static_cast<unsigned>(a.T * a.k)), kPackSlotThreads, st, true, &attr2);
-      return cudaLaunchKernelEx(&cfg2, experts_pack_kernel, a);
+      cudaLaunchConfig_t list = config(dim3(1), kPrepThreads, st, pdl, &attr);
+      list.dynamicSmemBytes = static_cast<size_t>(smem);
+      const cudaError_t e = cudaLaunchKernelEx(&list, experts_list_kernel, a);
+      if (e != cudaSuccess) return e;
+      cudaLaunchAttribute behind;
+      const cudaLaunchConfig_t cfg = config(pack.gridDim, kPackSlotThreads, st, true, &behind);
+      return cudaLaunchKernelEx(&cfg, experts_pack_kernel, a);
     }
     case EXP_GLU: return launch_tiles<TILE_GLU>(a, st, pdl);
     case EXP_DOWN: return launch_tiles<TILE_DOWN>(a, st, pdl);

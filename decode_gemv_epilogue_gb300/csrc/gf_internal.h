@@ -262,7 +262,7 @@ struct ExpertsArgs {
   int cp;               // columns stored per column tile: min(8, T)
   int max_tiles;        // upper bound on the column tiles of all experts
   // workspace
-  int32_t* slots;       // [T k] slots by expert, in slot order
+  int32_t* slots;       // the slots of each group, one after another
   int4* groups;         // {expert, first entry, columns, first column tile} of each column group
   int32_t* n_groups;
   int2* places;         // [T k] {column tile, column | columns stored << 8} of each slot, or {-1, 0}

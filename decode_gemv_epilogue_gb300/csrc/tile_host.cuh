@@ -49,8 +49,8 @@ int launch_tile(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
   m1 = m0;
   if (MODE == TILE_GLU) e = tile_map<WT>(o.W2, o.all_rows, t.row_bytes, &m1);
   if (e != cudaSuccess) return e;
-  // The columns' records of whole groups where they leave three stages of weights, in two
-  // buffers where those leave four, with as many CTAs per SM as the registers allow;
+  // The columns' records of whole groups where they leave three chunks of weights or more, in
+  // two buffers where those leave a stage more, with as many CTAs per SM as the registers allow;
   // else the records go with the weights.  1 KB a CTA is the system's.
   const int fixed = kTileHeadBytes + kTileRedBytes + 1024;
   const int64_t xb = tile_x_bytes(t.K, NT, t.cp);
@@ -59,7 +59,7 @@ int launch_tile(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
   auto plan = [&](int n, int buffers, int want) {
     const int budget = n == 1 ? o.smem_optin : (o.smem_optin + 1024) / n - 1024;
     if (fixed + buffers * xb >= budget) return false;
-    stage = tile_stage_bytes<WT>(t.period, NT, t.cp, buffers > 0);
+    stage = tile_chunks(WT, NT) * tile_stage_bytes<WT>(t.period, NT, t.cp, buffers > 0);
     ns = static_cast<int>(std::min<int64_t>(kTileMaxStages, (budget - fixed - buffers * xb) / stage));
     ctas = n;
     t.xbuffers = buffers;
@@ -67,7 +67,8 @@ int launch_tile(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
     return ns >= want;
   };
   const int most = tile_ctas(WT, NT);
-  if (!plan(most, 2, 4) && !plan(most, 1, 3) && !plan(most, 0, 3) && !plan(1, 1, 3)) plan(1, 0, 2);
+  constexpr int kFew = tile_chunks(WT, NT) == 2 ? 2 : 3;  // stages
+  if (!plan(most, 2, kFew + 1) && !plan(most, 1, kFew) && !plan(most, 0, kFew) && !plan(1, 1, kFew)) plan(1, 0, 2);
   if (ns < 2 || o.max_groups / (ctas * o.sm_count) + 2 > kTileMaxGroups) return cudaErrorInvalidConfiguration;
   t.NS = ns;
   const int smem = fixed + static_cast<int>(x_all) + ns * stage;

@@ -383,7 +383,10 @@ template <int WT>
 __host__ __device__ constexpr int tile_weight_bytes(int period) {
   return tile_plain(WT) ? kTileRows * tile_seg<WT>() : 2 * period * tile_part<WT>(period);
 }
-// A stage: weights, and in the chunk by chunk case the records of the chunk.
+// Chunks of a stage: two where a stage of one holds little (a wait serves two blocks of each
+// warp then, whose instructions interleave).
+__host__ __device__ constexpr int tile_chunks(int wt, int nt) { return (wt == WT_Q4_0 || wt == WT_Q4_K) && nt == 1 ? 2 : 1; }
+// One chunk of a stage: weights, and in the chunk by chunk case its records.
 template <int WT>
 __host__ __device__ constexpr int tile_stage_bytes(int period, int nt, int cp, bool resident) {
   return (tile_weight_bytes<WT>(period) + 16 + (resident ? 0 : nt * kTileBlocks * record_bytes(cp)) + 1023) / 1024 * 1024;
@@ -593,6 +596,7 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(WT, NT))
     tile_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
                 const __grid_constant__ TileArgs a) {
   constexpr int kOutRows = MODE == TILE_GLU ? 32 : kTileRows;
+  constexpr int CH = tile_chunks(WT, NT);
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(smem), full0 = sbase, empty0 = sbase + 8u * kTileMaxStages;
@@ -670,33 +674,39 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(WT, NT))
                      static_cast<uint32_t>(nblk) * rec, xfull0 + 8u * b);
           xgroups = gi + 1;
         }
-        for (int kc = 0; kc < n_kc; ++kc) {
+        for (int kc0 = 0; kc0 < n_kc; kc0 += CH) {
           if (issued >= a.NS && !mbar_wait_or_abort(empty0 + 8u * slot, phase, abort_flag, a.err)) {
             ok = false;
             break;
           }
-          const uint32_t st = ring + static_cast<uint32_t>(slot) * stage_bytes, full = full0 + 8u * slot;
-          const uint32_t xlen = resident ? 0u : static_cast<uint32_t>(min(kTileBlocks, nblk - kc * kTileBlocks)) * rec;
-          mbar_arrive_expect_tx(full, halves * wlen + nt * xlen);
-          for (int h = 0; h < halves; ++h) {
-            const CUtensorMap* map = MODE == TILE_GLU && h ? &map1 : &map0;
-            const int row = first + (MODE == TILE_GLU ? 0 : 32 * h);
-            if constexpr (tile_plain(WT)) {
-              constexpr int kBox = WT == WT_F16 ? 64 : 32;  // elements of 128 bytes
+          const uint32_t full = full0 + 8u * slot;
+          const int chunks = min(CH, n_kc - kc0);
+          const uint32_t blocks = static_cast<uint32_t>(min(CH * kTileBlocks, nblk - kc0 * kTileBlocks));
+          mbar_arrive_expect_tx(full, chunks * halves * wlen + (resident ? 0u : nt * blocks * rec));
+          for (int ch = 0; ch < chunks; ++ch) {
+            const int kc = kc0 + ch;
+            const uint32_t st = ring + static_cast<uint32_t>(slot * CH + ch) * stage_bytes;
+            for (int h = 0; h < halves; ++h) {
+              const CUtensorMap* map = MODE == TILE_GLU && h ? &map1 : &map0;
+              const int row = first + (MODE == TILE_GLU ? 0 : 32 * h);
+              if constexpr (tile_plain(WT)) {
+                constexpr int kBox = WT == WT_F16 ? 64 : 32;  // elements of 128 bytes
 #pragma unroll
-              for (int q = 0; q < kTileK / kBox; ++q)
-                tma_load_2d(st + static_cast<uint32_t>((2 * q + h) * 4096), map, kc * kTileK + kBox * q, row, full);
-            } else if constexpr (PER1) {
-              tma_load_2d(st + static_cast<uint32_t>(h * tile_part<WT>(1)), map, kc * (tile_seg<WT>() / 2), row, full);
-            } else {
-              for (int i = 0; i < a.period; ++i)
-                tma_load_2d(st + static_cast<uint32_t>((h * a.period + i) * tile_part<WT>(a.period)), map,
-                            ((i * a.row_bytes + kc * tile_seg<WT>()) & ~15) / 2, row / a.period, full);
+                for (int q = 0; q < kTileK / kBox; ++q)
+                  tma_load_2d(st + static_cast<uint32_t>((2 * q + h) * 4096), map, kc * kTileK + kBox * q, row, full);
+              } else if constexpr (PER1) {
+                tma_load_2d(st + static_cast<uint32_t>(h * tile_part<WT>(1)), map, kc * (tile_seg<WT>() / 2), row, full);
+              } else {
+                for (int i = 0; i < a.period; ++i)
+                  tma_load_2d(st + static_cast<uint32_t>((h * a.period + i) * tile_part<WT>(a.period)), map,
+                              ((i * a.row_bytes + kc * tile_seg<WT>()) & ~15) / 2, row / a.period, full);
+              }
             }
+            const uint32_t xlen = static_cast<uint32_t>(min(kTileBlocks, nblk - kc * kTileBlocks)) * rec;
+            for (int n = 0; n < nt && !resident; ++n)
+              bulk_g2s(st + xoff + static_cast<uint32_t>(n) * kTileBlocks * rec,
+                       xsrc + n * tile_stride + static_cast<uint32_t>(kc * kTileBlocks) * rec, xlen, full);
           }
-          for (int n = 0; n < nt && !resident; ++n)
-            bulk_g2s(st + xoff + static_cast<uint32_t>(n) * kTileBlocks * rec,
-                     xsrc + n * tile_stride + static_cast<uint32_t>(kc * kTileBlocks) * rec, xlen, full);
           ++issued;
           if (++slot == a.NS) {
             slot = 0;
@@ -785,21 +795,25 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(WT, NT))
       auto walk = [&](auto nta) {
         constexpr int NTA = decltype(nta)::value;
 #pragma unroll 1
-        for (int kc = 0; kc < n_kc; ++kc) {
+        for (int kc0 = 0; kc0 < n_kc; kc0 += CH) {
           ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(full0 + 8u * slot, phase, abort_flag, a.err));
-          const uint32_t st = ring + static_cast<uint32_t>(slot) * stage_bytes;
-          if (ok && kc * kTileBlocks + wk < nblk) {
-            const uint32_t blk = static_cast<uint32_t>(wk);
-            const uint32_t xs = resident ? xres + xbuf * xbytes + (static_cast<uint32_t>(kc * kTileBlocks) + blk) * l.rec
-                                         : st + xoff + blk * l.rec;
-            // codes behind a two-byte scale start on a word in every other block (in rows that
-            // themselves do)
-            if constexpr (WT == WT_F32)
-              tile_block_f32<MODE, NTA, NT>(l, st, xs, blk, acc);
-            else if (PER1 && (WT == WT_Q4_0 || WT == WT_Q8_0) && (wk & 1))
-              tile_block<WT, MODE, NTA, NT, PER1, true>(l, st, xs, blk, acc);
-            else
-              tile_block<WT, MODE, NTA, NT, PER1, false>(l, st, xs, blk, acc);
+#pragma unroll
+          for (int ch = 0; ch < CH; ++ch) {
+            const int kc = kc0 + ch;
+            const uint32_t st = ring + static_cast<uint32_t>(slot * CH + ch) * stage_bytes;
+            if (ok && kc * kTileBlocks + wk < nblk) {
+              const uint32_t blk = static_cast<uint32_t>(wk);
+              const uint32_t xs = resident ? xres + xbuf * xbytes + (static_cast<uint32_t>(kc * kTileBlocks) + blk) * l.rec
+                                           : st + xoff + blk * l.rec;
+              // codes behind a two-byte scale start on a word in every other block (in rows that
+              // themselves do)
+              if constexpr (WT == WT_F32)
+                tile_block_f32<MODE, NTA, NT>(l, st, xs, blk, acc);
+              else if (PER1 && (WT == WT_Q4_0 || WT == WT_Q8_0) && (wk & 1))
+                tile_block<WT, MODE, NTA, NT, PER1, true>(l, st, xs, blk, acc);
+              else
+                tile_block<WT, MODE, NTA, NT, PER1, false>(l, st, xs, blk, acc);
+            }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(empty0 + 8u * slot);

@@ -152,6 +152,20 @@ def test_ids_without_an_expert(G, wt):
 
 
 @pytest.mark.parametrize("wt", [F32, F16, Q8, Q4, Q4K])
+@pytest.mark.parametrize("T, k", [(1, 1), (1, 3), (1, 32), (2, 9), (5, 7), (7, 32), (8, 4), (31, 8), (40, 7), (256, 2)])
+def test_every_choice_the_same_expert(G, T, k, wt):
+    """A token may name an expert more than once, also more often than there are tokens."""
+    c = Case(G, T, 3, k, 256, 256, wt, wt, seed=T + k)
+    ids = np.full_like(c.ids, 2)
+    y, b = c.want(ids=ids)
+    assert_within(c.run(ids=ids), y, b)
+    ids[T // 2, k // 2] = 0
+    ids[0, 0] = -1
+    y, b = c.want(ids=ids)
+    assert_within(c.run(ids=ids), y, b)
+
+
+@pytest.mark.parametrize("wt", [F32, F16, Q8, Q4, Q4K])
 def test_all_tokens_take_one_expert(G, wt):
     c = Case(G, 67, 3, 1, 256, 256, wt, wt, seed=60)
     ids = np.ones_like(c.ids)
