@@ -4,17 +4,19 @@
 // x is "packed" first: every 32 elements of a column become 32 pairs of f16,
 //     x * 2^s = hi + lo,   hi = f16(x 2^s),   lo = f16(x 2^s - hi)
 // with a power of two 2^s that puts the largest magnitude into [2^14, 2^15): hi + lo carries
-// x to 2^-22 of itself (2^-35 of the largest where lo is subnormal), less than the rounding
+// x to 2^-22 of itself (2^-39 of the largest where lo is subnormal), less than the rounding
 // of a 32-bit sum.  The weights' codes are exact in f16, the products of f16 are exact in
 // the 32-bit accumulators, and the blocks' scales multiply the accumulated sum of a block in
 // 32 bits: the only roundings are those of 32-bit sums.
 //
 // Codes become f16 by masking alone: the f16 with the bits of a code c below 1024 is the
-// subnormal c 2^-24, which the matrix unit takes exactly (a 4-bit code four bits higher is
-// 16 c 2^-24; its x is packed 1/16 as large).  The sums are then in units of 2^-24, taken
-// back in the tail, and the formats' offsets (8 and 128) enter as the matrix instruction's
-// addend, -offset times the sum of x over the block: no instruction per weight is left but
-// the masks.
+// subnormal c 2^-24, which the matrix unit takes exactly.  It lines its products up by the
+// operands' exponents, though, a subnormal's being that of 2^-14: a code is placed high
+// enough (up to 255 for 8 bits, sixteen times the code for 4) that what it drops stays at the
+// level of a 32-bit sum's rounding (4-bit codes in the lowest bits: an error of 5e-6 of the
+// result, against 2e-7).  The sums are in units of 2^-24 or 2^-20, taken back in the tail,
+// and the formats' offsets (8 and 128) enter as the matrix instruction's addend, -offset
+// times the sum of x over the block: no instruction per weight is left but shifts and masks.
 //
 // Why mma.sync and not the asynchronous matrix unit: a block format's scale belongs to 32
 // weights of one row, so the accumulator of every 32 columns of K has to pass through
@@ -102,12 +104,10 @@ __host__ __device__ constexpr int pack_order(int wt) {
 // What the sum of a block is stored for: the offset of the codes, or Q4_K's mins, both in
 // the units of the accumulators.
 __host__ __device__ constexpr float pack_sum(int wt) {
-  return wt == WT_Q4_0 ? -8.0f * 0x1p-24f : wt == WT_Q8_0 ? -128.0f * 0x1p-24f : 0x1p-24f;
+  return wt == WT_Q4_0 ? -8.0f * 0x1p-20f : wt == WT_Q8_0 ? -128.0f * 0x1p-24f : 0x1p-20f;
 }
-// Factor of elements 16 .. 31 of a block: their Q4_0 codes are masked in place, 16 times as large.
-__host__ __device__ constexpr float pack_high(int wt) { return wt == WT_Q4_0 ? 0.0625f : 1.0f; }
 // Unit of the accumulators.
-__host__ __device__ constexpr float tile_unit(int wt) { return wt == WT_F16 || wt == WT_F32 ? 1.0f : 0x1p24f; }
+__host__ __device__ constexpr float tile_unit(int wt) { return wt == WT_F16 || wt == WT_F32 ? 1.0f : wt == WT_Q8_0 ? 0x1p24f : 0x1p20f; }
 __host__ __device__ constexpr int record_bytes(int cp) { return cp * 128 + (cp * 8 + 15) / 16 * 16; }
 // Byte offset in a record of the four elements 4q .. 4q + 3 of column c.
 __device__ __forceinline__ uint32_t record_offset(uint32_t q, uint32_t c, uint32_t cp, int order) {
@@ -167,7 +167,7 @@ __device__ inline void pack_column(const float* x, int c, int i0, int share, con
                                    int cp, uint8_t* base, float* wmax) {
   const int lane = threadIdx.x & 31;
   const int n4 = K / 4, order = pack_order(fmt);
-  const float high = pack_high(fmt), sumf = pack_sum(fmt);
+  const float sumf = pack_sum(fmt);
   const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(gamma)) & 15u) == 0;
   auto four = [&](const float* p, int i) -> float4 {
     if (vec) return reinterpret_cast<const float4*>(p)[i];
@@ -220,9 +220,6 @@ __device__ inline void pack_column(const float* x, int c, int i0, int share, con
     float sum = (v.x + v.y) + (v.z + v.w);
 #pragma unroll
     for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((i & 4) != 0) {
-      v.x *= high; v.y *= high; v.z *= high; v.w *= high;
-    }
     if (x != nullptr && i < n4) {
       uint8_t* r = base + static_cast<int64_t>(i >> 3) * rec;
       *reinterpret_cast<uint4*>(r + record_offset(i & 7, c, cp, order)) = pack_group(v, order == ORDER_NIBBLE);
@@ -248,12 +245,14 @@ __device__ __forceinline__ void q4k_scale_of(const uint4 hd, uint32_t j, float& 
   dmn = h2f(hd.x >> 16) * (__uint_as_float(0x4B000000u | mn) - kMagic);
 }
 
+constexpr uint32_t kNibbles = 0x00F000F0u;  // two 4-bit codes as 16 c 2^-24
+
 // One lane's place in a row of a stage: what it reads of its warp's block.
 struct RowPlace {
   uint32_t code;   // first aligned word of its codes
   uint32_t scale;  // the block's scale (Q4_0, Q8_0)
   uint32_t shift;  // bits the codes start above that word's first (0 or 16)
-  uint32_t mask;   // Q4_K: which nibbles
+  uint32_t left, right;  // Q4_K: shifts that bring its nibbles into place
 };
 template <int WT>
 __device__ __forceinline__ RowPlace row_place(uint32_t row, uint32_t blk, uint32_t t) {
@@ -265,7 +264,8 @@ __device__ __forceinline__ RowPlace row_place(uint32_t row, uint32_t blk, uint32
     p.shift = (c & 3u) * 8u;
   } else if constexpr (WT == WT_Q4_K) {
     p.code = row + 16u + ((blk >> 1) & 3u) * 32u + 4u * t;
-    p.mask = 0x000F000Fu << (4u * (blk & 1u));
+    p.left = 4u - 4u * (blk & 1u);
+    p.right = 4u + 4u * (blk & 1u);
   } else {
     p.code = row;  // F16: swizzled by the caller
   }
@@ -299,20 +299,19 @@ __device__ __forceinline__ void load_block_row(const RowPlace& p, uint32_t off, 
     a1[1] = __byte_perm(v, 0u, 0x4342);
   } else if constexpr (WT == WT_Q4_K) {  // scale and min come apart elsewhere
     const uint32_t w = lds32(p.code + off), v = lds32(p.code + off + 16u);
-    a0[0] = w & p.mask;
-    a0[1] = (w >> 8) & p.mask;
-    a1[0] = v & p.mask;
-    a1[1] = (v >> 8) & p.mask;
+    a0[0] = (w << p.left) & kNibbles;
+    a0[1] = (w >> p.right) & kNibbles;
+    a1[0] = (v << p.left) & kNibbles;
+    a1[1] = (v >> p.right) & kNibbles;
     d = 1.0f;
   } else {  // Q4_0
     d = h2f(lds16(p.scale + off));
     uint32_t w = lds32(p.code + off);
     if constexpr (!WHOLE) w = __funnelshift_r(w, lds32(p.code + off + 4u), p.shift);
-    const uint32_t w8 = w >> 8;
-    a0[0] = w & 0x000F000Fu;   // elements 4t, 4t + 2
-    a0[1] = w8 & 0x000F000Fu;  // 4t + 1, 4t + 3
-    a1[0] = w & 0x00F000F0u;
-    a1[1] = w8 & 0x00F000F0u;
+    a0[0] = (w << 4) & kNibbles;  // elements 4t, 4t + 2
+    a0[1] = (w >> 4) & kNibbles;  // 4t + 1, 4t + 3
+    a1[0] = w & kNibbles;         // the same + 16
+    a1[1] = (w >> 8) & kNibbles;
   }
 }
 
@@ -461,11 +460,8 @@ __device__ __forceinline__ void tile_block(const TileLane& l, uint32_t st, uint3
   float qd[2], qm[2];
   if constexpr (WT == WT_Q4_K) {
     const uint32_t mine = row + (l.t4 & 1u) * step16 + (l.t4 >> 1) * half;
-    const float nib = (blk & 1u) ? 0.0625f : 1.0f;  // high nibbles are masked in place
     q4k_scale_of(lds128(mine), blk, qd[0], qm[0]);
     q4k_scale_of(lds128(mine + step8), blk, qd[1], qm[1]);
-    qd[0] *= nib;
-    qd[1] *= nib;
   }
   // A matrix instruction takes long to give its sum back and the four of a block follow one
   // another in it: MG matrix tiles are taken side by side
@@ -861,7 +857,7 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(WT, NT))
             float sum = hs;
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const HiLo p = split_hi_lo(lane < 16 ? hs : hs * pack_high(a.out_format));
+            const HiLo p = split_hi_lo(hs);
             uint8_t* r = a.out_records + static_cast<int64_t>(g.w + n) * (a.rows / 32) * record_bytes(a.cp) +
                          static_cast<int64_t>(row0 / 32) * l.rec;
             const int order = pack_order(a.out_format);

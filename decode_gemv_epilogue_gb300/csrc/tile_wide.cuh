@@ -60,7 +60,6 @@ __device__ __forceinline__ void wide_pair(const TileLane& l, uint32_t row, uint3
     const uint4 hd = lds128(row + (t4 >> 1) * kM + (t4 & 1u) * (8u * kP));
     q4k_scale_of(hd, 2u * pair, qd[0], qm[0]);
     q4k_scale_of(hd, 2u * pair + 1u, qd[1], qm[1]);
-    qd[1] *= 0.0625f;  // high nibbles are masked in place
   }
 #pragma unroll
   for (int o = 0; o < 2; ++o) {
@@ -73,11 +72,10 @@ __device__ __forceinline__ void wide_pair(const TileLane& l, uint32_t row, uint3
       for (int h = 0; h < 2; ++h) {
         dm[m][h] = 0.0f;
         if constexpr (WT == WT_Q4_K) {
-          const uint32_t mask = o ? 0x00F000F0u : 0x000F000Fu;
-          a0[m][h][0] = kw[m][h] & mask;
-          a0[m][h][1] = (kw[m][h] >> 8) & mask;
-          a1[m][h][0] = kv[m][h] & mask;
-          a1[m][h][1] = (kv[m][h] >> 8) & mask;
+          a0[m][h][0] = (o ? kw[m][h] : kw[m][h] << 4) & kNibbles;
+          a0[m][h][1] = (kw[m][h] >> (o ? 8 : 4)) & kNibbles;
+          a1[m][h][0] = (o ? kv[m][h] : kv[m][h] << 4) & kNibbles;
+          a1[m][h][1] = (kv[m][h] >> (o ? 8 : 4)) & kNibbles;
           d[m][h] = __shfl_sync(0xffffffffu, qd[o], 2 * m + h, 4);
           dm[m][h] = __shfl_sync(0xffffffffu, qm[o], 2 * m + h, 4);
         } else {
@@ -86,7 +84,7 @@ __device__ __forceinline__ void wide_pair(const TileLane& l, uint32_t row, uint3
           p.scale = row + m * kM + h * 8u * kP + 2u * kBlock * pair + o * kBlock;
           p.code = p.scale + (o ? 2u : 0u) + 4u * t4;
           p.shift = 16u;
-          p.mask = 0u;
+          p.left = p.right = 0u;
           if (o)
             load_block_row<WT, true>(p, 0u, a0[m][h], a1[m][h], d[m][h]);
           else
@@ -326,7 +324,6 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
         const int r0 = row0 + 32 * (w >> 1);
         if (r0 < a.rows && ok && !*abort_flag) {
           const int order = pack_order(a.out_format);
-          const float high = pack_high(a.out_format);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             uint8_t* r = a.out_records + static_cast<int64_t>(g.w + n) * (a.rows / 32) * kRec +
@@ -342,7 +339,7 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
               for (int h = 0; h < 2; ++h) {
                 const uint32_t rr = 16u * (w & 1) + 8u * h + g4, i = rr & 3u;
                 const float hs = acc[0][n][2 * h + c] * sc;
-                const HiLo p = split_hi_lo((w & 1) ? hs * high : hs);
+                const HiLo p = split_hi_lo(hs);
                 uint8_t* q = r + record_offset(rr >> 2, col, cp, order) +
                              2u * (order == ORDER_NIBBLE ? ((i & 1u) << 1) | (i >> 1) : i);
                 *reinterpret_cast<__half*>(q) = p.hi;
