@@ -914,18 +914,21 @@ static int64_t lin_record_bytes(int64_t ncols, int64_t K) {
   return round_up256((ncols + 7) / 8 * ((K + 31) / 32) * (cp * 128 + (cp * 8 + 15) / 16 * 16));
 }
 
-// The tensor-core projection takes batches of any format but F16 (whose batches have a
-// tensor-core kernel already), K in whole blocks, where it beats blocks of eight columns on
-// the streamed kernel: from 17 columns, and in the block formats from three where the product
-// is large enough to hide one more launch.  Measured with 16-row adapters, us, tiles and
-// streamed: Q4_0 512 x 1024, 8 columns 18 / 12, 17 21 / 23, 64 28 / 48; 4096 x 4096, 6 columns
-// 29 / 27, 8 29 / 29, 64 57 / 160; 14336 x 4096, 2 columns 27 / 27, 4 29 / 37, 8 29 / 62; Q4_K
-// 35 / 106; F32 512 x 1024, 32 columns 29 / 27, 64 33 / 43; 14336 x 4096, 8 76 / 60, 32 122 / 209.
+// The tiled projection takes batches, K in whole blocks, where it beats blocks of columns on
+// the kernels of a plain batch: from 17 columns, and from three where the product is large
+// enough to hide one more launch (F32, F16: where several passes over the weights cost more).
+// Measured with 16-row adapters, us, tiles and plain: Q4_0 512 x 1024, 8 columns 18 / 12, 17
+// 21 / 23, 64 28 / 48; 4096 x 4096, 6 columns 29 / 27, 8 29 / 29, 64 57 / 160; 14336 x 4096, 2
+// columns 27 / 27, 4 29 / 37, 8 29 / 62; Q4_K 35 / 106; F32 512 x 1024, 32 columns 29 / 27, 64
+// 33 / 43; 14336 x 4096, 8 76 / 60, 32 122 / 209.  F16 on the tensor-core kernel: 4096 x 4096,
+// 32 columns 37 / 36, 64 59 / 62, 256 174 / 218; off it, 4096 x 4064, 8 29 / 29, 16 35 / 45.
 static bool lin_takes(const Call& c) {
-  if (c.wtype == GF_F16 || c.K < 32 || c.K % 32 != 0 || c.K > (1 << 20) || c.M < 8 || !aligned(c.W, 16) ||
+  if (c.K < 32 || c.K % 32 != 0 || c.K > (1 << 20) || c.M < 8 || !aligned(c.W, 16) ||
       (c.flags & GF_FLAG_NO_TENSOR_CORES))
     return false;
   const int64_t work = c.M * c.K * c.ncols;
+  if (c.wtype == GF_F16 && tc_eligible(c)) return c.ncols >= 64;
+  if (c.wtype == GF_F16) return (c.ncols > 16 && work >= (1LL << 25)) || (c.ncols > 1 && work >= (1LL << 28));
   if (c.wtype == GF_F32) return c.ncols > 16 && work >= (1LL << 25);
   return c.ncols > 16 || (c.ncols >= 3 && work >= (1LL << 27));
 }

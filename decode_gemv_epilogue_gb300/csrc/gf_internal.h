@@ -297,7 +297,7 @@ int launch_lora(const LoraArgs& a, cudaStream_t st, bool pdl);
 enum { LIN_PACK = 0, LIN_PRODUCT = 1, LIN_TAIL = 2 };
 struct LinArgs {
   int phase;
-  int wtype;            // GF_F32, GF_Q8_0, GF_Q4_0, GF_Q4_K
+  int wtype;            // any format
   const uint8_t* W;
   const float* x;       // [ncols][K]
   const float* gamma;

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(32) lin_tail_kernel(const __grid_constant__ Li
 
 int lin_cols(int wtype, int64_t M, int64_t K, int row_bytes, int ncols, int sms) {
   if (ncols <= 8) return ncols;
-  if (wtype == WT_F32) return 16;
+  if (tile_plain(wtype)) return 16;
   const double g8 = (ncols + 7) / 8, g16 = (ncols + 15) / 16;
   return wide_takes(wtype, row_bytes) &&
                  wide_cost(wtype, M, K, wide_rows(wtype), g16, sms) < tile_cost(M, K, kTileRows, g8, sms)
@@ -59,7 +59,7 @@ int lin_cols(int wtype, int64_t M, int64_t K, int row_bytes, int ncols, int sms)
 template <int WT, bool PER1>
 static int launch_lin_cols(const TileArgs& t, const LinArgs& a, cudaStream_t st, bool pdl) {
   const TileOperands o = {a.W, nullptr, t.rows, (a.ncols + a.cols - 1) / a.cols, a.sm_count, a.smem_optin};
-  if constexpr (WT == WT_F32) {
+  if constexpr (tile_plain(WT)) {
     if (a.cols > 8) return launch_tile<WT, TILE_LIN, 2, PER1>(t, o, st, pdl);
   } else if constexpr (PER1) {
     if (a.cols > 8) return launch_wide<WT, TILE_LIN>(t, o, st, pdl);
@@ -96,6 +96,7 @@ int launch_lin(const LinArgs& a, cudaStream_t st, bool pdl) {
   t.group_cols = a.cols;
   switch (a.wtype) {
     case WT_F32: return launch_lin_cols<WT_F32, true>(t, a, st, pdl);
+    case WT_F16: return launch_lin_cols<WT_F16, true>(t, a, st, pdl);
     case WT_Q8_0: return period == 1 ? launch_lin_cols<WT_Q8_0, true>(t, a, st, pdl) : launch_lin_cols<WT_Q8_0, false>(t, a, st, pdl);
     case WT_Q4_0: return period == 1 ? launch_lin_cols<WT_Q4_0, true>(t, a, st, pdl) : launch_lin_cols<WT_Q4_0, false>(t, a, st, pdl);
     case WT_Q4_K: return launch_lin_cols<WT_Q4_K, true>(t, a, st, pdl);

@@ -105,8 +105,8 @@ def test_ragged_shapes(G, M, K, at):
     Case(G, 4, M, K, F32, 3, 12, at, seed=M).check(2)
 
 
-@pytest.mark.parametrize("wt", [Q8, Q4])
-@pytest.mark.parametrize("N, M, K", [(2, 8, 32), (3, 71, 96), (9, 302, 3648), (20, 131, 1056), (33, 100, 1984)])
+@pytest.mark.parametrize("wt", [F32, F16, Q8, Q4])
+@pytest.mark.parametrize("N, M, K", [(60, 700, 1056), (2, 8, 32), (3, 71, 96), (9, 302, 3648), (20, 131, 1056), (33, 100, 1984)])
 def test_rows_of_no_whole_16_byte_words(G, N, M, K, wt):
     """Block-format batches whose rows a tensor map reaches only several at a time, and rows
     left over at the end."""
@@ -115,8 +115,9 @@ def test_rows_of_no_whole_16_byte_words(G, N, M, K, wt):
     c.check(4)
 
 
-@pytest.mark.parametrize("wt", [F32, Q8, Q4, Q4K])
-@pytest.mark.parametrize("N, M, K", [(2, 8, 256), (9, 33, 512), (16, 1000, 768), (17, 513, 256), (64, 600, 1024)])
+@pytest.mark.parametrize("wt", [F32, F16, Q8, Q4, Q4K])
+@pytest.mark.parametrize("N, M, K", [(2, 8, 256), (9, 33, 512), (16, 1000, 768), (17, 513, 256), (64, 600, 1024),
+                                     (70, 1000, 1024), (3, 10000, 4608), (8, 4100, 4096)])
 def test_batches(G, N, M, K, wt):
     c = Case(G, N, M, K, wt, 5, 16, F16, seed=N)
     c.check(2)
