@@ -247,14 +247,18 @@ __global__ void __launch_bounds__(kPrepThreads) experts_list_kernel(const __grid
     first_tile[e] = t0;
     totals[e] = total;
   }
-  uint32_t groups;
-  const uint32_t g0 = scan(ng, groups);
+  // every expert's first group, the largest, before the others'
+  uint32_t experts, groups;
+  const uint32_t g0 = scan(ng > 0 ? 1u : 0u, experts), g1 = experts + scan(ng > 0 ? ng - 1u : 0u, groups);
   for (uint32_t i = 0; i < ng; ++i) {
     const uint32_t f = i * gt * 8u;
-    a.groups[g0 + i] = make_int4(e, static_cast<int>(off + f), static_cast<int>(min(gt * 8u, total - f)),
-                                 static_cast<int>(t0 + i * gt));
+    a.groups[i == 0 ? g0 : g1 + i - 1u] = make_int4(e, static_cast<int>(off + f), static_cast<int>(min(gt * 8u, total - f)),
+                                                    static_cast<int>(t0 + i * gt));
   }
-  if (threadIdx.x == 0) *a.n_groups = static_cast<int>(groups);
+  if (threadIdx.x == 0) {
+    a.n_groups[0] = static_cast<int>(experts + groups);
+    a.n_groups[1] = a.n_groups[2] = 0;  // items of the two products taken
+  }
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kPrepMaxIter; ++j) {
@@ -304,6 +308,7 @@ static int launch_tiles(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
   t.groups = a.groups;
   t.n_groups = a.n_groups;
   t.max_groups = a.T * a.k;
+  t.next = reinterpret_cast<uint32_t*>(a.n_groups) + (MODE == TILE_GLU ? 1 : 2);
   t.slots = a.slots;
   t.records = MODE == TILE_GLU ? a.xrec : a.hrec;
   t.cp = a.cp;

@@ -115,7 +115,7 @@ int launch_wide(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
   if (e != cudaSuccess) return e;
   const int stage = wide_stage_bytes<WT>(), fixed = kTileHeadBytes + wide_xchg<WT>() + 1024;
   t.NS = std::min(kTileMaxStages, (o.smem_optin - fixed) / stage);
-  if (t.NS < 2 || o.max_groups / o.sm_count + 2 > kTileMaxGroups) return cudaErrorInvalidConfiguration;
+  if (t.NS < 2) return cudaErrorInvalidConfiguration;
   const int smem = fixed + t.NS * stage;
   static int configured[64] = {0};
   int dev = 0;

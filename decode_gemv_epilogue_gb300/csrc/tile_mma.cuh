@@ -401,6 +401,7 @@ struct TileArgs {
   const int4* groups;       // {matrix, first entry, columns, first column tile}
   const int32_t* n_groups;
   int max_groups;           // entries `groups` has room for
+  uint32_t* next;           // wide kernel, but for TILE_LIN: the next item to be taken (zero at the start)
   const int32_t* slots;     // slot of each entry
   const uint8_t* records;   // [column tile][K / 32] records of x
   int cp;                   // most columns stored per column tile

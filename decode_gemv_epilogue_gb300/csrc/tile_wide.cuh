@@ -13,7 +13,13 @@
 // Sixteen warps, four a scheduler (eight for Q8_0, whose rows leave no room for two stages of
 // sixteen warps' rows).  Measured on 256 tokens, 128 experts, 8 choices, 768 x 2048 Q4_K,
 // gate and up: eight warps with three column tiles 166 us, twelve (spilling) 178, sixteen
-// with two 153; 64 columns of 14336 x 4096 Q4_0: 77, 101, 67.
+// with two 153 (141 with items handed out, below); 64 columns of 14336 x 4096 Q4_0: 77, 101, 67.
+//
+// An item is a large piece of a launch (a quarter of a CTA's share, in that case), and column
+// groups differ in size: the experts' items are handed out one by one, large groups first,
+// instead of in equal ranges, which left the SMs idle for a fifth of the time.  What bounds it
+// now: the matrix unit, 41% busy on average while its four warps collide on it (throttled for
+// as long as they issue), and one issue slot in two.
 #pragma once
 
 #include "tile_mma.cuh"
@@ -135,6 +141,20 @@ __device__ __forceinline__ void wide_pair(const TileLane& l, uint32_t row, uint3
   }
 }
 
+// A barrier of nthreads threads that tells them all whether p holds for every one of them.
+__device__ __forceinline__ bool named_bar_all(uint32_t id, uint32_t nthreads, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %3, 0;\n\t"
+      "barrier.cta.red.and.pred b, %1, %2, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(nthreads), "r"(p ? 1u : 0u)
+      : "memory");
+  return r != 0u;
+}
+
 template <int WT, int MODE>
 __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
     wide_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
@@ -148,7 +168,7 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(smem), full0 = sbase, empty0 = sbase + 8u * kTileMaxStages;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 248);
-  int4* groups = reinterpret_cast<int4*>(smem + 256);
+  volatile int* item_of = reinterpret_cast<volatile int*>(smem + 128);  // per stage: item whose first chunk it holds
   float2* xchg = reinterpret_cast<float2*>(smem + kTileHeadBytes);
   const uint32_t ring = (sbase + kTileHeadBytes + wide_xchg<WT>() + 1023u) & ~1023u;
   if (threadIdx.x == 0) {
@@ -165,29 +185,34 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
   pdl_wait();
   const int tiles = (a.rows + kOutRows - 1) / kOutRows;
   const int n_groups = MODE == TILE_LIN ? (a.ncols + a.group_cols - 1) / a.group_cols : *a.n_groups;
-  const int64_t items = static_cast<int64_t>(n_groups) * tiles;
-  const int64_t lo = items * blockIdx.x / gridDim.x, hi = items * (blockIdx.x + 1) / gridDim.x;
-  const int g_lo = static_cast<int>(lo / tiles);
-  if (lo < hi)
-    for (int i = threadIdx.x; i <= static_cast<int>((hi - 1) / tiles) - g_lo; i += kThreads)
-      groups[i] = MODE == TILE_LIN ? make_int4(0, 0, min(a.group_cols, a.ncols - (g_lo + i) * a.group_cols),
-                                               (g_lo + i) * ((a.group_cols + 7) / 8))
-                                   : a.groups[g_lo + i];
+  const int items = n_groups * tiles;  // groups <= 2048, tiles <= 2^12
+  auto group_of = [&](int gi) -> int4 {
+    return MODE == TILE_LIN ? make_int4(0, 0, min(a.group_cols, a.ncols - gi * a.group_cols), gi * ((a.group_cols + 7) / 8))
+                            : a.groups[gi];
+  };
   __syncthreads();
   const int n_kc = (a.K + kTileK - 1) / kTileK, nblk = a.K / 32;
-  const int n_items = static_cast<int>(hi - lo);
-  const int tile_lo = static_cast<int>(lo - static_cast<int64_t>(g_lo) * tiles);
   const int64_t tile_stride = static_cast<int64_t>(nblk) * kRec;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int slot = 0, issued = 0, gi = 0, tile = tile_lo;
+      int slot = 0, issued = 0;
       uint32_t phase = 1u;
       bool ok = true;
-      for (int it = 0; it < n_items && ok; ++it) {
-        const int4 g = groups[gi];
-        const int row0 = tile * kOutRows;
+      // a batch's items are alike: every grid-th; the experts' as they come
+      for (int it = MODE == TILE_LIN ? static_cast<int>(blockIdx.x) : static_cast<int>(atomicAdd(a.next, 1u)); ok;
+           it = MODE == TILE_LIN ? it + static_cast<int>(gridDim.x) : static_cast<int>(atomicAdd(a.next, 1u))) {
+        if (it >= items) {  // the end: a stage without data
+          if (issued >= a.NS && !mbar_wait_or_abort(empty0 + 8u * slot, phase, abort_flag, a.err)) ok = false;
+          if (ok) {
+            item_of[slot] = -1;
+            mbar_arrive(full0 + 8u * slot);
+          }
+          break;
+        }
+        const int4 g = group_of(it / tiles);
+        const int row0 = (it % tiles) * kOutRows;
         const int boxes = min(kOutRows / 32, (a.rows - row0 + 31) / 32);  // of each matrix
         const int nt = (g.z + 7) / 8;
         const uint32_t rec = static_cast<uint32_t>(record_bytes(min(8, g.z)));
@@ -199,6 +224,7 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
           }
           const uint32_t st = ring + static_cast<uint32_t>(slot) * kStage, full = full0 + 8u * slot;
           const uint32_t xlen = static_cast<uint32_t>(min(kTileBlocks, nblk - kc * kTileBlocks)) * rec;
+          if (kc == 0) item_of[slot] = it;
           mbar_arrive_expect_tx(full, (MODE == TILE_GLU ? 2u : 1u) * boxes * 32u * P + nt * xlen);
           for (int i = 0; i < boxes; ++i) {
             tma_load_2d(st + i * kPart, &map0, kc * (tile_seg<WT>() / 2), g.x * a.rows + row0 + 32 * i, full);
@@ -214,10 +240,6 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
             phase ^= 1u;
           }
         }
-        if (++tile == tiles) {
-          tile = 0;
-          ++gi;
-        }
       }
       // Drain after an abort: every copy this thread issued lands before the CTA leaves.
       if (!ok)
@@ -232,12 +254,17 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
                                             : static_cast<uint32_t>(w) * kPart + g4 * P;
     TileLane l = {};
     l.t4 = t4;
-    int slot = 0, gi = 0, tile = tile_lo;
+    int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int it = 0; it < n_items; ++it) {
-      const int4 g = groups[gi];
-      const int row0 = tile * kOutRows;
+    for (uint32_t round = 0;; ++round) {
+      // the item's first chunk, or the end
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(full0 + 8u * slot, phase, abort_flag, a.err));
+      const int it = ok ? item_of[slot] : -1;
+      // gated, two warps meet at a barrier below: they go on, or stop, together
+      if (!(MODE == TILE_GLU ? named_bar_all(1u + static_cast<uint32_t>(w >> 1), 64u, it >= 0) : it >= 0)) break;
+      const int4 g = group_of(it / tiles);
+      const int row0 = (it % tiles) * kOutRows;
       const int ncol = g.z;
       l.cp = static_cast<uint32_t>(min(8, ncol));
       l.rec = static_cast<uint32_t>(record_bytes(static_cast<int>(l.cp)));
@@ -258,7 +285,7 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
         constexpr int NTA = decltype(nta)::value;
 #pragma unroll 1
         for (int kc = 0; kc < n_kc; ++kc) {
-          ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(full0 + 8u * slot, phase, abort_flag, a.err));
+          if (kc > 0) ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(full0 + 8u * slot, phase, abort_flag, a.err));
           const uint32_t st = ring + static_cast<uint32_t>(slot) * kStage;
           if (ok && mine) {
             // rows of whole 16-byte words have whole chunks
@@ -298,7 +325,7 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
       if constexpr (MODE == TILE_GLU) {
         // the gated values of rows 8h + g (of the warp's 16) and columns 2t + c, in place of the
         // gate sums
-        float2* mx = xchg + (it & 1) * (kWarps * 8 * NT);
+        float2* mx = xchg + (round & 1u) * (kWarps * 8 * NT);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -373,10 +400,6 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
                 }
               }
           }
-      }
-      if (++tile == tiles) {
-        tile = 0;
-        ++gi;
       }
     }
   }
