@@ -12,9 +12,9 @@
 // Codes become f16 by masking alone: the f16 with the bits of a code c below 1024 is the
 // subnormal c 2^-24, which the matrix unit takes exactly.  It lines its products up by the
 // operands' exponents, though, a subnormal's being that of 2^-14: a code is placed high
-// enough (up to 255 for 8 bits, sixteen times the code for 4) that what it drops stays at the
-// level of a 32-bit sum's rounding (4-bit codes in the lowest bits: an error of 5e-6 of the
-// result, against 2e-7).  The sums are in units of 2^-24 or 2^-20, taken back in the tail,
+// enough (up to 255 for 8 bits, 64 times the code for 4) that what it drops stays at the level
+// of a 32-bit sum's rounding (4-bit codes in the lowest bits: an error of 5e-6 of the result;
+// 16 times the code: 5e-7).  The sums are in units of 2^-24 or 2^-18, taken back in the tail,
 // and the formats' offsets (8 and 128) enter as the matrix instruction's addend, -offset
 // times the sum of x over the block: no instruction per weight is left but shifts and masks.
 //
@@ -104,10 +104,10 @@ __host__ __device__ constexpr int pack_order(int wt) {
 // What the sum of a block is stored for: the offset of the codes, or Q4_K's mins, both in
 // the units of the accumulators.
 __host__ __device__ constexpr float pack_sum(int wt) {
-  return wt == WT_Q4_0 ? -8.0f * 0x1p-20f : wt == WT_Q8_0 ? -128.0f * 0x1p-24f : 0x1p-20f;
+  return wt == WT_Q4_0 ? -8.0f * 0x1p-18f : wt == WT_Q8_0 ? -128.0f * 0x1p-24f : 0x1p-18f;
 }
 // Unit of the accumulators.
-__host__ __device__ constexpr float tile_unit(int wt) { return wt == WT_F16 || wt == WT_F32 ? 1.0f : wt == WT_Q8_0 ? 0x1p24f : 0x1p20f; }
+__host__ __device__ constexpr float tile_unit(int wt) { return wt == WT_F16 || wt == WT_F32 ? 1.0f : wt == WT_Q8_0 ? 0x1p24f : 0x1p18f; }
 __host__ __device__ constexpr int record_bytes(int cp) { return cp * 128 + (cp * 8 + 15) / 16 * 16; }
 // Byte offset in a record of the four elements 4q .. 4q + 3 of column c.
 __device__ __forceinline__ uint32_t record_offset(uint32_t q, uint32_t c, uint32_t cp, int order) {
@@ -245,7 +245,7 @@ __device__ __forceinline__ void q4k_scale_of(const uint4 hd, uint32_t j, float& 
   dmn = h2f(hd.x >> 16) * (__uint_as_float(0x4B000000u | mn) - kMagic);
 }
 
-constexpr uint32_t kNibbles = 0x00F000F0u;  // two 4-bit codes as 16 c 2^-24
+constexpr uint32_t kNibbles = 0x03C003C0u;  // two 4-bit codes as 64 c 2^-24
 
 // One lane's place in a row of a stage: what it reads of its warp's block.
 struct RowPlace {
@@ -264,8 +264,8 @@ __device__ __forceinline__ RowPlace row_place(uint32_t row, uint32_t blk, uint32
     p.shift = (c & 3u) * 8u;
   } else if constexpr (WT == WT_Q4_K) {
     p.code = row + 16u + ((blk >> 1) & 3u) * 32u + 4u * t;
-    p.left = 4u - 4u * (blk & 1u);
-    p.right = 4u + 4u * (blk & 1u);
+    p.left = 6u - 4u * (blk & 1u);
+    p.right = 2u + 4u * (blk & 1u);
   } else {
     p.code = row;  // F16: swizzled by the caller
   }
@@ -308,10 +308,10 @@ __device__ __forceinline__ void load_block_row(const RowPlace& p, uint32_t off, 
     d = h2f(lds16(p.scale + off));
     uint32_t w = lds32(p.code + off);
     if constexpr (!WHOLE) w = __funnelshift_r(w, lds32(p.code + off + 4u), p.shift);
-    a0[0] = (w << 4) & kNibbles;  // elements 4t, 4t + 2
-    a0[1] = (w >> 4) & kNibbles;  // 4t + 1, 4t + 3
-    a1[0] = w & kNibbles;         // the same + 16
-    a1[1] = (w >> 8) & kNibbles;
+    a0[0] = (w << 6) & kNibbles;  // elements 4t, 4t + 2
+    a0[1] = (w >> 2) & kNibbles;  // 4t + 1, 4t + 3
+    a1[0] = (w << 2) & kNibbles;  // the same + 16
+    a1[1] = (w >> 6) & kNibbles;
   }
 }
 

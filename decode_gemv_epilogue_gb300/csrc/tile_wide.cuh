@@ -78,10 +78,10 @@ __device__ __forceinline__ void wide_pair(const TileLane& l, uint32_t row, uint3
       for (int h = 0; h < 2; ++h) {
         dm[m][h] = 0.0f;
         if constexpr (WT == WT_Q4_K) {
-          a0[m][h][0] = (o ? kw[m][h] : kw[m][h] << 4) & kNibbles;
-          a0[m][h][1] = (kw[m][h] >> (o ? 8 : 4)) & kNibbles;
-          a1[m][h][0] = (o ? kv[m][h] : kv[m][h] << 4) & kNibbles;
-          a1[m][h][1] = (kv[m][h] >> (o ? 8 : 4)) & kNibbles;
+          a0[m][h][0] = (kw[m][h] << (o ? 2 : 6)) & kNibbles;
+          a0[m][h][1] = (kw[m][h] >> (o ? 6 : 2)) & kNibbles;
+          a1[m][h][0] = (kv[m][h] << (o ? 2 : 6)) & kNibbles;
+          a1[m][h][1] = (kv[m][h] >> (o ? 6 : 2)) & kNibbles;
           d[m][h] = __shfl_sync(0xffffffffu, qd[o], 2 * m + h, 4);
           dm[m][h] = __shfl_sync(0xffffffffu, qm[o], 2 * m + h, 4);
         } else {
