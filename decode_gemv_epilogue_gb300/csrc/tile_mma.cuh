@@ -142,9 +142,14 @@ __device__ __forceinline__ uint32_t half_pair(__half a, __half b) {
   return static_cast<uint32_t>(__half_as_ushort(a)) | (static_cast<uint32_t>(__half_as_ushort(b)) << 16);
 }
 
-// Four consecutive scaled elements as the 16 bytes of a packed group.
-__device__ __forceinline__ uint4 pack_group(float4 v, bool swapped) {
+__device__ __forceinline__ float value_of(const HiLo& p) { return __half2float(p.hi) + __half2float(p.lo); }
+
+// Four consecutive scaled elements as the 16 bytes of a packed group, and the sum of what these
+// hold: what stands in for the codes' offset has to be the sum of the same values that the codes
+// are multiplied by.
+__device__ __forceinline__ uint4 pack_group(float4 v, bool swapped, float& sum) {
   const HiLo a = split_hi_lo(v.x), b = split_hi_lo(v.y), c = split_hi_lo(v.z), d = split_hi_lo(v.w);
+  sum = (value_of(a) + value_of(b)) + (value_of(c) + value_of(d));
   return swapped ? make_uint4(half_pair(a.hi, c.hi), half_pair(b.hi, d.hi), half_pair(a.lo, c.lo), half_pair(b.lo, d.lo))
                  : make_uint4(half_pair(a.hi, b.hi), half_pair(c.hi, d.hi), half_pair(a.lo, b.lo), half_pair(c.lo, d.lo));
 }
@@ -217,12 +222,13 @@ __device__ inline void pack_column(const float* x, int c, int i0, int share, con
   const int rec = record_bytes(cp);
   auto put = [&](int i, float4 v) {
     v.x *= sc; v.y *= sc; v.z *= sc; v.w *= sc;
-    float sum = (v.x + v.y) + (v.z + v.w);
+    float sum;
+    const uint4 packed = pack_group(v, order == ORDER_NIBBLE, sum);
 #pragma unroll
     for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (x != nullptr && i < n4) {
       uint8_t* r = base + static_cast<int64_t>(i >> 3) * rec;
-      *reinterpret_cast<uint4*>(r + record_offset(i & 7, c, cp, order)) = pack_group(v, order == ORDER_NIBBLE);
+      *reinterpret_cast<uint4*>(r + record_offset(i & 7, c, cp, order)) = packed;
       if ((i & 7) == 0) *reinterpret_cast<float2*>(r + cp * 128 + c * 8) = make_float2(inv, sum * sumf);
     }
   };
@@ -434,7 +440,6 @@ __device__ __forceinline__ void tile_block(const TileLane& l, uint32_t st, uint3
                                            float (&acc)[4][NT][4]) {
   constexpr bool kMeta = MODE == TILE_DOWN || WT != WT_F16;  // per-block scales or sums are read here
   constexpr bool kOffset = WT == WT_Q4_0 || WT == WT_Q8_0;   // the sums are the codes' offset
-  constexpr bool kDirect = WT == WT_F16 && MODE != TILE_DOWN;  // one scale per column: no block scale at all
   constexpr uint32_t kP = tile_pitch<WT>(1);
   const uint32_t step8 = WT == WT_F16 ? 1024u : PER1 ? 8u * kP : l.step8;
   const uint32_t step16 = WT == WT_F16 ? 2048u : PER1 ? 16u * kP : l.step16;
@@ -483,18 +488,19 @@ __device__ __forceinline__ void tile_block(const TileLane& l, uint32_t st, uint3
           dm[j][h] = __shfl_sync(0xffffffffu, qm[h], m, 4);
         }
       }
+    // lo of both k-steps, then hi: the matrix unit cuts its sums off, toward zero, at the size
+    // they have reached.  For the same reason they end with the block (a sum over all of K in its
+    // accumulators was off by 2e-6 of itself, all to one side)
     float s[MG][NTA][4];
-    auto step = [&](int i) {  // hi of both k-steps, then lo of both
+    auto step = [&](int i) {
 #pragma unroll
       for (int j = 0; j < MG; ++j)
 #pragma unroll
         for (int n = 0; n < NTA; ++n) {
           const uint32_t (&x)[2][2] = (i & 1) ? a1[j] : a0[j];
           const uint4 v = b[n][i & 1];
-          const uint32_t p = i < 2 ? v.x : v.z, q = i < 2 ? v.y : v.w;
-          if constexpr (kDirect)
-            mma_f16(acc[mg + j][n], x[0][0], x[1][0], x[0][1], x[1][1], p, q);
-          else if (i == 0)
+          const uint32_t p = i < 2 ? v.z : v.x, q = i < 2 ? v.w : v.y;
+          if (i == 0)
             mma_f16_first(s[j][n], x[0][0], x[1][0], x[0][1], x[1][1], p, q, kOffset ? meta[n][0].y : 0.0f,
                           kOffset ? meta[n][1].y : 0.0f);
           else
@@ -505,25 +511,25 @@ __device__ __forceinline__ void tile_block(const TileLane& l, uint32_t st, uint3
     step(1);
     step(2);
     step(3);
-    if constexpr (!kDirect) {
 #pragma unroll
-      for (int j = 0; j < MG; ++j)
+    for (int j = 0; j < MG; ++j)
 #pragma unroll
-        for (int n = 0; n < NTA; ++n)
+      for (int n = 0; n < NTA; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // row row8 (0, 1) or row8 + 8 (2, 3), column 2t + (i & 1)
-            const int h = i >> 1, c = i & 1;
-            float& o = acc[mg + j][n][i];
-            if constexpr (MODE == TILE_DOWN) {
-              float v = WT == WT_F16 ? s[j][n][i] : d[j][h] * s[j][n][i];
-              if constexpr (WT == WT_Q4_K) v = fmaf(-dm[j][h], meta[n][c].y, v);
-              o = fmaf(meta[n][c].x, v, o);
-            } else {
-              o = fmaf(d[j][h], s[j][n][i], o);
-              if constexpr (WT == WT_Q4_K) o = fmaf(-dm[j][h], meta[n][c].y, o);
-            }
+        for (int i = 0; i < 4; ++i) {  // row row8 (0, 1) or row8 + 8 (2, 3), column 2t + (i & 1)
+          const int h = i >> 1, c = i & 1;
+          float& o = acc[mg + j][n][i];
+          if constexpr (MODE == TILE_DOWN) {
+            float v = WT == WT_F16 ? s[j][n][i] : d[j][h] * s[j][n][i];
+            if constexpr (WT == WT_Q4_K) v = fmaf(-dm[j][h], meta[n][c].y, v);
+            o = fmaf(meta[n][c].x, v, o);
+          } else if constexpr (WT == WT_F16) {  // one scale per column
+            o += s[j][n][i];
+          } else {
+            o = fmaf(d[j][h], s[j][n][i], o);
+            if constexpr (WT == WT_Q4_K) o = fmaf(-dm[j][h], meta[n][c].y, o);
           }
-    }
+        }
   }
 }
 
@@ -855,10 +861,10 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(WT, NT))
             const float h = tail_silu(gv) * uv;
             const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(finite_abs(h))));
             const float sc = pack_scale(m), hs = h * sc;
-            float sum = hs;
+            const HiLo p = split_hi_lo(hs);
+            float sum = value_of(p);
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const HiLo p = split_hi_lo(hs);
             uint8_t* r = a.out_records + static_cast<int64_t>(g.w + n) * (a.rows / 32) * record_bytes(a.cp) +
                          static_cast<int64_t>(row0 / 32) * l.rec;
             const int order = pack_order(a.out_format);

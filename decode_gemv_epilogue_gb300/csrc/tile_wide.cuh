@@ -106,9 +106,9 @@ __device__ __forceinline__ void wide_pair(const TileLane& l, uint32_t row, uint3
       const uint2 u = lds64(xa + l.m0), v = lds64(xa + l.m1);  // {2^-s, sum} of columns 2t and 2t + 1
       const float sx[2] = {__uint_as_float(u.x), __uint_as_float(v.x)}, xsum[2] = {__uint_as_float(u.y), __uint_as_float(v.y)};
       float s[2][4];
-      auto step = [&](int i) {  // hi of both k-steps, then lo of both
-        const uint32_t p = i == 0 ? b0.x : i == 1 ? b1.x : i == 2 ? b0.z : b1.z;
-        const uint32_t q = i == 0 ? b0.y : i == 1 ? b1.y : i == 2 ? b0.w : b1.w;
+      auto step = [&](int i) {  // lo of both k-steps, then hi (see tile_block)
+        const uint32_t p = i == 0 ? b0.z : i == 1 ? b1.z : i == 2 ? b0.x : b1.x;
+        const uint32_t q = i == 0 ? b0.w : i == 1 ? b1.w : i == 2 ? b0.y : b1.y;
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           const uint32_t (&x)[2][2] = (i & 1) ? a1[m] : a0[m];
