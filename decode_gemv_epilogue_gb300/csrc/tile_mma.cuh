@@ -15,8 +15,8 @@
 // enough (up to 255 for 8 bits, 64 times the code for 4) that what it drops stays at the level
 // of a 32-bit sum's rounding (4-bit codes in the lowest bits: an error of 5e-6 of the result;
 // 16 times the code: 5e-7).  The sums are in units of 2^-24 or 2^-18, taken back in the tail,
-// and the formats' offsets (8 and 128) enter as the matrix instruction's addend, -offset
-// times the sum of x over the block: no instruction per weight is left but shifts and masks.
+// and the formats' offsets (8 and 128) enter with the block's sum, -offset times the sum of x
+// over the block: no instruction per weight is left but shifts and masks.
 //
 // Why mma.sync and not the asynchronous matrix unit: a block format's scale belongs to 32
 // weights of one row, so the accumulator of every 32 columns of K has to pass through
@@ -39,13 +39,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// d = A B + {c0, c1, c0, c1}: an addend per column.
+// d = A B.
 __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1, float c0, float c1) {
+                                              uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %11, %10, %11};"
+      "{%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 // tf32 operands (f32 registers whose low 13 bits do not count), k = 8.
 __device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -501,8 +501,7 @@ __device__ __forceinline__ void tile_block(const TileLane& l, uint32_t st, uint3
           const uint4 v = b[n][i & 1];
           const uint32_t p = i < 2 ? v.z : v.x, q = i < 2 ? v.w : v.y;
           if (i == 0)
-            mma_f16_first(s[j][n], x[0][0], x[1][0], x[0][1], x[1][1], p, q, kOffset ? meta[n][0].y : 0.0f,
-                          kOffset ? meta[n][1].y : 0.0f);
+            mma_f16_first(s[j][n], x[0][0], x[1][0], x[0][1], x[1][1], p, q);
           else
             mma_f16(s[j][n], x[0][0], x[1][0], x[0][1], x[1][1], p, q);
         }
@@ -519,6 +518,7 @@ __device__ __forceinline__ void tile_block(const TileLane& l, uint32_t st, uint3
         for (int i = 0; i < 4; ++i) {  // row row8 (0, 1) or row8 + 8 (2, 3), column 2t + (i & 1)
           const int h = i >> 1, c = i & 1;
           float& o = acc[mg + j][n][i];
+          if constexpr (kOffset) s[j][n][i] += meta[n][c].y;
           if constexpr (MODE == TILE_DOWN) {
             float v = WT == WT_F16 ? s[j][n][i] : d[j][h] * s[j][n][i];
             if constexpr (WT == WT_Q4_K) v = fmaf(-dm[j][h], meta[n][c].y, v);

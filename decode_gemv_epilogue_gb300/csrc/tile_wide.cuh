@@ -113,7 +113,7 @@ __device__ __forceinline__ void wide_pair(const TileLane& l, uint32_t row, uint3
         for (int m = 0; m < 2; ++m) {
           const uint32_t (&x)[2][2] = (i & 1) ? a1[m] : a0[m];
           if (i == 0)
-            mma_f16_first(s[m], x[0][0], x[1][0], x[0][1], x[1][1], p, q, kOffset ? xsum[0] : 0.0f, kOffset ? xsum[1] : 0.0f);
+            mma_f16_first(s[m], x[0][0], x[1][0], x[0][1], x[1][1], p, q);
           else
             mma_f16(s[m], x[0][0], x[1][0], x[0][1], x[1][1], p, q);
         }
@@ -128,6 +128,7 @@ __device__ __forceinline__ void wide_pair(const TileLane& l, uint32_t row, uint3
         for (int i = 0; i < 4; ++i) {  // row g + 8 (i / 2), column 2t + i % 2
           const int h = i >> 1, c = i & 1;
           float& r = acc[m][n][i];
+          if constexpr (kOffset) s[m][i] += xsum[c];
           if constexpr (MODE == TILE_DOWN) {
             float y = d[m][h] * s[m][i];
             if constexpr (WT == WT_Q4_K) y = fmaf(-dm[m][h], xsum[c], y);
