@@ -8,9 +8,10 @@
 // order the shared product, launched with programmatic dependent launch, already streams its
 // weights while the two small kernels run, and the output is read and written once more only.
 //
-// Columns that share an adapter are served together: the CTA of the first such column takes
-// all of them, the others' CTAs leave at once, so that an adapter's rows are fetched once per
-// four columns (shrink) or once (expand).
+// Columns that share an adapter are served together, so that an adapter's rows are fetched
+// once per four columns (shrink) or once (expand): with fewer adapters than columns a CTA is
+// an adapter's (and one row of CTAs more the columns' without), else a column's, and the CTA
+// of the first column of an adapter takes all of them.
 //
 // Shrink: a CTA takes a few rows of an adapter's A; its 256 threads share the K axis, every
 // thread holding the sums of its rows and up to four columns, so that one round of
@@ -29,22 +30,33 @@ constexpr int kLoraThreads = 256;
 constexpr int kLoraCols = 4;      // columns of an adapter served at once
 constexpr int kExpandRows = 128;  // rows, and threads, of an expansion CTA
 
-// The columns from c on that take the adapter of column c, in order, into cols; their number.
-// 0 where an earlier column takes it: that column's CTA serves them all.  Called by every
-// thread of a CTA of `threads` >= 128.
-__device__ __forceinline__ int adapter_columns(const LoraArgs& a, int c, int threads, int* cols, int* seen) {
-  const int ad = a.ids[c];
-  if (threadIdx.x == 0) seen[0] = 0;
-  __syncthreads();
-  for (int q = threadIdx.x; q < c; q += threads)
-    if (a.ids[q] == ad) seen[0] = 1;
-  __syncthreads();
-  if (seen[0]) return 0;
-  if (threadIdx.x < 32) {  // one warp lists them, in order
+__host__ __device__ __forceinline__ bool lora_by_adapter(const LoraArgs& a) { return a.n < a.ncols; }
+
+// The columns that the CTAs of index y serve, in order, into cols; their number (0: another
+// index serves them), and their adapter (-1: none).  Called by every thread of a CTA.
+__device__ __forceinline__ int lora_columns(const LoraArgs& a, int y, int threads, int* cols, int* seen, int& ad) {
+  const bool by = lora_by_adapter(a);
+  ad = by ? y : a.ids[y];
+  if (ad < 0 || ad >= a.n) ad = -1;
+  if (!by) {
+    if (ad < 0 || a.ncols == 1) {  // a column without an adapter is served alone
+      if (threadIdx.x == 0) cols[0] = y;
+      __syncthreads();
+      return 1;
+    }
+    if (threadIdx.x == 0) seen[0] = 0;
+    __syncthreads();
+    for (int q = threadIdx.x; q < y; q += threads)
+      if (a.ids[q] == ad) seen[0] = 1;
+    __syncthreads();
+    if (seen[0]) return 0;
+  }
+  if (threadIdx.x < 32) {  // one warp lists them
     int n = 0;
-    for (int q0 = c; q0 < a.ncols; q0 += 32) {
+    for (int q0 = 0; q0 < a.ncols; q0 += 32) {
       const int q = q0 + static_cast<int>(threadIdx.x);
-      const bool is = q < a.ncols && a.ids[q] == ad;
+      const int id = q < a.ncols ? a.ids[q] : -2;
+      const bool is = q < a.ncols && (ad >= 0 ? id == ad : id < 0 || id >= a.n);
       const uint32_t m = __ballot_sync(0xffffffffu, is);
       if (is) cols[n + __popc(m & ((1u << threadIdx.x) - 1u))] = q;
       n += __popc(m);
@@ -87,18 +99,11 @@ __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const __grid_
   __shared__ int cols[256], seen[2];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.y, j0 = blockIdx.x * RB;
+  const int j0 = blockIdx.x * RB;
   const int rows = min(RB, a.r - j0);
-  const int ad = a.ids[c];
-  if (ad < 0 || ad >= a.n) return;  // the expansion does not read v for this column
-  int n = 1;
-  if (a.ncols > 1) {
-    n = adapter_columns(a, c, kLoraThreads, cols, seen);
-    if (n == 0) return;
-  } else if (threadIdx.x == 0) {
-    cols[0] = c;
-  }
-  __syncthreads();
+  int ad;
+  const int n = lora_columns(a, blockIdx.y, kLoraThreads, cols, seen, ad);
+  if (n == 0 || ad < 0) return;  // the expansion does not read v of a column without an adapter
   const uint8_t* A = a.A + (static_cast<int64_t>(ad) * a.r + j0) * a.K * kEl;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   for (int q0 = 0; q0 < n; q0 += CT) {
@@ -199,27 +204,22 @@ __global__ void __launch_bounds__(kExpandRows) lora_expand_kernel(const __grid_c
   __shared__ int cols[256], seen[2];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.y, m0 = blockIdx.x * kExpandRows, m = m0 + threadIdx.x;
-  const int ad = a.ids[c];
-  if (ad < 0 || ad >= a.n) {  // no adapter: the addend alone
-    if (m < a.M) {
-      const int64_t o = static_cast<int64_t>(c) * a.M + m;
+  const int m0 = blockIdx.x * kExpandRows, m = m0 + threadIdx.x;
+  int ad;
+  const int n = lora_columns(a, blockIdx.y, kExpandRows, cols, seen, ad);
+  if (ad < 0) {  // no adapter: the addend alone
+    for (int q = 0; q < n && m < a.M; ++q) {
+      const int64_t o = static_cast<int64_t>(cols[q]) * a.M + m;
       a.out[o] = a.aux ? a.aux[o] : 0.0f;
     }
     return;
   }
-  int n = 1;
-  if (a.ncols > 1) {
-    n = adapter_columns(a, c, kExpandRows, cols, seen);
-    if (n == 0) return;
-  } else if (threadIdx.x == 0) {
-    cols[0] = c;
-  }
+  if (n == 0) return;
   const int rows = min(kExpandRows, a.M - m0);
   const uint8_t* B = a.B + (static_cast<int64_t>(ad) * a.M + m0) * a.r * kEl;
   for (int k0 = 0; k0 < a.r; k0 += kChunk) {
     const int len = min(kChunk, a.r - k0);
-    __syncthreads();  // cols is listed; the previous chunk has been read
+    __syncthreads();  // the previous chunk has been read
     if constexpr (VEC) {
       const int words = len * kEl / 16;
       for (int i = threadIdx.x; i < rows * words; i += kExpandRows) {
@@ -293,9 +293,10 @@ static cudaError_t launch_lora_t(const LoraArgs& a, cudaStream_t st, bool pdl) {
   cfg.numAttrs = pdl ? 1 : 0;
   if (a.phase == LORA_SHRINK) {
     const bool vec = a.K % 8 == 0 && al16(a.A) && al16(a.x) && al16(a.gamma);
+    const int served = lora_by_adapter(a) ? a.n : a.ncols;
     const bool few = a.ncols * ((a.r + 7) / 8) <= 32;  // two rows a CTA, a column at a time
     const int rb = few ? 2 : 4;
-    cfg.gridDim = dim3(static_cast<unsigned>((a.r + rb - 1) / rb), static_cast<unsigned>(a.ncols));
+    cfg.gridDim = dim3(static_cast<unsigned>((a.r + rb - 1) / rb), static_cast<unsigned>(served));
     if (few)
       return vec ? cudaLaunchKernelEx(&cfg, lora_shrink_kernel<AT, true, 2, 1>, a)
                  : cudaLaunchKernelEx(&cfg, lora_shrink_kernel<AT, false, 2, 1>, a);
@@ -303,7 +304,8 @@ static cudaError_t launch_lora_t(const LoraArgs& a, cudaStream_t st, bool pdl) {
                : cudaLaunchKernelEx(&cfg, lora_shrink_kernel<AT, false, 4, kLoraCols>, a);
   }
   cfg.blockDim = dim3(kExpandRows);
-  cfg.gridDim = dim3(static_cast<unsigned>((a.M + kExpandRows - 1) / kExpandRows), static_cast<unsigned>(a.ncols));
+  cfg.gridDim = dim3(static_cast<unsigned>((a.M + kExpandRows - 1) / kExpandRows),
+                     static_cast<unsigned>(lora_by_adapter(a) ? a.n + 1 : a.ncols));
   const bool vec = a.r * (AT == WT_F16 ? 2 : 4) % 16 == 0 && al16(a.B);
   return vec ? cudaLaunchKernelEx(&cfg, lora_expand_kernel<AT, true>, a)
              : cudaLaunchKernelEx(&cfg, lora_expand_kernel<AT, false>, a);
