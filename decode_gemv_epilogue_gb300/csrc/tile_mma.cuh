@@ -1,5 +1,5 @@
 // Tiled products of block-format weights with several columns on the tensor cores: the
-// device code of the chosen experts' kernels.
+// device code of the chosen experts' kernels and of wide batches beside adapters.
 //
 // x is "packed" first: every 32 elements of a column become 32 pairs of f16,
 //     x * 2^s = hi + lo,   hi = f16(x 2^s),   lo = f16(x 2^s - hi)
@@ -7,7 +7,8 @@
 // x to 2^-22 of itself (2^-39 of the largest where lo is subnormal), less than the rounding
 // of a 32-bit sum.  The weights' codes are exact in f16, the products of f16 are exact in
 // the 32-bit accumulators, and the blocks' scales multiply the accumulated sum of a block in
-// 32 bits: the only roundings are those of 32-bit sums.
+// 32 bits: the only roundings are those of 32-bit sums (truncated ones in the matrix unit,
+// which is why its sums end with the block, and take the low parts first).
 //
 // Codes become f16 by masking alone: the f16 with the bits of a code c below 1024 is the
 // subnormal c 2^-24, which the matrix unit takes exactly.  It lines its products up by the
