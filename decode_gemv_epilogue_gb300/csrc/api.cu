@@ -1022,6 +1022,7 @@ static int plan_lora(const void* W, int wtype, const float* x, int64_t M, int64_
   l.out = out;
   l.aux = epilogue == GF_EPI_ADD ? aux : nullptr;
   const bool lin = lin_takes(c);
+  l.beside_pack = lin;
   LinArgs q = {};
   if (lin) {
     unsigned* err = device_error_word();

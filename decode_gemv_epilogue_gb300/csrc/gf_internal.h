@@ -290,6 +290,7 @@ struct LoraArgs {
   float* v;             // [ncols][r]
   float* out;           // [ncols][M]
   int n, r, M, K, ncols;
+  int beside_pack;      // behind the launch that packs x, of the same call
 };
 int launch_lora(const LoraArgs& a, cudaStream_t st, bool pdl);
 
