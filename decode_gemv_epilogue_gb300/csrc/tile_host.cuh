@@ -104,6 +104,34 @@ inline double wide_cost(int wt, int64_t rows, int64_t K, int tile_rows, double g
 }
 inline int wide_rows(int wt) { return wt == WT_Q8_0 ? 32 * wide_warps<WT_Q8_0>() : 32 * wide_warps<WT_Q4_0>(); }
 
+// A batch's items are alike and handed out in equal shares, so what counts is how many a CTA gets:
+// fewer rows an item where that saves a wave or fills one.  An item's time goes by the warps that
+// share a scheduler (Q4_0, K 4096: 64 us with 16 warps, 62 with 14, 50 with 12 or 10, 40 with 8):
+// the rows of 16, 12 or 8 warps (Q8_0: 8).  64 columns of 14336 x 4096 with rank-16 adapters:
+// 90 us, 76, 107.
+inline double wide_lin_cost(int wt, int64_t rows, int64_t K, double groups, int sms, int* item_rows) {
+  const int most = wide_rows(wt) / 32;
+  double best = 0.0;
+  for (int n = most; n >= 8; n -= 4) {
+    const double items = groups * static_cast<double>((rows + 32 * n - 1) / (32 * n));
+    const double us = std::ceil(items / sms) * (wt == WT_Q8_0 ? 46.0 : 16.0 + 3.0 * n) * static_cast<double>(K) / 4096.0;
+    if (n == most || us < best) {
+      best = us;
+      *item_rows = 32 * n;
+    }
+  }
+  return best;
+}
+// The K-sharing kernel's for the same, in groups of 8: 5 us and, by format, 11 to 15 a wave.  Whole
+// calls with rank-16 adapters, this kernel and the wide one: Q4_0, 32 columns of 14336 x 4096 55
+// us and 60, 48 of 11008 x 4096 68 and 62, 48 of 14336 x 4096 86 and 73; Q4_K, the same 64 and
+// 64, 80 and 66, 92 and 78; Q8_0, 256 of 4096 x 4096 144 and 131.
+inline double tile_lin_cost(int wt, int64_t rows, int64_t K, double groups, int sms) {
+  const double items = groups * static_cast<double>((rows + kTileRows - 1) / kTileRows);
+  const double wave = wt == WT_Q4_0 ? 11.0 : wt == WT_Q4_K ? 12.0 : 15.0;
+  return (5.0 + wave * std::max(1.0, items / (2.0 * sms))) * static_cast<double>(K) / 4096.0;
+}
+
 template <int WT, int MODE>
 int launch_wide(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
   auto kern = wide_kernel<WT, MODE>;

@@ -49,9 +49,9 @@ __global__ void __launch_bounds__(32) lin_tail_kernel(const __grid_constant__ Li
 int lin_cols(int wtype, int64_t M, int64_t K, int row_bytes, int ncols, int sms) {
   if (ncols <= 8) return ncols;
   if (tile_plain(wtype)) return 16;
-  const double g8 = (ncols + 7) / 8, g16 = (ncols + 15) / 16;
-  return wide_takes(wtype, row_bytes) &&
-                 wide_cost(wtype, M, K, wide_rows(wtype), g16, sms) < tile_cost(M, K, kTileRows, g8, sms)
+  int item_rows;
+  return wide_takes(wtype, row_bytes) && wide_lin_cost(wtype, M, K, (ncols + 15) / 16, sms, &item_rows) <
+                                             tile_lin_cost(wtype, M, K, (ncols + 7) / 8, sms)
              ? 16
              : 8;
 }
@@ -94,6 +94,7 @@ int launch_lin(const LinArgs& a, cudaStream_t st, bool pdl) {
   t.epi = a.epi;
   t.ncols = a.ncols;
   t.group_cols = a.cols;
+  if (!tile_plain(a.wtype)) wide_lin_cost(a.wtype, t.rows, a.K, (a.ncols + 15) / 16, a.sm_count, &t.item_rows);
   switch (a.wtype) {
     case WT_F32: return launch_lin_cols<WT_F32, true>(t, a, st, pdl);
     case WT_F16: return launch_lin_cols<WT_F16, true>(t, a, st, pdl);

@@ -424,6 +424,7 @@ struct TileArgs {
   const float* aux;         // TILE_LIN: may be `out`
   int epi;
   int ncols, group_cols;    // TILE_LIN: columns of the batch, of a group (no list of groups)
+  int item_rows;            // wide kernel, TILE_LIN: rows of an item
 };
 
 // One lane's constants of the walk over a stage.

@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
   }
   pdl_trigger();
   pdl_wait();
-  const int tiles = (a.rows + kOutRows - 1) / kOutRows;
+  const int out_rows = MODE == TILE_LIN ? min(a.item_rows, kOutRows) : kOutRows;  // of an item; the warps beyond idle
+  const int tiles = (a.rows + out_rows - 1) / out_rows;
   const int n_groups = MODE == TILE_LIN ? (a.ncols + a.group_cols - 1) / a.group_cols : *a.n_groups;
   const int items = n_groups * tiles;  // groups <= 2048, tiles <= 2^12
   auto group_of = [&](int gi) -> int4 {
@@ -213,8 +214,8 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
           break;
         }
         const int4 g = group_of(it / tiles);
-        const int row0 = (it % tiles) * kOutRows;
-        const int boxes = min(kOutRows / 32, (a.rows - row0 + 31) / 32);  // of each matrix
+        const int row0 = (it % tiles) * out_rows;
+        const int boxes = min(out_rows / 32, (a.rows - row0 + 31) / 32);  // of each matrix
         const int nt = (g.z + 7) / 8;
         const uint32_t rec = static_cast<uint32_t>(record_bytes(min(8, g.z)));
         const uint8_t* xsrc = a.records + g.w * tile_stride;
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
       // gated, two warps meet at a barrier below: they go on, or stop, together
       if (!(MODE == TILE_GLU ? named_bar_all(1u + static_cast<uint32_t>(w >> 1), 64u, it >= 0) : it >= 0)) break;
       const int4 g = group_of(it / tiles);
-      const int row0 = (it % tiles) * kOutRows;
+      const int row0 = (it % tiles) * out_rows;
       const int ncol = g.z;
       l.cp = static_cast<uint32_t>(min(8, ncol));
       l.rec = static_cast<uint32_t>(record_bytes(static_cast<int>(l.cp)));
@@ -274,7 +275,8 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
       l.m0 = l.cp * 128u + min(2u * t4, l.cp - 1u) * 8u;
       l.m1 = l.cp * 128u + min(2u * t4 + 1u, l.cp - 1u) * 8u;
       const uint32_t cp = l.cp, rec = l.rec;
-      const bool mine = MODE != TILE_GLU || row0 + 16 * w < a.rows;
+      const int at = MODE == TILE_GLU ? 16 * w : 32 * w;  // the warp's rows in the item
+      const bool mine = at < out_rows && row0 + at < a.rows;
       float acc[2][NT][4];
 #pragma unroll
       for (int m = 0; m < 2; ++m)
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
             }
           }
         }
-      } else if (ok && !*abort_flag) {
+      } else if (ok && mine && !*abort_flag) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
