@@ -124,6 +124,14 @@ def test_batches(G, N, M, K, wt):
     c.check(3)
 
 
+@pytest.mark.parametrize("wt", [Q8, Q4, Q4K])
+@pytest.mark.parametrize("N, M, K", [(125, 4009, 256), (64, 13101, 256), (57, 18002, 512), (250, 4500, 768)])
+def test_wide_batches_of_many_rows(G, N, M, K, wt):
+    """Enough rows and columns for the kernel of wide column groups, its items of 8, 12 and 16
+    warps' rows, the last item ragged."""
+    Case(G, N, M, K, wt, 9, 16, F16, seed=M).check(3)
+
+
 @pytest.mark.parametrize("at", [F16, F32])
 @pytest.mark.parametrize("shift", [1, 4])
 def test_adapters_off_a_16_byte_boundary(G, at, shift):
