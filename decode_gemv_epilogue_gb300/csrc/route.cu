@@ -308,26 +308,32 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
   int mine = -1;
   float pk = 0.0f, pl = 0.0f, pb = 0.0f;  // the previous round's key, logit and bias
   float last = -INFINITY;                 // the k-th key
-  uint32_t taken = 0;                     // of this lane's experts
+  uint32_t left[VPL];                     // ordered keys of this lane's experts not taken yet, 0: none
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) left[i] = key[i] > -INFINITY ? ordered(key[i]) : 0u;
   bool unsure = false;
   const int rounds = a.bias ? a.k + 1 : a.k;
   for (int j = 0; j < rounds; ++j) {
-    float bk = -INFINITY, bl = 0.0f, bb = 0.0f;
-    int bi = 0;
+    uint32_t u = 0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (!((taken >> i) & 1u) && key[i] > bk) {
-        bk = key[i];
-        bl = l[i];
-        bb = b[i];
-        bi = i;
-      }
-    const uint32_t u = ordered(bk), best = __reduce_max_sync(0xffffffffu, u);
-    if (best <= ordered(-INFINITY)) break;
-    const uint32_t cand = u == best ? static_cast<uint32_t>(lane + 32 * bi) : 0xffffffffu;
+    for (int i = 0; i < VPL; ++i) u = max(u, left[i]);
+    const uint32_t best = __reduce_max_sync(0xffffffffu, u);
+    if (best == 0u) break;
+    uint32_t cand = 0xffffffffu;
+#pragma unroll
+    for (int i = VPL - 1; i >= 0; --i)
+      if (left[i] == best) cand = static_cast<uint32_t>(lane + 32 * i);
     const uint32_t e = __reduce_min_sync(0xffffffffu, cand);
-    const int owner = static_cast<int>(e & 31u);
     if (a.bias) {
+      float bk = 0.0f, bl = 0.0f, bb = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (static_cast<uint32_t>(i) == e >> 5) {
+          bk = key[i];
+          bl = l[i];
+          bb = b[i];
+        }
+      const int owner = static_cast<int>(e & 31u);
       const float kk = __shfl_sync(0xffffffffu, bk, owner), kl = __shfl_sync(0xffffffffu, bl, owner),
                   kb = __shfl_sync(0xffffffffu, bb, owner);
       if (j > 0 && !(kl == pl && kb == pb) && pk - kk <= 2.0f * tol) unsure = true;
@@ -336,7 +342,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
       pb = kb;
       if (j == a.k - 1) last = kk;
     }
-    if (lane == owner) taken |= 1u << (e >> 5);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (static_cast<uint32_t>(lane + 32 * i) == e) left[i] = 0u;
     if (lane == j && j < a.k) mine = static_cast<int>(e);
   }
   if (unsure) mine = exact_choice<VPL>(a, l, key, lane, last - 2.0f * tol, top, a.sigmoid ? 1.0 : exact_sum<VPL>(l, top));
