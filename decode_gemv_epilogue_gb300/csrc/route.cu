@@ -234,7 +234,9 @@ __device__ __noinline__ double exact_sum(const float (&l)[VPL], float m) {
   return warp_sum(z);
 }
 
-template <int VPL>
+// PLAIN: no bias and no groups, the key is the logit (64 -> 25 registers a thread with
+// four experts a lane, and as many warps as an SM holds).
+template <int VPL, bool PLAIN>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_constant__ RouteArgs a) {
   pdl_wait();  // the logits may be the preceding grid's
   pdl_trigger();
@@ -252,15 +254,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
     l[i] = v == v ? fminf(v, FLT_MAX) : -INFINITY;
   }
   float key[VPL], b[VPL];
-  const bool plain_key = !a.bias && a.n_group <= 1;
+  const bool biased = !PLAIN && a.bias != nullptr;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = lane + 32 * i;
-    b[i] = (a.bias && e < a.E) ? a.bias[e] : 0.0f;
+    b[i] = (biased && e < a.E) ? a.bias[e] : 0.0f;
     key[i] = l[i] + 0.0f;  // -0 and +0 tie
   }
   float top = 0.0f, tol = 0.0f;  // largest logit; bound on the error of a 32-bit key
-  if (!plain_key) {
+  if constexpr (!PLAIN) {
     float s[VPL];
     if (a.sigmoid) {
 #pragma unroll
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = lane + 32 * i;
-      if (a.bias) key[i] = s[i];
+      if (biased) key[i] = s[i];
       if (a.n_group > 1 && e < a.E && !((kept >> (e / gs)) & 1u)) key[i] = -INFINITY;
     }
   }
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
 #pragma unroll
   for (int i = 0; i < VPL; ++i) left[i] = key[i] > -INFINITY ? ordered(key[i]) : 0u;
   bool unsure = false;
-  const int rounds = a.bias ? a.k + 1 : a.k;
+  const int rounds = biased ? a.k + 1 : a.k;
   for (int j = 0; j < rounds; ++j) {
     uint32_t u = 0;
 #pragma unroll
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
     for (int i = VPL - 1; i >= 0; --i)
       if (left[i] == best) cand = static_cast<uint32_t>(lane + 32 * i);
     const uint32_t e = __reduce_min_sync(0xffffffffu, cand);
-    if (a.bias) {
+    if (biased) {
       float bk = 0.0f, bl = 0.0f, bb = 0.0f;
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
       if (static_cast<uint32_t>(lane + 32 * i) == e) left[i] = 0u;
     if (lane == j && j < a.k) mine = static_cast<int>(e);
   }
-  if (unsure) mine = exact_choice<VPL>(a, l, key, lane, last - 2.0f * tol, top, a.sigmoid ? 1.0 : exact_sum<VPL>(l, top));
+  if (!PLAIN && unsure) mine = exact_choice<VPL>(a, l, key, lane, last - 2.0f * tol, top, a.sigmoid ? 1.0 : exact_sum<VPL>(l, top));
 
   // weights of the chosen, one lane each.  Normalised ones are taken relative to the largest
   // of them, so that scores that would vanish in 32 bits still share the whole.
@@ -398,7 +400,8 @@ static cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t st, bool pdl)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, route_kernel<VPL>, a);
+  return !a.bias && a.n_group <= 1 ? cudaLaunchKernelEx(&cfg, route_kernel<VPL, true>, a)
+                                   : cudaLaunchKernelEx(&cfg, route_kernel<VPL, false>, a);
 }
 
 int launch_route(const RouteArgs& a, cudaStream_t st, bool pdl) {
