@@ -940,12 +940,10 @@ int64_t gf_lora_workspace(int64_t ncols, int64_t M, int64_t K, int64_t rank, int
   return round_up256(ncols * rank * 4) + round_up256(ncols * M * 4) + lin_record_bytes(ncols, K);
 }
 
-// The launches of a gemv_lora call: [transform,] shrink, expand, the shared product with
-// the expansion as its addend [, the product with aux].
-static int plan_lora(const void* W, int wtype, const float* x, int64_t M, int64_t K, int epilogue, const float* aux,
-                     float* dst, const gf_lora* lo, const gf_opts* opts, LaunchRec* recs, int cap, int* n) {
-  *n = 0;
-  Call c = make_call(W, wtype, x, M, K, epilogue, aux, dst, opts);
+// Every check of a gemv_lora call.
+static int check_lora(const Call& c, const gf_lora* lo, const gf_opts* opts) {
+  const int64_t M = c.M, K = c.K;
+  const float *x = c.x, *aux = c.aux, *dst = c.dst;
   int v = validate(c);
   if (v != GF_OK) return v;
   v = check_view(opts, M);
@@ -966,7 +964,7 @@ static int plan_lora(const void* W, int wtype, const float* x, int64_t M, int64_
   if (lo->workspace_bytes < need) return GF_ERR_INVALID;
   const int64_t el = lo->atype == GF_F32 ? 4 : 2;
   const bool need_aux = c.aux != nullptr;
-  const int64_t dbytes = c.ncols * M * 4, xbytes = c.ncols * K * 4, wbytes = M * row_bytes_of(wtype, K);
+  const int64_t dbytes = c.ncols * M * 4, xbytes = c.ncols * K * 4, wbytes = M * row_bytes_of(c.wtype, K);
   const struct { const void* p; int64_t bytes; } side[4] = {{lo->A, lo->n * lo->rank * K * el},
                                                             {lo->B, lo->n * M * lo->rank * el},
                                                             {lo->ids, c.ncols * 4},
@@ -976,11 +974,22 @@ static int plan_lora(const void* W, int wtype, const float* x, int64_t M, int64_
         (c.workspace && ranges_overlap(c.workspace, xbytes, s.p, s.bytes)))
       return GF_ERR_ALIAS;
   if (ranges_overlap(lo->workspace, need, dst, dbytes) || ranges_overlap(lo->workspace, need, x, xbytes) ||
-      ranges_overlap(lo->workspace, need, W, wbytes) || (need_aux && ranges_overlap(lo->workspace, need, aux, dbytes)) ||
+      ranges_overlap(lo->workspace, need, c.W, wbytes) || (need_aux && ranges_overlap(lo->workspace, need, aux, dbytes)) ||
       (c.gamma && ranges_overlap(lo->workspace, need, c.gamma, K * 4)) ||
       (c.signs && ranges_overlap(lo->workspace, need, c.signs, c.nsigns * 4)) ||
       (c.workspace && ranges_overlap(lo->workspace, need, c.workspace, xbytes)))
     return GF_ERR_ALIAS;
+  return GF_OK;
+}
+
+// The launches of a gemv_lora call: [transform,] shrink, expand, the shared product with
+// the expansion as its addend [, the product with aux].
+static int plan_lora(const void* W, int wtype, const float* x, int64_t M, int64_t K, int epilogue, const float* aux,
+                     float* dst, const gf_lora* lo, const gf_opts* opts, LaunchRec* recs, int cap, int* n) {
+  *n = 0;
+  Call c = make_call(W, wtype, x, M, K, epilogue, aux, dst, opts);
+  int v = check_lora(c, lo, opts);
+  if (v != GF_OK || M == 0) return v;
   if (K == 0 || lo->n == 0) return plan_launches(c, dst, recs, cap, n);  // nothing to add
 
   bool pdl = (c.flags & GF_FLAG_PDL) != 0;
@@ -1116,6 +1125,26 @@ int gemv_lora(const void* W, int wtype, const float* x, int64_t M, int64_t K, in
     if (e != GF_OK) return e;
   }
   return GF_OK;
+}
+
+int gf_plan_lora(const void* W, int wtype, const float* x, int64_t M, int64_t K, int epilogue, const float* aux,
+                 const float* dst, const gf_lora* lora, const gf_opts* opts, int64_t info[8]) {
+  const Call c = make_call(W, wtype, x, M, K, epilogue, aux, dst, opts);
+  const int v = check_lora(c, lora, opts);
+  if (v != GF_OK || M == 0) return v;
+  Call pc = c;
+  if (pc.workspace) {  // the product reads x' without a prologue
+    pc.x = pc.workspace;
+    pc.signs = nullptr;
+  }
+  if (K == 0 || lora->n == 0 || !lin_takes(pc)) return plan_info(c, opts, info);
+  if (info) {
+    for (int i = 0; i < 8; ++i) info[i] = 0;
+    info[0] = lin_cols(wtype, M, K, static_cast<int>(row_bytes_of(wtype, K)), static_cast<int>(c.ncols),
+                       device_limits().sm_count);
+    info[1] = info[0] > 8 && (wtype == GF_Q8_0 || wtype == GF_Q4_0 || wtype == GF_Q4_K);
+  }
+  return PATH_TILE;
 }
 
 int gf_prepare_lora(const void* W, int wtype, const float* x, int64_t M, int64_t K, int epilogue, const float* aux,

@@ -127,13 +127,12 @@ static int experts_cols(const gf_experts* x, int64_t T, int sms) {
 
 constexpr int kExpMaxRecs = 4;
 
-static int plan_experts(const gf_experts* ex, const float* x, int64_t T, const float* aux, float* dst, LaunchRec* recs,
-                        int* n) {
-  *n = 0;
+// Every check of a call; its workspace layout.
+static int check_experts(const gf_experts* ex, const float* x, int64_t T, const float* aux, const float* dst,
+                         ExpertsLayout& l) {
   if (!ex) return GF_ERR_INVALID;
   const int wg = ex->wtype, wd = ex->wtype_down;
   if (wg < GF_F32 || wg > GF_Q4_K || wd < GF_F32 || wd > GF_Q4_K) return GF_ERR_INVALID;
-  ExpertsLayout l;
   const int v = experts_layout(ex->E, T, ex->top_k, ex->M, ex->K, l);
   if (v != GF_OK) return v;
   if (!columns_ok(wg, ex->K) || !columns_ok(wd, ex->M)) return GF_ERR_UNSUPPORTED;
@@ -159,6 +158,17 @@ static int plan_experts(const gf_experts* ex, const float* x, int64_t T, const f
   if (ranges_overlap(ex->workspace, l.bytes, dst, xb) || ranges_overlap(ex->workspace, l.bytes, aux, xb) ||
       (aux != dst && ranges_overlap(dst, xb, aux, xb)))
     return GF_ERR_ALIAS;
+  return GF_OK;
+}
+
+static int plan_experts(const gf_experts* ex, const float* x, int64_t T, const float* aux, float* dst, LaunchRec* recs,
+                        int* n) {
+  *n = 0;
+  ExpertsLayout l;
+  const int v = check_experts(ex, x, T, aux, dst, l);
+  if (v != GF_OK || T == 0 || ex->K == 0) return v;
+  const int wg = ex->wtype, wd = ex->wtype_down;
+  const bool some = ex->M > 0;
   unsigned* err = device_error_word();
   if (!err) return cuda_fail(cudaGetLastError());
   const DeviceLimits lim = device_limits();
@@ -249,6 +259,23 @@ int gemv_experts(const gf_experts* ex, const float* x, int64_t T, const float* a
   int n = 0;
   const int v = plan_experts(ex, x, T, aux, dst, recs, &n);
   return v != GF_OK ? v : issue_all(recs, n, stream);
+}
+
+int gf_plan_experts(const gf_experts* ex, const float* x, int64_t T, const float* aux, const float* dst,
+                    int64_t info[8]) {
+  ExpertsLayout l;
+  const int v = check_experts(ex, x, T, aux, dst, l);
+  if (v != GF_OK || T == 0 || ex->K == 0) return v;
+  const bool tiled = ex->M > 0 && experts_tiled(ex);
+  if (info) {
+    for (int i = 0; i < 8; ++i) info[i] = 0;
+    if (tiled) {
+      info[0] = experts_cols(ex, T, device_limits().sm_count);
+      info[1] = info[0] > 8 && !tile_plain(ex->wtype);
+      info[2] = info[0] > 8 && !tile_plain(ex->wtype_down);
+    }
+  }
+  return tiled ? PATH_TILE : PATH_GENERIC;
 }
 
 int gf_prepare_experts(const gf_experts* ex, const float* x, int64_t T, const float* aux, float* dst,

@@ -180,7 +180,7 @@ __host__ __device__ constexpr int64_t generic_smem_floats(int64_t ncols, int64_t
   return ncols * K + ncols + kGenericWarps * ncols;
 }
 
-enum { PATH_STREAM = 1, PATH_GENERIC = 2, PATH_TC = 3 };
+enum { PATH_STREAM = 1, PATH_GENERIC = 2, PATH_TC = 3, PATH_TILE = 4 };
 
 struct Plan {
   int path;

@@ -105,6 +105,9 @@ _route = _sig("gf_route", [_vp, _i64, _i64, ctypes.POINTER(RouteOpts), _vp, _vp,
 _prepare_route = _sig("gf_prepare_route", [_vp, _i64, _i64, ctypes.POINTER(RouteOpts), _vp, _vp, ctypes.POINTER(_vp)])
 _gemv_experts = _sig("gemv_experts", [ctypes.POINTER(Experts), _vp, _i64, _vp, _vp, _vp])
 _prepare_experts = _sig("gf_prepare_experts", [ctypes.POINTER(Experts), _vp, _i64, _vp, _vp, ctypes.POINTER(_vp)])
+_plan_experts = _sig("gf_plan_experts", [ctypes.POINTER(Experts), _vp, _i64, _vp, _vp, ctypes.POINTER(_i64 * 8)])
+_plan_lora = _sig("gf_plan_lora", [_vp, _i32, _vp, _i64, _i64, _i32, _vp, _vp, ctypes.POINTER(Lora),
+                                   ctypes.POINTER(GfOpts), ctypes.POINTER(_i64 * 8)])
 _experts_workspace = _sig("gf_experts_workspace", [_i64] * 5, _i64)
 _gemv_lora = _sig("gemv_lora", [_vp, _i32, _vp, _i64, _i64, _i32, _vp, _vp, ctypes.POINTER(Lora),
                                 ctypes.POINTER(GfOpts), _vp])
@@ -507,6 +510,18 @@ def prepare_experts(W_gate, W_up, wtype, W_down, wtype_down, E, x, M, K, ids, we
                               rms_norm_weight)) if st == OK else st
 
 
+def plan_experts(W_gate, W_up, wtype, W_down, wtype_down, E, x, M, K, ids, weights, T, top_k, aux, dst, workspace,
+                 workspace_bytes=None, rms_norm_weight=None, rms_norm_eps=0.0, pdl=False):
+    """gf_plan_experts: (path, info) of gemv_experts(...) without launching: path 0 = nothing to launch,
+    2 = generic, 4 = tiled, <0 = error; info: columns of a group, whether gate and up, and down, run on
+    the wide kernel."""
+    ex = _experts_struct(W_gate, W_up, wtype, W_down, wtype_down, E, M, K, ids, weights, top_k, workspace,
+                         workspace_bytes, rms_norm_weight, rms_norm_eps, pdl)
+    info = (_i64 * 8)()
+    path = _plan_experts(ctypes.byref(ex), _ptr(x), T, _ptr(aux), _ptr(dst), ctypes.byref(info))
+    return path, dict(cols=info[0], wide=bool(info[1]), wide_down=bool(info[2]))
+
+
 def lora_workspace(ncols, M, K, rank, n):
     """Bytes of workspace gemv_lora needs for these sizes."""
     b = _lora_workspace(ncols, M, K, rank, n)
@@ -541,3 +556,16 @@ def prepare_lora(W, wtype, x, M, K, epilogue, aux, dst, A, B, atype, n, rank, id
     if check:
         _check(st, "gf_prepare_lora")
     return Prepared(h.value, (W, x, aux, dst, A, B, ids, scales, workspace, opts)) if st == OK else st
+
+
+def plan_lora(W, wtype, x, M, K, epilogue, aux, dst, A, B, atype, n, rank, ids, scales, workspace,
+              workspace_bytes=None, **opts):
+    """gf_plan_lora: (path, info) of the shared product of gemv_lora(...) without launching: plan()'s, or
+    path 4 = tiled with info: columns of a group, whether it runs on the wide kernel."""
+    o = make_opts(**opts)
+    lo = Lora(_ptr(A), _ptr(B), atype, n, rank, _ptr(ids), _ptr(scales), _ptr(workspace),
+              _nbytes(workspace, workspace_bytes))
+    info = (_i64 * 8)()
+    path = _plan_lora(_ptr(W), wtype, _ptr(x), M, K, epilogue, _ptr(aux), _ptr(dst), ctypes.byref(lo), ctypes.byref(o),
+                      ctypes.byref(info))
+    return path, dict(cols=info[0], wide=bool(info[1])) if path == 4 else dict(zip(_PLAN_KEYS, list(info)))

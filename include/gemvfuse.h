@@ -358,6 +358,12 @@ GF_API int gemv_experts(const gf_experts* ex, const float* x, int64_t T, const f
                         void* stream);
 GF_API int gf_prepare_experts(const gf_experts* ex, const float* x, int64_t T, const float* aux, float* dst,
                               gf_prepared** out);
+/* Which kernels gemv_experts would launch for these arguments (host only, launches nothing):
+ * 0 = none, 2 = generic, 4 = tiled, <0 = the gf_status the call would return.  `info` (may be
+ * NULL) receives of the tiled kernels {columns a group may have, wide kernel for gate and up
+ * (0, 1), wide kernel for down (0, 1)}. */
+GF_API int gf_plan_experts(const gf_experts* ex, const float* x, int64_t T, const float* aux, const float* dst,
+                           int64_t info[8]);
 /* Bytes of workspace for these sizes (any format); negative: a gf_status. */
 GF_API int64_t gf_experts_workspace(int64_t E, int64_t T, int64_t top_k, int64_t M, int64_t K);
 
@@ -388,6 +394,11 @@ GF_API int gemv_lora(const void* W, int wtype, const float* x, int64_t M, int64_
                      float* dst, const gf_lora* lora, const gf_opts* opts, void* stream);
 GF_API int gf_prepare_lora(const void* W, int wtype, const float* x, int64_t M, int64_t K, int epilogue,
                            const float* aux, float* dst, const gf_lora* lora, const gf_opts* opts, gf_prepared** out);
+/* Which kernel gemv_lora would run the shared product on (host only, launches nothing): as
+ * gf_plan, or 4 = tiled.  `info` (may be NULL) is gf_plan's, or of the tiled kernels {columns
+ * a group may have, wide kernel (0, 1)}. */
+GF_API int gf_plan_lora(const void* W, int wtype, const float* x, int64_t M, int64_t K, int epilogue, const float* aux,
+                        const float* dst, const gf_lora* lora, const gf_opts* opts, int64_t info[8]);
 /* Bytes of workspace for these sizes (any format); negative: a gf_status. */
 GF_API int64_t gf_lora_workspace(int64_t ncols, int64_t M, int64_t K, int64_t rank, int64_t n);
 
