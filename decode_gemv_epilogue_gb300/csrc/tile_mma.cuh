@@ -10,14 +10,17 @@
 // 32 bits: the only roundings are those of 32-bit sums (truncated ones in the matrix unit,
 // which is why its sums end with the block, and take the low parts first).
 //
-// Codes become f16 by masking alone: the f16 with the bits of a code c below 1024 is the
-// subnormal c 2^-24, which the matrix unit takes exactly.  It lines its products up by the
-// operands' exponents, though, a subnormal's being that of 2^-14: a code is placed high
-// enough (up to 255 for 8 bits, 64 times the code for 4) that what it drops stays at the level
-// of a 32-bit sum's rounding (4-bit codes in the lowest bits: an error of 5e-6 of the result;
-// 16 times the code: 5e-7).  The sums are in units of 2^-24 or 2^-18, taken back in the tail,
-// and the formats' offsets (8 and 128) enter with the block's sum, -offset times the sum of x
-// over the block: no instruction per weight is left but shifts and masks.
+// Codes become f16 by masks and, where the format has an offset (8 and 128), one packed
+// operation for two of them: the f16 with the bits 0x6400 | c is 1024 + c, and taking 1024 and
+// the offset off is exact.  (Leaving the offset to the block's sum, as -offset times the sum of
+// x, saves that operation but not a sum's rounding: an x of 1e5 among units on a weight of zero
+// moved the other weights' products by more than the parity bound.)  Q4_K's codes have none,
+// its mins being a term of the format's own definition: masked in place, the f16 with the bits
+// of 64 c is the subnormal c 2^-18, which the matrix unit takes exactly.  It lines its products
+// up by the operands' exponents, though, a subnormal's being that of 2^-14: a code is placed
+// high enough that what it drops stays at the level of a 32-bit sum's rounding (in the lowest
+// bits: an error of 5e-6 of the result; 16 times the code: 5e-7).  Its sums are in units of
+// 2^-18, taken back in the tail.
 //
 // Why mma.sync and not the asynchronous matrix unit: a block format's scale belongs to 32
 // weights of one row, so the accumulator of every 32 columns of K has to pass through
@@ -91,7 +94,7 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 // Packed columns lie in the order in which the matrix instruction takes them.  Eight columns
 // form a column tile, and for every 32 elements a column tile has one record:
 //   [step s of 2][column of cp][thread t of 4] 16 bytes {hi, hi, hi, hi, lo, lo, lo, lo},
-//   then per column {2^-s, the block's sum of x 2^s times pack_sum(format)};
+//   then per column {2^-s, for Q4_K the block's sum of x 2^s in the units of its sums};
 // cp = min(8, columns of the group) columns are stored, so that a single column does not move
 // eight (column tiles are allocated for the most any group of the call can have).  A warp's 16-byte reads of a step are then consecutive, and the records of a K chunk
 // are one piece of memory for one bulk copy.  Which four elements (s, t) holds is the
@@ -102,13 +105,10 @@ enum { ORDER_NIBBLE = 0, ORDER_BYTE = 1, ORDER_F16 = 2 };
 __host__ __device__ constexpr int pack_order(int wt) {
   return wt == WT_F16 ? ORDER_F16 : wt == WT_Q8_0 || wt == WT_F32 ? ORDER_BYTE : ORDER_NIBBLE;
 }
-// What the sum of a block is stored for: the offset of the codes, or Q4_K's mins, both in
-// the units of the accumulators.
-__host__ __device__ constexpr float pack_sum(int wt) {
-  return wt == WT_Q4_0 ? -8.0f * 0x1p-18f : wt == WT_Q8_0 ? -128.0f * 0x1p-24f : 0x1p-18f;
-}
+// Q4_K's mins multiply the sum of x over a block.
+__host__ __device__ constexpr bool pack_sums(int wt) { return wt == WT_Q4_K; }
 // Unit of the accumulators.
-__host__ __device__ constexpr float tile_unit(int wt) { return wt == WT_F16 || wt == WT_F32 ? 1.0f : wt == WT_Q8_0 ? 0x1p24f : 0x1p18f; }
+__host__ __device__ constexpr float tile_unit(int wt) { return wt == WT_Q4_K ? 0x1p18f : 1.0f; }
 __host__ __device__ constexpr int record_bytes(int cp) { return cp * 128 + (cp * 8 + 15) / 16 * 16; }
 // Byte offset in a record of the four elements 4q .. 4q + 3 of column c.
 __device__ __forceinline__ uint32_t record_offset(uint32_t q, uint32_t c, uint32_t cp, int order) {
@@ -146,8 +146,7 @@ __device__ __forceinline__ uint32_t half_pair(__half a, __half b) {
 __device__ __forceinline__ float value_of(const HiLo& p) { return __half2float(p.hi) + __half2float(p.lo); }
 
 // Four consecutive scaled elements as the 16 bytes of a packed group, and the sum of what these
-// hold: what stands in for the codes' offset has to be the sum of the same values that the codes
-// are multiplied by.
+// hold: the mins multiply the sum of the same values that the codes multiply.
 __device__ __forceinline__ uint4 pack_group(float4 v, bool swapped, float& sum) {
   const HiLo a = split_hi_lo(v.x), b = split_hi_lo(v.y), c = split_hi_lo(v.z), d = split_hi_lo(v.w);
   sum = (value_of(a) + value_of(b)) + (value_of(c) + value_of(d));
@@ -173,7 +172,7 @@ __device__ inline void pack_column(const float* x, int c, int i0, int share, con
                                    int cp, uint8_t* base, float* wmax) {
   const int lane = threadIdx.x & 31;
   const int n4 = K / 4, order = pack_order(fmt);
-  const float sumf = pack_sum(fmt);
+  const bool sums = pack_sums(fmt);
   const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(gamma)) & 15u) == 0;
   auto four = [&](const float* p, int i) -> float4 {
     if (vec) return reinterpret_cast<const float4*>(p)[i];
@@ -225,12 +224,13 @@ __device__ inline void pack_column(const float* x, int c, int i0, int share, con
     v.x *= sc; v.y *= sc; v.z *= sc; v.w *= sc;
     float sum;
     const uint4 packed = pack_group(v, order == ORDER_NIBBLE, sum);
+    if (sums)
 #pragma unroll
-    for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (x != nullptr && i < n4) {
       uint8_t* r = base + static_cast<int64_t>(i >> 3) * rec;
       *reinterpret_cast<uint4*>(r + record_offset(i & 7, c, cp, order)) = packed;
-      if ((i & 7) == 0) *reinterpret_cast<float2*>(r + cp * 128 + c * 8) = make_float2(inv, sum * sumf);
+      if ((i & 7) == 0) *reinterpret_cast<float2*>(r + cp * 128 + c * 8) = make_float2(inv, sums ? sum / tile_unit(WT_Q4_K) : 0.0f);
     }
   };
 #pragma unroll
@@ -252,7 +252,19 @@ __device__ __forceinline__ void q4k_scale_of(const uint4 hd, uint32_t j, float& 
   dmn = h2f(hd.x >> 16) * (__uint_as_float(0x4B000000u | mn) - kMagic);
 }
 
-constexpr uint32_t kNibbles = 0x03C003C0u;  // two 4-bit codes as 64 c 2^-24
+constexpr uint32_t kNibbles = 0x03C003C0u;  // two 4-bit codes as c 2^-18
+
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 bits_half2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+// 1024 + c of two codes (f16) -> c - OFF.
+template <int OFF>
+__device__ __forceinline__ uint32_t code_pair(uint32_t u) {
+  return half2_bits(__hsub2(bits_half2(u), __half2half2(__int2half_rn(1024 + OFF))));
+}
+// 1024 + 16 c -> c - 8.
+__device__ __forceinline__ uint32_t code_pair_16(uint32_t u) {
+  return half2_bits(__hfma2(bits_half2(u), __float2half2_rn(0.0625f), __float2half2_rn(-72.0f)));
+}
 
 // One lane's place in a row of a stage: what it reads of its warp's block.
 struct RowPlace {
@@ -300,10 +312,10 @@ __device__ __forceinline__ void load_block_row(const RowPlace& p, uint32_t off, 
     }
     u ^= 0x80808080u;  // q + 128
     v ^= 0x80808080u;
-    a0[0] = __byte_perm(u, 0u, 0x4140);
-    a0[1] = __byte_perm(u, 0u, 0x4342);
-    a1[0] = __byte_perm(v, 0u, 0x4140);
-    a1[1] = __byte_perm(v, 0u, 0x4342);
+    a0[0] = code_pair<128>(__byte_perm(u, 0x64646464u, 0x4140));
+    a0[1] = code_pair<128>(__byte_perm(u, 0x64646464u, 0x4342));
+    a1[0] = code_pair<128>(__byte_perm(v, 0x64646464u, 0x4140));
+    a1[1] = code_pair<128>(__byte_perm(v, 0x64646464u, 0x4342));
   } else if constexpr (WT == WT_Q4_K) {  // scale and min come apart elsewhere
     const uint32_t w = lds32(p.code + off), v = lds32(p.code + off + 16u);
     a0[0] = (w << p.left) & kNibbles;
@@ -315,10 +327,11 @@ __device__ __forceinline__ void load_block_row(const RowPlace& p, uint32_t off, 
     d = h2f(lds16(p.scale + off));
     uint32_t w = lds32(p.code + off);
     if constexpr (!WHOLE) w = __funnelshift_r(w, lds32(p.code + off + 4u), p.shift);
-    a0[0] = (w << 6) & kNibbles;  // elements 4t, 4t + 2
-    a0[1] = (w >> 2) & kNibbles;  // 4t + 1, 4t + 3
-    a1[0] = (w << 2) & kNibbles;  // the same + 16
-    a1[1] = (w >> 6) & kNibbles;
+    const uint32_t v = w >> 8;
+    a0[0] = code_pair<8>((w & 0x000F000Fu) | 0x64006400u);   // elements 4t, 4t + 2
+    a0[1] = code_pair<8>((v & 0x000F000Fu) | 0x64006400u);   // 4t + 1, 4t + 3
+    a1[0] = code_pair_16((w & 0x00F000F0u) | 0x64006400u);   // the same + 16
+    a1[1] = code_pair_16((v & 0x00F000F0u) | 0x64006400u);
   }
 }
 
@@ -443,8 +456,7 @@ struct TileLane {
 template <int WT, int MODE, int NTA, int NT, bool PER1, bool WHOLE, bool FEW>
 __device__ __forceinline__ void tile_block(const TileLane& l, uint32_t st, uint32_t xs, uint32_t blk,
                                            float (&acc)[4][NT][4]) {
-  constexpr bool kMeta = MODE == TILE_DOWN || WT != WT_F16;  // per-block scales or sums are read here
-  constexpr bool kOffset = WT == WT_Q4_0 || WT == WT_Q8_0;   // the sums are the codes' offset
+  constexpr bool kMeta = MODE == TILE_DOWN || pack_sums(WT);  // per-block scales or sums are read here
   constexpr uint32_t kP = tile_pitch<WT>(1);
   const uint32_t step8 = WT == WT_F16 ? 1024u : PER1 ? 8u * kP : l.step8;
   const uint32_t step16 = WT == WT_F16 ? 2048u : PER1 ? 16u * kP : l.step16;
@@ -466,7 +478,7 @@ __device__ __forceinline__ void tile_block(const TileLane& l, uint32_t st, uint3
       const uint2 u = lds64(xa + l.m0), v = lds64(xa + l.m1);
       meta[n][0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
       meta[n][1] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
-      if constexpr (FEW) {  // a column's sum counts once, beside its hi part
+      if constexpr (FEW && pack_sums(WT)) {  // a column's sum counts once, beside its hi part
         meta[n][0].y = l.t4 < 2u ? meta[n][0].y : 0.0f;
         meta[n][1].y = l.t4 < 2u ? meta[n][1].y : 0.0f;
       }
@@ -535,7 +547,6 @@ __device__ __forceinline__ void tile_block(const TileLane& l, uint32_t st, uint3
         for (int i = 0; i < 4; ++i) {  // row row8 (0, 1) or row8 + 8 (2, 3), column 2t + (i & 1)
           const int h = i >> 1, c = i & 1;
           float& o = acc[mg + j][n][i];
-          if constexpr (kOffset) s[j][n][i] += meta[n][c].y;
           if constexpr (MODE == TILE_DOWN) {
             float v = WT == WT_F16 ? s[j][n][i] : d[j][h] * s[j][n][i];
             if constexpr (WT == WT_Q4_K) v = fmaf(-dm[j][h], meta[n][c].y, v);
@@ -892,8 +903,9 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(WT, NT))
             const float sc = pack_scale(m), hs = h * sc;
             const HiLo p = split_hi_lo(hs);
             float sum = value_of(p);
+            if (pack_sums(a.out_format))
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+              for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             uint8_t* r = a.out_records + static_cast<int64_t>(g.w + n) * (a.rows / 32) * record_bytes(a.cp) +
                          static_cast<int64_t>(row0 / 32) * l.rec;
             const int order = pack_order(a.out_format);
@@ -904,7 +916,7 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(WT, NT))
             *reinterpret_cast<__half*>(r + at + 8) = p.lo;
             if (lane == 0)
               *reinterpret_cast<float2*>(r + l.cp * 128u + static_cast<uint32_t>(wk) * 8u) =
-                  make_float2(pow2_inverse(sc), sum * pack_sum(a.out_format));
+                  make_float2(pow2_inverse(sc), pack_sums(a.out_format) ? sum / tile_unit(WT_Q4_K) : 0.0f);
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {

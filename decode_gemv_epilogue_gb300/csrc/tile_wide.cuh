@@ -97,14 +97,17 @@ __device__ __forceinline__ void wide_pair(const TileLane& l, uint32_t row, uint3
             load_block_row<WT, false>(p, 0u, a0[m][h], a1[m][h], d[m][h]);
         }
       }
-    constexpr bool kOffset = WT == WT_Q4_0 || WT == WT_Q8_0;
     // column tile by column tile: few registers, so that four warps a scheduler hide the latency
 #pragma unroll
     for (int n = 0; n < NTA; ++n) {
       const uint32_t xa = xo + static_cast<uint32_t>(n) * l.xtile;
       const uint4 b0 = lds128(xa + l.xlane), b1 = lds128(xa + l.xlane + l.cp * 64u);
-      const uint2 u = lds64(xa + l.m0), v = lds64(xa + l.m1);  // {2^-s, sum} of columns 2t and 2t + 1
-      const float sx[2] = {__uint_as_float(u.x), __uint_as_float(v.x)}, xsum[2] = {__uint_as_float(u.y), __uint_as_float(v.y)};
+      float sx[2] = {0.0f, 0.0f}, xsum[2] = {0.0f, 0.0f};  // 2^-s and sum of columns 2t and 2t + 1
+      if constexpr (MODE == TILE_DOWN || pack_sums(WT)) {
+        const uint2 u = lds64(xa + l.m0), v = lds64(xa + l.m1);
+        sx[0] = __uint_as_float(u.x); sx[1] = __uint_as_float(v.x);
+        xsum[0] = __uint_as_float(u.y); xsum[1] = __uint_as_float(v.y);
+      }
       float s[2][4];
       auto step = [&](int i) {  // lo of both k-steps, then hi (see tile_block)
         const uint32_t p = i == 0 ? b0.z : i == 1 ? b1.z : i == 2 ? b0.x : b1.x;
@@ -128,7 +131,6 @@ __device__ __forceinline__ void wide_pair(const TileLane& l, uint32_t row, uint3
         for (int i = 0; i < 4; ++i) {  // row g + 8 (i / 2), column 2t + i % 2
           const int h = i >> 1, c = i & 1;
           float& r = acc[m][n][i];
-          if constexpr (kOffset) s[m][i] += xsum[c];
           if constexpr (MODE == TILE_DOWN) {
             float y = d[m][h] * s[m][i];
             if constexpr (WT == WT_Q4_K) y = fmaf(-dm[m][h], xsum[c], y);
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
               }
               if (g4 == 0 && !(w & 1))
                 *reinterpret_cast<float2*>(r + cp * 128u + col * 8u) =
-                    make_float2(pow2_inverse(sc), (u.y + v.y) * sc * pack_sum(a.out_format));
+                    make_float2(pow2_inverse(sc), pack_sums(a.out_format) ? (u.y + v.y) * sc / tile_unit(WT_Q4_K) : 0.0f);
             }
           }
         }

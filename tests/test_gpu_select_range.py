@@ -1,0 +1,155 @@
+"""Dynamic range of x, and of the gated values, in the tiled products of gemv_experts and
+gemv_lora: outliers on columns whose weights are zero.  Gated on the literal bound of each
+product, as tests/test_gpu_int_dot.py gates the single-column kernels; each case asserts the
+kernel that its shape takes."""
+
+import numpy as np
+import pytest
+
+from decode_gemv_epilogue_gb300 import synth
+from gpu_util import assert_within, dev_tensor
+from oracle import quant as oquant
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import test_gpu_experts  # noqa: E402
+import test_gpu_lora  # noqa: E402
+from test_gpu_int_dot import zero_weight_columns  # noqa: E402
+
+F32, F16, Q8, Q4, Q4K = synth.F32, synth.F16, synth.Q8_0, synth.Q4_0, synth.Q4_K
+SPIKES = (5, 70, 71, 263)  # 70 and 71 share a block; of Q4_K's sub-blocks 0..3
+
+
+@pytest.fixture(scope="module")
+def G(lib):
+    assert lib.device_status(reset=True) == 0
+    yield lib
+    assert lib.device_status() == 0, "a kernel reported a bounded-wait timeout"
+
+
+def zero_columns(raw, wt, rows, K, cols):
+    if wt in (F32, F16):
+        w = raw.copy().view(np.float32 if wt == F32 else np.float16).reshape(rows, K)
+        w[:, list(cols)] = 0
+        return w.reshape(-1).view(np.uint8)
+    return zero_weight_columns(raw, wt, rows, K, cols)
+
+
+def spiked(x, cols, size):
+    """x with spikes of +-size on `cols` in every second row."""
+    x = x.copy()
+    x[::2, list(cols)] = size * np.where(np.arange(len(cols)) % 2 == 0, 1.0, -1.0)
+    return x.astype(np.float32)
+
+
+# (T, E, k, M, K) and the columns of a group: one, few, one tile, several, the wide kernel
+EXPERTS = {
+    "one": (1, 4, 3, 256, 512, 1),
+    "few": (3, 4, 2, 256, 512, 3),
+    "tile": (9, 3, 2, 256, 512, 8),
+    "wide": (256, 4, 4, 512, 512, 16),
+}
+
+
+def experts_case(G, wt, kind, seed):
+    T, E, k, M, K, cols = EXPERTS[kind]
+    if wt in (F32, F16):
+        cols = {"tile": 16, "wide": 24}.get(kind, cols)
+    c = test_gpu_experts.Case(G, T, E, k, M, K, wt, wt, seed=seed)
+    ws = torch.empty(G.experts_workspace(E, T, k, M, K), dtype=torch.uint8, device="cuda")
+    path, info = G.plan_experts(c.dev[0], c.dev[1], wt, c.dev[2], wt, E, dev_tensor(c.x), M, K, dev_tensor(c.ids),
+                                dev_tensor(c.w), T, k, None, torch.empty(T * K, device="cuda"), ws)
+    assert path == 4 and info["cols"] == cols
+    return c
+
+
+def set_raw(c, i, raw):
+    c.raw[i], c.dev[i] = raw, dev_tensor(raw)
+
+
+@pytest.mark.parametrize("wt", [F32, F16, Q8, Q4, Q4K])
+@pytest.mark.parametrize("kind", list(EXPERTS))
+@pytest.mark.parametrize("size", [1e3, 1e5, 1e6])
+def test_experts_outliers_of_x(G, wt, kind, size):
+    c = experts_case(G, wt, kind, seed=300)
+    for i in (0, 1):
+        set_raw(c, i, zero_columns(c.raw[i], wt, c.E * c.M, c.K, SPIKES))
+    x = spiked(c.x, SPIKES, size)
+    y, b = c.want(x=x)
+    assert_within(c.run(x=x), y, b, "spikes of %g" % size)
+
+
+def gated_spikes(c, wt, size):
+    """Weights whose gated values hold spikes of about `size` on the columns SPIKES[:3] of the down
+    product, which are zero there."""
+    cols = SPIKES[:3]
+    c.x[:, 0] = 1.0  # the up rows of the spikes take their size from this column
+    set_raw(c, 2, zero_columns(c.raw[2], wt, c.E * c.K, c.M, cols))
+    rb = oquant.row_bytes(wt, c.K)
+    for i in (0, 1):
+        raw = c.raw[i].copy().reshape(c.E, c.M, rb)
+        for m in cols:
+            if wt == F32:
+                raw[:, m].view(np.float32)[:, 0] = size if i else 3.0
+            elif wt == F16:
+                raw[:, m].view(np.float16)[:, 0] = min(size, 6e4) if i else 3.0
+            else:  # the first block's scale; its first code far from zero
+                d = np.frombuffer(np.float16(min(size / 4, 6e4) if i else 2.0).tobytes(), np.uint8)
+                raw[:, m, 0:2] = d
+                if wt == Q8:
+                    raw[:, m, 2:34] = 0
+                    raw[:, m, 2] = 100 if i else 2
+                elif wt == Q4:
+                    raw[:, m, 2:18] = 0x88
+                    raw[:, m, 2] = 0x8F if i else 0x8A
+                else:
+                    raw[:, m, 2:144] = 0  # no mins, scales 1 of sub-block 0 only
+                    raw[:, m, 4] = 1
+                    raw[:, m, 16] = 0x0F if i else 0x02
+        set_raw(c, i, raw.reshape(-1))
+
+
+@pytest.mark.parametrize("wt", [F32, F16, Q8, Q4, Q4K])
+@pytest.mark.parametrize("kind", list(EXPERTS))
+@pytest.mark.parametrize("size", [1e3, 1e5, 1e6])
+def test_experts_outliers_of_the_gated_values(G, wt, kind, size):
+    c = experts_case(G, wt, kind, seed=310)
+    gated_spikes(c, wt, size)
+    y, b = c.want()
+    assert_within(c.run(), y, b, "gated spikes of %g" % size)
+
+
+# (N, M, K) and the columns of a group
+LORA = {"few": (3, 16384, 2816, 3), "tile": (8, 8200, 2048, 8), "two": (40, 300, 512, 8), "wide": (250, 4500, 512, 16)}
+
+
+def lora_case(G, wt, kind, seed):
+    N, M, K, cols = LORA[kind]
+    if wt in (F32, F16):
+        if kind != "two":
+            pytest.skip("plain rows have one kernel here")
+        N, M, K, cols = 40, 2100, 512 if wt == F32 else 480, 16  # (F16 rows of whole 64s go to another)
+    c = test_gpu_lora.Case(G, N, M, K, wt, 3, 8, F16, seed=seed)
+    path, info = G.plan_lora(c.Wd, wt, dev_tensor(c.x), M, K, 0, None, torch.empty(N * M, device="cuda"), c.Ad, c.Bd, F16,
+                             c.n, c.r, dev_tensor(c.ids), None,
+                             torch.empty(G.lora_workspace(N, M, K, c.r, c.n), dtype=torch.uint8, device="cuda"), ncols=N)
+    assert path == 4 and info["cols"] == cols
+    return c
+
+
+@pytest.mark.parametrize("wt", [F32, F16, Q8, Q4, Q4K])
+@pytest.mark.parametrize("kind", list(LORA))
+@pytest.mark.parametrize("size", [1e3, 1e5, 1e6])
+def test_lora_outliers_of_x(G, wt, kind, size):
+    c = lora_case(G, wt, kind, seed=320)
+    c.raw = zero_columns(c.raw, wt, c.M, c.K, SPIKES)
+    c.Wd = dev_tensor(c.raw)
+    c.A[:, :, list(SPIKES)] = 0
+    c.Ad = dev_tensor(c.A)
+    x = spiked(c.x, SPIKES, size)
+    y, b = c.want(2, x=x)
+    assert_within(c.run(2, x=x), y, b, "spikes of %g" % size)
