@@ -329,13 +329,15 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
         }
       if constexpr (MODE == TILE_GLU) {
         // the gated values of rows 8h + g (of the warp's 16) and columns 2t + c, in place of the
-        // gate sums
+        // gate sums; two warps make a block: they exchange its largest value and, for Q4_K's
+        // mins, the sum of what they pack
         float2* mx = xchg + (round & 1u) * (kWarps * 8 * NT);
+        const uint32_t pair = 1u + static_cast<uint32_t>(w >> 1);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float top = 0.0f, sum = 0.0f;
+            float top = 0.0f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int i = 2 * h + c;
@@ -343,45 +345,58 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
               const float v = tail_silu(acc[0][n][i] * f) * (acc[1][n][i] * f);
               acc[0][n][i] = v;
               top = fmaxf(top, finite_abs(v));
-              sum += v;
             }
 #pragma unroll
-            for (int o = 4; o <= 16; o <<= 1) {
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-              sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            }
-            if (g4 == 0) mx[w * 8 * NT + 8 * n + 2 * t4 + c] = make_float2(top, sum);
+            for (int o = 4; o <= 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (g4 == 0) mx[w * 8 * NT + 8 * n + 2 * t4 + c].x = top;
           }
-        named_bar_sync(1u + static_cast<uint32_t>(w >> 1), 64u);
+        named_bar_sync(pair, 64u);
         const int r0 = row0 + 32 * (w >> 1);
-        if (r0 < a.rows && ok && !*abort_flag) {
-          const int order = pack_order(a.out_format);
+        const bool write = r0 < a.rows && ok && !*abort_flag;
+        const int order = pack_order(a.out_format);
+        const bool sums = pack_sums(a.out_format);
+        auto record = [&](int n) {
+          return a.out_records + static_cast<int64_t>(g.w + n) * (a.rows / 32) * kRec + static_cast<int64_t>(r0 / 32) * rec;
+        };
+        auto scale_of = [&](int col) { return pack_scale(fmaxf(mx[(w & ~1) * 8 * NT + col].x, mx[(w | 1) * 8 * NT + col].x)); };
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            uint8_t* r = a.out_records + static_cast<int64_t>(g.w + n) * (a.rows / 32) * kRec +
-                         static_cast<int64_t>(r0 / 32) * rec;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t col = 2u * t4 + c;
-              if (8 * n + static_cast<int>(col) >= ncol) continue;
-              // in the order of the rows, whichever warp looks
-              const float2 u = mx[(w & ~1) * 8 * NT + 8 * n + col], v = mx[(w | 1) * 8 * NT + 8 * n + col];
-              const float sc = pack_scale(fmaxf(u.x, v.x));
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t col = 2u * t4 + c;
+            const bool in = write && 8 * n + static_cast<int>(col) < ncol;
+            const float sc = scale_of(8 * n + static_cast<int>(col));
+            float sum = 0.0f;
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t rr = 16u * (w & 1) + 8u * h + g4, i = rr & 3u;
-                const float hs = acc[0][n][2 * h + c] * sc;
-                const HiLo p = split_hi_lo(hs);
-                uint8_t* q = r + record_offset(rr >> 2, col, cp, order) +
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t rr = 16u * (w & 1) + 8u * h + g4, i = rr & 3u;
+              const HiLo p = split_hi_lo(acc[0][n][2 * h + c] * sc);
+              sum += value_of(p);
+              if (in) {
+                uint8_t* q = record(n) + record_offset(rr >> 2, col, cp, order) +
                              2u * (order == ORDER_NIBBLE ? ((i & 1u) << 1) | (i >> 1) : i);
                 *reinterpret_cast<__half*>(q) = p.hi;
                 *reinterpret_cast<__half*>(q + 8) = p.lo;
               }
-              if (g4 == 0 && !(w & 1))
-                *reinterpret_cast<float2*>(r + cp * 128u + col * 8u) =
-                    make_float2(pow2_inverse(sc), pack_sums(a.out_format) ? (u.y + v.y) * sc / tile_unit(WT_Q4_K) : 0.0f);
+            }
+            if (sums) {
+#pragma unroll
+              for (int o = 4; o <= 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+              if (g4 == 0) mx[w * 8 * NT + 8 * n + col].y = sum;
             }
           }
+        if (sums) named_bar_sync(pair, 64u);
+        if (write && g4 == 0 && !(w & 1)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int col = 8 * n + 2 * static_cast<int>(t4) + c;
+              if (col >= ncol) continue;
+              const float sum = sums ? (mx[w * 8 * NT + col].y + mx[(w + 1) * 8 * NT + col].y) / tile_unit(WT_Q4_K) : 0.0f;
+              *reinterpret_cast<float2*>(record(n) + cp * 128u + (2u * t4 + c) * 8u) =
+                  make_float2(pow2_inverse(scale_of(col)), sum);
+            }
         }
       } else if (ok && mine && !*abort_flag) {
 #pragma unroll

@@ -6,7 +6,9 @@ import pytest
 
 from decode_gemv_epilogue_gb300 import synth
 from gpu_util import assert_within, dev_tensor
+from oracle import gemv as ogemv
 from oracle import norm as onorm
+from oracle import select as osel
 from test_select_plan import WIDE
 
 pytestmark = pytest.mark.gpu
@@ -86,3 +88,24 @@ def test_non_finite_values_stay_in_their_token(G, case):
     got = c.run(w=w)
     assert np.all(np.isnan(got[99]))
     assert np.array_equal(np.delete(got, 99, 0).view(np.uint32), np.delete(ref, 99, 0).view(np.uint32))
+
+
+def test_large_gated_values(G):
+    """Gated values whose sum over a block is beyond float32 while each of them, and the product with
+    Q4_K's mins, is not."""
+    wg, wd, T, E, k, M, K = WIDE[-1]
+    c = wide_case(G, wg, wd, T, E, k, M, K, seed=240)
+    c.raw[1] = c.raw[0].copy()  # the same rows: silu(g) g > 0
+    c.dev[1] = c.dev[0]
+    x = c.x.astype(np.float64)
+    W0 = ogemv.quant.dequantize(osel.quant_rows(c.raw[0], E)[0], wg, M, K)
+    x[0] = np.linalg.solve(W0, np.full(M, 4.5e18))  # every gate of token 0 for expert 0
+    x = x.astype(np.float32)
+    h = ogemv.silu(W0 @ x[0]) * (W0 @ x[0])
+    assert h.max() < 3e37 and h.reshape(-1, 32).sum(1).min() > 4e38
+    ids, w = c.ids.copy(), c.w.copy()
+    ids[0], w[0] = -1, 0.0
+    ids[0, 0], w[0, 0] = 0, 0.25
+    y, b = c.want(ids=ids, x=x, w=w)
+    assert np.abs(y).max() < 1e38
+    assert_within(c.run(ids=ids, x=x, w=w), y, b)
