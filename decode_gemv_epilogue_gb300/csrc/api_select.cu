@@ -213,14 +213,14 @@ static int plan_experts(const gf_experts* ex, const float* x, int64_t T, const f
     pdl = true;  // each launch of a call may start early behind the one before it
   };
   if (some && experts_tiled(ex)) {
-    add(EXP_PREP, wg, nullptr, nullptr);
+    add(EXP_PREP, wg, ex->W_gate, ex->W_up);
     add(EXP_GLU, wg, ex->W_gate, ex->W_up);
     add(EXP_DOWN, wd, ex->W_down, nullptr);
   } else {
     if (some) add(EXP_GLU_GENERIC, wg, ex->W_gate, ex->W_up);
     add(EXP_DOWN_GENERIC, wd, ex->W_down, nullptr);  // M == 0: empty sums, y = 0
   }
-  add(EXP_COMBINE, wd, nullptr, nullptr);
+  add(EXP_COMBINE, wd, some && experts_tiled(ex) ? ex->W_down : nullptr, nullptr);
   return GF_OK;
 }
 

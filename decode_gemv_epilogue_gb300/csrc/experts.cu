@@ -77,17 +77,67 @@ __global__ void __launch_bounds__(32 * kExpGenericWarps) experts_generic_kernel(
   }
 }
 
-__global__ void __launch_bounds__(256) experts_combine_kernel(const __grid_constant__ ExpertsArgs a) {
+// Row `row` of all experts' rows of K columns times column c of column tile `tile` of the records.
+template <int WT>
+__device__ __forceinline__ float exact_row(const ExpertsArgs& a, const uint8_t* W, int64_t row, const uint8_t* records,
+                                           int tile, uint32_t c, uint32_t cp, int K) {
+  return exact_product<WT>(W + row * expert_row_bytes<WT>(K),
+                           records + static_cast<int64_t>(tile) * (K / 32) * record_bytes(a.cp), c, cp, K);
+}
+
+// The gated values of slot s, a raw column (column c of `tile`), by the CTA that packed it.
+template <int WT>
+__device__ __forceinline__ void exact_gated(const ExpertsArgs& a, int s, int tile, uint32_t c, uint32_t cp) {
+  if (threadIdx.x == 0) atomicAdd(a.err + 1, 1u);  // counted for gf_repair_count
+#pragma unroll 1
+  for (int b = threadIdx.x >> 5; b < a.M / 32; b += blockDim.x >> 5) {
+    const int64_t row = static_cast<int64_t>(a.ids[s]) * a.M + 32 * b + (threadIdx.x & 31);
+    float y[2];
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      const float v = exact_row<WT>(a, i ? a.W2 : a.W, row, a.xrec, tile, c, cp, a.K);
+      if (i == 0) y[0] = v;
+      else y[1] = v;
+    }
+    write_gated(tail_silu(y[0]) * y[1],
+                a.hrec + static_cast<int64_t>(tile) * (a.M / 32) * record_bytes(a.cp) +
+                    static_cast<int64_t>(b) * record_bytes(static_cast<int>(cp)),
+                c, cp, a.out_format);
+  }
+}
+
+// W: the down matrices, where their products are the tiles' (nullptr: the generic kernel's).
+// (Six CTAs an SM, five of the packing: the code of raw columns must not cost the others their warps.)
+template <int WT>
+__global__ void __launch_bounds__(256, 6) experts_combine_kernel(const __grid_constant__ ExpertsArgs a) {
   pdl_wait();
   pdl_trigger();
   const int t = blockIdx.y;
   const int m = blockIdx.x * 256 + threadIdx.x;
   if (m >= a.K) return;
   const int64_t o = static_cast<int64_t>(t) * a.K + m;
-  float s = a.aux ? a.aux[o] : 0.0f;
+  const float first = a.aux ? a.aux[o] : 0.0f;
+  float s = first;
   for (int j = 0; j < a.k; ++j) {
     const int e = a.ids[t * a.k + j];
     if (e >= 0 && e < a.E) s += a.y[static_cast<int64_t>(t * a.k + j) * a.K + m];
+  }
+  // (the slots one by one only here: a look at each of them above took 9 -> 25 us of 256 tokens)
+  if (!is_finite(s) && a.W) {
+    s = first;
+    for (int j = 0; j < a.k; ++j) {
+      const int e = a.ids[t * a.k + j];
+      if (e < 0 || e >= a.E) continue;
+      const float y = a.y[static_cast<int64_t>(t * a.k + j) * a.K + m];
+      if (is_finite(y)) {
+        s += y;
+      } else {
+        const int2 p = a.places[t * a.k + j];
+        atomicAdd(a.err + 1, 1u);  // counted for gf_repair_count
+        s += a.weights[t * a.k + j] * exact_row<WT>(a, a.W, static_cast<int64_t>(e) * a.K + m, a.hrec, p.x,
+                                                    static_cast<uint32_t>(p.y) & 255u, static_cast<uint32_t>(p.y) >> 8, a.M);
+      }
+    }
   }
   a.dst[o] = s;
 }
@@ -103,11 +153,12 @@ static int prep_smem(int E) { return 32 * E * 2 + 3 * E * 4; }
 // A short list (at most a slot a thread, groups of one column tile): every CTA packs one
 // slot's column, and finds its place by counting over all slots; the first one writes the
 // groups too.  Groups are numbered in the order of their first slots.
-__global__ void __launch_bounds__(kPackSlotThreads) experts_prep_short_kernel(const __grid_constant__ ExpertsArgs a) {
+template <int WT>
+__global__ void __launch_bounds__(kPackSlotThreads, 6) experts_prep_short_kernel(const __grid_constant__ ExpertsArgs a) {
   __shared__ int ids[kPackSlotThreads];
   __shared__ uint32_t leaders[kPackSlotThreads / 32];
   __shared__ int place[3];  // of this CTA's slot: group (-1: none), column, columns of the group
-  __shared__ float wmax[2 * kPackThreads / 32];
+  __shared__ float wmax[kPackWords];
   pdl_wait();
   pdl_trigger();
   const int S = a.T * a.k, s = threadIdx.x, mine = blockIdx.x, lane = s & 31;
@@ -156,9 +207,12 @@ __global__ void __launch_bounds__(kPackSlotThreads) experts_prep_short_kernel(co
     *a.n_groups = n;
   }
   __syncthreads();
+  if (s == 0) a.places[mine] = place[0] < 0 ? make_int2(-1, 0) : make_int2(place[0], place[1] | (place[2] << 8));
   if (place[0] < 0) return;
-  pack_column(a.x + static_cast<int64_t>(mine / a.k) * a.K, place[1], s, kPackSlotThreads, a.gamma, a.eps, a.K, a.wtype,
-              place[2], a.xrec + static_cast<int64_t>(place[0]) * (a.K / 32) * record_bytes(a.cp), wmax);
+  const bool raw = pack_column(a.x + static_cast<int64_t>(mine / a.k) * a.K, place[1], s, kPackSlotThreads, a.gamma, a.eps,
+                               a.K, a.wtype, place[2],
+                               a.xrec + static_cast<int64_t>(place[0]) * (a.K / 32) * record_bytes(a.cp), wmax);
+  if (raw) exact_gated<WT>(a, mine, place[0], static_cast<uint32_t>(place[1]), static_cast<uint32_t>(place[2]));
 }
 
 // The slots of each expert in slot order: a counting sort whose counts are kept per warp
@@ -274,15 +328,18 @@ __global__ void __launch_bounds__(kPrepThreads) experts_list_kernel(const __grid
   }
 }
 
-__global__ void __launch_bounds__(kPackSlotThreads) experts_pack_kernel(const __grid_constant__ ExpertsArgs a) {
-  __shared__ float wmax[2 * kPackThreads / 32];
+template <int WT>
+__global__ void __launch_bounds__(kPackSlotThreads, 5) experts_pack_kernel(const __grid_constant__ ExpertsArgs a) {
+  __shared__ float wmax[kPackWords];
   pdl_wait();
   pdl_trigger();
   const int s = blockIdx.x;
   const int2 p = a.places[s];  // {column tile, column | columns stored << 8}
   if (p.x < 0) return;
-  pack_column(a.x + static_cast<int64_t>(s / a.k) * a.K, p.y & 255, threadIdx.x, kPackSlotThreads, a.gamma, a.eps, a.K,
-              a.wtype, p.y >> 8, a.xrec + static_cast<int64_t>(p.x) * (a.K / 32) * record_bytes(a.cp), wmax);
+  const bool raw = pack_column(a.x + static_cast<int64_t>(s / a.k) * a.K, p.y & 255, threadIdx.x, kPackSlotThreads, a.gamma,
+                               a.eps, a.K, WT, p.y >> 8,
+                               a.xrec + static_cast<int64_t>(p.x) * (a.K / 32) * record_bytes(a.cp), wmax);
+  if (raw) exact_gated<WT>(a, s, p.x, static_cast<uint32_t>(p.y) & 255u, static_cast<uint32_t>(p.y) >> 8);
 }
 
 // ------------------------------------------------------------------ tiled products
@@ -349,6 +406,31 @@ static cudaError_t launch_generic_phase(const ExpertsArgs& a, cudaStream_t st, b
   }
 }
 
+// The kernels that hold the raw columns' code, one for each format.
+struct ExpertsShort {
+  template <int WT>
+  static constexpr auto kernel() { return experts_prep_short_kernel<WT>; }
+};
+struct ExpertsPack {
+  template <int WT>
+  static constexpr auto kernel() { return experts_pack_kernel<WT>; }
+};
+struct ExpertsCombine {
+  template <int WT>
+  static constexpr auto kernel() { return experts_combine_kernel<WT>; }
+};
+template <class KERNEL>
+static cudaError_t launch_wt(const ExpertsArgs& a, const cudaLaunchConfig_t& cfg) {
+  switch (a.wtype) {
+    case WT_F32: return cudaLaunchKernelEx(&cfg, KERNEL::template kernel<WT_F32>(), a);
+    case WT_F16: return cudaLaunchKernelEx(&cfg, KERNEL::template kernel<WT_F16>(), a);
+    case WT_Q8_0: return cudaLaunchKernelEx(&cfg, KERNEL::template kernel<WT_Q8_0>(), a);
+    case WT_Q4_0: return cudaLaunchKernelEx(&cfg, KERNEL::template kernel<WT_Q4_0>(), a);
+    case WT_Q4_K: return cudaLaunchKernelEx(&cfg, KERNEL::template kernel<WT_Q4_K>(), a);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
 int launch_experts(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
   cudaLaunchAttribute attr;
   switch (a.phase) {
@@ -357,7 +439,7 @@ int launch_experts(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
           config(dim3(static_cast<unsigned>(a.T * a.k)), kPackSlotThreads, st, pdl, &attr);
       // (fewer than eight tokens always come this way: their groups are narrower than a column
       // tile; measured, 8 and 42 slots: 6.5 us through the list, 3.7 and 4.6 so)
-      if (a.T * a.k <= kPackSlotThreads && a.cols <= 8) return cudaLaunchKernelEx(&pack, experts_prep_short_kernel, a);
+      if (a.T * a.k <= kPackSlotThreads && a.cols <= 8) return launch_wt<ExpertsShort>(a, pack);
       static int configured[64] = {0};
       int dev = 0;
       cudaGetDevice(&dev);
@@ -373,7 +455,7 @@ int launch_experts(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
       if (e != cudaSuccess) return e;
       cudaLaunchAttribute behind;
       const cudaLaunchConfig_t cfg = config(pack.gridDim, kPackSlotThreads, st, true, &behind);
-      return cudaLaunchKernelEx(&cfg, experts_pack_kernel, a);
+      return launch_wt<ExpertsPack>(a, cfg);
     }
     case EXP_GLU: return launch_tiles<TILE_GLU>(a, st, pdl);
     case EXP_DOWN: return launch_tiles<TILE_DOWN>(a, st, pdl);
@@ -382,7 +464,7 @@ int launch_experts(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
     case EXP_COMBINE: {
       const cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>((a.K + 255) / 256), static_cast<unsigned>(a.T)),
                                             256, st, pdl, &attr);
-      return cudaLaunchKernelEx(&cfg, experts_combine_kernel, a);
+      return launch_wt<ExpertsCombine>(a, cfg);
     }
     default: return cudaErrorInvalidValue;
   }

@@ -246,7 +246,7 @@ struct ExpertsArgs {
   int phase;
   int wtype;            // of this phase's matrices
   int out_format;       // of the weights that take the gated product's records
-  const uint8_t* W;     // gate (EXP_GLU*) or down (EXP_DOWN*)
+  const uint8_t* W;     // gate (EXP_PREP, EXP_GLU*) or down (EXP_DOWN*; EXP_COMBINE behind the tiles)
   const uint8_t* W2;    // up
   const float* x;
   const int32_t* ids;
@@ -264,7 +264,7 @@ struct ExpertsArgs {
   // workspace
   int32_t* slots;       // the slots of each group, one after another
   int4* groups;         // {expert, first entry, columns, first column tile} of each column group
-  int32_t* n_groups;    // their number; then the items of the two products taken so far
+  int32_t* n_groups;    // their number; the items of the two products taken so far
   int2* places;         // [T k] {column tile, column | columns stored << 8} of each slot, or {-1, 0}
   uint8_t* xrec;        // [column tile][K / 32] records of packed x (see tile_mma.cuh)
   uint8_t* hrec;        // the same of the gated values, or [T k][M] float32 (generic)

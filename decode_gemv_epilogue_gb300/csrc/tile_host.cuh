@@ -47,6 +47,7 @@ int launch_tile(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
   int e = tile_map<WT>(o.W, o.all_rows, t.row_bytes, &m0);
   if (e != cudaSuccess) return e;
   m1 = m0;
+  t.W = static_cast<const uint8_t*>(o.W);
   if (MODE == TILE_GLU) e = tile_map<WT>(o.W2, o.all_rows, t.row_bytes, &m1);
   if (e != cudaSuccess) return e;
   // The columns' records of whole groups where they leave three chunks of weights or more, in
@@ -139,6 +140,7 @@ int launch_wide(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
   int e = tile_map<WT>(o.W, o.all_rows, t.row_bytes, &m0);
   if (e != cudaSuccess) return e;
   m1 = m0;
+  t.W = static_cast<const uint8_t*>(o.W);
   if (MODE == TILE_GLU) e = tile_map<WT>(o.W2, o.all_rows, t.row_bytes, &m1);
   if (e != cudaSuccess) return e;
   const int stage = wide_stage_bytes<WT>(), fixed = kTileHeadBytes + wide_xchg<WT>() + 1024;

@@ -7,7 +7,7 @@
 namespace gf {
 
 __global__ void __launch_bounds__(kPackThreads) tile_pack_kernel(const __grid_constant__ LinArgs a) {
-  __shared__ float wmax[2 * kPackThreads / 32];
+  __shared__ float wmax[kPackWords];
   pdl_wait();
   pdl_trigger();
   // a CTA a column

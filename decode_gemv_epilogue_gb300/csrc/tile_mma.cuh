@@ -95,6 +95,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 // form a column tile, and for every 32 elements a column tile has one record:
 //   [step s of 2][column of cp][thread t of 4] 16 bytes {hi, hi, hi, hi, lo, lo, lo, lo},
 //   then per column {2^-s, for Q4_K the block's sum of x 2^s in the units of its sums};
+// or, in a block that the two parts cannot carry (an infinite or NaN x), four 32-bit elements
+// in place of the 16 bytes and {kRawBlock, their factor} behind them (all blocks of a packed
+// column, single blocks of the gated values);
 // cp = min(8, columns of the group) columns are stored, so that a single column does not move
 // eight (column tiles are allocated for the most any group of the call can have).  A warp's 16-byte reads of a step are then consecutive, and the records of a K chunk
 // are one piece of memory for one bulk copy.  Which four elements (s, t) holds is the
@@ -127,15 +130,20 @@ __device__ __forceinline__ float pow2_inverse(float p) {
   return __uint_as_float((254u << 23) - __float_as_uint(p));
 }
 
+// In place of a block's 2^-s where its elements are stored as they are: a NaN that no arithmetic
+// makes, so that every sum with that block is NaN too.
+constexpr uint32_t kRawBlock = 0x7FC0AC7Fu;
+__device__ __forceinline__ bool is_finite(float v) { return fabsf(v) <= 3.402823466e38f; }
+
 struct HiLo {
   __half hi, lo;
 };
-// x must be scaled already.  An infinite or NaN x stays so in hi, with lo = 0.
+// x must be scaled already.
 __device__ __forceinline__ HiLo split_hi_lo(float v) {
   HiLo r;
   r.hi = __float2half_rn(v);
   const float rest = v - __half2float(r.hi);
-  r.lo = __float2half_rn(fabsf(v) <= 65504.0f ? rest : 0.0f);
+  r.lo = __float2half_rn(rest);
   return r;
 }
 
@@ -154,21 +162,22 @@ __device__ __forceinline__ uint4 pack_group(float4 v, bool swapped, float& sum) 
                  : make_uint4(half_pair(a.hi, b.hi), half_pair(c.hi, d.hi), half_pair(a.lo, b.lo), half_pair(c.lo, d.lo));
 }
 __device__ __forceinline__ float finite_abs(float v) {
-  const float a = fabsf(v);
-  return a <= 3.402823466e38f ? a : 0.0f;  // Inf and NaN do not set the scale
+  return is_finite(v) ? fabsf(v) : 0.0f;  // Inf and NaN do not set the scale
 }
 
 // Column c of a column tile's records, by `share` consecutive threads (a multiple of 32) of a
 // CTA of kPackThreads, thread i0 of them; one scale for the whole column.  x: the column
 // (nullptr: none).  With gamma the column is first normalised, x / sqrt(mean(x^2) + eps)
 // gamma: gamma multiplies before packing, the root enters through the stored scale.  Every
-// thread of the CTA takes part.  wmax: 2 kPackThreads / 32 floats of shared memory.
+// thread of the CTA takes part.  wmax: kPackWords floats of shared memory.  Returns whether the
+// column went raw.
 constexpr int kPackThreads = 1024;
+constexpr int kPackWords = 3 * kPackThreads / 32;
 // Threads of a column when `columns` (1..8) share a CTA.
 __device__ __forceinline__ int pack_share(int columns) {
   return columns <= 1 ? 1024 : columns <= 2 ? 512 : columns <= 4 ? 256 : 128;
 }
-__device__ inline void pack_column(const float* x, int c, int i0, int share, const float* gamma, float eps, int K, int fmt,
+__device__ inline bool pack_column(const float* x, int c, int i0, int share, const float* gamma, float eps, int K, int fmt,
                                    int cp, uint8_t* base, float* wmax) {
   const int lane = threadIdx.x & 31;
   const int n4 = K / 4, order = pack_order(fmt);
@@ -191,7 +200,9 @@ __device__ inline void pack_column(const float* x, int c, int i0, int share, con
     }
     return v;
   };
-  auto top = [](float4 v) {
+  bool odd = false;  // an element is not finite
+  auto top = [&](float4 v) {
+    odd |= !is_finite(fabsf(v.x) + fabsf(v.y) + fabsf(v.z) + fabsf(v.w));
     return fmaxf(fmaxf(finite_abs(v.x), finite_abs(v.y)), fmaxf(finite_abs(v.z), finite_abs(v.w)));
   };
   constexpr int kKeep = 4;  // groups of four a thread keeps between the two passes
@@ -205,9 +216,11 @@ __device__ inline void pack_column(const float* x, int c, int i0, int share, con
   m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  odd = __any_sync(0xffffffffu, odd);
   if (lane == 0) {
     wmax[threadIdx.x >> 5] = m;
     wmax[kPackThreads / 32 + (threadIdx.x >> 5)] = ss;
+    wmax[2 * kPackThreads / 32 + (threadIdx.x >> 5)] = odd ? 1.0f : 0.0f;
   }
   __syncthreads();
   ss = 0.0f;
@@ -215,12 +228,21 @@ __device__ inline void pack_column(const float* x, int c, int i0, int share, con
   for (int q = 0; q < share / 32; ++q) {
     m = fmaxf(m, wmax[w0 + q]);
     ss += wmax[kPackThreads / 32 + w0 + q];
+    odd |= wmax[2 * kPackThreads / 32 + w0 + q] != 0.0f;
   }
   const float sc = pack_scale(m);
-  float inv = pow2_inverse(sc);
-  if (gamma != nullptr) inv *= 1.0f / sqrtf(ss / static_cast<float>(K) + eps);
+  const float root = gamma != nullptr ? 1.0f / sqrtf(ss / static_cast<float>(K) + eps) : 1.0f;
+  const float inv = pow2_inverse(sc) * root;
   const int rec = record_bytes(cp);
   auto put = [&](int i, float4 v) {
+    if (odd) {
+      if (x != nullptr && i < n4) {
+        uint8_t* r = base + static_cast<int64_t>(i >> 3) * rec;
+        *reinterpret_cast<float4*>(r + record_offset(i & 7, c, cp, order)) = v;
+        if ((i & 7) == 0) *reinterpret_cast<float2*>(r + cp * 128 + c * 8) = make_float2(__uint_as_float(kRawBlock), root);
+      }
+      return;
+    }
     v.x *= sc; v.y *= sc; v.z *= sc; v.w *= sc;
     float sum;
     const uint4 packed = pack_group(v, order == ORDER_NIBBLE, sum);
@@ -237,6 +259,7 @@ __device__ inline void pack_column(const float* x, int c, int i0, int share, con
   for (int j = 0; j < kKeep; ++j) put(i0 + share * j, keep[j]);
   for (int b = share * kKeep; b < n4; b += share) put(b + i0, load(b + i0, false));
   __syncthreads();  // wmax may be used again
+  return odd;
 }
 
 // ------------------------------------------------------------------ A fragments
@@ -423,6 +446,7 @@ struct TileArgs {
   int max_groups;           // entries `groups` has room for
   uint32_t* next;           // wide kernel, but for TILE_LIN: the next item to be taken (zero at the start)
   const int32_t* slots;     // slot of each entry
+  const uint8_t* W;         // TILE_LIN: the matrix, for raw columns (the stages are filled by tensor maps)
   const uint8_t* records;   // [column tile][K / 32] records of x
   int cp;                   // most columns stored per column tile
   int NS;
@@ -439,6 +463,87 @@ struct TileArgs {
   int ncols, group_cols;    // TILE_LIN: columns of the batch, of a group (no list of groups)
   int item_rows;            // wide kernel, TILE_LIN: rows of an item
 };
+
+// ------------------------------------------------------------------ raw columns
+// A raw column's sums in the tiles are NaN and go nowhere.  Its products are taken element by
+// element: the gated ones by the launch that packs it, which the tiles follow (in the tiles'
+// kernel this code took 3 to 7% of every call's time without running), a batch's behind the
+// tiles' own; and a down product that a raw block made NaN by the combination.
+//
+// One row times one packed column in 32 bits, every lane its own row: lean, not quick, since the
+// kernels that hold it pay for its registers (and, where it needs a stack, at every launch).
+// rec: the column tile's first record, cp columns stored, this one c.
+template <int WT>
+__device__ __forceinline__ float exact_product(const uint8_t* row, const uint8_t* rec, uint32_t c, uint32_t cp, int K) {
+  constexpr int kOrder = pack_order(WT);
+  float sum = 0.0f, s = 0.0f;
+#pragma unroll 1
+  for (int k = 0; k < K; ++k) {
+    const uint32_t i = k & 3;
+    const float2 meta = *reinterpret_cast<const float2*>(rec + cp * 128u + c * 8u);
+    const uint8_t* at = rec + record_offset((k >> 2) & 7, c, cp, kOrder);
+    float x;
+    if (__float_as_uint(meta.x) == kRawBlock) {
+      x = meta.y * reinterpret_cast<const float*>(at)[i];
+    } else {
+      const __half* h = reinterpret_cast<const __half*>(at) + (kOrder == ORDER_NIBBLE ? ((i & 1u) << 1) | (i >> 1) : i);
+      x = meta.x * (__half2float(h[0]) + __half2float(h[4]));
+    }
+    s = fmaf(decode_elem<WT>(row, k), x, s);
+    if ((k & 31) == 31) {  // block by block, as the tiles
+      sum += s;
+      s = 0.0f;
+      rec += record_bytes(static_cast<int>(cp));
+    }
+  }
+  return sum;
+}
+
+// A block of 32 gated values of one column, a lane's each, into its record r (cp columns stored,
+// this one c) for a product in format fmt.
+__device__ __forceinline__ void write_gated(float h, uint8_t* r, uint32_t c, uint32_t cp, int fmt) {
+  const uint32_t lane = threadIdx.x & 31u, i = lane & 3u;
+  const int order = pack_order(fmt);
+  const uint32_t at = record_offset(lane >> 2, c, cp, order);
+  float2 meta;
+  if (__any_sync(0xffffffffu, !is_finite(h))) {
+    *reinterpret_cast<float*>(r + at + 4u * i) = h;
+    meta = make_float2(__uint_as_float(kRawBlock), 1.0f);
+  } else {
+    const float sc = pack_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(h)))));
+    const HiLo p = split_hi_lo(h * sc);
+    float sum = value_of(p);
+    if (pack_sums(fmt))
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const uint32_t place = at + 2u * (order == ORDER_NIBBLE ? ((i & 1u) << 1) | (i >> 1) : i);
+    *reinterpret_cast<__half*>(r + place) = p.hi;
+    *reinterpret_cast<__half*>(r + place + 8u) = p.lo;
+    meta = make_float2(pow2_inverse(sc), pack_sums(fmt) ? sum / tile_unit(WT_Q4_K) : 0.0f);
+  }
+  if (lane == 0) *reinterpret_cast<float2*>(r + cp * 128u + c * 8u) = meta;
+}
+
+__device__ __forceinline__ const uint8_t* column_records(const TileArgs& a, const int4& g, int col) {
+  return a.records + (g.w + col / 8) * (static_cast<int64_t>(a.K / 32) * record_bytes(a.cp));
+}
+// Whether column col of group g is raw.
+__device__ __forceinline__ bool raw_column(const TileArgs& a, const int4& g, int col) {
+  const uint32_t cp = static_cast<uint32_t>(min(8, g.z));
+  return *reinterpret_cast<const uint32_t*>(column_records(a, g, col) + cp * 128u + (col & 7) * 8u) == kRawBlock;
+}
+// TILE_LIN: the 32 output rows from row0 of a raw column of group g, by a warp.
+template <int WT>
+__device__ __forceinline__ void exact_rows(const TileArgs& a, const int4& g, int col, int row0) {
+  const int lane = threadIdx.x & 31, r = row0 + lane;
+  if (lane == 0) atomicAdd(a.err + 1, 1u);  // counted for gf_repair_count
+  const float y = exact_product<WT>(a.W + static_cast<int64_t>(min(r, a.rows - 1)) * a.row_bytes, column_records(a, g, col),
+                                    static_cast<uint32_t>(col) & 7u, static_cast<uint32_t>(min(8, g.z)), a.K);
+  if (r < a.rows) {
+    const int64_t o = (static_cast<int64_t>(g.w) * 8 + col) * a.out_ld + r;
+    a.out[o] = apply_tail(a.epi, y, epi_takes_aux(a.epi) ? a.aux[o] : 0.0f);  // aux may be out
+  }
+}
 
 // One lane's constants of the walk over a stage.
 struct TileLane {
@@ -782,7 +887,7 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(WT, NT))
     auto group_bar = [&]() { named_bar_sync(1u, 32u * kTileWarps); };
     int slot = 0, gi = 0, tile = tile_lo;
     uint32_t phase = 0;
-    bool ok = true;
+    bool ok = true, raw = false;  // raw: one of this warp's columns was
     for (int it = 0; it < n_items; ++it) {
       const int4 g = groups[g_at + gi];
       const int row0 = tile * kOutRows;
@@ -883,7 +988,9 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(WT, NT))
             red[(wk * 8 + 2 * l.t4 + (i & 1)) * kRedPitch + 16 * m + l.row8 + 8 * (i >> 1)] = acc[m][n][i];
         group_bar();
         const int c = 8 * n + wk;
-        if (c < ncol && ok && !*abort_flag) {
+        if (MODE != TILE_DOWN && c < ncol && __float_as_uint(factor[n]) == kRawBlock) {
+          raw = true;  // not this kernel's (TILE_GLU), or later
+        } else if (c < ncol && ok && !*abort_flag) {
           float v[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -898,25 +1005,10 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(WT, NT))
           if constexpr (MODE == TILE_GLU) {
             // 32 output rows of the gated product (rows are a multiple of 32): one record's column
             const float gv = v[0] * tile_unit(WT) * factor[n], uv = v[1] * tile_unit(WT) * factor[n];
-            const float h = tail_silu(gv) * uv;
-            const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(finite_abs(h))));
-            const float sc = pack_scale(m), hs = h * sc;
-            const HiLo p = split_hi_lo(hs);
-            float sum = value_of(p);
-            if (pack_sums(a.out_format))
-#pragma unroll
-              for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            uint8_t* r = a.out_records + static_cast<int64_t>(g.w + n) * (a.rows / 32) * record_bytes(a.cp) +
-                         static_cast<int64_t>(row0 / 32) * l.rec;
-            const int order = pack_order(a.out_format);
-            const uint32_t i = static_cast<uint32_t>(lane) & 3u;
-            const uint32_t at = record_offset(static_cast<uint32_t>(lane) >> 2, static_cast<uint32_t>(wk), l.cp, order) +
-                                2u * (order == ORDER_NIBBLE ? ((i & 1u) << 1) | (i >> 1) : i);
-            *reinterpret_cast<__half*>(r + at) = p.hi;
-            *reinterpret_cast<__half*>(r + at + 8) = p.lo;
-            if (lane == 0)
-              *reinterpret_cast<float2*>(r + l.cp * 128u + static_cast<uint32_t>(wk) * 8u) =
-                  make_float2(pow2_inverse(sc), pack_sums(a.out_format) ? sum / tile_unit(WT_Q4_K) : 0.0f);
+            write_gated(tail_silu(gv) * uv,
+                        a.out_records + static_cast<int64_t>(g.w + n) * (a.rows / 32) * record_bytes(a.cp) +
+                            static_cast<int64_t>(row0 / 32) * l.rec,
+                        static_cast<uint32_t>(wk), l.cp, a.out_format);
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -939,6 +1031,15 @@ __global__ void __launch_bounds__(kTileThreads, tile_ctas(WT, NT))
         ++gi;
       }
     }
+    // a batch's raw columns
+    if (MODE == TILE_LIN && raw && ok && !*abort_flag)
+      for (int64_t it = lo; it < hi; ++it) {
+        const int4 g = groups[g_at + static_cast<int>(it / tiles) - g_lo];
+        const int row0 = static_cast<int>(it % tiles) * kOutRows;
+        for (int c = wk; c < g.z; c += 8)
+          if (raw_column(a, g, c))
+            for (int r = row0; r < min(row0 + kOutRows, a.rows); r += 32) exact_rows<WT>(a, g, c, r);
+      }
   }
   __syncthreads();
 }

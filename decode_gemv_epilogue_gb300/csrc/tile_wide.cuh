@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
     l.t4 = t4;
     int slot = 0;
     uint32_t phase = 0;
-    bool ok = true;
+    bool ok = true, raw = false;  // raw: a column was
     for (uint32_t round = 0;; ++round) {
       // the item's first chunk, or the end
       ok = __all_sync(0xffffffffu, ok && mbar_wait_or_abort(full0 + 8u * slot, phase, abort_flag, a.err));
@@ -327,6 +327,9 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
             }
           }
         }
+      if constexpr (MODE == TILE_LIN)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) raw |= __float_as_uint(factor[n][0]) == kRawBlock || __float_as_uint(factor[n][1]) == kRawBlock;
       if constexpr (MODE == TILE_GLU) {
         // the gated values of rows 8h + g (of the warp's 16) and columns 2t + c, in place of the
         // gate sums; two warps make a block: they exchange its largest value and, for Q4_K's
@@ -338,6 +341,7 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             float top = 0.0f;
+            bool odd = false;  // a value is not finite: the block goes raw
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int i = 2 * h + c;
@@ -345,7 +349,9 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
               const float v = tail_silu(acc[0][n][i] * f) * (acc[1][n][i] * f);
               acc[0][n][i] = v;
               top = fmaxf(top, finite_abs(v));
+              odd |= !is_finite(v);
             }
+            top = odd ? INFINITY : top;
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             if (g4 == 0) mx[w * 8 * NT + 8 * n + 2 * t4 + c].x = top;
@@ -353,26 +359,30 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
         named_bar_sync(pair, 64u);
         const int r0 = row0 + 32 * (w >> 1);
         const bool write = r0 < a.rows && ok && !*abort_flag;
+        auto is_raw = [&](int n, int c) { return __float_as_uint(factor[n][c]) == kRawBlock; };
         const int order = pack_order(a.out_format);
         const bool sums = pack_sums(a.out_format);
         auto record = [&](int n) {
           return a.out_records + static_cast<int64_t>(g.w + n) * (a.rows / 32) * kRec + static_cast<int64_t>(r0 / 32) * rec;
         };
-        auto scale_of = [&](int col) { return pack_scale(fmaxf(mx[(w & ~1) * 8 * NT + col].x, mx[(w | 1) * 8 * NT + col].x)); };
+        auto top_of = [&](int col) { return fmaxf(mx[(w & ~1) * 8 * NT + col].x, mx[(w | 1) * 8 * NT + col].x); };
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const uint32_t col = 2u * t4 + c;
-            const bool in = write && 8 * n + static_cast<int>(col) < ncol;
-            const float sc = scale_of(8 * n + static_cast<int>(col));
+            const bool in = write && 8 * n + static_cast<int>(col) < ncol && !is_raw(n, c);
+            const float top = top_of(8 * n + static_cast<int>(col));
+            const float sc = pack_scale(is_finite(top) ? top : 0.0f);
             float sum = 0.0f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t rr = 16u * (w & 1) + 8u * h + g4, i = rr & 3u;
               const HiLo p = split_hi_lo(acc[0][n][2 * h + c] * sc);
               sum += value_of(p);
-              if (in) {
+              if (in && !is_finite(top)) {
+                *reinterpret_cast<float*>(record(n) + record_offset(rr >> 2, col, cp, order) + 4u * i) = acc[0][n][2 * h + c];
+              } else if (in) {
                 uint8_t* q = record(n) + record_offset(rr >> 2, col, cp, order) +
                              2u * (order == ORDER_NIBBLE ? ((i & 1u) << 1) | (i >> 1) : i);
                 *reinterpret_cast<__half*>(q) = p.hi;
@@ -392,10 +402,11 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const int col = 8 * n + 2 * static_cast<int>(t4) + c;
-              if (col >= ncol) continue;
+              if (col >= ncol || is_raw(n, c)) continue;
+              const float top = top_of(col);
               const float sum = sums ? (mx[w * 8 * NT + col].y + mx[(w + 1) * 8 * NT + col].y) / tile_unit(WT_Q4_K) : 0.0f;
               *reinterpret_cast<float2*>(record(n) + cp * 128u + (2u * t4 + c) * 8u) =
-                  make_float2(pow2_inverse(scale_of(col)), sum);
+                  is_finite(top) ? make_float2(pow2_inverse(pack_scale(top)), sum) : make_float2(__uint_as_float(kRawBlock), 1.0f);
             }
         }
       } else if (ok && mine && !*abort_flag) {
@@ -404,7 +415,7 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int col = 8 * n + 2 * static_cast<int>(t4) + c;
-            if (col >= ncol) continue;
+            if (col >= ncol || (MODE == TILE_LIN && __float_as_uint(factor[n][c]) == kRawBlock)) continue;
             const int64_t base = (MODE == TILE_LIN ? static_cast<int64_t>(g.w) * 8 + col : sl[n][c]) * a.out_ld;
 #pragma unroll
             for (int m = 0; m < 2; ++m)
@@ -422,6 +433,15 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
           }
       }
     }
+    // a batch's raw columns: this CTA's items again
+    if (MODE == TILE_LIN && __any_sync(0xffffffffu, raw) && ok && !*abort_flag)
+      for (int it = static_cast<int>(blockIdx.x); it < items; it += static_cast<int>(gridDim.x)) {
+        const int4 g = group_of(it / tiles);
+        const int row0 = (it % tiles) * out_rows + 32 * w;
+        if (32 * w >= out_rows || row0 >= a.rows) continue;
+        for (int c = 0; c < g.z; ++c)
+          if (raw_column(a, g, c)) exact_rows<WT>(a, g, c, row0);
+      }
   }
   __syncthreads();
 }

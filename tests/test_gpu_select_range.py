@@ -153,3 +153,94 @@ def test_lora_outliers_of_x(G, wt, kind, size):
     x = spiked(c.x, SPIKES, size)
     y, b = c.want(2, x=x)
     assert_within(c.run(2, x=x), y, b, "spikes of %g" % size)
+
+
+# ----------------------------------------------------------------------------- infinities and NaN
+
+def signed(wt, sign, seed):
+    """Raw weights of a format, of sign +1 or -1 where `sign` [rows, K] says so (0: any)."""
+    g = np.random.default_rng(seed)
+    rows, K = sign.shape
+    if wt in (F32, F16):
+        w = g.standard_normal((rows, K))
+        w = np.where(sign == 0, w, (np.abs(w) + 0.01) * sign) * 0.05
+        return w.astype(np.float32 if wt == F32 else np.float16).view(np.uint8).reshape(-1)
+    if wt == Q8:
+        c = g.integers(-127, 128, (rows, K))
+        c = np.where(sign == 0, c, np.maximum(np.abs(c), 1) * sign)
+        return synth.pack_q8_0(c, g.uniform(0.0005, 0.002, (rows, K // 32)).astype(np.float16)).reshape(-1)
+    if wt == Q4:
+        c = g.integers(0, 16, (rows, K))
+        c = np.where(sign > 0, np.maximum(c, 9), np.where(sign < 0, np.minimum(c, 7), c))
+        return synth.pack_q4_0(c, g.uniform(0.005, 0.02, (rows, K // 32)).astype(np.float16)).reshape(-1)
+    c = g.integers(0, 16, (rows, K))  # w = d (sc q - m): scales over 32, mins 1..20
+    c = np.where(sign > 0, np.maximum(c, 1), np.where(sign < 0, 0, c))
+    d = g.uniform(1e-4, 4e-4, (rows, K // 256)).astype(np.float16)
+    return synth.pack_q4_k(c, g.integers(32, 64, (rows, K // 256, 8)), g.integers(1, 21, (rows, K // 256, 8)), d, d).reshape(-1)
+
+
+def assert_classes(got, want):
+    assert np.array_equal(np.isnan(got), np.isnan(want)), "NaN pattern differs"
+    inf = np.isinf(want)
+    assert np.array_equal(np.isinf(got), inf), "Inf pattern differs"
+    assert np.array_equal(got[inf], want[inf]), "sign of an infinity differs"
+
+
+@pytest.mark.parametrize("wt", [F32, F16, Q8, Q4, Q4K])
+@pytest.mark.parametrize("kind", list(EXPERTS))
+def test_experts_infinite_x(G, wt, kind):
+    """Gate and up weights positive on one column, where x is +inf: every gated value is +inf, and
+    the outputs are +inf, -inf or NaN by the signs of the down rows (all +, all -, mixed)."""
+    c = experts_case(G, wt, kind, seed=330)
+    sign = np.zeros((c.E * c.M, c.K), dtype=int)
+    sign[:, 37] = 1
+    for i in (0, 1):
+        set_raw(c, i, signed(wt, sign, 331 + i))
+    sign = np.zeros((c.E * c.K, c.M), dtype=int)
+    sign[0::3], sign[1::3] = 1, -1
+    assert c.K % 3 != 0  # rows change their class from expert to expert, so keep them apart
+    sign = np.concatenate([sign[:c.K]] * c.E)
+    set_raw(c, 2, signed(wt, sign, 333))
+    c.w += 0.1
+    x = c.x.copy()
+    x[0, 37] = np.inf
+    if c.T > 2:
+        x[2, 37], x[c.T - 1, 38] = np.inf, -np.inf
+    G.repair_count(reset=True)
+    got = c.run(x=x)
+    assert G.repair_count(reset=True) > 0
+    with np.errstate(invalid="ignore", over="ignore"):
+        want, b = c.want(x=x)
+    assert np.any(want[0] == np.inf) and np.any(want[0] == -np.inf) and np.any(np.isnan(want[0]))
+    assert_classes(got, want)
+    fin = np.isfinite(want).all(axis=1)
+    assert_within(got[fin], want[fin], b[fin])
+    c.run()
+    assert G.repair_count() == 0
+
+
+@pytest.mark.parametrize("wt", [F32, F16, Q8, Q4, Q4K])
+@pytest.mark.parametrize("kind", list(LORA))
+def test_lora_non_finite_x(G, wt, kind):
+    c = lora_case(G, wt, kind, seed=340)
+    c.raw = zero_columns(c.raw, wt, c.M, c.K, (5,)) if wt != Q4K else c.raw
+    c.Wd = dev_tensor(c.raw)
+    x = c.x.copy()
+    c.ids[:3] = -1
+    x[0, 37], x[1, 5], x[2, 3] = np.inf, -np.inf, np.nan
+    if c.N > 3:
+        c.ids[5:8] = -1
+        x[6, 300] = -np.inf
+        x[7, 37], x[7, 300] = np.inf, -np.inf
+    for epi in (0, 1):
+        G.repair_count(reset=True)
+        got = c.run(epi, x=x)
+        assert G.repair_count(reset=True) > 0
+        with np.errstate(invalid="ignore", over="ignore"):
+            want, b = c.want(epi, x=x)
+        assert_classes(got, want)
+        fin = np.isfinite(want)
+        with np.errstate(invalid="ignore"):
+            assert_within(got[fin], want[fin], np.where(np.isfinite(b), b, 1e-6)[fin])
+    c.run(0)
+    assert G.repair_count() == 0
