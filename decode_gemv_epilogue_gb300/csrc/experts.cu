@@ -154,7 +154,7 @@ static int prep_smem(int E) { return 32 * E * 2 + 3 * E * 4; }
 // slot's column, and finds its place by counting over all slots; the first one writes the
 // groups too.  Groups are numbered in the order of their first slots.
 template <int WT>
-__global__ void __launch_bounds__(kPackSlotThreads, 6) experts_prep_short_kernel(const __grid_constant__ ExpertsArgs a) {
+__global__ void __launch_bounds__(kPackSlotThreads, 4) experts_prep_short_kernel(const __grid_constant__ ExpertsArgs a) {
   __shared__ int ids[kPackSlotThreads];
   __shared__ uint32_t leaders[kPackSlotThreads / 32];
   __shared__ int place[3];  // of this CTA's slot: group (-1: none), column, columns of the group

@@ -90,14 +90,21 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 
+constexpr int kTileK = 256;  // K of a chunk
+constexpr int kTileBlocks = kTileK / 32;
+template <int WT>
+__host__ __device__ constexpr int tile_seg() {  // bytes of a row and chunk
+  return WT == WT_F32 ? 4 * kTileK : WT == WT_F16 ? 2 * kTileK : WT == WT_Q8_0 ? kTileBlocks * 34 : 144;
+}
+
 // ------------------------------------------------------------------ packing x
 // Packed columns lie in the order in which the matrix instruction takes them.  Eight columns
 // form a column tile, and for every 32 elements a column tile has one record:
 //   [step s of 2][column of cp][thread t of 4] 16 bytes {hi, hi, hi, hi, lo, lo, lo, lo},
 //   then per column {2^-s, for Q4_K the block's sum of x 2^s in the units of its sums};
-// or, in a block that the two parts cannot carry (an infinite or NaN x), four 32-bit elements
-// in place of the 16 bytes and {kRawBlock, their factor} behind them (all blocks of a packed
-// column, single blocks of the gated values);
+// or, in a block that the two parts cannot carry (below), four 32-bit elements in place of the 16
+// bytes and {kRawBlock, their factor} behind them (all blocks of a packed column, single blocks
+// of the gated values);
 // cp = min(8, columns of the group) columns are stored, so that a single column does not move
 // eight (column tiles are allocated for the most any group of the call can have).  A warp's 16-byte reads of a step are then consecutive, and the records of a K chunk
 // are one piece of memory for one bulk copy.  Which four elements (s, t) holds is the
@@ -130,6 +137,20 @@ __device__ __forceinline__ float pow2_inverse(float p) {
   return __uint_as_float((254u << 23) - __float_as_uint(p));
 }
 
+// What the two parts carry.  Under one scale for a packed column (a block of gated values) whose
+// largest magnitude is m, hi + lo moves a value by at most 2^-22 of itself or 2^-39 m, whichever
+// is more.  That is little next to the products of a row unless many values lie far below m and
+// the weights of those near m are zero.  A value is tiny where it is not zero and below 2^-18 m
+// (the others move by at most 2^-21 of themselves).  Carried are finite values
+//  - of a packed column, if m times the sum over every four neighbours of 1 / q, q the sum of the
+//    two smaller of them, is at most 2^16 K (the four then move by at most 2^-19 q on the mean) or
+//    if at most an eighth of them are tiny (normal values: m up to 40000 standard deviations; the
+//    first rule needs no second look at the column);
+//  - of a block of 32 gated values, if none is tiny or four or more are at least 2^-14 m (all
+//    together then move by at most 2^-21 of the two smaller of these).
+// (A row whose weights are zero but where x is smallest can still exceed the parity bound.)
+constexpr float kCarryTiny = 0x1p-18f, kCarryFours = 0x1p-16f, kCarryBlock = 0x1p-14f;
+
 // In place of a block's 2^-s where its elements are stored as they are: a NaN that no arithmetic
 // makes, so that every sum with that block is NaN too.
 constexpr uint32_t kRawBlock = 0x7FC0AC7Fu;
@@ -161,9 +182,6 @@ __device__ __forceinline__ uint4 pack_group(float4 v, bool swapped, float& sum) 
   return swapped ? make_uint4(half_pair(a.hi, c.hi), half_pair(b.hi, d.hi), half_pair(a.lo, c.lo), half_pair(b.lo, d.lo))
                  : make_uint4(half_pair(a.hi, b.hi), half_pair(c.hi, d.hi), half_pair(a.lo, b.lo), half_pair(c.lo, d.lo));
 }
-__device__ __forceinline__ float finite_abs(float v) {
-  return is_finite(v) ? fabsf(v) : 0.0f;  // Inf and NaN do not set the scale
-}
 
 // Column c of a column tile's records, by `share` consecutive threads (a multiple of 32) of a
 // CTA of kPackThreads, thread i0 of them; one scale for the whole column.  x: the column
@@ -172,7 +190,7 @@ __device__ __forceinline__ float finite_abs(float v) {
 // thread of the CTA takes part.  wmax: kPackWords floats of shared memory.  Returns whether the
 // column went raw.
 constexpr int kPackThreads = 1024;
-constexpr int kPackWords = 3 * kPackThreads / 32;
+constexpr int kPackWords = 4 * kPackThreads / 32;
 // Threads of a column when `columns` (1..8) share a CTA.
 __device__ __forceinline__ int pack_share(int columns) {
   return columns <= 1 ? 1024 : columns <= 2 ? 512 : columns <= 4 ? 256 : 128;
@@ -200,35 +218,61 @@ __device__ inline bool pack_column(const float* x, int c, int i0, int share, con
     }
     return v;
   };
-  bool odd = false;  // an element is not finite
+  bool odd = false;   // an element is not finite; later, the column is not carried
+  float small = 0.0f;  // sum over every four elements of 1 / (the two smaller magnitudes)
   auto top = [&](float4 v) {
-    odd |= !is_finite(fabsf(v.x) + fabsf(v.y) + fabsf(v.z) + fabsf(v.w));
-    return fmaxf(fmaxf(finite_abs(v.x), finite_abs(v.y)), fmaxf(finite_abs(v.z), finite_abs(v.w)));
+    const float a = fabsf(v.x), b = fabsf(v.y), c4 = fabsf(v.z), d = fabsf(v.w);
+    odd |= !is_finite(a + b + c4 + d);
+    const float h0 = fmaxf(a, b), h1 = fmaxf(c4, d), l0 = fminf(a, b), l1 = fminf(c4, d);
+    small += __frcp_rn(fminf(l0, l1) + fminf(fmaxf(l0, l1), fminf(h0, h1)));
+    return is_finite(fmaxf(h0, h1)) ? fmaxf(h0, h1) : 0.0f;
   };
-  constexpr int kKeep = 4;  // groups of four a thread keeps between the two passes
+  auto tiny = [&](float4 v, float edge) {
+    auto is = [&](float e) { return e != 0.0f && fabsf(e) < edge ? 1u : 0u; };
+    return is(v.x) + is(v.y) + is(v.z) + is(v.w);
+  };
+  constexpr int kKeep = 2;  // groups of four a thread keeps between the two passes
   float4 keep[kKeep];
   float m = 0.0f;
 #pragma unroll
   for (int j = 0; j < kKeep; ++j) keep[j] = load(i0 + share * j, true);
 #pragma unroll
-  for (int j = 0; j < kKeep; ++j) m = fmaxf(m, top(keep[j]));
+  for (int j = 0; j < kKeep; ++j)
+    if (i0 + share * j < n4) m = fmaxf(m, top(keep[j]));
   for (int i = i0 + share * kKeep; i < n4; i += share) m = fmaxf(m, top(load(i, true)));
   m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  for (int o = 16; o >= 1; o >>= 1) {
+    ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    small += __shfl_xor_sync(0xffffffffu, small, o);
+  }
   odd = __any_sync(0xffffffffu, odd);
   if (lane == 0) {
     wmax[threadIdx.x >> 5] = m;
     wmax[kPackThreads / 32 + (threadIdx.x >> 5)] = ss;
     wmax[2 * kPackThreads / 32 + (threadIdx.x >> 5)] = odd ? 1.0f : 0.0f;
+    wmax[3 * kPackThreads / 32 + (threadIdx.x >> 5)] = small;
   }
   __syncthreads();
-  ss = 0.0f;
+  ss = small = 0.0f;
   const int w0 = (threadIdx.x - i0) >> 5;  // the column's first warp
   for (int q = 0; q < share / 32; ++q) {
     m = fmaxf(m, wmax[w0 + q]);
     ss += wmax[kPackThreads / 32 + w0 + q];
     odd |= wmax[2 * kPackThreads / 32 + w0 + q] != 0.0f;
+    small += wmax[3 * kPackThreads / 32 + w0 + q];
+  }
+  if (!odd && !(m * kCarryFours * small <= static_cast<float>(K))) {  // (the same for the whole column)
+    unsigned n = 0;
+#pragma unroll 1
+    for (int i = i0; i < n4; i += share) n += tiny(load(i, false), m * kCarryTiny);
+    n = __reduce_add_sync(0xffffffffu, n);
+    __syncthreads();
+    if (lane == 0) wmax[threadIdx.x >> 5] = static_cast<float>(n);
+    __syncthreads();
+    float all = 0.0f;
+    for (int q = 0; q < share / 32; ++q) all += wmax[w0 + q];
+    odd = 8.0f * all > static_cast<float>(K);
   }
   const float sc = pack_scale(m);
   const float root = gamma != nullptr ? 1.0f / sqrtf(ss / static_cast<float>(K) + eps) : 1.0f;
@@ -388,8 +432,6 @@ __device__ __forceinline__ void load_block_row(const RowPlace& p, uint32_t off, 
 // Every wait is bounded; a timeout sets the device error word, and the kernel returns after
 // draining its own copies.
 constexpr int kTileRows = 64;
-constexpr int kTileK = 256;
-constexpr int kTileBlocks = kTileK / 32;
 constexpr int kTileWarps = 8;           // consumer warps, sharing K
 constexpr int kTileThreads = 32 * (1 + kTileWarps);
 constexpr int kTileMaxStages = 8;
@@ -406,10 +448,6 @@ __host__ __device__ constexpr bool tile_plain(int wt) { return wt == WT_F16 || w
 // (F32's stages are too large for two CTAs.)
 __host__ __device__ constexpr int tile_ctas(int wt, int nt) { return nt <= 2 && wt != WT_F32 ? 2 : 1; }
 
-template <int WT>
-__host__ __device__ constexpr int tile_seg() {  // bytes of a row and chunk
-  return WT == WT_F32 ? 4 * kTileK : WT == WT_F16 ? 2 * kTileK : WT == WT_Q8_0 ? kTileBlocks * 34 : 144;
-}
 // Rows that make a whole number of 16-byte words.
 __host__ __device__ constexpr int tile_period(int row_bytes) {
   return row_bytes % 16 == 0 ? 1 : row_bytes % 8 == 0 ? 2 : row_bytes % 4 == 0 ? 4 : 8;
@@ -489,12 +527,13 @@ __device__ __forceinline__ float exact_product(const uint8_t* row, const uint8_t
       const __half* h = reinterpret_cast<const __half*>(at) + (kOrder == ORDER_NIBBLE ? ((i & 1u) << 1) | (i >> 1) : i);
       x = meta.x * (__half2float(h[0]) + __half2float(h[4]));
     }
-    s = fmaf(decode_elem<WT>(row, k), x, s);
+    s = fmaf(decode_elem<WT>(row, k & 255), x, s);
     if ((k & 31) == 31) {  // block by block, as the tiles
       sum += s;
       s = 0.0f;
       rec += record_bytes(static_cast<int>(cp));
     }
+    if ((k & 255) == 255) row += tile_seg<WT>();
   }
   return sum;
 }
@@ -506,11 +545,14 @@ __device__ __forceinline__ void write_gated(float h, uint8_t* r, uint32_t c, uin
   const int order = pack_order(fmt);
   const uint32_t at = record_offset(lane >> 2, c, cp, order);
   float2 meta;
-  if (__any_sync(0xffffffffu, !is_finite(h))) {
+  const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(h))));  // (a NaN is largest)
+  const uint32_t big = __ballot_sync(0xffffffffu, fabsf(h) >= m * kCarryBlock);
+  const uint32_t not_tiny = __ballot_sync(0xffffffffu, h == 0.0f || fabsf(h) >= m * kCarryTiny);
+  if (!is_finite(m) || (__popc(big) < 4 && not_tiny != 0xffffffffu)) {
     *reinterpret_cast<float*>(r + at + 4u * i) = h;
     meta = make_float2(__uint_as_float(kRawBlock), 1.0f);
   } else {
-    const float sc = pack_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(h)))));
+    const float sc = pack_scale(m);
     const HiLo p = split_hi_lo(h * sc);
     float sum = value_of(p);
     if (pack_sums(fmt))

@@ -31,8 +31,8 @@ constexpr int kWideNT = 2;  // column tiles
 template <int WT>
 __host__ __device__ constexpr int wide_warps() { return WT == WT_Q8_0 ? 8 : 16; }
 template <int WT>
-__host__ __device__ constexpr int wide_xchg() {  // [item parity][warp][column] {largest, sum}
-  return 2 * wide_warps<WT>() * 8 * kWideNT * 8;
+__host__ __device__ constexpr int wide_xchg() {  // [item parity][warp][column] {largest, sum}, then counts
+  return 2 * wide_warps<WT>() * 8 * kWideNT * 12;
 }
 template <int WT>
 __host__ __device__ constexpr int wide_weight_bytes() { return wide_warps<WT>() * tile_part<WT>(1); }
@@ -332,26 +332,24 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
         for (int n = 0; n < NT; ++n) raw |= __float_as_uint(factor[n][0]) == kRawBlock || __float_as_uint(factor[n][1]) == kRawBlock;
       if constexpr (MODE == TILE_GLU) {
         // the gated values of rows 8h + g (of the warp's 16) and columns 2t + c, in place of the
-        // gate sums; two warps make a block: they exchange its largest value and, for Q4_K's
-        // mins, the sum of what they pack
+        // gate sums; two warps make a block: they exchange its largest value, then how many values
+        // lie how far below it and, for Q4_K's mins, the sum of what they pack
         float2* mx = xchg + (round & 1u) * (kWarps * 8 * NT);
+        int* mc = reinterpret_cast<int*>(xchg + 2 * kWarps * 8 * NT) + (round & 1u) * (kWarps * 8 * NT);
         const uint32_t pair = 1u + static_cast<uint32_t>(w >> 1);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float top = 0.0f;
-            bool odd = false;  // a value is not finite: the block goes raw
+            float top = 0.0f;  // infinite where a value is not finite: the block goes raw
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int i = 2 * h + c;
               const float f = tile_unit(WT) * factor[n][c];
               const float v = tail_silu(acc[0][n][i] * f) * (acc[1][n][i] * f);
               acc[0][n][i] = v;
-              top = fmaxf(top, finite_abs(v));
-              odd |= !is_finite(v);
+              top = fmaxf(top, is_finite(v) ? fabsf(v) : INFINITY);
             }
-            top = odd ? INFINITY : top;
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             if (g4 == 0) mx[w * 8 * NT + 8 * n + 2 * t4 + c].x = top;
@@ -375,28 +373,33 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
             const float top = top_of(8 * n + static_cast<int>(col));
             const float sc = pack_scale(is_finite(top) ? top : 0.0f);
             float sum = 0.0f;
+            int counts = 0;  // values of at least kCarryBlock of the largest; tiny ones (x 256)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t rr = 16u * (w & 1) + 8u * h + g4, i = rr & 3u;
-              const HiLo p = split_hi_lo(acc[0][n][2 * h + c] * sc);
+              const float v = acc[0][n][2 * h + c];
+              const HiLo p = split_hi_lo(v * sc);
               sum += value_of(p);
-              if (in && !is_finite(top)) {
-                *reinterpret_cast<float*>(record(n) + record_offset(rr >> 2, col, cp, order) + 4u * i) = acc[0][n][2 * h + c];
-              } else if (in) {
+              counts += (fabsf(v) >= top * kCarryBlock ? 1 : 0) + (v != 0.0f && fabsf(v) < top * kCarryTiny ? 256 : 0);
+              if (in) {
                 uint8_t* q = record(n) + record_offset(rr >> 2, col, cp, order) +
                              2u * (order == ORDER_NIBBLE ? ((i & 1u) << 1) | (i >> 1) : i);
                 *reinterpret_cast<__half*>(q) = p.hi;
                 *reinterpret_cast<__half*>(q + 8) = p.lo;
               }
             }
-            if (sums) {
 #pragma unroll
-              for (int o = 4; o <= 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-              if (g4 == 0) mx[w * 8 * NT + 8 * n + col].y = sum;
+            for (int o = 4; o <= 16; o <<= 1) {
+              if (sums) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+              counts += __shfl_xor_sync(0xffffffffu, counts, o);
+            }
+            if (g4 == 0) {
+              mx[w * 8 * NT + 8 * n + col].y = sum;
+              mc[w * 8 * NT + 8 * n + col] = counts;
             }
           }
-        if (sums) named_bar_sync(pair, 64u);
-        if (write && g4 == 0 && !(w & 1)) {
+        named_bar_sync(pair, 64u);
+        if (write) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -404,9 +407,19 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
               const int col = 8 * n + 2 * static_cast<int>(t4) + c;
               if (col >= ncol || is_raw(n, c)) continue;
               const float top = top_of(col);
+              const int counts = mc[(w & ~1) * 8 * NT + col] + mc[(w | 1) * 8 * NT + col];
+              const bool carried = is_finite(top) && ((counts & 255) >= 4 || counts < 256);
+              if (!carried)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t rr = 16u * (w & 1) + 8u * h + g4;
+                  *reinterpret_cast<float*>(record(n) + record_offset(rr >> 2, 2u * t4 + c, cp, order) + 4u * (rr & 3u)) =
+                      acc[0][n][2 * h + c];
+                }
+              if (g4 != 0 || (w & 1)) continue;
               const float sum = sums ? (mx[w * 8 * NT + col].y + mx[(w + 1) * 8 * NT + col].y) / tile_unit(WT_Q4_K) : 0.0f;
               *reinterpret_cast<float2*>(record(n) + cp * 128u + (2u * t4 + c) * 8u) =
-                  is_finite(top) ? make_float2(pow2_inverse(pack_scale(top)), sum) : make_float2(__uint_as_float(kRawBlock), 1.0f);
+                  carried ? make_float2(pow2_inverse(pack_scale(top)), sum) : make_float2(__uint_as_float(kRawBlock), 1.0f);
             }
         }
       } else if (ok && mine && !*abort_flag) {

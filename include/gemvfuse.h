@@ -451,7 +451,8 @@ GF_API int gf_device_status(int reset);
  * the values around it, or a NaN / Inf): a count since the last reset, on the current
  * device.  Such a launch reads its weights twice; the count says how often that
  * happens for a workload.  The tiled kernels of gemv_experts and gemv_lora count here too: a
- * column of packed x that they do not carry (a NaN / Inf), once for the gated products of an
+ * column of packed x that they do not carry (a NaN / Inf, or an outlier far above an eighth of
+ * the other values), once for the gated products of an
  * expert and once for every 32 rows of a shared projection, and every output of a down product
  * computed again; such a call takes many times as long.  Synchronises with the device; reset != 0 clears it.
  * Negative: a gf_status (GF_ERR_CUDA). */

@@ -244,3 +244,127 @@ def test_lora_non_finite_x(G, wt, kind):
             assert_within(got[fin], want[fin], np.where(np.isfinite(b), b, 1e-6)[fin])
     c.run(0)
     assert G.repair_count() == 0
+
+
+# ----------------------------------------------------------------------------- values that two f16 parts cannot carry
+
+@pytest.mark.parametrize("wt", [F32, F16, Q8, Q4, Q4K])
+@pytest.mark.parametrize("kind", list(EXPERTS))
+@pytest.mark.parametrize("size", [1e7, 1e9, 1e13, 1e25])
+def test_experts_far_outliers_of_x(G, wt, kind, size):
+    c = experts_case(G, wt, kind, seed=350)
+    for i in (0, 1):
+        set_raw(c, i, zero_columns(c.raw[i], wt, c.E * c.M, c.K, SPIKES))
+    x = spiked(c.x, SPIKES, size)
+    y, b = c.want(x=x)
+    G.repair_count(reset=True)
+    assert_within(c.run(x=x), y, b, "spikes of %g" % size)
+    assert G.repair_count(reset=True) > 0
+    c.run(x=spiked(c.x, SPIKES, 1e4))
+    assert G.repair_count() == 0
+
+
+@pytest.mark.parametrize("kind", list(EXPERTS))
+@pytest.mark.parametrize("wd", [F32, F16, Q8, Q4, Q4K])
+@pytest.mark.parametrize("size", [1e9, 1e12, 1e20])
+def test_experts_far_outliers_of_the_gated_values(G, kind, wd, size):
+    if kind == "wide" and wd in (F32, F16):
+        pytest.skip("no wide kernel of these rows")
+    T, E, k, M, K, _ = EXPERTS[kind]
+    c = experts_case(G, wd, kind, seed=360)
+    # two rows of the up matrix, whose gate is 3, take their value from one element of x alone
+    cols = SPIKES[1:3]
+    set_raw(c, 2, zero_columns(c.raw[2], wd, E * K, M, cols))
+    c.x[:, 300:332] = 0.0
+    c.x[::2, 300] = size
+    for i in (0, 1):  # x is far above the rest there: zero weights but in those rows
+        raw = zero_columns(c.raw[i], wd, E * M, K, range(288, 320))
+        rows = raw.reshape(E, M, -1)
+        for m in cols:
+            one = np.zeros((1, K))
+            one[0, 300 if i else 5] = 1.0
+            rows[:, m] = one_hot(wd, one)
+        set_raw(c, i, rows.reshape(-1))
+    c.x[:, 5] = 1.0 if wd in (F32, F16) else 3.0
+    y, b = c.want()
+    G.repair_count(reset=True)
+    assert_within(c.run(), y, b, "gated spikes")
+    assert G.repair_count() > 0
+
+
+def one_hot(wt, w):
+    """Raw row of weights that are zero but for one of about 1."""
+    K = w.shape[1]
+    if wt in (F32, F16):
+        return w.astype(np.float32 if wt == F32 else np.float16).view(np.uint8).reshape(-1)
+    if wt == Q8:
+        return synth.pack_q8_0((w * 100).astype(np.int16), np.full((1, K // 32), 0.01, np.float16)).reshape(-1)
+    if wt == Q4:
+        return synth.pack_q4_0((w * 7 + 8).astype(np.int16), np.full((1, K // 32), 0.14, np.float16)).reshape(-1)
+    z = np.zeros((1, K // 256, 8), dtype=np.int16)
+    one = np.full((1, K // 256), 0.01, np.float16)
+    return synth.pack_q4_k((w * 10).astype(np.int16), z + 10, z, one, one).reshape(-1)
+
+
+@pytest.mark.parametrize("wt", [F32, F16, Q8, Q4, Q4K])
+@pytest.mark.parametrize("kind", list(LORA))
+@pytest.mark.parametrize("size", [1e7, 1e9, 1e13, 1e25])
+def test_lora_far_outliers_of_x(G, wt, kind, size):
+    c = lora_case(G, wt, kind, seed=370)
+    c.raw = zero_columns(c.raw, wt, c.M, c.K, SPIKES)
+    c.Wd = dev_tensor(c.raw)
+    c.A[:, :, list(SPIKES)] = 0
+    c.Ad = dev_tensor(c.A)
+    x = spiked(c.x, SPIKES, size)
+    y, b = c.want(2, x=x)
+    G.repair_count(reset=True)
+    assert_within(c.run(2, x=x), y, b, "spikes of %g" % size)
+    assert G.repair_count(reset=True) > 0
+    c.run(2, x=spiked(c.x, SPIKES, 1e4))
+    assert G.repair_count() == 0
+
+
+@pytest.mark.parametrize("wt", [F32, F16, Q8, Q4])
+@pytest.mark.parametrize("size", [1e3, 1e4, 1e5, 3e5, 1e6])
+def test_outliers_in_one_block(G, wt, size):
+    """K of one block: nothing else in the row hides what its one outlier costs."""
+    c = test_gpu_experts.Case(G, 9, 3, 2, 64, 32, wt, wt, seed=380)
+    for i in (0, 1):
+        set_raw(c, i, zero_columns(c.raw[i], wt, c.E * c.M, 32, (7,)))
+    x = spiked(c.x, (7,), size)
+    y, b = c.want(x=x)
+    assert_within(c.run(x=x), y, b)
+
+
+@pytest.mark.parametrize("wt", [F32, F16, Q8, Q4, Q4K])
+@pytest.mark.parametrize("case", ["one block", "half", "tiny block", "sparse", "one-hot", "zeros", "cubes"])
+def test_uneven_x(G, wt, case):
+    """Columns whose blocks differ by many magnitudes, with zero weights on the large ones; and
+    columns of few values, which the two parts carry."""
+    c = experts_case(G, wt, "tile", seed=390)
+    g = np.random.default_rng(391)
+    x, large = c.x.astype(np.float64), ()
+    if case == "one block":
+        x[:, 64:96] *= 1e10
+        large = range(64, 96)
+    elif case == "half":
+        large = [k for k in range(c.K) if k % 256 < 128]
+        x[:, large] *= 1e8
+    elif case == "tiny block":
+        x[:, 64:96] *= 1e-10
+    elif case == "sparse":
+        x = np.where(g.random(x.shape) < 1 / 64, x, 0.0)
+    elif case == "one-hot":
+        x = np.where(np.arange(c.K) == np.arange(c.T)[:, None] * 41, x, 0.0)
+    elif case == "zeros":
+        x[::2] = 0.0
+        x[1::2, 5:] = 0.0
+    else:
+        x = x ** 3
+    for i in (0, 1):
+        set_raw(c, i, zero_columns(c.raw[i], wt, c.E * c.M, c.K, large) if len(large) else c.raw[i])
+    x = x.astype(np.float32)
+    y, b = c.want(x=x)
+    G.repair_count(reset=True)
+    assert_within(c.run(x=x), y, b)
+    assert (G.repair_count() > 0) == (case in ("one block", "half"))
