@@ -77,36 +77,30 @@ __global__ void __launch_bounds__(32 * kExpGenericWarps) experts_generic_kernel(
   }
 }
 
-// Row `row` of all experts' rows of K columns times column c of column tile `tile` of the records.
-template <int WT>
-__device__ __forceinline__ float exact_row(const ExpertsArgs& a, const uint8_t* W, int64_t row, const uint8_t* records,
-                                           int tile, uint32_t c, uint32_t cp, int K) {
-  return exact_product<WT>(W + row * expert_row_bytes<WT>(K),
-                           records + static_cast<int64_t>(tile) * (K / 32) * record_bytes(a.cp), c, cp, K);
-}
-
 // The gated values of slot s, a raw column (column c of `tile`), by the CTA that packed it.
 template <int WT>
 __device__ __forceinline__ void exact_gated(const ExpertsArgs& a, int s, int tile, uint32_t c, uint32_t cp) {
+  const int64_t rb = expert_row_bytes<WT>(a.K);
+  const uint8_t* rec = a.xrec + static_cast<int64_t>(tile) * (a.K / 32) * record_bytes(a.cp);
   if (threadIdx.x == 0) atomicAdd(a.err + 1, 1u);  // counted for gf_repair_count
 #pragma unroll 1
   for (int b = threadIdx.x >> 5; b < a.M / 32; b += blockDim.x >> 5) {
-    const int64_t row = static_cast<int64_t>(a.ids[s]) * a.M + 32 * b + (threadIdx.x & 31);
-    float y[2];
+    const int64_t at = (static_cast<int64_t>(a.ids[s]) * a.M + 32 * b) * rb;
+    float g = 0.0f, u = 0.0f;
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-      const float v = exact_row<WT>(a, i ? a.W2 : a.W, row, a.xrec, tile, c, cp, a.K);
-      if (i == 0) y[0] = v;
-      else y[1] = v;
+      g = u;
+      u = exact_block<WT, 4>((i ? a.W2 : a.W) + at, rb, rec, c, cp, a.K);
     }
-    write_gated(tail_silu(y[0]) * y[1],
+    write_gated(tail_silu(g) * u,
                 a.hrec + static_cast<int64_t>(tile) * (a.M / 32) * record_bytes(a.cp) +
                     static_cast<int64_t>(b) * record_bytes(static_cast<int>(cp)),
                 c, cp, a.out_format);
   }
 }
 
-// W: the down matrices, where their products are the tiles' (nullptr: the generic kernel's).
+// W: the down matrices, where their products are the tiles' (nullptr: the generic kernel's).  A
+// product that a raw block among its gated values made NaN is taken again, element by element.
 // (Six CTAs an SM, five of the packing: the code of raw columns must not cost the others their warps.)
 template <int WT>
 __global__ void __launch_bounds__(256, 6) experts_combine_kernel(const __grid_constant__ ExpertsArgs a) {
@@ -114,31 +108,41 @@ __global__ void __launch_bounds__(256, 6) experts_combine_kernel(const __grid_co
   pdl_trigger();
   const int t = blockIdx.y;
   const int m = blockIdx.x * 256 + threadIdx.x;
-  if (m >= a.K) return;
+  const bool in = m < a.K;
   const int64_t o = static_cast<int64_t>(t) * a.K + m;
-  const float first = a.aux ? a.aux[o] : 0.0f;
+  const float first = in && a.aux ? a.aux[o] : 0.0f;
   float s = first;
-  for (int j = 0; j < a.k; ++j) {
-    const int e = a.ids[t * a.k + j];
-    if (e >= 0 && e < a.E) s += a.y[static_cast<int64_t>(t * a.k + j) * a.K + m];
-  }
+  if (in)
+    for (int j = 0; j < a.k; ++j) {
+      const int e = a.ids[t * a.k + j];
+      if (e >= 0 && e < a.E) s += a.y[static_cast<int64_t>(t * a.k + j) * a.K + m];
+    }
   // (the slots one by one only here: a look at each of them above took 9 -> 25 us of 256 tokens)
-  if (!is_finite(s) && a.W) {
-    s = first;
+  const uint32_t odd = __ballot_sync(0xffffffffu, in && !is_finite(s));
+  if (odd && a.W) {
+    if (odd >> (threadIdx.x & 31) & 1u) s = first;
+#pragma unroll 1
     for (int j = 0; j < a.k; ++j) {
       const int e = a.ids[t * a.k + j];
       if (e < 0 || e >= a.E) continue;
-      const float y = a.y[static_cast<int64_t>(t * a.k + j) * a.K + m];
-      if (is_finite(y)) {
-        s += y;
-      } else {
-        const int2 p = a.places[t * a.k + j];
-        atomicAdd(a.err + 1, 1u);  // counted for gf_repair_count
-        s += a.weights[t * a.k + j] * exact_row<WT>(a, a.W, static_cast<int64_t>(e) * a.K + m, a.hrec, p.x,
-                                                    static_cast<uint32_t>(p.y) & 255u, static_cast<uint32_t>(p.y) >> 8, a.M);
+      float y = in ? a.y[static_cast<int64_t>(t * a.k + j) * a.K + m] : 0.0f;
+      const int2 p = a.places[t * a.k + j];
+      const uint32_t c = static_cast<uint32_t>(p.y) & 255u, cp = static_cast<uint32_t>(p.y) >> 8;
+      const uint8_t* rec = a.hrec + static_cast<int64_t>(p.x) * (a.M / 32) * record_bytes(a.cp);
+      bool raw = false;
+      for (int b = threadIdx.x & 31; b < a.M / 32 && !is_finite(y); b += 32)
+        raw |= *reinterpret_cast<const uint32_t*>(rec + b * record_bytes(static_cast<int>(cp)) + cp * 128u + c * 8u) == kRawBlock;
+      if (__any_sync(0xffffffffu, raw)) {
+        if ((threadIdx.x & 31) == 0) atomicAdd(a.err + 1, 1u);  // counted for gf_repair_count
+        const int64_t rb = expert_row_bytes<WT>(a.M);
+        const int m0 = m - static_cast<int>(threadIdx.x & 31);
+        const float v = exact_block<WT, 2>(a.W + (static_cast<int64_t>(e) * a.K + m0) * rb, rb, rec, c, cp, a.M);
+        if (!is_finite(y)) y = a.weights[t * a.k + j] * v;
       }
+      if (odd >> (threadIdx.x & 31) & 1u) s += y;
     }
   }
+  if (!in) return;
   a.dst[o] = s;
 }
 

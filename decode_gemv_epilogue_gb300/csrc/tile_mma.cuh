@@ -140,8 +140,10 @@ __device__ __forceinline__ float pow2_inverse(float p) {
 // What the two parts carry.  Under one scale for a packed column (a block of gated values) whose
 // largest magnitude is m, hi + lo moves a value by at most 2^-22 of itself or 2^-39 m, whichever
 // is more.  That is little next to the products of a row unless many values lie far below m and
-// the weights of those near m are zero.  A value is tiny where it is not zero and below 2^-18 m
-// (the others move by at most 2^-21 of themselves).  Carried are finite values
+// the weights of those near m are zero; and a NaN or an infinity in hi makes NaN of what should be
+// an infinity (the other part, or Q4_K's mins, take it off again).  A value is tiny where it is not zero and below 2^-18 m
+// (the others move by at most 2^-21 of themselves).  Carried is what holds a NaN, since nothing
+// but NaN comes of it, and are finite values
 //  - of a packed column, if m times the sum over every four neighbours of 1 / q, q the sum of the
 //    two smaller of them, is at most 2^16 K (the four then move by at most 2^-19 q on the mean) or
 //    if at most an eighth of them are tiny (normal values: m up to 40000 standard deviations; the
@@ -218,14 +220,15 @@ __device__ inline bool pack_column(const float* x, int c, int i0, int share, con
     }
     return v;
   };
-  bool odd = false;   // an element is not finite; later, the column is not carried
-  float small = 0.0f;  // sum over every four elements of 1 / (the two smaller magnitudes)
+  bool nan = false, inf = false;  // of any element
+  float small = 0.0f;             // sum over every four elements of 1 / (the two smaller magnitudes)
   auto top = [&](float4 v) {
-    const float a = fabsf(v.x), b = fabsf(v.y), c4 = fabsf(v.z), d = fabsf(v.w);
-    odd |= !is_finite(a + b + c4 + d);
+    const float a = fabsf(v.x), b = fabsf(v.y), c4 = fabsf(v.z), d = fabsf(v.w), all = (a + b) + (c4 + d);
+    nan |= all != all;
+    inf |= all > 3.402823466e38f;
     const float h0 = fmaxf(a, b), h1 = fmaxf(c4, d), l0 = fminf(a, b), l1 = fminf(c4, d);
     small += __frcp_rn(fminf(l0, l1) + fminf(fmaxf(l0, l1), fminf(h0, h1)));
-    return is_finite(fmaxf(h0, h1)) ? fmaxf(h0, h1) : 0.0f;
+    return is_finite(fmaxf(h0, h1)) ? fmaxf(h0, h1) : 0.0f;  // (the others do not set the scale)
   };
   auto tiny = [&](float4 v, float edge) {
     auto is = [&](float e) { return e != 0.0f && fabsf(e) < edge ? 1u : 0u; };
@@ -246,11 +249,12 @@ __device__ inline bool pack_column(const float* x, int c, int i0, int share, con
     ss += __shfl_xor_sync(0xffffffffu, ss, o);
     small += __shfl_xor_sync(0xffffffffu, small, o);
   }
-  odd = __any_sync(0xffffffffu, odd);
+  nan = __any_sync(0xffffffffu, nan);
+  inf = __any_sync(0xffffffffu, inf);
   if (lane == 0) {
     wmax[threadIdx.x >> 5] = m;
     wmax[kPackThreads / 32 + (threadIdx.x >> 5)] = ss;
-    wmax[2 * kPackThreads / 32 + (threadIdx.x >> 5)] = odd ? 1.0f : 0.0f;
+    wmax[2 * kPackThreads / 32 + (threadIdx.x >> 5)] = nan ? 2.0f : inf ? 1.0f : 0.0f;
     wmax[3 * kPackThreads / 32 + (threadIdx.x >> 5)] = small;
   }
   __syncthreads();
@@ -259,10 +263,13 @@ __device__ inline bool pack_column(const float* x, int c, int i0, int share, con
   for (int q = 0; q < share / 32; ++q) {
     m = fmaxf(m, wmax[w0 + q]);
     ss += wmax[kPackThreads / 32 + w0 + q];
-    odd |= wmax[2 * kPackThreads / 32 + w0 + q] != 0.0f;
+    nan |= wmax[2 * kPackThreads / 32 + w0 + q] == 2.0f;
+    inf |= wmax[2 * kPackThreads / 32 + w0 + q] == 1.0f;
     small += wmax[3 * kPackThreads / 32 + w0 + q];
   }
-  if (!odd && !(m * kCarryFours * small <= static_cast<float>(K))) {  // (the same for the whole column)
+  // (normalised by an infinite mean square, what is finite is zero and the rest NaN: as packed)
+  bool raw = inf && !nan && (gamma == nullptr || is_finite(ss));
+  if (!inf && !nan && !(m * kCarryFours * small <= static_cast<float>(K))) {  // (the same for the whole column)
     unsigned n = 0;
 #pragma unroll 1
     for (int i = i0; i < n4; i += share) n += tiny(load(i, false), m * kCarryTiny);
@@ -272,14 +279,14 @@ __device__ inline bool pack_column(const float* x, int c, int i0, int share, con
     __syncthreads();
     float all = 0.0f;
     for (int q = 0; q < share / 32; ++q) all += wmax[w0 + q];
-    odd = 8.0f * all > static_cast<float>(K);
+    raw = 8.0f * all > static_cast<float>(K);
   }
   const float sc = pack_scale(m);
   const float root = gamma != nullptr ? 1.0f / sqrtf(ss / static_cast<float>(K) + eps) : 1.0f;
   const float inv = pow2_inverse(sc) * root;
   const int rec = record_bytes(cp);
   auto put = [&](int i, float4 v) {
-    if (odd) {
+    if (raw) {
       if (x != nullptr && i < n4) {
         uint8_t* r = base + static_cast<int64_t>(i >> 3) * rec;
         *reinterpret_cast<float4*>(r + record_offset(i & 7, c, cp, order)) = v;
@@ -303,7 +310,7 @@ __device__ inline bool pack_column(const float* x, int c, int i0, int share, con
   for (int j = 0; j < kKeep; ++j) put(i0 + share * j, keep[j]);
   for (int b = share * kKeep; b < n4; b += share) put(b + i0, load(b + i0, false));
   __syncthreads();  // wmax may be used again
-  return odd;
+  return raw;
 }
 
 // ------------------------------------------------------------------ A fragments
@@ -503,39 +510,55 @@ struct TileArgs {
 };
 
 // ------------------------------------------------------------------ raw columns
-// A raw column's sums in the tiles are NaN and go nowhere.  Its products are taken element by
+// A raw column's sums in the tiles go nowhere.  Its products are taken element by
 // element: the gated ones by the launch that packs it, which the tiles follow (in the tiles'
 // kernel this code took 3 to 7% of every call's time without running), a batch's behind the
 // tiles' own; and a down product that a raw block made NaN by the combination.
 //
-// One row times one packed column in 32 bits, every lane its own row: lean, not quick, since the
-// kernels that hold it pay for its registers (and, where it needs a stack, at every launch).
-// rec: the column tile's first record, cp columns stored, this one c.
-template <int WT>
-__device__ __forceinline__ float exact_product(const uint8_t* row, const uint8_t* rec, uint32_t c, uint32_t cp, int K) {
+// R rows, `stride` bytes apart, times one packed column in 32 bits, by a warp; every lane gets the
+// sums.  Lean: the kernels that hold it pay for its registers and, where it needs a stack, at
+// every launch.  rec: the column tile's first record, cp columns stored, this one c.
+template <int WT, int R>
+__device__ __forceinline__ void exact_products(const uint8_t* row, int64_t stride, const uint8_t* rec, uint32_t c, uint32_t cp,
+                                               int K, float (&s)[R]) {
   constexpr int kOrder = pack_order(WT);
-  float sum = 0.0f, s = 0.0f;
+  const uint32_t lane = threadIdx.x & 31u, i = lane & 3u;
+  const uint32_t at = record_offset(lane >> 2, c, cp, kOrder), half = kOrder == ORDER_NIBBLE ? ((i & 1u) << 1) | (i >> 1) : i;
+#pragma unroll
+  for (int r = 0; r < R; ++r) s[r] = 0.0f;
 #pragma unroll 1
-  for (int k = 0; k < K; ++k) {
-    const uint32_t i = k & 3;
+  for (int b = 0; b < K / 32; ++b) {  // a lane's element of each block
     const float2 meta = *reinterpret_cast<const float2*>(rec + cp * 128u + c * 8u);
-    const uint8_t* at = rec + record_offset((k >> 2) & 7, c, cp, kOrder);
     float x;
     if (__float_as_uint(meta.x) == kRawBlock) {
-      x = meta.y * reinterpret_cast<const float*>(at)[i];
+      x = meta.y * reinterpret_cast<const float*>(rec + at)[i];
     } else {
-      const __half* h = reinterpret_cast<const __half*>(at) + (kOrder == ORDER_NIBBLE ? ((i & 1u) << 1) | (i >> 1) : i);
+      const __half* h = reinterpret_cast<const __half*>(rec + at) + half;
       x = meta.x * (__half2float(h[0]) + __half2float(h[4]));
     }
-    s = fmaf(decode_elem<WT>(row, k & 255), x, s);
-    if ((k & 31) == 31) {  // block by block, as the tiles
-      sum += s;
-      s = 0.0f;
-      rec += record_bytes(static_cast<int>(cp));
-    }
-    if ((k & 255) == 255) row += tile_seg<WT>();
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[r] = fmaf(decode_elem<WT>(row + r * stride, 32 * (b & 7) + static_cast<int>(lane)), x, s[r]);
+    rec += record_bytes(static_cast<int>(cp));
+    if ((b & 7) == 7) row += tile_seg<WT>();
   }
-  return sum;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+}
+// 32 rows from `row` on, R at a time: lane r gets the r-th.
+template <int WT, int R>
+__device__ __forceinline__ float exact_block(const uint8_t* row, int64_t stride, const uint8_t* rec, uint32_t c, uint32_t cp,
+                                             int K) {
+  float y = 0.0f, s[R];
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += R) {
+    exact_products<WT, R>(row + r0 * stride, stride, rec, c, cp, K, s);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (static_cast<int>(threadIdx.x & 31u) == r0 + r) y = s[r];
+  }
+  return y;
 }
 
 // A block of 32 gated values of one column, a lane's each, into its record r (cp columns stored,
@@ -545,14 +568,15 @@ __device__ __forceinline__ void write_gated(float h, uint8_t* r, uint32_t c, uin
   const int order = pack_order(fmt);
   const uint32_t at = record_offset(lane >> 2, c, cp, order);
   float2 meta;
-  const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(h))));  // (a NaN is largest)
+  const bool nan = __any_sync(0xffffffffu, h != h);
+  const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, h == h ? __float_as_uint(fabsf(h)) : 0u));
   const uint32_t big = __ballot_sync(0xffffffffu, fabsf(h) >= m * kCarryBlock);
   const uint32_t not_tiny = __ballot_sync(0xffffffffu, h == 0.0f || fabsf(h) >= m * kCarryTiny);
-  if (!is_finite(m) || (__popc(big) < 4 && not_tiny != 0xffffffffu)) {
+  if (!nan && (!is_finite(m) || (__popc(big) < 4 && not_tiny != 0xffffffffu))) {
     *reinterpret_cast<float*>(r + at + 4u * i) = h;
     meta = make_float2(__uint_as_float(kRawBlock), 1.0f);
   } else {
-    const float sc = pack_scale(m);
+    const float sc = pack_scale(is_finite(m) ? m : 0.0f);
     const HiLo p = split_hi_lo(h * sc);
     float sum = value_of(p);
     if (pack_sums(fmt))
@@ -579,8 +603,19 @@ template <int WT>
 __device__ __forceinline__ void exact_rows(const TileArgs& a, const int4& g, int col, int row0) {
   const int lane = threadIdx.x & 31, r = row0 + lane;
   if (lane == 0) atomicAdd(a.err + 1, 1u);  // counted for gf_repair_count
-  const float y = exact_product<WT>(a.W + static_cast<int64_t>(min(r, a.rows - 1)) * a.row_bytes, column_records(a, g, col),
-                                    static_cast<uint32_t>(col) & 7u, static_cast<uint32_t>(min(8, g.z)), a.K);
+  const uint8_t *W = a.W + static_cast<int64_t>(row0) * a.row_bytes, *rec = column_records(a, g, col);
+  const uint32_t c = static_cast<uint32_t>(col) & 7u, cp = static_cast<uint32_t>(min(8, g.z));
+  float y = 0.0f;
+  if (row0 + 32 <= a.rows) {
+    y = exact_block<WT, 4>(W, a.row_bytes, rec, c, cp, a.K);
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < a.rows - row0; ++i) {
+      float s[1];
+      exact_products<WT, 1>(W + i * static_cast<int64_t>(a.row_bytes), 0, rec, c, cp, a.K, s);
+      if (i == lane) y = s[0];
+    }
+  }
   if (r < a.rows) {
     const int64_t o = (static_cast<int64_t>(g.w) * 8 + col) * a.out_ld + r;
     a.out[o] = apply_tail(a.epi, y, epi_takes_aux(a.epi) ? a.aux[o] : 0.0f);  // aux may be out

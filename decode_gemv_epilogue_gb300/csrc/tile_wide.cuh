@@ -341,14 +341,14 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float top = 0.0f;  // infinite where a value is not finite: the block goes raw
+            float top = 0.0f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int i = 2 * h + c;
               const float f = tile_unit(WT) * factor[n][c];
               const float v = tail_silu(acc[0][n][i] * f) * (acc[1][n][i] * f);
               acc[0][n][i] = v;
-              top = fmaxf(top, is_finite(v) ? fabsf(v) : INFINITY);
+              top = fmaxf(top, fabsf(v));  // (not a NaN)
             }
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -373,14 +373,15 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
             const float top = top_of(8 * n + static_cast<int>(col));
             const float sc = pack_scale(is_finite(top) ? top : 0.0f);
             float sum = 0.0f;
-            int counts = 0;  // values of at least kCarryBlock of the largest; tiny ones (x 256)
+            int counts = 0;  // values of at least kCarryBlock of the largest; tiny ones (x 256); NaN (x 65536)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t rr = 16u * (w & 1) + 8u * h + g4, i = rr & 3u;
               const float v = acc[0][n][2 * h + c];
               const HiLo p = split_hi_lo(v * sc);
               sum += value_of(p);
-              counts += (fabsf(v) >= top * kCarryBlock ? 1 : 0) + (v != 0.0f && fabsf(v) < top * kCarryTiny ? 256 : 0);
+              counts += (fabsf(v) >= top * kCarryBlock ? 1 : 0) + (v != 0.0f && fabsf(v) < top * kCarryTiny ? 256 : 0) +
+                        (v != v ? 65536 : 0);
               if (in) {
                 uint8_t* q = record(n) + record_offset(rr >> 2, col, cp, order) +
                              2u * (order == ORDER_NIBBLE ? ((i & 1u) << 1) | (i >> 1) : i);
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
               if (col >= ncol || is_raw(n, c)) continue;
               const float top = top_of(col);
               const int counts = mc[(w & ~1) * 8 * NT + col] + mc[(w | 1) * 8 * NT + col];
-              const bool carried = is_finite(top) && ((counts & 255) >= 4 || counts < 256);
+              const bool carried = counts >= 65536 || (is_finite(top) && ((counts & 255) >= 4 || counts < 256));
               if (!carried)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(32 * (1 + wide_warps<WT>()), 1)
               if (g4 != 0 || (w & 1)) continue;
               const float sum = sums ? (mx[w * 8 * NT + col].y + mx[(w + 1) * 8 * NT + col].y) / tile_unit(WT_Q4_K) : 0.0f;
               *reinterpret_cast<float2*>(record(n) + cp * 128u + (2u * t4 + c) * 8u) =
-                  carried ? make_float2(pow2_inverse(pack_scale(top)), sum) : make_float2(__uint_as_float(kRawBlock), 1.0f);
+                  carried ? make_float2(pow2_inverse(pack_scale(is_finite(top) ? top : 0.0f)), sum) : make_float2(__uint_as_float(kRawBlock), 1.0f);
             }
         }
       } else if (ok && mine && !*abort_flag) {

@@ -368,3 +368,20 @@ def test_uneven_x(G, wt, case):
     G.repair_count(reset=True)
     assert_within(c.run(x=x), y, b)
     assert (G.repair_count() > 0) == (case in ("one block", "half"))
+
+
+@pytest.mark.parametrize("wt", [F32, F16, Q8, Q4, Q4K])
+@pytest.mark.parametrize("kind", list(EXPERTS))
+def test_experts_nan_goes_the_ordinary_way(G, wt, kind):
+    """Nothing but NaN comes of a NaN, so a token that holds one (and one whose x is infinite ahead of
+    the normalisation) costs the batch nothing."""
+    c = experts_case(G, wt, kind, seed=400)
+    x = c.x.copy()
+    x[0, 5] = np.nan
+    G.repair_count(reset=True)
+    got = c.run(x=x)
+    assert np.all(np.isnan(got[0])) and np.all(np.isfinite(got[1:]))
+    x[0, 5] = np.inf
+    got = c.run(x=x, norm=np.ones(c.K, np.float32))
+    assert np.all(np.isnan(got[0])) and np.all(np.isfinite(got[1:]))
+    assert G.repair_count() == 0
