@@ -444,18 +444,12 @@ int launch_experts(const ExpertsArgs& a, cudaStream_t st, bool pdl) {
       // (fewer than eight tokens always come this way: their groups are narrower than a column
       // tile; measured, 8 and 42 slots: 6.5 us through the list, 3.7 and 4.6 so)
       if (a.T * a.k <= kPackSlotThreads && a.cols <= 8) return launch_wt<ExpertsShort>(a, pack);
-      static int configured[64] = {0};
-      int dev = 0;
-      cudaGetDevice(&dev);
-      const int smem = prep_smem(a.E);
-      if (smem > 48 * 1024 && dev < 64 && configured[dev] < smem) {
-        const cudaError_t e = cudaFuncSetAttribute(experts_list_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        configured[dev] = smem;
-      }
+      static SmemLimit limit;
+      cudaError_t e = limit.raise(reinterpret_cast<const void*>(experts_list_kernel));
+      if (e != cudaSuccess) return e;
       cudaLaunchConfig_t list = config(dim3(1), kPrepThreads, st, pdl, &attr);
-      list.dynamicSmemBytes = static_cast<size_t>(smem);
-      const cudaError_t e = cudaLaunchKernelEx(&list, experts_list_kernel, a);
+      list.dynamicSmemBytes = static_cast<size_t>(prep_smem(a.E));
+      e = cudaLaunchKernelEx(&list, experts_list_kernel, a);
       if (e != cudaSuccess) return e;
       cudaLaunchAttribute behind;
       const cudaLaunchConfig_t cfg = config(pack.gridDim, kPackSlotThreads, st, true, &behind);

@@ -91,14 +91,9 @@ __global__ void __launch_bounds__(kGenericThreads) gemv_generic_kernel(const Gen
 template <int WT, int NC>
 static int launch_generic_t(const GenericArgs& a, int grid, int smem, cudaStream_t st, bool pdl) {
   auto kern = gemv_generic_kernel<WT, NC>;
-  static int configured[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (smem > 48 * 1024 && dev < 64 && configured[dev] < smem) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    configured[dev] = smem;
-  }
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern));
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kGenericThreads);

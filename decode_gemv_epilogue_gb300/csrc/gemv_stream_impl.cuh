@@ -923,14 +923,9 @@ __global__ void __launch_bounds__(stream_threads(WT, NC), 1)
 template <int WT, int NC, int FEAT>
 int launch_stream_t(const Plan& p, cudaStream_t st, bool pdl) {
   auto kern = gemv_stream_kernel<WT, NC, FEAT>;
-  static int configured_smem[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && configured_smem[dev] < p.smem) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
-    if (e != cudaSuccess) return e;
-    configured_smem[dev] = p.smem;
-  }
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern));
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.grid);
   cfg.blockDim = dim3(p.threads);
@@ -960,12 +955,8 @@ int launch_stream_t(const Plan& p, cudaStream_t st, bool pdl) {
 template <int WT, int NC>
 int max_active_clusters_t(const Plan& p) {
   auto kern = gemv_stream_kernel<WT, NC, FEAT_SPLIT>;
-  // raise the limit to the device maximum, never below what a launch of this kernel set
-  int dev = 0, smem_max = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&smem_max, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-      smem_max < p.smem ||
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max) != cudaSuccess) {
+  static SmemLimit limit;
+  if (limit.raise(reinterpret_cast<const void*>(kern)) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }

@@ -454,9 +454,7 @@ static int round_up_i(int v, int a) { return (v + a - 1) / a * a; }
 // Clusters of S CTAs of the split kernel that can be resident at once (0 if the device
 // cannot be asked): a cluster's CTAs share a GPC, so clusters of S may fit fewer times
 // than SMs / S.  Every plan holds one CTA per SM; the answer is kept per device and S.
-// The query raises the kernel's shared-memory limit to the device maximum, which keeps
-// every later launch's own (smaller) setting valid.
-static int tc_max_clusters(int S, int smem_max) {
+static int tc_max_clusters(int S) {
   static int cache[64][kMaxSplit + 1];
   static bool init[64][kMaxSplit + 1];
   static std::mutex mu;
@@ -469,7 +467,8 @@ static int tc_max_clusters(int S, int smem_max) {
   if (init[dev][S]) return cache[dev][S];
   int n = 0;
   auto kern = gemv_tc_kernel<true>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max) == cudaSuccess) {
+  static SmemLimit limit;
+  if (limit.raise(reinterpret_cast<const void*>(kern)) == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(S * 64);
     cfg.blockDim = dim3(kTcThreads);
@@ -503,7 +502,7 @@ bool plan_tc(int64_t M, int64_t K, int ncols, int epi, const DeviceLimits& lim, 
   S = std::min(S, nsub_all);
   while (S >= 2 && Np * kTcRows * 4 * (S <= 4 ? 4 : 8) > 64 * 1024) --S;
   while (S >= 2) {  // every cluster resident at once (when the device can say)
-    const int fit = tc_max_clusters(S, lim.smem_optin);
+    const int fit = tc_max_clusters(S);
     if (fit == 0 || tiles <= fit) break;
     --S;
   }
@@ -551,14 +550,9 @@ bool plan_tc(int64_t M, int64_t K, int ncols, int epi, const DeviceLimits& lim, 
 template <bool SPLIT>
 static int launch_tc_t(const CUtensorMap& map, const CUtensorMap& xmap, const TcPlan& p, cudaStream_t st, bool pdl) {
   auto kern = gemv_tc_kernel<SPLIT>;
-  static int configured[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && configured[dev] < p.smem) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
-    if (e != cudaSuccess) return e;
-    configured[dev] = p.smem;
-  }
+  static SmemLimit limit;
+  const cudaError_t raised = limit.raise(reinterpret_cast<const void*>(kern));
+  if (raised != cudaSuccess) return raised;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.grid);
   cfg.blockDim = dim3(kTcThreads);

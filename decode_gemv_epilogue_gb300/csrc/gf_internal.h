@@ -4,6 +4,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "smem_limit.h"
+
 struct CUtensorMap_st;  // the driver's tensor-map descriptor (cuda.h)
 struct gf_prepared;
 

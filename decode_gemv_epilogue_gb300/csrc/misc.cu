@@ -67,14 +67,9 @@ int launch_fwht(const float* x, const float* signs, float* dst, int64_t n, int B
   if (E > n) E = n;
   const int64_t grid = (n + E - 1) / E;
   const int smem = static_cast<int>(E * 4);
-  static int configured[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (smem > 48 * 1024 && dev < 64 && configured[dev] < smem) {
-    cudaError_t e = cudaFuncSetAttribute(fwht_signed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    configured[dev] = smem;
-  }
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(fwht_signed_kernel));
+  if (e != cudaSuccess) return e;
   const float scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(B)));
   fwht_signed_kernel<<<static_cast<unsigned>(grid), kFwhtThreads, smem, st>>>(x, signs, dst, n, B, nsigns,
                                                                             scale, static_cast<int>(E));

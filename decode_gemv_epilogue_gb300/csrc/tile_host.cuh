@@ -73,14 +73,9 @@ int launch_tile(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
   if (ns < 2 || o.max_groups / (ctas * o.sm_count) + 2 > kTileMaxGroups) return cudaErrorInvalidConfiguration;
   t.NS = ns;
   const int smem = fixed + static_cast<int>(x_all) + ns * stage;
-  static int configured[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && configured[dev] < smem) {
-    const cudaError_t c = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (c != cudaSuccess) return c;
-    configured[dev] = smem;
-  }
+  static SmemLimit limit;
+  e = limit.raise(reinterpret_cast<const void*>(kern));
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(ctas * o.sm_count)), kTileThreads, st, pdl, &attr);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
@@ -147,14 +142,9 @@ int launch_wide(TileArgs t, const TileOperands& o, cudaStream_t st, bool pdl) {
   t.NS = std::min(kTileMaxStages, (o.smem_optin - fixed) / stage);
   if (t.NS < 2) return cudaErrorInvalidConfiguration;
   const int smem = fixed + t.NS * stage;
-  static int configured[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && configured[dev] < smem) {
-    const cudaError_t c = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (c != cudaSuccess) return c;
-    configured[dev] = smem;
-  }
+  static SmemLimit limit;
+  e = limit.raise(reinterpret_cast<const void*>(kern));
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(o.sm_count)), 32 * (1 + wide_warps<WT>()), st, pdl, &attr);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
