@@ -596,14 +596,15 @@ int encode_map_2d(CUtensorMap* map, int dtype, const void* base, uint64_t inner,
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Encoded tensor maps of recent operands: a map holds only the address, shape, stride
-// and box, so an entry with the same key is always the right one.
+// Encoded tensor maps of recent operands: a map holds only the address, shape, stride,
+// box and swizzle, so an entry with the same key is always the right one.
 namespace {
 struct MapEntry {
   const void* base;
   uint64_t inner, rows;
   uint32_t box_inner, box_rows;
   int dtype;
+  bool swizzle128;
   CUtensorMap map;  // the type carries the 64-byte alignment the driver requires
 };
 constexpr int kMapCache = 64;
@@ -619,7 +620,7 @@ int cached_map_2d(const void* base, int dtype, uint64_t inner, uint64_t rows, ui
   for (int i = 0; i < g_map_used; ++i) {
     const MapEntry& e = g_maps[i];
     if (e.base == base && e.dtype == dtype && e.inner == inner && e.rows == rows && e.box_inner == box_inner &&
-        e.box_rows == box_rows) {
+        e.box_rows == box_rows && e.swizzle128 == swizzle128) {
       *out = e.map;
       return cudaSuccess;
     }
@@ -636,6 +637,7 @@ int cached_map_2d(const void* base, int dtype, uint64_t inner, uint64_t rows, ui
   e.rows = rows;
   e.box_inner = box_inner;
   e.box_rows = box_rows;
+  e.swizzle128 = swizzle128;
   *out = e.map;
   g_map_next = (g_map_next + 1) % kMapCache;
   if (g_map_used < kMapCache) ++g_map_used;
@@ -647,12 +649,12 @@ int launch_tc(const TcPlan& p, const void* W, cudaStream_t st, bool pdl) {
   // W: 128 x 64 f16 boxes, 128-byte swizzle; x (beyond 8 columns): [ncols][K] fp32, one
   // stage of every column
   int e = cached_map_2d(W, kMapF16, static_cast<uint64_t>(p.a.K), static_cast<uint64_t>(p.a.M), kTcK, kTcRows, true,
-                     &wmap);
+                        &wmap);
   if (e != cudaSuccess) return e;
   std::memset(&xmap, 0, sizeof(xmap));  // unused up to 8 columns
   if (p.a.ncols > 8) {
     e = cached_map_2d(p.a.x, kMapF32, static_cast<uint64_t>(p.a.K), static_cast<uint64_t>(p.a.ncols),
-                   static_cast<uint32_t>(p.a.subs * kTcK), static_cast<uint32_t>(p.a.ncols), false, &xmap);
+                      static_cast<uint32_t>(p.a.subs * kTcK), static_cast<uint32_t>(p.a.ncols), false, &xmap);
     if (e != cudaSuccess) return e;
   }
   return p.a.S > 1 ? launch_tc_t<true>(wmap, xmap, p, st, pdl) : launch_tc_t<false>(wmap, xmap, p, st, pdl);
