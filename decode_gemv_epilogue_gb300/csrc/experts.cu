@@ -213,9 +213,10 @@ __global__ void __launch_bounds__(kPackSlotThreads, 4) experts_prep_short_kernel
   __syncthreads();
   if (s == 0) a.places[mine] = place[0] < 0 ? make_int2(-1, 0) : make_int2(place[0], place[1] | (place[2] << 8));
   if (place[0] < 0) return;
-  const bool raw = pack_column(a.x + static_cast<int64_t>(mine / a.k) * a.K, place[1], s, kPackSlotThreads, a.gamma, a.eps,
-                               a.K, a.wtype, place[2],
-                               a.xrec + static_cast<int64_t>(place[0]) * (a.K / 32) * record_bytes(a.cp), wmax);
+  const bool raw = pack_column<kPackSlotThreads>(a.x + static_cast<int64_t>(mine / a.k) * a.K, place[1], a.gamma, a.eps,
+                                                 a.K, WT, place[2],
+                                                 a.xrec + static_cast<int64_t>(place[0]) * (a.K / 32) * record_bytes(a.cp),
+                                                 wmax);
   if (raw) exact_gated<WT>(a, mine, place[0], static_cast<uint32_t>(place[1]), static_cast<uint32_t>(place[2]));
 }
 
@@ -340,9 +341,9 @@ __global__ void __launch_bounds__(kPackSlotThreads, 5) experts_pack_kernel(const
   const int s = blockIdx.x;
   const int2 p = a.places[s];  // {column tile, column | columns stored << 8}
   if (p.x < 0) return;
-  const bool raw = pack_column(a.x + static_cast<int64_t>(s / a.k) * a.K, p.y & 255, threadIdx.x, kPackSlotThreads, a.gamma,
-                               a.eps, a.K, WT, p.y >> 8,
-                               a.xrec + static_cast<int64_t>(p.x) * (a.K / 32) * record_bytes(a.cp), wmax);
+  const bool raw = pack_column<kPackSlotThreads>(a.x + static_cast<int64_t>(s / a.k) * a.K, p.y & 255, a.gamma,
+                                                 a.eps, a.K, WT, p.y >> 8,
+                                                 a.xrec + static_cast<int64_t>(p.x) * (a.K / 32) * record_bytes(a.cp), wmax);
   if (raw) exact_gated<WT>(a, s, p.x, static_cast<uint32_t>(p.y) & 255u, static_cast<uint32_t>(p.y) >> 8);
 }
 

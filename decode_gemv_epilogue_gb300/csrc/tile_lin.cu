@@ -14,7 +14,7 @@ __global__ void __launch_bounds__(kPackThreads) tile_pack_kernel(const __grid_co
   const int col = static_cast<int>(blockIdx.x), tile = col / 8;
   const int first = tile * 8 / a.cols * a.cols;  // of the column group
   const int cp = min(8, min(a.cols, a.ncols - first));
-  pack_column(a.x + static_cast<int64_t>(col) * a.K, col % 8, threadIdx.x, kPackThreads, a.gamma, a.eps, a.K, a.wtype, cp,
+  pack_column<kPackThreads>(a.x + static_cast<int64_t>(col) * a.K, col % 8, a.gamma, a.eps, a.K, a.wtype, cp,
               a.records + static_cast<int64_t>(tile) * (a.K / 32) * record_bytes(a.cp), wmax);
 }
 

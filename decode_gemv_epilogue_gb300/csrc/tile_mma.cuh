@@ -185,20 +185,16 @@ __device__ __forceinline__ uint4 pack_group(float4 v, bool swapped, float& sum) 
                  : make_uint4(half_pair(a.hi, b.hi), half_pair(c.hi, d.hi), half_pair(a.lo, b.lo), half_pair(c.lo, d.lo));
 }
 
-// Column c of a column tile's records, by `share` consecutive threads (a multiple of 32) of a
-// CTA of kPackThreads, thread i0 of them; one scale for the whole column.  x: the column
-// (nullptr: none).  With gamma the column is first normalised, x / sqrt(mean(x^2) + eps)
-// gamma: gamma multiplies before packing, the root enters through the stored scale.  Every
-// thread of the CTA takes part.  wmax: kPackWords floats of shared memory.  Returns whether the
-// column went raw.
+// Column c of a column tile's records, by a CTA of THREADS (at most kPackThreads); one scale
+// for the whole column.  With gamma the column is first normalised, x / sqrt(mean(x^2) + eps)
+// gamma: gamma multiplies before packing, the root enters through the stored scale.  wmax:
+// kPackWords floats of shared memory.  Returns whether the column went raw.
 constexpr int kPackThreads = 1024;
 constexpr int kPackWords = 4 * kPackThreads / 32;
-// Threads of a column when `columns` (1..8) share a CTA.
-__device__ __forceinline__ int pack_share(int columns) {
-  return columns <= 1 ? 1024 : columns <= 2 ? 512 : columns <= 4 ? 256 : 128;
-}
-__device__ inline bool pack_column(const float* x, int c, int i0, int share, const float* gamma, float eps, int K, int fmt,
-                                   int cp, uint8_t* base, float* wmax) {
+template <int THREADS>
+__device__ __forceinline__ bool pack_column(const float* x, int c, const float* gamma, float eps, int K, int fmt, int cp, uint8_t* base,
+                                   float* wmax) {
+  const int i0 = threadIdx.x;
   const int lane = threadIdx.x & 31;
   const int n4 = K / 4, order = pack_order(fmt);
   const bool sums = pack_sums(fmt);
@@ -210,7 +206,7 @@ __device__ inline bool pack_column(const float* x, int c, int i0, int share, con
   float ss = 0.0f;
   auto load = [&](int i, bool sq) -> float4 {
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (x != nullptr && i < n4) {
+    if (i < n4) {
       v = four(x, i);
       if (gamma != nullptr) {
         if (sq) ss = fmaf(v.x, v.x, fmaf(v.y, v.y, fmaf(v.z, v.z, fmaf(v.w, v.w, ss))));
@@ -238,11 +234,11 @@ __device__ inline bool pack_column(const float* x, int c, int i0, int share, con
   float4 keep[kKeep];
   float m = 0.0f;
 #pragma unroll
-  for (int j = 0; j < kKeep; ++j) keep[j] = load(i0 + share * j, true);
+  for (int j = 0; j < kKeep; ++j) keep[j] = load(i0 + THREADS * j, true);
 #pragma unroll
   for (int j = 0; j < kKeep; ++j)
-    if (i0 + share * j < n4) m = fmaxf(m, top(keep[j]));
-  for (int i = i0 + share * kKeep; i < n4; i += share) m = fmaxf(m, top(load(i, true)));
+    if (i0 + THREADS * j < n4) m = fmaxf(m, top(keep[j]));
+  for (int i = i0 + THREADS * kKeep; i < n4; i += THREADS) m = fmaxf(m, top(load(i, true)));
   m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) {
@@ -259,26 +255,25 @@ __device__ inline bool pack_column(const float* x, int c, int i0, int share, con
   }
   __syncthreads();
   ss = small = 0.0f;
-  const int w0 = (threadIdx.x - i0) >> 5;  // the column's first warp
-  for (int q = 0; q < share / 32; ++q) {
-    m = fmaxf(m, wmax[w0 + q]);
-    ss += wmax[kPackThreads / 32 + w0 + q];
-    nan |= wmax[2 * kPackThreads / 32 + w0 + q] == 2.0f;
-    inf |= wmax[2 * kPackThreads / 32 + w0 + q] == 1.0f;
-    small += wmax[3 * kPackThreads / 32 + w0 + q];
+  for (int q = 0; q < THREADS / 32; ++q) {
+    m = fmaxf(m, wmax[q]);
+    ss += wmax[kPackThreads / 32 + q];
+    nan |= wmax[2 * kPackThreads / 32 + q] == 2.0f;
+    inf |= wmax[2 * kPackThreads / 32 + q] == 1.0f;
+    small += wmax[3 * kPackThreads / 32 + q];
   }
   // (normalised by an infinite mean square, what is finite is zero and the rest NaN: as packed)
   bool raw = inf && !nan && (gamma == nullptr || is_finite(ss));
   if (!inf && !nan && !(m * kCarryFours * small <= static_cast<float>(K))) {  // (the same for the whole column)
     unsigned n = 0;
 #pragma unroll 1
-    for (int i = i0; i < n4; i += share) n += tiny(load(i, false), m * kCarryTiny);
+    for (int i = i0; i < n4; i += THREADS) n += tiny(load(i, false), m * kCarryTiny);
     n = __reduce_add_sync(0xffffffffu, n);
     __syncthreads();
     if (lane == 0) wmax[threadIdx.x >> 5] = static_cast<float>(n);
     __syncthreads();
     float all = 0.0f;
-    for (int q = 0; q < share / 32; ++q) all += wmax[w0 + q];
+    for (int q = 0; q < THREADS / 32; ++q) all += wmax[q];
     raw = 8.0f * all > static_cast<float>(K);
   }
   const float sc = pack_scale(m);
@@ -287,7 +282,7 @@ __device__ inline bool pack_column(const float* x, int c, int i0, int share, con
   const int rec = record_bytes(cp);
   auto put = [&](int i, float4 v) {
     if (raw) {
-      if (x != nullptr && i < n4) {
+      if (i < n4) {
         uint8_t* r = base + static_cast<int64_t>(i >> 3) * rec;
         *reinterpret_cast<float4*>(r + record_offset(i & 7, c, cp, order)) = v;
         if ((i & 7) == 0) *reinterpret_cast<float2*>(r + cp * 128 + c * 8) = make_float2(__uint_as_float(kRawBlock), root);
@@ -300,16 +295,16 @@ __device__ inline bool pack_column(const float* x, int c, int i0, int share, con
     if (sums)
 #pragma unroll
       for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (x != nullptr && i < n4) {
+    if (i < n4) {
       uint8_t* r = base + static_cast<int64_t>(i >> 3) * rec;
       *reinterpret_cast<uint4*>(r + record_offset(i & 7, c, cp, order)) = packed;
       if ((i & 7) == 0) *reinterpret_cast<float2*>(r + cp * 128 + c * 8) = make_float2(inv, sums ? sum / tile_unit(WT_Q4_K) : 0.0f);
     }
   };
 #pragma unroll
-  for (int j = 0; j < kKeep; ++j) put(i0 + share * j, keep[j]);
-  for (int b = share * kKeep; b < n4; b += share) put(b + i0, load(b + i0, false));
-  __syncthreads();  // wmax may be used again
+  for (int j = 0; j < kKeep; ++j) put(i0 + THREADS * j, keep[j]);
+  for (int b = THREADS * kKeep; b < n4; b += THREADS) put(b + i0, load(b + i0, false));
+  __syncthreads();  // the column is written; wmax may be used again
   return raw;
 }
 
