@@ -393,22 +393,26 @@ static void fill_stream_ptrs(const Call& c, float* dst, unsigned* err, StreamArg
 // Plans one launch of at most one column block into r.
 static int plan_one(const Call& c, float* dst, LaunchRec& r) {
   int gsmem = 0, ggrid = 0;
-  const int path = plan_call(c, r.p, &gsmem, &ggrid, &r.tp);
+  Plan p;
+  TcPlan tp;
+  const int path = plan_call(c, p, &gsmem, &ggrid, &tp);
   if (path < 0) return path;
   unsigned* err = device_error_word();
   if (!err) return cuda_fail(cudaGetLastError());
   r.pdl = (c.flags & GF_FLAG_PDL) != 0;
   r.wtype = c.wtype;
   r.ncols = static_cast<int>(c.ncols);
-  r.W = c.W;
   if (path == PATH_TC) {
     r.kind = REC_TC;
+    r.tp = tp;
+    r.W = c.W;
     r.tp.a.x = c.x;
     r.tp.a.aux = c.aux;
     r.tp.a.dst = dst;
     r.tp.a.err = err;
   } else if (path == PATH_STREAM) {
     r.kind = REC_STREAM;
+    r.p = p;
     fill_stream_ptrs(c, dst, err, r.p.s);
   } else {
     r.kind = REC_GENERIC;
@@ -860,7 +864,7 @@ int gf_version(void) { return 5; }
 struct gf_prepared {
   int device;
   int n;
-  gf::LaunchRec recs[gf::kMaxRecs];
+  gf::LaunchRec* recs;  // n of them
 };
 
 static int prepare(const Call& c, const gf_opts* opts, gf_prepared** out) {
@@ -870,19 +874,10 @@ static int prepare(const Call& c, const gf_opts* opts, gf_prepared** out) {
   if (v != GF_OK) return v;
   v = c.nseg > 0 ? GF_OK : check_view(opts, c.M);
   if (v != GF_OK) return v;
-  gf_prepared* p = new (std::nothrow) gf_prepared;
-  if (!p) return GF_ERR_INVALID;
-  if (cudaGetDevice(&p->device) != cudaSuccess) {
-    delete p;
-    return cuda_fail(cudaGetLastError());
-  }
-  v = plan_launches(c, const_cast<float*>(c.dst), p->recs, kMaxRecs, &p->n);  // dst came in as float*
-  if (v != GF_OK) {
-    delete p;
-    return v;
-  }
-  *out = p;
-  return GF_OK;
+  LaunchRec recs[kMaxRecs];
+  int n = 0;
+  v = plan_launches(c, const_cast<float*>(c.dst), recs, kMaxRecs, &n);  // dst came in as float*
+  return v != GF_OK ? v : make_prepared(recs, n, out);
 }
 
 int gf_prepare(const void* W, int wtype, const float* x, int64_t M, int64_t K, int epilogue, const float* aux,
@@ -1177,6 +1172,7 @@ int gf_launch_prepared(const gf_prepared* const* calls, int n, void* stream) {
 
 void gf_free_prepared(gf_prepared* p) {
   if (!p) return;
+  delete[] p->recs;
   delete p;
 }
 
@@ -1232,24 +1228,13 @@ int gf_prepare_copy(void* dst, const void* src, int64_t bytes, uint32_t flags, g
   void* kd = nullptr;
   const int v = check_copy(dst, src, bytes, &ks, &kd);
   if (v != GF_OK) return v;
-  gf_prepared* p = new (std::nothrow) gf_prepared;
-  if (!p) return GF_ERR_INVALID;
-  if (cudaGetDevice(&p->device) != cudaSuccess) {
-    delete p;
-    return cuda_fail(cudaGetLastError());
-  }
-  p->n = 0;
-  if (bytes > 0) {
-    gf::LaunchRec& r = p->recs[0];
-    r.kind = gf::REC_COPY;
-    r.pdl = (flags & GF_FLAG_PDL) != 0;
-    r.csrc = ks;
-    r.cdst = kd;
-    r.cbytes = bytes;
-    p->n = 1;
-  }
-  *out = p;
-  return GF_OK;
+  gf::LaunchRec r;
+  r.kind = gf::REC_COPY;
+  r.pdl = (flags & GF_FLAG_PDL) != 0;
+  r.csrc = ks;
+  r.cdst = kd;
+  r.cbytes = bytes;
+  return make_prepared(&r, bytes > 0 ? 1 : 0, out);
 }
 
 // ------------------------------------------------------------------ step graphs
@@ -1324,14 +1309,19 @@ void gf_graph_free(gf_graph* g) {
 namespace gf {
 
 int make_prepared(const LaunchRec* recs, int n, gf_prepared** out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cuda_fail(cudaGetLastError());
   gf_prepared* p = new (std::nothrow) gf_prepared;
-  if (!p) return GF_ERR_INVALID;
-  if (cudaGetDevice(&p->device) != cudaSuccess) {
+  LaunchRec* copy = new (std::nothrow) LaunchRec[static_cast<size_t>(n)];
+  if (!p || !copy) {
     delete p;
-    return cuda_fail(cudaGetLastError());
+    delete[] copy;
+    return GF_ERR_INVALID;
   }
+  std::copy(recs, recs + n, copy);
+  p->device = dev;
   p->n = n;
-  for (int i = 0; i < n; ++i) p->recs[i] = recs[i];
+  p->recs = copy;
   *out = p;
   return GF_OK;
 }

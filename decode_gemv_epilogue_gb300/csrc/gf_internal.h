@@ -326,26 +326,37 @@ enum {
 struct LaunchRec {
   int kind;
   bool pdl;
-  const void* csrc;  // host staging copy (device-addressable pointers)
-  void* cdst;
-  int64_t cbytes;
-  int wtype, ncols;
-  const void* W;  // tensor-core path: the matrix of the tensor map
-  const float* fx;  // stand-alone FWHT
-  const float* fsigns;
-  float* fdst;
-  int64_t fn;
-  int fB, fnsigns;
-  TcPlan tp;
-  Plan p;
-  GenericArgs g;
-  int ggrid, gsmem;
-  int ewop;           // element-wise op over fx and fsigns (fn elements)
-  RouteArgs route;
-  ExpertsArgs experts;
-  LoraArgs lora;
-  LinArgs lin;
+  int wtype, ncols;  // REC_STREAM, REC_GENERIC
+  union {            // by kind
+    struct {         // REC_COPY: host staging copy (device-addressable pointers)
+      const void* csrc;
+      void* cdst;
+      int64_t cbytes;
+    };
+    struct {  // REC_FWHT: stand-alone FWHT; REC_EW: element-wise op over fx and fsigns (fn elements)
+      const float* fx;
+      const float* fsigns;
+      float* fdst;
+      int64_t fn;
+      int fB, fnsigns, ewop;
+    };
+    struct {  // REC_TC
+      TcPlan tp;
+      const void* W;  // the matrix of the tensor map
+    };
+    Plan p;   // REC_STREAM
+    struct {  // REC_GENERIC
+      GenericArgs g;
+      int ggrid, gsmem;
+    };
+    RouteArgs route;
+    ExpertsArgs experts;
+    LoraArgs lora;
+    LinArgs lin;
+  };
 };
+// (a direct call plans into kMaxRecs of them on its stack)
+static_assert(sizeof(LaunchRec) <= sizeof(Plan) + 16, "the streamed kernel's plan is the largest");
 constexpr int kMaxRecs = 1 + kMaxSeg * (kMaxBatch / kMaxCols);  // transform + column blocks (per matrix)
 
 // Shared by the entry points (api.cu, api_select.cu).
@@ -354,7 +365,7 @@ bool ranges_overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes
 int cuda_fail(cudaError_t e);
 DeviceLimits device_limits();
 int issue(const LaunchRec& r, cudaStream_t st);
-// A handle over n (<= kMaxRecs) planned launches; a gf_status.
+// A handle over n planned launches; a gf_status.
 int make_prepared(const LaunchRec* recs, int n, gf_prepared** out);
 
 unsigned* device_error_word();  // this device's error word (nullptr on failure)
