@@ -102,7 +102,7 @@ static bool columns_ok(int wtype, int64_t n) {
 
 // Whether the tiled kernels take this call (both products or neither).
 static bool experts_tiled(const gf_experts* x) {
-  return x->K % 32 == 0 && x->M % 32 == 0 && x->M > 0 &&
+  return x->K % 32 == 0 && x->M % 32 == 0 && x->M > 0 && !(x->flags & GF_FLAG_NO_TENSOR_CORES) &&
          aligned_to(x->W_gate, 16) && aligned_to(x->W_up, 16) && aligned_to(x->W_down, 16);
 }
 

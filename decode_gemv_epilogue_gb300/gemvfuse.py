@@ -479,18 +479,19 @@ def experts_workspace(E, T, top_k, M, K):
 
 
 def _experts_struct(W_gate, W_up, wtype, W_down, wtype_down, E, M, K, ids, weights, top_k, workspace,
-                    workspace_bytes, rms_norm_weight, rms_norm_eps, pdl):
+                    workspace_bytes, rms_norm_weight, rms_norm_eps, pdl, tensor_cores):
     return Experts(_ptr(W_gate), _ptr(W_up), _ptr(W_down), wtype, wtype_down, E, M, K, _ptr(ids), _ptr(weights),
                    top_k, _ptr(workspace), _nbytes(workspace, workspace_bytes), _ptr(rms_norm_weight), rms_norm_eps,
-                   FLAG_PDL if pdl else 0)
+                   (FLAG_PDL if pdl else 0) | (0 if tensor_cores else FLAG_NO_TENSOR_CORES))
 
 
 def gemv_experts(W_gate, W_up, wtype, W_down, wtype_down, E, x, M, K, ids, weights, T, top_k, aux, dst, workspace,
-                 workspace_bytes=None, rms_norm_weight=None, rms_norm_eps=0.0, pdl=False, stream=None, check=True):
+                 workspace_bytes=None, rms_norm_weight=None, rms_norm_eps=0.0, pdl=False, stream=None, check=True,
+                 tensor_cores=True):
     """dst_t = aux_t + sum_j weights_tj Wd_e (silu(Wg_e x'_t) * (Wu_e x'_t)), e = ids_tj (see
     include/gemvfuse.h)."""
     ex = _experts_struct(W_gate, W_up, wtype, W_down, wtype_down, E, M, K, ids, weights, top_k, workspace,
-                         workspace_bytes, rms_norm_weight, rms_norm_eps, pdl)
+                         workspace_bytes, rms_norm_weight, rms_norm_eps, pdl, tensor_cores)
     st = _gemv_experts(ctypes.byref(ex), _ptr(x), T, _ptr(aux), _ptr(dst), _stream(stream))
     if check:
         _check(st, "gemv_experts")
@@ -498,10 +499,11 @@ def gemv_experts(W_gate, W_up, wtype, W_down, wtype_down, E, x, M, K, ids, weigh
 
 
 def prepare_experts(W_gate, W_up, wtype, W_down, wtype_down, E, x, M, K, ids, weights, T, top_k, aux, dst, workspace,
-                    workspace_bytes=None, rms_norm_weight=None, rms_norm_eps=0.0, pdl=False, check=True):
+                    workspace_bytes=None, rms_norm_weight=None, rms_norm_eps=0.0, pdl=False, check=True,
+                    tensor_cores=True):
     """gf_prepare_experts: the call gemv_experts(...) would make, planned once (see Prepared)."""
     ex = _experts_struct(W_gate, W_up, wtype, W_down, wtype_down, E, M, K, ids, weights, top_k, workspace,
-                         workspace_bytes, rms_norm_weight, rms_norm_eps, pdl)
+                         workspace_bytes, rms_norm_weight, rms_norm_eps, pdl, tensor_cores)
     h = _vp()
     st = _prepare_experts(ctypes.byref(ex), _ptr(x), T, _ptr(aux), _ptr(dst), ctypes.byref(h))
     if check:
@@ -511,12 +513,12 @@ def prepare_experts(W_gate, W_up, wtype, W_down, wtype_down, E, x, M, K, ids, we
 
 
 def plan_experts(W_gate, W_up, wtype, W_down, wtype_down, E, x, M, K, ids, weights, T, top_k, aux, dst, workspace,
-                 workspace_bytes=None, rms_norm_weight=None, rms_norm_eps=0.0, pdl=False):
+                 workspace_bytes=None, rms_norm_weight=None, rms_norm_eps=0.0, pdl=False, tensor_cores=True):
     """gf_plan_experts: (path, info) of gemv_experts(...) without launching: path 0 = nothing to launch,
     2 = generic, 4 = tiled, <0 = error; info: columns of a group, whether gate and up, and down, run on
     the wide kernel."""
     ex = _experts_struct(W_gate, W_up, wtype, W_down, wtype_down, E, M, K, ids, weights, top_k, workspace,
-                         workspace_bytes, rms_norm_weight, rms_norm_eps, pdl)
+                         workspace_bytes, rms_norm_weight, rms_norm_eps, pdl, tensor_cores)
     info = (_i64 * 8)()
     path = _plan_experts(ctypes.byref(ex), _ptr(x), T, _ptr(aux), _ptr(dst), ctypes.byref(info))
     return path, dict(cols=info[0], wide=bool(info[1]), wide_down=bool(info[2]))

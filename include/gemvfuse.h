@@ -334,7 +334,8 @@ GF_API int gf_prepare_route(const float* logits, int64_t T, int64_t E, const gf_
  *  workspace    : device memory of at least gf_experts_workspace() bytes, 256-byte aligned,
  *                 contents undefined before and after; not shared by calls that may overlap.
  *  Shapes: K and M multiples of 32 (256 for a Q4_K matrix's columns) with 16-byte aligned
- *  matrices take the tiled kernels, anything else the generic ones.
+ *  matrices take the tiled kernels on the tensor cores (x and the gated values as f16 hi + lo
+ *  parts), anything else, and GF_FLAG_NO_TENSOR_CORES, the generic ones in 32 bits.
  *  dst may not overlap W_*, x, ids, weights, rms_norm_weight or the workspace; the workspace
  *  no argument.
  *  Limits (GF_ERR_UNSUPPORTED beyond): T <= 256, top_k <= 32, E <= 1024, M and K <= 2^20,
@@ -352,7 +353,7 @@ typedef struct {
   int64_t workspace_bytes;
   const float* rms_norm_weight;  /* [K] or NULL: no normalisation of x              */
   float rms_norm_eps;
-  uint32_t flags;      /* GF_FLAG_PDL                                               */
+  uint32_t flags;      /* GF_FLAG_PDL, GF_FLAG_NO_TENSOR_CORES (the generic kernels) */
 } gf_experts;
 GF_API int gemv_experts(const gf_experts* ex, const float* x, int64_t T, const float* aux, float* dst,
                         void* stream);

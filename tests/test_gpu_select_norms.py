@@ -64,3 +64,24 @@ def test_lora(G, N, M, K, wt):
     c = test_gpu_lora.Case(G, N, M, K, wt, 3, 8, F16, seed=540 + N)
     c.ids[:] = np.arange(N) % 4 - 1
     print("off by %.3g" % assert_norms(c.run(0), c.want(0)[0]))
+
+
+@pytest.mark.parametrize("wt", ALL)
+def test_experts_without_tensor_cores(G, wt):
+    """The generic kernels where the tiled ones would take the call: 32 bits throughout."""
+    T, E, k, M, K = 9, 4, 2, 256, 512
+    c = test_gpu_experts.Case(G, T, E, k, M, K, wt, wt, seed=560)
+    ws = torch.empty(G.experts_workspace(E, T, k, M, K), dtype=torch.uint8, device="cuda")
+    dst = torch.empty(T, K, device="cuda")
+    args = (c.dev[0], c.dev[1], wt, c.dev[2], wt, E, dev_tensor(c.x), M, K, dev_tensor(c.ids), dev_tensor(c.w), T, k, None,
+            dst, ws)
+    assert G.plan_experts(*args)[0] == 4 and G.plan_experts(*args, tensor_cores=False)[0] == 2
+    G.gemv_experts(*args, tensor_cores=False)
+    torch.cuda.synchronize()
+    got = dst.cpu().numpy()
+    assert_norms(got, c.want(aux=False)[0], tol=1e-6)
+    graph = G.Graph([G.prepare_experts(*args, tensor_cores=False)])
+    dst.zero_()
+    graph.launch()
+    torch.cuda.synchronize()
+    assert np.array_equal(got.view(np.uint32), dst.cpu().numpy().view(np.uint32))

@@ -46,6 +46,8 @@ def test_experts_other_answers(lib):
     assert experts(lib, Q4, Q4, 4, 8, 2, 256, 256, shift=8)[0] == 2  # off a 16-byte boundary
     assert experts(lib, F16, F16, 4, 8, 2, 250, 256)[0] == 2
     assert experts(lib, F16, F16, 4, 8, 2, 0, 256)[0] == 2
+    assert experts(lib, Q4, Q4, 4, 8, 2, 256, 256)[0] == 4
+    assert experts(lib, Q4, Q4, 4, 8, 2, 256, 256, tensor_cores=False)[0] == 2
     assert experts(lib, Q4, Q4, 0, 8, 2, 256, 256)[0] == 0
     assert experts(lib, Q4, Q4, 257, 8, 2, 256, 256)[0] == lib.ERR_UNSUPPORTED
     assert experts(lib, Q4, Q4, 4, 8, 9, 256, 0)[0] == 0
