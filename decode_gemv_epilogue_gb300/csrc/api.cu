@@ -918,7 +918,7 @@ static int64_t lin_record_bytes(int64_t ncols, int64_t K) {
 // 33 / 43; 14336 x 4096, 8 76 / 60, 32 122 / 209.  F16 on the tensor-core kernel: 4096 x 4096,
 // 32 columns 37 / 36, 64 59 / 62, 256 174 / 218; off it, 4096 x 4064, 8 29 / 29, 16 35 / 45.
 static bool lin_takes(const Call& c) {
-  if (c.K < 32 || c.K % 32 != 0 || c.K > (1 << 20) || c.M < 8 || !aligned(c.W, 16) ||
+  if (c.K < 32 || c.K % 32 != 0 || c.K > (1 << 20) || c.M < 8 || c.M > (1 << 30) || !aligned(c.W, 16) ||
       (c.flags & GF_FLAG_NO_TENSOR_CORES))
     return false;
   const int64_t work = c.M * c.K * c.ncols;

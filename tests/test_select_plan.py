@@ -66,3 +66,9 @@ def test_lora_answers(lib):
     assert lora(lib, Q4, 64, 0, 1024)[0] == 0
     assert lora(lib, Q4, 64, 600, 1024, r=257)[0] == lib.ERR_UNSUPPORTED
     assert lib.raw.gf_plan_lora(BASE[0], Q4, BASE[1], 8, 32, 0, None, BASE[2], None, None, None) == lib.ERR_INVALID
+
+
+@pytest.mark.parametrize("M, path", [(1 << 30, 4), ((1 << 30) + 64, 1), ((1 << 31) - 8, 1)])
+def test_lora_rows_near_the_end_of_32_bits(lib, M, path):
+    """The tiled kernels count rows, rounded up to a tile, in 32 bits."""
+    assert lora(lib, Q4, 17, M, 256)[0] == path
