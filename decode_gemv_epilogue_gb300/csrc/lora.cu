@@ -5,8 +5,9 @@
 //   expand:  out_c = B_a v_c (+ aux_c)     [M values per column]
 //
 // and the shared product then adds out in its epilogue, before the activation.  In this
-// order the shared product, launched with programmatic dependent launch, already streams its
-// weights while the two small kernels run, and the output is read and written once more only.
+// order the output is read and written once more only, and the kernels of plain batches, launched
+// with programmatic dependent launch, already stream their weights while the two small kernels
+// run (the tiled ones wait for both before their first copy).
 //
 // Columns that share an adapter are served together, so that an adapter's rows are fetched
 // once per four columns (shrink) or once (expand): with fewer adapters than columns a CTA is
@@ -233,8 +234,8 @@ __device__ __forceinline__ void stage_b(const LoraArgs& a, const uint8_t* B, int
 }
 
 // The first chunk of B and the ids are read before the wait for the shrinking grid: whatever
-// precedes that one is complete once its CTAs have triggered.  The product may start (it reads W
-// before its own wait) as soon as every CTA here has started.  With the asynchronous copies, the
+// precedes that one is complete once its CTAs have triggered.  The product may start as soon as
+// every CTA here has started (and, but for the tiled one, reads W before its own wait).  With the asynchronous copies, the
 // whole call: one column of 4096 x 4096 Q4_0 13.7 -> 13.0 us, eight of F16 24.0 -> 22.8, 64 of
 // 14336 x 4096 Q4_0 106 -> 103.
 // VEC: rows of B are whole 16-byte words.

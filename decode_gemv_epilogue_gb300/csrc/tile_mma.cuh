@@ -1,11 +1,12 @@
 // Tiled products of block-format weights with several columns on the tensor cores: the
 // device code of the chosen experts' kernels and of wide batches beside adapters.
 //
-// x is "packed" first: every 32 elements of a column become 32 pairs of f16,
+// x is "packed" first: its elements become pairs of f16,
 //     x * 2^s = hi + lo,   hi = f16(x 2^s),   lo = f16(x 2^s - hi)
-// with a power of two 2^s that puts the largest magnitude into [2^14, 2^15): hi + lo carries
-// x to 2^-22 of itself (2^-39 of the largest where lo is subnormal), less than the rounding
-// of a 32-bit sum.  The weights' codes are exact in f16, the products of f16 are exact in
+// with a power of two 2^s, one for a column of x and one for every 32 gated values, that puts the
+// largest magnitude under it into [2^14, 2^15): hi + lo carries x to 2^-22 of itself or 2^-39 of
+// the largest, whichever is more (columns for which that is too much go another way, below): 22
+// bits where 24 would need a third product.  The weights' codes are exact in f16, the products of f16 are exact in
 // the 32-bit accumulators, and the blocks' scales multiply the accumulated sum of a block in
 // 32 bits: the only roundings are those of 32-bit sums (truncated ones in the matrix unit,
 // which is why its sums end with the block, and take the low parts first).
@@ -22,10 +23,13 @@
 // bits: an error of 5e-6 of the result; 16 times the code: 5e-7).  Its sums are in units of
 // 2^-18, taken back in the tail.
 //
-// Why mma.sync and not the asynchronous matrix unit: a block format's scale belongs to 32
-// weights of one row, so the accumulator of every 32 columns of K has to pass through
-// registers to be scaled (folding the scale into f16 weights would round them); with
-// accumulators in tensor memory that is one read-back per two instructions.
+// Why mma.sync: a block format's scale belongs to 32 weights of one row, and here a block's sum is
+// scaled where it arises, in registers; with accumulators in tensor memory that would be one
+// read-back per two instructions.  (The asynchronous unit could take weights that are scaled
+// already: two f16 parts hold a scale times a code exactly, 11 bits times 4, 8 or 10, under a
+// power of two per row, at three products instead of two and a way through shared memory for
+// every decoded weight.  That is not built.  F16 batches of up to 16 columns a pass, which
+// have no scales, go that way in gemv_tc.cu.)
 //
 // F32 weights take tf32 instructions: w = hi + lo in two tf32 (to 2^-22 of it), and the sums
 // hi(w) hi(x) + lo(w) hi(x) + hi(w) lo(x); hi(x) and lo(x), f16, are exact in tf32.
@@ -106,8 +110,9 @@ __host__ __device__ constexpr int tile_seg() {  // bytes of a row and chunk
 // bytes and {kRawBlock, their factor} behind them (all blocks of a packed column, single blocks
 // of the gated values);
 // cp = min(8, columns of the group) columns are stored, so that a single column does not move
-// eight (column tiles are allocated for the most any group of the call can have).  A warp's 16-byte reads of a step are then consecutive, and the records of a K chunk
-// are one piece of memory for one bulk copy.  Which four elements (s, t) holds is the
+// eight (column tiles are allocated for the most any group of the call can have).  A warp's
+// 16-byte reads of a step are then consecutive, and the records of a K chunk are one piece of
+// memory for one bulk copy.  Which four elements (s, t) holds is the
 // weights' choice: 16 s + 4 t + .. in the order 0, 2, 1, 3 for the nibble formats (two masks
 // take a code word apart in that order), 16 s + 4 t + 0..3 for Q8_0 and F32, and 8 t + 4 s + 0..3
 // for F16 (a thread then reads 16 bytes of a row at once).
@@ -126,7 +131,7 @@ __device__ __forceinline__ uint32_t record_offset(uint32_t q, uint32_t c, uint32
   return (s * cp + c) * 64u + t * 16u;
 }
 
-// 2^s for the largest magnitude m (finite), s in [-112, 126]; 1 for m = 0.
+// 2^s for the largest magnitude m (finite), s in [-113, 126]; 1 for m = 0.
 __device__ __forceinline__ float pack_scale(float m) {
   const int e = static_cast<int>((__float_as_uint(m) >> 23) & 0xFFu);  // m in [2^(e-127), 2^(e-126))
   const int s = m == 0.0f ? 0 : max(-126, min(126, 14 + 127 - e));
@@ -141,9 +146,9 @@ __device__ __forceinline__ float pow2_inverse(float p) {
 // largest magnitude is m, hi + lo moves a value by at most 2^-22 of itself or 2^-39 m, whichever
 // is more.  That is little next to the products of a row unless many values lie far below m and
 // the weights of those near m are zero; and a NaN or an infinity in hi makes NaN of what should be
-// an infinity (the other part, or Q4_K's mins, take it off again).  A value is tiny where it is not zero and below 2^-18 m
-// (the others move by at most 2^-21 of themselves).  Carried is what holds a NaN, since nothing
-// but NaN comes of it, and are finite values
+// an infinity (the other part, or Q4_K's mins, take it off again).  A value is tiny where it is
+// not zero and below 2^-18 m (the others move by at most 2^-21 of themselves).  Carried is what
+// holds a NaN, since nothing but NaN comes of it, and are finite values
 //  - of a packed column, if m times the sum over every four neighbours of 1 / q, q the sum of the
 //    two smaller of them, is at most 2^16 K (the four then move by at most 2^-19 q on the mean) or
 //    if at most an eighth of them are tiny (normal values: m up to 40000 standard deviations; the
@@ -628,8 +633,9 @@ struct TileLane {
 // This warp's block `blk` of a stage (weights at st, its records at xs): acc += W x for 64
 // rows and NTA column tiles.  PER1: rows lie at the constant pitch of period 1.  FEW: up to four
 // columns, whose hi parts are the columns 0..3 and whose lo parts are the columns 4..7 of one
-// matrix tile: half the matrix instructions, and half as many in a row (gate and up of 7 tokens
-// through 6 of 64 Q4_0 experts of 1408 x 2048: 35.8 -> 33.9 us).
+// matrix tile: half the matrix instructions, and half as many in a row (whole calls with cold
+// weights: one token through 8 of 128 Q4_0 experts of 768 x 2048 24.0 -> 23.2 us, Q8_0 26.8 ->
+// 26.0; 4 columns of 14336 x 4096 Q4_0 with adapters 28.0 -> 27.1, Q4_K 31.7 -> 30.6).
 template <int WT, int MODE, int NTA, int NT, bool PER1, bool WHOLE, bool FEW>
 __device__ __forceinline__ void tile_block(const TileLane& l, uint32_t st, uint32_t xs, uint32_t blk,
                                            float (&acc)[4][NT][4]) {
