@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemv_tc_kernel(const __grid_con
       const uint32_t bits = __float_as_uint(m);
       const int E = static_cast<int>((bits >> 23) & 255u);
       int sh = 0;
-      if (m > 0.0f && E < 255) sh = min(120, max(-120, 15 - (E == 0 ? -126 : E - 126)));
+      if (m > 0.0f) sh = min(120, max(-120, 15 - (E == 0 ? -126 : E - 126)));  // (infinite: -114, no finite x overflows)
       scl[ctid] = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
       iscl[ctid] = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
     }
@@ -282,7 +282,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemv_tc_kernel(const __grid_con
           for (int t = 0; t < 4; ++t) {
             const __half2 h = __floats2half2_rn(v[t].x, v[t].y);
             const float2 rr = fsub2(v[t], __half22float2(h));
-            const __half2 l = __floats2half2_rn(rr.x, rr.y);
+            // (at most 8 in size; a NaN, behind an infinite or NaN hi, becomes a number: hi alone
+            // then gives the definition's infinity or NaN)
+            const __half2 l = __floats2half2_rn(fmaxf(rr.x, -8.0f), fmaxf(rr.y, -8.0f));
             hw[t] = *reinterpret_cast<const uint32_t*>(&h);
             lw[t] = *reinterpret_cast<const uint32_t*>(&l);
           }
