@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemv_tc_kernel(const __grid_con
             const float2 rr = fsub2(v[t], __half22float2(h));
             // (at most 8 in size; a NaN, behind an infinite or NaN hi, becomes a number: hi alone
             // then gives the definition's infinity or NaN)
-            const __half2 l = __floats2half2_rn(fmaxf(rr.x, -8.0f), fmaxf(rr.y, -8.0f));
+            const __half2 l = __hmax2(__floats2half2_rn(rr.x, rr.y), __float2half2_rn(-8.0f));
             hw[t] = *reinterpret_cast<const uint32_t*>(&h);
             lw[t] = *reinterpret_cast<const uint32_t*>(&l);
           }
