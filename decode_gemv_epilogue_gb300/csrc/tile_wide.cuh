@@ -18,7 +18,7 @@
 // An item is a large piece of a launch (a quarter of a CTA's share, in that case), and column
 // groups differ in size: the experts' items are handed out one by one, large groups first,
 // instead of in equal ranges, which left the SMs idle for a fifth of the time.  What bounds it
-// now: the matrix unit, 41% busy on average while its four warps collide on it (throttled for
+// now: the matrix unit, 39% busy on average while its four warps collide on it (throttled for
 // as long as they issue), and one issue slot in two.
 #pragma once
 
