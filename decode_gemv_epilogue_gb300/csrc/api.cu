@@ -449,6 +449,14 @@ int issue(const LaunchRec& r, cudaStream_t st) {
     e = launch_lora(r.lora, st, r.pdl);
   } else if (r.kind == REC_LIN) {
     e = launch_lin(r.lin, st, r.pdl);
+  } else if (r.kind == REC_ROPE) {
+    e = launch_rope(r.rope, st, r.pdl);
+  } else if (r.kind == REC_STORE) {
+    e = launch_store(r.store, device_limits().sm_count, st, r.pdl);
+  } else if (r.kind == REC_LOAD) {
+    e = launch_load(r.load, st, r.pdl);
+  } else if (r.kind == REC_ATTEND) {
+    e = launch_attend(r.attend, st, r.pdl);
   } else if (r.kind == REC_EW) {
     e = launch_elementwise(r.ewop, r.fx, r.fsigns, r.fn, r.fdst, r.fn, st);
   } else if (r.kind == REC_COPY) {

@@ -1,0 +1,748 @@
+// Attention of a decode step over the 8-bit cache (gf_attend).
+//
+// One pass over a row's keys and values with the running maximum and sum of the softmax.  What bounds it
+// is reading the codes, so they go straight from memory to the registers that feed the matrix
+// instructions: each lane copies (cp.async) just the bytes that it decodes itself, into slots of its own.
+//
+// A warp takes a chunk of CT tokens.  m16n8k16 with the queries as the 16 rows: eight rows' f16 high parts and
+// the same rows' low parts (q = hi + lo to 22 bits under a power of two a row), so that one instruction
+// gives both and a lane holds the two halves of its own sums.  Codes are exact in f16.  The contraction
+// over dims and the order of the tokens are free, so that
+//   keys  : lane (g, c) takes 16-byte units c, c + 4, .. of token g; the four bytes of a word are the
+//           two k pairs of one instruction;
+//   values: lane (g, c) takes unit g of the four tokens that its k indices mean; the bytes of four
+//           tokens' words are paired by dim, and dim j of unit g is column g of instruction j.
+// The weights p * scale_v are split into hi + lo like the queries.  A chunk's products are added to the
+// running ones in 32 bits, outside the matrix unit (which truncates).
+//
+// Items, (tokens of a sequence next to each other, head of the cache, part of its queries), are laid end
+// to end by their number of chunks, and every CTA takes an equal stretch; the parts of an item that
+// stretches over CTAs go through the workspace, and a second launch joins them in order.
+#include "cache_device.cuh"
+#include "gf_device.cuh"
+#include "rope_device.cuh"
+
+namespace gf {
+
+template <int DC, int NM>
+struct AttShape {
+  static constexpr int kTokens = DC == 256 ? 16 : 32;               // of a chunk
+  static constexpr int kWarps = (DC <= 128 && NM == 1) || DC == 256 ? 6 : 4;
+  static constexpr int kRows = 8 * NM;
+  static constexpr int kSteps = DC / 16;                            // instructions along the dims
+  static constexpr int kScaleAt = 2 * kTokens * DC;                 // of a stage: keys, values, scales
+  static constexpr int kStage = kScaleAt + 2 * kTokens * 4;
+  static constexpr int kStages = 2;
+  static constexpr int kQBytes = NM * kSteps * 512;
+  static constexpr int kRowFloats = DC + 2;                         // a row's part: sums, maximum, sum of weights
+  static constexpr int kSmem = kQBytes + kWarps * kStages * kStage;
+  static_assert(kRows * kRowFloats * 4 <= kStage, "a warp's part fits the stage that it has used up");
+};
+
+constexpr float kNoMax = -1e30f;   // running maximum of a row without keys
+constexpr float kHidden = -1.0f;   // scale of a token that no row sees (stored ones are positive, or NaN)
+constexpr uint32_t kWeightBits = 8;     // weights times the largest scale reach 2^8 (f16 parts)
+
+// ------------------------------------------------------------------ small pieces
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Bytes (0, 1) and (2, 3) of a word of codes as pairs of f16.  i8: 1024 + (code + 128) is an f16 whose
+// low byte is the code, less 1152.
+template <int FMT>
+__device__ __forceinline__ void pairs_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (FMT == 0) {
+    w ^= 0x80808080u;
+    lo = h2_sub(__byte_perm(w, 0x64646464u, 0x4140), 0x64806480u);
+    hi = h2_sub(__byte_perm(w, 0x64646464u, 0x4342), 0x64806480u);
+  } else {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<uint16_t>(w)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(w >> 16)));
+  }
+}
+
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// f16 high and low parts of two values, as pairs.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+// ------------------------------------------------------------------ items
+struct Item {
+  int64_t begin;   // its first chunk, among all items'
+  int t0, n;       // tokens
+  int seq;
+  int lo, hi;      // keys [lo, hi) that its tokens see together
+  int chunks;      // of one (head, part) of it
+  int hs;          // head * subs + part
+};
+
+// Keys that token t sees, [lo, hi); none: hi = 0.
+__device__ __forceinline__ void keys_of(const AttendArgs& a, int t, int& seq, int& lo, int& hi) {
+  seq = a.seq ? a.seq[t] : t;
+  lo = hi = 0;
+  if (seq < 0 || seq >= a.c.n_seqs) {
+    seq = -1;
+    return;
+  }
+  const int64_t most = a.c.table_ld << a.c.page_log2;
+  const int p = a.pos[t];
+  if (p < 0) {
+    seq = -1;
+    return;
+  }
+  hi = static_cast<int>(static_cast<int64_t>(p) + 1 < most ? p + 1 : most);
+  const int64_t first = a.window > 0 ? static_cast<int64_t>(p) + 1 - a.window : 0;
+  lo = static_cast<int>(first < 0 ? 0 : first < hi ? first : hi);
+}
+
+// Whether an item may begin with token t wherever the sequences lie: `run` tokens of a sequence are expected
+// next to each other, and fall into items of `tokens`.
+__device__ __forceinline__ bool item_edge(const AttendArgs& a, int t) { return t % a.run % a.tokens == 0; }
+
+// The item that begins with token t, if one does: neighbouring tokens of one sequence up to the next edge.
+template <int CT>
+__device__ __forceinline__ bool item_at(const AttendArgs& a, int t, Item& it) {
+  int seq, lo, hi;
+  keys_of(a, t, seq, lo, hi);
+  it.t0 = t;
+  it.n = 1;
+  it.seq = seq;
+  if (a.tokens > 1 && seq >= 0) {
+    if (!item_edge(a, t)) {
+      int s, l, h;
+      keys_of(a, t - 1, s, l, h);
+      if (s == seq) return false;
+    }
+    for (int i = t + 1; i < a.T && !item_edge(a, i); ++i) {
+      int s, l, h;
+      keys_of(a, i, s, l, h);
+      if (s != seq) break;
+      lo = l < lo ? l : lo;
+      hi = h > hi ? h : hi;
+      ++it.n;
+    }
+  }
+  it.lo = lo;
+  it.hi = hi;
+  const int c = (hi + CT - 1) / CT - lo / CT;
+  it.chunks = c > 0 ? c : 1;
+  return true;
+}
+
+// Workspace: a header, a record for each CTA's first item, then each CTA's two parts.
+struct AttHeader {
+  int64_t chunks;
+  int64_t ctas;
+};
+struct AttFirst {
+  int64_t begin, end;
+  int t0, n, hs, pad;
+};
+constexpr int kAttHead = 64;
+__host__ __device__ constexpr int64_t att_parts_at(int ctas) { return kAttHead + static_cast<int64_t>(ctas) * 32; }
+
+// Chunk at which CTA i of n begins.
+__device__ __forceinline__ int64_t share(int64_t chunks, int64_t i, int64_t n) { return chunks * i / n; }
+
+template <typename T>
+__device__ __forceinline__ T block_sum(T v, T* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if (lane == 0) scratch[warp] = v;
+  __syncthreads();
+  T s = 0;
+  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) s += scratch[i];
+  return s;
+}
+
+__device__ __forceinline__ void write_out(const AttendArgs& a, int64_t at, float4 v) {
+  if (a.type == 0) {
+    float* p = static_cast<float*>(a.dst) + at;
+    if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+      store4(p, v.x, v.y, v.z, v.w);
+    } else {
+      p[0] = v.x, p[1] = v.y, p[2] = v.z, p[3] = v.w;
+    }
+  } else {
+    __half* p = static_cast<__half*>(a.dst) + at;
+    if ((reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+      store4(p, v.x, v.y, v.z, v.w);
+    } else {
+      store1(p, v.x), store1(p + 1, v.y), store1(p + 2, v.z), store1(p + 3, v.w);
+    }
+  }
+}
+
+// Where elements d .. d + 3 of a warp's row r lie in its part: 16-byte places exchanged so that the eight
+// lanes that write at once, two rows' columns of four c4, meet eight different ones.
+template <int DC>
+__device__ __forceinline__ int part_at(int r, int d) {
+  const int q = d >> 2;
+  return r * DC + ((q ^ (((q >> (DC == 64 ? 2 : 3)) & 3) * 2 + (r & 1))) << 2);
+}
+
+// Token and query head of row r of an item; false where it has none.
+__device__ __forceinline__ bool row_of(const AttendArgs& a, int t0, int n, int hs, int r, int& t, int& head) {
+  const int i = r / a.rows, h = r - i * a.rows, sub = hs % a.subs;
+  t = t0 + i;
+  const int in_group = sub * a.rows + h;
+  head = hs / a.subs * a.group + in_group;
+  return i < n && in_group < a.group;
+}
+
+// ------------------------------------------------------------------ the kernel
+template <int DC, int FMT, int NM>
+__global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kernel(const __grid_constant__ AttendArgs a) {
+  using S = AttShape<DC, NM>;
+  constexpr int CT = S::kTokens, W = S::kWarps, KS = S::kSteps, NT = CT / 8, KG = CT / 16;
+  constexpr int UC = DC == 256 ? 2 : 1;       // 16-byte (DC 64: 8-byte) units of a value row a lane holds
+  constexpr int UB = DC == 64 ? 8 : 16;       // bytes of a unit of values
+  constexpr int NO = DC / 8;                  // column tiles of the output
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int64_t scan[32];
+  __shared__ Item found;
+  __shared__ float row_scale[S::kRows];       // of the products: the query's power of two, scale and log2(e)
+  __shared__ int row_lo[S::kRows], row_hi[S::kRows];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c4 = lane & 3;
+  const int HS = a.c.heads * a.subs;
+  const int D = a.c.dim, U16 = D / 16;
+
+  // ---- this CTA's stretch of chunks
+  int64_t mine = 0;
+  for (int t = threadIdx.x; t < a.T; t += blockDim.x) {
+    Item it;
+    if (item_at<CT>(a, t, it)) mine += it.chunks;
+  }
+  const int64_t total = block_sum(mine, scan) * HS;
+  // a CTA takes one chunk a warp at least, so that short rows are not cut for nothing
+  int64_t ctas = (total + W - 1) / W;
+  if (ctas > a.ctas) ctas = a.ctas;
+  if (blockIdx.x >= ctas) return;
+  const int64_t start = share(total, blockIdx.x, ctas), stop = share(total, blockIdx.x + 1, ctas);
+  // the item that holds `start`
+  int64_t before = 0;
+  for (int base = 0; base < a.T; base += blockDim.x) {
+    const int t = base + threadIdx.x;
+    Item it;
+    const bool has = t < a.T && item_at<CT>(a, t, it);
+    const int64_t n = has ? it.chunks : 0;
+    int64_t incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    __syncthreads();
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int64_t ahead = before, all = before;
+    for (int i = 0; i < W; ++i) {
+      if (i < warp) ahead += scan[i];
+      all += scan[i];
+    }
+    const int64_t b = (ahead + incl - n) * HS;
+    if (n > 0 && start >= b && start < b + n * HS) {
+      it.hs = static_cast<int>((start - b) / n);
+      it.begin = b + it.hs * n;
+      found = it;
+    }
+    before = all;
+    if (before * HS > start) break;
+  }
+  __syncthreads();
+  Item item = found;
+  if (threadIdx.x == 0) {
+    if (blockIdx.x == 0) {
+      AttHeader h = {total, ctas};
+      *reinterpret_cast<AttHeader*>(a.workspace) = h;
+    }
+    AttFirst f = {item.begin, item.begin + item.chunks, item.t0, item.n, item.hs, 0};
+    reinterpret_cast<AttFirst*>(reinterpret_cast<uint8_t*>(a.workspace) + kAttHead)[blockIdx.x] = f;
+  }
+  float* parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.workspace) + att_parts_at(a.ctas)) +
+                 static_cast<int64_t>(blockIdx.x) * 2 * S::kRows * S::kRowFloats;
+
+  uint8_t* ring = smem + S::kQBytes + warp * (S::kStages * S::kStage);
+  const uint32_t ring_at = smem_u32(ring);
+  // Copies of one chunk of an item into a stage.  Tokens outside [lo, hi) or without a page: zeros under the
+  // scale kHidden.
+  auto fetch = [&](const Item& it, int64_t idx, int stage) {
+    const int p0 = (it.lo / CT + static_cast<int>(idx - it.begin)) * CT, head = it.hs / a.subs;
+    const uint32_t to = ring_at + stage * S::kStage;
+    int64_t page[KG];
+#pragma unroll
+    for (int h = 0; h < KG; ++h) page[h] = it.hi > 0 ? cache_page(a.c, it.seq, p0 + 16 * h) : -1;
+    const int slot = p0 & ((1 << a.c.page_log2) - 1);
+#pragma unroll
+    for (int h = 0; h < KG; ++h) {
+      const int s = (slot + 16 * h) & ((1 << a.c.page_log2) - 1);
+      const int64_t at = page[h] >= 0 ? cache_row(a.c, page[h], head, s) : 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = 8 * i + g, p = p0 + 16 * h + row;
+        const bool on = page[h] >= 0 && p >= it.lo && p < it.hi;
+#pragma unroll
+        for (int u = 0; u < DC / 64; ++u)
+          if (DC == D || c4 + 4 * u < U16)
+            cp_async16(to + (((2 * h + i) * (DC / 64) + u) * 32 + lane) * 16,
+                       a.c.k + at + static_cast<int64_t>(on ? row : 0) * D + (c4 + 4 * u) * 16, on);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 2 * c4 + (i & 1) + 8 * (i >> 1), p = p0 + 16 * h + row;
+        const bool on = page[h] >= 0 && p >= it.lo && p < it.hi;
+#pragma unroll
+        for (int u = 0; u < UC; ++u)
+          if (DC == D || (g + 8 * u) * UB < D) {
+            const uint32_t dst = to + CT * DC + (((4 * h + i) * UC + u) * 32 + lane) * UB;
+            const uint8_t* src = a.c.v + at + static_cast<int64_t>(on ? row : 0) * D + (g + 8 * u) * UB;
+            if constexpr (UB == 16)
+              cp_async16(dst, src, on);
+            else
+              cp_async8(dst, src, on);
+          }
+      }
+    }
+    {
+      const int j = lane & (CT - 1), h = j / 16, p = p0 + j;
+      const bool is_v = CT == 16 && lane >= 16;
+      const int64_t pg = KG == 2 && h == 1 ? page[KG - 1] : page[0];
+      const bool on = pg >= 0 && p >= it.lo && p < it.hi;
+      const int64_t at = on ? cache_scale(a.c, pg, head, (slot + j) & ((1 << a.c.page_log2) - 1)) : 0;
+      float* scales = reinterpret_cast<float*>(ring + stage * S::kStage + S::kScaleAt);
+      const uint32_t dst = to + S::kScaleAt + 4 * lane;
+      if (!on) {
+        scales[lane] = is_v ? 0.0f : kHidden;
+        if (CT == 32) scales[CT + lane] = 0.0f;
+      } else if (CT == 32) {
+        cp_async4(dst, a.c.k_scale + at);
+        cp_async4(dst + 4 * CT, a.c.v_scale + at);
+      } else {
+        cp_async4(dst, (is_v ? a.c.v_scale : a.c.k_scale) + at);
+      }
+    }
+  };
+
+  int stage = 0;
+  int64_t first = start;  // of the item's chunks that this CTA takes
+  if (start + warp < min(stop, item.begin + item.chunks)) fetch(item, start + warp, 0);
+  cp_commit();
+
+  for (;;) {
+    const int64_t end = min(stop, item.begin + item.chunks);
+    // ---- the item's queries: hi and lo parts in the order of the instructions' rows
+    __syncthreads();
+    for (int r = warp; r < S::kRows; r += W) {
+      int t, head;
+      const bool live = row_of(a, item.t0, item.n, item.hs, r, t, head);
+      constexpr int E = DC == 256 ? 8 : 4;
+      float v[E];
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int d = (e / 4) * 128 + lane * 4 + e % 4;
+        v[e] = 0.0f;
+        if (live && d < D) {
+          const int64_t at = t * a.ldq + static_cast<int64_t>(head) * D + d;
+          v[e] = a.type == 0 ? static_cast<const float*>(a.q)[at] : __half2float(static_cast<const __half*>(a.q)[at]);
+        }
+        top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      // |q| 2^-x lies in [2^14, 2^15) for the largest
+      int x = static_cast<int>(top >> 23) - 127 - 14;
+      x = x < -110 ? -110 : x;
+      const bool number = top < 0x7f800000u;
+      const float f = __uint_as_float(static_cast<uint32_t>(127 - x) << 23);
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const int d = (e / 4) * 128 + lane * 4;
+        if (d >= DC) continue;
+        uint4 w;
+        split2(number ? v[e] * f : 0.0f, number ? v[e + 1] * f : 0.0f, w.x, w.y);
+        split2(number ? v[e + 2] * f : 0.0f, number ? v[e + 3] * f : 0.0f, w.z, w.w);
+        const int step = d / 64 * 4 + d % 16 / 4, lane_of = (r % 8) * 4 + d % 64 / 16;
+        *reinterpret_cast<uint4*>(smem + (((r / 8) * KS + step) * 32 + lane_of) * 16) = w;
+      }
+      if (lane == 0) {
+        row_scale[r] = number ? a.scale * __uint_as_float(static_cast<uint32_t>(127 + x) << 23) : __uint_as_float(0x7fffffffu);
+        int s, lo = 0, hi = 0;
+        if (live) keys_of(a, t, s, lo, hi);
+        row_lo[r] = lo;
+        row_hi[r] = hi;
+      }
+    }
+    __syncthreads();
+
+    float o[NM][NO][2], m[NM], l[NM], f[NM];
+    int lo[NM], hi[NM];
+#pragma unroll
+    for (int i = 0; i < NM; ++i) {
+      m[i] = kNoMax;
+      l[i] = 0.0f;
+      f[i] = row_scale[8 * i + g];
+      lo[i] = row_lo[8 * i + g];
+      hi[i] = row_hi[8 * i + g];
+#pragma unroll
+      for (int n = 0; n < NO; ++n) o[i][n][0] = o[i][n][1] = 0.0f;
+    }
+    // biased exponent of the power of two, above every scale so far, that the values' scales are taken by; at
+    // least that of the format's smallest scale
+    uint32_t vexp = 127 - 111;
+
+    for (int64_t idx = first + warp; idx < end; idx += W) {
+      if (idx + W < end) fetch(item, idx + W, stage ^ 1);
+      cp_commit();
+      cp_wait<1>();
+      __syncwarp();
+      const uint8_t* st = ring + stage * S::kStage;
+      const float* ks = reinterpret_cast<const float*>(st + S::kScaleAt);
+      const float* vs = ks + CT;
+      const int p0 = (item.lo / CT + static_cast<int>(idx - item.begin)) * CT;
+
+      // ---- scores
+      float s[NM][NT][4];
+#pragma unroll
+      for (int i = 0; i < NM; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[i][n][0] = s[i][n][1] = s[i][n][2] = s[i][n][3] = 0.0f;
+#pragma unroll
+      for (int u = 0; u < DC / 64; ++u) {
+        uint4 q[NM][4];
+#pragma unroll
+        for (int i = 0; i < NM; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            q[i][j] = *reinterpret_cast<const uint4*>(smem + ((i * KS + u * 4 + j) * 32 + lane) * 16);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          uint4 w = make_uint4(0, 0, 0, 0);  // a unit that the head does not have
+          if (DC == D || c4 + 4 * u < U16)
+            w = *reinterpret_cast<const uint4*>(st + ((n * (DC / 64) + u) * 32 + lane) * 16);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t b0, b1;
+            pairs_of<FMT>(ww[j], b0, b1);
+#pragma unroll
+            for (int i = 0; i < NM; ++i) mma(s[i][n], q[i][j], b0, b1);
+          }
+        }
+      }
+
+      // ---- softmax; the weights, times the values' scales, as instructions' rows
+      const bool hidden = __any_sync(0xffffffffu, ks[lane & (CT - 1)] < 0.0f);
+      const uint32_t vtop = __reduce_max_sync(0xffffffffu, min(__float_as_uint(vs[lane & (CT - 1)]), 0x7e000000u));
+      const uint32_t vnow = max(vexp, (vtop >> 23) + 1);
+      // 2^(kWeightBits - (vnow - 127)): weights times it lie below 2^8
+      const float vinv = __uint_as_float((254 + kWeightBits - vnow) << 23);
+      const float vstep = vexp == vnow ? 1.0f : exp2f(static_cast<float>(static_cast<int>(vexp) - static_cast<int>(vnow)));
+      vexp = vnow;
+      uint4 pf[NM][KG];
+      float alpha[NM];
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {
+        float x[NT][2], top = kNoMax;
+        const bool whole = !hidden && p0 >= lo[i] && p0 + CT <= hi[i];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float2 k2 = *reinterpret_cast<const float2*>(ks + 8 * n + 2 * c4);
+          x[n][0] = (s[i][n][0] + s[i][n][2]) * (k2.x * f[i]);
+          x[n][1] = (s[i][n][1] + s[i][n][3]) * (k2.y * f[i]);
+          if (!whole) {
+            const int p = p0 + 8 * n + 2 * c4;
+            if (k2.x < 0.0f || p < lo[i] || p >= hi[i]) x[n][0] = -INFINITY;
+            if (k2.y < 0.0f || p + 1 < lo[i] || p + 1 >= hi[i]) x[n][1] = -INFINITY;
+          }
+          top = fmaxf(top, fmaxf(x[n][0], x[n][1]));
+        }
+        top = fmaxf(m[i], quad_max(top));
+        alpha[i] = exp2f(m[i] - top);
+        m[i] = top;
+        float sum = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float2 v2 = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c4);
+          const float p = exp2f(x[n][0] - top), q = exp2f(x[n][1] - top);
+          sum += p + q;
+          // a masked token's weight is zero whatever lies in its scale
+          float y = p * (v2.x * vinv), z = q * (v2.y * vinv);
+          if (x[n][0] == -INFINITY) y = 0.0f;
+          if (x[n][1] == -INFINITY) z = 0.0f;
+          uint32_t h, w;
+          split2(y, z, h, w);
+          if (n % 2 == 0) {
+            pf[i][n / 2].x = h;
+            pf[i][n / 2].y = w;
+          } else {
+            pf[i][n / 2].z = h;
+            pf[i][n / 2].w = w;
+          }
+        }
+        l[i] = l[i] * alpha[i] + sum;
+        alpha[i] *= vstep;
+      }
+
+      // ---- values
+#pragma unroll
+      for (int u = 0; u < UC; ++u) {
+        uint32_t raw[KG][4][UB / 4];
+#pragma unroll
+        for (int k = 0; k < KG; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint8_t* at = st + CT * DC + (((4 * k + i) * UC + u) * 32 + lane) * UB;
+            if constexpr (UB == 16) {
+              const uint4 w = *reinterpret_cast<const uint4*>(at);
+              raw[k][i][0] = w.x, raw[k][i][1] = w.y, raw[k][i][2] = w.z, raw[k][i][3] = w.w;
+            } else {
+              const uint2 w = *reinterpret_cast<const uint2*>(at);
+              raw[k][i][0] = w.x, raw[k][i][1] = w.y;
+            }
+          }
+#pragma unroll
+        for (int w = 0; w < UB / 4; ++w) {
+          float acc[NM][4][4];
+#pragma unroll
+          for (int i = 0; i < NM; ++i)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) acc[i][d][0] = acc[i][d][1] = acc[i][d][2] = acc[i][d][3] = 0.0f;
+#pragma unroll
+          for (int k = 0; k < KG; ++k) {
+            uint32_t b0[4], b1[4];
+            pairs_of<FMT>(__byte_perm(raw[k][0][w], raw[k][1][w], 0x5140), b0[0], b0[1]);
+            pairs_of<FMT>(__byte_perm(raw[k][0][w], raw[k][1][w], 0x7362), b0[2], b0[3]);
+            pairs_of<FMT>(__byte_perm(raw[k][2][w], raw[k][3][w], 0x5140), b1[0], b1[1]);
+            pairs_of<FMT>(__byte_perm(raw[k][2][w], raw[k][3][w], 0x7362), b1[2], b1[3]);
+#pragma unroll
+            for (int i = 0; i < NM; ++i)
+#pragma unroll
+              for (int d = 0; d < 4; ++d) mma(acc[i][d], pf[i][k], b0[d], b1[d]);
+          }
+#pragma unroll
+          for (int i = 0; i < NM; ++i)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+              float* at = o[i][(u * UB / 4 + w) * 4 + d];
+              at[0] = fmaf(at[0], alpha[i], acc[i][d][0] + acc[i][d][2]);
+              at[1] = fmaf(at[1], alpha[i], acc[i][d][1] + acc[i][d][3]);
+            }
+        }
+      }
+      stage ^= 1;
+      __syncwarp();
+    }
+
+    // ---- the next item's first chunk starts on its way
+    cp_wait<0>();
+    const bool last = end == stop;
+    Item next = item;
+    if (!last) {
+      next.begin = item.begin + item.chunks;
+      if (item.hs + 1 < HS) {
+        ++next.hs;
+      } else {
+        next.hs = 0;
+        int t = item.t0 + item.n;
+        while (!item_at<CT>(a, t, next) && t < a.T - 1) ++t;  // (the token behind an item begins one)
+        next.begin = item.begin + item.chunks;
+      }
+      const int64_t to = min(stop, next.begin + next.chunks);
+      if (next.begin + warp < to) fetch(next, next.begin + warp, stage);
+    }
+    cp_commit();
+
+    // ---- the warps' parts together: each in the stage that it has used up
+    {
+      float* part = reinterpret_cast<float*>(ring + (stage ^ 1) * S::kStage);
+      const float back = __uint_as_float((vexp - kWeightBits) << 23);
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {
+#pragma unroll
+        for (int u = 0; u < UC; ++u)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int n = 0; n < UB; n += 4) {
+              const int d = (2 * c4 + e + 8 * u) * UB + n;
+              *reinterpret_cast<float4*>(part + part_at<DC>(8 * i + g, d)) =
+                  make_float4(o[i][u * UB + n][e] * back, o[i][u * UB + n + 1][e] * back, o[i][u * UB + n + 2][e] * back,
+                              o[i][u * UB + n + 3][e] * back);
+            }
+        const float z = quad_sum(l[i]);
+        if (c4 == 0) {
+          part[S::kRows * DC + 8 * i + g] = m[i];
+          part[S::kRows * DC + S::kRows + 8 * i + g] = z;
+        }
+      }
+    }
+    __shared__ int used[W];
+    if (lane == 0) used[warp] = static_cast<int>(ring - smem) + (stage ^ 1) * S::kStage;
+    __syncthreads();
+    const bool split = first > item.begin || end < item.begin + item.chunks;
+    float* out = parts + (first == start ? 0 : S::kRows * S::kRowFloats);
+    for (int i = threadIdx.x; i < S::kRows * DC / 4; i += blockDim.x) {
+      const int r = i / (DC / 4), d = i % (DC / 4) * 4;
+      float top = kNoMax;
+#pragma unroll
+      for (int w = 0; w < W; ++w) top = fmaxf(top, reinterpret_cast<const float*>(smem + used[w])[S::kRows * DC + r]);
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float z = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float* p = reinterpret_cast<const float*>(smem + used[w]);
+        const float e = exp2f(p[S::kRows * DC + r] - top);
+        const float4 x = *reinterpret_cast<const float4*>(p + part_at<DC>(r, d));
+        v.x = fmaf(x.x, e, v.x), v.y = fmaf(x.y, e, v.y), v.z = fmaf(x.z, e, v.z), v.w = fmaf(x.w, e, v.w);
+        z = fmaf(p[S::kRows * DC + S::kRows + r], e, z);
+      }
+      if (split) {
+        *reinterpret_cast<float4*>(out + r * DC + d) = v;
+        if (d == 0) {
+          out[S::kRows * DC + r] = top;
+          out[S::kRows * DC + S::kRows + r] = z;
+        }
+        continue;
+      }
+      int t, head;
+      if (d >= D || !row_of(a, item.t0, item.n, item.hs, r, t, head)) continue;
+      const float inv = z == 0.0f ? 0.0f : 1.0f / z;  // no keys: zeros
+      write_out(a, t * a.ld_dst + static_cast<int64_t>(head) * D + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+      if (d == 0 && a.lse)
+        a.lse[static_cast<int64_t>(t) * a.q_heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * 0.693147181f;
+    }
+    if (last) break;
+    item = next;
+    first = item.begin;
+  }
+}
+
+// Joins the parts of the items that reach over CTAs: CTA (i, y) takes the item that CTA i's stretch begins
+// within, if it is the first to do so, rows y, y + gridDim.y, ..
+template <int DC, int NM>
+__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendArgs a) {
+  using S = AttShape<DC, NM>;
+  pdl_wait();
+  pdl_trigger();
+  const AttHeader h = *reinterpret_cast<const AttHeader*>(a.workspace);
+  const int64_t i = static_cast<int64_t>(blockIdx.x) + 1;
+  if (i >= h.ctas) return;
+  const AttFirst f = reinterpret_cast<const AttFirst*>(reinterpret_cast<const uint8_t*>(a.workspace) + kAttHead)[i];
+  const int64_t prev = share(h.chunks, i - 1, h.ctas);
+  if (share(h.chunks, i, h.ctas) == f.begin || prev > f.begin) return;
+  int n = 1;  // parts
+  while (i - 1 + n < h.ctas && share(h.chunks, i - 1 + n, h.ctas) < f.end) ++n;
+  constexpr int64_t kPart = S::kRows * S::kRowFloats;
+  const float* parts = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.workspace) + att_parts_at(a.ctas));
+  // CTA i - 1 holds its part second, unless its stretch begins with the item
+  const float* head_part = parts + ((i - 1) * 2 + (prev < f.begin ? 1 : 0)) * kPart;
+  const float* rest = parts + i * 2 * kPart;
+  for (int k = threadIdx.x + blockIdx.y * blockDim.x; k < S::kRows * DC / 4; k += blockDim.x * gridDim.y) {
+    const int r = k / (DC / 4), d = k % (DC / 4) * 4;
+    int t, head;
+    if (d >= a.c.dim || !row_of(a, f.t0, f.n, f.hs, r, t, head)) continue;
+    float top = kNoMax;
+    for (int j = 0; j < n; ++j) top = fmaxf(top, (j == 0 ? head_part : rest + (j - 1) * 2 * kPart)[S::kRows * DC + r]);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float z = 0.0f;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const float* p = j == 0 ? head_part : rest + (j - 1) * 2 * kPart;
+      const float e = exp2f(p[S::kRows * DC + r] - top);
+      const float4 x = *reinterpret_cast<const float4*>(p + r * DC + d);
+      v.x = fmaf(x.x, e, v.x), v.y = fmaf(x.y, e, v.y), v.z = fmaf(x.z, e, v.z), v.w = fmaf(x.w, e, v.w);
+      z = fmaf(p[S::kRows * DC + S::kRows + r], e, z);
+    }
+    const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+    write_out(a, t * a.ld_dst + static_cast<int64_t>(head) * a.c.dim + d,
+              make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+    if (d == 0 && a.lse)
+      a.lse[static_cast<int64_t>(t) * a.q_heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * 0.693147181f;
+  }
+}
+
+// ------------------------------------------------------------------ host
+int64_t attend_workspace_bytes(int dim, int tiles, int ctas) {
+  const int dc = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
+  return att_parts_at(ctas) + static_cast<int64_t>(ctas) * 2 * 8 * tiles * (dc + 2) * 4;
+}
+
+// Two CTAs an SM: one decodes while the other fetches queries or joins its warps.
+int attend_ctas(int, int, int sms) { return 2 * sms; }
+
+template <int DC, int FMT, int NM>
+static int launch_attend_t(const AttendArgs& a, cudaStream_t st, bool pdl) {
+  using S = AttShape<DC, NM>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  if (a.phase == ATT_JOIN) {
+    cfg.gridDim = dim3(static_cast<unsigned>(a.ctas - 1), 2);
+    cfg.blockDim = dim3(128);
+    return cudaLaunchKernelEx(&cfg, attend_join_kernel<DC, NM>, a);
+  }
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(attend_kernel<DC, FMT, NM>));
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
+  cfg.blockDim = dim3(32 * S::kWarps);
+  cfg.dynamicSmemBytes = S::kSmem;
+  return cudaLaunchKernelEx(&cfg, attend_kernel<DC, FMT, NM>, a);
+}
+
+template <int DC, int NM>
+static int launch_attend_f(const AttendArgs& a, cudaStream_t st, bool pdl) {
+  return a.c.format == 0 ? launch_attend_t<DC, 0, NM>(a, st, pdl) : launch_attend_t<DC, 1, NM>(a, st, pdl);
+}
+
+int launch_attend(const AttendArgs& a, cudaStream_t st, bool pdl) {
+  if (a.c.dim <= 64) return a.tiles == 1 ? launch_attend_f<64, 1>(a, st, pdl) : launch_attend_f<64, 2>(a, st, pdl);
+  if (a.c.dim <= 128) return a.tiles == 1 ? launch_attend_f<128, 1>(a, st, pdl) : launch_attend_f<128, 2>(a, st, pdl);
+  return launch_attend_f<256, 1>(a, st, pdl);
+}
+
+}  // namespace gf

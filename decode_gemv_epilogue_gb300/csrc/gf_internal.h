@@ -317,11 +317,96 @@ int launch_lin(const LinArgs& a, cudaStream_t st, bool pdl);
 // Columns of a group.
 int lin_cols(int wtype, int64_t M, int64_t K, int row_bytes, int ncols, int sms);
 
+// ------------------------------------------------------------------ attention over an 8-bit cache
+// Rotary positions (rope.cu).
+struct RopeTableArgs {
+  void* table;
+  const float* divisors;
+  double base, factor, span, fast, slow;
+  float magnitude;
+  int pairs, kind;
+};
+int launch_rope_table(const RopeTableArgs& a, cudaStream_t st);
+struct RopeArgs {
+  const void* x;
+  void* dst;
+  const int32_t* pos;
+  const void* table;
+  int64_t T, ld, ld_dst;
+  int heads, dim, n_rot, halves;
+  int type;             // GF_F32 or GF_F16
+  int vec;              // units of eight elements, 16-byte (F16: 8-byte) aligned
+};
+int launch_rope(const RopeArgs& a, cudaStream_t st, bool pdl);
+
+// The cache (cache.cu).
+constexpr int kCacheMaxBlock = 64;
+constexpr int kCacheMaxDim = 256;
+struct CacheArgs {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* table;
+  int64_t n_pages, table_ld;
+  int n_seqs, heads, dim, page_log2, block_log2, format;
+};
+struct StoreArgs {
+  CacheArgs c;
+  const void* k;
+  const void* v;
+  const int32_t* seq;   // nullptr: token t is of sequence t
+  const int32_t* pos;
+  const void* table;    // rotation (nullptr: none)
+  const void* q;
+  void* q_dst;
+  int64_t T, ldk, ldv, ldq, ld_q_dst;
+  int n_rot, halves, q_heads, type, vec;
+  int wpu;              // warps that share a block of a head
+};
+int launch_store(const StoreArgs& a, int sms, cudaStream_t st, bool pdl);
+struct LoadArgs {
+  CacheArgs c;
+  const int32_t* seq;
+  const int32_t* pos;
+  void* k;              // nullptr: not read back
+  void* v;
+  int64_t T, ldk, ldv;
+  int type, vec;
+};
+int launch_load(const LoadArgs& a, cudaStream_t st, bool pdl);
+
+// Attention (attend.cu): one launch of one phase.
+enum { ATT_PART = 0, ATT_JOIN = 1 };
+constexpr int kAttMaxTokens = 1 << 16;  // tokens of a call
+struct AttendArgs {
+  CacheArgs c;
+  const void* q;
+  void* dst;
+  const int32_t* seq;
+  const int32_t* pos;
+  float* lse;           // [T][q_heads] or nullptr
+  float* workspace;
+  int64_t ldq, ld_dst;
+  float scale;          // of q . k, times log2(e)
+  int phase;
+  int T, q_heads, group;
+  int window;           // keys back from a token's own (0: all)
+  int type;
+  int tiles;            // of 8 rows an item has (1 or 2)
+  int subs, rows;       // parts that the heads of a group fall into, heads of a part
+  int run, tokens;      // tokens of a sequence expected next to each other; most tokens of an item
+  int ctas;
+};
+int64_t attend_workspace_bytes(int dim, int tiles, int ctas);
+int attend_ctas(int dim, int tiles, int sms);
+int launch_attend(const AttendArgs& a, cudaStream_t st, bool pdl);
+
 // One kernel launch with every argument resolved: what a call plans, and what a
 // prepared call keeps (gf_prepare) so that launching it does no planning at all.
 enum {
   REC_FWHT = 0, REC_TC = 1, REC_STREAM = 2, REC_GENERIC = 3, REC_COPY = 4, REC_ROUTE = 5, REC_EXPERTS = 6,
-  REC_LORA = 7, REC_EW = 8, REC_LIN = 9
+  REC_LORA = 7, REC_EW = 8, REC_LIN = 9, REC_ROPE = 10, REC_STORE = 11, REC_LOAD = 12, REC_ATTEND = 13
 };
 struct LaunchRec {
   int kind;
@@ -353,13 +438,17 @@ struct LaunchRec {
     ExpertsArgs experts;
     LoraArgs lora;
     LinArgs lin;
+    RopeArgs rope;
+    StoreArgs store;
+    LoadArgs load;
+    AttendArgs attend;
   };
 };
 // (a direct call plans into kMaxRecs of them on its stack)
 static_assert(sizeof(LaunchRec) <= sizeof(Plan) + 16, "the streamed kernel's plan is the largest");
 constexpr int kMaxRecs = 1 + kMaxSeg * (kMaxBatch / kMaxCols);  // transform + column blocks (per matrix)
 
-// Shared by the entry points (api.cu, api_select.cu).
+// Shared by the entry points (api.cu, api_select.cu, api_attend.cu).
 int64_t row_bytes_of(int wtype, int64_t K);
 bool ranges_overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes);
 int cuda_fail(cudaError_t e);

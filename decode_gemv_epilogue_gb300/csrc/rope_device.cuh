@@ -1,0 +1,72 @@
+// Rotary positions: the angle of a pair and the rotation of a head's row, shared by gf_rope and the
+// cache store.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_fp16.h>
+
+#include "gf_internal.h"
+
+namespace gf {
+
+// The table of gf_rope_table: a header, then one word a pair.
+struct RopeHeader {
+  float magnitude;  // of cosine and sine
+  uint32_t pairs;
+  uint32_t unused[2];
+};
+
+// Cosine and sine of position `pos` for a pair that makes turns * 2^-64 turns a position.  The
+// product modulo one turn is exact in 64-bit integers: far positions lose nothing.
+__device__ __forceinline__ float2 rope_cs(uint64_t turns, int pos, float magnitude) {
+  const uint64_t a = turns * static_cast<uint64_t>(static_cast<int64_t>(pos));
+  float s, c;
+  sincospif(static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077393e-10f, &s, &c);  // half turns
+  return make_float2(c * magnitude, s * magnitude);
+}
+
+__device__ __forceinline__ const uint64_t* rope_turns(const void* table) {
+  return reinterpret_cast<const uint64_t*>(static_cast<const uint8_t*>(table) + sizeof(RopeHeader));
+}
+
+__device__ __forceinline__ void rope_turn(float& a, float& b, float2 cs) {
+  const float u = fmaf(a, cs.x, -(b * cs.y)), v = fmaf(a, cs.y, b * cs.x);
+  a = u;
+  b = v;
+}
+
+// Eight elements of a row: unit u (four adjacent pairs) of a head whose first n_rot elements turn.
+// They lie at o0 .. o0 + 3 and o1 .. o1 + 3; pair i is (v[i], v[4 + i]) in halves, else (v[2i],
+// v[2i + 1]).
+__device__ __forceinline__ void unit_offsets(int u, int n_rot, bool halves, int& o0, int& o1) {
+  if (halves && 8 * u < n_rot) {
+    o0 = 4 * u;
+    o1 = n_rot / 2 + 4 * u;
+  } else {
+    o0 = 8 * u;
+    o1 = 8 * u + 4;
+  }
+}
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __half* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void store4(__half* p, float a, float b, float c, float d) {
+  const __half2 x = __floats2half2_rn(a, b), y = __floats2half2_rn(c, d);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+}
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const __half* p) { return __half2float(*p); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(__half* p, float v) { *p = __float2half_rn(v); }
+
+}  // namespace gf

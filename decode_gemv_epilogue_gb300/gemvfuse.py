@@ -571,3 +571,185 @@ def plan_lora(W, wtype, x, M, K, epilogue, aux, dst, A, B, atype, n, rank, ids, 
     path = _plan_lora(_ptr(W), wtype, _ptr(x), M, K, epilogue, _ptr(aux), _ptr(dst), ctypes.byref(lo), ctypes.byref(o),
                       ctypes.byref(info))
     return path, dict(cols=info[0], wide=bool(info[1])) if path == 4 else dict(zip(_PLAN_KEYS, list(info)))
+
+
+# ---- attention over an 8-bit cache
+
+ROPE_HALVES, ROPE_PAIRS = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_RAMP, ROPE_BANDS = 0, 1, 2, 3
+CACHE_I8, CACHE_E4M3 = 0, 1
+
+
+class RopeFreqs(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_double), ("kind", _i32), ("factor", ctypes.c_double), ("span", _i64),
+                ("fast", ctypes.c_double), ("slow", ctypes.c_double), ("magnitude", ctypes.c_double), ("divisors", _vp)]
+
+
+class RopeOpts(ctypes.Structure):
+    _fields_ = [("table", _vp), ("n_rot", _i64), ("layout", _i32), ("type", _i32), ("ld", _i64), ("ld_dst", _i64),
+                ("flags", _u32)]
+
+
+class GfCache(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("format", _i32), ("n_pages", _i64),
+                ("heads", _i64), ("page", _i64), ("dim", _i64), ("block", _i64), ("table", _vp), ("n_seqs", _i64),
+                ("table_ld", _i64)]
+
+
+class StoreOpts(ctypes.Structure):
+    _fields_ = [("type", _i32), ("ldk", _i64), ("ldv", _i64), ("rope", ctypes.POINTER(RopeOpts)), ("q", _vp),
+                ("q_dst", _vp), ("q_heads", _i64), ("ldq", _i64), ("ld_q_dst", _i64), ("flags", _u32)]
+
+
+class LoadOpts(ctypes.Structure):
+    _fields_ = [("type", _i32), ("ldk", _i64), ("ldv", _i64), ("flags", _u32)]
+
+
+class AttendOpts(ctypes.Structure):
+    _fields_ = [("type", _i32), ("ldq", _i64), ("ld_dst", _i64), ("scale", ctypes.c_float), ("window", _i64),
+                ("run", _i64), ("lse", _vp), ("workspace", _vp), ("workspace_bytes", _i64), ("flags", _u32)]
+
+
+_cachep, _out = ctypes.POINTER(GfCache), ctypes.POINTER(_vp)
+_rope_table_bytes = _sig("gf_rope_table_bytes", [_i64], _i64)
+_rope_table = _sig("gf_rope_table", [_vp, _i64, ctypes.POINTER(RopeFreqs), _vp])
+_rope = _sig("gf_rope", [_vp, _i64, _i64, _i64, _vp, ctypes.POINTER(RopeOpts), _vp, _vp])
+_prepare_rope = _sig("gf_prepare_rope", [_vp, _i64, _i64, _i64, _vp, ctypes.POINTER(RopeOpts), _vp, _out])
+_cache_store = _sig("gf_cache_store", [_cachep, _vp, _vp, _i64, _vp, _vp, ctypes.POINTER(StoreOpts), _vp])
+_prepare_cache_store = _sig("gf_prepare_cache_store", [_cachep, _vp, _vp, _i64, _vp, _vp, ctypes.POINTER(StoreOpts), _out])
+_cache_load = _sig("gf_cache_load", [_cachep, _i64, _vp, _vp, ctypes.POINTER(LoadOpts), _vp, _vp, _vp])
+_prepare_cache_load = _sig("gf_prepare_cache_load", [_cachep, _i64, _vp, _vp, ctypes.POINTER(LoadOpts), _vp, _vp, _out])
+_attend = _sig("gf_attend", [_cachep, _vp, _i64, _i64, _vp, _vp, ctypes.POINTER(AttendOpts), _vp, _vp])
+_prepare_attend = _sig("gf_prepare_attend", [_cachep, _vp, _i64, _i64, _vp, _vp, ctypes.POINTER(AttendOpts), _vp, _out])
+_attend_workspace = _sig("gf_attend_workspace", [_i64] * 5, _i64)
+
+
+def rope_table_bytes(n_rot):
+    """Bytes of the table that rope_table fills for n_rot rotated elements of a head."""
+    n = _rope_table_bytes(n_rot)
+    if n < 0:
+        raise GemvFuseError(n, "gf_rope_table_bytes")
+    return n
+
+
+def rope_table(table, n_rot, base=10000.0, kind=ROPE_PLAIN, factor=1.0, span=0, fast=32.0, slow=1.0, magnitude=0.0,
+               divisors=None, stream=None, check=True):
+    """gf_rope_table: the frequencies of rotary positions, made once (see include/gemvfuse.h)."""
+    f = RopeFreqs(base, kind, factor, span, fast, slow, magnitude, _ptr(divisors))
+    st = _rope_table(_ptr(table), n_rot, ctypes.byref(f), _stream(stream))
+    if check:
+        _check(st, "gf_rope_table")
+    return st
+
+
+def rope(x, T, heads, dim, pos, table, dst, n_rot=0, layout=ROPE_HALVES, type=F32, ld=0, ld_dst=0, pdl=False, stream=None,
+         check=True):
+    """gf_rope: dst = x [T][heads][dim] rotated by the tokens' positions (see include/gemvfuse.h)."""
+    o = RopeOpts(_ptr(table), n_rot, layout, type, ld, ld_dst, FLAG_PDL if pdl else 0)
+    st = _rope(_ptr(x), T, heads, dim, _ptr(pos), ctypes.byref(o), _ptr(dst), _stream(stream))
+    if check:
+        _check(st, "gf_rope")
+    return st
+
+
+def prepare_rope(x, T, heads, dim, pos, table, dst, n_rot=0, layout=ROPE_HALVES, type=F32, ld=0, ld_dst=0, pdl=False,
+                 check=True):
+    """gf_prepare_rope: the call rope(...) would make, planned once (see Prepared)."""
+    o = RopeOpts(_ptr(table), n_rot, layout, type, ld, ld_dst, FLAG_PDL if pdl else 0)
+    h = _vp()
+    st = _prepare_rope(_ptr(x), T, heads, dim, _ptr(pos), ctypes.byref(o), _ptr(dst), ctypes.byref(h))
+    if check:
+        _check(st, "gf_prepare_rope")
+    return Prepared(h.value, (x, pos, table, dst)) if st == OK else st
+
+
+class Cache:
+    """The arrays of an 8-bit cache and their sizes (gf_cache, see include/gemvfuse.h); keeps them alive."""
+
+    def __init__(self, k, v, k_scale, v_scale, format, n_pages, heads, page, dim, block, table, n_seqs, table_ld):
+        self.keep = (k, v, k_scale, v_scale, table)
+        self.struct = GfCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), format, n_pages, heads, page, dim, block,
+                              _ptr(table), n_seqs, table_ld)
+
+
+def _store_opts(type, ldk, ldv, rope, n_rot, layout, q, q_heads, ldq, q_dst, ld_q_dst, pdl):
+    turn = None if rope is None else ctypes.pointer(RopeOpts(_ptr(rope), n_rot, layout, type, 0, 0, 0))
+    return StoreOpts(type, ldk, ldv, turn, _ptr(q), _ptr(q_dst), q_heads, ldq, ld_q_dst, FLAG_PDL if pdl else 0)
+
+
+def cache_store(cache, k, v, T, seq, pos, type=F32, ldk=0, ldv=0, rope=None, n_rot=0, layout=ROPE_HALVES, q=None, q_heads=0,
+                ldq=0, q_dst=None, ld_q_dst=0, pdl=False, stream=None, check=True):
+    """gf_cache_store: T tokens' keys and values quantised into the cache; with `rope` (a table) keys, and
+    queries q into q_dst, are rotated first (see include/gemvfuse.h)."""
+    o = _store_opts(type, ldk, ldv, rope, n_rot, layout, q, q_heads, ldq, q_dst, ld_q_dst, pdl)
+    st = _cache_store(ctypes.byref(cache.struct), _ptr(k), _ptr(v), T, _ptr(seq), _ptr(pos), ctypes.byref(o),
+                      _stream(stream))
+    if check:
+        _check(st, "gf_cache_store")
+    return st
+
+
+def prepare_cache_store(cache, k, v, T, seq, pos, type=F32, ldk=0, ldv=0, rope=None, n_rot=0, layout=ROPE_HALVES, q=None,
+                        q_heads=0, ldq=0, q_dst=None, ld_q_dst=0, pdl=False, check=True):
+    """gf_prepare_cache_store: the call cache_store(...) would make, planned once (see Prepared)."""
+    o = _store_opts(type, ldk, ldv, rope, n_rot, layout, q, q_heads, ldq, q_dst, ld_q_dst, pdl)
+    h = _vp()
+    st = _prepare_cache_store(ctypes.byref(cache.struct), _ptr(k), _ptr(v), T, _ptr(seq), _ptr(pos), ctypes.byref(o),
+                              ctypes.byref(h))
+    if check:
+        _check(st, "gf_prepare_cache_store")
+    return Prepared(h.value, (cache, k, v, seq, pos, rope, q, q_dst)) if st == OK else st
+
+
+def cache_load(cache, T, seq, pos, k, v, type=F32, ldk=0, ldv=0, pdl=False, stream=None, check=True):
+    """gf_cache_load: T tokens' keys and values read back into k, v (see include/gemvfuse.h)."""
+    o = LoadOpts(type, ldk, ldv, FLAG_PDL if pdl else 0)
+    st = _cache_load(ctypes.byref(cache.struct), T, _ptr(seq), _ptr(pos), ctypes.byref(o), _ptr(k), _ptr(v),
+                     _stream(stream))
+    if check:
+        _check(st, "gf_cache_load")
+    return st
+
+
+def prepare_cache_load(cache, T, seq, pos, k, v, type=F32, ldk=0, ldv=0, pdl=False, check=True):
+    """gf_prepare_cache_load: the call cache_load(...) would make, planned once (see Prepared)."""
+    o = LoadOpts(type, ldk, ldv, FLAG_PDL if pdl else 0)
+    h = _vp()
+    st = _prepare_cache_load(ctypes.byref(cache.struct), T, _ptr(seq), _ptr(pos), ctypes.byref(o), _ptr(k), _ptr(v),
+                             ctypes.byref(h))
+    if check:
+        _check(st, "gf_prepare_cache_load")
+    return Prepared(h.value, (cache, k, v, seq, pos)) if st == OK else st
+
+
+def attend_workspace(T, q_heads, heads, dim, run=1):
+    """Bytes of workspace attend needs for these sizes."""
+    n = _attend_workspace(T, q_heads, heads, dim, run)
+    if n < 0:
+        raise GemvFuseError(n, "gf_attend_workspace")
+    return n
+
+
+def attend(cache, q, T, q_heads, seq, pos, dst, workspace, type=F32, ldq=0, ld_dst=0, scale=0.0, window=0, run=1, lse=None,
+           workspace_bytes=None, pdl=False, stream=None, check=True):
+    """gf_attend: attention of T tokens' queries over the cache (see include/gemvfuse.h)."""
+    o = AttendOpts(type, ldq, ld_dst, scale, window, run, _ptr(lse), _ptr(workspace), _nbytes(workspace, workspace_bytes),
+                   FLAG_PDL if pdl else 0)
+    st = _attend(ctypes.byref(cache.struct), _ptr(q), T, q_heads, _ptr(seq), _ptr(pos), ctypes.byref(o), _ptr(dst),
+                 _stream(stream))
+    if check:
+        _check(st, "gf_attend")
+    return st
+
+
+def prepare_attend(cache, q, T, q_heads, seq, pos, dst, workspace, type=F32, ldq=0, ld_dst=0, scale=0.0, window=0, run=1,
+                   lse=None, workspace_bytes=None, pdl=False, check=True):
+    """gf_prepare_attend: the call attend(...) would make, planned once (see Prepared)."""
+    o = AttendOpts(type, ldq, ld_dst, scale, window, run, _ptr(lse), _ptr(workspace), _nbytes(workspace, workspace_bytes),
+                   FLAG_PDL if pdl else 0)
+    h = _vp()
+    st = _prepare_attend(ctypes.byref(cache.struct), _ptr(q), T, q_heads, _ptr(seq), _ptr(pos), ctypes.byref(o),
+                         _ptr(dst), ctypes.byref(h))
+    if check:
+        _check(st, "gf_prepare_attend")
+    return Prepared(h.value, (cache, q, seq, pos, dst, workspace, lse)) if st == OK else st

@@ -403,6 +403,154 @@ GF_API int gf_plan_lora(const void* W, int wtype, const float* x, int64_t M, int
 /* Bytes of workspace for these sizes (any format); negative: a gf_status. */
 GF_API int64_t gf_lora_workspace(int64_t ncols, int64_t M, int64_t K, int64_t rank, int64_t n);
 
+/* ---- Attention of a decode step over a cache held in 8 bits (no counterpart on the pages): what
+ * stands between a layer's q, k, v products and its output projection.  The conventions of this header
+ * hold; each call has a prepared form.  Vectors here are rows of heads, [T][heads][dim], float32 or
+ * binary16 (`type`: GF_F32, GF_F16), rows `ld` elements apart (0: dense).
+ *
+ * Tokens are named by two lists on the device, which may change between launches of a prepared call:
+ * token t of a call is position pos[t] of sequence seq[t] (seq == NULL: of sequence t). */
+
+/* Rotary positions.  A pair (a, b) of a head at position p becomes
+ *     m (a cos(p f) - b sin(p f)),  m (a sin(p f) + b cos(p f)),      pair i: f_i = base^(-2i / n_rot)
+ * HALVES: the pair is elements (i, i + n_rot/2) of the head; PAIRS: (2i, 2i + 1).  Elements from n_rot
+ * on stay.  Frequencies and m are held in a table that a program makes once (gf_rope_table):
+ *  PLAIN  : f_i.       LINEAR : f_i / factor.
+ *  RAMP   : (1 - r) f_i + r f_i / factor, r rising linearly in i from 0 at the pair that makes `fast`
+ *           turns over `span` positions, i = floor(x(fast)), to 1 at i = ceil(x(slow)), with x(turns) =
+ *           n_rot/2 * ln(span / (2 pi turns)) / ln(base); floor and ceil are held within 0..n_rot - 1.
+ *  BANDS  : (1 - r) f_i + r f_i / factor, r falling linearly in the turns span f_i / 2 pi, from 1 at
+ *           `slow` and fewer to 0 at `fast` and more.
+ *  divisors[i] (device float32 [n_rot/2] or NULL) divides f_i last.
+ *  m = magnitude, or where that is 0: 0.1 ln(factor) + 1 for RAMP with factor > 1, else 1.
+ * Frequencies are computed in 64 bits and held as 64-bit fractions of a turn, the product with a 32-bit
+ * position is exact: an angle is off by 2^-33 turns and by the frequency's own error, some 2^-49 of the
+ * angle.  A negative position turns back. */
+typedef enum { GF_ROPE_HALVES = 0, GF_ROPE_PAIRS = 1 } gf_rope_layout;
+typedef enum { GF_ROPE_PLAIN = 0, GF_ROPE_LINEAR = 1, GF_ROPE_RAMP = 2, GF_ROPE_BANDS = 3 } gf_rope_kind;
+typedef struct {
+  double base;             /* > 1                                                    */
+  int kind;                /* gf_rope_kind                                           */
+  double factor;           /* > 0; read unless PLAIN                                 */
+  int64_t span;            /* positions of the unscaled context (RAMP, BANDS)        */
+  double fast, slow;       /* turns over the span, fast > slow > 0 (RAMP, BANDS)     */
+  double magnitude;        /* of cosine and sine; 0: see above                       */
+  const float* divisors;
+} gf_rope_freqs;
+/* Bytes of a table, and its making (16-byte aligned, on the device): n_rot even, 2..1024. */
+GF_API int64_t gf_rope_table_bytes(int64_t n_rot);
+GF_API int gf_rope_table(void* table, int64_t n_rot, const gf_rope_freqs* freqs, void* stream);
+typedef struct {
+  const void* table;   /* made for n_rot                                             */
+  int64_t n_rot;       /* elements of a head that turn; 0: all                       */
+  int layout;          /* gf_rope_layout                                             */
+  int type;            /* of x and dst (gf_rope only)                                */
+  int64_t ld, ld_dst;  /* gf_rope only                                               */
+  uint32_t flags;      /* GF_FLAG_PDL (gf_rope only)                                 */
+} gf_rope_opts;
+/* dst = x rotated by pos (int32 [T]).  dst == x with equal ld is allowed, no other overlap.  dim 2..1024,
+ * T <= 2^20, heads <= 1024. */
+GF_API int gf_rope(const void* x, int64_t T, int64_t heads, int64_t dim, const int32_t* pos, const gf_rope_opts* opts,
+                   void* dst, void* stream);
+GF_API int gf_prepare_rope(const void* x, int64_t T, int64_t heads, int64_t dim, const int32_t* pos,
+                           const gf_rope_opts* opts, void* dst, gf_prepared** out);
+
+/* A cache of keys and values in pages of `page` tokens, one byte an element and a float32 scale for every
+ * `block` tokens of a page and head:
+ *   k, v             : [n_pages][heads][page][dim] codes, 16-byte aligned
+ *   k_scale, v_scale : [n_pages][heads][page / block]
+ *   table            : int32 [n_seqs][table_ld]; position p of sequence s lies in page table[s][p / page]
+ * A value is code * scale.  I8: codes -127..127, scales of 12 significant bits; E4M3: 4-bit exponents and
+ * 3-bit mantissas up to 448, scales that are powers of two.
+ *  Limits (GF_ERR_UNSUPPORTED beyond): page 16..2^20 and block 1..64, powers of two, block <= page; dim a
+ *  multiple of 16 up to 256; heads <= 1024; page * table_ld <= 2^30.
+ * A token has no place where its seq is outside 0..n_seqs - 1, its pos below 0 or not under page *
+ * table_ld, or the page outside 0..n_pages - 1: such rows (of a padded batch) are not stored, load as
+ * zeros, and see no keys. */
+typedef enum { GF_CACHE_I8 = 0, GF_CACHE_E4M3 = 1 } gf_cache_format;
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int format;
+  int64_t n_pages, heads, page, dim, block;
+  const int32_t* table;
+  int64_t n_seqs, table_ld;
+} gf_cache;
+
+/* Writes T tokens' keys and values [T][heads][dim].  With opts->rope the keys are rotated by their
+ * position first, and the queries q [T][q_heads][dim], if given, into q_dst (q_dst == q allowed).
+ * For every block of tokens of a head that is written to, with a the largest magnitude of its new values:
+ *     need  = the least scale of the format with 127 (E4M3: 448) * need >= a, within 2^-112..2^121 (2^119)
+ *     scale = need, or where the block holds earlier tokens the larger of need and its scale before
+ *     code  = value / scale rounded to the nearest code, ties to even
+ * and where the scale grew, the earlier tokens' codes become code * old scale / scale, rounded the same
+ * way.  A block holds earlier tokens if its first position of this call is not its first one; later
+ * positions of it count as new.  A value that is not finite makes its block's scale NaN: the block reads
+ * back as NaN until its first position is written again.
+ * Tokens of one sequence stand next to each other in the call, by rising positions; a position at most
+ * once (else the blocks concerned hold some of the values, and nothing else is touched).
+ * n_rot must be a multiple of 8 here (GF_ERR_UNSUPPORTED); T <= 2^20, q_heads <= 1024.  No argument may
+ * overlap the cache's arrays, and q_dst no input but q (rows of one fused q, k, v buffer may lie between
+ * each other). */
+typedef struct {
+  int type;                   /* of k, v, q, q_dst                                    */
+  int64_t ldk, ldv;
+  const gf_rope_opts* rope;   /* table, n_rot and layout are read; NULL: no rotation  */
+  const void* q;              /* NULL: none (must be NULL without rope)               */
+  void* q_dst;
+  int64_t q_heads, ldq, ld_q_dst;
+  uint32_t flags;             /* GF_FLAG_PDL                                          */
+} gf_store_opts;
+GF_API int gf_cache_store(const gf_cache* cache, const void* k, const void* v, int64_t T, const int32_t* seq,
+                          const int32_t* pos, const gf_store_opts* opts, void* stream);
+GF_API int gf_prepare_cache_store(const gf_cache* cache, const void* k, const void* v, int64_t T, const int32_t* seq,
+                                  const int32_t* pos, const gf_store_opts* opts, gf_prepared** out);
+
+/* Reads T tokens' keys and values back as [T][heads][dim] (k or v may be NULL: not wanted).  The outputs
+ * overlap nothing else.  T <= 2^20. */
+typedef struct {
+  int type;
+  int64_t ldk, ldv;
+  uint32_t flags;  /* GF_FLAG_PDL */
+} gf_load_opts;
+GF_API int gf_cache_load(const gf_cache* cache, int64_t T, const int32_t* seq, const int32_t* pos,
+                         const gf_load_opts* opts, void* k, void* v, void* stream);
+GF_API int gf_prepare_cache_load(const gf_cache* cache, int64_t T, const int32_t* seq, const int32_t* pos,
+                                 const gf_load_opts* opts, void* k, void* v, gf_prepared** out);
+
+/* Attention of T tokens over the cache: query head h of token t sees the keys of head h / (q_heads / heads)
+ * at positions max(0, pos - window + 1) .. pos of its sequence,
+ *     s_j = scale * q . K_j,   dst = sum_j softmax(s)_j V_j,   lse = ln sum_j exp(s_j)
+ * in 32-bit arithmetic (q and the weights as pairs of binary16, to 2^-22).  The tokens' own keys have been
+ * stored before.  Positions in pages that the table does not have are not seen; a row that sees nothing
+ * (of a token without a place, for instance) is 0, its lse -inf.  A token whose pos reaches beyond the table
+ * sees what lies in it.
+ *  q, dst    : [T][q_heads][dim]; q_heads a multiple of heads, <= 1024.  T <= 2^16.
+ *  run       : how many tokens of one sequence stand next to each other (drafted tokens, a prompt's part;
+ *              0 or 1: a decode step).  They then share one reading of the keys.  Only speed depends on it.
+ *  workspace : device memory of at least gf_attend_workspace() bytes, 256-byte aligned, contents undefined
+ *              before and after; not shared by calls that may overlap.
+ *  dst, lse and the workspace overlap nothing else. */
+typedef struct {
+  int type;
+  int64_t ldq, ld_dst;
+  float scale;          /* > 0; 0: 1 / sqrt(dim)                                      */
+  int64_t window;       /* keys that a token sees, itself among them; 0: all          */
+  int64_t run;
+  float* lse;           /* [T][q_heads] or NULL                                       */
+  void* workspace;
+  int64_t workspace_bytes;
+  uint32_t flags;       /* GF_FLAG_PDL                                                */
+} gf_attend_opts;
+GF_API int gf_attend(const gf_cache* cache, const void* q, int64_t T, int64_t q_heads, const int32_t* seq,
+                     const int32_t* pos, const gf_attend_opts* opts, void* dst, void* stream);
+GF_API int gf_prepare_attend(const gf_cache* cache, const void* q, int64_t T, int64_t q_heads, const int32_t* seq,
+                             const int32_t* pos, const gf_attend_opts* opts, void* dst, gf_prepared** out);
+/* Bytes of workspace for these sizes on the current device; negative: a gf_status. */
+GF_API int64_t gf_attend_workspace(int64_t T, int64_t q_heads, int64_t heads, int64_t dim, int64_t run);
+
 /* Signed FWHT, stand-alone ([FWHT] Overview): for every block of `block` consecutive
  * elements of x[0..n), dst_b = H_block (x_b * s) / sqrt(block), with element i using
  * signs[i % nsigns]; signs == NULL means all +1 (the plain normalised transform).
