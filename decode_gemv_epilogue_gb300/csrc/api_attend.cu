@@ -322,13 +322,16 @@ static int check_attend(const gf_cache* c, const void* q, int64_t T, int64_t q_h
   if (e != GF_OK) return e;
   if (q_heads % c->heads != 0) return GF_ERR_INVALID;
   if (T > kAttMaxTokens || q_heads > kMaxHeads || o->run > kAttMaxTokens || o->window > INT32_MAX) return GF_ERR_UNSUPPORTED;
+  // (chunks of all items, counted in 64 bits times the warps that share them)
+  if (static_cast<double>(T) * q_heads * (c->table_ld * c->page / 16 + 2) > 2251799813685248.0) return GF_ERR_UNSUPPORTED;
   if (T == 0) return GF_OK;
   if ((e = check_tokens(seq, pos)) != GF_OK) return e;
   int vec = 1;
   int64_t ldq = o->ldq, ldd = o->ld_dst;
   const int64_t width = q_heads * c->dim;
+  int any = 1;
   if ((e = check_rows(q, &ldq, width, o->type, &vec)) != GF_OK) return e;
-  if ((e = check_rows(dst, &ldd, width, o->type, &vec)) != GF_OK) return e;
+  if ((e = check_rows(dst, &ldd, width, o->type, &any)) != GF_OK) return e;
   if (!aligned_to(o->lse, 4)) return GF_ERR_ALIGN;
   const int64_t need = attend_bytes(T, q_heads, c->heads, c->dim, o->run);
   if (!o->workspace || o->workspace_bytes < need) return GF_ERR_INVALID;
@@ -358,6 +361,7 @@ static int check_attend(const gf_cache* c, const void* q, int64_t T, int64_t q_h
   a.group = static_cast<int>(q_heads / c->heads);
   a.window = static_cast<int>(o->window);
   a.type = o->type;
+  a.vec = vec;
   attend_shape(a.group, c->dim, std::max<int64_t>(o->run, 1), a);
   a.ctas = attend_ctas(ca.dim, a.tiles, device_limits().sm_count);
   return GF_OK;

@@ -16,8 +16,11 @@
 // running ones in 32 bits, outside the matrix unit (which truncates).
 //
 // Items, (tokens of a sequence next to each other, head of the cache, part of its queries), are laid end
-// to end by their number of chunks, and every CTA takes an equal stretch; the parts of an item that
-// stretches over CTAs go through the workspace, and a second launch joins them in order.
+// to end by their number of chunks and one more for their start and end, and every warp takes an equal
+// stretch, whatever the sequences' lengths.  Warps know nothing of each other: the parts of an item that reaches over
+// several go through the workspace, and a second launch joins them in order.  (A CTA to an item, its warps joined in
+// shared memory, took 152 us where this takes XX for 61 sequences of 100 to 8000 keys: short ones cost it
+// a barrier's round each.)
 #include "cache_device.cuh"
 #include "gf_device.cuh"
 #include "rope_device.cuh"
@@ -27,17 +30,20 @@ namespace gf {
 template <int DC, int NM>
 struct AttShape {
   static constexpr int kTokens = DC == 256 ? 16 : 32;               // of a chunk
-  static constexpr int kWarps = (DC <= 128 && NM == 1) || DC == 256 ? 6 : 4;
+  static constexpr bool kQRegs = DC <= 128 && NM == 1;              // queries in registers, else in shared memory
+  static constexpr int kWarps = kQRegs ? 6 : 4;
   static constexpr int kRows = 8 * NM;
   static constexpr int kSteps = DC / 16;                            // instructions along the dims
   static constexpr int kScaleAt = 2 * kTokens * DC;                 // of a stage: keys, values, scales
   static constexpr int kStage = kScaleAt + 2 * kTokens * 4;
   static constexpr int kStages = 2;
-  static constexpr int kQBytes = NM * kSteps * 512;
-  static constexpr int kRowFloats = DC + 2;                         // a row's part: sums, maximum, sum of weights
-  static constexpr int kSmem = kQBytes + kWarps * kStages * kStage;
-  static_assert(kRows * kRowFloats * 4 <= kStage, "a warp's part fits the stage that it has used up");
+  static constexpr int kWarpBytes = kStages * kStage + (kQRegs ? 0 : NM * kSteps * 512);
+  static constexpr int kSmem = kWarps * kWarpBytes;
+  static constexpr int kSlices = kRows * DC / 128;                  // float4 a lane of a row part
+  static constexpr int64_t kPart = kRows * (DC + 2);                // floats: sums, maxima, sums of weights
 };
+template <int DC>
+constexpr int kUnitBytes = DC == 64 ? 8 : 16;  // of a value row, in a lane's hands
 
 constexpr float kNoMax = -1e30f;   // running maximum of a row without keys
 constexpr float kHidden = -1.0f;   // scale of a token that no row sees (stored ones are positive, or NaN)
@@ -104,7 +110,7 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
 
 // ------------------------------------------------------------------ items
 struct Item {
-  int64_t begin;   // its first chunk, among all items'
+  int64_t begin;   // its first unit, among all items'
   int t0, n;       // tokens
   int seq;
   int lo, hi;      // keys [lo, hi) that its tokens see together
@@ -165,32 +171,34 @@ __device__ __forceinline__ bool item_at(const AttendArgs& a, int t, Item& it) {
   return true;
 }
 
-// Workspace: a header, a record for each CTA's first item, then each CTA's two parts.
+// Workspace: a header, a record of each warp's first item, then each warp's two parts.
 struct AttHeader {
-  int64_t chunks;
-  int64_t ctas;
+  int64_t units;
+  int64_t workers;
 };
 struct AttFirst {
   int64_t begin, end;
   int t0, n, hs, pad;
 };
 constexpr int kAttHead = 64;
-__host__ __device__ constexpr int64_t att_parts_at(int ctas) { return kAttHead + static_cast<int64_t>(ctas) * 32; }
+__host__ __device__ constexpr int64_t att_parts_at(int workers) { return kAttHead + static_cast<int64_t>(workers) * 32; }
 
-// Chunk at which CTA i of n begins.
-__device__ __forceinline__ int64_t share(int64_t chunks, int64_t i, int64_t n) { return chunks * i / n; }
+// Unit at which worker i of n begins.
+__device__ __forceinline__ int64_t share(int64_t units, int64_t i, int64_t n) { return units * i / n; }
 
-template <typename T>
-__device__ __forceinline__ T block_sum(T v, T* scratch) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+template <int CT>
+__device__ __forceinline__ uint32_t units_at(const AttendArgs& a, int t) {
+  Item it;
+  return t < a.T && item_at<CT>(a, t, it) ? it.chunks + 1 : 0;
+}
+
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {  // inclusive
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if (lane == 0) scratch[warp] = v;
-  __syncthreads();
-  T s = 0;
-  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) s += scratch[i];
-  return s;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += up;
+  }
+  return v;
 }
 
 __device__ __forceinline__ void write_out(const AttendArgs& a, int64_t at, float4 v) {
@@ -211,14 +219,6 @@ __device__ __forceinline__ void write_out(const AttendArgs& a, int64_t at, float
   }
 }
 
-// Where elements d .. d + 3 of a warp's row r lie in its part: 16-byte places exchanged so that the eight
-// lanes that write at once, two rows' columns of four c4, meet eight different ones.
-template <int DC>
-__device__ __forceinline__ int part_at(int r, int d) {
-  const int q = d >> 2;
-  return r * DC + ((q ^ (((q >> (DC == 64 ? 2 : 3)) & 3) * 2 + (r & 1))) << 2);
-}
-
 // Token and query head of row r of an item; false where it has none.
 __device__ __forceinline__ bool row_of(const AttendArgs& a, int t0, int n, int hs, int r, int& t, int& head) {
   const int i = r / a.rows, h = r - i * a.rows, sub = hs % a.subs;
@@ -233,81 +233,77 @@ template <int DC, int FMT, int NM>
 __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kernel(const __grid_constant__ AttendArgs a) {
   using S = AttShape<DC, NM>;
   constexpr int CT = S::kTokens, W = S::kWarps, KS = S::kSteps, NT = CT / 8, KG = CT / 16;
-  constexpr int UC = DC == 256 ? 2 : 1;       // 16-byte (DC 64: 8-byte) units of a value row a lane holds
-  constexpr int UB = DC == 64 ? 8 : 16;       // bytes of a unit of values
+  constexpr int UC = DC == 256 ? 2 : 1;       // units of a value row that a lane holds
+  constexpr int UB = kUnitBytes<DC>;
   constexpr int NO = DC / 8;                  // column tiles of the output
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int64_t scan[32];
-  __shared__ Item found;
-  __shared__ float row_scale[S::kRows];       // of the products: the query's power of two, scale and log2(e)
-  __shared__ int row_lo[S::kRows], row_hi[S::kRows];
+  __shared__ uint32_t group_units[kAttMaxTokens / 32];  // of 32 tokens each, for one (head, part)
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c4 = lane & 3;
   const int HS = a.c.heads * a.subs;
   const int D = a.c.dim, U16 = D / 16;
 
-  // ---- this CTA's stretch of chunks
-  int64_t mine = 0;
-  for (int t = threadIdx.x; t < a.T; t += blockDim.x) {
-    Item it;
-    if (item_at<CT>(a, t, it)) mine += it.chunks;
-  }
-  const int64_t total = block_sum(mine, scan) * HS;
-  // a CTA takes one chunk a warp at least, so that short rows are not cut for nothing
-  int64_t ctas = (total + W - 1) / W;
-  if (ctas > a.ctas) ctas = a.ctas;
-  if (blockIdx.x >= ctas) return;
-  const int64_t start = share(total, blockIdx.x, ctas), stop = share(total, blockIdx.x + 1, ctas);
-  // the item that holds `start`
-  int64_t before = 0;
-  for (int base = 0; base < a.T; base += blockDim.x) {
-    const int t = base + threadIdx.x;
-    Item it;
-    const bool has = t < a.T && item_at<CT>(a, t, it);
-    const int64_t n = has ? it.chunks : 0;
-    int64_t incl = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
-    }
-    __syncthreads();
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    int64_t ahead = before, all = before;
-    for (int i = 0; i < W; ++i) {
-      if (i < warp) ahead += scan[i];
-      all += scan[i];
-    }
-    const int64_t b = (ahead + incl - n) * HS;
-    if (n > 0 && start >= b && start < b + n * HS) {
-      it.hs = static_cast<int>((start - b) / n);
-      it.begin = b + it.hs * n;
-      found = it;
-    }
-    before = all;
-    if (before * HS > start) break;
+  // ---- this warp's stretch of units
+  const int groups = (a.T + 31) / 32;
+  for (int k = warp; k < groups; k += W) {
+    const uint32_t n = __reduce_add_sync(0xffffffffu, units_at<CT>(a, k * 32 + lane));
+    if (lane == 0) group_units[k] = n;
   }
   __syncthreads();
-  Item item = found;
-  if (threadIdx.x == 0) {
-    if (blockIdx.x == 0) {
-      AttHeader h = {total, ctas};
+  int64_t total = 0;
+  for (int k = lane; k < groups; k += 32) total += group_units[k];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= HS;
+  // two units each at least; neighbours among the workers lie on different SMs
+  const int64_t workers = min(static_cast<int64_t>(a.ctas) * W, (total + 1) / 2);
+  const int64_t me = static_cast<int64_t>(warp) * a.ctas + blockIdx.x;
+  if (me >= workers) return;
+  const int64_t start = share(total, me, workers), stop = share(total, me + 1, workers);
+  Item item;
+  {
+    int64_t before = 0;  // units of one (head, part) ahead of the group
+    int k = 0;
+    for (; k < groups; k += 32) {
+      const int64_t n = k + lane < groups ? group_units[k + lane] : 0;
+      const int64_t incl = warp_scan(n, lane) + before;
+      const uint32_t past = __ballot_sync(0xffffffffu, incl * HS > start);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        before = __shfl_sync(0xffffffffu, incl - n, l);
+        k += l;
+        break;
+      }
+      before = __shfl_sync(0xffffffffu, incl, 31);
+    }
+    const int64_t n = units_at<CT>(a, k * 32 + lane);
+    const int64_t incl = warp_scan(n, lane) + before;
+    const int l = __ffs(__ballot_sync(0xffffffffu, incl * HS > start)) - 1;
+    item_at<CT>(a, k * 32 + l, item);
+    const int64_t b = __shfl_sync(0xffffffffu, incl - n, l) * HS;
+    item.hs = static_cast<int>((start - b) / (item.chunks + 1));
+    item.begin = b + static_cast<int64_t>(item.hs) * (item.chunks + 1);
+  }
+  if (lane == 0) {
+    if (me == 0) {
+      AttHeader h = {total, workers};
       *reinterpret_cast<AttHeader*>(a.workspace) = h;
     }
-    AttFirst f = {item.begin, item.begin + item.chunks, item.t0, item.n, item.hs, 0};
-    reinterpret_cast<AttFirst*>(reinterpret_cast<uint8_t*>(a.workspace) + kAttHead)[blockIdx.x] = f;
+    AttFirst f = {item.begin, item.begin + item.chunks + 1, item.t0, item.n, item.hs, 0};
+    reinterpret_cast<AttFirst*>(reinterpret_cast<uint8_t*>(a.workspace) + kAttHead)[me] = f;
   }
-  float* parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.workspace) + att_parts_at(a.ctas)) +
-                 static_cast<int64_t>(blockIdx.x) * 2 * S::kRows * S::kRowFloats;
+  float* parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.workspace) + att_parts_at(a.ctas * W)) +
+                 me * 2 * S::kPart;
 
-  uint8_t* ring = smem + S::kQBytes + warp * (S::kStages * S::kStage);
+  uint8_t* ring = smem + warp * S::kWarpBytes;
   const uint32_t ring_at = smem_u32(ring);
+  uint8_t* qs = ring + S::kStages * S::kStage;
+
   // Copies of one chunk of an item into a stage.  Tokens outside [lo, hi) or without a page: zeros under the
   // scale kHidden.
-  auto fetch = [&](const Item& it, int64_t idx, int stage) {
-    const int p0 = (it.lo / CT + static_cast<int>(idx - it.begin)) * CT, head = it.hs / a.subs;
+  auto fetch = [&](const Item& it, int chunk, int stage) {
+    const int p0 = (it.lo / CT + chunk) * CT, head = it.hs / a.subs;
     const uint32_t to = ring_at + stage * S::kStage;
     int64_t page[KG];
 #pragma unroll
@@ -362,67 +358,76 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
       }
     }
   };
+  // The item's chunks [c0, c1) of this warp's stretch.
+  auto stretch = [&](const Item& it, int& c0, int& c1) {
+    const int64_t from = start - it.begin - 1, to = stop - it.begin - 1;
+    c0 = from < 0 ? 0 : static_cast<int>(from);
+    c1 = to < it.chunks ? static_cast<int>(to) : it.chunks;
+  };
 
-  int stage = 0;
-  int64_t first = start;  // of the item's chunks that this CTA takes
-  if (start + warp < min(stop, item.begin + item.chunks)) fetch(item, start + warp, 0);
+  int stage = 0, c0, c1;
+  stretch(item, c0, c1);
+  if (c0 < c1) fetch(item, c0, 0);
   cp_commit();
 
   for (;;) {
-    const int64_t end = min(stop, item.begin + item.chunks);
-    // ---- the item's queries: hi and lo parts in the order of the instructions' rows
-    __syncthreads();
-    for (int r = warp; r < S::kRows; r += W) {
+    // ---- the item's queries, hi and lo parts in the order of the instructions' rows: of row g, lane (g, c4)
+    // takes units c4, c4 + 4, .. as it does of a key
+    uint4 qr[S::kQRegs ? KS : 1];
+    float f[NM];  // of the products: the query's power of two, scale and log2(e)
+    int lo[NM], hi[NM];
+#pragma unroll
+    for (int i = 0; i < NM; ++i) {
       int t, head;
-      const bool live = row_of(a, item.t0, item.n, item.hs, r, t, head);
-      constexpr int E = DC == 256 ? 8 : 4;
-      float v[E];
+      const bool live = row_of(a, item.t0, item.n, item.hs, 8 * i + g, t, head);
+      const int64_t row = t * a.ldq + static_cast<int64_t>(head) * D;
+      float4 v[KS];
       uint32_t top = 0;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int d = (e / 4) * 128 + lane * 4 + e % 4;
-        v[e] = 0.0f;
+      for (int k = 0; k < KS; ++k) {
+        const int d = (k / 4) * 64 + c4 * 16 + (k % 4) * 4;
+        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (live && d < D) {
-          const int64_t at = t * a.ldq + static_cast<int64_t>(head) * D + d;
-          v[e] = a.type == 0 ? static_cast<const float*>(a.q)[at] : __half2float(static_cast<const __half*>(a.q)[at]);
+          const int64_t at = row + d;
+          if (a.type == 0) {
+            const float* p = static_cast<const float*>(a.q) + at;
+            v[k] = a.vec ? load4(p) : make_float4(p[0], p[1], p[2], p[3]);
+          } else {
+            const __half* p = static_cast<const __half*>(a.q) + at;
+            v[k] = a.vec ? load4(p) : make_float4(load1(p), load1(p + 1), load1(p + 2), load1(p + 3));
+          }
         }
-        top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+        top = max(top, max(max(__float_as_uint(v[k].x) & 0x7fffffffu, __float_as_uint(v[k].y) & 0x7fffffffu),
+                           max(__float_as_uint(v[k].z) & 0x7fffffffu, __float_as_uint(v[k].w) & 0x7fffffffu)));
       }
-      top = __reduce_max_sync(0xffffffffu, top);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // |q| 2^-x lies in [2^14, 2^15) for the largest
       int x = static_cast<int>(top >> 23) - 127 - 14;
       x = x < -110 ? -110 : x;
       const bool number = top < 0x7f800000u;
-      const float f = __uint_as_float(static_cast<uint32_t>(127 - x) << 23);
+      const float w = __uint_as_float(static_cast<uint32_t>(127 - x) << 23);
 #pragma unroll
-      for (int e = 0; e < E; e += 4) {
-        const int d = (e / 4) * 128 + lane * 4;
-        if (d >= DC) continue;
-        uint4 w;
-        split2(number ? v[e] * f : 0.0f, number ? v[e + 1] * f : 0.0f, w.x, w.y);
-        split2(number ? v[e + 2] * f : 0.0f, number ? v[e + 3] * f : 0.0f, w.z, w.w);
-        const int step = d / 64 * 4 + d % 16 / 4, lane_of = (r % 8) * 4 + d % 64 / 16;
-        *reinterpret_cast<uint4*>(smem + (((r / 8) * KS + step) * 32 + lane_of) * 16) = w;
+      for (int k = 0; k < KS; ++k) {
+        uint4 h;
+        split2(number ? v[k].x * w : 0.0f, number ? v[k].y * w : 0.0f, h.x, h.y);
+        split2(number ? v[k].z * w : 0.0f, number ? v[k].w * w : 0.0f, h.z, h.w);
+        if constexpr (S::kQRegs)
+          qr[k] = h;
+        else
+          *reinterpret_cast<uint4*>(qs + ((i * KS + k) * 32 + lane) * 16) = h;  // read back by this lane alone
       }
-      if (lane == 0) {
-        row_scale[r] = number ? a.scale * __uint_as_float(static_cast<uint32_t>(127 + x) << 23) : __uint_as_float(0x7fffffffu);
-        int s, lo = 0, hi = 0;
-        if (live) keys_of(a, t, s, lo, hi);
-        row_lo[r] = lo;
-        row_hi[r] = hi;
-      }
+      f[i] = number ? a.scale * __uint_as_float(static_cast<uint32_t>(127 + x) << 23) : __uint_as_float(0x7fffffffu);
+      lo[i] = hi[i] = 0;
+      int s;
+      if (live) keys_of(a, t, s, lo[i], hi[i]);
     }
-    __syncthreads();
 
-    float o[NM][NO][2], m[NM], l[NM], f[NM];
-    int lo[NM], hi[NM];
+    float o[NM][NO][2], m[NM], l[NM];
 #pragma unroll
     for (int i = 0; i < NM; ++i) {
       m[i] = kNoMax;
       l[i] = 0.0f;
-      f[i] = row_scale[8 * i + g];
-      lo[i] = row_lo[8 * i + g];
-      hi[i] = row_hi[8 * i + g];
 #pragma unroll
       for (int n = 0; n < NO; ++n) o[i][n][0] = o[i][n][1] = 0.0f;
     }
@@ -430,15 +435,15 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
     // least that of the format's smallest scale
     uint32_t vexp = 127 - 111;
 
-    for (int64_t idx = first + warp; idx < end; idx += W) {
-      if (idx + W < end) fetch(item, idx + W, stage ^ 1);
+    for (int c = c0; c < c1; ++c) {
+      if (c + 1 < c1) fetch(item, c + 1, stage ^ 1);
       cp_commit();
       cp_wait<1>();
       __syncwarp();
       const uint8_t* st = ring + stage * S::kStage;
       const float* ks = reinterpret_cast<const float*>(st + S::kScaleAt);
       const float* vs = ks + CT;
-      const int p0 = (item.lo / CT + static_cast<int>(idx - item.begin)) * CT;
+      const int p0 = (item.lo / CT + c) * CT;
 
       // ---- scores
       float s[NM][NT][4];
@@ -452,8 +457,12 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 #pragma unroll
         for (int i = 0; i < NM; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            q[i][j] = *reinterpret_cast<const uint4*>(smem + ((i * KS + u * 4 + j) * 32 + lane) * 16);
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (S::kQRegs)
+              q[i][j] = qr[u * 4 + j];
+            else
+              q[i][j] = *reinterpret_cast<const uint4*>(qs + ((i * KS + u * 4 + j) * 32 + lane) * 16);
+          }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           uint4 w = make_uint4(0, 0, 0, 0);  // a unit that the head does not have
@@ -574,140 +583,166 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
     }
 
     // ---- the next item's first chunk starts on its way
-    cp_wait<0>();
-    const bool last = end == stop;
+    const int64_t end = item.begin + item.chunks + 1;
+    const bool last = end >= stop;
     Item next = item;
+    int n0 = 0, n1 = 0;
     if (!last) {
-      next.begin = item.begin + item.chunks;
       if (item.hs + 1 < HS) {
         ++next.hs;
       } else {
         next.hs = 0;
         int t = item.t0 + item.n;
         while (!item_at<CT>(a, t, next) && t < a.T - 1) ++t;  // (the token behind an item begins one)
-        next.begin = item.begin + item.chunks;
       }
-      const int64_t to = min(stop, next.begin + next.chunks);
-      if (next.begin + warp < to) fetch(next, next.begin + warp, stage);
+      next.begin = end;
+      stretch(next, n0, n1);
+      if (n0 < n1) fetch(next, n0, stage);
     }
     cp_commit();
 
-    // ---- the warps' parts together: each in the stage that it has used up
-    {
-      float* part = reinterpret_cast<float*>(ring + (stage ^ 1) * S::kStage);
-      const float back = __uint_as_float((vexp - kWeightBits) << 23);
+    // ---- results, or a part for the joining launch
+    const bool split = start > item.begin || end > stop;
+    float* part = parts + (start >= item.begin ? 0 : S::kPart);
+    const float back = __uint_as_float((vexp - kWeightBits) << 23);
 #pragma unroll
-      for (int i = 0; i < NM; ++i) {
+    for (int i = 0; i < NM; ++i) {
+      const float z = quad_sum(l[i]);
+      int t, head;
+      const bool live = row_of(a, item.t0, item.n, item.hs, 8 * i + g, t, head);
+      const float inv = split ? back : z == 0.0f ? 0.0f : back / z;  // no keys: zeros
 #pragma unroll
-        for (int u = 0; u < UC; ++u)
+      for (int u = 0; u < UC; ++u)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int n = 0; n < UB; n += 4) {
-              const int d = (2 * c4 + e + 8 * u) * UB + n;
-              *reinterpret_cast<float4*>(part + part_at<DC>(8 * i + g, d)) =
-                  make_float4(o[i][u * UB + n][e] * back, o[i][u * UB + n + 1][e] * back, o[i][u * UB + n + 2][e] * back,
-                              o[i][u * UB + n + 3][e] * back);
-            }
-        const float z = quad_sum(l[i]);
-        if (c4 == 0) {
+          for (int n = 0; n < UB; n += 4) {
+            const int d = (2 * c4 + e + 8 * u) * UB + n;
+            const float4 v = make_float4(o[i][u * UB + n][e] * inv, o[i][u * UB + n + 1][e] * inv,
+                                         o[i][u * UB + n + 2][e] * inv, o[i][u * UB + n + 3][e] * inv);
+            if (split)
+              *reinterpret_cast<float4*>(part + (((i * UC + u) * 2 + e) * (UB / 4) + n / 4) * 128 + lane * 4) = v;
+            else if (live && d < D)
+              write_out(a, t * a.ld_dst + static_cast<int64_t>(head) * D + d, v);
+          }
+      if (c4 == 0) {
+        if (split) {
           part[S::kRows * DC + 8 * i + g] = m[i];
           part[S::kRows * DC + S::kRows + 8 * i + g] = z;
+        } else if (live && a.lse) {
+          a.lse[static_cast<int64_t>(t) * a.q_heads + head] = z == 0.0f ? -INFINITY : (m[i] + log2f(z)) * 0.693147181f;
         }
       }
-    }
-    __shared__ int used[W];
-    if (lane == 0) used[warp] = static_cast<int>(ring - smem) + (stage ^ 1) * S::kStage;
-    __syncthreads();
-    const bool split = first > item.begin || end < item.begin + item.chunks;
-    float* out = parts + (first == start ? 0 : S::kRows * S::kRowFloats);
-    for (int i = threadIdx.x; i < S::kRows * DC / 4; i += blockDim.x) {
-      const int r = i / (DC / 4), d = i % (DC / 4) * 4;
-      float top = kNoMax;
-#pragma unroll
-      for (int w = 0; w < W; ++w) top = fmaxf(top, reinterpret_cast<const float*>(smem + used[w])[S::kRows * DC + r]);
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float z = 0.0f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float* p = reinterpret_cast<const float*>(smem + used[w]);
-        const float e = exp2f(p[S::kRows * DC + r] - top);
-        const float4 x = *reinterpret_cast<const float4*>(p + part_at<DC>(r, d));
-        v.x = fmaf(x.x, e, v.x), v.y = fmaf(x.y, e, v.y), v.z = fmaf(x.z, e, v.z), v.w = fmaf(x.w, e, v.w);
-        z = fmaf(p[S::kRows * DC + S::kRows + r], e, z);
-      }
-      if (split) {
-        *reinterpret_cast<float4*>(out + r * DC + d) = v;
-        if (d == 0) {
-          out[S::kRows * DC + r] = top;
-          out[S::kRows * DC + S::kRows + r] = z;
-        }
-        continue;
-      }
-      int t, head;
-      if (d >= D || !row_of(a, item.t0, item.n, item.hs, r, t, head)) continue;
-      const float inv = z == 0.0f ? 0.0f : 1.0f / z;  // no keys: zeros
-      write_out(a, t * a.ld_dst + static_cast<int64_t>(head) * D + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-      if (d == 0 && a.lse)
-        a.lse[static_cast<int64_t>(t) * a.q_heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * 0.693147181f;
     }
     if (last) break;
     item = next;
-    first = item.begin;
+    c0 = n0;
+    c1 = n1;
   }
+  cp_wait<0>();
 }
 
-// Joins the parts of the items that reach over CTAs: CTA (i, y) takes the item that CTA i's stretch begins
-// within, if it is the first to do so, rows y, y + gridDim.y, ..
+// Joins the parts of the items that reach over warps' stretches: CTA (i, y) takes the item that the stretch of
+// worker i + 1 begins within, if it is the first to do so, and of its parts' float4 slices every gridDim.y-th.
+// Its warps take the parts in turn; a lane holds a slice's place of all of them.
+constexpr int kJoinWarps = 4;
 template <int DC, int NM>
-__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __grid_constant__ AttendArgs a) {
   using S = AttShape<DC, NM>;
+  constexpr int UB = kUnitBytes<DC>, UC = DC == 256 ? 2 : 1, PER = S::kSlices / NM;  // slices of eight rows
+  __shared__ float4 sums[kJoinWarps][32];
+  __shared__ float2 tops[kJoinWarps][32];
   pdl_wait();
   pdl_trigger();
   const AttHeader h = *reinterpret_cast<const AttHeader*>(a.workspace);
   const int64_t i = static_cast<int64_t>(blockIdx.x) + 1;
-  if (i >= h.ctas) return;
+  if (i >= h.workers) return;
   const AttFirst f = reinterpret_cast<const AttFirst*>(reinterpret_cast<const uint8_t*>(a.workspace) + kAttHead)[i];
-  const int64_t prev = share(h.chunks, i - 1, h.ctas);
-  if (share(h.chunks, i, h.ctas) == f.begin || prev > f.begin) return;
-  int n = 1;  // parts
-  while (i - 1 + n < h.ctas && share(h.chunks, i - 1 + n, h.ctas) < f.end) ++n;
-  constexpr int64_t kPart = S::kRows * S::kRowFloats;
-  const float* parts = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.workspace) + att_parts_at(a.ctas));
-  // CTA i - 1 holds its part second, unless its stretch begins with the item
-  const float* head_part = parts + ((i - 1) * 2 + (prev < f.begin ? 1 : 0)) * kPart;
-  const float* rest = parts + i * 2 * kPart;
-  for (int k = threadIdx.x + blockIdx.y * blockDim.x; k < S::kRows * DC / 4; k += blockDim.x * gridDim.y) {
-    const int r = k / (DC / 4), d = k % (DC / 4) * 4;
-    int t, head;
-    if (d >= a.c.dim || !row_of(a, f.t0, f.n, f.hs, r, t, head)) continue;
-    float top = kNoMax;
-    for (int j = 0; j < n; ++j) top = fmaxf(top, (j == 0 ? head_part : rest + (j - 1) * 2 * kPart)[S::kRows * DC + r]);
+  const int64_t prev = share(h.units, i - 1, h.workers);
+  if (share(h.units, i, h.workers) == f.begin || prev > f.begin) return;
+  // parts: those of workers i - 1 .. the last whose stretch begins within the item
+  int64_t n = (f.end * h.workers + h.units - 1) / h.units;  // share(n) >= end > share(n - 1), or one beyond
+  while (n > i && share(h.units, n - 1, h.workers) >= f.end) --n;
+  n = min(n, h.workers) - (i - 1);
+  const float* parts = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.workspace) +
+                                                      att_parts_at(a.ctas * S::kWarps));
+  // worker i - 1 holds its part second, unless its stretch begins with the item
+  const float* head_part = parts + ((i - 1) * 2 + (prev < f.begin ? 1 : 0)) * S::kPart;
+  const float* rest = parts + i * 2 * S::kPart;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
+  for (int k = blockIdx.y; k < S::kSlices; k += gridDim.y) {
+    const int tile = k / PER, r = 8 * tile + g;
+    float top = kNoMax, z = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float z = 0.0f;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const float* p = j == 0 ? head_part : rest + (j - 1) * 2 * kPart;
-      const float e = exp2f(p[S::kRows * DC + r] - top);
-      const float4 x = *reinterpret_cast<const float4*>(p + r * DC + d);
-      v.x = fmaf(x.x, e, v.x), v.y = fmaf(x.y, e, v.y), v.z = fmaf(x.z, e, v.z), v.w = fmaf(x.w, e, v.w);
-      z = fmaf(p[S::kRows * DC + S::kRows + r], e, z);
+    constexpr int B = 4;
+    for (int64_t j = warp; j < n; j += kJoinWarps * B) {
+      float m[B], l[B];
+      float4 x[B];
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int64_t jj = j + b * kJoinWarps;
+        m[b] = kNoMax;
+        l[b] = 0.0f;
+        x[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (jj < n) {
+          const float* p = jj == 0 ? head_part : rest + (jj - 1) * 2 * S::kPart;
+          m[b] = p[S::kRows * DC + r];
+          l[b] = p[S::kRows * DC + S::kRows + r];
+          x[b] = *reinterpret_cast<const float4*>(p + k * 128 + lane * 4);
+        }
+      }
+      float now = top;
+#pragma unroll
+      for (int b = 0; b < B; ++b) now = fmaxf(now, m[b]);
+      const float e0 = exp2f(top - now);
+      top = now;
+      z *= e0;
+      v.x *= e0, v.y *= e0, v.z *= e0, v.w *= e0;
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const float e = exp2f(m[b] - now);
+        z = fmaf(l[b], e, z);
+        v.x = fmaf(x[b].x, e, v.x), v.y = fmaf(x[b].y, e, v.y), v.z = fmaf(x[b].z, e, v.z), v.w = fmaf(x[b].w, e, v.w);
+      }
     }
-    const float inv = z == 0.0f ? 0.0f : 1.0f / z;
-    write_out(a, t * a.ld_dst + static_cast<int64_t>(head) * a.c.dim + d,
-              make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-    if (d == 0 && a.lse)
-      a.lse[static_cast<int64_t>(t) * a.q_heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * 0.693147181f;
+    sums[warp][lane] = v;
+    tops[warp][lane] = make_float2(top, z);
+    __syncthreads();
+    if (warp == 0) {
+      for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, tops[w][lane].x);
+      v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      z = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) {
+        const float2 t = tops[w][lane];
+        const float4 x = sums[w][lane];
+        const float e = exp2f(t.x - top);
+        z = fmaf(t.y, e, z);
+        v.x = fmaf(x.x, e, v.x), v.y = fmaf(x.y, e, v.y), v.z = fmaf(x.z, e, v.z), v.w = fmaf(x.w, e, v.w);
+      }
+      const int s = k % PER, d = (2 * c4 + s / (UB / 4) % 2 + 8 * (s / (UB / 2))) * UB + s % (UB / 4) * 4;
+      int t, head;
+      if (row_of(a, f.t0, f.n, f.hs, r, t, head)) {
+        const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+        if (d < a.c.dim)
+          write_out(a, t * a.ld_dst + static_cast<int64_t>(head) * a.c.dim + d,
+                    make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+        if (d == 0 && a.lse)
+          a.lse[static_cast<int64_t>(t) * a.q_heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * 0.693147181f;
+      }
+    }
+    __syncthreads();
   }
+  static_assert(UC * 2 * (UB / 4) == PER, "slices of a row tile: unit, column parity, four dims");
 }
 
 // ------------------------------------------------------------------ host
 int64_t attend_workspace_bytes(int dim, int tiles, int ctas) {
   const int dc = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
-  return att_parts_at(ctas) + static_cast<int64_t>(ctas) * 2 * 8 * tiles * (dc + 2) * 4;
+  const int64_t workers = static_cast<int64_t>(ctas) * (dc <= 128 && tiles == 1 ? 6 : 4);
+  return att_parts_at(static_cast<int>(workers)) + workers * 2 * 8 * tiles * (dc + 2) * 4;
 }
 
-// Two CTAs an SM: one decodes while the other fetches queries or joins its warps.
 int attend_ctas(int, int, int sms) { return 2 * sms; }
 
 template <int DC, int FMT, int NM>
@@ -721,8 +756,10 @@ static int launch_attend_t(const AttendArgs& a, cudaStream_t st, bool pdl) {
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   if (a.phase == ATT_JOIN) {
-    cfg.gridDim = dim3(static_cast<unsigned>(a.ctas - 1), 2);
-    cfg.blockDim = dim3(128);
+    // Few items have many parts each: their slices spread over CTAs.
+    const int64_t items = static_cast<int64_t>(a.T) * a.c.heads * a.subs;
+    cfg.gridDim = dim3(static_cast<unsigned>(a.ctas * S::kWarps - 1), items <= 64 ? 8 : 2);
+    cfg.blockDim = dim3(32 * kJoinWarps);
     return cudaLaunchKernelEx(&cfg, attend_join_kernel<DC, NM>, a);
   }
   static SmemLimit limit;

@@ -392,7 +392,7 @@ struct AttendArgs {
   int phase;
   int T, q_heads, group;
   int window;           // keys back from a token's own (0: all)
-  int type;
+  int type, vec;        // vec: queries are read four elements at a time
   int tiles;            // of 8 rows an item has (1 or 2)
   int subs, rows;       // parts that the heads of a group fall into, heads of a part
   int run, tokens;      // tokens of a sequence expected next to each other; most tokens of an item
