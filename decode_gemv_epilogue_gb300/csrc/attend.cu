@@ -71,6 +71,20 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint4& a, uint32_t b0, 
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
+// The same with nothing to add to.
+__device__ __forceinline__ void mma0(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// 2^x to two units, results below 2^-126 as zero.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -173,8 +187,8 @@ __device__ __forceinline__ bool item_at(const AttendArgs& a, int t, Item& it) {
 
 // Workspace: a header, a record of each warp's first item, then each warp's two parts.
 struct AttHeader {
-  int64_t units;
   int64_t workers;
+  int64_t each, more;  // units of a worker; the first `more` take one more
 };
 struct AttFirst {
   int64_t begin, end;
@@ -183,8 +197,8 @@ struct AttFirst {
 constexpr int kAttHead = 64;
 __host__ __device__ constexpr int64_t att_parts_at(int workers) { return kAttHead + static_cast<int64_t>(workers) * 32; }
 
-// Unit at which worker i of n begins.
-__device__ __forceinline__ int64_t share(int64_t units, int64_t i, int64_t n) { return units * i / n; }
+// Unit at which worker i begins.
+__device__ __forceinline__ int64_t share(const AttHeader& h, int64_t i) { return i * h.each + (i < h.more ? i : h.more); }
 
 template <int CT>
 __device__ __forceinline__ uint32_t units_at(const AttendArgs& a, int t) {
@@ -229,7 +243,7 @@ __device__ __forceinline__ bool row_of(const AttendArgs& a, int t0, int n, int h
 }
 
 // ------------------------------------------------------------------ the kernel
-template <int DC, int FMT, int NM>
+template <int DC, bool EXACT, int FMT, int NM>
 __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kernel(const __grid_constant__ AttendArgs a) {
   using S = AttShape<DC, NM>;
   constexpr int CT = S::kTokens, W = S::kWarps, KS = S::kSteps, NT = CT / 8, KG = CT / 16;
@@ -242,7 +256,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c4 = lane & 3;
   const int HS = a.c.heads * a.subs;
-  const int D = a.c.dim, U16 = D / 16;
+  const int D = EXACT ? DC : a.c.dim, U16 = D / 16;
 
   // ---- this warp's stretch of units
   const int groups = (a.T + 31) / 32;
@@ -260,7 +274,11 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
   const int64_t workers = min(static_cast<int64_t>(a.ctas) * W, (total + 1) / 2);
   const int64_t me = static_cast<int64_t>(warp) * a.ctas + blockIdx.x;
   if (me >= workers) return;
-  const int64_t start = share(total, me, workers), stop = share(total, me + 1, workers);
+  AttHeader head;
+  head.workers = workers;
+  head.each = total / workers;
+  head.more = total - head.each * workers;
+  const int64_t start = share(head, me), stop = share(head, me + 1);
   Item item;
   {
     int64_t before = 0;  // units of one (head, part) ahead of the group
@@ -287,8 +305,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
   }
   if (lane == 0) {
     if (me == 0) {
-      AttHeader h = {total, workers};
-      *reinterpret_cast<AttHeader*>(a.workspace) = h;
+      *reinterpret_cast<AttHeader*>(a.workspace) = head;
     }
     AttFirst f = {item.begin, item.begin + item.chunks + 1, item.t0, item.n, item.hs, 0};
     reinterpret_cast<AttFirst*>(reinterpret_cast<uint8_t*>(a.workspace) + kAttHead)[me] = f;
@@ -300,61 +317,105 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
   const uint32_t ring_at = smem_u32(ring);
   uint8_t* qs = ring + S::kStages * S::kStage;
 
-  // Copies of one chunk of an item into a stage.  Tokens outside [lo, hi) or without a page: zeros under the
-  // scale kHidden.
-  auto fetch = [&](const Item& it, int chunk, int stage) {
-    const int p0 = (it.lo / CT + chunk) * CT, head = it.hs / a.subs;
-    const uint32_t to = ring_at + stage * S::kStage;
-    int64_t page[KG];
-#pragma unroll
-    for (int h = 0; h < KG; ++h) page[h] = it.hi > 0 ? cache_page(a.c, it.seq, p0 + 16 * h) : -1;
-    const int slot = p0 & ((1 << a.c.page_log2) - 1);
+  // The pages of a chunk's 16-token halves, as the table has them (-1: outside the table).
+  struct Pages {
+    int id[KG];
+  };
+  auto pages_of = [&](const Item& it, int chunk) {
+    Pages p;
 #pragma unroll
     for (int h = 0; h < KG; ++h) {
-      const int s = (slot + 16 * h) & ((1 << a.c.page_log2) - 1);
-      const int64_t at = page[h] >= 0 ? cache_row(a.c, page[h], head, s) : 0;
+      const int64_t i = ((it.lo / CT + chunk) * CT + 16 * h) >> a.c.page_log2;
+      p.id[h] = it.hi > 0 && i < a.c.table_ld ? a.c.table[it.seq * a.c.table_ld + i] : -1;
+    }
+    return p;
+  };
+  const int page_mask = (1 << a.c.page_log2) - 1;
+  const uint32_t k_lane = g * D + c4 * 16, v_lane = 2 * c4 * D + g * UB;  // of a lane's first token and unit
+  // Copies of one chunk of an item into a stage.  Tokens outside [lo, hi) or without a page: zeros under the
+  // scale kHidden.
+  auto fetch = [&](const Item& it, int chunk, const Pages& pages, int stage) {
+    const int p0 = (it.lo / CT + chunk) * CT, head = it.hs / a.subs, slot = p0 & page_mask;
+    const uint32_t to = ring_at + stage * S::kStage, k_to = to + lane * 16, v_to = to + CT * DC + lane * UB;
+    bool held[KG], all = p0 >= it.lo && p0 + CT <= it.hi;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = 8 * i + g, p = p0 + 16 * h + row;
-        const bool on = page[h] >= 0 && p >= it.lo && p < it.hi;
+    for (int h = 0; h < KG; ++h) {
+      held[h] = pages.id[h] >= 0 && pages.id[h] < a.c.n_pages;
+      all = all && held[h];
+    }
+    if (all) {
 #pragma unroll
-        for (int u = 0; u < DC / 64; ++u)
-          if (DC == D || c4 + 4 * u < U16)
-            cp_async16(to + (((2 * h + i) * (DC / 64) + u) * 32 + lane) * 16,
-                       a.c.k + at + static_cast<int64_t>(on ? row : 0) * D + (c4 + 4 * u) * 16, on);
+      for (int h = 0; h < KG; ++h) {
+        const int64_t at = cache_row(a.c, pages.id[h], head, (slot + 16 * h) & page_mask);
+        const uint8_t* k = a.c.k + at + k_lane;
+        const uint8_t* v = a.c.v + at + v_lane;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int u = 0; u < DC / 64; ++u)
+            if (EXACT || c4 + 4 * u < U16) cp_async16(k_to + ((2 * h + i) * (DC / 64) + u) * 512, k + 8 * i * D + 64 * u, true);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int u = 0; u < UC; ++u)
+            if (EXACT || (g + 8 * u) * UB < D) {
+              const uint32_t dst = v_to + ((4 * h + i) * UC + u) * 32 * UB;
+              const uint8_t* src = v + ((i & 1) + 8 * (i >> 1)) * D + 8 * u * UB;
+              if constexpr (UB == 16)
+                cp_async16(dst, src, true);
+              else
+                cp_async8(dst, src, true);
+            }
       }
+    } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 2 * c4 + (i & 1) + 8 * (i >> 1), p = p0 + 16 * h + row;
-        const bool on = page[h] >= 0 && p >= it.lo && p < it.hi;
+      for (int h = 0; h < KG; ++h) {
+        const int64_t at = held[h] ? cache_row(a.c, pages.id[h], head, (slot + 16 * h) & page_mask) : 0;
 #pragma unroll
-        for (int u = 0; u < UC; ++u)
-          if (DC == D || (g + 8 * u) * UB < D) {
-            const uint32_t dst = to + CT * DC + (((4 * h + i) * UC + u) * 32 + lane) * UB;
-            const uint8_t* src = a.c.v + at + static_cast<int64_t>(on ? row : 0) * D + (g + 8 * u) * UB;
-            if constexpr (UB == 16)
-              cp_async16(dst, src, on);
-            else
-              cp_async8(dst, src, on);
-          }
+        for (int i = 0; i < 2; ++i) {
+          const int row = 8 * i + g, p = p0 + 16 * h + row;
+          const bool on = held[h] && p >= it.lo && p < it.hi;
+#pragma unroll
+          for (int u = 0; u < DC / 64; ++u)
+            if (EXACT || c4 + 4 * u < U16)
+              cp_async16(k_to + ((2 * h + i) * (DC / 64) + u) * 512,
+                         a.c.k + (on ? at + row * D + (c4 + 4 * u) * 16 : 0), on);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 2 * c4 + (i & 1) + 8 * (i >> 1), p = p0 + 16 * h + row;
+          const bool on = held[h] && p >= it.lo && p < it.hi;
+#pragma unroll
+          for (int u = 0; u < UC; ++u)
+            if (EXACT || (g + 8 * u) * UB < D) {
+              const uint32_t dst = v_to + ((4 * h + i) * UC + u) * 32 * UB;
+              const uint8_t* src = a.c.v + (on ? at + row * D + (g + 8 * u) * UB : 0);
+              if constexpr (UB == 16)
+                cp_async16(dst, src, on);
+              else
+                cp_async8(dst, src, on);
+            }
+        }
       }
     }
     {
-      const int j = lane & (CT - 1), h = j / 16, p = p0 + j;
-      const bool is_v = CT == 16 && lane >= 16;
-      const int64_t pg = KG == 2 && h == 1 ? page[KG - 1] : page[0];
-      const bool on = pg >= 0 && p >= it.lo && p < it.hi;
-      const int64_t at = on ? cache_scale(a.c, pg, head, (slot + j) & ((1 << a.c.page_log2) - 1)) : 0;
+      const int j = lane & (CT - 1), p = p0 + j;
+      const bool is_v = CT == 16 && lane >= 16, upper = KG == 2 && j >= 16;
+      const int id = upper ? pages.id[KG - 1] : pages.id[0];
+      const bool on = all || ((upper ? held[KG - 1] : held[0]) && p >= it.lo && p < it.hi);
       float* scales = reinterpret_cast<float*>(ring + stage * S::kStage + S::kScaleAt);
       const uint32_t dst = to + S::kScaleAt + 4 * lane;
       if (!on) {
         scales[lane] = is_v ? 0.0f : kHidden;
         if (CT == 32) scales[CT + lane] = 0.0f;
-      } else if (CT == 32) {
-        cp_async4(dst, a.c.k_scale + at);
-        cp_async4(dst + 4 * CT, a.c.v_scale + at);
       } else {
-        cp_async4(dst, (is_v ? a.c.v_scale : a.c.k_scale) + at);
+        const int64_t at = cache_scale(a.c, id, head, (slot + j) & page_mask);
+        if (CT == 32) {
+          cp_async4(dst, a.c.k_scale + at);
+          cp_async4(dst + 4 * CT, a.c.v_scale + at);
+        } else {
+          cp_async4(dst, (is_v ? a.c.v_scale : a.c.k_scale) + at);
+        }
       }
     }
   };
@@ -367,7 +428,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 
   int stage = 0, c0, c1;
   stretch(item, c0, c1);
-  if (c0 < c1) fetch(item, c0, 0);
+  if (c0 < c1) fetch(item, c0, pages_of(item, c0), 0);
   cp_commit();
 
   for (;;) {
@@ -423,21 +484,24 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
       if (live) keys_of(a, t, s, lo[i], hi[i]);
     }
 
-    float o[NM][NO][2], m[NM], l[NM];
+    float2 o[NM][NO];
+    float m[NM], l[NM];
 #pragma unroll
     for (int i = 0; i < NM; ++i) {
       m[i] = kNoMax;
       l[i] = 0.0f;
 #pragma unroll
-      for (int n = 0; n < NO; ++n) o[i][n][0] = o[i][n][1] = 0.0f;
+      for (int n = 0; n < NO; ++n) o[i][n] = make_float2(0.0f, 0.0f);
     }
     // biased exponent of the power of two, above every scale so far, that the values' scales are taken by; at
     // least that of the format's smallest scale
     uint32_t vexp = 127 - 111;
 
+    Pages pages = pages_of(item, c0 + 1);  // of the chunk that is fetched next, loaded a chunk ahead
     for (int c = c0; c < c1; ++c) {
-      if (c + 1 < c1) fetch(item, c + 1, stage ^ 1);
+      if (c + 1 < c1) fetch(item, c + 1, pages, stage ^ 1);
       cp_commit();
+      pages = pages_of(item, c + 2);
       cp_wait<1>();
       __syncwarp();
       const uint8_t* st = ring + stage * S::kStage;
@@ -447,10 +511,6 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 
       // ---- scores
       float s[NM][NT][4];
-#pragma unroll
-      for (int i = 0; i < NM; ++i)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) s[i][n][0] = s[i][n][1] = s[i][n][2] = s[i][n][3] = 0.0f;
 #pragma unroll
       for (int u = 0; u < DC / 64; ++u) {
         uint4 q[NM][4];
@@ -466,7 +526,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           uint4 w = make_uint4(0, 0, 0, 0);  // a unit that the head does not have
-          if (DC == D || c4 + 4 * u < U16)
+          if (EXACT || c4 + 4 * u < U16)
             w = *reinterpret_cast<const uint4*>(st + ((n * (DC / 64) + u) * 32 + lane) * 16);
           const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -474,7 +534,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
             uint32_t b0, b1;
             pairs_of<FMT>(ww[j], b0, b1);
 #pragma unroll
-            for (int i = 0; i < NM; ++i) mma(s[i][n], q[i][j], b0, b1);
+            for (int i = 0; i < NM; ++i) u + j == 0 ? mma0(s[i][n], q[i][j], b0, b1) : mma(s[i][n], q[i][j], b0, b1);
           }
         }
       }
@@ -485,7 +545,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
       const uint32_t vnow = max(vexp, (vtop >> 23) + 1);
       // 2^(kWeightBits - (vnow - 127)): weights times it lie below 2^8
       const float vinv = __uint_as_float((254 + kWeightBits - vnow) << 23);
-      const float vstep = vexp == vnow ? 1.0f : exp2f(static_cast<float>(static_cast<int>(vexp) - static_cast<int>(vnow)));
+      const float vstep = vexp == vnow ? 1.0f : exp2_fast(static_cast<float>(static_cast<int>(vexp) - static_cast<int>(vnow)));
       vexp = vnow;
       uint4 pf[NM][KG];
       float alpha[NM];
@@ -506,18 +566,19 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
           top = fmaxf(top, fmaxf(x[n][0], x[n][1]));
         }
         top = fmaxf(m[i], quad_max(top));
-        alpha[i] = exp2f(m[i] - top);
+        alpha[i] = exp2_fast(m[i] - top);
         m[i] = top;
         float sum = 0.0f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float2 v2 = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c4);
-          const float p = exp2f(x[n][0] - top), q = exp2f(x[n][1] - top);
+          const float p = exp2_fast(x[n][0] - top), q = exp2_fast(x[n][1] - top);
           sum += p + q;
-          // a masked token's weight is zero whatever lies in its scale
           float y = p * (v2.x * vinv), z = q * (v2.y * vinv);
-          if (x[n][0] == -INFINITY) y = 0.0f;
-          if (x[n][1] == -INFINITY) z = 0.0f;
+          if (!whole) {  // a masked token's weight is zero whatever lies in its scale
+            if (x[n][0] == -INFINITY) y = 0.0f;
+            if (x[n][1] == -INFINITY) z = 0.0f;
+          }
           uint32_t h, w;
           split2(y, z, h, w);
           if (n % 2 == 0) {
@@ -553,10 +614,6 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
         for (int w = 0; w < UB / 4; ++w) {
           float acc[NM][4][4];
 #pragma unroll
-          for (int i = 0; i < NM; ++i)
-#pragma unroll
-            for (int d = 0; d < 4; ++d) acc[i][d][0] = acc[i][d][1] = acc[i][d][2] = acc[i][d][3] = 0.0f;
-#pragma unroll
           for (int k = 0; k < KG; ++k) {
             uint32_t b0[4], b1[4];
             pairs_of<FMT>(__byte_perm(raw[k][0][w], raw[k][1][w], 0x5140), b0[0], b0[1]);
@@ -566,15 +623,16 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 #pragma unroll
             for (int i = 0; i < NM; ++i)
 #pragma unroll
-              for (int d = 0; d < 4; ++d) mma(acc[i][d], pf[i][k], b0[d], b1[d]);
+              for (int d = 0; d < 4; ++d)
+                k == 0 ? mma0(acc[i][d], pf[i][k], b0[d], b1[d]) : mma(acc[i][d], pf[i][k], b0[d], b1[d]);
           }
 #pragma unroll
           for (int i = 0; i < NM; ++i)
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
-              float* at = o[i][(u * UB / 4 + w) * 4 + d];
-              at[0] = fmaf(at[0], alpha[i], acc[i][d][0] + acc[i][d][2]);
-              at[1] = fmaf(at[1], alpha[i], acc[i][d][1] + acc[i][d][3]);
+              float2& at = o[i][(u * UB / 4 + w) * 4 + d];
+              at = ffma2(at, make_float2(alpha[i], alpha[i]),
+                         fadd2(make_float2(acc[i][d][0], acc[i][d][1]), make_float2(acc[i][d][2], acc[i][d][3])));
             }
         }
       }
@@ -597,7 +655,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
       }
       next.begin = end;
       stretch(next, n0, n1);
-      if (n0 < n1) fetch(next, n0, stage);
+      if (n0 < n1) fetch(next, n0, pages_of(next, n0), stage);
     }
     cp_commit();
 
@@ -618,8 +676,9 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 #pragma unroll
           for (int n = 0; n < UB; n += 4) {
             const int d = (2 * c4 + e + 8 * u) * UB + n;
-            const float4 v = make_float4(o[i][u * UB + n][e] * inv, o[i][u * UB + n + 1][e] * inv,
-                                         o[i][u * UB + n + 2][e] * inv, o[i][u * UB + n + 3][e] * inv);
+            const float2* x = &o[i][u * UB + n];
+            const float4 v = e == 0 ? make_float4(x[0].x * inv, x[1].x * inv, x[2].x * inv, x[3].x * inv)
+                                    : make_float4(x[0].y * inv, x[1].y * inv, x[2].y * inv, x[3].y * inv);
             if (split)
               *reinterpret_cast<float4*>(part + (((i * UC + u) * 2 + e) * (UB / 4) + n / 4) * 128 + lane * 4) = v;
             else if (live && d < D)
@@ -642,98 +701,165 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
   cp_wait<0>();
 }
 
-// Joins the parts of the items that reach over warps' stretches: CTA (i, y) takes the item that the stretch of
-// worker i + 1 begins within, if it is the first to do so, and of its parts' float4 slices every gridDim.y-th.
-// Its warps take the parts in turn; a lane holds a slice's place of all of them.
+// An item that reaches over warps' stretches, as the joining launch finds it at the record of the first
+// worker whose stretch begins within it.
+struct Split {
+  AttFirst f;
+  int64_t n;                // parts: of the worker before, and of those that begin within the item
+  const float* head_part;   // the first; the others are kPart * 2 apart
+  const float* rest;
+};
+
+// Whether worker i's is such a record.
+__device__ __forceinline__ bool split_at(const AttendArgs& a, const AttHeader& h, int64_t i, AttFirst& f) {
+  if (i >= h.workers) return false;
+  f = reinterpret_cast<const AttFirst*>(reinterpret_cast<const uint8_t*>(a.workspace) + kAttHead)[i];
+  return share(h, i) > f.begin && share(h, i - 1) <= f.begin;
+}
+
+// The rest of it, by a whole warp.
+template <int DC, int NM>
+__device__ __forceinline__ Split split_of(const AttendArgs& a, const AttHeader& h, int64_t i, const AttFirst& f, int lane) {
+  using S = AttShape<DC, NM>;
+  Split s;
+  s.f = f;
+  int64_t k = i + 1;  // the first worker that begins behind the item
+  for (;; k += 32) {
+    const uint32_t behind = __ballot_sync(0xffffffffu, k + lane >= h.workers || share(h, k + lane) >= f.end);
+    if (behind) {
+      k += __ffs(behind) - 1;
+      break;
+    }
+  }
+  s.n = k - (i - 1);
+  const float* parts = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.workspace) +
+                                                      att_parts_at(a.ctas * S::kWarps));
+  // worker i - 1 holds its part second, unless its stretch begins with the item
+  s.head_part = parts + ((i - 1) * 2 + (share(h, i - 1) < f.begin ? 1 : 0)) * S::kPart;
+  s.rest = parts + i * 2 * S::kPart;
+  return s;
+}
+
+// Parts first, first + step, .. of a slice's place: running maximum, sum of weights and sums.
+template <int DC, int NM>
+__device__ __forceinline__ void join_parts(const Split& s, int slice, int lane, int first, int step, float& top, float& z,
+                                           float4& v) {
+  using S = AttShape<DC, NM>;
+  constexpr int B = 4;
+  const int r = 8 * (slice / (S::kSlices / NM)) + (lane >> 2);
+  top = kNoMax;
+  z = 0.0f;
+  v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int64_t j = first; j < s.n; j += step * B) {
+    float m[B], l[B];
+    float4 x[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int64_t jj = j + b * step;
+      m[b] = kNoMax;
+      l[b] = 0.0f;
+      x[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (jj < s.n) {
+        const float* p = jj == 0 ? s.head_part : s.rest + (jj - 1) * 2 * S::kPart;
+        m[b] = p[S::kRows * DC + r];
+        l[b] = p[S::kRows * DC + S::kRows + r];
+        x[b] = *reinterpret_cast<const float4*>(p + slice * 128 + lane * 4);
+      }
+    }
+    float now = top;
+#pragma unroll
+    for (int b = 0; b < B; ++b) now = fmaxf(now, m[b]);
+    const float e0 = exp2_fast(top - now);
+    top = now;
+    z *= e0;
+    v.x *= e0, v.y *= e0, v.z *= e0, v.w *= e0;
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const float e = exp2_fast(m[b] - now);
+      z = fmaf(l[b], e, z);
+      v.x = fmaf(x[b].x, e, v.x), v.y = fmaf(x[b].y, e, v.y), v.z = fmaf(x[b].z, e, v.z), v.w = fmaf(x[b].w, e, v.w);
+    }
+  }
+}
+
+template <int DC, int NM>
+__device__ __forceinline__ void join_out(const AttendArgs& a, const Split& s, int slice, int lane, float top, float z, float4 v) {
+  using S = AttShape<DC, NM>;
+  constexpr int UB = kUnitBytes<DC>, PER = S::kSlices / NM;  // slices of eight rows: unit, column parity, four dims
+  static_assert((DC == 256 ? 2 : 1) * 2 * (UB / 4) == PER, "as the parts are laid out");
+  const int k = slice % PER, r = 8 * (slice / PER) + (lane >> 2);
+  const int d = (2 * (lane & 3) + k / (UB / 4) % 2 + 8 * (k / (UB / 2))) * UB + k % (UB / 4) * 4;
+  int t, head;
+  if (!row_of(a, s.f.t0, s.f.n, s.f.hs, r, t, head)) return;
+  const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+  if (d < a.c.dim)
+    write_out(a, t * a.ld_dst + static_cast<int64_t>(head) * a.c.dim + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+  if (d == 0 && a.lse)
+    a.lse[static_cast<int64_t>(t) * a.q_heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * 0.693147181f;
+}
+
+// Many items, few parts each: CTA i looks at worker i + 1's record; its warps share the slices.
 constexpr int kJoinWarps = 4;
 template <int DC, int NM>
 __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __grid_constant__ AttendArgs a) {
-  using S = AttShape<DC, NM>;
-  constexpr int UB = kUnitBytes<DC>, UC = DC == 256 ? 2 : 1, PER = S::kSlices / NM;  // slices of eight rows
-  __shared__ float4 sums[kJoinWarps][32];
-  __shared__ float2 tops[kJoinWarps][32];
   pdl_wait();
   pdl_trigger();
   const AttHeader h = *reinterpret_cast<const AttHeader*>(a.workspace);
   const int64_t i = static_cast<int64_t>(blockIdx.x) + 1;
-  if (i >= h.workers) return;
-  const AttFirst f = reinterpret_cast<const AttFirst*>(reinterpret_cast<const uint8_t*>(a.workspace) + kAttHead)[i];
-  const int64_t prev = share(h.units, i - 1, h.workers);
-  if (share(h.units, i, h.workers) == f.begin || prev > f.begin) return;
-  // parts: those of workers i - 1 .. the last whose stretch begins within the item
-  int64_t n = (f.end * h.workers + h.units - 1) / h.units;  // share(n) >= end > share(n - 1), or one beyond
-  while (n > i && share(h.units, n - 1, h.workers) >= f.end) --n;
-  n = min(n, h.workers) - (i - 1);
-  const float* parts = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.workspace) +
-                                                      att_parts_at(a.ctas * S::kWarps));
-  // worker i - 1 holds its part second, unless its stretch begins with the item
-  const float* head_part = parts + ((i - 1) * 2 + (prev < f.begin ? 1 : 0)) * S::kPart;
-  const float* rest = parts + i * 2 * S::kPart;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
-  for (int k = blockIdx.y; k < S::kSlices; k += gridDim.y) {
-    const int tile = k / PER, r = 8 * tile + g;
-    float top = kNoMax, z = 0.0f;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    constexpr int B = 4;
-    for (int64_t j = warp; j < n; j += kJoinWarps * B) {
-      float m[B], l[B];
-      float4 x[B];
-#pragma unroll
-      for (int b = 0; b < B; ++b) {
-        const int64_t jj = j + b * kJoinWarps;
-        m[b] = kNoMax;
-        l[b] = 0.0f;
-        x[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (jj < n) {
-          const float* p = jj == 0 ? head_part : rest + (jj - 1) * 2 * S::kPart;
-          m[b] = p[S::kRows * DC + r];
-          l[b] = p[S::kRows * DC + S::kRows + r];
-          x[b] = *reinterpret_cast<const float4*>(p + k * 128 + lane * 4);
-        }
-      }
-      float now = top;
-#pragma unroll
-      for (int b = 0; b < B; ++b) now = fmaxf(now, m[b]);
-      const float e0 = exp2f(top - now);
-      top = now;
-      z *= e0;
-      v.x *= e0, v.y *= e0, v.z *= e0, v.w *= e0;
-#pragma unroll
-      for (int b = 0; b < B; ++b) {
-        const float e = exp2f(m[b] - now);
-        z = fmaf(l[b], e, z);
-        v.x = fmaf(x[b].x, e, v.x), v.y = fmaf(x[b].y, e, v.y), v.z = fmaf(x[b].z, e, v.z), v.w = fmaf(x[b].w, e, v.w);
-      }
-    }
+  AttFirst f;
+  if (!split_at(a, h, i, f)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Split s = split_of<DC, NM>(a, h, i, f, lane);
+#pragma unroll 2
+  for (int k = warp; k < AttShape<DC, NM>::kSlices; k += kJoinWarps) {
+    float top, z;
+    float4 v;
+    join_parts<DC, NM>(s, k, lane, 0, 1, top, z, v);
+    join_out<DC, NM>(a, s, k, lane, top, z, v);
+  }
+}
+
+// Few items, many parts: CTA (i, slice) looks at 32 records; its warps share the parts.
+constexpr int kJoinFewWarps = 8;
+template <int DC, int NM>
+__global__ void __launch_bounds__(32 * kJoinFewWarps) attend_join_few_kernel(const __grid_constant__ AttendArgs a) {
+  __shared__ float4 sums[kJoinFewWarps][32];
+  __shared__ float2 tops[kJoinFewWarps][32];
+  pdl_wait();
+  pdl_trigger();
+  const AttHeader h = *reinterpret_cast<const AttHeader*>(a.workspace);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = blockIdx.y;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * 32 + 1;
+  AttFirst mine;
+  uint32_t todo = __ballot_sync(0xffffffffu, split_at(a, h, first + lane, mine));
+  for (; todo; todo &= todo - 1) {
+    const int64_t i = first + __ffs(todo) - 1;
+    AttFirst f;
+    split_at(a, h, i, f);
+    const Split s = split_of<DC, NM>(a, h, i, f, lane);
+    float top, z;
+    float4 v;
+    join_parts<DC, NM>(s, slice, lane, warp, kJoinFewWarps, top, z, v);
     sums[warp][lane] = v;
     tops[warp][lane] = make_float2(top, z);
     __syncthreads();
     if (warp == 0) {
-      for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, tops[w][lane].x);
+#pragma unroll
+      for (int w = 1; w < kJoinFewWarps; ++w) top = fmaxf(top, tops[w][lane].x);
       v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       z = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) {
+      for (int w = 0; w < kJoinFewWarps; ++w) {
         const float2 t = tops[w][lane];
         const float4 x = sums[w][lane];
-        const float e = exp2f(t.x - top);
+        const float e = exp2_fast(t.x - top);
         z = fmaf(t.y, e, z);
         v.x = fmaf(x.x, e, v.x), v.y = fmaf(x.y, e, v.y), v.z = fmaf(x.z, e, v.z), v.w = fmaf(x.w, e, v.w);
       }
-      const int s = k % PER, d = (2 * c4 + s / (UB / 4) % 2 + 8 * (s / (UB / 2))) * UB + s % (UB / 4) * 4;
-      int t, head;
-      if (row_of(a, f.t0, f.n, f.hs, r, t, head)) {
-        const float inv = z == 0.0f ? 0.0f : 1.0f / z;
-        if (d < a.c.dim)
-          write_out(a, t * a.ld_dst + static_cast<int64_t>(head) * a.c.dim + d,
-                    make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-        if (d == 0 && a.lse)
-          a.lse[static_cast<int64_t>(t) * a.q_heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * 0.693147181f;
-      }
+      join_out<DC, NM>(a, s, slice, lane, top, z, v);
     }
     __syncthreads();
   }
-  static_assert(UC * 2 * (UB / 4) == PER, "slices of a row tile: unit, column parity, four dims");
 }
 
 // ------------------------------------------------------------------ host
@@ -745,7 +871,19 @@ int64_t attend_workspace_bytes(int dim, int tiles, int ctas) {
 
 int attend_ctas(int, int, int sms) { return 2 * sms; }
 
-template <int DC, int FMT, int NM>
+template <int DC, bool EXACT, int FMT, int NM>
+static int launch_part(cudaLaunchConfig_t& cfg, const AttendArgs& a) {
+  using S = AttShape<DC, NM>;
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(attend_kernel<DC, EXACT, FMT, NM>));
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
+  cfg.blockDim = dim3(32 * S::kWarps);
+  cfg.dynamicSmemBytes = S::kSmem;
+  return cudaLaunchKernelEx(&cfg, attend_kernel<DC, EXACT, FMT, NM>, a);
+}
+
+template <int DC, int NM>
 static int launch_attend_t(const AttendArgs& a, cudaStream_t st, bool pdl) {
   using S = AttShape<DC, NM>;
   cudaLaunchConfig_t cfg = {};
@@ -755,31 +893,26 @@ static int launch_attend_t(const AttendArgs& a, cudaStream_t st, bool pdl) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  if (a.phase == ATT_JOIN) {
-    // Few items have many parts each: their slices spread over CTAs.
-    const int64_t items = static_cast<int64_t>(a.T) * a.c.heads * a.subs;
-    cfg.gridDim = dim3(static_cast<unsigned>(a.ctas * S::kWarps - 1), items <= 64 ? 8 : 2);
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    return cudaLaunchKernelEx(&cfg, attend_join_kernel<DC, NM>, a);
+  if (a.phase == ATT_PART) {
+    if (a.c.dim == DC)
+      return a.c.format == 0 ? launch_part<DC, true, 0, NM>(cfg, a) : launch_part<DC, true, 1, NM>(cfg, a);
+    return a.c.format == 0 ? launch_part<DC, false, 0, NM>(cfg, a) : launch_part<DC, false, 1, NM>(cfg, a);
   }
-  static SmemLimit limit;
-  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(attend_kernel<DC, FMT, NM>));
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
-  cfg.blockDim = dim3(32 * S::kWarps);
-  cfg.dynamicSmemBytes = S::kSmem;
-  return cudaLaunchKernelEx(&cfg, attend_kernel<DC, FMT, NM>, a);
-}
-
-template <int DC, int NM>
-static int launch_attend_f(const AttendArgs& a, cudaStream_t st, bool pdl) {
-  return a.c.format == 0 ? launch_attend_t<DC, 0, NM>(a, st, pdl) : launch_attend_t<DC, 1, NM>(a, st, pdl);
+  const unsigned records = static_cast<unsigned>(a.ctas * S::kWarps - 1);  // of workers behind the first
+  if (static_cast<int64_t>(a.T) * a.c.heads * a.subs <= 64) {
+    cfg.gridDim = dim3((records + 31) / 32, S::kSlices);
+    cfg.blockDim = dim3(32 * kJoinFewWarps);
+    return cudaLaunchKernelEx(&cfg, attend_join_few_kernel<DC, NM>, a);
+  }
+  cfg.gridDim = dim3(records);
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel<DC, NM>, a);
 }
 
 int launch_attend(const AttendArgs& a, cudaStream_t st, bool pdl) {
-  if (a.c.dim <= 64) return a.tiles == 1 ? launch_attend_f<64, 1>(a, st, pdl) : launch_attend_f<64, 2>(a, st, pdl);
-  if (a.c.dim <= 128) return a.tiles == 1 ? launch_attend_f<128, 1>(a, st, pdl) : launch_attend_f<128, 2>(a, st, pdl);
-  return launch_attend_f<256, 1>(a, st, pdl);
+  if (a.c.dim <= 64) return a.tiles == 1 ? launch_attend_t<64, 1>(a, st, pdl) : launch_attend_t<64, 2>(a, st, pdl);
+  if (a.c.dim <= 128) return a.tiles == 1 ? launch_attend_t<128, 1>(a, st, pdl) : launch_attend_t<128, 2>(a, st, pdl);
+  return launch_attend_t<256, 1>(a, st, pdl);
 }
 
 }  // namespace gf
