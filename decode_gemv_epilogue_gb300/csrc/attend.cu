@@ -1,8 +1,9 @@
 // Attention of a decode step over the 8-bit cache (gf_attend).
 //
 // One pass over a row's keys and values with the running maximum and sum of the softmax.  What bounds it
-// is reading the codes, so they go straight from memory to the registers that feed the matrix
-// instructions: each lane copies (cp.async) just the bytes that it decodes itself, into slots of its own.
+// is reading the codes: each warp copies (cp.async) chunks of CT tokens, whole lines of consecutive addresses, into
+// stages of its own, a chunk ahead.  (Copies of just the bytes that a lane decodes itself, in fours of rows, left
+// the memory at 5.0 TB/s where consecutive ones reach 6.4.)
 //
 // A warp takes a chunk of CT tokens.  m16n8k16 with the queries as the 16 rows: eight rows' f16 high parts and
 // the same rows' low parts (q = hi + lo to 22 bits under a power of two a row), so that one instruction
@@ -10,8 +11,8 @@
 // over dims and the order of the tokens are free, so that
 //   keys  : lane (g, c) takes 16-byte units c, c + 4, .. of token g; the four bytes of a word are the
 //           two k pairs of one instruction;
-//   values: lane (g, c) takes unit g of the four tokens that its k indices mean; the bytes of four
-//           tokens' words are paired by dim, and dim j of unit g is column g of instruction j.
+//   values: lane (g, c) takes a unit of the four tokens that its k indices mean; the bytes of four
+//           tokens' words are paired by dim, and dim j of column g's unit is column g of instruction j.
 // The weights p * scale_v are split into hi + lo like the queries.  A chunk's products are added to the
 // running ones in 32 bits, outside the matrix unit (which truncates).
 //
@@ -27,18 +28,20 @@
 
 namespace gf {
 
+// Warps of a CTA, two of which share an SM: as many as the registers allow (NM: tiles of eight rows).
+__host__ __device__ constexpr int att_warps(int dc, int nm) { return dc <= 128 && nm == 1 ? 6 : 4; }
+
 template <int DC, int NM>
 struct AttShape {
   static constexpr int kTokens = DC == 256 ? 16 : 32;               // of a chunk
   static constexpr bool kQRegs = DC <= 128 && NM == 1;              // queries in registers, else in shared memory
-  static constexpr int kWarps = kQRegs ? 6 : 4;
+  static constexpr int kWarps = att_warps(DC, NM);
   static constexpr int kRows = 8 * NM;
   static constexpr int kSteps = DC / 16;                            // instructions along the dims
-  static constexpr int kScaleAt = 2 * kTokens * DC;                 // of a stage: keys, values, scales
-  static constexpr int kStage = kScaleAt + 2 * kTokens * 4;
-  static constexpr int kStages = 2;
-  static constexpr int kWarpBytes = kStages * kStage + (kQRegs ? 0 : NM * kSteps * 512);
-  static constexpr int kSmem = kWarps * kWarpBytes;
+  static constexpr int kStage = kTokens * DC;                       // a chunk's keys or values; two of each
+  static constexpr int kScalesAt = kWarps * 4 * kStage;             // of all warps: keys' and values' scales
+  static constexpr int kQueriesAt = kScalesAt + kWarps * 8 * kTokens;
+  static constexpr int kSmem = kQueriesAt + (kQRegs ? 0 : kWarps * NM * kSteps * 512);
   static constexpr int kSlices = kRows * DC / 128;                  // float4 a lane of a row part
   static constexpr int64_t kPart = kRows * (DC + 2);                // floats: sums, maxima, sums of weights
 };
@@ -46,18 +49,42 @@ template <int DC>
 constexpr int kUnitBytes = DC == 64 ? 8 : 16;  // of a value row, in a lane's hands
 
 constexpr float kNoMax = -1e30f;   // running maximum of a row without keys
-constexpr float kHidden = -1.0f;   // scale of a token that no row sees (stored ones are positive, or NaN)
 constexpr uint32_t kWeightBits = 8;     // weights times the largest scale reach 2^8 (f16 parts)
+
+// A stage is lines of 128 bytes (two tokens of 64, half a token of 256) whose 16-byte units are exchanged by
+// the line's number.  Unit u of token r of a chunk:
+template <int DC>
+__device__ __forceinline__ uint32_t smem_place(int r, int u) {
+  const int line = r * (DC / 64) / 2 + (DC == 256 ? u >> 3 : 0), at = DC == 64 ? (r & 1) * 4 + u : u & 7;
+  return line * 128 + ((at ^ (line & 7)) * 16);
+}
+// The same eight tokens n times further on (from an offset within the first eight).
+template <int DC>
+__device__ __forceinline__ uint32_t further(uint32_t place, int n) {
+  return (DC == 64 && n % 2 ? place ^ 64u : place) + n * 8 * DC;
+}
+
+// The token of eight that is column n of the instructions, and the unit of values that is column g (DC 64: half
+// units): chosen so that lanes which read together meet all banks.  They read keys as units c .. c + 3 of
+// columns 2p and 2p + 1, values as two units of columns 0, 2, 4, 6 or 1, 3, 5, 7.
+template <int DC>
+__device__ __forceinline__ int token_of(int n) {
+  constexpr uint32_t order = DC == 64 ? 0x65742130u : DC == 128 ? 0x73625140u : 0x53427160u;
+  return order >> 4 * n & 7;
+}
+template <int DC>
+__device__ __forceinline__ int column_of(int token) {
+  constexpr uint32_t order = DC == 64 ? 0x57641320u : DC == 128 ? 0x75316420u : 0x31756420u;
+  return order >> 4 * token & 7;
+}
+template <int DC>
+__device__ __forceinline__ int value_unit(int g) {
+  return DC == 128 ? (g >> 1) | (g & 1) << 2 : g;
+}
 
 // ------------------------------------------------------------------ small pieces
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -90,18 +117,24 @@ __device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Bytes (0, 1) and (2, 3) of a word of codes as pairs of f16.  i8: 1024 + (code + 128) is an f16 whose
-// low byte is the code, less 1152.
+// A word's four codes as two pairs of f16: bytes 0 and kSecond, and the others.  i8: 1024 + (code + 128) is an
+// f16 whose low byte is the code's with its top bit turned, less 1152.
+template <int FMT>
+constexpr int kSecond = FMT == 0 ? 2 : 1;
 template <int FMT>
 __device__ __forceinline__ void pairs_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (FMT == 0) {
-    w ^= 0x80808080u;
-    lo = h2_sub(__byte_perm(w, 0x64646464u, 0x4140), 0x64806480u);
-    hi = h2_sub(__byte_perm(w, 0x64646464u, 0x4342), 0x64806480u);
+    lo = h2_sub((w & 0x00ff00ffu) ^ 0x64806480u, 0x64806480u);
+    hi = h2_sub((w >> 8 & 0x00ff00ffu) ^ 0x64806480u, 0x64806480u);
   } else {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<uint16_t>(w)));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(w >> 16)));
   }
+}
+// Dims 0, 1 (and 2, 3) of two tokens' words as such a word: the pairs are then a dim's two tokens.
+template <int FMT>
+__device__ __forceinline__ uint32_t weave(uint32_t a, uint32_t b, bool upper) {
+  return FMT == 0 ? __byte_perm(a, b, upper ? 0x7632 : 0x5410) : __byte_perm(a, b, upper ? 0x7362 : 0x5140);
 }
 
 __device__ __forceinline__ float quad_max(float v) {
@@ -117,7 +150,8 @@ __device__ __forceinline__ float quad_sum(float v) {
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(a, b);
   const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+  const float2 r = fsub2(make_float2(a, b), f);
+  const __half2 l = __floats2half2_rn(r.x, r.y);
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
@@ -243,6 +277,7 @@ __device__ __forceinline__ bool row_of(const AttendArgs& a, int t0, int n, int h
 }
 
 // ------------------------------------------------------------------ the kernel
+// EXACT: heads of DC elements, else of fewer (a multiple of 16).
 template <int DC, bool EXACT, int FMT, int NM>
 __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kernel(const __grid_constant__ AttendArgs a) {
   using S = AttShape<DC, NM>;
@@ -250,7 +285,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
   constexpr int UC = DC == 256 ? 2 : 1;       // units of a value row that a lane holds
   constexpr int UB = kUnitBytes<DC>;
   constexpr int NO = DC / 8;                  // column tiles of the output
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t group_units[kAttMaxTokens / 32];  // of 32 tokens each, for one (head, part)
   pdl_wait();
   pdl_trigger();
@@ -276,7 +311,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
   if (me >= workers) return;
   AttHeader head;
   head.workers = workers;
-  head.each = total / workers;
+  head.each = total >> 32 ? total / workers : static_cast<uint32_t>(total) / static_cast<uint32_t>(workers);
   head.more = total - head.each * workers;
   const int64_t start = share(head, me), stop = share(head, me + 1);
   Item item;
@@ -304,120 +339,102 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
     item.begin = b + static_cast<int64_t>(item.hs) * (item.chunks + 1);
   }
   if (lane == 0) {
-    if (me == 0) {
-      *reinterpret_cast<AttHeader*>(a.workspace) = head;
-    }
+    if (me == 0) *reinterpret_cast<AttHeader*>(a.workspace) = head;
     AttFirst f = {item.begin, item.begin + item.chunks + 1, item.t0, item.n, item.hs, 0};
     reinterpret_cast<AttFirst*>(reinterpret_cast<uint8_t*>(a.workspace) + kAttHead)[me] = f;
   }
   float* parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.workspace) + att_parts_at(a.ctas * W)) +
                  me * 2 * S::kPart;
 
-  uint8_t* ring = smem + warp * S::kWarpBytes;
+  uint8_t* ring = smem + warp * 4 * S::kStage;
   const uint32_t ring_at = smem_u32(ring);
-  uint8_t* qs = ring + S::kStages * S::kStage;
+  float* ring_scales = reinterpret_cast<float*>(smem + S::kScalesAt) + warp * 2 * CT;
+  uint8_t* qs = smem + S::kQueriesAt + warp * NM * KS * 512;
 
-  // The pages of a chunk's 16-token halves, as the table has them (-1: outside the table).
+  const int page_log2 = a.c.page_log2, page_mask = (1 << page_log2) - 1, table_ld = static_cast<int>(a.c.table_ld);
+  const int64_t page_bytes = static_cast<int64_t>(a.c.heads * D) << page_log2;
+  const int64_t page_scales = static_cast<int64_t>(a.c.heads) << (page_log2 - a.c.block_log2);
+  const bool one_page = CT == 16 || page_log2 >= 5;  // a chunk never crosses a page's end
+  const int unit_inv = 65536 / U16 + 1;              // n / U16 = n * unit_inv >> 16 for n < CT * 16
+  const int scale_lane = (lane & ~7) + column_of<DC>(lane & 7);  // scales lie in the order of the columns
+  // where a lane's copies go, less 512 bytes a copy: repeating after kPlaces
+  constexpr int kPlaces = DC == 256 ? 4 : 2;
+  uint32_t copy_to[kPlaces];
+#pragma unroll
+  for (int k = 0; k < kPlaces; ++k)
+    copy_to[k] = ring_at + smem_place<DC>(lane / (DC / 16) + k * (512 / DC), lane % (DC / 16)) - k * 512;
+
+  // What a chunk's copies need of its item.
+  struct Source {
+    int seq, first, lo, hi, head;  // first: of the item's chunks, among those of its sequence
+  };
+  auto source_of = [&](const Item& it) {
+    return Source{it.seq, it.lo / CT, it.lo, it.hi, it.hs / a.subs};
+  };
   struct Pages {
     int id[KG];
   };
-  auto pages_of = [&](const Item& it, int chunk) {
+  // The pages of a chunk's 16-token halves, as the table has them (-1: outside the table).
+  auto pages_of = [&](const Source& s, int chunk) {
     Pages p;
-#pragma unroll
-    for (int h = 0; h < KG; ++h) {
-      const int64_t i = ((it.lo / CT + chunk) * CT + 16 * h) >> a.c.page_log2;
-      p.id[h] = it.hi > 0 && i < a.c.table_ld ? a.c.table[it.seq * a.c.table_ld + i] : -1;
-    }
+    const int i = (s.first + chunk) * CT >> page_log2;
+    const int32_t* row = a.c.table + s.seq * a.c.table_ld;
+    p.id[0] = s.hi > 0 && i < table_ld ? row[i] : -1;
+    if (KG == 2) p.id[KG - 1] = one_page ? p.id[0] : s.hi > 0 && i + 1 < table_ld ? row[i + 1] : -1;
     return p;
   };
-  const int page_mask = (1 << a.c.page_log2) - 1;
-  const uint32_t k_lane = g * D + c4 * 16, v_lane = 2 * c4 * D + g * UB;  // of a lane's first token and unit
-  // Copies of one chunk of an item into a stage.  Tokens outside [lo, hi) or without a page: zeros under the
-  // scale kHidden.
-  auto fetch = [&](const Item& it, int chunk, const Pages& pages, int stage) {
-    const int p0 = (it.lo / CT + chunk) * CT, head = it.hs / a.subs, slot = p0 & page_mask;
-    const uint32_t to = ring_at + stage * S::kStage, k_to = to + lane * 16, v_to = to + CT * DC + lane * UB;
-    bool held[KG], all = p0 >= it.lo && p0 + CT <= it.hi;
+  float key_scale = 0.0f, value_scale = 0.0f;  // of token `lane` of the chunk fetched last, on their way
+  // Copies a chunk's keys and values into stage chunk % 2.  Tokens outside [lo, hi) or without a page: zeros,
+  // scales and codes.  Returns which tokens of the chunk those are.
+  auto fetch = [&](const Source& s, int chunk, const Pages& pages) {
+    const int p0 = (s.first + chunk) * CT, slot = p0 & page_mask;
+    const uint32_t stage = (chunk & 1) * 2 * S::kStage;
+    const int64_t head_at = static_cast<int64_t>(s.head * D) << page_log2, n_pages = a.c.n_pages;
+    const int64_t head_scales = static_cast<int64_t>(s.head) << (page_log2 - a.c.block_log2);
+    bool held[KG];
 #pragma unroll
-    for (int h = 0; h < KG; ++h) {
-      held[h] = pages.id[h] >= 0 && pages.id[h] < a.c.n_pages;
-      all = all && held[h];
-    }
-    if (all) {
+    for (int h = 0; h < KG; ++h) held[h] = static_cast<uint32_t>(pages.id[h]) < n_pages;
+    uint32_t hidden = 0;
+    key_scale = value_scale = 0.0f;
+    if (EXACT && one_page && held[0] && p0 >= s.lo && p0 + CT <= s.hi) {
+      const int64_t at = pages.id[0] * page_bytes + (head_at + slot * D + lane * 16);
+      const uint8_t* k = a.c.k + at;
+      const uint8_t* v = a.c.v + at;
 #pragma unroll
-      for (int h = 0; h < KG; ++h) {
-        const int64_t at = cache_row(a.c, pages.id[h], head, (slot + 16 * h) & page_mask);
-        const uint8_t* k = a.c.k + at + k_lane;
-        const uint8_t* v = a.c.v + at + v_lane;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int u = 0; u < DC / 64; ++u)
-            if (EXACT || c4 + 4 * u < U16) cp_async16(k_to + ((2 * h + i) * (DC / 64) + u) * 512, k + 8 * i * D + 64 * u, true);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int u = 0; u < UC; ++u)
-            if (EXACT || (g + 8 * u) * UB < D) {
-              const uint32_t dst = v_to + ((4 * h + i) * UC + u) * 32 * UB;
-              const uint8_t* src = v + ((i & 1) + 8 * (i >> 1)) * D + 8 * u * UB;
-              if constexpr (UB == 16)
-                cp_async16(dst, src, true);
-              else
-                cp_async8(dst, src, true);
-            }
+      for (int i = 0; i < CT * DC / 512; ++i) {
+        cp_async16(copy_to[i % kPlaces] + stage + i * 512, k + i * 512, true);
+        cp_async16(copy_to[i % kPlaces] + stage + S::kStage + i * 512, v + i * 512, true);
       }
+      const int64_t sc = pages.id[0] * page_scales + (head_scales + ((slot + (lane & (CT - 1))) >> a.c.block_log2));
+      key_scale = a.c.k_scale[sc];
+      value_scale = a.c.v_scale[sc];
     } else {
-#pragma unroll
-      for (int h = 0; h < KG; ++h) {
-        const int64_t at = held[h] ? cache_row(a.c, pages.id[h], head, (slot + 16 * h) & page_mask) : 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = 8 * i + g, p = p0 + 16 * h + row;
-          const bool on = held[h] && p >= it.lo && p < it.hi;
-#pragma unroll
-          for (int u = 0; u < DC / 64; ++u)
-            if (EXACT || c4 + 4 * u < U16)
-              cp_async16(k_to + ((2 * h + i) * (DC / 64) + u) * 512,
-                         a.c.k + (on ? at + row * D + (c4 + 4 * u) * 16 : 0), on);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = 2 * c4 + (i & 1) + 8 * (i >> 1), p = p0 + 16 * h + row;
-          const bool on = held[h] && p >= it.lo && p < it.hi;
-#pragma unroll
-          for (int u = 0; u < UC; ++u)
-            if (EXACT || (g + 8 * u) * UB < D) {
-              const uint32_t dst = v_to + ((4 * h + i) * UC + u) * 32 * UB;
-              const uint8_t* src = a.c.v + (on ? at + row * D + (g + 8 * u) * UB : 0);
-              if constexpr (UB == 16)
-                cp_async16(dst, src, on);
-              else
-                cp_async8(dst, src, on);
-            }
+#pragma unroll 2
+      for (int i = 0; i < CT * DC / 512; ++i) {
+        const int n = lane + 32 * i, row = n * unit_inv >> 16, u = n - row * U16;
+        if (row < CT) {
+          const bool up = KG == 2 && row >= 16;
+          const bool on = (up ? held[KG - 1] : held[0]) && p0 + row >= s.lo && p0 + row < s.hi;
+          const int64_t at = (up ? pages.id[KG - 1] : pages.id[0]) * page_bytes +
+                             (head_at + ((slot + row) & page_mask) * D + u * 16);
+          const uint32_t to = ring_at + stage + smem_place<DC>(row, u);
+          cp_async16(to, a.c.k + (on ? at : 0), on);
+          cp_async16(to + S::kStage, a.c.v + (on ? at : 0), on);
         }
       }
-    }
-    {
-      const int j = lane & (CT - 1), p = p0 + j;
-      const bool is_v = CT == 16 && lane >= 16, upper = KG == 2 && j >= 16;
-      const int id = upper ? pages.id[KG - 1] : pages.id[0];
-      const bool on = all || ((upper ? held[KG - 1] : held[0]) && p >= it.lo && p < it.hi);
-      float* scales = reinterpret_cast<float*>(ring + stage * S::kStage + S::kScaleAt);
-      const uint32_t dst = to + S::kScaleAt + 4 * lane;
-      if (!on) {
-        scales[lane] = is_v ? 0.0f : kHidden;
-        if (CT == 32) scales[CT + lane] = 0.0f;
-      } else {
-        const int64_t at = cache_scale(a.c, id, head, (slot + j) & page_mask);
-        if (CT == 32) {
-          cp_async4(dst, a.c.k_scale + at);
-          cp_async4(dst + 4 * CT, a.c.v_scale + at);
-        } else {
-          cp_async4(dst, (is_v ? a.c.v_scale : a.c.k_scale) + at);
-        }
+      const int j = lane & (CT - 1);
+      const bool up = KG == 2 && j >= 16;
+      const bool on = (up ? held[KG - 1] : held[0]) && p0 + j >= s.lo && p0 + j < s.hi;
+      hidden = __ballot_sync(0xffffffffu, !on);
+      if (on) {
+        const int64_t sc = (up ? pages.id[KG - 1] : pages.id[0]) * page_scales +
+                           (head_scales + (((slot + j) & page_mask) >> a.c.block_log2));
+        key_scale = a.c.k_scale[sc];
+        value_scale = a.c.v_scale[sc];
       }
     }
+    cp_commit();
+    return hidden;
   };
   // The item's chunks [c0, c1) of this warp's stretch.
   auto stretch = [&](const Item& it, int& c0, int& c1) {
@@ -426,10 +443,11 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
     c1 = to < it.chunks ? static_cast<int>(to) : it.chunks;
   };
 
-  int stage = 0, c0, c1;
+  int c0, c1;
   stretch(item, c0, c1);
-  if (c0 < c1) fetch(item, c0, pages_of(item, c0), 0);
-  cp_commit();
+  Source src = source_of(item);
+  uint32_t hidden_next = c0 < c1 ? fetch(src, c0, pages_of(src, c0)) : 0;
+  Pages pages = pages_of(src, c0 + 1);  // of the chunk that is fetched next: looked up a chunk ahead
 
   for (;;) {
     // ---- the item's queries, hi and lo parts in the order of the instructions' rows: of row g, lane (g, c4)
@@ -471,8 +489,10 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         uint4 h;
-        split2(number ? v[k].x * w : 0.0f, number ? v[k].y * w : 0.0f, h.x, h.y);
-        split2(number ? v[k].z * w : 0.0f, number ? v[k].w * w : 0.0f, h.z, h.w);
+        const float e[4] = {number ? v[k].x * w : 0.0f, number ? v[k].y * w : 0.0f, number ? v[k].z * w : 0.0f,
+                            number ? v[k].w * w : 0.0f};
+        split2(e[0], e[kSecond<FMT>], h.x, h.y);
+        split2(e[3 - kSecond<FMT>], e[3], h.z, h.w);
         if constexpr (S::kQRegs)
           qr[k] = h;
         else
@@ -496,52 +516,71 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
     // biased exponent of the power of two, above every scale so far, that the values' scales are taken by; at
     // least that of the format's smallest scale
     uint32_t vexp = 127 - 111;
+    const int t0 = token_of<DC>(2 * c4), t1 = token_of<DC>(2 * c4 + 1);  // this lane's columns
 
-    Pages pages = pages_of(item, c0 + 1);  // of the chunk that is fetched next, loaded a chunk ahead
     for (int c = c0; c < c1; ++c) {
-      if (c + 1 < c1) fetch(item, c + 1, pages, stage ^ 1);
-      cp_commit();
-      pages = pages_of(item, c + 2);
-      cp_wait<1>();
+      const uint32_t hidden = hidden_next;
+      if (CT == 32 || lane < CT) {
+        ring_scales[scale_lane] = key_scale;
+        ring_scales[CT + scale_lane] = value_scale;
+      }
+      const uint32_t vtop = __reduce_max_sync(0xffffffffu, min(__float_as_uint(value_scale), 0x7e000000u));
+      if (c + 1 < c1) {
+        hidden_next = fetch(src, c + 1, pages);
+        pages = pages_of(src, c + 2);
+        cp_wait<1>();
+      } else {
+        cp_wait<0>();
+      }
       __syncwarp();
-      const uint8_t* st = ring + stage * S::kStage;
-      const float* ks = reinterpret_cast<const float*>(st + S::kScaleAt);
+      const uint8_t* kt = ring + (c & 1) * 2 * S::kStage;
+      const uint8_t* vt = kt + S::kStage;
+      const float* ks = ring_scales;
       const float* vs = ks + CT;
-      const int p0 = (item.lo / CT + c) * CT;
+      const int p0 = (src.first + c) * CT;
 
-      // ---- scores
-      float s[NM][NT][4];
+      // ---- scores (powers of two)
+      float2 x[NM][NT];
+      {
+        float s[NM][NT][4];
 #pragma unroll
-      for (int u = 0; u < DC / 64; ++u) {
-        uint4 q[NM][4];
+        for (int u = 0; u < DC / 64; ++u) {
+          uint4 q[NM][4];
 #pragma unroll
-        for (int i = 0; i < NM; ++i)
+          for (int i = 0; i < NM; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (S::kQRegs)
-              q[i][j] = qr[u * 4 + j];
-            else
-              q[i][j] = *reinterpret_cast<const uint4*>(qs + ((i * KS + u * 4 + j) * 32 + lane) * 16);
+            for (int j = 0; j < 4; ++j) {
+              if constexpr (S::kQRegs)
+                q[i][j] = qr[u * 4 + j];
+              else
+                q[i][j] = *reinterpret_cast<const uint4*>(qs + ((i * KS + u * 4 + j) * 32 + lane) * 16);
+            }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            uint4 w = make_uint4(0, 0, 0, 0);  // a unit that the head does not have
+            if (EXACT || c4 + 4 * u < U16)
+              w = *reinterpret_cast<const uint4*>(kt + further<DC>(smem_place<DC>(token_of<DC>(g), c4 + 4 * u), n));
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t b0, b1;
+              pairs_of<FMT>(ww[j], b0, b1);
+#pragma unroll
+              for (int i = 0; i < NM; ++i) u + j == 0 ? mma0(s[i][n], q[i][j], b0, b1) : mma(s[i][n], q[i][j], b0, b1);
+            }
           }
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          uint4 w = make_uint4(0, 0, 0, 0);  // a unit that the head does not have
-          if (EXACT || c4 + 4 * u < U16)
-            w = *reinterpret_cast<const uint4*>(st + ((n * (DC / 64) + u) * 32 + lane) * 16);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          const float2 k2 = *reinterpret_cast<const float2*>(ks + 8 * n + 2 * c4);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t b0, b1;
-            pairs_of<FMT>(ww[j], b0, b1);
-#pragma unroll
-            for (int i = 0; i < NM; ++i) u + j == 0 ? mma0(s[i][n], q[i][j], b0, b1) : mma(s[i][n], q[i][j], b0, b1);
-          }
+          for (int i = 0; i < NM; ++i)
+            x[i][n] = fmul2(fadd2(make_float2(s[i][n][0], s[i][n][1]), make_float2(s[i][n][2], s[i][n][3])),
+                            fmul2(k2, make_float2(f[i], f[i])));
         }
       }
 
       // ---- softmax; the weights, times the values' scales, as instructions' rows
-      const bool hidden = __any_sync(0xffffffffu, ks[lane & (CT - 1)] < 0.0f);
-      const uint32_t vtop = __reduce_max_sync(0xffffffffu, min(__float_as_uint(vs[lane & (CT - 1)]), 0x7e000000u));
       const uint32_t vnow = max(vexp, (vtop >> 23) + 1);
       // 2^(kWeightBits - (vnow - 127)): weights times it lie below 2^8
       const float vinv = __uint_as_float((254 + kWeightBits - vnow) << 23);
@@ -551,36 +590,35 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
       float alpha[NM];
 #pragma unroll
       for (int i = 0; i < NM; ++i) {
-        float x[NT][2], top = kNoMax;
-        const bool whole = !hidden && p0 >= lo[i] && p0 + CT <= hi[i];
+        const bool whole = hidden == 0 && p0 >= lo[i] && p0 + CT <= hi[i];
+        if (!whole) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float2 k2 = *reinterpret_cast<const float2*>(ks + 8 * n + 2 * c4);
-          x[n][0] = (s[i][n][0] + s[i][n][2]) * (k2.x * f[i]);
-          x[n][1] = (s[i][n][1] + s[i][n][3]) * (k2.y * f[i]);
-          if (!whole) {
-            const int p = p0 + 8 * n + 2 * c4;
-            if (k2.x < 0.0f || p < lo[i] || p >= hi[i]) x[n][0] = -INFINITY;
-            if (k2.y < 0.0f || p + 1 < lo[i] || p + 1 >= hi[i]) x[n][1] = -INFINITY;
+          for (int n = 0; n < NT; ++n) {
+            const int j0 = 8 * n + t0, j1 = 8 * n + t1;
+            if ((hidden >> j0 & 1) || p0 + j0 < lo[i] || p0 + j0 >= hi[i]) x[i][n].x = -INFINITY;
+            if ((hidden >> j1 & 1) || p0 + j1 < lo[i] || p0 + j1 >= hi[i]) x[i][n].y = -INFINITY;
           }
-          top = fmaxf(top, fmaxf(x[n][0], x[n][1]));
         }
+        float top = kNoMax;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) top = fmaxf(top, fmaxf(x[i][n].x, x[i][n].y));
         top = fmaxf(m[i], quad_max(top));
         alpha[i] = exp2_fast(m[i] - top);
         m[i] = top;
-        float sum = 0.0f;
+        float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float2 v2 = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c4);
-          const float p = exp2_fast(x[n][0] - top), q = exp2_fast(x[n][1] - top);
-          sum += p + q;
-          float y = p * (v2.x * vinv), z = q * (v2.y * vinv);
+          const float2 e = fsub2(x[i][n], make_float2(top, top));
+          const float2 p = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+          sum = fadd2(sum, p);
+          float2 y = fmul2(p, fmul2(v2, make_float2(vinv, vinv)));
           if (!whole) {  // a masked token's weight is zero whatever lies in its scale
-            if (x[n][0] == -INFINITY) y = 0.0f;
-            if (x[n][1] == -INFINITY) z = 0.0f;
+            if (x[i][n].x == -INFINITY) y.x = 0.0f;
+            if (x[i][n].y == -INFINITY) y.y = 0.0f;
           }
           uint32_t h, w;
-          split2(y, z, h, w);
+          split2(y.x, y.y, h, w);
           if (n % 2 == 0) {
             pf[i][n / 2].x = h;
             pf[i][n / 2].y = w;
@@ -589,7 +627,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
             pf[i][n / 2].w = w;
           }
         }
-        l[i] = l[i] * alpha[i] + sum;
+        l[i] = l[i] * alpha[i] + (sum.x + sum.y);
         alpha[i] *= vstep;
       }
 
@@ -601,7 +639,10 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
         for (int k = 0; k < KG; ++k)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint8_t* at = st + CT * DC + (((4 * k + i) * UC + u) * 32 + lane) * UB;
+            // this lane's unit of the tokens that are its k indices: columns 2 c4 and 2 c4 + 1 of two eights
+            const int t = i % 2 ? t1 : t0;
+            const uint8_t* at = vt + further<DC>(DC == 64 ? smem_place<DC>(t, g >> 1) + (g & 1) * 8
+                                                          : smem_place<DC>(t, value_unit<DC>(g) + 8 * u), 2 * k + i / 2);
             if constexpr (UB == 16) {
               const uint4 w = *reinterpret_cast<const uint4*>(at);
               raw[k][i][0] = w.x, raw[k][i][1] = w.y, raw[k][i][2] = w.z, raw[k][i][3] = w.w;
@@ -616,10 +657,10 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 #pragma unroll
           for (int k = 0; k < KG; ++k) {
             uint32_t b0[4], b1[4];
-            pairs_of<FMT>(__byte_perm(raw[k][0][w], raw[k][1][w], 0x5140), b0[0], b0[1]);
-            pairs_of<FMT>(__byte_perm(raw[k][0][w], raw[k][1][w], 0x7362), b0[2], b0[3]);
-            pairs_of<FMT>(__byte_perm(raw[k][2][w], raw[k][3][w], 0x5140), b1[0], b1[1]);
-            pairs_of<FMT>(__byte_perm(raw[k][2][w], raw[k][3][w], 0x7362), b1[2], b1[3]);
+            pairs_of<FMT>(weave<FMT>(raw[k][0][w], raw[k][1][w], false), b0[0], b0[1]);
+            pairs_of<FMT>(weave<FMT>(raw[k][0][w], raw[k][1][w], true), b0[2], b0[3]);
+            pairs_of<FMT>(weave<FMT>(raw[k][2][w], raw[k][3][w], false), b1[0], b1[1]);
+            pairs_of<FMT>(weave<FMT>(raw[k][2][w], raw[k][3][w], true), b1[2], b1[3]);
 #pragma unroll
             for (int i = 0; i < NM; ++i)
 #pragma unroll
@@ -636,15 +677,13 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
             }
         }
       }
-      stage ^= 1;
-      __syncwarp();
+      __syncwarp();  // the stage and the scales may be written again
     }
 
     // ---- the next item's first chunk starts on its way
     const int64_t end = item.begin + item.chunks + 1;
     const bool last = end >= stop;
     Item next = item;
-    int n0 = 0, n1 = 0;
     if (!last) {
       if (item.hs + 1 < HS) {
         ++next.hs;
@@ -654,10 +693,11 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
         while (!item_at<CT>(a, t, next) && t < a.T - 1) ++t;  // (the token behind an item begins one)
       }
       next.begin = end;
-      stretch(next, n0, n1);
-      if (n0 < n1) fetch(next, n0, pages_of(next, n0), stage);
+      stretch(next, c0, c1);
+      src = source_of(next);
+      if (c0 < c1) hidden_next = fetch(src, c0, pages_of(src, c0));
+      pages = pages_of(src, c0 + 1);
     }
-    cp_commit();
 
     // ---- results, or a part for the joining launch
     const bool split = start > item.begin || end > stop;
@@ -675,7 +715,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int n = 0; n < UB; n += 4) {
-            const int d = (2 * c4 + e + 8 * u) * UB + n;
+            const int d = (value_unit<DC>(2 * c4 + e) + 8 * u) * UB + n;
             const float2* x = &o[i][u * UB + n];
             const float4 v = e == 0 ? make_float4(x[0].x * inv, x[1].x * inv, x[2].x * inv, x[3].x * inv)
                                     : make_float4(x[0].y * inv, x[1].y * inv, x[2].y * inv, x[3].y * inv);
@@ -695,10 +735,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
     }
     if (last) break;
     item = next;
-    c0 = n0;
-    c1 = n1;
   }
-  cp_wait<0>();
 }
 
 // An item that reaches over warps' stretches, as the joining launch finds it at the record of the first
@@ -788,7 +825,7 @@ __device__ __forceinline__ void join_out(const AttendArgs& a, const Split& s, in
   constexpr int UB = kUnitBytes<DC>, PER = S::kSlices / NM;  // slices of eight rows: unit, column parity, four dims
   static_assert((DC == 256 ? 2 : 1) * 2 * (UB / 4) == PER, "as the parts are laid out");
   const int k = slice % PER, r = 8 * (slice / PER) + (lane >> 2);
-  const int d = (2 * (lane & 3) + k / (UB / 4) % 2 + 8 * (k / (UB / 2))) * UB + k % (UB / 4) * 4;
+  const int d = (value_unit<DC>(2 * (lane & 3) + k / (UB / 4) % 2) + 8 * (k / (UB / 2))) * UB + k % (UB / 4) * 4;
   int t, head;
   if (!row_of(a, s.f.t0, s.f.n, s.f.hs, r, t, head)) return;
   const float inv = z == 0.0f ? 0.0f : 1.0f / z;
@@ -865,7 +902,7 @@ __global__ void __launch_bounds__(32 * kJoinFewWarps) attend_join_few_kernel(con
 // ------------------------------------------------------------------ host
 int64_t attend_workspace_bytes(int dim, int tiles, int ctas) {
   const int dc = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
-  const int64_t workers = static_cast<int64_t>(ctas) * (dc <= 128 && tiles == 1 ? 6 : 4);
+  const int64_t workers = static_cast<int64_t>(ctas) * att_warps(dc, tiles);
   return att_parts_at(static_cast<int>(workers)) + workers * 2 * 8 * tiles * (dc + 2) * 4;
 }
 
