@@ -17,11 +17,12 @@
 // running ones in 32 bits, outside the matrix unit (which truncates).
 //
 // Items, (tokens of a sequence next to each other, head of the cache, part of its queries), are laid end
-// to end by their number of chunks and one more for their start and end, and every warp takes an equal
-// stretch, whatever the sequences' lengths.  Warps know nothing of each other: the parts of an item that reaches over
-// several go through the workspace, and a second launch joins them in order.  (A CTA to an item, its warps joined in
-// shared memory, took 152 us where this takes XX for 61 sequences of 100 to 8000 keys: short ones cost it
-// a barrier's round each.)
+// to end by their number of chunks and one more for their start and end; every CTA takes an equal stretch
+// and every warp an equal stretch of that, whatever the sequences' lengths.  Warps know nothing of each other
+// until they are done: the parts of an item that reaches over several go through the workspace, where the CTA
+// joins its own and a second launch joins the CTAs', both in order.  (A CTA to an item, its warps joined in shared
+// memory at each one's end, took twice as long for 61 sequences of 100 to 8000 keys: short ones cost it a
+// barrier's round each.)
 #include "cache_device.cuh"
 #include "gf_device.cuh"
 #include "rope_device.cuh"
@@ -117,15 +118,31 @@ __device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// Constants that the conversion wants in registers: with immediates it takes five instructions a word, not
+// three (the inner loop's arithmetic units were busy 56% of the time with them).
+struct Magic {
+  uint32_t mask, turn;
+  __device__ __forceinline__ Magic() {
+    asm volatile("mov.b32 %0, 0x00ff00ff;" : "=r"(mask));
+    asm volatile("mov.b32 %0, 0x64806480;" : "=r"(turn));
+  }
+};
+
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
 // A word's four codes as two pairs of f16: bytes 0 and kSecond, and the others.  i8: 1024 + (code + 128) is an
 // f16 whose low byte is the code's with its top bit turned, less 1152.
 template <int FMT>
 constexpr int kSecond = FMT == 0 ? 2 : 1;
 template <int FMT>
-__device__ __forceinline__ void pairs_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
+__device__ __forceinline__ void pairs_of(const Magic& k, uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (FMT == 0) {
-    lo = h2_sub((w & 0x00ff00ffu) ^ 0x64806480u, 0x64806480u);
-    hi = h2_sub((w >> 8 & 0x00ff00ffu) ^ 0x64806480u, 0x64806480u);
+    lo = h2_sub(and_xor(w, k.mask, k.turn), k.turn);
+    hi = h2_sub(and_xor(w >> 8, k.mask, k.turn), k.turn);
   } else {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<uint16_t>(w)));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(w >> 16)));
@@ -219,20 +236,24 @@ __device__ __forceinline__ bool item_at(const AttendArgs& a, int t, Item& it) {
   return true;
 }
 
-// Workspace: a header, a record of each warp's first item, then each warp's two parts.
+// Workspace: a header, a record of each CTA's first item, each CTA's two parts, each warp's two parts.
 struct AttHeader {
-  int64_t workers;
-  int64_t each, more;  // units of a worker; the first `more` take one more
+  int64_t ctas;
+  int64_t each, more;  // units of a CTA; the first `more` take one more
 };
-struct AttFirst {
-  int64_t begin, end;
+struct AttSpan {       // an item as the joining needs it
+  int64_t begin, end;  // units
   int t0, n, hs, pad;
 };
 constexpr int kAttHead = 64;
-__host__ __device__ constexpr int64_t att_parts_at(int workers) { return kAttHead + static_cast<int64_t>(workers) * 32; }
+__host__ __device__ constexpr int64_t att_parts_at(int ctas) { return kAttHead + static_cast<int64_t>(ctas) * 32; }
 
-// Unit at which worker i begins.
+// Unit at which CTA i begins.
 __device__ __forceinline__ int64_t share(const AttHeader& h, int64_t i) { return i * h.each + (i < h.more ? i : h.more); }
+
+__device__ __forceinline__ AttSpan span_of(const Item& it) {
+  return AttSpan{it.begin, it.begin + it.chunks + 1, it.t0, it.n, it.hs, 0};
+}
 
 template <int CT>
 __device__ __forceinline__ uint32_t units_at(const AttendArgs& a, int t) {
@@ -276,6 +297,35 @@ __device__ __forceinline__ bool row_of(const AttendArgs& a, int t0, int n, int h
   return i < n && in_group < a.group;
 }
 
+// A part's place, if there is one, added to a running maximum, sum of weights and sums.
+__device__ __forceinline__ void join_part(bool on, const float* part, int max_at, int rows, int sums_at, float& top, float& z,
+                                          float4& v) {
+  const float m = on ? __ldcg(part + max_at) : kNoMax, l = on ? __ldcg(part + max_at + rows) : 0.0f;
+  const float4 x = on ? __ldcg(reinterpret_cast<const float4*>(part + sums_at)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float now = fmaxf(top, m), e0 = exp2_fast(top - now), e = exp2_fast(m - now);
+  top = now;
+  z = fmaf(l, e, z * e0);
+  v.x = fmaf(x.x, e, v.x * e0), v.y = fmaf(x.y, e, v.y * e0);
+  v.z = fmaf(x.z, e, v.z * e0), v.w = fmaf(x.w, e, v.w * e0);
+}
+
+// A slice's place of a joined item as output.
+template <int DC, int NM>
+__device__ __forceinline__ void join_out(const AttendArgs& a, const AttSpan& s, int slice, int lane, float top, float z, float4 v) {
+  using S = AttShape<DC, NM>;
+  constexpr int UB = kUnitBytes<DC>, PER = S::kSlices / NM;  // slices of eight rows: unit, column parity, four dims
+  static_assert((DC == 256 ? 2 : 1) * 2 * (UB / 4) == PER, "as the parts are laid out");
+  const int k = slice % PER, r = 8 * (slice / PER) + (lane >> 2);
+  const int d = (value_unit<DC>(2 * (lane & 3) + k / (UB / 4) % 2) + 8 * (k / (UB / 2))) * UB + k % (UB / 4) * 4;
+  int t, head;
+  if (!row_of(a, s.t0, s.n, s.hs, r, t, head)) return;
+  const float inv = z == 0.0f ? 0.0f : 1.0f / z;  // no keys: zeros
+  if (d < a.c.dim)
+    write_out(a, t * a.ld_dst + static_cast<int64_t>(head) * a.c.dim + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+  if (d == 0 && a.lse)
+    a.lse[static_cast<int64_t>(t) * a.q_heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * 0.693147181f;
+}
+
 // ------------------------------------------------------------------ the kernel
 // EXACT: heads of DC elements, else of fewer (a multiple of 16).
 template <int DC, bool EXACT, int FMT, int NM>
@@ -287,9 +337,11 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
   constexpr int NO = DC / 8;                  // column tiles of the output
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t group_units[kAttMaxTokens / 32];  // of 32 tokens each, for one (head, part)
+  __shared__ AttSpan spans[W][2];                       // the items of the warps' parts
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c4 = lane & 3;
+  const Magic magic;
   const int HS = a.c.heads * a.subs;
   const int D = EXACT ? DC : a.c.dim, U16 = D / 16;
 
@@ -305,15 +357,21 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   total *= HS;
-  // two units each at least; neighbours among the workers lie on different SMs
-  const int64_t workers = min(static_cast<int64_t>(a.ctas) * W, (total + 1) / 2);
-  const int64_t me = static_cast<int64_t>(warp) * a.ctas + blockIdx.x;
-  if (me >= workers) return;
+  // a CTA takes one unit a warp at least
   AttHeader head;
-  head.workers = workers;
-  head.each = total >> 32 ? total / workers : static_cast<uint32_t>(total) / static_cast<uint32_t>(workers);
-  head.more = total - head.each * workers;
-  const int64_t start = share(head, me), stop = share(head, me + 1);
+  head.ctas = min(static_cast<int64_t>(a.ctas), (total + W - 1) / W);
+  if (blockIdx.x >= head.ctas) return;
+  head.each = total >> 32 ? total / head.ctas : static_cast<uint32_t>(total) / static_cast<uint32_t>(head.ctas);
+  head.more = total - head.each * head.ctas;
+  const int64_t cta_start = share(head, blockIdx.x), cta_units = share(head, blockIdx.x + 1) - cta_start;
+  const int64_t start = cta_start + cta_units * warp / W, stop = cta_start + cta_units * (warp + 1) / W;
+  float* cta_parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.workspace) + att_parts_at(a.ctas)) +
+                     static_cast<int64_t>(blockIdx.x) * 2 * S::kPart;
+  float* warp_parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.workspace) + att_parts_at(a.ctas)) +
+                      (static_cast<int64_t>(a.ctas) + static_cast<int64_t>(blockIdx.x) * W) * 2 * S::kPart;
+  if (lane < 2) spans[warp][lane].end = 0;  // no part
+  __syncwarp();
+  if (start < stop) {
   Item item;
   {
     int64_t before = 0;  // units of one (head, part) ahead of the group
@@ -338,14 +396,10 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
     item.hs = static_cast<int>((start - b) / (item.chunks + 1));
     item.begin = b + static_cast<int64_t>(item.hs) * (item.chunks + 1);
   }
-  if (lane == 0) {
-    if (me == 0) *reinterpret_cast<AttHeader*>(a.workspace) = head;
-    AttFirst f = {item.begin, item.begin + item.chunks + 1, item.t0, item.n, item.hs, 0};
-    reinterpret_cast<AttFirst*>(reinterpret_cast<uint8_t*>(a.workspace) + kAttHead)[me] = f;
+  if (start == cta_start && lane == 0) {
+    if (blockIdx.x == 0) *reinterpret_cast<AttHeader*>(a.workspace) = head;
+    reinterpret_cast<AttSpan*>(reinterpret_cast<uint8_t*>(a.workspace) + kAttHead)[blockIdx.x] = span_of(item);
   }
-  float* parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.workspace) + att_parts_at(a.ctas * W)) +
-                 me * 2 * S::kPart;
-
   uint8_t* ring = smem + warp * 4 * S::kStage;
   const uint32_t ring_at = smem_u32(ring);
   float* ring_scales = reinterpret_cast<float*>(smem + S::kScalesAt) + warp * 2 * CT;
@@ -564,7 +618,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               uint32_t b0, b1;
-              pairs_of<FMT>(ww[j], b0, b1);
+              pairs_of<FMT>(magic, ww[j], b0, b1);
 #pragma unroll
               for (int i = 0; i < NM; ++i) u + j == 0 ? mma0(s[i][n], q[i][j], b0, b1) : mma(s[i][n], q[i][j], b0, b1);
             }
@@ -657,10 +711,10 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 #pragma unroll
           for (int k = 0; k < KG; ++k) {
             uint32_t b0[4], b1[4];
-            pairs_of<FMT>(weave<FMT>(raw[k][0][w], raw[k][1][w], false), b0[0], b0[1]);
-            pairs_of<FMT>(weave<FMT>(raw[k][0][w], raw[k][1][w], true), b0[2], b0[3]);
-            pairs_of<FMT>(weave<FMT>(raw[k][2][w], raw[k][3][w], false), b1[0], b1[1]);
-            pairs_of<FMT>(weave<FMT>(raw[k][2][w], raw[k][3][w], true), b1[2], b1[3]);
+            pairs_of<FMT>(magic, weave<FMT>(raw[k][0][w], raw[k][1][w], false), b0[0], b0[1]);
+            pairs_of<FMT>(magic, weave<FMT>(raw[k][0][w], raw[k][1][w], true), b0[2], b0[3]);
+            pairs_of<FMT>(magic, weave<FMT>(raw[k][2][w], raw[k][3][w], false), b1[0], b1[1]);
+            pairs_of<FMT>(magic, weave<FMT>(raw[k][2][w], raw[k][3][w], true), b1[2], b1[3]);
 #pragma unroll
             for (int i = 0; i < NM; ++i)
 #pragma unroll
@@ -701,7 +755,9 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 
     // ---- results, or a part for the joining launch
     const bool split = start > item.begin || end > stop;
-    float* part = parts + (start >= item.begin ? 0 : S::kPart);
+    const int slot = start >= item.begin ? 0 : 1;
+    float* part = warp_parts + (2 * warp + slot) * S::kPart;
+    if (split && lane == 0) spans[warp][slot] = span_of(item);
     const float back = __uint_as_float((vexp - kWeightBits) << 23);
 #pragma unroll
     for (int i = 0; i < NM; ++i) {
@@ -736,174 +792,122 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
     if (last) break;
     item = next;
   }
+  }
+
+  // ---- the CTA's parts together: neighbours of one item, a warp a group
+  __syncthreads();
+  int group = 0;
+  for (int e = 0; e < 2 * W;) {
+    const AttSpan s = spans[e / 2][e % 2];
+    if (s.end == 0) {
+      ++e;
+      continue;
+    }
+    int n = 1, seen = 1;  // parts, places they are spread over
+    for (int k = e + 1; k < 2 * W; ++k) {
+      const AttSpan& b = spans[k / 2][k % 2];
+      if (b.end == 0) continue;
+      if (b.begin != s.begin) break;
+      ++n;
+      seen = k - e + 1;
+    }
+    if (group++ % W == warp) {
+      const bool done = s.begin >= cta_start && s.end <= cta_start + cta_units;
+      float* out = cta_parts + (s.begin <= cta_start ? 0 : S::kPart);
+#pragma unroll 1
+      for (int k = 0; k < S::kSlices; k += 4) {
+        float top[4], z[4];
+        float4 v[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          top[b] = kNoMax;
+          z[b] = 0.0f;
+          v[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll 3
+        for (int p = 0; p < seen; ++p) {
+          const bool on = spans[(e + p) / 2][(e + p) % 2].end != 0;
+          const float* from = warp_parts + (e + p) * S::kPart;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int r = 8 * ((k + b) / (S::kSlices / NM)) + g;
+            join_part(on, from, S::kRows * DC + r, S::kRows, (k + b) * 128 + lane * 4, top[b], z[b], v[b]);
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          if (done) {
+            join_out<DC, NM>(a, s, k + b, lane, top[b], z[b], v[b]);
+          } else {
+            const int r = 8 * ((k + b) / (S::kSlices / NM)) + g;
+            *reinterpret_cast<float4*>(out + (k + b) * 128 + lane * 4) = v[b];
+            if (c4 == 0 && (k + b) % (S::kSlices / NM) == 0) {
+              out[S::kRows * DC + r] = top[b];
+              out[S::kRows * DC + S::kRows + r] = z[b];
+            }
+          }
+        }
+      }
+    }
+    e += seen;
+  }
 }
 
-// An item that reaches over warps' stretches, as the joining launch finds it at the record of the first
-// worker whose stretch begins within it.
-struct Split {
-  AttFirst f;
-  int64_t n;                // parts: of the worker before, and of those that begin within the item
-  const float* head_part;   // the first; the others are kPart * 2 apart
-  const float* rest;
-};
-
-// Whether worker i's is such a record.
-__device__ __forceinline__ bool split_at(const AttendArgs& a, const AttHeader& h, int64_t i, AttFirst& f) {
-  if (i >= h.workers) return false;
-  f = reinterpret_cast<const AttFirst*>(reinterpret_cast<const uint8_t*>(a.workspace) + kAttHead)[i];
-  return share(h, i) > f.begin && share(h, i - 1) <= f.begin;
-}
-
-// The rest of it, by a whole warp.
+// Joins the items that reach over CTAs' stretches: CTA (i, slice) takes the item that stretch i + 1 begins within,
+// if it is the first to do so; its warps share the parts.
+constexpr int kJoinWarps = 4;
 template <int DC, int NM>
-__device__ __forceinline__ Split split_of(const AttendArgs& a, const AttHeader& h, int64_t i, const AttFirst& f, int lane) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __grid_constant__ AttendArgs a) {
   using S = AttShape<DC, NM>;
-  Split s;
-  s.f = f;
-  int64_t k = i + 1;  // the first worker that begins behind the item
+  __shared__ float4 sums[kJoinWarps][32];
+  __shared__ float2 tops[kJoinWarps][32];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) + 1;
+  const AttHeader h = *reinterpret_cast<const AttHeader*>(a.workspace);
+  const AttSpan f = reinterpret_cast<const AttSpan*>(reinterpret_cast<const uint8_t*>(a.workspace) + kAttHead)[i];
+  if (i >= h.ctas || share(h, i) <= f.begin || share(h, i - 1) > f.begin) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = blockIdx.y;
+  int64_t k = i + 1;  // the first CTA that begins behind the item
   for (;; k += 32) {
-    const uint32_t behind = __ballot_sync(0xffffffffu, k + lane >= h.workers || share(h, k + lane) >= f.end);
+    const uint32_t behind = __ballot_sync(0xffffffffu, k + lane >= h.ctas || share(h, k + lane) >= f.end);
     if (behind) {
       k += __ffs(behind) - 1;
       break;
     }
   }
-  s.n = k - (i - 1);
-  const float* parts = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.workspace) +
-                                                      att_parts_at(a.ctas * S::kWarps));
-  // worker i - 1 holds its part second, unless its stretch begins with the item
-  s.head_part = parts + ((i - 1) * 2 + (share(h, i - 1) < f.begin ? 1 : 0)) * S::kPart;
-  s.rest = parts + i * 2 * S::kPart;
-  return s;
-}
-
-// Parts first, first + step, .. of a slice's place: running maximum, sum of weights and sums.
-template <int DC, int NM>
-__device__ __forceinline__ void join_parts(const Split& s, int slice, int lane, int first, int step, float& top, float& z,
-                                           float4& v) {
-  using S = AttShape<DC, NM>;
-  constexpr int B = 4;
-  const int r = 8 * (slice / (S::kSlices / NM)) + (lane >> 2);
-  top = kNoMax;
-  z = 0.0f;
+  const float* parts = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.workspace) + att_parts_at(a.ctas));
+  // CTA i - 1 holds its part second, unless its stretch begins with the item
+  const float* first = parts + ((i - 1) * 2 + (share(h, i - 1) < f.begin ? 1 : 0)) * S::kPart;
+  const int r = 8 * (slice / (S::kSlices / NM)) + (lane >> 2), at = slice * 128 + lane * 4;
+  float top = kNoMax, z = 0.0f;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int64_t j = i - 1 + warp; j < k; j += kJoinWarps)
+    join_part(true, j == i - 1 ? first : parts + j * 2 * S::kPart, S::kRows * DC + r, S::kRows, at, top, z, v);
+  sums[warp][lane] = v;
+  tops[warp][lane] = make_float2(top, z);
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, tops[w][lane].x);
   v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int64_t j = first; j < s.n; j += step * B) {
-    float m[B], l[B];
-    float4 x[B];
+  z = 0.0f;
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int64_t jj = j + b * step;
-      m[b] = kNoMax;
-      l[b] = 0.0f;
-      x[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (jj < s.n) {
-        const float* p = jj == 0 ? s.head_part : s.rest + (jj - 1) * 2 * S::kPart;
-        m[b] = p[S::kRows * DC + r];
-        l[b] = p[S::kRows * DC + S::kRows + r];
-        x[b] = *reinterpret_cast<const float4*>(p + slice * 128 + lane * 4);
-      }
-    }
-    float now = top;
-#pragma unroll
-    for (int b = 0; b < B; ++b) now = fmaxf(now, m[b]);
-    const float e0 = exp2_fast(top - now);
-    top = now;
-    z *= e0;
-    v.x *= e0, v.y *= e0, v.z *= e0, v.w *= e0;
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const float e = exp2_fast(m[b] - now);
-      z = fmaf(l[b], e, z);
-      v.x = fmaf(x[b].x, e, v.x), v.y = fmaf(x[b].y, e, v.y), v.z = fmaf(x[b].z, e, v.z), v.w = fmaf(x[b].w, e, v.w);
-    }
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float2 t = tops[w][lane];
+    const float4 x = sums[w][lane];
+    const float e = exp2_fast(t.x - top);
+    z = fmaf(t.y, e, z);
+    v.x = fmaf(x.x, e, v.x), v.y = fmaf(x.y, e, v.y), v.z = fmaf(x.z, e, v.z), v.w = fmaf(x.w, e, v.w);
   }
-}
-
-template <int DC, int NM>
-__device__ __forceinline__ void join_out(const AttendArgs& a, const Split& s, int slice, int lane, float top, float z, float4 v) {
-  using S = AttShape<DC, NM>;
-  constexpr int UB = kUnitBytes<DC>, PER = S::kSlices / NM;  // slices of eight rows: unit, column parity, four dims
-  static_assert((DC == 256 ? 2 : 1) * 2 * (UB / 4) == PER, "as the parts are laid out");
-  const int k = slice % PER, r = 8 * (slice / PER) + (lane >> 2);
-  const int d = (value_unit<DC>(2 * (lane & 3) + k / (UB / 4) % 2) + 8 * (k / (UB / 2))) * UB + k % (UB / 4) * 4;
-  int t, head;
-  if (!row_of(a, s.f.t0, s.f.n, s.f.hs, r, t, head)) return;
-  const float inv = z == 0.0f ? 0.0f : 1.0f / z;
-  if (d < a.c.dim)
-    write_out(a, t * a.ld_dst + static_cast<int64_t>(head) * a.c.dim + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-  if (d == 0 && a.lse)
-    a.lse[static_cast<int64_t>(t) * a.q_heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * 0.693147181f;
-}
-
-// Many items, few parts each: CTA i looks at worker i + 1's record; its warps share the slices.
-constexpr int kJoinWarps = 4;
-template <int DC, int NM>
-__global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __grid_constant__ AttendArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  const AttHeader h = *reinterpret_cast<const AttHeader*>(a.workspace);
-  const int64_t i = static_cast<int64_t>(blockIdx.x) + 1;
-  AttFirst f;
-  if (!split_at(a, h, i, f)) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Split s = split_of<DC, NM>(a, h, i, f, lane);
-#pragma unroll 2
-  for (int k = warp; k < AttShape<DC, NM>::kSlices; k += kJoinWarps) {
-    float top, z;
-    float4 v;
-    join_parts<DC, NM>(s, k, lane, 0, 1, top, z, v);
-    join_out<DC, NM>(a, s, k, lane, top, z, v);
-  }
-}
-
-// Few items, many parts: CTA (i, slice) looks at 32 records; its warps share the parts.
-constexpr int kJoinFewWarps = 8;
-template <int DC, int NM>
-__global__ void __launch_bounds__(32 * kJoinFewWarps) attend_join_few_kernel(const __grid_constant__ AttendArgs a) {
-  __shared__ float4 sums[kJoinFewWarps][32];
-  __shared__ float2 tops[kJoinFewWarps][32];
-  pdl_wait();
-  pdl_trigger();
-  const AttHeader h = *reinterpret_cast<const AttHeader*>(a.workspace);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = blockIdx.y;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * 32 + 1;
-  AttFirst mine;
-  uint32_t todo = __ballot_sync(0xffffffffu, split_at(a, h, first + lane, mine));
-  for (; todo; todo &= todo - 1) {
-    const int64_t i = first + __ffs(todo) - 1;
-    AttFirst f;
-    split_at(a, h, i, f);
-    const Split s = split_of<DC, NM>(a, h, i, f, lane);
-    float top, z;
-    float4 v;
-    join_parts<DC, NM>(s, slice, lane, warp, kJoinFewWarps, top, z, v);
-    sums[warp][lane] = v;
-    tops[warp][lane] = make_float2(top, z);
-    __syncthreads();
-    if (warp == 0) {
-#pragma unroll
-      for (int w = 1; w < kJoinFewWarps; ++w) top = fmaxf(top, tops[w][lane].x);
-      v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      z = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kJoinFewWarps; ++w) {
-        const float2 t = tops[w][lane];
-        const float4 x = sums[w][lane];
-        const float e = exp2_fast(t.x - top);
-        z = fmaf(t.y, e, z);
-        v.x = fmaf(x.x, e, v.x), v.y = fmaf(x.y, e, v.y), v.z = fmaf(x.z, e, v.z), v.w = fmaf(x.w, e, v.w);
-      }
-      join_out<DC, NM>(a, s, slice, lane, top, z, v);
-    }
-    __syncthreads();
-  }
+  join_out<DC, NM>(a, f, slice, lane, top, z, v);
 }
 
 // ------------------------------------------------------------------ host
 int64_t attend_workspace_bytes(int dim, int tiles, int ctas) {
   const int dc = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
-  const int64_t workers = static_cast<int64_t>(ctas) * att_warps(dc, tiles);
-  return att_parts_at(static_cast<int>(workers)) + workers * 2 * 8 * tiles * (dc + 2) * 4;
+  return att_parts_at(ctas) + static_cast<int64_t>(ctas) * (1 + att_warps(dc, tiles)) * 2 * 8 * tiles * (dc + 2) * 4;
 }
 
 int attend_ctas(int, int, int sms) { return 2 * sms; }
@@ -935,13 +939,7 @@ static int launch_attend_t(const AttendArgs& a, cudaStream_t st, bool pdl) {
       return a.c.format == 0 ? launch_part<DC, true, 0, NM>(cfg, a) : launch_part<DC, true, 1, NM>(cfg, a);
     return a.c.format == 0 ? launch_part<DC, false, 0, NM>(cfg, a) : launch_part<DC, false, 1, NM>(cfg, a);
   }
-  const unsigned records = static_cast<unsigned>(a.ctas * S::kWarps - 1);  // of workers behind the first
-  if (static_cast<int64_t>(a.T) * a.c.heads * a.subs <= 64) {
-    cfg.gridDim = dim3((records + 31) / 32, S::kSlices);
-    cfg.blockDim = dim3(32 * kJoinFewWarps);
-    return cudaLaunchKernelEx(&cfg, attend_join_few_kernel<DC, NM>, a);
-  }
-  cfg.gridDim = dim3(records);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.ctas - 1), S::kSlices);
   cfg.blockDim = dim3(32 * kJoinWarps);
   return cudaLaunchKernelEx(&cfg, attend_join_kernel<DC, NM>, a);
 }
