@@ -248,9 +248,16 @@ static int plan_store(const gf_cache* c, const void* k, const void* v, int64_t T
   a.vec = vec;
   // Decode steps bring one token a block, a warp's work.  Prompts bring whole blocks: as many warps as hold
   // their values in registers between finding the scale and writing the codes.
-  a.wpu = 1;
-  const int64_t tpw = 32 / (c->dim / 8);
-  while (T > 256 && a.wpu < 8 && a.wpu * tpw * 4 < c->block) a.wpu *= 2;
+  a.tpw = static_cast<int>(32 / (c->dim / 8));
+  a.lane_inv = static_cast<int>(65536 / (c->dim / 8) + 1);
+  while (T > 256 && (kStoreWarps >> a.wpu_log2) > 1 && (a.tpw * kStoreKept << a.wpu_log2) < c->block) ++a.wpu_log2;
+  const int upg = kStoreWarps >> a.wpu_log2;
+  a.unit_groups = static_cast<int>((2 * c->heads + upg - 1) / upg);
+  a.q_groups = a.q ? (a.q_heads + kStoreWarps * a.tpw - 1) / (kStoreWarps * a.tpw) : 0;
+  // Each token may begin a block (decode steps); of a prompt's every block-th does, and CTAs that find none only
+  // cost their start: as many tokens a CTA as leave eight CTAs to an SM.
+  a.window = 1;
+  while (a.window < 32 && a.window < c->block && T * (a.unit_groups + a.q_groups) > 2432LL * a.window) a.window *= 2;
   *n = 1;
   return GF_OK;
 }
@@ -270,6 +277,7 @@ static int plan_load(const gf_cache* c, int64_t T, const int32_t* seq, const int
   const int64_t width = c->heads * c->dim;
   if (k && (e = check_rows(k, &ldk, width, o->type, &vec)) != GF_OK) return e;
   if (v && (e = check_rows(v, &ldv, width, o->type, &vec)) != GF_OK) return e;
+  if (!aligned_to(k, 16) || !aligned_to(v, 16) || (ldk | ldv) * elem_bytes(o->type) % 16 != 0) vec = 0;
   const int64_t kb = k ? rows_bytes(T, ldk, width, o->type) : 0, vb = v ? rows_bytes(T, ldv, width, o->type) : 0;
   if (!output_clear(c, k, kb, T, seq, pos) || !output_clear(c, v, vb, T, seq, pos) || ranges_overlap(k, kb, v, vb))
     return GF_ERR_ALIAS;

@@ -10,9 +10,6 @@
 
 namespace gf {
 
-constexpr int kStoreWarps = 8;
-constexpr int kStoreKept = 4;  // iterations whose values stay in registers between the two passes
-
 __device__ __forceinline__ int seq_of(const int32_t* seq, int64_t t) { return seq ? seq[t] : static_cast<int>(t); }
 
 template <typename E, bool VEC>
@@ -55,54 +52,58 @@ __device__ __forceinline__ void turn8(float (&v)[8], const float2* cs, bool halv
   }
 }
 
-// A CTA takes the new tokens of one block (those behind the first find that they are not the first and
-// leave), and of its work, units of (block, head, keys or values) and rows of queries, every gridDim.y-th
-// group of kStoreWarps warps.  A unit is wpu warps'; a warp holds 32 / (dim / 8) tokens at a time, eight
-// elements a lane.
+// A CTA looks for first tokens of blocks among `window` tokens of the call, and takes the new tokens of each one's
+// block in turn: of their work, units of (block, head, keys or values) and rows of queries, every gridDim.y-th
+// group of kStoreWarps warps.  A unit is 1 << wpu_log2 warps'; a warp holds 32 / (dim / 8) tokens at a time, eight
+// elements a lane.  (With a CTA to every token, those of a prompt that begin no block cost more than the
+// others: 8191 tokens in blocks of 32 took 90 us where XX.)
 template <int FMT, typename E, bool VEC>
-__global__ void __launch_bounds__(32 * kStoreWarps) store_kernel(const __grid_constant__ StoreArgs a) {
+__global__ void __launch_bounds__(32 * kStoreWarps, 3) store_kernel(const __grid_constant__ StoreArgs a) {
   extern __shared__ float2 cs[];  // [token][pair]
   __shared__ uint32_t tops[kStoreWarps];
-  __shared__ int first_other;
   pdl_wait();
   pdl_trigger();
   const CacheArgs& c = a.c;
-  const int64_t t = blockIdx.x;
-  const int seq = seq_of(a.seq, t), pos = a.pos[t];
-  const int64_t page = cache_page(c, seq, pos);
-  if (page < 0) return;
-  const int block = 1 << c.block_log2, i0 = pos & (block - 1);
-  if (t > 0 && i0 > 0 && seq_of(a.seq, t - 1) == seq && a.pos[t - 1] == pos - 1) return;
-  int n = 1;
-  if (block > 1) {
-    if (threadIdx.x == 0) first_other = block - i0;
-    __syncthreads();
-    const int i = threadIdx.x;
-    if (i > 0 && i < block - i0 &&
-        !(t + i < a.T && seq_of(a.seq, t + i) == seq && a.pos[t + i] == pos + i))
-      atomicMin(&first_other, i);
-    __syncthreads();
-    n = first_other;
+  const int block = 1 << c.block_log2, pairs = a.n_rot / 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int L = c.dim >> 3, tpw = a.tpw, lg = lane * a.lane_inv >> 16, u = lane - lg * L;  // lane / L; lanes over: unit 0 ..
+  const bool on = lg < tpw, halves = a.halves != 0, turns = a.table && 8 * u < a.n_rot;
+  int o0, o1;
+  unit_offsets(u, a.table ? a.n_rot : 0, halves, o0, o1);
+  const int wpu = 1 << a.wpu_log2, upg = kStoreWarps >> a.wpu_log2, unit_groups = a.unit_groups;
+  uint32_t firsts;  // of the window's tokens, those that begin a block's new ones
+  {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * a.window + lane;
+    bool first = false;
+    if (lane < a.window && t < a.T) {
+      const int pos = a.pos[t], seq = seq_of(a.seq, t);
+      first = !(t > 0 && (pos & (block - 1)) > 0 && seq_of(a.seq, t - 1) == seq && a.pos[t - 1] == pos - 1);
+    }
+    firsts = __ballot_sync(0xffffffffu, first);
   }
-  const int pairs = a.n_rot / 2;
+  for (; firsts; firsts &= firsts - 1) {
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * a.window + __ffs(firsts) - 1;
+  const int seq = seq_of(a.seq, t), pos = a.pos[t], i0 = pos & (block - 1);
+  int n = 0;  // tokens of the run within the block
+  for (int k = 0; k < block - i0; k += 32) {
+    const int i = k + lane;
+    const uint32_t same = __ballot_sync(0xffffffffu, i < block - i0 && t + i < a.T && seq_of(a.seq, t + i) == seq &&
+                                                         a.pos[t + i] == pos + i);
+    n += __ffs(~same) ? __ffs(~same) - 1 : 32;
+    if (~same) break;
+  }
   if (a.table) {
+    __syncthreads();  // the block before is done with
     const float mag = static_cast<const RopeHeader*>(a.table)->magnitude;
     for (int i = threadIdx.x; i < n * pairs; i += blockDim.x)
       cs[i] = rope_cs(rope_turns(a.table)[i % pairs], pos + i / pairs, mag);
     __syncthreads();
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int L = c.dim >> 3, tpw = 32 / L, lg = lane / L, u = lane - lg * L;
-  const bool on = lg < tpw, halves = a.halves != 0, turns = a.table && 8 * u < a.n_rot;
-  int o0, o1;
-  unit_offsets(u, a.table ? a.n_rot : 0, halves, o0, o1);
   const int slot0 = pos & ((1 << c.page_log2) - 1);
-  const int upg = kStoreWarps / a.wpu, unit_groups = (2 * c.heads + upg - 1) / upg;
-  const int q_groups = a.q ? (a.q_heads + kStoreWarps * tpw - 1) / (kStoreWarps * tpw) : 0;
-  for (int item = blockIdx.y; item < unit_groups + q_groups; item += gridDim.y) {
+  for (int item = blockIdx.y; item < unit_groups + a.q_groups; item += gridDim.y) {
     if (item >= unit_groups) {
       const int h = ((item - unit_groups) * kStoreWarps + warp) * tpw + lg;
-      if (!on || h >= a.q_heads) continue;
+      if (!on || h >= a.q_heads || cache_page(c, seq, pos) < 0) continue;
       for (int i = 0; i < n; ++i) {
         float v[8];
         load8<E, VEC>(static_cast<const E*>(a.q) + (t + i) * a.ldq + static_cast<int64_t>(h) * c.dim, o0, o1, v);
@@ -111,48 +112,59 @@ __global__ void __launch_bounds__(32 * kStoreWarps) store_kernel(const __grid_co
       }
       continue;
     }
-    const int unit = item * upg + warp / a.wpu, w = warp % a.wpu;
-    const bool live = unit < 2 * c.heads, is_v = unit >= c.heads;
+    const int unit = item * upg + (warp >> a.wpu_log2), w = warp & (wpu - 1);
+    bool live = unit < 2 * c.heads;
+    const bool is_v = unit >= c.heads;
     const int head = is_v ? unit - c.heads : unit;
-    const int step = a.wpu * tpw, iters = (n + step - 1) / step;
+    const int step = tpw << a.wpu_log2;
     // values are at their plain places in V and, where nothing turns, in K
     const int p0 = is_v ? 8 * u : o0, p1 = is_v ? 8 * u + 4 : o1;
+    const bool plain = p1 == p0 + 4;
     const E* src = static_cast<const E*>(is_v ? a.v : a.k) + static_cast<int64_t>(head) * c.dim;
     const int64_t ld = is_v ? a.ldv : a.ldk;
-    auto fetch = [&](int i, float (&v)[8]) {
-      load8<E, VEC>(src + (t + i) * ld, p0, p1, v);
+    auto turn = [&](int i, float (&v)[8]) {
       if (turns && !is_v) turn8(v, cs + i * pairs + 4 * u, halves);
     };
-    float kept[kStoreKept][8];
-    uint32_t top = 0;
+    float widest = 0.0f;
     auto widen = [&](const float (&v)[8]) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);  // NaN is the largest
+      for (int e = 0; e < 8; ++e) widest = top_of(widest, v[e]);
     };
+    // All of the kept values are on their way before the first is waited for: lanes and iterations that have no token
+    // take the run's last one.
+    float kept[kStoreKept][8];
+    if (live) {
 #pragma unroll
-    for (int k = 0; k < kStoreKept; ++k) {
-      const int i = k * step + w * tpw + lg;
-      if (live && on && i < n) {
-        fetch(i, kept[k]);
+      for (int k = 0; k < kStoreKept; ++k)
+        if (k == 0 || k * step < n) load8<E, VEC>(src + (t + min(k * step + w * tpw + lg, n - 1)) * ld, p0, p1, kept[k]);
+    }
+    // (looked up behind the loads, so that they do not wait for it)
+    const int64_t page = cache_page(c, seq, pos);
+    live = live && page >= 0;
+    float* scale = live ? (is_v ? c.v_scale : c.k_scale) + cache_scale(c, page, head, slot0) : nullptr;
+    const float old = live && i0 > 0 ? *scale : 0.0f;
+    if (live) {
+#pragma unroll
+      for (int k = 0; k < kStoreKept; ++k) {
+        if (k > 0 && k * step >= n) break;
+        turn(min(k * step + w * tpw + lg, n - 1), kept[k]);
         widen(kept[k]);
       }
-    }
-    for (int k = kStoreKept; k < iters; ++k) {
-      const int i = k * step + w * tpw + lg;
-      if (live && on && i < n) {
+#pragma unroll 2
+      for (int k = kStoreKept; k * step < n; ++k) {
+        const int i = min(k * step + w * tpw + lg, n - 1);
         float v[8];
-        fetch(i, v);
+        load8<E, VEC>(src + (t + i) * ld, p0, p1, v);
+        turn(i, v);
         widen(v);
       }
     }
-    float* scale = live ? (is_v ? c.v_scale : c.k_scale) + cache_scale(c, page, head, slot0) : nullptr;
-    const float old = live && i0 > 0 ? *scale : 0.0f;
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (a.wpu > 1) {
+    uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(widest));  // NaN is the largest
+    if (wpu > 1) {
       __syncthreads();  // the group before has read its tops
       if (lane == 0) tops[warp] = top;
       __syncthreads();
-      for (int i = 0; i < a.wpu; ++i) top = max(top, tops[warp - w + i]);
+      for (int i = 0; i < wpu; ++i) top = max(top, tops[warp - w + i]);
     }
     if (!live) continue;
     float d;
@@ -166,21 +178,25 @@ __global__ void __launch_bounds__(32 * kStoreWarps) store_kernel(const __grid_co
     uint8_t* codes = (is_v ? c.v : c.k) + cache_row(c, page, head, slot0);
     auto write = [&](int i, const float (&v)[8]) {
       uint8_t* row = codes + static_cast<int64_t>(i) * c.dim;
-      const uint32_t x = number ? codes4<FMT>(v[0], v[1], v[2], v[3], d, inv) : 0u;
-      const uint32_t y = number ? codes4<FMT>(v[4], v[5], v[6], v[7], d, inv) : 0u;
-      *reinterpret_cast<uint32_t*>(row + p0) = x;
-      *reinterpret_cast<uint32_t*>(row + p1) = y;
+      const uint2 w = number ? codes8<FMT>(v, d, inv) : make_uint2(0u, 0u);
+      if (plain) {
+        *reinterpret_cast<uint2*>(row + p0) = w;
+      } else {
+        *reinterpret_cast<uint32_t*>(row + p0) = w.x;
+        *reinterpret_cast<uint32_t*>(row + p1) = w.y;
+      }
     };
 #pragma unroll
     for (int k = 0; k < kStoreKept; ++k) {
       const int i = k * step + w * tpw + lg;
       if (on && i < n) write(i, kept[k]);
     }
-    for (int k = kStoreKept; k < iters; ++k) {
+    for (int k = kStoreKept; k * step < n; ++k) {
       const int i = k * step + w * tpw + lg;
       if (on && i < n) {
         float v[8];
-        fetch(i, v);
+        load8<E, VEC>(src + (t + i) * ld, p0, p1, v);
+        turn(i, v);
         write(i, v);
       }
     }
@@ -193,25 +209,25 @@ __global__ void __launch_bounds__(32 * kStoreWarps) store_kernel(const __grid_co
         values4<FMT>(raw.y, y);
         // i8: code * old is exact; e4m3: the scales' quotient is
         const float f = FMT == 0 ? old : 1.0f, r = FMT == 0 ? inv : old * inv;
-        *row = make_uint2(codes4<FMT>(x[0] * f, x[1] * f, x[2] * f, x[3] * f, d, r),
-                          codes4<FMT>(y[0] * f, y[1] * f, y[2] * f, y[3] * f, d, r));
+        const float v[8] = {x[0] * f, x[1] * f, x[2] * f, x[3] * f, y[0] * f, y[1] * f, y[2] * f, y[3] * f};
+        *row = codes8<FMT>(v, d, r);
       }
     }
+  }
   }
 }
 
 template <int FMT, typename E, bool VEC>
 static int launch_store_t(const StoreArgs& a, int sms, cudaStream_t st, bool pdl) {
-  const int64_t tpw = 32 / (a.c.dim / 8), upg = kStoreWarps / a.wpu;
-  int64_t groups = (2 * a.c.heads + upg - 1) / upg;
-  if (a.q) groups += (a.q_heads + kStoreWarps * tpw - 1) / (kStoreWarps * tpw);
-  // Groups spread over as many CTAs as keep eight on every SM, counting whole blocks of new tokens
-  // (a prompt's); every CTA of a block computes its tokens' cosines again.
+  const int64_t groups = a.unit_groups + a.q_groups;
+  // Groups spread over as many CTAs as make 32 for every SM, counting whole blocks of new tokens (a prompt's):
+  // a CTA waits for its values once, and others fill the time; every CTA of a block computes its tokens'
+  // cosines again.
   const int64_t blocks = (a.T + (1 << a.c.block_log2) - 1) >> a.c.block_log2;
-  int64_t y = (8 * sms + blocks - 1) / blocks;
+  int64_t y = (32 * sms + blocks - 1) / blocks;
   if (y > groups) y = groups;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.T), static_cast<unsigned>(y));
+  cfg.gridDim = dim3(static_cast<unsigned>((a.T + a.window - 1) / a.window), static_cast<unsigned>(y));
   cfg.blockDim = dim3(32 * kStoreWarps);
   cfg.dynamicSmemBytes = a.table ? static_cast<size_t>(a.n_rot / 2) << (3 + a.c.block_log2) : 0;
   cfg.stream = st;
@@ -239,55 +255,96 @@ int launch_store(const StoreArgs& a, int sms, cudaStream_t st, bool pdl) {
   return a.vec ? launch_store_t<1, __half, true>(a, sms, st, pdl) : launch_store_t<1, __half, false>(a, sms, st, pdl);
 }
 
-// A lane takes eight elements of a (token, head) row.
-template <int FMT, typename E, bool VEC>
+// A thread takes 16 bytes of output, at the same place of TOKENS tokens' rows: all their positions, then
+// all their pages, then all their codes are on the way together.
+template <int FMT, typename E, bool VEC, int TOKENS>
 __global__ void __launch_bounds__(256) load_kernel(const __grid_constant__ LoadArgs a) {
+  constexpr int N = 16 / sizeof(E), WORDS = N / 4;
   pdl_wait();
   pdl_trigger();
   const CacheArgs& c = a.c;
-  const int L = c.dim >> 3;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, row = i / L;
-  const int u = static_cast<int>(i - row * L);
-  const int64_t t = row / c.heads;
-  const int h = static_cast<int>(row - t * c.heads);
-  if (t >= a.T) return;
-  const int pos = a.pos[t], slot = pos & ((1 << c.page_log2) - 1);
-  const int64_t page = cache_page(c, seq_of(a.seq, t), pos);
-  const int64_t at = cache_row(c, page, h, slot) + 8 * u, sc = cache_scale(c, page, h, slot);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * TOKENS;
+  int pos[TOKENS], seq[TOKENS];
+  int64_t page[TOKENS];
 #pragma unroll
-  for (int is_v = 0; is_v < 2; ++is_v) {
-    E* out = static_cast<E*>(is_v ? a.v : a.k);
-    if (!out) continue;
-    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (page >= 0) {
-      const uint2 raw = *reinterpret_cast<const uint2*>((is_v ? c.v : c.k) + at);
-      const float d = (is_v ? c.v_scale : c.k_scale)[sc];
-      float x[4], y[4];
-      values4<FMT>(raw.x, x);
-      values4<FMT>(raw.y, y);
+  for (int i = 0; i < TOKENS; ++i) {
+    pos[i] = t0 + i < a.T ? a.pos[t0 + i] : -1;
+    seq[i] = t0 + i < a.T ? seq_of(a.seq, t0 + i) : -1;
+  }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = x[e] * d;
-        v[4 + e] = y[e] * d;
+  for (int i = 0; i < TOKENS; ++i) page[i] = cache_page(c, seq[i], pos[i]);
+  for (int at = (threadIdx.x + blockIdx.y * blockDim.x) * N; at < c.heads * c.dim; at += blockDim.x * gridDim.y * N) {
+    const int h = at / c.dim, d = at - h * c.dim;
+#pragma unroll
+    for (int is_v = 0; is_v < 2; ++is_v) {
+      E* out = static_cast<E*>(is_v ? a.v : a.k);
+      if (!out) continue;
+      uint32_t raw[TOKENS][WORDS];
+      float scale[TOKENS];
+#pragma unroll
+      for (int i = 0; i < TOKENS; ++i) {
+        const int slot = pos[i] & ((1 << c.page_log2) - 1);
+        scale[i] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) raw[i][w] = 0;
+        if (page[i] >= 0) {
+          const uint8_t* p = (is_v ? c.v : c.k) + cache_row(c, page[i], h, slot) + d;
+          if constexpr (WORDS == 2) {
+            const uint2 r = *reinterpret_cast<const uint2*>(p);
+            raw[i][0] = r.x, raw[i][1] = r.y;
+          } else {
+            raw[i][0] = *reinterpret_cast<const uint32_t*>(p);
+          }
+          scale[i] = (is_v ? c.v_scale : c.k_scale)[cache_scale(c, page[i], h, slot)];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < TOKENS; ++i) {
+        if (t0 + i >= a.T) break;
+        E* to = out + (t0 + i) * (is_v ? a.ldv : a.ldk) + at;
+        float v[N];
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) {
+          float x[4];
+          values4<FMT>(raw[i][w], x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * w + e] = page[i] >= 0 ? x[e] * scale[i] : 0.0f;
+        }
+        if constexpr (!VEC) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) store1(to + e, v[e]);
+        } else if constexpr (WORDS == 2) {
+          const __half2 q[4] = {__floats2half2_rn(v[0], v[1]), __floats2half2_rn(v[2], v[3]), __floats2half2_rn(v[4], v[5]),
+                                __floats2half2_rn(v[6], v[7])};
+          *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(q);
+        } else {
+          store4(to, v[0], v[1], v[2], v[3]);
+        }
       }
     }
-    store8<E, VEC>(out + t * (is_v ? a.ldv : a.ldk) + static_cast<int64_t>(h) * c.dim, 8 * u, 8 * u + 4, v);
   }
 }
 
 template <int FMT, typename E>
 static int launch_load_t(const LoadArgs& a, cudaStream_t st, bool pdl) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.T * a.c.heads * (a.c.dim / 8) + 255) / 256));
-  cfg.blockDim = dim3(256);
+  // few tokens: one a CTA, its heads spread over CTAs
+  const bool few = a.T < 1024;
+  const int64_t units = static_cast<int64_t>(a.c.heads) * a.c.dim * sizeof(E) / 16;
+  cfg.blockDim = dim3(static_cast<unsigned>(units < 256 ? (units + 31) / 32 * 32 : 256));
+  cfg.gridDim = few ? dim3(static_cast<unsigned>(a.T), static_cast<unsigned>((units + 255) / 256))
+                    : dim3(static_cast<unsigned>((a.T + 3) / 4));
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return a.vec ? cudaLaunchKernelEx(&cfg, load_kernel<FMT, E, true>, a)
-               : cudaLaunchKernelEx(&cfg, load_kernel<FMT, E, false>, a);
+  if (few)
+    return a.vec ? cudaLaunchKernelEx(&cfg, load_kernel<FMT, E, true, 1>, a)
+                 : cudaLaunchKernelEx(&cfg, load_kernel<FMT, E, false, 1>, a);
+  return a.vec ? cudaLaunchKernelEx(&cfg, load_kernel<FMT, E, true, 4>, a)
+               : cudaLaunchKernelEx(&cfg, load_kernel<FMT, E, false, 4>, a);
 }
 
 int launch_load(const LoadArgs& a, cudaStream_t st, bool pdl) {

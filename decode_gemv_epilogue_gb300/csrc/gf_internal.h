@@ -340,6 +340,8 @@ struct RopeArgs {
 int launch_rope(const RopeArgs& a, cudaStream_t st, bool pdl);
 
 // The cache (cache.cu).
+constexpr int kStoreWarps = 8;
+constexpr int kStoreKept = 4;  // iterations whose values stay in registers between the store's two passes
 constexpr int kCacheMaxBlock = 64;
 constexpr int kCacheMaxDim = 256;
 struct CacheArgs {
@@ -362,7 +364,10 @@ struct StoreArgs {
   void* q_dst;
   int64_t T, ldk, ldv, ldq, ld_q_dst;
   int n_rot, halves, q_heads, type, vec;
-  int wpu;              // warps that share a block of a head
+  int wpu_log2;         // warps that share a block of a head
+  int tpw, lane_inv;    // tokens a warp holds at a time; 65536 over a token's lanes, rounded up
+  int unit_groups, q_groups;
+  int window;           // tokens that a CTA looks through, up to 32
 };
 int launch_store(const StoreArgs& a, int sms, cudaStream_t st, bool pdl);
 struct LoadArgs {
