@@ -236,7 +236,7 @@ __device__ __forceinline__ bool item_at(const AttendArgs& a, int t, Item& it) {
   return true;
 }
 
-// Workspace: a header, a record of each CTA's first item, each CTA's two parts, each warp's two parts.
+// Workspace: a header, a record of each CTA's first item, each CTA's two parts, each warp's first part.
 struct AttHeader {
   int64_t ctas;
   int64_t each, more;  // units of a CTA; the first `more` take one more
@@ -297,11 +297,8 @@ __device__ __forceinline__ bool row_of(const AttendArgs& a, int t0, int n, int h
   return i < n && in_group < a.group;
 }
 
-// A part's place, if there is one, added to a running maximum, sum of weights and sums.
-__device__ __forceinline__ void join_part(bool on, const float* part, int max_at, int rows, int sums_at, float& top, float& z,
-                                          float4& v) {
-  const float m = on ? __ldcg(part + max_at) : kNoMax, l = on ? __ldcg(part + max_at + rows) : 0.0f;
-  const float4 x = on ? __ldcg(reinterpret_cast<const float4*>(part + sums_at)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+// A part's place (maximum, sum of weights, four sums) added to a running one.
+__device__ __forceinline__ void join_part(float m, float l, float4 x, float& top, float& z, float4& v) {
   const float now = fmaxf(top, m), e0 = exp2_fast(top - now), e = exp2_fast(m - now);
   top = now;
   z = fmaf(l, e, z * e0);
@@ -337,7 +334,8 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
   constexpr int NO = DC / 8;                  // column tiles of the output
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t group_units[kAttMaxTokens / 32];  // of 32 tokens each, for one (head, part)
-  __shared__ AttSpan spans[W][2];                       // the items of the warps' parts
+  __shared__ AttSpan spans[W][2];                       // the items of the warps' parts: first, last
+  __shared__ float2 part_rows[W][2][S::kRows];          // maxima and sums of weights of their rows
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c4 = lane & 3;
@@ -367,8 +365,9 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
   const int64_t start = cta_start + cta_units * warp / W, stop = cta_start + cta_units * (warp + 1) / W;
   float* cta_parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.workspace) + att_parts_at(a.ctas)) +
                      static_cast<int64_t>(blockIdx.x) * 2 * S::kPart;
-  float* warp_parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.workspace) + att_parts_at(a.ctas)) +
-                      (static_cast<int64_t>(a.ctas) + static_cast<int64_t>(blockIdx.x) * W) * 2 * S::kPart;
+  float* warp_part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.workspace) + att_parts_at(a.ctas)) +
+                     (static_cast<int64_t>(a.ctas) * 2 + static_cast<int64_t>(blockIdx.x) * W + warp) * S::kPart;
+  bool kept = false;  // a part lies there
   if (lane < 2) spans[warp][lane].end = 0;  // no part
   __syncwarp();
   if (start < stop) {
@@ -401,6 +400,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
     reinterpret_cast<AttSpan*>(reinterpret_cast<uint8_t*>(a.workspace) + kAttHead)[blockIdx.x] = span_of(item);
   }
   uint8_t* ring = smem + warp * 4 * S::kStage;
+  static_assert(S::kRows * DC * 4 <= 2 * S::kStage, "a warp's two parts fit its stages");
   const uint32_t ring_at = smem_u32(ring);
   float* ring_scales = reinterpret_cast<float*>(smem + S::kScalesAt) + warp * 2 * CT;
   uint8_t* qs = smem + S::kQueriesAt + warp * NM * KS * 512;
@@ -753,103 +753,101 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
       pages = pages_of(src, c0 + 1);
     }
 
-    // ---- results, or a part for the joining launch
-    const bool split = start > item.begin || end > stop;
-    const int slot = start >= item.begin ? 0 : 1;
-    float* part = warp_parts + (2 * warp + slot) * S::kPart;
-    if (split && lane == 0) spans[warp][slot] = span_of(item);
+    // ---- results, or a part to be joined: the warp's last one into its stages, which nothing comes into any
+    // more, one before into the workspace
     const float back = __uint_as_float((vexp - kWeightBits) << 23);
+    auto give = [&](auto put_sums, auto put_row, bool divide) {
 #pragma unroll
-    for (int i = 0; i < NM; ++i) {
-      const float z = quad_sum(l[i]);
-      int t, head;
-      const bool live = row_of(a, item.t0, item.n, item.hs, 8 * i + g, t, head);
-      const float inv = split ? back : z == 0.0f ? 0.0f : back / z;  // no keys: zeros
+      for (int i = 0; i < NM; ++i) {
+        const float z = quad_sum(l[i]);
+        const float inv = !divide ? back : z == 0.0f ? 0.0f : back / z;  // no keys: zeros
+        int t, head;
+        const bool live = row_of(a, item.t0, item.n, item.hs, 8 * i + g, t, head);
+        const int64_t row = live ? t * a.ld_dst + static_cast<int64_t>(head) * D : -1;
 #pragma unroll
-      for (int u = 0; u < UC; ++u)
+        for (int u = 0; u < UC; ++u)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int n = 0; n < UB; n += 4) {
-            const int d = (value_unit<DC>(2 * c4 + e) + 8 * u) * UB + n;
-            const float2* x = &o[i][u * UB + n];
-            const float4 v = e == 0 ? make_float4(x[0].x * inv, x[1].x * inv, x[2].x * inv, x[3].x * inv)
-                                    : make_float4(x[0].y * inv, x[1].y * inv, x[2].y * inv, x[3].y * inv);
-            if (split)
-              *reinterpret_cast<float4*>(part + (((i * UC + u) * 2 + e) * (UB / 4) + n / 4) * 128 + lane * 4) = v;
-            else if (live && d < D)
-              write_out(a, t * a.ld_dst + static_cast<int64_t>(head) * D + d, v);
-          }
-      if (c4 == 0) {
-        if (split) {
-          part[S::kRows * DC + 8 * i + g] = m[i];
-          part[S::kRows * DC + S::kRows + 8 * i + g] = z;
-        } else if (live && a.lse) {
-          a.lse[static_cast<int64_t>(t) * a.q_heads + head] = z == 0.0f ? -INFINITY : (m[i] + log2f(z)) * 0.693147181f;
-        }
+            for (int n = 0; n < UB; n += 4) {
+              const float2* x = &o[i][u * UB + n];
+              const float4 v = e == 0 ? make_float4(x[0].x * inv, x[1].x * inv, x[2].x * inv, x[3].x * inv)
+                                      : make_float4(x[0].y * inv, x[1].y * inv, x[2].y * inv, x[3].y * inv);
+              put_sums((((i * UC + u) * 2 + e) * (UB / 4) + n / 4) * 128 + lane * 4, row,
+                       (value_unit<DC>(2 * c4 + e) + 8 * u) * UB + n, v);
+            }
+        if (c4 == 0) put_row(8 * i + g, row >= 0, t, head, m[i], z);
       }
+    };
+    if (start > item.begin || end > stop) {
+      const int slot = start >= item.begin ? 0 : 1;
+      auto put_row = [&](int r, bool, int, int, float top, float z) { part_rows[warp][slot][r] = make_float2(top, z); };
+      if (last) {
+        float* part = reinterpret_cast<float*>(ring + slot * 2 * S::kStage);
+        give([&](int at, int64_t, int, float4 v) { *reinterpret_cast<float4*>(part + at) = v; }, put_row, false);
+      } else {
+        give([&](int at, int64_t, int, float4 v) { *reinterpret_cast<float4*>(warp_part + at) = v; }, put_row, false);
+        kept = true;
+      }
+      if (lane == 0) spans[warp][slot] = span_of(item);
+    } else {
+      give([&](int, int64_t row, int d, float4 v) {
+             if (row >= 0 && d < D) write_out(a, row + d, v);
+           },
+           [&](int, bool live, int t, int head, float top, float z) {
+             if (live && a.lse)
+               a.lse[static_cast<int64_t>(t) * a.q_heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * 0.693147181f;
+           },
+           true);
     }
     if (last) break;
     item = next;
   }
+  if (kept) {  // back from the workspace: each lane what it wrote
+    float4 v[S::kSlices];
+#pragma unroll
+    for (int k = 0; k < S::kSlices; ++k) v[k] = *reinterpret_cast<const float4*>(warp_part + k * 128 + lane * 4);
+#pragma unroll
+    for (int k = 0; k < S::kSlices; ++k) *reinterpret_cast<float4*>(ring + k * 512 + lane * 16) = v[k];
+  }
   }
 
-  // ---- the CTA's parts together: neighbours of one item, a warp a group
+  // ---- the CTA's parts together: neighbours of one item, a warp a slice of them.  Lane k looks at place k.
   __syncthreads();
-  int group = 0;
-  for (int e = 0; e < 2 * W;) {
+  AttSpan mine = {};
+  if (lane < 2 * W) mine = spans[lane / 2][lane % 2];
+  const uint32_t there = __ballot_sync(0xffffffffu, mine.end != 0);
+  const uint32_t below = there & ((1u << lane) - 1);
+  const int64_t before = __shfl_sync(0xffffffffu, mine.begin, below ? 31 - __clz(below) : 0);
+  uint32_t firsts = __ballot_sync(0xffffffffu, mine.end != 0 && (below == 0 || before != mine.begin));
+  int task = 0;
+  for (; firsts; firsts &= firsts - 1) {
+    const int e = __ffs(firsts) - 1;
+    const uint32_t behind = firsts & (firsts - 1);
+    const uint32_t members = there & ~((1u << e) - 1) & (behind ? (behind & -behind) - 1 : 0xffffffffu);
     const AttSpan s = spans[e / 2][e % 2];
-    if (s.end == 0) {
-      ++e;
-      continue;
-    }
-    int n = 1, seen = 1;  // parts, places they are spread over
-    for (int k = e + 1; k < 2 * W; ++k) {
-      const AttSpan& b = spans[k / 2][k % 2];
-      if (b.end == 0) continue;
-      if (b.begin != s.begin) break;
-      ++n;
-      seen = k - e + 1;
-    }
-    if (group++ % W == warp) {
-      const bool done = s.begin >= cta_start && s.end <= cta_start + cta_units;
-      float* out = cta_parts + (s.begin <= cta_start ? 0 : S::kPart);
-#pragma unroll 1
-      for (int k = 0; k < S::kSlices; k += 4) {
-        float top[4], z[4];
-        float4 v[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          top[b] = kNoMax;
-          z[b] = 0.0f;
-          v[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-#pragma unroll 3
-        for (int p = 0; p < seen; ++p) {
-          const bool on = spans[(e + p) / 2][(e + p) % 2].end != 0;
-          const float* from = warp_parts + (e + p) * S::kPart;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int r = 8 * ((k + b) / (S::kSlices / NM)) + g;
-            join_part(on, from, S::kRows * DC + r, S::kRows, (k + b) * 128 + lane * 4, top[b], z[b], v[b]);
-          }
-        }
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          if (done) {
-            join_out<DC, NM>(a, s, k + b, lane, top[b], z[b], v[b]);
-          } else {
-            const int r = 8 * ((k + b) / (S::kSlices / NM)) + g;
-            *reinterpret_cast<float4*>(out + (k + b) * 128 + lane * 4) = v[b];
-            if (c4 == 0 && (k + b) % (S::kSlices / NM) == 0) {
-              out[S::kRows * DC + r] = top[b];
-              out[S::kRows * DC + S::kRows + r] = z[b];
-            }
-          }
+    const bool done = s.begin >= cta_start && s.end <= cta_start + cta_units;
+    float* out = cta_parts + (s.begin <= cta_start ? 0 : S::kPart);
+    for (int k = 0; k < S::kSlices; ++k) {
+      if (task++ % W != warp) continue;
+      const int r = 8 * (k / (S::kSlices / NM)) + g;
+      float top = kNoMax, z = 0.0f;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (uint32_t left = members; left; left &= left - 1) {
+        const int p = __ffs(left) - 1;
+        const float2 ml = part_rows[p / 2][p % 2][r];
+        join_part(ml.x, ml.y, *reinterpret_cast<const float4*>(smem + p * 2 * S::kStage + k * 512 + lane * 16), top, z, v);
+      }
+      if (done) {
+        join_out<DC, NM>(a, s, k, lane, top, z, v);
+      } else {
+        *reinterpret_cast<float4*>(out + k * 128 + lane * 4) = v;
+        if (c4 == 0 && k % (S::kSlices / NM) == 0) {
+          out[S::kRows * DC + r] = top;
+          out[S::kRows * DC + S::kRows + r] = z;
         }
       }
     }
-    e += seen;
   }
 }
 
@@ -882,9 +880,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __gr
   const int r = 8 * (slice / (S::kSlices / NM)) + (lane >> 2), at = slice * 128 + lane * 4;
   float top = kNoMax, z = 0.0f;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int64_t j = i - 1 + warp; j < k; j += kJoinWarps)
-    join_part(true, j == i - 1 ? first : parts + j * 2 * S::kPart, S::kRows * DC + r, S::kRows, at, top, z, v);
+  constexpr int B = 8;  // parts on their way together
+  for (int64_t j0 = i - 1 + warp; j0 < k; j0 += kJoinWarps * B) {
+    float m[B], l[B];
+    float4 x[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int64_t j = j0 + b * kJoinWarps;
+      const float* part = j == i - 1 ? first : parts + j * 2 * S::kPart;
+      m[b] = j < k ? part[S::kRows * DC + r] : kNoMax;
+      l[b] = j < k ? part[S::kRows * DC + S::kRows + r] : 0.0f;
+      x[b] = j < k ? *reinterpret_cast<const float4*>(part + at) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) join_part(m[b], l[b], x[b], top, z, v);
+  }
   sums[warp][lane] = v;
   tops[warp][lane] = make_float2(top, z);
   __syncthreads();
@@ -907,7 +917,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __gr
 // ------------------------------------------------------------------ host
 int64_t attend_workspace_bytes(int dim, int tiles, int ctas) {
   const int dc = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
-  return att_parts_at(ctas) + static_cast<int64_t>(ctas) * (1 + att_warps(dc, tiles)) * 2 * 8 * tiles * (dc + 2) * 4;
+  return att_parts_at(ctas) + static_cast<int64_t>(ctas) * (2 + att_warps(dc, tiles)) * 8 * tiles * (dc + 2) * 4;
 }
 
 int attend_ctas(int, int, int sms) { return 2 * sms; }
