@@ -851,67 +851,119 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
   }
 }
 
-// Joins the items that reach over CTAs' stretches: CTA (i, slice) takes the item that stretch i + 1 begins within,
-// if it is the first to do so; its warps share the parts.
-constexpr int kJoinWarps = 4;
+// An item that reaches over CTAs' stretches: the first CTA's part, and n - 1 others' two parts apart.
+struct Split {
+  const float* first;
+  const float* rest;
+  int n;
+};
+
+// Whether CTA i's record is of an item that begins before it and within the stretch before.
+__device__ __forceinline__ bool split_at(const AttendArgs& a, const AttHeader& h, int64_t i, AttSpan& s) {
+  if (i >= a.ctas) return false;
+  s = reinterpret_cast<const AttSpan*>(reinterpret_cast<const uint8_t*>(a.workspace) + kAttHead)[i];
+  return i < h.ctas && share(h, i) > s.begin && share(h, i - 1) <= s.begin;
+}
+
+// Its parts, by a whole warp.
 template <int DC, int NM>
-__global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __grid_constant__ AttendArgs a) {
-  using S = AttShape<DC, NM>;
-  __shared__ float4 sums[kJoinWarps][32];
-  __shared__ float2 tops[kJoinWarps][32];
-  pdl_wait();
-  pdl_trigger();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) + 1;
-  const AttHeader h = *reinterpret_cast<const AttHeader*>(a.workspace);
-  const AttSpan f = reinterpret_cast<const AttSpan*>(reinterpret_cast<const uint8_t*>(a.workspace) + kAttHead)[i];
-  if (i >= h.ctas || share(h, i) <= f.begin || share(h, i - 1) > f.begin) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = blockIdx.y;
-  int64_t k = i + 1;  // the first CTA that begins behind the item
-  for (;; k += 32) {
-    const uint32_t behind = __ballot_sync(0xffffffffu, k + lane >= h.ctas || share(h, k + lane) >= f.end);
-    if (behind) {
-      k += __ffs(behind) - 1;
+__device__ __forceinline__ Split split_of(const AttendArgs& a, const AttHeader& h, int64_t i, const AttSpan& s, int lane) {
+  constexpr int64_t kPart = AttShape<DC, NM>::kPart;
+  Split p;
+  for (int64_t k = i + 1;; k += 32) {  // the first CTA that begins behind the item
+    const uint32_t past = __ballot_sync(0xffffffffu, k + lane >= h.ctas || share(h, k + lane) >= s.end);
+    if (past) {
+      p.n = static_cast<int>(k - i) + __ffs(past);
       break;
     }
   }
   const float* parts = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(a.workspace) + att_parts_at(a.ctas));
   // CTA i - 1 holds its part second, unless its stretch begins with the item
-  const float* first = parts + ((i - 1) * 2 + (share(h, i - 1) < f.begin ? 1 : 0)) * S::kPart;
-  const int r = 8 * (slice / (S::kSlices / NM)) + (lane >> 2), at = slice * 128 + lane * 4;
-  float top = kNoMax, z = 0.0f;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  constexpr int B = 8;  // parts on their way together
-  for (int64_t j0 = i - 1 + warp; j0 < k; j0 += kJoinWarps * B) {
+  p.first = parts + ((i - 1) * 2 + (share(h, i - 1) < s.begin ? 1 : 0)) * kPart;
+  p.rest = parts + (i - 1) * 2 * kPart;
+  return p;
+}
+
+// Parts from, from + STEP, .. of a slice's place, B on their way together.
+template <int DC, int NM, int STEP, int B>
+__device__ __forceinline__ void join_parts(const Split& p, int slice, int lane, int from, float& top, float& z, float4& v) {
+  using S = AttShape<DC, NM>;
+  const int r = S::kRows * DC + 8 * (slice / (S::kSlices / NM)) + (lane >> 2), at = slice * 128 + lane * 4;
+  top = kNoMax;
+  z = 0.0f;
+  v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int j0 = from; j0 < p.n; j0 += STEP * B) {
     float m[B], l[B];
     float4 x[B];
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      const int64_t j = j0 + b * kJoinWarps;
-      const float* part = j == i - 1 ? first : parts + j * 2 * S::kPart;
-      m[b] = j < k ? part[S::kRows * DC + r] : kNoMax;
-      l[b] = j < k ? part[S::kRows * DC + S::kRows + r] : 0.0f;
-      x[b] = j < k ? *reinterpret_cast<const float4*>(part + at) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const int j = j0 + b * STEP;
+      const float* part = j == 0 ? p.first : p.rest + j * (2 * S::kPart);
+      m[b] = kNoMax;
+      l[b] = 0.0f;
+      x[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (j < p.n) {
+        m[b] = part[r];
+        l[b] = part[r + S::kRows];
+        x[b] = *reinterpret_cast<const float4*>(part + at);
+      }
     }
 #pragma unroll
     for (int b = 0; b < B; ++b) join_part(m[b], l[b], x[b], top, z, v);
   }
-  sums[warp][lane] = v;
-  tops[warp][lane] = make_float2(top, z);
-  __syncthreads();
-  if (warp != 0) return;
-#pragma unroll
-  for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, tops[w][lane].x);
-  v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  z = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    const float2 t = tops[w][lane];
-    const float4 x = sums[w][lane];
-    const float e = exp2_fast(t.x - top);
-    z = fmaf(t.y, e, z);
-    v.x = fmaf(x.x, e, v.x), v.y = fmaf(x.y, e, v.y), v.z = fmaf(x.z, e, v.z), v.w = fmaf(x.w, e, v.w);
+}
+
+// Many items, few parts each: CTA (i, y) looks at record i + 1; a warp a slice.
+constexpr int kJoinWarps = 4;
+template <int DC, int NM>
+__global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __grid_constant__ AttendArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) + 1;
+  const AttHeader h = *reinterpret_cast<const AttHeader*>(a.workspace);
+  AttSpan s;
+  if (!split_at(a, h, i, s)) return;
+  const int lane = threadIdx.x & 31;
+  const Split p = split_of<DC, NM>(a, h, i, s, lane);
+  for (int k = threadIdx.x / 32 + kJoinWarps * blockIdx.y; k < AttShape<DC, NM>::kSlices; k += kJoinWarps * gridDim.y) {
+    float top, z;
+    float4 v;
+    join_parts<DC, NM, 1, 4>(p, k, lane, 0, top, z, v);
+    join_out<DC, NM>(a, s, k, lane, top, z, v);
   }
-  join_out<DC, NM>(a, f, slice, lane, top, z, v);
+}
+
+// Few items, many parts: CTA (i, slice) looks at kFewRecords; its warps share the parts.  (A CTA to every record and
+// slice took 2 us to find that most have nothing to do.)
+constexpr int kFewWarps = 8, kFewRecords = 8, kFewItems = 64;
+template <int DC, int NM>
+__global__ void __launch_bounds__(32 * kFewWarps) attend_join_few_kernel(const __grid_constant__ AttendArgs a) {
+  __shared__ float4 sums[kFewWarps][32];
+  __shared__ float2 tops[kFewWarps][32];
+  pdl_wait();
+  pdl_trigger();
+  const AttHeader h = *reinterpret_cast<const AttHeader*>(a.workspace);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = blockIdx.y;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kFewRecords + 1;
+  AttSpan s;
+  uint32_t todo = __ballot_sync(0xffffffffu, lane < kFewRecords && split_at(a, h, i0 + lane, s));
+  for (; todo; todo &= todo - 1) {
+    const int64_t i = i0 + __ffs(todo) - 1;
+    split_at(a, h, i, s);
+    const Split p = split_of<DC, NM>(a, h, i, s, lane);
+    float top, z;
+    float4 v;
+    join_parts<DC, NM, kFewWarps, 5>(p, slice, lane, warp, top, z, v);
+    sums[warp][lane] = v;
+    tops[warp][lane] = make_float2(top, z);
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int w = 1; w < kFewWarps; ++w) join_part(tops[w][lane].x, tops[w][lane].y, sums[w][lane], top, z, v);
+      join_out<DC, NM>(a, s, slice, lane, top, z, v);
+    }
+    __syncthreads();
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -949,7 +1001,12 @@ static int launch_attend_t(const AttendArgs& a, cudaStream_t st, bool pdl) {
       return a.c.format == 0 ? launch_part<DC, true, 0, NM>(cfg, a) : launch_part<DC, true, 1, NM>(cfg, a);
     return a.c.format == 0 ? launch_part<DC, false, 0, NM>(cfg, a) : launch_part<DC, false, 1, NM>(cfg, a);
   }
-  cfg.gridDim = dim3(static_cast<unsigned>(a.ctas - 1), S::kSlices);
+  if (static_cast<int64_t>(a.T) * a.c.heads * a.subs <= kFewItems) {
+    cfg.gridDim = dim3(static_cast<unsigned>((a.ctas - 2) / kFewRecords + 1), S::kSlices);
+    cfg.blockDim = dim3(32 * kFewWarps);
+    return cudaLaunchKernelEx(&cfg, attend_join_few_kernel<DC, NM>, a);
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(a.ctas - 1), 2);
   cfg.blockDim = dim3(32 * kJoinWarps);
   return cudaLaunchKernelEx(&cfg, attend_join_kernel<DC, NM>, a);
 }
