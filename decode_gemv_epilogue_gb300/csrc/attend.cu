@@ -371,445 +371,446 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
   if (lane < 2) spans[warp][lane].end = 0;  // no part
   __syncwarp();
   if (start < stop) {
-  Item item;
-  {
-    int64_t before = 0;  // units of one (head, part) ahead of the group
-    int k = 0;
-    for (; k < groups; k += 32) {
-      const int64_t n = k + lane < groups ? group_units[k + lane] : 0;
-      const int64_t incl = warp_scan(n, lane) + before;
-      const uint32_t past = __ballot_sync(0xffffffffu, incl * HS > start);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        before = __shfl_sync(0xffffffffu, incl - n, l);
-        k += l;
-        break;
-      }
-      before = __shfl_sync(0xffffffffu, incl, 31);
-    }
-    const int64_t n = units_at<CT>(a, k * 32 + lane);
-    const int64_t incl = warp_scan(n, lane) + before;
-    const int l = __ffs(__ballot_sync(0xffffffffu, incl * HS > start)) - 1;
-    item_at<CT>(a, k * 32 + l, item);
-    const int64_t b = __shfl_sync(0xffffffffu, incl - n, l) * HS;
-    item.hs = static_cast<int>((start - b) / (item.chunks + 1));
-    item.begin = b + static_cast<int64_t>(item.hs) * (item.chunks + 1);
-  }
-  if (start == cta_start && lane == 0) {
-    if (blockIdx.x == 0) *reinterpret_cast<AttHeader*>(a.workspace) = head;
-    reinterpret_cast<AttSpan*>(reinterpret_cast<uint8_t*>(a.workspace) + kAttHead)[blockIdx.x] = span_of(item);
-  }
-  uint8_t* ring = smem + warp * 4 * S::kStage;
-  static_assert(S::kRows * DC * 4 <= 2 * S::kStage, "a warp's two parts fit its stages");
-  const uint32_t ring_at = smem_u32(ring);
-  float* ring_scales = reinterpret_cast<float*>(smem + S::kScalesAt) + warp * 2 * CT;
-  uint8_t* qs = smem + S::kQueriesAt + warp * NM * KS * 512;
-
-  const int page_log2 = a.c.page_log2, page_mask = (1 << page_log2) - 1, table_ld = static_cast<int>(a.c.table_ld);
-  const int64_t page_bytes = static_cast<int64_t>(a.c.heads * D) << page_log2;
-  const int64_t page_scales = static_cast<int64_t>(a.c.heads) << (page_log2 - a.c.block_log2);
-  const bool one_page = CT == 16 || page_log2 >= 5;  // a chunk never crosses a page's end
-  const int unit_inv = 65536 / U16 + 1;              // n / U16 = n * unit_inv >> 16 for n < CT * 16
-  const int scale_lane = (lane & ~7) + column_of<DC>(lane & 7);  // scales lie in the order of the columns
-  // where a lane's copies go, less 512 bytes a copy: repeating after kPlaces
-  constexpr int kPlaces = DC == 256 ? 4 : 2;
-  uint32_t copy_to[kPlaces];
-#pragma unroll
-  for (int k = 0; k < kPlaces; ++k)
-    copy_to[k] = ring_at + smem_place<DC>(lane / (DC / 16) + k * (512 / DC), lane % (DC / 16)) - k * 512;
-
-  // What a chunk's copies need of its item.
-  struct Source {
-    int seq, first, lo, hi, head;  // first: of the item's chunks, among those of its sequence
-  };
-  auto source_of = [&](const Item& it) {
-    return Source{it.seq, it.lo / CT, it.lo, it.hi, it.hs / a.subs};
-  };
-  struct Pages {
-    int id[KG];
-  };
-  // The pages of a chunk's 16-token halves, as the table has them (-1: outside the table).
-  auto pages_of = [&](const Source& s, int chunk) {
-    Pages p;
-    const int i = (s.first + chunk) * CT >> page_log2;
-    const int32_t* row = a.c.table + s.seq * a.c.table_ld;
-    p.id[0] = s.hi > 0 && i < table_ld ? row[i] : -1;
-    if (KG == 2) p.id[KG - 1] = one_page ? p.id[0] : s.hi > 0 && i + 1 < table_ld ? row[i + 1] : -1;
-    return p;
-  };
-  float key_scale = 0.0f, value_scale = 0.0f;  // of token `lane` of the chunk fetched last, on their way
-  // Copies a chunk's keys and values into stage chunk % 2.  Tokens outside [lo, hi) or without a page: zeros,
-  // scales and codes.  Returns which tokens of the chunk those are.
-  auto fetch = [&](const Source& s, int chunk, const Pages& pages) {
-    const int p0 = (s.first + chunk) * CT, slot = p0 & page_mask;
-    const uint32_t stage = (chunk & 1) * 2 * S::kStage;
-    const int64_t head_at = static_cast<int64_t>(s.head * D) << page_log2, n_pages = a.c.n_pages;
-    const int64_t head_scales = static_cast<int64_t>(s.head) << (page_log2 - a.c.block_log2);
-    bool held[KG];
-#pragma unroll
-    for (int h = 0; h < KG; ++h) held[h] = static_cast<uint32_t>(pages.id[h]) < n_pages;
-    uint32_t hidden = 0;
-    key_scale = value_scale = 0.0f;
-    if (EXACT && one_page && held[0] && p0 >= s.lo && p0 + CT <= s.hi) {
-      const int64_t at = pages.id[0] * page_bytes + (head_at + slot * D + lane * 16);
-      const uint8_t* k = a.c.k + at;
-      const uint8_t* v = a.c.v + at;
-#pragma unroll
-      for (int i = 0; i < CT * DC / 512; ++i) {
-        cp_async16(copy_to[i % kPlaces] + stage + i * 512, k + i * 512, true);
-        cp_async16(copy_to[i % kPlaces] + stage + S::kStage + i * 512, v + i * 512, true);
-      }
-      const int64_t sc = pages.id[0] * page_scales + (head_scales + ((slot + (lane & (CT - 1))) >> a.c.block_log2));
-      key_scale = a.c.k_scale[sc];
-      value_scale = a.c.v_scale[sc];
-    } else {
-#pragma unroll 2
-      for (int i = 0; i < CT * DC / 512; ++i) {
-        const int n = lane + 32 * i, row = n * unit_inv >> 16, u = n - row * U16;
-        if (row < CT) {
-          const bool up = KG == 2 && row >= 16;
-          const bool on = (up ? held[KG - 1] : held[0]) && p0 + row >= s.lo && p0 + row < s.hi;
-          const int64_t at = (up ? pages.id[KG - 1] : pages.id[0]) * page_bytes +
-                             (head_at + ((slot + row) & page_mask) * D + u * 16);
-          const uint32_t to = ring_at + stage + smem_place<DC>(row, u);
-          cp_async16(to, a.c.k + (on ? at : 0), on);
-          cp_async16(to + S::kStage, a.c.v + (on ? at : 0), on);
+    Item item;
+    {
+      int64_t before = 0;  // units of one (head, part) ahead of the group
+      int k = 0;
+      for (; k < groups; k += 32) {
+        const int64_t n = k + lane < groups ? group_units[k + lane] : 0;
+        const int64_t incl = warp_scan(n, lane) + before;
+        const uint32_t past = __ballot_sync(0xffffffffu, incl * HS > start);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          before = __shfl_sync(0xffffffffu, incl - n, l);
+          k += l;
+          break;
         }
+        before = __shfl_sync(0xffffffffu, incl, 31);
       }
-      const int j = lane & (CT - 1);
-      const bool up = KG == 2 && j >= 16;
-      const bool on = (up ? held[KG - 1] : held[0]) && p0 + j >= s.lo && p0 + j < s.hi;
-      hidden = __ballot_sync(0xffffffffu, !on);
-      if (on) {
-        const int64_t sc = (up ? pages.id[KG - 1] : pages.id[0]) * page_scales +
-                           (head_scales + (((slot + j) & page_mask) >> a.c.block_log2));
+      const int64_t n = units_at<CT>(a, k * 32 + lane);
+      const int64_t incl = warp_scan(n, lane) + before;
+      const int l = __ffs(__ballot_sync(0xffffffffu, incl * HS > start)) - 1;
+      item_at<CT>(a, k * 32 + l, item);
+      const int64_t b = __shfl_sync(0xffffffffu, incl - n, l) * HS;
+      item.hs = static_cast<int>((start - b) / (item.chunks + 1));
+      item.begin = b + static_cast<int64_t>(item.hs) * (item.chunks + 1);
+    }
+    if (start == cta_start && lane == 0) {
+      if (blockIdx.x == 0) *reinterpret_cast<AttHeader*>(a.workspace) = head;
+      reinterpret_cast<AttSpan*>(reinterpret_cast<uint8_t*>(a.workspace) + kAttHead)[blockIdx.x] = span_of(item);
+    }
+    uint8_t* ring = smem + warp * 4 * S::kStage;
+    static_assert(S::kRows * DC * 4 <= 2 * S::kStage, "a warp's two parts fit its stages");
+    const uint32_t ring_at = smem_u32(ring);
+    float* ring_scales = reinterpret_cast<float*>(smem + S::kScalesAt) + warp * 2 * CT;
+    uint8_t* qs = smem + S::kQueriesAt + warp * NM * KS * 512;
+
+    const int page_log2 = a.c.page_log2, page_mask = (1 << page_log2) - 1, table_ld = static_cast<int>(a.c.table_ld);
+    const int64_t page_bytes = static_cast<int64_t>(a.c.heads * D) << page_log2;
+    const int64_t page_scales = static_cast<int64_t>(a.c.heads) << (page_log2 - a.c.block_log2);
+    const bool one_page = CT == 16 || page_log2 >= 5;  // a chunk never crosses a page's end
+    const int unit_inv = 65536 / U16 + 1;              // n / U16 = n * unit_inv >> 16 for n < CT * 16
+    const int scale_lane = (lane & ~7) + column_of<DC>(lane & 7);  // scales lie in the order of the columns
+    // where a lane's copies go, less 512 bytes a copy: repeating after kPlaces
+    constexpr int kPlaces = DC == 256 ? 4 : 2;
+    uint32_t copy_to[kPlaces];
+#pragma unroll
+    for (int k = 0; k < kPlaces; ++k)
+      copy_to[k] = ring_at + smem_place<DC>(lane / (DC / 16) + k * (512 / DC), lane % (DC / 16)) - k * 512;
+
+    // What a chunk's copies need of its item.
+    struct Source {
+      int seq, first, lo, hi, head;  // first: of the item's chunks, among those of its sequence
+    };
+    auto source_of = [&](const Item& it) {
+      return Source{it.seq, it.lo / CT, it.lo, it.hi, it.hs / a.subs};
+    };
+    struct Pages {
+      int id[KG];
+    };
+    // The pages of a chunk's 16-token halves, as the table has them (-1: outside the table).
+    auto pages_of = [&](const Source& s, int chunk) {
+      Pages p;
+      const int i = (s.first + chunk) * CT >> page_log2;
+      const int32_t* row = a.c.table + s.seq * a.c.table_ld;
+      p.id[0] = s.hi > 0 && i < table_ld ? row[i] : -1;
+      if (KG == 2) p.id[KG - 1] = one_page ? p.id[0] : s.hi > 0 && i + 1 < table_ld ? row[i + 1] : -1;
+      return p;
+    };
+    float key_scale = 0.0f, value_scale = 0.0f;  // of token `lane` of the chunk fetched last, on their way
+    // Copies a chunk's keys and values into stage chunk % 2.  Tokens outside [lo, hi) or without a page: zeros,
+    // scales and codes.  Returns which tokens of the chunk those are.
+    auto fetch = [&](const Source& s, int chunk, const Pages& pages) {
+      const int p0 = (s.first + chunk) * CT, slot = p0 & page_mask;
+      const uint32_t stage = (chunk & 1) * 2 * S::kStage;
+      const int64_t head_at = static_cast<int64_t>(s.head * D) << page_log2, n_pages = a.c.n_pages;
+      const int64_t head_scales = static_cast<int64_t>(s.head) << (page_log2 - a.c.block_log2);
+      bool held[KG];
+#pragma unroll
+      for (int h = 0; h < KG; ++h) held[h] = static_cast<uint32_t>(pages.id[h]) < n_pages;
+      uint32_t hidden = 0;
+      key_scale = value_scale = 0.0f;
+      if (EXACT && one_page && held[0] && p0 >= s.lo && p0 + CT <= s.hi) {
+        const int64_t at = pages.id[0] * page_bytes + (head_at + slot * D + lane * 16);
+        const uint8_t* k = a.c.k + at;
+        const uint8_t* v = a.c.v + at;
+#pragma unroll
+        for (int i = 0; i < CT * DC / 512; ++i) {
+          cp_async16(copy_to[i % kPlaces] + stage + i * 512, k + i * 512, true);
+          cp_async16(copy_to[i % kPlaces] + stage + S::kStage + i * 512, v + i * 512, true);
+        }
+        const int64_t sc = pages.id[0] * page_scales + (head_scales + ((slot + (lane & (CT - 1))) >> a.c.block_log2));
         key_scale = a.c.k_scale[sc];
         value_scale = a.c.v_scale[sc];
-      }
-    }
-    cp_commit();
-    return hidden;
-  };
-  // The item's chunks [c0, c1) of this warp's stretch.
-  auto stretch = [&](const Item& it, int& c0, int& c1) {
-    const int64_t from = start - it.begin - 1, to = stop - it.begin - 1;
-    c0 = from < 0 ? 0 : static_cast<int>(from);
-    c1 = to < it.chunks ? static_cast<int>(to) : it.chunks;
-  };
-
-  int c0, c1;
-  stretch(item, c0, c1);
-  Source src = source_of(item);
-  uint32_t hidden_next = c0 < c1 ? fetch(src, c0, pages_of(src, c0)) : 0;
-  Pages pages = pages_of(src, c0 + 1);  // of the chunk that is fetched next: looked up a chunk ahead
-
-  for (;;) {
-    // ---- the item's queries, hi and lo parts in the order of the instructions' rows: of row g, lane (g, c4)
-    // takes units c4, c4 + 4, .. as it does of a key
-    uint4 qr[S::kQRegs ? KS : 1];
-    float f[NM];  // of the products: the query's power of two, scale and log2(e)
-    int lo[NM], hi[NM];
-#pragma unroll
-    for (int i = 0; i < NM; ++i) {
-      int t, head;
-      const bool live = row_of(a, item.t0, item.n, item.hs, 8 * i + g, t, head);
-      const int64_t row = t * a.ldq + static_cast<int64_t>(head) * D;
-      float4 v[KS];
-      uint32_t top = 0;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const int d = (k / 4) * 64 + c4 * 16 + (k % 4) * 4;
-        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (live && d < D) {
-          const int64_t at = row + d;
-          if (a.type == 0) {
-            const float* p = static_cast<const float*>(a.q) + at;
-            v[k] = a.vec ? load4(p) : make_float4(p[0], p[1], p[2], p[3]);
-          } else {
-            const __half* p = static_cast<const __half*>(a.q) + at;
-            v[k] = a.vec ? load4(p) : make_float4(load1(p), load1(p + 1), load1(p + 2), load1(p + 3));
-          }
-        }
-        top = max(top, max(max(__float_as_uint(v[k].x) & 0x7fffffffu, __float_as_uint(v[k].y) & 0x7fffffffu),
-                           max(__float_as_uint(v[k].z) & 0x7fffffffu, __float_as_uint(v[k].w) & 0x7fffffffu)));
-      }
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // |q| 2^-x lies in [2^14, 2^15) for the largest
-      int x = static_cast<int>(top >> 23) - 127 - 14;
-      x = x < -110 ? -110 : x;
-      const bool number = top < 0x7f800000u;
-      const float w = __uint_as_float(static_cast<uint32_t>(127 - x) << 23);
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        uint4 h;
-        const float e[4] = {number ? v[k].x * w : 0.0f, number ? v[k].y * w : 0.0f, number ? v[k].z * w : 0.0f,
-                            number ? v[k].w * w : 0.0f};
-        split2(e[0], e[kSecond<FMT>], h.x, h.y);
-        split2(e[3 - kSecond<FMT>], e[3], h.z, h.w);
-        if constexpr (S::kQRegs)
-          qr[k] = h;
-        else
-          *reinterpret_cast<uint4*>(qs + ((i * KS + k) * 32 + lane) * 16) = h;  // read back by this lane alone
-      }
-      f[i] = number ? a.scale * __uint_as_float(static_cast<uint32_t>(127 + x) << 23) : __uint_as_float(0x7fffffffu);
-      lo[i] = hi[i] = 0;
-      int s;
-      if (live) keys_of(a, t, s, lo[i], hi[i]);
-    }
-
-    float2 o[NM][NO];
-    float m[NM], l[NM];
-#pragma unroll
-    for (int i = 0; i < NM; ++i) {
-      m[i] = kNoMax;
-      l[i] = 0.0f;
-#pragma unroll
-      for (int n = 0; n < NO; ++n) o[i][n] = make_float2(0.0f, 0.0f);
-    }
-    // biased exponent of the power of two, above every scale so far, that the values' scales are taken by; at
-    // least that of the format's smallest scale
-    uint32_t vexp = 127 - 111;
-    const int t0 = token_of<DC>(2 * c4), t1 = token_of<DC>(2 * c4 + 1);  // this lane's columns
-
-    for (int c = c0; c < c1; ++c) {
-      const uint32_t hidden = hidden_next;
-      if (CT == 32 || lane < CT) {
-        ring_scales[scale_lane] = key_scale;
-        ring_scales[CT + scale_lane] = value_scale;
-      }
-      const uint32_t vtop = __reduce_max_sync(0xffffffffu, min(__float_as_uint(value_scale), 0x7e000000u));
-      if (c + 1 < c1) {
-        hidden_next = fetch(src, c + 1, pages);
-        pages = pages_of(src, c + 2);
-        cp_wait<1>();
       } else {
-        cp_wait<0>();
-      }
-      __syncwarp();
-      const uint8_t* kt = ring + (c & 1) * 2 * S::kStage;
-      const uint8_t* vt = kt + S::kStage;
-      const float* ks = ring_scales;
-      const float* vs = ks + CT;
-      const int p0 = (src.first + c) * CT;
-
-      // ---- scores (powers of two)
-      float2 x[NM][NT];
-      {
-        float s[NM][NT][4];
-#pragma unroll
-        for (int u = 0; u < DC / 64; ++u) {
-          uint4 q[NM][4];
-#pragma unroll
-          for (int i = 0; i < NM; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if constexpr (S::kQRegs)
-                q[i][j] = qr[u * 4 + j];
-              else
-                q[i][j] = *reinterpret_cast<const uint4*>(qs + ((i * KS + u * 4 + j) * 32 + lane) * 16);
-            }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            uint4 w = make_uint4(0, 0, 0, 0);  // a unit that the head does not have
-            if (EXACT || c4 + 4 * u < U16)
-              w = *reinterpret_cast<const uint4*>(kt + further<DC>(smem_place<DC>(token_of<DC>(g), c4 + 4 * u), n));
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t b0, b1;
-              pairs_of<FMT>(magic, ww[j], b0, b1);
-#pragma unroll
-              for (int i = 0; i < NM; ++i) u + j == 0 ? mma0(s[i][n], q[i][j], b0, b1) : mma(s[i][n], q[i][j], b0, b1);
-            }
+#pragma unroll 2
+        for (int i = 0; i < CT * DC / 512; ++i) {
+          const int n = lane + 32 * i, row = n * unit_inv >> 16, u = n - row * U16;
+          if (row < CT) {
+            const bool up = KG == 2 && row >= 16;
+            const bool on = (up ? held[KG - 1] : held[0]) && p0 + row >= s.lo && p0 + row < s.hi;
+            const int64_t at = (up ? pages.id[KG - 1] : pages.id[0]) * page_bytes +
+                               (head_at + ((slot + row) & page_mask) * D + u * 16);
+            const uint32_t to = ring_at + stage + smem_place<DC>(row, u);
+            cp_async16(to, a.c.k + (on ? at : 0), on);
+            cp_async16(to + S::kStage, a.c.v + (on ? at : 0), on);
           }
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float2 k2 = *reinterpret_cast<const float2*>(ks + 8 * n + 2 * c4);
-#pragma unroll
-          for (int i = 0; i < NM; ++i)
-            x[i][n] = fmul2(fadd2(make_float2(s[i][n][0], s[i][n][1]), make_float2(s[i][n][2], s[i][n][3])),
-                            fmul2(k2, make_float2(f[i], f[i])));
+        const int j = lane & (CT - 1);
+        const bool up = KG == 2 && j >= 16;
+        const bool on = (up ? held[KG - 1] : held[0]) && p0 + j >= s.lo && p0 + j < s.hi;
+        hidden = __ballot_sync(0xffffffffu, !on);
+        if (on) {
+          const int64_t sc = (up ? pages.id[KG - 1] : pages.id[0]) * page_scales +
+                             (head_scales + (((slot + j) & page_mask) >> a.c.block_log2));
+          key_scale = a.c.k_scale[sc];
+          value_scale = a.c.v_scale[sc];
         }
       }
+      cp_commit();
+      return hidden;
+    };
+    // The item's chunks [c0, c1) of this warp's stretch.
+    auto stretch = [&](const Item& it, int& c0, int& c1) {
+      const int64_t from = start - it.begin - 1, to = stop - it.begin - 1;
+      c0 = from < 0 ? 0 : static_cast<int>(from);
+      c1 = to < it.chunks ? static_cast<int>(to) : it.chunks;
+    };
 
-      // ---- softmax; the weights, times the values' scales, as instructions' rows
-      const uint32_t vnow = max(vexp, (vtop >> 23) + 1);
-      // 2^(kWeightBits - (vnow - 127)): weights times it lie below 2^8
-      const float vinv = __uint_as_float((254 + kWeightBits - vnow) << 23);
-      const float vstep = vexp == vnow ? 1.0f : exp2_fast(static_cast<float>(static_cast<int>(vexp) - static_cast<int>(vnow)));
-      vexp = vnow;
-      uint4 pf[NM][KG];
-      float alpha[NM];
+    int c0, c1;
+    stretch(item, c0, c1);
+    Source src = source_of(item);
+    uint32_t hidden_next = c0 < c1 ? fetch(src, c0, pages_of(src, c0)) : 0;
+    Pages pages = pages_of(src, c0 + 1);  // of the chunk that is fetched next: looked up a chunk ahead
+
+    for (;;) {
+      // ---- the item's queries, hi and lo parts in the order of the instructions' rows: of row g, lane (g, c4)
+      // takes units c4, c4 + 4, .. as it does of a key
+      uint4 qr[S::kQRegs ? KS : 1];
+      float f[NM];  // of the products: the query's power of two, scale and log2(e)
+      int lo[NM], hi[NM];
 #pragma unroll
       for (int i = 0; i < NM; ++i) {
-        const bool whole = hidden == 0 && p0 >= lo[i] && p0 + CT <= hi[i];
-        if (!whole) {
+        int t, head;
+        const bool live = row_of(a, item.t0, item.n, item.hs, 8 * i + g, t, head);
+        const int64_t row = t * a.ldq + static_cast<int64_t>(head) * D;
+        float4 v[KS];
+        uint32_t top = 0;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int j0 = 8 * n + t0, j1 = 8 * n + t1;
-            if ((hidden >> j0 & 1) || p0 + j0 < lo[i] || p0 + j0 >= hi[i]) x[i][n].x = -INFINITY;
-            if ((hidden >> j1 & 1) || p0 + j1 < lo[i] || p0 + j1 >= hi[i]) x[i][n].y = -INFINITY;
-          }
-        }
-        float top = kNoMax;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) top = fmaxf(top, fmaxf(x[i][n].x, x[i][n].y));
-        top = fmaxf(m[i], quad_max(top));
-        alpha[i] = exp2_fast(m[i] - top);
-        m[i] = top;
-        float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float2 v2 = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c4);
-          const float2 e = fsub2(x[i][n], make_float2(top, top));
-          const float2 p = make_float2(exp2_fast(e.x), exp2_fast(e.y));
-          sum = fadd2(sum, p);
-          float2 y = fmul2(p, fmul2(v2, make_float2(vinv, vinv)));
-          if (!whole) {  // a masked token's weight is zero whatever lies in its scale
-            if (x[i][n].x == -INFINITY) y.x = 0.0f;
-            if (x[i][n].y == -INFINITY) y.y = 0.0f;
-          }
-          uint32_t h, w;
-          split2(y.x, y.y, h, w);
-          if (n % 2 == 0) {
-            pf[i][n / 2].x = h;
-            pf[i][n / 2].y = w;
-          } else {
-            pf[i][n / 2].z = h;
-            pf[i][n / 2].w = w;
-          }
-        }
-        l[i] = l[i] * alpha[i] + (sum.x + sum.y);
-        alpha[i] *= vstep;
-      }
-
-      // ---- values
-#pragma unroll
-      for (int u = 0; u < UC; ++u) {
-        uint32_t raw[KG][4][UB / 4];
-#pragma unroll
-        for (int k = 0; k < KG; ++k)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // this lane's unit of the tokens that are its k indices: columns 2 c4 and 2 c4 + 1 of two eights
-            const int t = i % 2 ? t1 : t0;
-            const uint8_t* at = vt + further<DC>(DC == 64 ? smem_place<DC>(t, g >> 1) + (g & 1) * 8
-                                                          : smem_place<DC>(t, value_unit<DC>(g) + 8 * u), 2 * k + i / 2);
-            if constexpr (UB == 16) {
-              const uint4 w = *reinterpret_cast<const uint4*>(at);
-              raw[k][i][0] = w.x, raw[k][i][1] = w.y, raw[k][i][2] = w.z, raw[k][i][3] = w.w;
+        for (int k = 0; k < KS; ++k) {
+          const int d = (k / 4) * 64 + c4 * 16 + (k % 4) * 4;
+          v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (live && d < D) {
+            const int64_t at = row + d;
+            if (a.type == 0) {
+              const float* p = static_cast<const float*>(a.q) + at;
+              v[k] = a.vec ? load4(p) : make_float4(p[0], p[1], p[2], p[3]);
             } else {
-              const uint2 w = *reinterpret_cast<const uint2*>(at);
-              raw[k][i][0] = w.x, raw[k][i][1] = w.y;
+              const __half* p = static_cast<const __half*>(a.q) + at;
+              v[k] = a.vec ? load4(p) : make_float4(load1(p), load1(p + 1), load1(p + 2), load1(p + 3));
             }
           }
+          top = max(top, max(max(__float_as_uint(v[k].x) & 0x7fffffffu, __float_as_uint(v[k].y) & 0x7fffffffu),
+                             max(__float_as_uint(v[k].z) & 0x7fffffffu, __float_as_uint(v[k].w) & 0x7fffffffu)));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // |q| 2^-x lies in [2^14, 2^15) for the largest
+        int x = static_cast<int>(top >> 23) - 127 - 14;
+        x = x < -110 ? -110 : x;
+        const bool number = top < 0x7f800000u;
+        const float w = __uint_as_float(static_cast<uint32_t>(127 - x) << 23);
 #pragma unroll
-        for (int w = 0; w < UB / 4; ++w) {
-          float acc[NM][4][4];
+        for (int k = 0; k < KS; ++k) {
+          uint4 h;
+          const float e[4] = {number ? v[k].x * w : 0.0f, number ? v[k].y * w : 0.0f, number ? v[k].z * w : 0.0f,
+                              number ? v[k].w * w : 0.0f};
+          split2(e[0], e[kSecond<FMT>], h.x, h.y);
+          split2(e[3 - kSecond<FMT>], e[3], h.z, h.w);
+          if constexpr (S::kQRegs)
+            qr[k] = h;
+          else
+            *reinterpret_cast<uint4*>(qs + ((i * KS + k) * 32 + lane) * 16) = h;  // read back by this lane alone
+        }
+        f[i] = number ? a.scale * __uint_as_float(static_cast<uint32_t>(127 + x) << 23) : __uint_as_float(0x7fffffffu);
+        lo[i] = hi[i] = 0;
+        int s;
+        if (live) keys_of(a, t, s, lo[i], hi[i]);
+      }
+
+      float2 o[NM][NO];
+      float m[NM], l[NM];
 #pragma unroll
-          for (int k = 0; k < KG; ++k) {
-            uint32_t b0[4], b1[4];
-            pairs_of<FMT>(magic, weave<FMT>(raw[k][0][w], raw[k][1][w], false), b0[0], b0[1]);
-            pairs_of<FMT>(magic, weave<FMT>(raw[k][0][w], raw[k][1][w], true), b0[2], b0[3]);
-            pairs_of<FMT>(magic, weave<FMT>(raw[k][2][w], raw[k][3][w], false), b1[0], b1[1]);
-            pairs_of<FMT>(magic, weave<FMT>(raw[k][2][w], raw[k][3][w], true), b1[2], b1[3]);
+      for (int i = 0; i < NM; ++i) {
+        m[i] = kNoMax;
+        l[i] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NO; ++n) o[i][n] = make_float2(0.0f, 0.0f);
+      }
+      // biased exponent of the power of two, above every scale so far, that the values' scales are taken by; at
+      // least that of the format's smallest scale
+      uint32_t vexp = 127 - 111;
+      const int t0 = token_of<DC>(2 * c4), t1 = token_of<DC>(2 * c4 + 1);  // this lane's columns
+
+      for (int c = c0; c < c1; ++c) {
+        const uint32_t hidden = hidden_next;
+        if (CT == 32 || lane < CT) {
+          ring_scales[scale_lane] = key_scale;
+          ring_scales[CT + scale_lane] = value_scale;
+        }
+        // (a scale that is not finite makes its own rows NaN, and is no measure for the others)
+        const uint32_t vbits = __float_as_uint(value_scale), vtop = __reduce_max_sync(0xffffffffu, vbits < 0x7f800000u ? vbits : 0u);
+        if (c + 1 < c1) {
+          hidden_next = fetch(src, c + 1, pages);
+          pages = pages_of(src, c + 2);
+          cp_wait<1>();
+        } else {
+          cp_wait<0>();
+        }
+        __syncwarp();
+        const uint8_t* kt = ring + (c & 1) * 2 * S::kStage;
+        const uint8_t* vt = kt + S::kStage;
+        const float* ks = ring_scales;
+        const float* vs = ks + CT;
+        const int p0 = (src.first + c) * CT;
+
+        // ---- scores (powers of two)
+        float2 x[NM][NT];
+        {
+          float s[NM][NT][4];
+#pragma unroll
+          for (int u = 0; u < DC / 64; ++u) {
+            uint4 q[NM][4];
 #pragma unroll
             for (int i = 0; i < NM; ++i)
 #pragma unroll
-              for (int d = 0; d < 4; ++d)
-                k == 0 ? mma0(acc[i][d], pf[i][k], b0[d], b1[d]) : mma(acc[i][d], pf[i][k], b0[d], b1[d]);
+              for (int j = 0; j < 4; ++j) {
+                if constexpr (S::kQRegs)
+                  q[i][j] = qr[u * 4 + j];
+                else
+                  q[i][j] = *reinterpret_cast<const uint4*>(qs + ((i * KS + u * 4 + j) * 32 + lane) * 16);
+              }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              uint4 w = make_uint4(0, 0, 0, 0);  // a unit that the head does not have
+              if (EXACT || c4 + 4 * u < U16)
+                w = *reinterpret_cast<const uint4*>(kt + further<DC>(smem_place<DC>(token_of<DC>(g), c4 + 4 * u), n));
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t b0, b1;
+                pairs_of<FMT>(magic, ww[j], b0, b1);
+#pragma unroll
+                for (int i = 0; i < NM; ++i) u + j == 0 ? mma0(s[i][n], q[i][j], b0, b1) : mma(s[i][n], q[i][j], b0, b1);
+              }
+            }
           }
 #pragma unroll
-          for (int i = 0; i < NM; ++i)
+          for (int n = 0; n < NT; ++n) {
+            const float2 k2 = *reinterpret_cast<const float2*>(ks + 8 * n + 2 * c4);
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-              float2& at = o[i][(u * UB / 4 + w) * 4 + d];
-              at = ffma2(at, make_float2(alpha[i], alpha[i]),
-                         fadd2(make_float2(acc[i][d][0], acc[i][d][1]), make_float2(acc[i][d][2], acc[i][d][3])));
-            }
+            for (int i = 0; i < NM; ++i)
+              x[i][n] = fmul2(fadd2(make_float2(s[i][n][0], s[i][n][1]), make_float2(s[i][n][2], s[i][n][3])),
+                              fmul2(k2, make_float2(f[i], f[i])));
+          }
         }
-      }
-      __syncwarp();  // the stage and the scales may be written again
-    }
 
-    // ---- the next item's first chunk starts on its way
-    const int64_t end = item.begin + item.chunks + 1;
-    const bool last = end >= stop;
-    Item next = item;
-    if (!last) {
-      if (item.hs + 1 < HS) {
-        ++next.hs;
-      } else {
-        next.hs = 0;
-        int t = item.t0 + item.n;
-        while (!item_at<CT>(a, t, next) && t < a.T - 1) ++t;  // (the token behind an item begins one)
-      }
-      next.begin = end;
-      stretch(next, c0, c1);
-      src = source_of(next);
-      if (c0 < c1) hidden_next = fetch(src, c0, pages_of(src, c0));
-      pages = pages_of(src, c0 + 1);
-    }
-
-    // ---- results, or a part to be joined: the warp's last one into its stages, which nothing comes into any
-    // more, one before into the workspace
-    const float back = __uint_as_float((vexp - kWeightBits) << 23);
-    auto give = [&](auto put_sums, auto put_row, bool divide) {
+        // ---- softmax; the weights, times the values' scales, as instructions' rows
+        const uint32_t vnow = max(vexp, (vtop >> 23) + 1);
+        // 2^(kWeightBits - (vnow - 127)): weights times it lie below 2^8
+        const float vinv = __uint_as_float((254 + kWeightBits - vnow) << 23);
+        const float vstep = vexp == vnow ? 1.0f : exp2_fast(static_cast<float>(static_cast<int>(vexp) - static_cast<int>(vnow)));
+        vexp = vnow;
+        uint4 pf[NM][KG];
+        float alpha[NM];
 #pragma unroll
-      for (int i = 0; i < NM; ++i) {
-        const float z = quad_sum(l[i]);
-        const float inv = !divide ? back : z == 0.0f ? 0.0f : back / z;  // no keys: zeros
-        int t, head;
-        const bool live = row_of(a, item.t0, item.n, item.hs, 8 * i + g, t, head);
-        const int64_t row = live ? t * a.ld_dst + static_cast<int64_t>(head) * D : -1;
+        for (int i = 0; i < NM; ++i) {
+          const bool whole = hidden == 0 && p0 >= lo[i] && p0 + CT <= hi[i];
+          if (!whole) {
 #pragma unroll
-        for (int u = 0; u < UC; ++u)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int n = 0; n < UB; n += 4) {
-              const float2* x = &o[i][u * UB + n];
-              const float4 v = e == 0 ? make_float4(x[0].x * inv, x[1].x * inv, x[2].x * inv, x[3].x * inv)
-                                      : make_float4(x[0].y * inv, x[1].y * inv, x[2].y * inv, x[3].y * inv);
-              put_sums((((i * UC + u) * 2 + e) * (UB / 4) + n / 4) * 128 + lane * 4, row,
-                       (value_unit<DC>(2 * c4 + e) + 8 * u) * UB + n, v);
+            for (int n = 0; n < NT; ++n) {
+              const int j0 = 8 * n + t0, j1 = 8 * n + t1;
+              if ((hidden >> j0 & 1) || p0 + j0 < lo[i] || p0 + j0 >= hi[i]) x[i][n].x = -INFINITY;
+              if ((hidden >> j1 & 1) || p0 + j1 < lo[i] || p0 + j1 >= hi[i]) x[i][n].y = -INFINITY;
             }
-        if (c4 == 0) put_row(8 * i + g, row >= 0, t, head, m[i], z);
+          }
+          float top = kNoMax;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) top = fmaxf(top, fmaxf(x[i][n].x, x[i][n].y));
+          top = fmaxf(m[i], quad_max(top));
+          alpha[i] = exp2_fast(m[i] - top);
+          m[i] = top;
+          float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float2 v2 = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c4);
+            const float2 e = fsub2(x[i][n], make_float2(top, top));
+            const float2 p = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+            sum = fadd2(sum, p);
+            float2 y = fmul2(p, fmul2(v2, make_float2(vinv, vinv)));
+            if (!whole) {  // a masked token's weight is zero whatever lies in its scale
+              if (x[i][n].x == -INFINITY) y.x = 0.0f;
+              if (x[i][n].y == -INFINITY) y.y = 0.0f;
+            }
+            uint32_t h, w;
+            split2(y.x, y.y, h, w);
+            if (n % 2 == 0) {
+              pf[i][n / 2].x = h;
+              pf[i][n / 2].y = w;
+            } else {
+              pf[i][n / 2].z = h;
+              pf[i][n / 2].w = w;
+            }
+          }
+          l[i] = l[i] * alpha[i] + (sum.x + sum.y);
+          alpha[i] *= vstep;
+        }
+
+        // ---- values
+#pragma unroll
+        for (int u = 0; u < UC; ++u) {
+          uint32_t raw[KG][4][UB / 4];
+#pragma unroll
+          for (int k = 0; k < KG; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // this lane's unit of the tokens that are its k indices: columns 2 c4 and 2 c4 + 1 of two eights
+              const int t = i % 2 ? t1 : t0;
+              const uint8_t* at = vt + further<DC>(DC == 64 ? smem_place<DC>(t, g >> 1) + (g & 1) * 8
+                                                            : smem_place<DC>(t, value_unit<DC>(g) + 8 * u), 2 * k + i / 2);
+              if constexpr (UB == 16) {
+                const uint4 w = *reinterpret_cast<const uint4*>(at);
+                raw[k][i][0] = w.x, raw[k][i][1] = w.y, raw[k][i][2] = w.z, raw[k][i][3] = w.w;
+              } else {
+                const uint2 w = *reinterpret_cast<const uint2*>(at);
+                raw[k][i][0] = w.x, raw[k][i][1] = w.y;
+              }
+            }
+#pragma unroll
+          for (int w = 0; w < UB / 4; ++w) {
+            float acc[NM][4][4];
+#pragma unroll
+            for (int k = 0; k < KG; ++k) {
+              uint32_t b0[4], b1[4];
+              pairs_of<FMT>(magic, weave<FMT>(raw[k][0][w], raw[k][1][w], false), b0[0], b0[1]);
+              pairs_of<FMT>(magic, weave<FMT>(raw[k][0][w], raw[k][1][w], true), b0[2], b0[3]);
+              pairs_of<FMT>(magic, weave<FMT>(raw[k][2][w], raw[k][3][w], false), b1[0], b1[1]);
+              pairs_of<FMT>(magic, weave<FMT>(raw[k][2][w], raw[k][3][w], true), b1[2], b1[3]);
+#pragma unroll
+              for (int i = 0; i < NM; ++i)
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                  k == 0 ? mma0(acc[i][d], pf[i][k], b0[d], b1[d]) : mma(acc[i][d], pf[i][k], b0[d], b1[d]);
+            }
+#pragma unroll
+            for (int i = 0; i < NM; ++i)
+#pragma unroll
+              for (int d = 0; d < 4; ++d) {
+                float2& at = o[i][(u * UB / 4 + w) * 4 + d];
+                at = ffma2(at, make_float2(alpha[i], alpha[i]),
+                           fadd2(make_float2(acc[i][d][0], acc[i][d][1]), make_float2(acc[i][d][2], acc[i][d][3])));
+              }
+          }
+        }
+        __syncwarp();  // the stage and the scales may be written again
       }
-    };
-    if (start > item.begin || end > stop) {
-      const int slot = start >= item.begin ? 0 : 1;
-      auto put_row = [&](int r, bool, int, int, float top, float z) { part_rows[warp][slot][r] = make_float2(top, z); };
-      if (last) {
-        float* part = reinterpret_cast<float*>(ring + slot * 2 * S::kStage);
-        give([&](int at, int64_t, int, float4 v) { *reinterpret_cast<float4*>(part + at) = v; }, put_row, false);
+
+      // ---- the next item's first chunk starts on its way
+      const int64_t end = item.begin + item.chunks + 1;
+      const bool last = end >= stop;
+      Item next = item;
+      if (!last) {
+        if (item.hs + 1 < HS) {
+          ++next.hs;
+        } else {
+          next.hs = 0;
+          int t = item.t0 + item.n;
+          while (!item_at<CT>(a, t, next) && t < a.T - 1) ++t;  // (the token behind an item begins one)
+        }
+        next.begin = end;
+        stretch(next, c0, c1);
+        src = source_of(next);
+        if (c0 < c1) hidden_next = fetch(src, c0, pages_of(src, c0));
+        pages = pages_of(src, c0 + 1);
+      }
+
+      // ---- results, or a part to be joined: the warp's last one into its stages, which nothing comes into any
+      // more, one before into the workspace
+      const float back = __uint_as_float((vexp - kWeightBits) << 23);
+      auto give = [&](auto put_sums, auto put_row, bool divide) {
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+          const float z = quad_sum(l[i]);
+          const float inv = !divide ? back : z == 0.0f ? 0.0f : back / z;  // no keys: zeros
+          int t, head;
+          const bool live = row_of(a, item.t0, item.n, item.hs, 8 * i + g, t, head);
+          const int64_t row = live ? t * a.ld_dst + static_cast<int64_t>(head) * D : -1;
+#pragma unroll
+          for (int u = 0; u < UC; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int n = 0; n < UB; n += 4) {
+                const float2* x = &o[i][u * UB + n];
+                const float4 v = e == 0 ? make_float4(x[0].x * inv, x[1].x * inv, x[2].x * inv, x[3].x * inv)
+                                        : make_float4(x[0].y * inv, x[1].y * inv, x[2].y * inv, x[3].y * inv);
+                put_sums((((i * UC + u) * 2 + e) * (UB / 4) + n / 4) * 128 + lane * 4, row,
+                         (value_unit<DC>(2 * c4 + e) + 8 * u) * UB + n, v);
+              }
+          if (c4 == 0) put_row(8 * i + g, row >= 0, t, head, m[i], z);
+        }
+      };
+      if (start > item.begin || end > stop) {
+        const int slot = start >= item.begin ? 0 : 1;
+        auto put_row = [&](int r, bool, int, int, float top, float z) { part_rows[warp][slot][r] = make_float2(top, z); };
+        if (last) {
+          float* part = reinterpret_cast<float*>(ring + slot * 2 * S::kStage);
+          give([&](int at, int64_t, int, float4 v) { *reinterpret_cast<float4*>(part + at) = v; }, put_row, false);
+        } else {
+          give([&](int at, int64_t, int, float4 v) { *reinterpret_cast<float4*>(warp_part + at) = v; }, put_row, false);
+          kept = true;
+        }
+        if (lane == 0) spans[warp][slot] = span_of(item);
       } else {
-        give([&](int at, int64_t, int, float4 v) { *reinterpret_cast<float4*>(warp_part + at) = v; }, put_row, false);
-        kept = true;
+        give([&](int, int64_t row, int d, float4 v) {
+               if (row >= 0 && d < D) write_out(a, row + d, v);
+             },
+             [&](int, bool live, int t, int head, float top, float z) {
+               if (live && a.lse)
+                 a.lse[static_cast<int64_t>(t) * a.q_heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * 0.693147181f;
+             },
+             true);
       }
-      if (lane == 0) spans[warp][slot] = span_of(item);
-    } else {
-      give([&](int, int64_t row, int d, float4 v) {
-             if (row >= 0 && d < D) write_out(a, row + d, v);
-           },
-           [&](int, bool live, int t, int head, float top, float z) {
-             if (live && a.lse)
-               a.lse[static_cast<int64_t>(t) * a.q_heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * 0.693147181f;
-           },
-           true);
+      if (last) break;
+      item = next;
     }
-    if (last) break;
-    item = next;
-  }
-  if (kept) {  // back from the workspace: each lane what it wrote
-    float4 v[S::kSlices];
+    if (kept) {  // back from the workspace: each lane what it wrote
+      float4 v[S::kSlices];
 #pragma unroll
-    for (int k = 0; k < S::kSlices; ++k) v[k] = *reinterpret_cast<const float4*>(warp_part + k * 128 + lane * 4);
+      for (int k = 0; k < S::kSlices; ++k) v[k] = *reinterpret_cast<const float4*>(warp_part + k * 128 + lane * 4);
 #pragma unroll
-    for (int k = 0; k < S::kSlices; ++k) *reinterpret_cast<float4*>(ring + k * 512 + lane * 16) = v[k];
-  }
+      for (int k = 0; k < S::kSlices; ++k) *reinterpret_cast<float4*>(ring + k * 512 + lane * 16) = v[k];
+    }
   }
 
   // ---- the CTA's parts together: neighbours of one item, a warp a slice of them.  Lane k looks at place k.

@@ -82,138 +82,138 @@ __global__ void __launch_bounds__(32 * kStoreWarps, 3) store_kernel(const __grid
     firsts = __ballot_sync(0xffffffffu, first);
   }
   for (; firsts; firsts &= firsts - 1) {
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * a.window + __ffs(firsts) - 1;
-  const int seq = seq_of(a.seq, t), pos = a.pos[t], i0 = pos & (block - 1);
-  int n = 0;  // tokens of the run within the block
-  for (int k = 0; k < block - i0; k += 32) {
-    const int i = k + lane;
-    const uint32_t same = __ballot_sync(0xffffffffu, i < block - i0 && t + i < a.T && seq_of(a.seq, t + i) == seq &&
-                                                         a.pos[t + i] == pos + i);
-    n += __ffs(~same) ? __ffs(~same) - 1 : 32;
-    if (~same) break;
-  }
-  if (a.table) {
-    __syncthreads();  // the block before is done with
-    const float mag = static_cast<const RopeHeader*>(a.table)->magnitude;
-    for (int i = threadIdx.x; i < n * pairs; i += blockDim.x)
-      cs[i] = rope_cs(rope_turns(a.table)[i % pairs], pos + i / pairs, mag);
-    __syncthreads();
-  }
-  const int slot0 = pos & ((1 << c.page_log2) - 1);
-  for (int item = blockIdx.y; item < unit_groups + a.q_groups; item += gridDim.y) {
-    if (item >= unit_groups) {
-      const int h = ((item - unit_groups) * kStoreWarps + warp) * tpw + lg;
-      if (!on || h >= a.q_heads || cache_page(c, seq, pos) < 0) continue;
-      for (int i = 0; i < n; ++i) {
-        float v[8];
-        load8<E, VEC>(static_cast<const E*>(a.q) + (t + i) * a.ldq + static_cast<int64_t>(h) * c.dim, o0, o1, v);
-        if (turns) turn8(v, cs + i * pairs + 4 * u, halves);
-        store8<E, VEC>(static_cast<E*>(a.q_dst) + (t + i) * a.ld_q_dst + static_cast<int64_t>(h) * c.dim, o0, o1, v);
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * a.window + __ffs(firsts) - 1;
+    const int seq = seq_of(a.seq, t), pos = a.pos[t], i0 = pos & (block - 1);
+    int n = 0;  // tokens of the run within the block
+    for (int k = 0; k < block - i0; k += 32) {
+      const int i = k + lane;
+      const uint32_t same = __ballot_sync(0xffffffffu, i < block - i0 && t + i < a.T && seq_of(a.seq, t + i) == seq &&
+                                                           a.pos[t + i] == pos + i);
+      n += __ffs(~same) ? __ffs(~same) - 1 : 32;
+      if (~same) break;
+    }
+    if (a.table) {
+      __syncthreads();  // the block before is done with
+      const float mag = static_cast<const RopeHeader*>(a.table)->magnitude;
+      for (int i = threadIdx.x; i < n * pairs; i += blockDim.x)
+        cs[i] = rope_cs(rope_turns(a.table)[i % pairs], pos + i / pairs, mag);
+      __syncthreads();
+    }
+    const int slot0 = pos & ((1 << c.page_log2) - 1);
+    for (int item = blockIdx.y; item < unit_groups + a.q_groups; item += gridDim.y) {
+      if (item >= unit_groups) {
+        const int h = ((item - unit_groups) * kStoreWarps + warp) * tpw + lg;
+        if (!on || h >= a.q_heads || cache_page(c, seq, pos) < 0) continue;
+        for (int i = 0; i < n; ++i) {
+          float v[8];
+          load8<E, VEC>(static_cast<const E*>(a.q) + (t + i) * a.ldq + static_cast<int64_t>(h) * c.dim, o0, o1, v);
+          if (turns) turn8(v, cs + i * pairs + 4 * u, halves);
+          store8<E, VEC>(static_cast<E*>(a.q_dst) + (t + i) * a.ld_q_dst + static_cast<int64_t>(h) * c.dim, o0, o1, v);
+        }
+        continue;
       }
-      continue;
-    }
-    const int unit = item * upg + (warp >> a.wpu_log2), w = warp & (wpu - 1);
-    bool live = unit < 2 * c.heads;
-    const bool is_v = unit >= c.heads;
-    const int head = is_v ? unit - c.heads : unit;
-    const int step = tpw << a.wpu_log2;
-    // values are at their plain places in V and, where nothing turns, in K
-    const int p0 = is_v ? 8 * u : o0, p1 = is_v ? 8 * u + 4 : o1;
-    const bool plain = p1 == p0 + 4;
-    const E* src = static_cast<const E*>(is_v ? a.v : a.k) + static_cast<int64_t>(head) * c.dim;
-    const int64_t ld = is_v ? a.ldv : a.ldk;
-    auto turn = [&](int i, float (&v)[8]) {
-      if (turns && !is_v) turn8(v, cs + i * pairs + 4 * u, halves);
-    };
-    float widest = 0.0f;
-    auto widen = [&](const float (&v)[8]) {
+      const int unit = item * upg + (warp >> a.wpu_log2), w = warp & (wpu - 1);
+      bool live = unit < 2 * c.heads;
+      const bool is_v = unit >= c.heads;
+      const int head = is_v ? unit - c.heads : unit;
+      const int step = tpw << a.wpu_log2;
+      // values are at their plain places in V and, where nothing turns, in K
+      const int p0 = is_v ? 8 * u : o0, p1 = is_v ? 8 * u + 4 : o1;
+      const bool plain = p1 == p0 + 4;
+      const E* src = static_cast<const E*>(is_v ? a.v : a.k) + static_cast<int64_t>(head) * c.dim;
+      const int64_t ld = is_v ? a.ldv : a.ldk;
+      auto turn = [&](int i, float (&v)[8]) {
+        if (turns && !is_v) turn8(v, cs + i * pairs + 4 * u, halves);
+      };
+      float widest = 0.0f;
+      auto widen = [&](const float (&v)[8]) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) widest = top_of(widest, v[e]);
-    };
-    // All of the kept values are on their way before the first is waited for: lanes and iterations that have no token
-    // take the run's last one.
-    float kept[kStoreKept][8];
-    if (live) {
+        for (int e = 0; e < 8; ++e) widest = top_of(widest, v[e]);
+      };
+      // All of the kept values are on their way before the first is waited for: lanes and iterations that have no token
+      // take the run's last one.
+      float kept[kStoreKept][8];
+      if (live) {
 #pragma unroll
-      for (int k = 0; k < kStoreKept; ++k)
-        if (k == 0 || k * step < n) load8<E, VEC>(src + (t + min(k * step + w * tpw + lg, n - 1)) * ld, p0, p1, kept[k]);
-    }
-    // (looked up behind the loads, so that they do not wait for it)
-    const int64_t page = cache_page(c, seq, pos);
-    live = live && page >= 0;
-    float* scale = live ? (is_v ? c.v_scale : c.k_scale) + cache_scale(c, page, head, slot0) : nullptr;
-    const float old = live && i0 > 0 ? *scale : 0.0f;
-    if (live) {
+        for (int k = 0; k < kStoreKept; ++k)
+          if (k == 0 || k * step < n) load8<E, VEC>(src + (t + min(k * step + w * tpw + lg, n - 1)) * ld, p0, p1, kept[k]);
+      }
+      // (looked up behind the loads, so that they do not wait for it)
+      const int64_t page = cache_page(c, seq, pos);
+      live = live && page >= 0;
+      float* scale = live ? (is_v ? c.v_scale : c.k_scale) + cache_scale(c, page, head, slot0) : nullptr;
+      const float old = live && i0 > 0 ? *scale : 0.0f;
+      if (live) {
+#pragma unroll
+        for (int k = 0; k < kStoreKept; ++k) {
+          if (k > 0 && k * step >= n) break;
+          turn(min(k * step + w * tpw + lg, n - 1), kept[k]);
+          widen(kept[k]);
+        }
+#pragma unroll 2
+        for (int k = kStoreKept; k * step < n; ++k) {
+          const int i = min(k * step + w * tpw + lg, n - 1);
+          float v[8];
+          load8<E, VEC>(src + (t + i) * ld, p0, p1, v);
+          turn(i, v);
+          widen(v);
+        }
+      }
+      uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(widest));  // NaN is the largest
+      if (wpu > 1) {
+        __syncthreads();  // the group before has read its tops
+        if (lane == 0) tops[warp] = top;
+        __syncthreads();
+        for (int i = 0; i < wpu; ++i) top = max(top, tops[warp - w + i]);
+      }
+      if (!live) continue;
+      float d;
+      if (top >= 0x7f800000u || !(old == old))
+        d = __uint_as_float(0x7fffffffu);  // not finite: the block reads back as NaN
+      else
+        d = fmaxf(scale_for<FMT>(__uint_as_float(top)), old);
+      const bool number = d == d;
+      const float inv = number ? 1.0f / d : 0.0f;
+      if (lane == 0 && w == 0) *scale = d;
+      uint8_t* codes = (is_v ? c.v : c.k) + cache_row(c, page, head, slot0);
+      auto write = [&](int i, const float (&v)[8]) {
+        uint8_t* row = codes + static_cast<int64_t>(i) * c.dim;
+        const uint2 w = number ? codes8<FMT>(v, d, inv) : make_uint2(0u, 0u);
+        if (plain) {
+          *reinterpret_cast<uint2*>(row + p0) = w;
+        } else {
+          *reinterpret_cast<uint32_t*>(row + p0) = w.x;
+          *reinterpret_cast<uint32_t*>(row + p1) = w.y;
+        }
+      };
 #pragma unroll
       for (int k = 0; k < kStoreKept; ++k) {
-        if (k > 0 && k * step >= n) break;
-        turn(min(k * step + w * tpw + lg, n - 1), kept[k]);
-        widen(kept[k]);
+        const int i = k * step + w * tpw + lg;
+        if (on && i < n) write(i, kept[k]);
       }
-#pragma unroll 2
       for (int k = kStoreKept; k * step < n; ++k) {
-        const int i = min(k * step + w * tpw + lg, n - 1);
-        float v[8];
-        load8<E, VEC>(src + (t + i) * ld, p0, p1, v);
-        turn(i, v);
-        widen(v);
+        const int i = k * step + w * tpw + lg;
+        if (on && i < n) {
+          float v[8];
+          load8<E, VEC>(src + (t + i) * ld, p0, p1, v);
+          turn(i, v);
+          write(i, v);
+        }
+      }
+      if (number && i0 > 0 && d > old && on) {  // the block's earlier tokens, under the larger scale
+        for (int i = w * tpw + lg; i < i0; i += step) {
+          uint2* row = reinterpret_cast<uint2*>(codes - static_cast<int64_t>(i0 - i) * c.dim + 8 * u);
+          const uint2 raw = *row;
+          float x[4], y[4];
+          values4<FMT>(raw.x, x);
+          values4<FMT>(raw.y, y);
+          // i8: code * old is exact; e4m3: the scales' quotient is
+          const float f = FMT == 0 ? old : 1.0f, r = FMT == 0 ? inv : old * inv;
+          const float v[8] = {x[0] * f, x[1] * f, x[2] * f, x[3] * f, y[0] * f, y[1] * f, y[2] * f, y[3] * f};
+          *row = codes8<FMT>(v, d, r);
+        }
       }
     }
-    uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(widest));  // NaN is the largest
-    if (wpu > 1) {
-      __syncthreads();  // the group before has read its tops
-      if (lane == 0) tops[warp] = top;
-      __syncthreads();
-      for (int i = 0; i < wpu; ++i) top = max(top, tops[warp - w + i]);
-    }
-    if (!live) continue;
-    float d;
-    if (top >= 0x7f800000u || !(old == old))
-      d = __uint_as_float(0x7fffffffu);  // not finite: the block reads back as NaN
-    else
-      d = fmaxf(scale_for<FMT>(__uint_as_float(top)), old);
-    const bool number = d == d;
-    const float inv = number ? 1.0f / d : 0.0f;
-    if (lane == 0 && w == 0) *scale = d;
-    uint8_t* codes = (is_v ? c.v : c.k) + cache_row(c, page, head, slot0);
-    auto write = [&](int i, const float (&v)[8]) {
-      uint8_t* row = codes + static_cast<int64_t>(i) * c.dim;
-      const uint2 w = number ? codes8<FMT>(v, d, inv) : make_uint2(0u, 0u);
-      if (plain) {
-        *reinterpret_cast<uint2*>(row + p0) = w;
-      } else {
-        *reinterpret_cast<uint32_t*>(row + p0) = w.x;
-        *reinterpret_cast<uint32_t*>(row + p1) = w.y;
-      }
-    };
-#pragma unroll
-    for (int k = 0; k < kStoreKept; ++k) {
-      const int i = k * step + w * tpw + lg;
-      if (on && i < n) write(i, kept[k]);
-    }
-    for (int k = kStoreKept; k * step < n; ++k) {
-      const int i = k * step + w * tpw + lg;
-      if (on && i < n) {
-        float v[8];
-        load8<E, VEC>(src + (t + i) * ld, p0, p1, v);
-        turn(i, v);
-        write(i, v);
-      }
-    }
-    if (number && i0 > 0 && d > old && on) {  // the block's earlier tokens, under the larger scale
-      for (int i = w * tpw + lg; i < i0; i += step) {
-        uint2* row = reinterpret_cast<uint2*>(codes - static_cast<int64_t>(i0 - i) * c.dim + 8 * u);
-        const uint2 raw = *row;
-        float x[4], y[4];
-        values4<FMT>(raw.x, x);
-        values4<FMT>(raw.y, y);
-        // i8: code * old is exact; e4m3: the scales' quotient is
-        const float f = FMT == 0 ? old : 1.0f, r = FMT == 0 ? inv : old * inv;
-        const float v[8] = {x[0] * f, x[1] * f, x[2] * f, x[3] * f, y[0] * f, y[1] * f, y[2] * f, y[3] * f};
-        *row = codes8<FMT>(v, d, r);
-      }
-    }
-  }
   }
 }
 

@@ -194,6 +194,60 @@ def test_nan_block_is_seen(G):
     assert np.isnan(lse[0, 2:]).all() and np.isfinite(lse[2]).all()
 
 
+@pytest.mark.parametrize("D, window", [(64, 0), (128, 0), (256, 0), (128, 20)])
+def test_nan_block_beside(G, D, window):
+    """Rows that share their keys' reading with rows that see such a block, and do not see it themselves, are as
+    without it."""
+    rng = np.random.default_rng(12)
+    c = setup(rng, "i8", [200], 1, 16, D, 16)
+    seq, pos = np.zeros(4, dtype=np.int32), np.array([40, 100, 120, 199], dtype=np.int32)
+    q = queries(rng, 4, 2, D)
+    for name in ("k_scale", "v_scale"):
+        bad = {k: v.copy() if isinstance(v, np.ndarray) else v for k, v in c.items()}
+        bad[name][c["table"][0, 7], 0, 0] = np.nan  # positions 112 to 127: the token at 100 is of their chunk
+        got, _ = call(G, au.DeviceCache(G, bad), q, seq, pos, run=4, window=window)
+        want, lse, mass, spread = oatt.attend(c, q, seq, pos, window=window)
+        sees = [p >= 112 and (not window or p - window < 127) for p in pos]
+        b, _ = au.attend_bounds(c, want, lse, mass, spread, np.repeat(pos[:, None] + 1.0, 2, 1), False)
+        for t in range(4):
+            if sees[t]:
+                assert np.isnan(got[t]).all()
+            else:
+                assert_within(got[t], want[t], b[t], "token %d" % t)
+
+
+def test_captured_by_a_user(G):
+    """Direct calls recorded by a capture of the user's own, replayed over changed inputs."""
+    rng = np.random.default_rng(13)
+    table, pages = au.shuffled_table(rng, [100, 100], 16)
+    c = au.cache_arrays(rng, "i8", pages, 2, 16, 64, 4, table)
+    dc = au.DeviceCache(G, c)
+    k, v, q = (torch.empty(2, h, 64, device="cuda") for h in (2, 2, 8))
+    out, turned = torch.empty_like(q), torch.empty_like(q)
+    pos = torch.zeros(2, dtype=torch.int32, device="cuda")
+    rot = torch.empty(G.rope_table_bytes(64), dtype=torch.uint8, device="cuda")
+    G.rope_table(rot, 64)
+    ws = torch.empty(G.attend_workspace(2, 8, 2, 64), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        G.rope(q, 2, 8, 64, pos, rot, turned)
+        G.cache_store(dc.cache, k, v, 2, None, pos)
+        G.attend(dc.cache, turned, 2, 8, None, pos, out, ws)
+    for p in ([0, 7], [1, 8], [2, 9], [50, 99]):
+        kn, vn, qn = (rng.standard_normal((2, h, 64)).astype(np.float32) for h in (2, 2, 8))
+        for t, x in ((k, kn), (v, vn), (q, qn)):
+            t.copy_(dev_tensor(x))
+        pos.copy_(torch.tensor(p, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        oatt.store(c, kn, vn, [0, 1], p)
+        want, lse, mass, spread = oatt.attend(c, turned.cpu().numpy(), [0, 1], p)
+        b, _ = au.attend_bounds(c, want, lse, mass, spread, np.repeat(np.array(p, dtype=float)[:, None] + 1, 8, 1), False)
+        assert_within(out.double().cpu().numpy(), want, b)
+        assert np.array_equal(dc.host("k"), c["k"]) and np.array_equal(dc.host("v_scale"), c["v_scale"])
+
+
 def test_hard_queries(G):
     """Zero, tiny, huge and not finite queries; scores far apart; a scale of its own."""
     rng = np.random.default_rng(3)
