@@ -200,7 +200,8 @@ static int plan_store(const gf_cache* c, const void* k, const void* v, int64_t T
   if ((e = check_rows(k, &ldk, width, o->type, &vec)) != GF_OK) return e;
   if ((e = check_rows(v, &ldv, width, o->type, &vec)) != GF_OK) return e;
   const int64_t kb = rows_bytes(T, ldk, width, o->type), vb = rows_bytes(T, ldv, width, o->type);
-  if (overlaps_cache(c, k, kb) || overlaps_cache(c, v, vb) || overlaps_cache(c, seq, T * 4) || overlaps_cache(c, pos, T * 4) ||
+  if (overlaps_cache(c, k, kb) || overlaps_cache(c, v, vb) || overlaps_cache(c, seq, T * 4) ||
+      overlaps_cache(c, pos, T * 4) ||
       (o->rope && overlaps_cache(c, o->rope->table, rope_table_bytes(rot))))
     return GF_ERR_ALIAS;
   const bool with_q = o->q != nullptr || o->q_dst != nullptr;
@@ -251,13 +252,23 @@ static int plan_store(const gf_cache* c, const void* k, const void* v, int64_t T
   a.tpw = static_cast<int>(32 / (c->dim / 8));
   a.lane_inv = static_cast<int>(65536 / (c->dim / 8) + 1);
   while (T > 256 && (kStoreWarps >> a.wpu_log2) > 1 && (a.tpw * kStoreKept << a.wpu_log2) < c->block) ++a.wpu_log2;
-  const int upg = kStoreWarps >> a.wpu_log2;
-  a.unit_groups = static_cast<int>((2 * c->heads + upg - 1) / upg);
-  a.q_groups = a.q ? (a.q_heads + kStoreWarps * a.tpw - 1) / (kStoreWarps * a.tpw) : 0;
-  // Each token may begin a block (decode steps); of a prompt's every block-th does, and CTAs that find none only
-  // cost their start: as many tokens a CTA as leave eight CTAs to an SM.
-  a.window = 1;
-  while (a.window < 32 && a.window < c->block && T * (a.unit_groups + a.q_groups) > 2432LL * a.window) a.window *= 2;
+  a.small = T > 256 && c->block <= a.tpw;
+  if (a.small) {  // tasks of warps, two to a warp
+    const int64_t tasks = 2 * ((c->heads + kStoreKept - 1) / kStoreKept);
+    a.window = 8;
+    a.unit_groups = static_cast<int>((a.window * tasks + 2 * kStoreWarps - 1) / (2 * kStoreWarps));
+  } else {
+    const int upg = kStoreWarps >> a.wpu_log2;
+    a.unit_groups = static_cast<int>((2 * c->heads + upg - 1) / upg);
+    // Each token may begin a block (decode steps); of a prompt's every block-th does, and CTAs that find none
+    // only cost their start: as many tokens a CTA as leave sixteen CTAs to an SM.
+    a.window = 1;
+    while (a.window < 32 && a.window < c->block && T * a.unit_groups > 2432LL * a.window) a.window *= 2;
+  }
+  a.q_rows = T > 256 ? kStoreKept : 1;
+  const int chunks = a.q ? (a.q_heads + a.q_rows * a.tpw - 1) / (a.q_rows * a.tpw) : 0;
+  const int per_cta = kStoreWarps * (T > 256 ? 2 : 1);
+  a.q_slices = (a.window * chunks + per_cta - 1) / per_cta;
   *n = 1;
   return GF_OK;
 }
@@ -318,18 +329,19 @@ static int64_t attend_bytes(int64_t T, int64_t q_heads, int64_t heads, int64_t d
     return GF_ERR_UNSUPPORTED;
   AttendArgs a = {};
   attend_shape(q_heads / heads, dim, std::max<int64_t>(run, 1), a);
-  return attend_workspace_bytes(static_cast<int>(dim), a.tiles, attend_ctas(static_cast<int>(dim), a.tiles, device_limits().sm_count));
+  return attend_workspace_bytes(static_cast<int>(dim), a.tiles, attend_ctas(device_limits().sm_count));
 }
 
-static int check_attend(const gf_cache* c, const void* q, int64_t T, int64_t q_heads, const int32_t* seq, const int32_t* pos,
-                        const gf_attend_opts* o, const void* dst, AttendArgs& a) {
+static int check_attend(const gf_cache* c, const void* q, int64_t T, int64_t q_heads, const int32_t* seq,
+                        const int32_t* pos, const gf_attend_opts* o, const void* dst, AttendArgs& a) {
   if (!o || T < 0 || q_heads < 1 || !type_ok(o->type) || o->run < 0 || o->window < 0) return GF_ERR_INVALID;
   if (!std::isfinite(o->scale) || o->scale < 0.0f) return GF_ERR_INVALID;
   CacheArgs ca;
   int e = check_cache(c, ca);
   if (e != GF_OK) return e;
   if (q_heads % c->heads != 0) return GF_ERR_INVALID;
-  if (T > kAttMaxTokens || q_heads > kMaxHeads || o->run > kAttMaxTokens || o->window > INT32_MAX) return GF_ERR_UNSUPPORTED;
+  if (T > kAttMaxTokens || q_heads > kMaxHeads || o->run > kAttMaxTokens || o->window > INT32_MAX)
+    return GF_ERR_UNSUPPORTED;
   // (chunks of all items, counted in 64 bits times the warps that share them)
   if (static_cast<double>(T) * q_heads * (c->table_ld * c->page / 16 + 2) > 2251799813685248.0) return GF_ERR_UNSUPPORTED;
   if (T == 0) return GF_OK;
@@ -371,7 +383,7 @@ static int check_attend(const gf_cache* c, const void* q, int64_t T, int64_t q_h
   a.type = o->type;
   a.vec = vec;
   attend_shape(a.group, c->dim, std::max<int64_t>(o->run, 1), a);
-  a.ctas = attend_ctas(ca.dim, a.tiles, device_limits().sm_count);
+  a.ctas = attend_ctas(device_limits().sm_count);
   return GF_OK;
 }
 

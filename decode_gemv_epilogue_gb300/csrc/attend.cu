@@ -249,7 +249,9 @@ constexpr int kAttHead = 64;
 __host__ __device__ constexpr int64_t att_parts_at(int ctas) { return kAttHead + static_cast<int64_t>(ctas) * 32; }
 
 // Unit at which CTA i begins.
-__device__ __forceinline__ int64_t share(const AttHeader& h, int64_t i) { return i * h.each + (i < h.more ? i : h.more); }
+__device__ __forceinline__ int64_t share(const AttHeader& h, int64_t i) {
+  return i * h.each + (i < h.more ? i : h.more);
+}
 
 __device__ __forceinline__ AttSpan span_of(const Item& it) {
   return AttSpan{it.begin, it.begin + it.chunks + 1, it.t0, it.n, it.hs, 0};
@@ -308,7 +310,8 @@ __device__ __forceinline__ void join_part(float m, float l, float4 x, float& top
 
 // A slice's place of a joined item as output.
 template <int DC, int NM>
-__device__ __forceinline__ void join_out(const AttendArgs& a, const AttSpan& s, int slice, int lane, float top, float z, float4 v) {
+__device__ __forceinline__ void join_out(const AttendArgs& a, const AttSpan& s, int slice, int lane, float top, float z,
+                                         float4 v) {
   using S = AttShape<DC, NM>;
   constexpr int UB = kUnitBytes<DC>, PER = S::kSlices / NM;  // slices of eight rows: unit, column parity, four dims
   static_assert((DC == 256 ? 2 : 1) * 2 * (UB / 4) == PER, "as the parts are laid out");
@@ -318,7 +321,8 @@ __device__ __forceinline__ void join_out(const AttendArgs& a, const AttSpan& s, 
   if (!row_of(a, s.t0, s.n, s.hs, r, t, head)) return;
   const float inv = z == 0.0f ? 0.0f : 1.0f / z;  // no keys: zeros
   if (d < a.c.dim)
-    write_out(a, t * a.ld_dst + static_cast<int64_t>(head) * a.c.dim + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+    write_out(a, t * a.ld_dst + static_cast<int64_t>(head) * a.c.dim + d,
+              make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
   if (d == 0 && a.lse)
     a.lse[static_cast<int64_t>(t) * a.q_heads + head] = z == 0.0f ? -INFINITY : (top + log2f(z)) * 0.693147181f;
 }
@@ -592,7 +596,8 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
           ring_scales[CT + scale_lane] = value_scale;
         }
         // (a scale that is not finite makes its own rows NaN, and is no measure for the others)
-        const uint32_t vbits = __float_as_uint(value_scale), vtop = __reduce_max_sync(0xffffffffu, vbits < 0x7f800000u ? vbits : 0u);
+        const uint32_t vbits = __float_as_uint(value_scale);
+        const uint32_t vtop = __reduce_max_sync(0xffffffffu, vbits < 0x7f800000u ? vbits : 0u);
         if (c + 1 < c1) {
           hidden_next = fetch(src, c + 1, pages);
           pages = pages_of(src, c + 2);
@@ -652,7 +657,8 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
         const uint32_t vnow = max(vexp, (vtop >> 23) + 1);
         // 2^(kWeightBits - (vnow - 127)): weights times it lie below 2^8
         const float vinv = __uint_as_float((254 + kWeightBits - vnow) << 23);
-        const float vstep = vexp == vnow ? 1.0f : exp2_fast(static_cast<float>(static_cast<int>(vexp) - static_cast<int>(vnow)));
+        const int rise = static_cast<int>(vexp) - static_cast<int>(vnow);
+        const float vstep = rise == 0 ? 1.0f : exp2_fast(static_cast<float>(rise));
         vexp = vnow;
         uint4 pf[NM][KG];
         float alpha[NM];
@@ -795,7 +801,9 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
       };
       if (start > item.begin || end > stop) {
         const int slot = start >= item.begin ? 0 : 1;
-        auto put_row = [&](int r, bool, int, int, float top, float z) { part_rows[warp][slot][r] = make_float2(top, z); };
+        auto put_row = [&](int r, bool, int, int, float top, float z) {
+          part_rows[warp][slot][r] = make_float2(top, z);
+        };
         if (last) {
           float* part = reinterpret_cast<float*>(ring + slot * 2 * S::kStage);
           give([&](int at, int64_t, int, float4 v) { *reinterpret_cast<float4*>(part + at) = v; }, put_row, false);
@@ -986,7 +994,7 @@ int64_t attend_workspace_bytes(int dim, int tiles, int ctas) {
   return att_parts_at(ctas) + static_cast<int64_t>(ctas) * (2 + att_warps(dc, tiles)) * 8 * tiles * (dc + 2) * 4;
 }
 
-int attend_ctas(int, int, int sms) { return 2 * sms; }
+int attend_ctas(int sms) { return 2 * sms; }
 
 template <int DC, bool EXACT, int FMT, int NM>
 static int launch_part(cudaLaunchConfig_t& cfg, const AttendArgs& a) {

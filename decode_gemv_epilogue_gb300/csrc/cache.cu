@@ -52,12 +52,142 @@ __device__ __forceinline__ void turn8(float (&v)[8], const float2* cs, bool halv
   }
 }
 
-// A CTA looks for first tokens of blocks among `window` tokens of the call, and takes the new tokens of each one's
-// block in turn: of their work, units of (block, head, keys or values) and rows of queries, every gridDim.y-th
-// group of kStoreWarps warps.  A unit is 1 << wpu_log2 warps'; a warp holds 32 / (dim / 8) tokens at a time, eight
-// elements a lane.  (With a CTA to every token, those of a prompt that begin no block cost more than the
-// others: 8191 tokens in blocks of 32 took 90 us where XX.)
+// Queries of a window's tokens: a warp takes q_rows times tpw heads of a token at a time, every (q_slices *
+// kStoreWarps)th such task; a lane turns its four pairs of all of them by the same angles.  (As rows of a block's
+// work, behind its scan and between its CTAs' cosines, they made 86 us of 66 for 8191 tokens of 32 query and 8 key
+// heads.)
+template <typename E, bool VEC>
+__device__ __forceinline__ void store_queries(const StoreArgs& a, int task, int lg, int u, bool on, int o0, int o1) {
+  const CacheArgs& c = a.c;
+  const int heads = a.q_rows * a.tpw, chunks = (a.q_heads + heads - 1) / heads;
+  const bool halves = a.halves != 0, turns = 8 * u < a.n_rot;
+  for (; task < a.window * chunks; task += a.q_slices * kStoreWarps) {
+    const int i = task / chunks, h0 = (task - i * chunks) * heads + lg;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * a.window + i;
+    if (t >= a.T) return;
+    const E* from = static_cast<const E*>(a.q) + t * a.ldq;
+    E* to = static_cast<E*>(a.q_dst) + t * a.ld_q_dst;
+    const int pos = a.pos[t], seq = seq_of(a.seq, t);
+    float v[kStoreKept][8];
+#pragma unroll
+    for (int k = 0; k < kStoreKept; ++k) {
+      const int h = h0 + k * a.tpw;
+      if (on && k < a.q_rows && h < a.q_heads) load8<E, VEC>(from + static_cast<int64_t>(h) * c.dim, o0, o1, v[k]);
+    }
+    float2 cs[4];
+    if (turns) {
+      const float mag = static_cast<const RopeHeader*>(a.table)->magnitude;
+      const uint64_t* f = rope_turns(a.table) + 4 * u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) cs[e] = rope_cs(f[e], pos, mag);
+    }
+    if (cache_page(c, seq, pos) < 0) continue;
+#pragma unroll
+    for (int k = 0; k < kStoreKept; ++k) {
+      const int h = h0 + k * a.tpw;
+      if (on && k < a.q_rows && h < a.q_heads) {
+        if (turns) turn8(v[k], cs, halves);
+        store8<E, VEC>(to + static_cast<int64_t>(h) * c.dim, o0, o1, v[k]);
+      }
+    }
+  }
+}
+
+// A block's scale: what its new values of magnitude up to `top` (as bits) and its earlier ones need; NaN where
+// a value is not finite, and the block then reads back as NaN.
+template <int FMT>
+__device__ __forceinline__ float block_scale(uint32_t top, float old) {
+  if (top >= 0x7f800000u || !(old == old)) return __uint_as_float(0x7fffffffu);
+  return fmaxf(scale_for<FMT>(__uint_as_float(top)), old);
+}
+
+// Eight codes of an earlier token, under the larger scale d.  i8: code * old is exact; e4m3: the scales' quotient is.
+template <int FMT>
+__device__ __forceinline__ void rescale8(uint2* row, float old, float d, float inv) {
+  const uint2 raw = *row;
+  float x[4], y[4];
+  values4<FMT>(raw.x, x);
+  values4<FMT>(raw.y, y);
+  const float f = FMT == 0 ? old : 1.0f, r = FMT == 0 ? inv : old * inv;
+  const float v[8] = {x[0] * f, x[1] * f, x[2] * f, x[3] * f, y[0] * f, y[1] * f, y[2] * f, y[3] * f};
+  *row = codes8<FMT>(v, d, r);
+}
+
+// Codes of a unit of eight, which lie at p0 and p1 of a row.
+__device__ __forceinline__ void put_codes(uint8_t* row, int p0, int p1, uint2 w) {
+  if (p1 == p0 + 4) {
+    *reinterpret_cast<uint2*>(row + p0) = w;
+  } else {
+    *reinterpret_cast<uint32_t*>(row + p0) = w.x;
+    *reinterpret_cast<uint32_t*>(row + p1) = w.y;
+  }
+}
+
+// Blocks no longer than a warp's tokens, of a prompt: a task is a window's token and kStoreKept heads, all values
+// of the token's block on their way together if it begins one.  (As units of a head, 8191 tokens with a scale each
+// took 90 us where 44.)
 template <int FMT, typename E, bool VEC>
+__device__ __forceinline__ void store_small(const StoreArgs& a, int task, int step, int lg, int u, bool on, int o0, int o1) {
+  const CacheArgs& c = a.c;
+  const int block = 1 << c.block_log2, chunks = (c.heads + kStoreKept - 1) / kStoreKept, lane = threadIdx.x & 31;
+  const bool halves = a.halves != 0;
+  for (; task < a.window * 2 * chunks; task += step) {
+    const int j = task / (2 * chunks), part = task - j * 2 * chunks;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * a.window + j;
+    if (t >= a.T) return;
+    const int seq = seq_of(a.seq, t), pos = a.pos[t], i0 = pos & (block - 1);
+    if (t > 0 && i0 > 0 && seq_of(a.seq, t - 1) == seq && a.pos[t - 1] == pos - 1) continue;
+    const uint32_t same = __ballot_sync(0xffffffffu, lane < block - i0 && t + lane < a.T && seq_of(a.seq, t + lane) == seq &&
+                                                         a.pos[t + lane] == pos + lane);
+    const int n = __ffs(~same) - 1;  // (blocks are shorter than a warp)
+    const bool is_v = part >= chunks, turns = a.table && !is_v && 8 * u < a.n_rot;
+    const int head0 = (is_v ? part - chunks : part) * kStoreKept, slot0 = pos & ((1 << c.page_log2) - 1);
+    const int p0 = is_v ? 8 * u : o0, p1 = is_v ? 8 * u + 4 : o1, i = min(lg, n - 1);
+    const E* src = static_cast<const E*>(is_v ? a.v : a.k) + (t + i) * (is_v ? a.ldv : a.ldk);
+    float v[kStoreKept][8];
+#pragma unroll
+    for (int k = 0; k < kStoreKept; ++k)
+      load8<E, VEC>(src + static_cast<int64_t>(min(head0 + k, c.heads - 1)) * c.dim, p0, p1, v[k]);
+    float2 cs[4];
+    if (turns) {
+      const float mag = static_cast<const RopeHeader*>(a.table)->magnitude;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) cs[e] = rope_cs(rope_turns(a.table)[4 * u + e], pos + i, mag);
+    }
+    const int64_t page = cache_page(c, seq, pos);
+    if (page < 0) continue;
+    float* scales = is_v ? c.v_scale : c.k_scale;
+    uint8_t* codes = is_v ? c.v : c.k;
+#pragma unroll
+    for (int k = 0; k < kStoreKept; ++k) {
+      if (head0 + k >= c.heads) break;
+      float* scale = scales + cache_scale(c, page, head0 + k, slot0);
+      const float old = i0 > 0 ? *scale : 0.0f;
+      if (turns) turn8(v[k], cs, halves);
+      float widest = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) widest = top_of(widest, v[k][e]);
+      const float d = block_scale<FMT>(__reduce_max_sync(0xffffffffu, __float_as_uint(widest)), old);
+      const bool number = d == d;
+      const float inv = number ? 1.0f / d : 0.0f;
+      __syncwarp();  // the scale before has been read
+      if (lane == 0) *scale = d;
+      uint8_t* rows = codes + cache_row(c, page, head0 + k, slot0);
+      if (on && lg < n) put_codes(rows + lg * c.dim, p0, p1, number ? codes8<FMT>(v[k], d, inv) : make_uint2(0u, 0u));
+      if (number && on && lg < i0 && d > old)
+        rescale8<FMT>(reinterpret_cast<uint2*>(rows + (lg - i0) * c.dim + 8 * u), old, d, inv);
+    }
+  }
+}
+
+// A CTA looks for first tokens of blocks among `window` tokens of the call, and takes the new tokens of each one's
+// block in turn: of their units of (block, head, keys or values), every (gridDim.y - q_slices)th group of
+// kStoreWarps warps.  A unit is 1 << wpu_log2 warps'; a warp holds 32 / (dim / 8) tokens at a time, eight elements
+// a lane.  The last q_slices CTAs of a window turn its queries.
+// Every value is read once, every code written once; 8191 tokens of 8 heads of 128 in blocks of 32, f16, take 32 us
+// (50 MB, 7.5 us of the memory's): the chain from positions to values, scale and codes is what a CTA waits for.
+// With a CTA to every token, those of a prompt that begin no block cost more than the others: 120 us.
+template <int FMT, typename E, bool VEC, bool SMALL>
 __global__ void __launch_bounds__(32 * kStoreWarps, 3) store_kernel(const __grid_constant__ StoreArgs a) {
   extern __shared__ float2 cs[];  // [token][pair]
   __shared__ uint32_t tops[kStoreWarps];
@@ -70,6 +200,15 @@ __global__ void __launch_bounds__(32 * kStoreWarps, 3) store_kernel(const __grid
   const bool on = lg < tpw, halves = a.halves != 0, turns = a.table && 8 * u < a.n_rot;
   int o0, o1;
   unit_offsets(u, a.table ? a.n_rot : 0, halves, o0, o1);
+  const int slices = gridDim.y - a.q_slices;
+  if (static_cast<int>(blockIdx.y) >= slices) {
+    store_queries<E, VEC>(a, (blockIdx.y - slices) * kStoreWarps + warp, lg, u, on, o0, o1);
+    return;
+  }
+  if constexpr (SMALL) {
+    store_small<FMT, E, VEC>(a, blockIdx.y * kStoreWarps + warp, slices * kStoreWarps, lg, u, on, o0, o1);
+    return;
+  }
   const int wpu = 1 << a.wpu_log2, upg = kStoreWarps >> a.wpu_log2, unit_groups = a.unit_groups;
   uint32_t firsts;  // of the window's tokens, those that begin a block's new ones
   {
@@ -92,25 +231,16 @@ __global__ void __launch_bounds__(32 * kStoreWarps, 3) store_kernel(const __grid
       n += __ffs(~same) ? __ffs(~same) - 1 : 32;
       if (~same) break;
     }
-    if (a.table) {
-      __syncthreads();  // the block before is done with
-      const float mag = static_cast<const RopeHeader*>(a.table)->magnitude;
-      for (int i = threadIdx.x; i < n * pairs; i += blockDim.x)
-        cs[i] = rope_cs(rope_turns(a.table)[i % pairs], pos + i / pairs, mag);
-      __syncthreads();
-    }
     const int slot0 = pos & ((1 << c.page_log2) - 1);
-    for (int item = blockIdx.y; item < unit_groups + a.q_groups; item += gridDim.y) {
-      if (item >= unit_groups) {
-        const int h = ((item - unit_groups) * kStoreWarps + warp) * tpw + lg;
-        if (!on || h >= a.q_heads || cache_page(c, seq, pos) < 0) continue;
-        for (int i = 0; i < n; ++i) {
-          float v[8];
-          load8<E, VEC>(static_cast<const E*>(a.q) + (t + i) * a.ldq + static_cast<int64_t>(h) * c.dim, o0, o1, v);
-          if (turns) turn8(v, cs + i * pairs + 4 * u, halves);
-          store8<E, VEC>(static_cast<E*>(a.q_dst) + (t + i) * a.ld_q_dst + static_cast<int64_t>(h) * c.dim, o0, o1, v);
-        }
-        continue;
+    bool turned = false;  // the run's cosines are there
+    for (int item = blockIdx.y; item < unit_groups; item += slices) {
+      if (a.table && item * upg < c.heads && !turned) {
+        turned = true;
+        __syncthreads();  // the block before is done with
+        const float mag = static_cast<const RopeHeader*>(a.table)->magnitude;
+        for (int i = threadIdx.x; i < n * pairs; i += blockDim.x)
+          cs[i] = rope_cs(rope_turns(a.table)[i % pairs], pos + i / pairs, mag);
+        __syncthreads();
       }
       const int unit = item * upg + (warp >> a.wpu_log2), w = warp & (wpu - 1);
       bool live = unit < 2 * c.heads;
@@ -119,7 +249,6 @@ __global__ void __launch_bounds__(32 * kStoreWarps, 3) store_kernel(const __grid
       const int step = tpw << a.wpu_log2;
       // values are at their plain places in V and, where nothing turns, in K
       const int p0 = is_v ? 8 * u : o0, p1 = is_v ? 8 * u + 4 : o1;
-      const bool plain = p1 == p0 + 4;
       const E* src = static_cast<const E*>(is_v ? a.v : a.k) + static_cast<int64_t>(head) * c.dim;
       const int64_t ld = is_v ? a.ldv : a.ldk;
       auto turn = [&](int i, float (&v)[8]) {
@@ -167,24 +296,14 @@ __global__ void __launch_bounds__(32 * kStoreWarps, 3) store_kernel(const __grid
         for (int i = 0; i < wpu; ++i) top = max(top, tops[warp - w + i]);
       }
       if (!live) continue;
-      float d;
-      if (top >= 0x7f800000u || !(old == old))
-        d = __uint_as_float(0x7fffffffu);  // not finite: the block reads back as NaN
-      else
-        d = fmaxf(scale_for<FMT>(__uint_as_float(top)), old);
+      const float d = block_scale<FMT>(top, old);
       const bool number = d == d;
       const float inv = number ? 1.0f / d : 0.0f;
       if (lane == 0 && w == 0) *scale = d;
       uint8_t* codes = (is_v ? c.v : c.k) + cache_row(c, page, head, slot0);
       auto write = [&](int i, const float (&v)[8]) {
         uint8_t* row = codes + static_cast<int64_t>(i) * c.dim;
-        const uint2 w = number ? codes8<FMT>(v, d, inv) : make_uint2(0u, 0u);
-        if (plain) {
-          *reinterpret_cast<uint2*>(row + p0) = w;
-        } else {
-          *reinterpret_cast<uint32_t*>(row + p0) = w.x;
-          *reinterpret_cast<uint32_t*>(row + p1) = w.y;
-        }
+        put_codes(row, p0, p1, number ? codes8<FMT>(v, d, inv) : make_uint2(0u, 0u));
       };
 #pragma unroll
       for (int k = 0; k < kStoreKept; ++k) {
@@ -201,17 +320,8 @@ __global__ void __launch_bounds__(32 * kStoreWarps, 3) store_kernel(const __grid
         }
       }
       if (number && i0 > 0 && d > old && on) {  // the block's earlier tokens, under the larger scale
-        for (int i = w * tpw + lg; i < i0; i += step) {
-          uint2* row = reinterpret_cast<uint2*>(codes - static_cast<int64_t>(i0 - i) * c.dim + 8 * u);
-          const uint2 raw = *row;
-          float x[4], y[4];
-          values4<FMT>(raw.x, x);
-          values4<FMT>(raw.y, y);
-          // i8: code * old is exact; e4m3: the scales' quotient is
-          const float f = FMT == 0 ? old : 1.0f, r = FMT == 0 ? inv : old * inv;
-          const float v[8] = {x[0] * f, x[1] * f, x[2] * f, x[3] * f, y[0] * f, y[1] * f, y[2] * f, y[3] * f};
-          *row = codes8<FMT>(v, d, r);
-        }
+        for (int i = w * tpw + lg; i < i0; i += step)
+          rescale8<FMT>(reinterpret_cast<uint2*>(codes - static_cast<int64_t>(i0 - i) * c.dim + 8 * u), old, d, inv);
       }
     }
   }
@@ -219,29 +329,29 @@ __global__ void __launch_bounds__(32 * kStoreWarps, 3) store_kernel(const __grid
 
 template <int FMT, typename E, bool VEC>
 static int launch_store_t(const StoreArgs& a, int sms, cudaStream_t st, bool pdl) {
-  const int64_t groups = a.unit_groups + a.q_groups;
-  // Groups spread over as many CTAs as make 32 for every SM, counting whole blocks of new tokens (a prompt's):
-  // a CTA waits for its values once, and others fill the time; every CTA of a block computes its tokens'
-  // cosines again.
-  const int64_t blocks = (a.T + (1 << a.c.block_log2) - 1) >> a.c.block_log2;
-  int64_t y = (32 * sms + blocks - 1) / blocks;
-  if (y > groups) y = groups;
+  // A block's units are spread over as many CTAs as make 32 for every SM, counting those that find a block (a
+  // prompt's): a CTA waits for its values once, and others fill the time; every CTA of a block computes its
+  // tokens' cosines again.
+  const int64_t windows = (a.T + a.window - 1) / a.window, blocks = (a.T + (1 << a.c.block_log2) - 1) >> a.c.block_log2;
+  const int64_t busy = windows < blocks ? windows : blocks, wanted = (32 * sms + busy - 1) / busy;
+  const int64_t y = wanted < a.unit_groups ? wanted : a.unit_groups;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.T + a.window - 1) / a.window), static_cast<unsigned>(y));
+  cfg.gridDim = dim3(static_cast<unsigned>(windows), static_cast<unsigned>(y + a.q_slices));
   cfg.blockDim = dim3(32 * kStoreWarps);
-  cfg.dynamicSmemBytes = a.table ? static_cast<size_t>(a.n_rot / 2) << (3 + a.c.block_log2) : 0;
+  cfg.dynamicSmemBytes = a.table && !a.small ? static_cast<size_t>(a.n_rot / 2) << (3 + a.c.block_log2) : 0;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
+  const auto kernel = a.small ? store_kernel<FMT, E, VEC, true> : store_kernel<FMT, E, VEC, false>;
   if (cfg.dynamicSmemBytes > 40 * 1024) {
-    static SmemLimit limit;
-    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(store_kernel<FMT, E, VEC>));
+    static SmemLimit limit;  // (blocks that a warp holds take less)
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kernel));
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, store_kernel<FMT, E, VEC>, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 int launch_store(const StoreArgs& a, int sms, cudaStream_t st, bool pdl) {

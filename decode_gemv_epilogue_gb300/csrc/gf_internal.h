@@ -366,7 +366,9 @@ struct StoreArgs {
   int n_rot, halves, q_heads, type, vec;
   int wpu_log2;         // warps that share a block of a head
   int tpw, lane_inv;    // tokens a warp holds at a time; 65536 over a token's lanes, rounded up
-  int unit_groups, q_groups;
+  int small;            // blocks no longer than tpw, of a prompt
+  int unit_groups;      // CTAs that have work for a block (small: for a window)
+  int q_rows, q_slices; // heads a lane turns at a time; CTAs that share a window's queries
   int window;           // tokens that a CTA looks through, up to 32
 };
 int launch_store(const StoreArgs& a, int sms, cudaStream_t st, bool pdl);
@@ -404,7 +406,7 @@ struct AttendArgs {
   int ctas;
 };
 int64_t attend_workspace_bytes(int dim, int tiles, int ctas);
-int attend_ctas(int dim, int tiles, int sms);
+int attend_ctas(int sms);  // two an SM
 int launch_attend(const AttendArgs& a, cudaStream_t st, bool pdl);
 
 // One kernel launch with every argument resolved: what a call plans, and what a

@@ -489,8 +489,8 @@ typedef struct {
  * way.  A block holds earlier tokens if its first position of this call is not its first one; later
  * positions of it count as new.  A value that is not finite makes its block's scale NaN: the block reads
  * back as NaN until its first position is written again.
- * Tokens of one sequence stand next to each other in the call, by rising positions; a position at most
- * once (else the blocks concerned hold some of the values, and nothing else is touched).
+ * Tokens of one sequence stand next to each other in the call, each at the position behind the one before it
+ * (else the blocks concerned hold some of the values, and nothing else is touched).
  * n_rot must be a multiple of 8 here (GF_ERR_UNSUPPORTED); T <= 2^20, q_heads <= 1024.  No argument may
  * overlap the cache's arrays, and q_dst no input but q (rows of one fused q, k, v buffer may lie between
  * each other). */

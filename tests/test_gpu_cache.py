@@ -109,6 +109,45 @@ def test_long_prompts(G, heads, dim, page, block, T, fmt):
     same_cache(dc, c)
 
 
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("heads, dim, page, block", [(1, 16, 16, 16), (5, 64, 32, 4), (6, 80, 16, 2), (9, 128, 64, 1), (3, 256, 16, 1),
+                                                     (2, 48, 64, 4)])
+def test_small_blocks_of_prompts(G, heads, dim, page, block, fmt, f16):
+    """Blocks that a warp holds at once, several heads of them; blocks begun before, tokens without a place."""
+    rng = np.random.default_rng(3 * dim + block)
+    lengths, begun = [270, 1, 98], [3, 0, 7]
+    table, pages = au.shuffled_table(rng, lengths, page)
+    table[0, 2] = -1
+    c = au.cache_arrays(rng, fmt, pages, heads, page, dim, block, table)
+    dc = au.DeviceCache(G, c)
+    for a, b in ((np.zeros(3, dtype=int), begun), (begun, lengths)):
+        seq = np.repeat([0, 1, 5, 2], [b[0] - a[0], b[1] - a[1], 4, b[2] - a[2]]).astype(np.int32)
+        pos = np.concatenate([np.arange(a[0], b[0]), np.arange(a[1], b[1]), np.arange(4), np.arange(a[2], b[2])]).astype(np.int32)
+        k, v = values(rng, (len(seq), heads, dim), f16), values(rng, (len(seq), heads, dim), f16)
+        G.cache_store(dc.cache, dev_tensor(k), dev_tensor(v), len(seq), dev_tensor(seq), dev_tensor(pos), type=fmt_type(G, k))
+        oatt.store(c, k, v, seq, pos)
+        same_cache(dc, c)
+
+
+@pytest.mark.parametrize("T", [3, 600])
+def test_queries_without_a_place(G, T):
+    """Left as they were, among ones that are turned."""
+    H, Hq, D, block = 2, 5, 48, 1
+    rng = np.random.default_rng(T)
+    c = au.cache_arrays(rng, "i8", 40, H, 16, D, block, np.arange(40)[None, :])
+    dc = au.DeviceCache(G, c)
+    seq, pos = np.where(np.arange(T) % 7 == 2, 1, 0).astype(np.int32), np.arange(T, dtype=np.int32)
+    q, k, v = (dev_tensor(values(rng, (T, h, D), False)) for h in (Hq, H, H))
+    rot = torch.empty(G.rope_table_bytes(D), dtype=torch.uint8, device="cuda")
+    G.rope_table(rot, D)
+    want, got = torch.empty_like(q), torch.full_like(q, 7.0)
+    G.rope(q, T, Hq, D, dev_tensor(pos), rot, want)
+    G.cache_store(dc.cache, k, v, T, dev_tensor(seq), dev_tensor(pos), rope=rot, q=q, q_heads=Hq, q_dst=got)
+    want[dev_tensor(seq) == 1] = 7.0
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("fmt", ["i8", "e4m3"])
 def test_hard_values(G, fmt):
     """Ties, zeros, the largest and smallest magnitudes, scales at both ends."""
@@ -201,7 +240,8 @@ def test_strides_and_alignment(G, ld, at, f16):
 @pytest.mark.parametrize("f16", [False, True])
 @pytest.mark.parametrize("layout", [0, 1])
 @pytest.mark.parametrize("T, dim, n_rot, block, fused", [(5, 128, 128, 16, True), (1, 64, 32, 1, False), (300, 128, 64, 32, True),
-                                                         (40, 80, 40, 4, False), (270, 256, 256, 64, False), (3, 96, 0, 16, True)])
+                                                         (40, 80, 40, 4, False), (270, 256, 256, 64, False), (3, 96, 0, 16, True),
+                                                         (290, 128, 64, 2, True), (400, 80, 0, 1, False)])
 def test_with_rotation(G, T, dim, n_rot, block, fused, layout, f16):
     """Equal, bit for bit, to gf_rope followed by the store of its 32-bit results; queries to gf_rope's."""
     rng = np.random.default_rng(T + dim)
