@@ -5,7 +5,7 @@
     ids, w = the top_k experts of l
     y   = h + sum_j w_j Wd_e (silu(Wg_e n) * (Wu_e n)),  n = h / rms(h) * gamma
 
-(attention is not part of the library: x stands for its output).
+(x stands for the attention block's output; attn_step is a step of that block).
 
     python -m decode_gemv_epilogue_gb300.moe_step
 
