@@ -342,8 +342,8 @@ static int check_attend(const gf_cache* c, const void* q, int64_t T, int64_t q_h
   if (q_heads % c->heads != 0) return GF_ERR_INVALID;
   if (T > kAttMaxTokens || q_heads > kMaxHeads || o->run > kAttMaxTokens || o->window > INT32_MAX)
     return GF_ERR_UNSUPPORTED;
-  // (chunks of all items, counted in 64 bits times the warps that share them)
-  if (static_cast<double>(T) * q_heads * (c->table_ld * c->page / 16 + 2) > 2251799813685248.0) return GF_ERR_UNSUPPORTED;
+  // (units of all items, counted in 64 bits times the warps that share them)
+  if (static_cast<double>(T) * q_heads * (c->table_ld * c->page / 16 + 4) > 2251799813685248.0) return GF_ERR_UNSUPPORTED;
   if (T == 0) return GF_OK;
   if ((e = check_tokens(seq, pos)) != GF_OK) return e;
   int vec = 1;

@@ -18,7 +18,7 @@
 // running ones in 32 bits, outside the matrix unit (which truncates).
 //
 // Items, (tokens of a sequence next to each other, head of the cache, part of its queries), are laid end
-// to end by their number of chunks and one more for their start and end; every CTA takes an equal stretch
+// to end by their number of chunks and some more for their start and end; every CTA takes an equal stretch
 // and every warp an equal stretch of that, whatever the sequences' lengths.  Warps know nothing of each other
 // until they are done: the parts of an item that reaches over several go through the workspace, where the CTA
 // joins its own and a second launch joins the CTAs', both in order.  (A CTA to an item, its warps joined in shared
@@ -50,6 +50,10 @@ struct AttShape {
 template <int DC>
 constexpr int kUnitBytes = DC == 64 ? 8 : 16;  // of a value row, in a lane's hands
 
+// An item's start and end in units of a chunk's time.  At one unit 61 sequences of 100 to 8000 keys took 66 us where
+// 61, 244 of them 219 where 209; at six 63 and 215.  They come first, and a share that ends within them leaves the
+// item to the next: only a share's chunks make a part.
+constexpr int kItemUnits = 3;
 constexpr float kNoMax = -1e30f;   // running maximum of a row without keys
 constexpr uint32_t kWeightBits = 8;     // weights times the largest scale reach 2^8 (f16 parts)
 
@@ -255,13 +259,13 @@ __device__ __forceinline__ int64_t share(const AttHeader& h, int64_t i) {
 }
 
 __device__ __forceinline__ AttSpan span_of(const Item& it) {
-  return AttSpan{it.begin, it.begin + it.chunks + 1, it.t0, it.n, it.hs, 0};
+  return AttSpan{it.begin, it.begin + it.chunks + kItemUnits, it.t0, it.n, it.hs, 0};
 }
 
 template <int CT>
 __device__ __forceinline__ uint32_t units_at(const AttendArgs& a, int t) {
   Item it;
-  return t < a.T && item_at<CT>(a, t, it) ? it.chunks + 1 : 0;
+  return t < a.T && item_at<CT>(a, t, it) ? it.chunks + kItemUnits : 0;
 }
 
 __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {  // inclusive
@@ -397,8 +401,8 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
       const int l = __ffs(__ballot_sync(0xffffffffu, incl * HS > start)) - 1;
       item_at<CT>(a, k * 32 + l, item);
       const int64_t b = __shfl_sync(0xffffffffu, incl - n, l) * HS;
-      item.hs = static_cast<int>((start - b) / (item.chunks + 1));
-      item.begin = b + static_cast<int64_t>(item.hs) * (item.chunks + 1);
+      item.hs = static_cast<int>((start - b) / (item.chunks + kItemUnits));
+      item.begin = b + static_cast<int64_t>(item.hs) * (item.chunks + kItemUnits);
     }
     if (start == cta_start && lane == 0) {
       if (blockIdx.x == 0) *reinterpret_cast<AttHeader*>(a.workspace) = head;
@@ -510,7 +514,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
     };
     // The item's chunks [c0, c1) of this warp's stretch.
     auto stretch = [&](const Item& it, int& c0, int& c1) {
-      const int64_t from = start - it.begin - 1, to = stop - it.begin - 1;
+      const int64_t from = start - it.begin - kItemUnits, to = stop - it.begin - kItemUnits;
       c0 = from < 0 ? 0 : static_cast<int>(from);
       c1 = to < it.chunks ? static_cast<int>(to) : it.chunks;
     };
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
     uint32_t hidden_next = c0 < c1 ? fetch(src, c0, pages_of(src, c0)) : 0;
     Pages pages = pages_of(src, c0 + 1);  // of the chunk that is fetched next: looked up a chunk ahead
 
-    for (;;) {
+    while (stop > item.begin + kItemUnits) {  // (a first item without a chunk of its own is the next warp's)
       // ---- the item's queries, hi and lo parts in the order of the instructions' rows: of row g, lane (g, c4)
       // takes units c4, c4 + 4, .. as it does of a key
       uint4 qr[S::kQRegs ? KS : 1];
@@ -756,8 +760,8 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
       }
 
       // ---- the next item's first chunk starts on its way
-      const int64_t end = item.begin + item.chunks + 1;
-      const bool last = end >= stop;
+      const int64_t end = item.begin + item.chunks + kItemUnits;
+      const bool last = end + kItemUnits >= stop;
       Item next = item;
       if (!last) {
         if (item.hs + 1 < HS) {
@@ -800,7 +804,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
           if (c4 == 0) put_row(8 * i + g, row >= 0, t, head, m[i], z);
         }
       };
-      if (start > item.begin || end > stop) {
+      if (start > item.begin + kItemUnits || end > stop) {
         const int slot = start >= item.begin ? 0 : 1;
         auto put_row = [&](int r, bool, int, int, float top, float z) {
           part_rows[warp][slot][r] = make_float2(top, z);
@@ -849,7 +853,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
     const uint32_t behind = firsts & (firsts - 1);
     const uint32_t members = there & ~((1u << e) - 1) & (behind ? (behind & -behind) - 1 : 0xffffffffu);
     const AttSpan s = spans[e / 2][e % 2];
-    const bool done = s.begin >= cta_start && s.end <= cta_start + cta_units;
+    const bool done = s.begin + kItemUnits >= cta_start && s.end <= cta_start + cta_units;
     float* out = cta_parts + (s.begin <= cta_start ? 0 : S::kPart);
     for (int k = 0; k < S::kSlices; ++k) {
       if (task++ % W != warp) continue;
@@ -881,11 +885,11 @@ struct Split {
   int n;
 };
 
-// Whether CTA i's record is of an item that begins before it and within the stretch before.
+// Whether CTA i's record is of an item whose first chunk is in the stretch before.
 __device__ __forceinline__ bool split_at(const AttendArgs& a, const AttHeader& h, int64_t i, AttSpan& s) {
   if (i >= a.ctas) return false;
   s = reinterpret_cast<const AttSpan*>(reinterpret_cast<const uint8_t*>(a.workspace) + kAttHead)[i];
-  return i < h.ctas && share(h, i) > s.begin && share(h, i - 1) <= s.begin;
+  return i < h.ctas && share(h, i) > s.begin + kItemUnits && share(h, i - 1) <= s.begin + kItemUnits;
 }
 
 // Its parts, by a whole warp.
