@@ -208,11 +208,9 @@ __device__ __forceinline__ void keys_of(const AttendArgs& a, int t, int& seq, in
   lo = static_cast<int>(first < 0 ? 0 : first < hi ? first : hi);
 }
 
-// Whether an item may begin with token t wherever the sequences lie: `run` tokens of a sequence are expected
-// next to each other, and fall into items of `tokens`.
-__device__ __forceinline__ bool item_edge(const AttendArgs& a, int t) { return t % a.run % a.tokens == 0; }
-
-// The item that begins with token t, if one does: neighbouring tokens of one sequence up to the next edge.
+// The item that begins with token t, if one does: neighbouring tokens of one sequence up to the next edge.  `run`
+// tokens of a sequence are expected next to each other, and fall into items of `tokens`: an item may begin at their
+// edges wherever the sequences lie.
 template <int CT>
 __device__ __forceinline__ bool item_at(const AttendArgs& a, int t, Item& it) {
   int seq, lo, hi;
@@ -221,18 +219,24 @@ __device__ __forceinline__ bool item_at(const AttendArgs& a, int t, Item& it) {
   it.n = 1;
   it.seq = seq;
   if (a.tokens > 1 && seq >= 0) {
-    if (!item_edge(a, t)) {
+    const int in_run = t % a.run, in_item = in_run % a.tokens;
+    if (in_item > 0) {
       int s, l, h;
       keys_of(a, t - 1, s, l, h);
       if (s == seq) return false;
     }
-    for (int i = t + 1; i < a.T && !item_edge(a, i); ++i) {
+    const int most = min(min(a.tokens - in_item, a.run - in_run), a.T - t);
+    bool same = true;
+#pragma unroll 4
+    for (int i = 1; i < most; ++i) {  // (no way out: the loads do not wait for one another)
       int s, l, h;
-      keys_of(a, i, s, l, h);
-      if (s != seq) break;
-      lo = l < lo ? l : lo;
-      hi = h > hi ? h : hi;
-      ++it.n;
+      keys_of(a, t + i, s, l, h);
+      same &= s == seq;
+      if (same) {
+        lo = l < lo ? l : lo;
+        hi = h > hi ? h : hi;
+        ++it.n;
+      }
     }
   }
   it.lo = lo;
