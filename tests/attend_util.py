@@ -22,7 +22,7 @@ def cache_arrays(rng, fmt, n_pages, heads, page, dim, block, table, codes="rando
         c[name] = x
         shape = (n_pages, heads, page // block)
         if fmt == "i8":  # values about 1
-            s = (1024 + rng.integers(0, 3072, shape)) * 2.0 ** -17
+            s = rng.integers(1024, 4096, shape) * 2.0 ** -17
         else:
             s = 2.0 ** rng.integers(-8, -5, shape)
         c[name + "_scale"] = s.astype(np.float32)
