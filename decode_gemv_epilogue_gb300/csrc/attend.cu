@@ -4,7 +4,7 @@
 // is reading the codes: each warp copies (cp.async) chunks of CT tokens, whole lines of consecutive addresses, into
 // stages of its own, a chunk ahead.  (Copies of just the bytes that a lane decodes itself, in fours of rows, left
 // the memory at 5.0 TB/s where consecutive ones reach 6.4.)  With the arithmetic, 927 instructions a chunk at three
-// warps a scheduler, 256 sequences of 4000 to 8000 keys and 32 query heads over 8 of 128 take 546 us, 5.6 TB/s.
+// warps a scheduler, 256 sequences of 4000 to 8000 keys and 32 query heads over 8 of 128 take 555 us, 5.5 TB/s.
 //
 // A warp takes a chunk of CT tokens.  m16n8k16 with the queries as the 16 rows: eight rows' f16 high parts and
 // the same rows' low parts (q = hi + lo to 22 bits under a power of two a row), so that one instruction
@@ -14,7 +14,7 @@
 //           two k pairs of one instruction;
 //   values: lane (g, c) takes a unit of the four tokens that its k indices mean; the bytes of four
 //           tokens' words are paired by dim, and dim j of column g's unit is column g of instruction j.
-// The weights p * scale_v are split into hi + lo like the queries.  A chunk's products are added to the
+// The weights p * scale_v are split into hi + lo like the queries, under a power of two a row.  A chunk's products are added to the
 // running ones in 32 bits, outside the matrix unit (which truncates).
 //
 // Items, (tokens of a sequence next to each other, head of the cache, part of its queries), are laid end
@@ -56,7 +56,12 @@ constexpr int kUnitBytes = DC == 64 ? 8 : 16;  // of a value row, in a lane's ha
 // item to the next: only a share's chunks make a part.
 constexpr int kItemUnits = 3;
 constexpr float kNoMax = -1e30f;   // running maximum of a row without keys
-constexpr uint32_t kWeightBits = 8;     // weights times the largest scale reach 2^8 (f16 parts)
+// Weights times their values' scales, as f16 parts, reach 2^15 in units of a power of two a row.  A unit serves
+// chunks whose scales lie within 2^-13 of it: the parts' last step, 2^-24, is then 2^-26 of the smallest of them.
+constexpr int kWeightBits = 15;
+constexpr int kScaleSpread = 12;  // exponents below the unit's
+// A unit may fall to 2^-64 of what earlier keys may have left in the sums: those reach 2^(64 + 24) then, times the keys.
+constexpr float kUnitFall = 64.0f;
 
 // A stage is lines of 128 bytes (two tokens of 64, half a token of 256) whose 16-byte units are exchanged by
 // the line's number.  Unit u of token r of a chunk:
@@ -594,9 +599,15 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 #pragma unroll
         for (int n = 0; n < NO; ++n) o[i][n] = make_float2(0.0f, 0.0f);
       }
-      // biased exponent of the power of two, above every scale so far, that the values' scales are taken by; at
-      // least that of the format's smallest scale
-      uint32_t vexp = 127 - 111;
+      // Biased exponent of each row's unit, at least that of the format's smallest scale, and by how many powers of
+      // two the sums' own (the largest weight times scale that went in, at the present maximum) may lie above it.
+      int unit[NM];
+      float room[NM];
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {
+        unit[i] = 127 - 111;
+        room[i] = 0.0f;
+      }
       const int t0 = token_of<DC>(2 * c4), t1 = token_of<DC>(2 * c4 + 1);  // this lane's columns
 
       for (int c = c0; c < c1; ++c) {
@@ -605,9 +616,11 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
           ring_scales[scale_lane] = key_scale;
           ring_scales[CT + scale_lane] = value_scale;
         }
-        // (a scale that is not finite makes its own rows NaN, and is no measure for the others)
-        const uint32_t vbits = __float_as_uint(value_scale);
-        const uint32_t vtop = __reduce_max_sync(0xffffffffu, vbits < 0x7f800000u ? vbits : 0u);
+        // The chunk's largest and smallest scale.  (One that is not finite makes its own rows NaN, and is no measure
+        // for the others; nor is zero, which tokens without a place have.)
+        const uint32_t vbits = __float_as_uint(value_scale) & 0x7fffffffu;
+        const int vtop = static_cast<int>(__reduce_max_sync(0xffffffffu, vbits < 0x7f800000u ? vbits : 0u) >> 23) + 1;
+        const int vlow = static_cast<int>(__reduce_min_sync(0xffffffffu, vbits - 1u) >> 23) + 1;
         if (c + 1 < c1) {
           hidden_next = fetch(src, c + 1, pages);
           pages = pages_of(src, c + 2);
@@ -664,12 +677,10 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
         }
 
         // ---- softmax; the weights, times the values' scales, as instructions' rows
-        const uint32_t vnow = max(vexp, (vtop >> 23) + 1);
-        // 2^(kWeightBits - (vnow - 127)): weights times it lie below 2^8
-        const float vinv = __uint_as_float((254 + kWeightBits - vnow) << 23);
-        const int rise = static_cast<int>(vexp) - static_cast<int>(vnow);
-        const float vstep = rise == 0 ? 1.0f : exp2_fast(static_cast<float>(rise));
-        vexp = vnow;
+        bool other = false;  // a row's unit does not serve this chunk
+#pragma unroll
+        for (int i = 0; i < NM; ++i) other |= vtop > unit[i] || vlow < unit[i] - kScaleSpread;
+        other = __any_sync(0xffffffffu, other);
         uint4 pf[NM][KG];
         float alpha[NM];
 #pragma unroll
@@ -687,8 +698,36 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 #pragma unroll
           for (int n = 0; n < NT; ++n) top = fmaxf(top, fmaxf(x[i][n].x, x[i][n].y));
           top = fmaxf(m[i], quad_max(top));
-          alpha[i] = exp2_fast(m[i] - top);
+          const float down = m[i] - top, keep = exp2_fast(down);
+          alpha[i] = keep;
           m[i] = top;
+          if (__builtin_expect(other, 0)) {
+            // A unit for this chunk: above its scales, or where those lie far apart, above the largest weight times
+            // scale among the keys that the row sees.  A block of large values that the softmax gives no weight, or that
+            // only other rows see, so takes no bits from the others (with a unit above every scale so far, 2^20 between
+            // scales left errors of 1e-3 of the row, 2^34 zeros; it took 545 us where 555 in the case above).
+            int now = vtop;
+            if (vlow < vtop - kScaleSpread) {
+              float most = 0.0f;
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const float2 v2 = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c4);
+                const float a = fabsf(exp2_fast(x[i][n].x - top) * v2.x), b = fabsf(exp2_fast(x[i][n].y - top) * v2.y);
+                most = fmaxf(most, fmaxf(a < INFINITY ? a : 0.0f, b < INFINITY ? b : 0.0f));
+              }
+              now = static_cast<int>(__float_as_uint(quad_max(most)) >> 23) + 1;
+            }
+            const float held = fmaxf(static_cast<float>(unit[i]) + room[i] + down, 0.0f);  // the sums' own, as an exponent
+            now = max(max(now, 127 - 111), static_cast<int>(ceilf(held - kUnitFall)));
+            const int step = unit[i] - now, half = step / 2;
+            alpha[i] = keep * __uint_as_float((127 + half) << 23) * __uint_as_float((127 + step - half) << 23);
+            unit[i] = now;
+            room[i] = fmaxf(held - static_cast<float>(now), 0.0f);
+          } else {
+            room[i] = fmaxf(room[i] + down, 0.0f);
+          }
+          // 2^kWeightBits a unit
+          const float vinv = __uint_as_float((254 + kWeightBits - unit[i]) << 23);
           float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
@@ -696,7 +735,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
             const float2 e = fsub2(x[i][n], make_float2(top, top));
             const float2 p = make_float2(exp2_fast(e.x), exp2_fast(e.y));
             sum = fadd2(sum, p);
-            float2 y = fmul2(p, fmul2(v2, make_float2(vinv, vinv)));
+            float2 y = fmul2(fmul2(p, v2), make_float2(vinv, vinv));
             if (!whole) {  // a masked token's weight is zero whatever lies in its scale
               if (x[i][n].x == -INFINITY) y.x = 0.0f;
               if (x[i][n].y == -INFINITY) y.y = 0.0f;
@@ -711,8 +750,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
               pf[i][n / 2].w = w;
             }
           }
-          l[i] = l[i] * alpha[i] + (sum.x + sum.y);
-          alpha[i] *= vstep;
+          l[i] = l[i] * keep + (sum.x + sum.y);
         }
 
         // ---- values
@@ -785,11 +823,10 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 
       // ---- results, or a part to be joined: the warp's last one into its stages, which nothing comes into any
       // more, one before into the workspace
-      const float back = __uint_as_float((vexp - kWeightBits) << 23);
       auto give = [&](auto put_sums, auto put_row, bool divide) {
 #pragma unroll
         for (int i = 0; i < NM; ++i) {
-          const float z = quad_sum(l[i]);
+          const float back = __uint_as_float((unit[i] - kWeightBits) << 23), z = quad_sum(l[i]);
           const float inv = !divide ? back : z == 0.0f ? 0.0f : back / z;  // no keys: zeros
           int t, head;
           const bool live = row_of(a, item.t0, item.n, item.hs, 8 * i + g, t, head);

@@ -523,8 +523,10 @@ GF_API int gf_prepare_cache_load(const gf_cache* cache, int64_t T, const int32_t
 /* Attention of T tokens over the cache: query head h of token t sees the keys of head h / (q_heads / heads)
  * at positions max(0, pos - window + 1) .. pos of its sequence,
  *     s_j = scale * q . K_j,   dst = sum_j softmax(s)_j V_j,   lse = ln sum_j exp(s_j)
- * in 32-bit arithmetic (q and the weights as pairs of binary16, to 2^-22).  The tokens' own keys have been
- * stored before.  Positions in pages that the table does not have are not seen; a row that sees nothing
+ * in 32-bit arithmetic.  q is taken as pairs of binary16, to 2^-22 of an element or 2^-39 of its row's largest; so
+ * are the softmax's weights (1 for the largest) times their values' scales, to 2^-22 of each or 2^-27 of the scale,
+ * or, where the scales of 32 neighbouring keys lie more than 2^12 apart, 2^-39 of the largest weight times scale
+ * that the row sees among them.  Weights below 2^-126 are zero.  The tokens' own keys have been stored before.  Positions in pages that the table does not have are not seen; a row that sees nothing
  * (of a token without a place, for instance) is 0, its lse -inf.  A token whose pos reaches beyond the table
  * sees what lies in it.
  *  q, dst    : [T][q_heads][dim]; q_heads a multiple of heads, <= 1024.  T <= 2^16.

@@ -1,0 +1,136 @@
+"""gf_attend on the GPU where the values' scales of a sequence lie far apart: a block of large values that a row
+gives no weight, or does not see, takes nothing from the others."""
+
+import numpy as np
+import pytest
+
+import attend_util as au
+from gpu_util import assert_within
+from oracle import attend as oatt
+from test_gpu_attend import call, check, queries, setup
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+
+@pytest.fixture(scope="module")
+def G(lib):
+    yield lib
+    assert lib.device_status() == 0
+
+
+LOWEST = {"i8": 0x81, "e4m3": 0xfe}  # the codes of -127 and -448
+
+
+def no_zeros(codes):
+    """A large value that is zero would leave its element to the small ones."""
+    return np.where(codes & 0x7f, codes, codes | 0x18).astype(np.uint8)
+
+
+def blocks_at(c, s, blocks):
+    """(page, block of the page) of blocks of sequence s."""
+    per = c["k"].shape[2] // c["block"]
+    return [(int(c["table"][s, b // per]), b % per) for b in blocks]
+
+
+def repel(c, s, blocks, q, weight=100.0):
+    """Keys of these blocks, by their first element alone, score `weight` and more below what the others make of it."""
+    D, H = c["k"].shape[3], c["k"].shape[1]
+    c["k"][..., 0] = 0
+    least = c["k_scale"].min() * {"i8": 127.0, "e4m3": 448.0}[c["fmt"]]
+    q[..., 0] = np.float32((weight + 40.0) * np.sqrt(D) / least)  # (others' scores lie within some 20 of zero)
+    for p, b in blocks_at(c, s, blocks):
+        c["k"][p, :, b * c["block"]:(b + 1) * c["block"], 0] = LOWEST[c["fmt"]]
+
+
+def bounds_beside(c, q, seq, pos, window, blocks):
+    """attend_bounds with the scores of the keys that have weight, and all of what the blocks contribute: their keys'
+    scores are large, and so are their errors, but they have no weight to be wrong."""
+    want, lse, mass, spread = oatt.attend(c, q, seq, pos, window=window)
+    rest = {k: v.copy() if isinstance(v, np.ndarray) else v for k, v in c.items()}
+    for p, b in blocks:
+        rest["v"][p, :, b * c["block"]:(b + 1) * c["block"]] = 0
+        rest["k"][p, :, b * c["block"]:(b + 1) * c["block"]] = 0
+    without = {k: v.copy() if isinstance(v, np.ndarray) else v for k, v in rest.items()}
+    without["k"] = c["k"]
+    _, _, mass_rest, _ = oatt.attend(without, q, seq, pos, window=window)
+    spread = oatt.attend(rest, q, seq, pos, window=window)[3]
+    keys = np.array([[len(oatt.seen(c, int(s), int(p), window))] * q.shape[1] for s, p in zip(seq, pos)], dtype=np.float64)
+    b, bl = au.attend_bounds(c, want, lse, mass_rest, spread, keys, False)
+    return want, lse, b + (mass - mass_rest), bl
+
+
+def where_of(where, n, block):
+    last = (n - 1) // block
+    return {"first": [0], "middle": [last // 2], "last": [last], "half": list(range(last // 2 + 1))}[where]
+
+
+# H, group, D, page, block
+SHAPES = [(1, 4, 128, 64, 16), (2, 1, 64, 16, 4), (1, 16, 128, 16, 1), (1, 8, 256, 64, 32), (1, 4, 96, 32, 8), (1, 12, 64, 64, 64)]
+
+
+@pytest.mark.parametrize("where", ["first", "middle", "last", "half"])
+@pytest.mark.parametrize("ratio", [10, 20, 40, 90])
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("H, group, D, page, block", SHAPES)
+def test_large_values_without_weight(G, H, group, D, page, block, fmt, ratio, where):
+    """Weights below e^-100, values 2^ratio times the others': they count for nothing."""
+    rng = np.random.default_rng(D + ratio)
+    n = 1000
+    c = setup(rng, fmt, [n], H, page, D, block)
+    q = queries(rng, 1, H * group, D)
+    which = where_of(where, n, block)
+    repel(c, 0, which, q)
+    at = blocks_at(c, 0, which)
+    for p, b in at:
+        c["v_scale"][p, :, b] *= np.float32(2.0 ** ratio)
+    seq, pos = [0], [n - 1]
+    want, lse, b, bl = bounds_beside(c, q, seq, pos, 0, at)
+    got, gl = call(G, au.DeviceCache(G, c), q, seq, pos)
+    assert_within(got, want, b, "out")
+    assert_within(gl, lse, bl, "lse")
+    assert au.norm_error(got, want) <= au.NORM_TOL
+
+
+@pytest.mark.parametrize("window", [0, 60])
+@pytest.mark.parametrize("ratio", [20, 40, 100])
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("group, D", [(2, 64), (2, 128), (4, 128), (2, 256), (1, 80)])
+def test_large_values_beside(G, group, D, fmt, ratio, window):
+    """Rows that share their keys' reading with rows that see a block of large values, and do not see it themselves, are
+    right by their own measure, as are those that do."""
+    rng = np.random.default_rng(ratio + D)
+    c = setup(rng, fmt, [200], 1, 16, D, 16)
+    c["v"][c["table"][0, 7]] = no_zeros(c["v"][c["table"][0, 7]])
+    c["v_scale"][c["table"][0, 7]] *= np.float32(2.0 ** ratio)  # positions 112 to 127
+    seq, pos = np.zeros(4, dtype=np.int32), np.array([40, 100, 120, 199], dtype=np.int32)
+    dc = au.DeviceCache(G, c)
+    q = queries(rng, 4, group, D)
+    got, _ = check(G, c, q, seq, pos, window=window, dc=dc, run=4)
+    want = oatt.attend(c, q, seq, pos, window=window)[0]
+    for t in range(4):
+        assert au.norm_error(got[t], want[t]) <= au.NORM_TOL, t
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scales_that_come_and_go(G, D, fmt):
+    """Each block of 32 keys has more weight than all before it, and values of quite another size."""
+    rng = np.random.default_rng(D)
+    n, block = 640, 32
+    c = setup(rng, fmt, [n], 1, 64, D, block)
+    q = queries(rng, 1, 4, D, size=0.02)
+    c["k"][..., 0] = 0
+    q[..., 0] = np.float32(2.0 * np.sqrt(D))
+    one = {"i8": lambda v: v & 0xff, "e4m3": lambda v: int(oatt.encode("e4m3", np.array([float(v)]))[0])}[fmt]
+    for i in range(n // block):  # scores rise by 5 a block or so
+        (p, b), = blocks_at(c, 0, [i])
+        c["k"][p, :, b * block:(b + 1) * block, 0] = one(i * 5)
+        c["k_scale"][p, :, b] = 0.5
+        c["v_scale"][p, :, b] = np.float32(2.0 ** [-60, 3, -20, 40, -7][i % 5])
+    c["v"] = no_zeros(c["v"])
+    for last in (n - 1, 400, 330, 100):
+        check(G, c, q, [0], [last], norm=False)
