@@ -24,6 +24,8 @@
 // joins its own and a second launch joins the CTAs', both in order.  (A CTA to an item, its warps joined in shared
 // memory at each one's end, took twice as long for 61 sequences of 100 to 8000 keys: short ones cost it a
 // barrier's round each.)
+#include <cfloat>
+
 #include "cache_device.cuh"
 #include "gf_device.cuh"
 #include "rope_device.cuh"
@@ -55,7 +57,8 @@ constexpr int kUnitBytes = DC == 64 ? 8 : 16;  // of a value row, in a lane's ha
 // 61, 244 of them 219 where 209; at six 63 and 215.  They come first, and a share that ends within them leaves the
 // item to the next: only a share's chunks make a part.
 constexpr int kItemUnits = 3;
-constexpr float kNoMax = -1e30f;   // running maximum of a row without keys
+// Running maximum of a row without keys: no finite score lies below it, and a masked one, -inf, has no weight under it.
+constexpr float kNoMax = -FLT_MAX;
 // Weights times their values' scales, as f16 parts, reach 2^15 in units of a power of two a row.  A unit serves
 // chunks whose scales lie within 2^-13 of it: the parts' last step, 2^-24, is then 2^-26 of the smallest of them.
 constexpr int kWeightBits = 15;

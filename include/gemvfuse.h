@@ -526,9 +526,10 @@ GF_API int gf_prepare_cache_load(const gf_cache* cache, int64_t T, const int32_t
  * in 32-bit arithmetic.  q is taken as pairs of binary16, to 2^-22 of an element or 2^-39 of its row's largest; so
  * are the softmax's weights (1 for the largest) times their values' scales, to 2^-22 of each or 2^-27 of the scale,
  * or, where the scales of 32 neighbouring keys lie more than 2^12 apart, 2^-39 of the largest weight times scale
- * that the row sees among them.  Weights below 2^-126 are zero.  The tokens' own keys have been stored before.  Positions in pages that the table does not have are not seen; a row that sees nothing
- * (of a token without a place, for instance) is 0, its lse -inf.  A token whose pos reaches beyond the table
- * sees what lies in it.
+ * that the row sees among them.  Weights below 2^-126 are zero, and a key whose score times log2(e) leaves the
+ * finite numbers downwards has none.  The tokens' own keys have been stored before.
+ * Positions in pages that the table does not have are not seen; a row that sees nothing (of a token without a
+ * place, for instance) is 0, its lse -inf.  A token whose pos reaches beyond the table sees what lies in it.
  *  q, dst    : [T][q_heads][dim]; q_heads a multiple of heads, <= 1024.  T <= 2^16.
  *  run       : how many tokens of one sequence stand next to each other (drafted tokens, a prompt's part;
  *              0 or 1: a decode step).  They then share one reading of the keys.  Only speed depends on it.

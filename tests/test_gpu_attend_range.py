@@ -134,3 +134,50 @@ def test_scales_that_come_and_go(G, D, fmt):
     c["v"] = no_zeros(c["v"])
     for last in (n - 1, 400, 330, 100):
         check(G, c, q, [0], [last], norm=False)
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("D, group", [(64, 1), (128, 4), (128, 16), (256, 2)])
+@pytest.mark.parametrize("size", [1e20, 1e30, 1e34, 1e36])
+def test_lowest_scores(G, size, D, group, fmt):
+    """Scores far below zero, all of them: one key is seen whatever its score, and the largest of many is alone."""
+    rng = np.random.default_rng(D)
+    n, block = 1500, 4
+    c = setup(rng, fmt, [n], 1, 16, D, block)
+    one = {"i8": lambda v: v, "e4m3": lambda v: int(oatt.encode("e4m3", np.array([float(v)]))[0])}[fmt]
+    c["k"][:] = one(96)
+    c["k_scale"][:] = 1.0 / 64
+    best = 1000  # the key whose score is the largest, and the last one's the next
+    p, s = oatt.place(c, 0, best)
+    c["k"][p, :, s] = one(32)
+    p, s = oatt.place(c, 0, n - 1)
+    c["k"][p, :, s] = one(64)
+    dc = au.DeviceCache(G, c)
+    for last, window in ((0, 0), (n - 1, 1), (n - 1, 0), (n - 1, 400), (best, 0), (40, 0)):
+        q = np.full((1, group, D), -size, dtype=np.float32)
+        if last == 40:  # neighbours' scores: the middle one the largest
+            p, s = oatt.place(c, 0, 20)
+            c["k"][p, :, s] = one(48)
+            dc = au.DeviceCache(G, c)
+        want, lse, mass, _ = oatt.attend(c, q, [0], [last], window=window)
+        assert np.isfinite(lse).all() and (lse < -1e18).all()
+        got, gl = call(G, dc, q, [0], [last], window=window)
+        # one weight of 1: its parts, the matrix unit, the joining and the division, as attend_bounds counts them
+        rel = 2.0 ** -20 + (1500 / 16 + 300) * 4 * au.U
+        assert_within(got, want, mass * rel + 1e-30, "out")
+        # q exactly so in two parts to 2^-22, D / 16 instructions 2^-22 each, and ten roundings
+        assert_within(gl, lse, np.abs(lse) * (2.0 ** -22 * (1 + D / 16) + 10 * au.U), "lse")
+
+
+def test_lowest_scores_of_two_parts(G):
+    """Sequences whose scores are all low are joined from many warps' parts, beside ones that see nothing."""
+    rng = np.random.default_rng(20)
+    c = setup(rng, "i8", [900, 900], 2, 16, 64, 16)
+    c["k"][:] = 64
+    c["k_scale"][:] = 1.0
+    q = np.full((3, 4, 64), -1e33, dtype=np.float32)
+    want, lse, mass, _ = oatt.attend(c, q, [0, -1, 1], [899, 0, 700])
+    got, gl = call(G, au.DeviceCache(G, c), q, [0, -1, 1], [899, 0, 700])
+    assert_within(got, want, mass * (2.0 ** -20 + 400 * 4 * au.U) + 1e-30, "out")
+    assert not got[1].any() and np.isneginf(gl[1]).all()
+    assert np.all(np.abs(gl[[0, 2]] - lse[[0, 2]]) <= np.abs(lse[[0, 2]]) * (2.0 ** -22 * 5 + 10 * au.U))
