@@ -65,6 +65,8 @@ constexpr int kWeightBits = 15;
 constexpr int kScaleSpread = 12;  // exponents below the unit's
 // A unit may fall to 2^-64 of what earlier keys may have left in the sums: those reach 2^(64 + 24) then, times the keys.
 constexpr float kUnitFall = 64.0f;
+// Parts hold their sums times this: a mean of the largest values is finite, and so is what a million of them add up to.
+constexpr float kPartScale = 0x1p-20f;
 
 // A stage is lines of 128 bytes (two tokens of 64, half a token of 256) whose 16-byte units are exchanged by
 // the line's number.  Unit u of token r of a chunk:
@@ -337,7 +339,7 @@ __device__ __forceinline__ void join_out(const AttendArgs& a, const AttSpan& s, 
   const int d = (value_unit<DC>(2 * (lane & 3) + k / (UB / 4) % 2) + 8 * (k / (UB / 2))) * UB + k % (UB / 4) * 4;
   int t, head;
   if (!row_of(a, s.t0, s.n, s.hs, r, t, head)) return;
-  const float inv = z == 0.0f ? 0.0f : 1.0f / z;  // no keys: zeros
+  const float inv = z == 0.0f ? 0.0f : 1.0f / kPartScale / z;  // no keys: zeros
   if (d < a.c.dim)
     write_out(a, t * a.ld_dst + static_cast<int64_t>(head) * a.c.dim + d,
               make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
@@ -830,7 +832,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 #pragma unroll
         for (int i = 0; i < NM; ++i) {
           const float back = __uint_as_float((unit[i] - kWeightBits) << 23), z = quad_sum(l[i]);
-          const float inv = !divide ? back : z == 0.0f ? 0.0f : back / z;  // no keys: zeros
+          const float inv = !divide ? back * kPartScale : z == 0.0f ? 0.0f : back / z;  // no keys: zeros
           int t, head;
           const bool live = row_of(a, item.t0, item.n, item.hs, 8 * i + g, t, head);
           const int64_t row = live ? t * a.ld_dst + static_cast<int64_t>(head) * D : -1;

@@ -181,3 +181,17 @@ def test_lowest_scores_of_two_parts(G):
     assert_within(got, want, mass * (2.0 ** -20 + 400 * 4 * au.U) + 1e-30, "out")
     assert not got[1].any() and np.isneginf(gl[1]).all()
     assert np.all(np.abs(gl[[0, 2]] - lse[[0, 2]]) <= np.abs(lse[[0, 2]]) * (2.0 ** -22 * 5 + 10 * au.U))
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("D, group, n", [(64, 1, 40), (64, 2, 3000), (128, 4, 3000), (128, 16, 700), (256, 2, 1000), (128, 4, 20000)])
+def test_largest_values(G, D, group, n, fmt):
+    """Values as large as the format holds: their mean is no larger, whatever the number of keys."""
+    rng = np.random.default_rng(n)
+    c = setup(rng, fmt, [n], 1, 64, D, 16)
+    c["v"] = (rng.integers(0x68, 0x7f, c["v"].shape)).astype(np.uint8)  # i8: 104 to 126, e4m3: 64 to 416
+    c["v"][..., 5] |= 0x80 if fmt == "e4m3" else 0
+    c["v_scale"][:] = 2.0 ** {"i8": 121, "e4m3": 119}[fmt]
+    check(G, c, queries(rng, 1, group, D, size=0.1), [0], [n - 1])
+    c["v_scale"][:] = 2.0 ** -90  # (bounds reach down to 1e-30)
+    check(G, c, queries(rng, 1, group, D, size=0.1), [0], [n - 1])
