@@ -17,13 +17,18 @@ struct RopeHeader {
   uint32_t unused[2];
 };
 
-// Cosine and sine of position `pos` for a pair that makes turns * 2^-64 turns a position.  The
-// product modulo one turn is exact in 64-bit integers: far positions lose nothing.
+// Cosine and sine of position `pos` for a pair that makes turns * 2^-64 turns a position.  The product modulo one
+// turn is exact in 64-bit integers, and so is the nearest quarter turn that is taken off it; what is left, an eighth of
+// a turn at most, is rounded to 32 bits: by 2^-28 turns, or 2^-24 of itself.  (The whole angle rounded to 32 bits was
+// off by 2^-26 turns.)
 __device__ __forceinline__ float2 rope_cs(uint64_t turns, int pos, float magnitude) {
   const uint64_t a = turns * static_cast<uint64_t>(static_cast<int64_t>(pos));
+  const uint32_t quarter = static_cast<uint32_t>((a + (1ull << 61)) >> 62) & 3u;
+  const int64_t left = static_cast<int64_t>(a - (static_cast<uint64_t>(quarter) << 62));
   float s, c;
-  sincospif(static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077393e-10f, &s, &c);  // half turns
-  return make_float2(c * magnitude, s * magnitude);
+  sincospif(static_cast<float>(left) * 0x1p-63f, &s, &c);  // half turns
+  const float x = quarter & 1u ? s : c, y = quarter & 1u ? c : s;
+  return make_float2((quarter == 1u || quarter == 2u ? -x : x) * magnitude, (quarter & 2u ? -y : y) * magnitude);
 }
 
 __device__ __forceinline__ const uint64_t* rope_turns(const void* table) {

@@ -423,9 +423,10 @@ GF_API int64_t gf_lora_workspace(int64_t ncols, int64_t M, int64_t K, int64_t ra
  *           `slow` and fewer to 0 at `fast` and more.
  *  divisors[i] (device float32 [n_rot/2] or NULL) divides f_i last.
  *  m = magnitude, or where that is 0: 0.1 ln(factor) + 1 for RAMP with factor > 1, else 1.
- * Frequencies are computed in 64 bits and held as 64-bit fractions of a turn, the product with a 32-bit
- * position is exact: an angle is off by 2^-33 turns and by the frequency's own error, some 2^-49 of the
- * angle.  A negative position turns back. */
+ * Frequencies are computed in 64 bits and held as 64-bit fractions of a turn; the product with a 32-bit
+ * position is exact, and so is the quarter turn that is taken off it before the rest is rounded to 32 bits.  An
+ * angle is off by 2^-28 turns (2^-24 of its distance from that quarter turn), and by the frequency's own error, some
+ * 2^-49 of the whole angle: 2^-18 radians at position 2^31.  A negative position turns back. */
 typedef enum { GF_ROPE_HALVES = 0, GF_ROPE_PAIRS = 1 } gf_rope_layout;
 typedef enum { GF_ROPE_PLAIN = 0, GF_ROPE_LINEAR = 1, GF_ROPE_RAMP = 2, GF_ROPE_BANDS = 3 } gf_rope_kind;
 typedef struct {
