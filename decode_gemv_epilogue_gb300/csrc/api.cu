@@ -21,7 +21,7 @@
 
 namespace gf {
 
-// Per device: [0] the error bits of bounded waits that gave up, [1] the row chunks whose
+// Per device: [0] the error bits of bounded waits that gave up and of rotation tables that do not fit, [1] the row chunks whose
 // sums the integer path handed to the fp32 repair (see the streamed kernel).
 __device__ unsigned int g_error_word[2];
 
@@ -831,7 +831,7 @@ int gf_device_status(int reset) {
     e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  return (v & ERRBIT_TIMEOUT) ? GF_ERR_TIMEOUT : GF_OK;
+  return (v & ERRBIT_TIMEOUT) ? GF_ERR_TIMEOUT : (v & ERRBIT_TABLE) ? GF_ERR_INVALID : GF_OK;
 }
 
 int64_t gf_repair_count(int reset) {

@@ -98,6 +98,8 @@ static int plan_rope(const void* x, int64_t T, int64_t heads, int64_t dim, const
   const int64_t xb = rows_bytes(T, ld, width, o->type), db = rows_bytes(T, ld_dst, width, o->type);
   if (ranges_overlap(dst, db, x, xb) && !(dst == x && ld == ld_dst)) return GF_ERR_ALIAS;
   if (ranges_overlap(dst, db, pos, T * 4) || ranges_overlap(dst, db, o->table, rope_table_bytes(rot))) return GF_ERR_ALIAS;
+  unsigned* err = device_error_word();
+  if (!err) return cuda_fail(cudaGetLastError());
   r->kind = REC_ROPE;
   r->pdl = (o->flags & GF_FLAG_PDL) != 0;
   RopeArgs& a = r->rope;
@@ -106,6 +108,7 @@ static int plan_rope(const void* x, int64_t T, int64_t heads, int64_t dim, const
   a.dst = dst;
   a.pos = pos;
   a.table = o->table;
+  a.err = err;
   a.T = T;
   a.ld = ld;
   a.ld_dst = ld_dst;
@@ -225,6 +228,8 @@ static int plan_store(const gf_cache* c, const void* k, const void* v, int64_t T
       if (off < qwidth * eb || off + width * eb > step) return GF_ERR_ALIAS;
     }
   }
+  unsigned* err = device_error_word();
+  if (!err) return cuda_fail(cudaGetLastError());
   r->kind = REC_STORE;
   r->pdl = (o->flags & GF_FLAG_PDL) != 0;
   StoreArgs& a = r->store;
@@ -235,6 +240,7 @@ static int plan_store(const gf_cache* c, const void* k, const void* v, int64_t T
   a.seq = seq;
   a.pos = pos;
   a.table = o->rope ? o->rope->table : nullptr;
+  a.err = err;
   a.q = with_q && o->q_heads > 0 ? o->q : nullptr;
   a.q_dst = o->q_dst;
   a.T = T;

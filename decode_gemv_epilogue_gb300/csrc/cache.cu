@@ -202,16 +202,19 @@ __global__ void __launch_bounds__(32 * kStoreWarps, 3) store_kernel(const __grid
   unit_offsets(u, a.table ? a.n_rot : 0, halves, o0, o1);
   const int slices = gridDim.y - a.q_slices;
   if (static_cast<int>(blockIdx.y) >= slices) {
+    if (!rope_fits(a.table, a.n_rot, a.err)) return;
     store_queries<E, VEC>(a, (blockIdx.y - slices) * kStoreWarps + warp, lg, u, on, o0, o1);
     return;
   }
   if constexpr (SMALL) {
+    if (a.table && !rope_fits(a.table, a.n_rot, a.err)) return;
     store_small<FMT, E, VEC>(a, blockIdx.y * kStoreWarps + warp, slices * kStoreWarps, lg, u, on, o0, o1);
     return;
   }
   const int wpu = 1 << a.wpu_log2, upg = kStoreWarps >> a.wpu_log2, unit_groups = a.unit_groups;
   uint32_t firsts;  // of the window's tokens, those that begin a block's new ones
   {
+    const uint32_t table_pairs = a.table ? static_cast<const RopeHeader*>(a.table)->pairs : 0;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * a.window + lane;
     bool first = false;
     if (lane < a.window && t < a.T) {
@@ -219,6 +222,7 @@ __global__ void __launch_bounds__(32 * kStoreWarps, 3) store_kernel(const __grid
       first = !(t > 0 && (pos & (block - 1)) > 0 && seq_of(a.seq, t - 1) == seq && a.pos[t - 1] == pos - 1);
     }
     firsts = __ballot_sync(0xffffffffu, first);
+    if (a.table && !rope_fits(table_pairs, a.n_rot, a.err)) return;  // (positions do not wait for it)
   }
   for (; firsts; firsts &= firsts - 1) {
     const int64_t t = static_cast<int64_t>(blockIdx.x) * a.window + __ffs(firsts) - 1;

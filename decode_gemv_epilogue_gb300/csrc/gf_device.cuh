@@ -17,7 +17,7 @@ enum { EPI_ADD_SIGMOID = 6, EPI_ADD_SILU = 7 };
 __host__ __device__ constexpr bool epi_takes_aux(int e) {
   return e == EPI_SILU_MUL || e == EPI_ADD || e == EPI_ADD_SIGMOID || e == EPI_ADD_SILU;
 }
-enum { ERRBIT_TIMEOUT = 1u };
+enum { ERRBIT_TIMEOUT = 1u, ERRBIT_TABLE = 2u };
 
 // A bounded wait gives up after this many nanoseconds of %globaltimer.
 constexpr uint64_t kWaitLimitNs = 1000000000ull;

@@ -332,6 +332,7 @@ struct RopeArgs {
   void* dst;
   const int32_t* pos;
   const void* table;
+  unsigned* err;        // device error word
   int64_t T, ld, ld_dst;
   int heads, dim, n_rot, halves;
   int type;             // GF_F32 or GF_F16
@@ -360,6 +361,7 @@ struct StoreArgs {
   const int32_t* seq;   // nullptr: token t is of sequence t
   const int32_t* pos;
   const void* table;    // rotation (nullptr: none)
+  unsigned* err;        // device error word
   const void* q;
   void* q_dst;
   int64_t T, ldk, ldv, ldq, ld_q_dst;

@@ -50,8 +50,9 @@ int launch_rope_table(const RopeTableArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// VEC: a thread holds unit u (four pairs) of a token and goes through heads, blockDim / units at a time.
-template <typename E, bool HALVES>
+// VEC: a thread holds unit u (four pairs) of a token and goes through heads, blockDim / units at a time.  ONCE: it has
+// one at most, whose row is on its way before the table's header is looked at.
+template <typename E, bool HALVES, bool ONCE>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -59,20 +60,29 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
   const int64_t t = blockIdx.x;
   const E* x = static_cast<const E*>(a.x) + t * a.ld;
   E* y = static_cast<E*>(a.dst) + t * a.ld_dst;
+  const uint32_t table_pairs = static_cast<const RopeHeader*>(a.table)->pairs;
+  const int pos = a.pos[t], first = threadIdx.x / units + hp * blockIdx.y;
+  int o0, o1;
+  unit_offsets(u, a.n_rot, HALVES, o0, o1);
+  float4 l = {}, r = {};
+  if (ONCE && first < a.heads) {
+    const E* p = x + static_cast<int64_t>(first) * a.dim;
+    l = load4(p + o0), r = load4(p + o1);
+  }
+  if (!rope_fits(table_pairs, a.n_rot, a.err)) return;
   float2 cs[4];
   const bool turns = 8 * u < a.n_rot;
   if (turns) {
-    const int pos = a.pos[t];
     const float mag = static_cast<const RopeHeader*>(a.table)->magnitude;
     const uint64_t* f = rope_turns(a.table) + 4 * u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) cs[i] = rope_cs(f[i], pos, mag);
   }
-  int o0, o1;
-  unit_offsets(u, a.n_rot, HALVES, o0, o1);
-  for (int h = threadIdx.x / units + hp * blockIdx.y; h < a.heads; h += hp * gridDim.y) {
-    const E* p = x + static_cast<int64_t>(h) * a.dim;
-    const float4 l = load4(p + o0), r = load4(p + o1);
+  for (int h = first; h < a.heads; h += hp * gridDim.y) {
+    if (!ONCE) {
+      const E* p = x + static_cast<int64_t>(h) * a.dim;
+      l = load4(p + o0), r = load4(p + o1);
+    }
     float v[8] = {l.x, l.y, l.z, l.w, r.x, r.y, r.z, r.w};
     if (turns) {
 #pragma unroll
@@ -81,6 +91,7 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
     E* q = y + static_cast<int64_t>(h) * a.dim;
     store4(q + o0, v[0], v[1], v[2], v[3]);
     store4(q + o1, v[4], v[5], v[6], v[7]);
+    if (ONCE) break;
   }
 }
 
@@ -89,6 +100,7 @@ template <typename E>
 __global__ void __launch_bounds__(256) rope_generic_kernel(const __grid_constant__ RopeArgs a) {
   pdl_wait();
   pdl_trigger();
+  if (!rope_fits(a.table, a.n_rot, a.err)) return;
   const int pairs = a.n_rot / 2, units = pairs + a.dim - a.n_rot;
   const int64_t t = blockIdx.x;
   const E* x = static_cast<const E*>(a.x) + t * a.ld;
@@ -111,6 +123,11 @@ __global__ void __launch_bounds__(256) rope_generic_kernel(const __grid_constant
   }
 }
 
+template <typename E, bool ONCE>
+static int launch_rope_t(const cudaLaunchConfig_t& cfg, const RopeArgs& a) {
+  return a.halves ? cudaLaunchKernelEx(&cfg, rope_kernel<E, true, ONCE>, a) : cudaLaunchKernelEx(&cfg, rope_kernel<E, false, ONCE>, a);
+}
+
 int launch_rope(const RopeArgs& a, cudaStream_t st, bool pdl) {
   cudaLaunchConfig_t cfg = {};
   cfg.stream = st;
@@ -126,11 +143,9 @@ int launch_rope(const RopeArgs& a, cudaStream_t st, bool pdl) {
     const int passes = (a.heads + most - 1) / most, hp = (a.heads + passes - 1) / passes;
     cfg.blockDim = dim3(static_cast<unsigned>(units * hp));
     cfg.gridDim = dim3(static_cast<unsigned>(a.T), static_cast<unsigned>(a.T <= 256 ? passes : 1));
-    if (f32)
-      return a.halves ? cudaLaunchKernelEx(&cfg, rope_kernel<float, true>, a)
-                      : cudaLaunchKernelEx(&cfg, rope_kernel<float, false>, a);
-    return a.halves ? cudaLaunchKernelEx(&cfg, rope_kernel<__half, true>, a)
-                    : cudaLaunchKernelEx(&cfg, rope_kernel<__half, false>, a);
+    const bool once = static_cast<int>(cfg.gridDim.y) == passes;
+    if (f32) return once ? launch_rope_t<float, true>(cfg, a) : launch_rope_t<float, false>(cfg, a);
+    return once ? launch_rope_t<__half, true>(cfg, a) : launch_rope_t<__half, false>(cfg, a);
   }
   cfg.blockDim = dim3(128);
   cfg.gridDim = dim3(static_cast<unsigned>(a.T), static_cast<unsigned>(a.heads < 64 ? a.heads : 64));

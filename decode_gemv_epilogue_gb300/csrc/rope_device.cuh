@@ -6,6 +6,7 @@
 
 #include <cuda_fp16.h>
 
+#include "gf_device.cuh"
 #include "gf_internal.h"
 
 namespace gf {
@@ -29,6 +30,17 @@ __device__ __forceinline__ float2 rope_cs(uint64_t turns, int pos, float magnitu
   sincospif(static_cast<float>(left) * 0x1p-63f, &s, &c);  // half turns
   const float x = quarter & 1u ? s : c, y = quarter & 1u ? c : s;
   return make_float2((quarter == 1u || quarter == 2u ? -x : x) * magnitude, (quarter & 2u ? -y : y) * magnitude);
+}
+
+// Whether the table is one for n_rot elements.  Where it is not, what lies behind its header is not read and the
+// device error word says so.
+__device__ __forceinline__ bool rope_fits(uint32_t pairs, int n_rot, unsigned* err) {
+  if (pairs == static_cast<uint32_t>(n_rot) / 2) return true;
+  if (threadIdx.x == 0) set_error(err, ERRBIT_TABLE);
+  return false;
+}
+__device__ __forceinline__ bool rope_fits(const void* table, int n_rot, unsigned* err) {
+  return rope_fits(static_cast<const RopeHeader*>(table)->pairs, n_rot, err);
 }
 
 __device__ __forceinline__ const uint64_t* rope_turns(const void* table) {

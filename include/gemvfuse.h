@@ -442,7 +442,7 @@ typedef struct {
 GF_API int64_t gf_rope_table_bytes(int64_t n_rot);
 GF_API int gf_rope_table(void* table, int64_t n_rot, const gf_rope_freqs* freqs, void* stream);
 typedef struct {
-  const void* table;   /* made for n_rot                                             */
+  const void* table;   /* made for n_rot, else nothing is written (gf_device_status) */
   int64_t n_rot;       /* elements of a head that turn; 0: all                       */
   int layout;          /* gf_rope_layout                                             */
   int type;            /* of x and dst (gf_rope only)                                */
@@ -593,9 +593,10 @@ GF_API int gf_plan_glu(const void* W_gate, const void* W_up, int wtype, const fl
  * abort flag), microseconds spent in the first wait, microseconds in the second}. */
 GF_API int gf_selftest_wait_timeout(int64_t limit_us, int* out, void* stream);
 
-/* Device error word of the current device: GF_OK, or GF_ERR_TIMEOUT if a kernel gave up
- * on a bounded wait since the last reset.  Synchronises with the device.  reset != 0
- * clears it. */
+/* Device error word of the current device: GF_OK, GF_ERR_TIMEOUT if a kernel gave up
+ * on a bounded wait since the last reset, or GF_ERR_INVALID if gf_rope or gf_cache_store
+ * met a rotation table of another n_rot than its own (it then wrote nothing).
+ * Synchronises with the device.  reset != 0 clears it. */
 GF_API int gf_device_status(int reset);
 
 /* Row chunks (a CTA's rows of one launch, or of one row chunk of it) whose sums the
