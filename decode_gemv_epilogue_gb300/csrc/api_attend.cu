@@ -36,10 +36,12 @@ static int check_rows(const void* p, int64_t* ld, int64_t width, int type, int* 
 
 static bool type_ok(int type) { return type == GF_F32 || type == GF_F16; }
 
+// Of a power of two, else -1 (for any v).
 static int log2_of(int64_t v) {
+  if (v < 1 || (v & (v - 1)) != 0) return -1;
   int l = 0;
-  while ((1LL << l) < v) ++l;
-  return (1LL << l) == v ? l : -1;
+  while (v >>= 1) ++l;
+  return l;
 }
 
 // ------------------------------------------------------------------ rotary positions
