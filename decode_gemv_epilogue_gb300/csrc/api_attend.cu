@@ -271,7 +271,8 @@ static int plan_store(const gf_cache* c, const void* k, const void* v, int64_t T
     // Each token may begin a block (decode steps); of a prompt's every block-th does, and CTAs that find none
     // only cost their start: as many tokens a CTA as leave sixteen CTAs to an SM.
     a.window = 1;
-    while (a.window < 32 && a.window < c->block && T * a.unit_groups > 2432LL * a.window) a.window *= 2;
+    const int64_t ctas = 16LL * device_limits().sm_count;
+    while (a.window < 32 && a.window < c->block && T * a.unit_groups > ctas * a.window) a.window *= 2;
   }
   a.q_rows = T > 256 ? kStoreKept : 1;
   const int chunks = a.q ? (a.q_heads + a.q_rows * a.tpw - 1) / (a.q_rows * a.tpw) : 0;
