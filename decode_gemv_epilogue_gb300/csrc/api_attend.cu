@@ -256,11 +256,18 @@ static int plan_store(const gf_cache* c, const void* k, const void* v, int64_t T
   a.type = o->type;
   a.vec = vec;
   // Decode steps bring one token a block, a warp's work.  Prompts bring whole blocks: as many warps as hold
-  // their values in registers between finding the scale and writing the codes.
+  // their values in registers between finding the scale and writing the codes.  Which of them a call is stands in its
+  // lists on the device; without a list of sequences every token is one's own, else more than 256 tokens are taken for
+  // prompts.  300 tokens of 8 heads of 128, f16, in the decode steps' plan and in the prompts', cold: one token a
+  // sequence 13 and 18 us with blocks of 16, 13 and 38 with 64; one prompt 18 and 16, 42 and 17.  (64 tokens of one
+  // prompt 16 and 12, 34 and 14: short prompts pay.)
   a.tpw = static_cast<int>(32 / (c->dim / 8));
   a.lane_inv = static_cast<int>(65536 / (c->dim / 8) + 1);
-  while (T > 256 && (kStoreWarps >> a.wpu_log2) > 1 && (a.tpw * kStoreKept << a.wpu_log2) < c->block) ++a.wpu_log2;
-  a.small = T > 256 && c->block <= a.tpw;
+  const bool prompt = T > 256 && (seq || c->block <= a.tpw);
+  while (prompt && (kStoreWarps >> a.wpu_log2) > 1 && (a.tpw * kStoreKept << a.wpu_log2) < c->block) ++a.wpu_log2;
+  // (one token of each of 64 sequences with a scale each 9 us as units of a head and 13 as tasks, of 300 13 and 14, of
+  // 512 16 and 14, of 1000 22 and 16)
+  a.small = prompt && c->block <= a.tpw;
   if (a.small) {  // tasks of warps, two to a warp
     const int64_t tasks = 2 * ((c->heads + kStoreKept - 1) / kStoreKept);
     a.window = 8;
@@ -274,9 +281,11 @@ static int plan_store(const gf_cache* c, const void* k, const void* v, int64_t T
     const int64_t ctas = 16LL * device_limits().sm_count;
     while (a.window < 32 && a.window < c->block && T * a.unit_groups > ctas * a.window) a.window *= 2;
   }
-  a.q_rows = T > 256 ? kStoreKept : 1;
+  // (with 32 query heads to turn, blocks of 16: one token of each of 300 sequences 16 us by one row a lane and the decode
+  // steps' plan, 22 by four and the prompts'; 300 tokens of a prompt 20 and 16)
+  a.q_rows = prompt ? kStoreKept : 1;
   const int chunks = a.q ? (a.q_heads + a.q_rows * a.tpw - 1) / (a.q_rows * a.tpw) : 0;
-  const int per_cta = kStoreWarps * (T > 256 ? 2 : 1);
+  const int per_cta = kStoreWarps * (prompt ? 2 : 1);
   a.q_slices = (a.window * chunks + per_cta - 1) / per_cta;
   *n = 1;
   return GF_OK;

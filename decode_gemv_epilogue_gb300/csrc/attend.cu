@@ -1008,8 +1008,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __gr
 }
 
 // Few items, many parts: CTA (i, slice) looks at kFewRecords; its warps share the parts.  (A CTA to every record and
-// slice took 2 us to find that most have nothing to do.)
-constexpr int kFewWarps = 8, kFewRecords = 8, kFewItems = 64;
+// slice took 2 us to find that most have nothing to do.)  Whole calls with this kernel and with the one above: 8 items of
+// 16000 keys 30 and 42 us, of 1000 20 and 21; 24 44 and 48, 24 and 24; 40 59 and 59, 26 and 25; 64 77 and 77, 28 and 26.
+constexpr int kFewWarps = 8, kFewRecords = 8, kFewItems = 40;
 template <int DC, int NM>
 __global__ void __launch_bounds__(32 * kFewWarps) attend_join_few_kernel(const __grid_constant__ AttendArgs a) {
   __shared__ float4 sums[kFewWarps][32];

@@ -442,7 +442,8 @@ __global__ void __launch_bounds__(256) load_kernel(const __grid_constant__ LoadA
 template <int FMT, typename E>
 static int launch_load_t(const LoadArgs& a, cudaStream_t st, bool pdl) {
   cudaLaunchConfig_t cfg = {};
-  // few tokens: one a CTA, its heads spread over CTAs
+  // Few tokens: one a CTA, its heads spread over CTAs.  64 tokens of 32 heads of 128, f16, 9.3 us so and 11.4 with four
+  // tokens a CTA; of 8 heads 9.3 either way up to 1000; 2000 of them, f32, 13.4 and 11.4, 4000 20 and 16.
   const bool few = a.T < 1024;
   const int64_t units = static_cast<int64_t>(a.c.heads) * a.c.dim * sizeof(E) / 16;
   cfg.blockDim = dim3(static_cast<unsigned>(units < 256 ? (units + 31) / 32 * 32 : 256));

@@ -139,7 +139,8 @@ int launch_rope(const RopeArgs& a, cudaStream_t st, bool pdl) {
   const bool f32 = a.type == 0;
   if (a.vec) {
     const int units = a.dim / 8, most = 256 / units;
-    // whole passes over the heads, equally full; few tokens spread their heads over CTAs
+    // Whole passes over the heads, equally full; few tokens spread their heads over CTAs: 40 heads of 128, f32, for 32
+    // tokens 7.3 us where a CTA a token takes 9.3, for 200 9.3 and 10.3, for 256 10.4 either way, for 1000 17.5 and 14.4.
     const int passes = (a.heads + most - 1) / most, hp = (a.heads + passes - 1) / passes;
     cfg.blockDim = dim3(static_cast<unsigned>(units * hp));
     cfg.gridDim = dim3(static_cast<unsigned>(a.T), static_cast<unsigned>(a.T <= 256 ? passes : 1));

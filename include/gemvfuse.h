@@ -492,6 +492,8 @@ typedef struct {
  * back as NaN until its first position is written again.
  * Tokens of one sequence stand next to each other in the call, each at the position behind the one before it
  * (else the blocks concerned hold some of the values, and nothing else is touched).
+ * More than 256 tokens with a list of sequences are taken for prompts, without one for a token of each: only speed
+ * depends on it.
  * n_rot must be a multiple of 8 here (GF_ERR_UNSUPPORTED); T <= 2^20, q_heads <= 1024.  No argument may
  * overlap the cache's arrays, and q_dst no input but q (rows of one fused q, k, v buffer may lie between
  * each other). */
