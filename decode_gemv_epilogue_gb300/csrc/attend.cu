@@ -3,8 +3,8 @@
 // One pass over a row's keys and values with the running maximum and sum of the softmax.  What bounds it
 // is reading the codes: each warp copies (cp.async) chunks of CT tokens, whole lines of consecutive addresses, into
 // stages of its own, a chunk ahead.  (Copies of just the bytes that a lane decodes itself, in fours of rows, left
-// the memory at 5.0 TB/s where consecutive ones reach 6.4.)  With the arithmetic, 927 instructions a chunk at three
-// warps a scheduler, 256 sequences of 4000 to 8000 keys and 32 query heads over 8 of 128 take 555 us, 5.5 TB/s.
+// the memory at 5.0 TB/s where consecutive ones reach 6.4.)  With the arithmetic, 936 instructions a chunk at three
+// warps a scheduler, 256 sequences of 4000 to 8000 keys and 32 query heads over 8 of 128 take 552 us, 5.5 TB/s.
 //
 // A warp takes a chunk of CT tokens.  m16n8k16 with the queries as the 16 rows: eight rows' f16 high parts and
 // the same rows' low parts (q = hi + lo to 22 bits under a power of two a row), so that one instruction
@@ -14,8 +14,8 @@
 //           two k pairs of one instruction;
 //   values: lane (g, c) takes a unit of the four tokens that its k indices mean; the bytes of four
 //           tokens' words are paired by dim, and dim j of column g's unit is column g of instruction j.
-// The weights p * scale_v are split into hi + lo like the queries, under a power of two a row.  A chunk's products are added to the
-// running ones in 32 bits, outside the matrix unit (which truncates).
+// The weights p * scale_v are split into hi + lo like the queries, under a power of two a row.  A chunk's products are
+// added to the running ones in 32 bits, outside the matrix unit (which truncates).
 //
 // Items, (tokens of a sequence next to each other, head of the cache, part of its queries), are laid end
 // to end by their number of chunks and some more for their start and end; every CTA takes an equal stretch
@@ -33,7 +33,7 @@
 namespace gf {
 
 // Warps of a CTA, two of which share an SM: as many as the registers allow (NM: tiles of eight rows).  Six for two
-// tiles of 64 dims take 77 us where four take 86 (33 sequences, two tokens of 64 query heads each).
+// tiles of 64 dims take 79 us where four take 86 (33 sequences, two tokens of 64 query heads each).
 __host__ __device__ constexpr int att_warps(int dc, int nm) { return dc == 64 || (dc == 128 && nm == 1) ? 6 : 4; }
 
 template <int DC, int NM>
@@ -53,8 +53,8 @@ struct AttShape {
 template <int DC>
 constexpr int kUnitBytes = DC == 64 ? 8 : 16;  // of a value row, in a lane's hands
 
-// An item's start and end in units of a chunk's time.  At one unit 61 sequences of 100 to 8000 keys took 66 us where
-// 61, 244 of them 219 where 209; at six 63 and 215.  They come first, and a share that ends within them leaves the
+// An item's start and end in units of a chunk's time.  At one unit 61 sequences of 100 to 8000 keys take 66 us where
+// 63, 244 of them 226 where 212; at six 64 and 220.  They come first, and a share that ends within them leaves the
 // item to the next: only a share's chunks make a part.
 constexpr int kItemUnits = 3;
 // Running maximum of a row without keys: no finite score lies below it, and a masked one, -inf, has no weight under it.
@@ -360,6 +360,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
   __shared__ uint32_t group_units[kAttMaxTokens / 32];  // of 32 tokens each, for one (head, part)
   __shared__ AttSpan spans[W][2];                       // the items of the warps' parts: first, last
   __shared__ float2 part_rows[W][2][S::kRows];          // maxima and sums of weights of their rows
+  __shared__ float rooms[W][NM][32];                    // a lane's rows: see `unit`
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c4 = lane & 3;
@@ -477,8 +478,8 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
       uint32_t hidden = 0;
       key_scale = value_scale = 0.0f;
       // Whole chunks, by halves (a page may hold 16 tokens): one address for each, its copies at fixed steps.  With
-      // an address for each copy instead, 64 sequences of 6000 keys in pages of 16 took 195 us where 167, heads of
-      // 96 took 192 where 171.
+      // an address for each copy instead, 64 sequences of 6000 keys in pages of 16 took 195 us where 168, heads of
+      // 96 took 192 where 175.
       if (all && p0 >= s.lo && p0 + CT <= s.hi) {
 #pragma unroll
         for (int h = 0; h < KG; ++h) {
@@ -604,14 +605,13 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 #pragma unroll
         for (int n = 0; n < NO; ++n) o[i][n] = make_float2(0.0f, 0.0f);
       }
-      // Biased exponent of each row's unit, at least that of the format's smallest scale, and by how many powers of
-      // two the sums' own (the largest weight times scale that went in, at the present maximum) may lie above it.
+      // Biased exponent of each row's unit, at least that of the format's smallest scale.  The sums' own (the largest
+      // weight times scale that went in, at the present maximum) may lie above it, by `rooms` powers of two at most.
       int unit[NM];
-      float room[NM];
 #pragma unroll
       for (int i = 0; i < NM; ++i) {
         unit[i] = 127 - 111;
-        room[i] = 0.0f;
+        rooms[warp][i][lane] = 0.0f;
       }
       const int t0 = token_of<DC>(2 * c4), t1 = token_of<DC>(2 * c4 + 1);  // this lane's columns
 
@@ -707,29 +707,31 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
           alpha[i] = keep;
           m[i] = top;
           if (__builtin_expect(other, 0)) {
-            // A unit for this chunk: above its scales, or where those lie far apart, above the largest weight times
-            // scale among the keys that the row sees.  A block of large values that the softmax gives no weight, or that
-            // only other rows see, so takes no bits from the others (with a unit above every scale so far, 2^20 between
-            // scales left errors of 1e-3 of the row, 2^34 zeros; it took 545 us where 555 in the case above).
-            int now = vtop;
-            if (vlow < vtop - kScaleSpread) {
-              float most = 0.0f;
+            // A unit for this chunk.  Above its scales, unless those lie far apart, or far above the unit without the
+            // weights to match: then above the largest weight times scale among the keys that the row sees, and the unit
+            // stays if that is what it serves.  A block of large values that the softmax gives no weight, or that only other
+            // rows see, so takes no bits from the others (with a unit above every scale so far, 2^20 between scales left
+            // errors of 1e-3 of the row, 2^34 zeros; it took 545 us where 552 in the case above).
+            float most = 0.0f;
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                const float2 v2 = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c4);
-                const float a = fabsf(exp2_fast(x[i][n].x - top) * v2.x), b = fabsf(exp2_fast(x[i][n].y - top) * v2.y);
-                most = fmaxf(most, fmaxf(a < INFINITY ? a : 0.0f, b < INFINITY ? b : 0.0f));
-              }
-              now = static_cast<int>(__float_as_uint(quad_max(most)) >> 23) + 1;
+            for (int n = 0; n < NT; ++n) {
+              const float2 v2 = *reinterpret_cast<const float2*>(vs + 8 * n + 2 * c4);
+              const float a = fabsf(exp2_fast(x[i][n].x - top) * v2.x), b = fabsf(exp2_fast(x[i][n].y - top) * v2.y);
+              most = fmaxf(most, fmaxf(a < INFINITY ? a : 0.0f, b < INFINITY ? b : 0.0f));
             }
-            const float held = fmaxf(static_cast<float>(unit[i]) + room[i] + down, 0.0f);  // the sums' own, as an exponent
+            const int fit = static_cast<int>(__float_as_uint(quad_max(most)) >> 23) + 1;  // (1: no weight at all)
+            const bool alike = vlow >= vtop - kScaleSpread;
+            int now = unit[i];
+            if (hi[i] == 0 || (alike && (vtop <= unit[i] + kScaleSpread || fit > vtop - kScaleSpread)))
+              now = vtop;
+            else if (fit > unit[i] || (!alike && fit > 1 && fit < unit[i] - kScaleSpread))
+              now = fit;
+            const float held = fmaxf(static_cast<float>(unit[i]) + rooms[warp][i][lane] + down, 0.0f);  // the sums' own
             now = max(max(now, 127 - 111), static_cast<int>(ceilf(held - kUnitFall)));
             const int step = unit[i] - now, half = step / 2;
             alpha[i] = keep * __uint_as_float((127 + half) << 23) * __uint_as_float((127 + step - half) << 23);
             unit[i] = now;
-            room[i] = fmaxf(held - static_cast<float>(now), 0.0f);
-          } else {
-            room[i] = fmaxf(room[i] + down, 0.0f);
+            rooms[warp][i][lane] = fmaxf(held - static_cast<float>(now), 0.0f);
           }
           // 2^kWeightBits a unit
           const float vinv = __uint_as_float((254 + kWeightBits - unit[i]) << 23);

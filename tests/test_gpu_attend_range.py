@@ -46,19 +46,50 @@ def repel(c, s, blocks, q, weight=100.0):
         c["k"][p, :, b * c["block"]:(b + 1) * c["block"], 0] = LOWEST[c["fmt"]]
 
 
-def bounds_beside(c, q, seq, pos, window, blocks):
+def one_sequence(c, q, seq, pos, window=0):
+    """The oracle's attend for rows that are all of sequence 0, or of none (pos < 0), at once."""
+    T, Hq, D = q.shape
+    n, H = int(max(pos)) + 1, c["k"].shape[1]
+    k, v = (x.transpose(1, 0, 2) for x in oatt.load(c, np.zeros(n, dtype=int), np.arange(n)))  # [H, n, D]
+    x = q.astype(np.float64).reshape(T, H, Hq // H, D).transpose(1, 0, 2, 3).reshape(H, -1, D) * D ** -0.5
+    p = np.repeat(np.asarray(pos), Hq // H)[:, None]
+    sees = (np.arange(n) <= p) & ((np.arange(n) > p - window) if window else True)
+    a = np.where(sees, x @ k.transpose(0, 2, 1), -np.inf)
+    m = a.max(-1, keepdims=True)
+    e = np.exp(a - np.where(np.isfinite(m), m, 0.0))
+    z = e.sum(-1, keepdims=True)
+    w = e / np.where(z > 0, z, 1.0)
+    spread = np.where(sees, np.abs(x) @ np.abs(k).transpose(0, 2, 1), 0.0).max(-1)
+    with np.errstate(divide="ignore"):
+        lse = np.where(z > 0, m + np.log(z), -np.inf)[..., 0]
+
+    def rows(y):
+        return y.reshape((H, T, Hq // H) + y.shape[2:]).swapaxes(0, 1).reshape((T, Hq) + y.shape[2:])
+    return rows(w @ v), rows(lse), rows(w @ np.abs(v)), rows(spread)
+
+
+def test_one_sequence_is_the_oracle():
+    rng = np.random.default_rng(0)
+    c = setup(rng, "i8", [50], 2, 16, 16, 4)
+    q, pos = queries(rng, 6, 6, 16), [3, -1, 49, 20, 0, 30]
+    for window in (0, 7):
+        for a, b in zip(one_sequence(c, q, [0] * 6, pos, window), oatt.attend(c, q, np.zeros(6, dtype=int), pos, window=window)):
+            assert np.allclose(a, b, rtol=1e-12, atol=1e-14)
+
+
+def bounds_beside(c, q, seq, pos, window, blocks, attend=oatt.attend):
     """attend_bounds with the scores of the keys that have weight, and all of what the blocks contribute: their keys'
     scores are large, and so are their errors, but they have no weight to be wrong."""
-    want, lse, mass, spread = oatt.attend(c, q, seq, pos, window=window)
+    want, lse, mass, spread = attend(c, q, seq, pos, window=window)
     rest = {k: v.copy() if isinstance(v, np.ndarray) else v for k, v in c.items()}
     for p, b in blocks:
         rest["v"][p, :, b * c["block"]:(b + 1) * c["block"]] = 0
         rest["k"][p, :, b * c["block"]:(b + 1) * c["block"]] = 0
     without = {k: v.copy() if isinstance(v, np.ndarray) else v for k, v in rest.items()}
     without["k"] = c["k"]
-    _, _, mass_rest, _ = oatt.attend(without, q, seq, pos, window=window)
-    spread = oatt.attend(rest, q, seq, pos, window=window)[3]
-    keys = np.array([[len(oatt.seen(c, int(s), int(p), window))] * q.shape[1] for s, p in zip(seq, pos)], dtype=np.float64)
+    _, _, mass_rest, _ = attend(without, q, seq, pos, window=window)
+    spread = attend(rest, q, seq, pos, window=window)[3]
+    keys = np.repeat(np.clip(np.asarray(pos, dtype=np.float64) + 1, 0, window or None)[:, None], q.shape[1], 1)
     b, bl = au.attend_bounds(c, want, lse, mass_rest, spread, keys, False)
     return want, lse, b + (mass - mass_rest), bl
 
@@ -195,3 +226,58 @@ def test_largest_values(G, D, group, n, fmt):
     check(G, c, queries(rng, 1, group, D, size=0.1), [0], [n - 1])
     c["v_scale"][:] = 2.0 ** -90  # (bounds reach down to 1e-30)
     check(G, c, queries(rng, 1, group, D, size=0.1), [0], [n - 1])
+
+
+@pytest.mark.parametrize("where", ["middle", "half", "stripes"])
+@pytest.mark.parametrize("ratio", [-40, 20, 90])
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("group, D, rows, run", [(4, 128, 80, 1), (16, 128, 70, 1), (8, 64, 80, 1), (3, 256, 70, 1), (4, 128, 160, 4)])
+def test_large_values_within_a_warp(G, group, D, rows, run, fmt, ratio, where):
+    """As test_large_values_without_weight, with so many rows over one sequence that each warp takes many chunks of it
+    in turn; blocks of two chunks."""
+    rng = np.random.default_rng(D + ratio + rows)
+    n, block, H = 1500, 64, 4
+    c = setup(rng, fmt, [n], H, 64, D, block)
+    q = queries(rng, rows, H * group, D)
+    last = (n - 1) // block
+    which = list(range(1, last, 3)) if where == "stripes" else where_of(where, n, block)
+    repel(c, 0, which, q)
+    at = blocks_at(c, 0, which)
+    for p, b in at:
+        c["v_scale"][p, :, b] *= np.float32(2.0 ** ratio)
+    pos = np.full(rows, n - 1, dtype=np.int32) - rng.integers(0, 3, rows).astype(np.int32)
+    pos[::7] = -1  # (and some rows see nothing)
+    seq = np.zeros(rows, dtype=np.int32)
+    want, lse, b, bl = bounds_beside(c, q, seq, pos, 0, at, one_sequence)
+    got, gl = call(G, au.DeviceCache(G, c), q, seq, pos, run=run)
+    assert_within(got, want, b, "out")
+    seen = pos >= 0
+    assert_within(gl[seen], lse[seen], bl[seen], "lse")
+    assert np.isneginf(gl[~seen]).all()
+    for t in np.flatnonzero(seen):
+        assert au.norm_error(got[t], want[t]) <= au.NORM_TOL, t
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scales_that_come_and_go_within_a_warp(G, D, fmt):
+    """As test_scales_that_come_and_go, and its scores falling too: the first blocks have all the weight."""
+    rng = np.random.default_rng(D + 1)
+    n, block, rows = 1280, 64, 90
+    c = setup(rng, fmt, [n], 4, 64, D, block)
+    q = queries(rng, rows, 16, D, size=0.02)
+    c["k"][..., 0] = 0
+    q[..., 0] = np.float32(2.0 * np.sqrt(D)) * rng.choice([-1.0, 1.0, 0.1, -0.1], (rows, 16)).astype(np.float32)
+    one = {"i8": lambda v: v & 0xff, "e4m3": lambda v: int(oatt.encode("e4m3", np.array([float(v)]))[0])}[fmt]
+    for i in range(n // block):
+        (p, b), = blocks_at(c, 0, [i])
+        c["k"][p, :, b * block:(b + 1) * block, 0] = one(i * 5)
+        c["k_scale"][p, :, b] = 0.5
+        c["v_scale"][p, :, b] = np.float32(2.0 ** [-60, 3, -20, 40, -7, -7, 70, -90][i % 8])
+    c["v"] = no_zeros(c["v"])
+    seq, pos = np.zeros(rows, dtype=np.int32), np.full(rows, n - 1, dtype=np.int32)
+    want, lse, mass, spread = one_sequence(c, q, seq, pos)
+    got, gl = call(G, au.DeviceCache(G, c), q, seq, pos)
+    b, bl = au.attend_bounds(c, want, lse, mass, spread, np.full(lse.shape, float(n)), False)
+    assert_within(got, want, b, "out")
+    assert_within(gl, lse, bl, "lse")
