@@ -4,7 +4,7 @@
 // is reading the codes: each warp copies (cp.async) chunks of CT tokens, whole lines of consecutive addresses, into
 // stages of its own, a chunk ahead.  (Copies of just the bytes that a lane decodes itself, in fours of rows, left
 // the memory at 5.0 TB/s where consecutive ones reach 6.4.)  With the arithmetic, 936 instructions a chunk at three
-// warps a scheduler, 256 sequences of 4000 to 8000 keys and 32 query heads over 8 of 128 take 552 us, 5.5 TB/s.
+// warps a scheduler, 256 sequences of 4000 to 8000 keys and 32 query heads over 8 of 128 take 556 us, 5.5 TB/s.
 //
 // A warp takes a chunk of CT tokens.  m16n8k16 with the queries as the 16 rows: eight rows' f16 high parts and
 // the same rows' low parts (q = hi + lo to 22 bits under a power of two a row), so that one instruction
@@ -33,7 +33,7 @@
 namespace gf {
 
 // Warps of a CTA, two of which share an SM: as many as the registers allow (NM: tiles of eight rows).  Six for two
-// tiles of 64 dims take 79 us where four take 86 (33 sequences, two tokens of 64 query heads each).
+// tiles of 64 dims take 77 us where four take 86 (33 sequences, two tokens of 64 query heads each).
 __host__ __device__ constexpr int att_warps(int dc, int nm) { return dc == 64 || (dc == 128 && nm == 1) ? 6 : 4; }
 
 template <int DC, int NM>
@@ -60,11 +60,12 @@ constexpr int kItemUnits = 3;
 // Running maximum of a row without keys: no finite score lies below it, and a masked one, -inf, has no weight under it.
 constexpr float kNoMax = -FLT_MAX;
 // Weights times their values' scales, as f16 parts, reach 2^15 in units of a power of two a row.  A unit serves
-// chunks whose scales lie within 2^-13 of it: the parts' last step, 2^-24, is then 2^-26 of the smallest of them.
+// chunks whose scales lie within 2^-9 of it: the parts' last step, 2^-24, is then 2^-30 of the smallest of them.
 constexpr int kWeightBits = 15;
-constexpr int kScaleSpread = 12;  // exponents below the unit's
-// A unit may fall to 2^-64 of what earlier keys may have left in the sums: those reach 2^(64 + 24) then, times the keys.
-constexpr float kUnitFall = 64.0f;
+constexpr int kScaleSpread = 8;  // exponents below the unit's
+// A unit may fall to 2^-56 of what earlier keys have left in the sums, as far as that is known (2^kScaleSpread more at
+// worst): those reach 2^(24 + 56 + 8) then, times the keys.
+constexpr float kUnitFall = 56.0f;
 // Parts hold their sums times this: a mean of the largest values is finite, and so is what a million of them add up to.
 constexpr float kPartScale = 0x1p-20f;
 
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
   __shared__ uint32_t group_units[kAttMaxTokens / 32];  // of 32 tokens each, for one (head, part)
   __shared__ AttSpan spans[W][2];                       // the items of the warps' parts: first, last
   __shared__ float2 part_rows[W][2][S::kRows];          // maxima and sums of weights of their rows
-  __shared__ float rooms[W][NM][32];                    // a lane's rows: see `unit`
+  __shared__ float2 rooms[W][NM][32];                   // a lane's rows: see `unit`
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c4 = lane & 3;
@@ -605,13 +606,14 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 #pragma unroll
         for (int n = 0; n < NO; ++n) o[i][n] = make_float2(0.0f, 0.0f);
       }
-      // Biased exponent of each row's unit, at least that of the format's smallest scale.  The sums' own (the largest
-      // weight times scale that went in, at the present maximum) may lie above it, by `rooms` powers of two at most.
+      // Biased exponent of each row's unit, at least that of the format's smallest scale.  Beside it, when it was last
+      // looked at: how far above (or, after chunks without weight, below) it the sums' own lay, the largest weight times
+      // scale that went in, and the maximum then.
       int unit[NM];
 #pragma unroll
       for (int i = 0; i < NM; ++i) {
         unit[i] = 127 - 111;
-        rooms[warp][i][lane] = 0.0f;
+        rooms[warp][i][lane] = make_float2(0.0f, kNoMax);
       }
       const int t0 = token_of<DC>(2 * c4), t1 = token_of<DC>(2 * c4 + 1);  // this lane's columns
 
@@ -703,15 +705,15 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
 #pragma unroll
           for (int n = 0; n < NT; ++n) top = fmaxf(top, fmaxf(x[i][n].x, x[i][n].y));
           top = fmaxf(m[i], quad_max(top));
-          const float down = m[i] - top, keep = exp2_fast(down);
+          const float before = m[i], down = before - top, keep = exp2_fast(down);
           alpha[i] = keep;
           m[i] = top;
           if (__builtin_expect(other, 0)) {
-            // A unit for this chunk.  Above its scales, unless those lie far apart, or far above the unit without the
-            // weights to match: then above the largest weight times scale among the keys that the row sees, and the unit
-            // stays if that is what it serves.  A block of large values that the softmax gives no weight, or that only other
-            // rows see, so takes no bits from the others (with a unit above every scale so far, 2^20 between scales left
-            // errors of 1e-3 of the row, 2^34 zeros; it took 545 us where 552 in the case above).
+            // A unit for this chunk.  Above its scales, unless those lie far apart, or far above both the sums' own and
+            // what this chunk's weights make of them: then above the largest weight times scale among the keys that the row
+            // sees, and the unit stays if that is what it serves.  A block of large values that the softmax gives no weight,
+            // or that only other rows see, so takes no bits from the others (with a unit above every scale so far, 2^20
+            // between scales left errors of 1e-3 of the row, 2^34 zeros; it took 545 us where 556 in the case above).
             float most = 0.0f;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -720,18 +722,23 @@ __global__ void __launch_bounds__(32 * AttShape<DC, NM>::kWarps, 2) attend_kerne
               most = fmaxf(most, fmaxf(a < INFINITY ? a : 0.0f, b < INFINITY ? b : 0.0f));
             }
             const int fit = static_cast<int>(__float_as_uint(quad_max(most)) >> 23) + 1;  // (1: no weight at all)
+            // The sums' own: as it was and this chunk's; a maximum since then came with a weight of 1 and a scale that the
+            // unit served.
+            const float2 was = rooms[warp][i][lane];
+            float own = fmaxf(static_cast<float>(unit[i]) + was.x + (was.y - top), static_cast<float>(fit));
+            if (before > was.y) own = fmaxf(own, static_cast<float>(unit[i] - kScaleSpread) + down);
             const bool alike = vlow >= vtop - kScaleSpread;
             int now = unit[i];
-            if (hi[i] == 0 || (alike && (vtop <= unit[i] + kScaleSpread || fit > vtop - kScaleSpread)))
+            if (hi[i] == 0 || (alike && static_cast<float>(vtop - kScaleSpread) <= own))
               now = vtop;
             else if (fit > unit[i] || (!alike && fit > 1 && fit < unit[i] - kScaleSpread))
               now = fit;
-            const float held = fmaxf(static_cast<float>(unit[i]) + rooms[warp][i][lane] + down, 0.0f);  // the sums' own
-            now = max(max(now, 127 - 111), static_cast<int>(ceilf(held - kUnitFall)));
+            const float most_own = fmaxf(fmaxf(own, static_cast<float>(unit[i]) + down), 0.0f);
+            now = max(max(now, 127 - 111), static_cast<int>(ceilf(most_own - kUnitFall)));
             const int step = unit[i] - now, half = step / 2;
             alpha[i] = keep * __uint_as_float((127 + half) << 23) * __uint_as_float((127 + step - half) << 23);
             unit[i] = now;
-            rooms[warp][i][lane] = fmaxf(held - static_cast<float>(now), 0.0f);
+            rooms[warp][i][lane] = make_float2(own - static_cast<float>(now), top);
           }
           // 2^kWeightBits a unit
           const float vinv = __uint_as_float((254 + kWeightBits - unit[i]) << 23);

@@ -281,3 +281,54 @@ def test_scales_that_come_and_go_within_a_warp(G, D, fmt):
     b, bl = au.attend_bounds(c, want, lse, mass, spread, np.full(lse.shape, float(n)), False)
     assert_within(got, want, b, "out")
     assert_within(gl, lse, bl, "lse")
+
+
+def dropped(c, q, pos):
+    """What keys with weights below 2^-125 contribute: they may count as zero."""
+    T, Hq, D = q.shape
+    n, H = int(max(pos)) + 1, c["k"].shape[1]
+    k, v = (x.transpose(1, 0, 2) for x in oatt.load(c, np.zeros(n, dtype=int), np.arange(n)))
+    a = q.astype(np.float64).reshape(T, H, -1, D).transpose(1, 0, 2, 3).reshape(H, -1, D) * D ** -0.5 @ k.transpose(0, 2, 1)
+    a = np.where(np.arange(n) <= np.repeat(pos, Hq // H)[:, None], a, -np.inf)
+    w = np.exp(a - a.max(-1, keepdims=True))
+    w[w >= 2.0 ** -125] = 0.0
+    return (w @ np.abs(v)).reshape(H, T, Hq // H, D).swapaxes(0, 1).reshape(q.shape)
+
+
+# (values' exponent, scores' level in powers of two) of a sequence's blocks
+BLOCKS = {
+    # a unit that falls, a maximum that comes while it serves, and large values whose weights make them count
+    "weights that just count": [(52, 0), (22, -15), (18, 58), (53, 24), (31, 20)],
+    # ever larger values, none of weight, between two blocks that have all of it
+    "steps up": [(-55, 62)] + [(-45 + 10 * i, -62) for i in range(11)] + [(-55, 60)],
+    "steps up and down": [(-30, 40)] + [(-22 + 8 * i, -60) for i in range(12)] + [(70 - 8 * i, -50) for i in range(12)] + [(-30, 44)],
+    "ever more weight": [(60, -100), (30, -60), (0, -20), (-30, 20), (-60, 60), (-90, 110)],
+    "ever less weight": [(-90, 110), (-60, 60), (-30, 20), (0, -20), (30, -60), (60, -100)],
+    "more weight within a unit": [(20, -100), (19, -40), (18, 0), (17, 30), (90, -35), (-20, 50), (-21, 90)],
+}
+
+
+@pytest.mark.parametrize("blocks", list(BLOCKS))
+@pytest.mark.parametrize("block", [16, 32, 64])
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+@pytest.mark.parametrize("group, D", [(2, 128), (10, 64), (2, 256)])
+def test_scores_and_scales_by_blocks(G, group, D, fmt, block, blocks):
+    """Blocks of any weight with values of any size: so many rows of one sequence that a warp takes most of it in turn."""
+    rng = np.random.default_rng(D + block)
+    rows, H, n = 480, 4, len(BLOCKS[blocks]) * block
+    c = setup(rng, fmt, [n], H, 64, D, block)
+    c["v"] = no_zeros(c["v"])
+    q = queries(rng, rows, H * group, D, size=0.02 if fmt == "i8" else 0.005)  # (within a block scores lie close)
+    q[..., 0] = np.float32(np.sqrt(D) * np.log(2.0))
+    one = {"i8": lambda v: v & 0xff, "e4m3": lambda v: int(oatt.encode("e4m3", np.array([float(v)]))[0])}[fmt]
+    c["k_scale"][:] = 1.0
+    for i, (e, level) in enumerate(BLOCKS[blocks]):
+        (p, b), = blocks_at(c, 0, [i])
+        c["k"][p, :, b * block:(b + 1) * block, 0] = one(level)
+        c["v_scale"][p, :, b] *= np.float32(2.0 ** e)
+    seq, pos = np.zeros(rows, dtype=np.int32), n - 1 - rng.integers(0, 5, rows).astype(np.int32)
+    want, lse, mass, spread = one_sequence(c, q, seq, pos)
+    got, gl = call(G, au.DeviceCache(G, c), q, seq, pos)
+    b, bl = au.attend_bounds(c, want, lse, mass, spread, np.full(lse.shape, float(n)), False)
+    assert_within(got, want, b + dropped(c, q, pos), "out")
+    assert_within(gl, lse, bl, "lse")
