@@ -3,7 +3,7 @@
 // One pass over a row's keys and values with the running maximum and sum of the softmax.  What bounds it
 // is reading the codes: each warp copies (cp.async) chunks of CT tokens, whole lines of consecutive addresses, into
 // stages of its own, a chunk ahead.  (Copies of just the bytes that a lane decodes itself, in fours of rows, left
-// the memory at 5.0 TB/s where consecutive ones reach 6.4.)  With the arithmetic, 936 instructions a chunk at three
+// the memory at 5.0 TB/s where consecutive ones reach 6.4.)  With the arithmetic, 938 instructions a chunk at three
 // warps a scheduler, 256 sequences of 4000 to 8000 keys and 32 query heads over 8 of 128 take 556 us, 5.5 TB/s.
 //
 // A warp takes a chunk of CT tokens.  m16n8k16 with the queries as the 16 rows: eight rows' f16 high parts and

@@ -462,7 +462,8 @@ GF_API int gf_prepare_rope(const void* x, int64_t T, int64_t heads, int64_t dim,
  *   k_scale, v_scale : [n_pages][heads][page / block]
  *   table            : int32 [n_seqs][table_ld]; position p of sequence s lies in page table[s][p / page]
  * A value is code * scale.  I8: codes -127..127, scales of 12 significant bits; E4M3: 4-bit exponents and
- * 3-bit mantissas up to 448, scales that are powers of two.
+ * 3-bit mantissas up to 448, scales that are powers of two.  Codes that are no values (E4M3's NaN, which the library
+ * does not write) may reach rows that share the reading of their keys.
  *  Limits (GF_ERR_UNSUPPORTED beyond): page 16..2^20 and block 1..64, powers of two, block <= page; dim a
  *  multiple of 16 up to 256; heads <= 1024; page * table_ld <= 2^30.
  * A token has no place where its seq is outside 0..n_seqs - 1, its pos below 0 or not under page *
@@ -527,13 +528,14 @@ GF_API int gf_prepare_cache_load(const gf_cache* cache, int64_t T, const int32_t
  * at positions max(0, pos - window + 1) .. pos of its sequence,
  *     s_j = scale * q . K_j,   dst = sum_j softmax(s)_j V_j,   lse = ln sum_j exp(s_j)
  * in 32-bit arithmetic.  q is taken as pairs of binary16, to 2^-22 of an element or 2^-39 of its row's largest; so
- * are the softmax's weights (1 for the largest) times their values' scales, to 2^-22 of each or 2^-27 of the scale,
- * or, where the scales of 32 neighbouring keys lie more than 2^12 apart, 2^-39 of the largest weight times scale
- * that the row sees among them.  Weights below 2^-126 are zero, and a key whose score times log2(e) leaves the
+ * are the softmax's weights (1 for the largest) times their values' scales: to 2^-22 of each, or 2^-30 of the scale,
+ * or, where the scales of neighbouring keys lie more than 2^8 apart, 2^-31 of the largest weight times scale that
+ * the row has met.  Weights below 2^-126 are zero, and a key whose score times log2(e) leaves the
  * finite numbers downwards has none.  The tokens' own keys have been stored before.
  * Positions in pages that the table does not have are not seen; a row that sees nothing (of a token without a
  * place, for instance) is 0, its lse -inf.  A token whose pos reaches beyond the table sees what lies in it.
- *  q, dst    : [T][q_heads][dim]; q_heads a multiple of heads, <= 1024.  T <= 2^16.
+ *  q, dst    : [T][q_heads][dim]; q_heads a multiple of heads, <= 1024.  T <= 2^16, and T * q_heads times
+ *              (page * table_ld / 16 + 4) <= 2^51.
  *  run       : how many tokens of one sequence stand next to each other (drafted tokens, a prompt's part;
  *              0 or 1: a decode step).  They then share one reading of the keys.  Only speed depends on it.
  *  workspace : device memory of at least gf_attend_workspace() bytes, 256-byte aligned, contents undefined
